@@ -573,6 +573,130 @@ int tcl_lag_select(const double *arrival, const int32_t *req_ptr, const int32_t 
                    double theta, int32_t max_batch, int32_t n_slots, int32_t *chosen,
                    int32_t *n_chosen);
 
+/* ------------------------------------------------------------------------
+ * Int8 base projections: the rows y that the apply adds its updates to.
+ * A base weight is held in 8 bits with one scale a channel (output column);
+ * activations are rounded to 8 bits with one scale a token.
+ * ------------------------------------------------------------------------ */
+
+/* One int8 base weight.  d_in is a multiple of 16 and at most
+ * TCL_I8_MAX_D_IN (the integer sums then fit 32 bits for any entries), d_out
+ * a multiple of 8.  Rows are contiguous; W is 16-byte, scale 4-byte aligned. */
+#define TCL_I8_MAX_D_IN 131056
+typedef struct {
+  int32_t d_in;
+  int32_t d_out;
+  const int8_t *W;     /* device [d_out][d_in] */
+  const float *scale;  /* device [d_out]       */
+} tcl_i8_weight;
+
+/*
+ * Activations to 8 bits, a scale for each token:
+ *   scale[t] = max_d |x[t][d]| / 127, rounded to fp32;
+ *   q[t][d]  = x[t][d] / scale[t] rounded to the nearest integer, ties to
+ *              even, of the real quotient (no rounding before that one).
+ * A row of zeros gets scale 0 and q 0.  A row that holds an infinity or a NaN
+ * gets scale NaN and q 0, so that its products are NaN.  Where the scale is a
+ * subnormal number q is held to +-127.
+ * x: device [n_tokens][ldx] of dtype xd, 16-byte aligned, ldx a multiple of
+ * 8; q: device [n_tokens][ldq], 16-byte aligned, ldq a multiple of 16; scale:
+ * device [n_tokens].  d is a multiple of 16.  Columns of q at or beyond d are
+ * left as they were.  n_tokens == 0 is a no-op.
+ * Errors: TCL_EINVAL (NULL, n_tokens < 0, d < 16, ldx or ldq < d), TCL_EALIGN,
+ * TCL_EUNSUPPORTED (xd), TCL_EHIP.
+ */
+int tcl_i8_quant(const void *x, int64_t ldx, tcl_dtype xd, int32_t n_tokens, int32_t d,
+                 int8_t *q, int64_t ldq, float *scale, void *stream);
+
+/*
+ * The product: y[t][c] = (sum_d q[t][d] * W[c][d]) * scale[t] * w->scale[c],
+ * the sum exact in 32-bit integers, the two multiplications in fp32, one
+ * rounding to yd.  q and scale as tcl_i8_quant writes them (any int8 entries
+ * are allowed); y: device [n_tokens][ldy], written, not added to, so that
+ * tcl_fused_apply on the same rows completes the projection.  Each output
+ * element has one owner; results are bitwise reproducible.  y must not
+ * overlap an input.  n_tokens == 0 or d_out == 0 is a no-op.
+ * Errors: TCL_EINVAL (NULL, sizes, ldq < d_in, ldy < d_out), TCL_EALIGN (q, W
+ * or y not 16-byte aligned, scales not 4-byte aligned, d_in or ldq not a
+ * multiple of 16, d_out or ldy not a multiple of 8), TCL_EUNSUPPORTED (yd,
+ * d_in beyond TCL_I8_MAX_D_IN), TCL_EHIP.
+ */
+int tcl_i8_product(const tcl_i8_weight *w, const int8_t *q, int64_t ldq, const float *scale,
+                   int32_t n_tokens, void *y, int64_t ldy, tcl_dtype yd, void *stream);
+
+/* Device workspace of tcl_i8_linear (host only). */
+int tcl_i8_workspace_bytes(const tcl_i8_weight *w, int32_t n_tokens, size_t *bytes);
+
+/*
+ * A base projection in one call: tcl_i8_quant of x into the workspace, then
+ * tcl_i8_product.  ws: device workspace of at least tcl_i8_workspace_bytes
+ * bytes, 256-byte aligned, in use until the call's work has run; calls that
+ * may run at the same time need one each.  Errors: those of the two calls;
+ * TCL_ENOSPC (ws_bytes too small).
+ */
+int tcl_i8_linear(const tcl_i8_weight *w, const void *x, int64_t ldx, tcl_dtype xd,
+                  int32_t n_tokens, void *y, int64_t ldy, tcl_dtype yd, void *ws,
+                  size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Paged key/value cache (ELORA, section V: keys and values hang off the
+ * adapter they were computed with, in blocks of one pool; section III-A, Eq.
+ * 2: the adapters update W_K and W_V).
+ * ------------------------------------------------------------------------ */
+
+/* One layer's cache: n_pages pages of page_size slots; slot s lies in page s
+ * / page_size.  Element d of head h of slot o in page p is at p * stride_page
+ * + o * stride_slot + h * stride_head + d of K and of V, bf16, so pages may
+ * be ordered by head or by slot.  page_size is a power of two, 1..1024;
+ * head_dim a multiple of 16, 16..256; strides are multiples of 8 elements; K
+ * and V are 16-byte aligned.  Heads and slots must not overlap. */
+typedef struct {
+  int32_t n_pages;
+  int32_t page_size;
+  int32_t n_kv_heads;
+  int32_t head_dim;
+  int64_t stride_page, stride_slot, stride_head; /* elements */
+  void *K;
+  void *V;
+} tcl_kv_cache;
+
+/* Position rotation: pair j < rot_dim / 2 of a head turns by pos *
+ * inv_freq[j] (device fp32, the product and its reduction in 64 bits): (a, b)
+ * becomes (a cos - b sin, b cos + a sin).  Pair j is elements (j, j + rot_dim
+ * / 2), or (2j, 2j + 1) when interleaved is not 0; elements at and beyond
+ * rot_dim are left alone.  rot_dim is a multiple of 16, 0 (no rotation,
+ * inv_freq may be NULL) .. head_dim. */
+typedef struct {
+  const float *inv_freq;
+  int32_t rot_dim;
+  int32_t interleaved;
+} tcl_rope;
+
+/*
+ * Appends the keys and values of n_tokens tokens: k's heads, rotated, and v's
+ * heads go to slot[t] of K and V, and q's heads, rotated, to q_out (q NULL:
+ * no queries, n_q_heads ignored).  k, v: device [n_tokens][ldk / ldv], row t
+ * holding n_kv_heads heads of head_dim one after another, of dtype xd (the
+ * rows a projection and its adapters left); q: [n_tokens][ldq], n_q_heads
+ * heads; q_out: bf16 [n_tokens][ldqo].  q_out may be q itself (bf16, the same
+ * leading dimension); other overlaps are not allowed.  The rotation is
+ * computed in fp32 and rounded to bf16 once.
+ * pos: device int32 [n_tokens]; slot: device int64 [n_tokens].  A token whose
+ * slot is negative or at or beyond n_pages * page_size is padding: nothing of
+ * it goes to the cache (its q_out row is written).  The other slots must
+ * differ from each other.  All other slots of the cache are left as they
+ * were.  n_tokens == 0 is a no-op.
+ * Errors: TCL_EINVAL (NULL, sizes, leading dimensions below the rows),
+ * TCL_EALIGN (k, v, q, q_out, K or V not 16-byte aligned, slot not 8-byte,
+ * pos or inv_freq not 4-byte aligned, leading dimensions or strides not
+ * multiples of 8), TCL_EUNSUPPORTED (head_dim, page_size, rot_dim, xd),
+ * TCL_EHIP.
+ */
+int tcl_kv_append(const tcl_kv_cache *c, const tcl_rope *rope, const void *k, int64_t ldk,
+                  const void *v, int64_t ldv, const void *q, int64_t ldq, int32_t n_q_heads,
+                  tcl_dtype xd, void *q_out, int64_t ldqo, int32_t n_tokens, const int32_t *pos,
+                  const int64_t *slot, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -35,7 +35,9 @@ EXPORTS = ["tcl_last_error", "tcl_version", "tcl_plan_bytes", "tcl_plan_map", "t
            "tcl_module_init", "tcl_composites_validate", "tcl_plan_map_host",
            "tcl_plan_remap_host", "tcl_plan_info", "tcl_plan_status_async",
            "tcl_module_pack_bytes", "tcl_module_pack", "tcl_fused_apply_noalloc",
-           "tcl_bam_pool_init", "tcl_bam_load"]
+           "tcl_bam_pool_init", "tcl_bam_load",
+           "tcl_i8_quant", "tcl_i8_product", "tcl_i8_workspace_bytes", "tcl_i8_linear",
+           "tcl_kv_append"]
 
 # bytes of the static device workspace of tcl_fused_apply_noalloc
 SCRATCH_BYTES = 32 << 20
@@ -61,6 +63,23 @@ class ModuleDesc(ctypes.Structure):
                 ("wdtype", ctypes.c_int32), ("A_t", ctypes.c_void_p),
                 ("B_t", ctypes.c_void_p), ("k_dev", ctypes.c_void_p),
                 ("B_k", ctypes.c_void_p)]
+
+
+class I8WeightDesc(ctypes.Structure):
+    _fields_ = [("d_in", ctypes.c_int32), ("d_out", ctypes.c_int32), ("W", ctypes.c_void_p),
+                ("scale", ctypes.c_void_p)]
+
+
+class KVDesc(ctypes.Structure):
+    _fields_ = [("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("stride_page", ctypes.c_int64), ("stride_slot", ctypes.c_int64),
+                ("stride_head", ctypes.c_int64), ("K", ctypes.c_void_p), ("V", ctypes.c_void_p)]
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32)]
 
 
 _lib = None
@@ -125,6 +144,13 @@ def lib(path: Optional[str] = None):
     L.tcl_bam_slots.argtypes = [vp, vp]
     L.tcl_bam_pool_init.argtypes = [ctypes.POINTER(ModuleDesc), vp, vp, sz, vp]
     L.tcl_bam_load.argtypes = [ctypes.POINTER(ModuleDesc), vp, vp, vp, i32, i32, vp, vp, vp]
+    L.tcl_i8_quant.argtypes = [vp, i64, i32, i32, i32, vp, i64, vp, vp]
+    L.tcl_i8_product.argtypes = [ctypes.POINTER(I8WeightDesc), vp, i64, vp, i32, vp, i64, i32, vp]
+    L.tcl_i8_workspace_bytes.argtypes = [ctypes.POINTER(I8WeightDesc), i32, ctypes.POINTER(sz)]
+    L.tcl_i8_linear.argtypes = [ctypes.POINTER(I8WeightDesc), vp, i64, i32, i32, vp, i64, i32, vp,
+                                sz, vp]
+    L.tcl_kv_append.argtypes = [ctypes.POINTER(KVDesc), ctypes.POINTER(RopeDesc), vp, i64, vp, i64,
+                                vp, i64, i32, i32, vp, i64, i32, vp, vp, vp]
     L.tcl_lag_select.argtypes = [vp, vp, vp, i32, vp, i32, ctypes.c_double, ctypes.c_double,
                                  i32, i32, vp, vp]
     if path is None:
@@ -702,3 +728,226 @@ def lag_select(now: float, theta: float, arrival, adapters, resident, max_batch:
                                n, res.ctypes.data, len(resident), float(now), float(theta),
                                int(max_batch), int(n_slots), out.ctypes.data, ctypes.byref(nc)))
     return out[:nc.value].tolist()
+
+
+# ---------------------------------------------------------------------------
+# the base model's operators around the apply
+# ---------------------------------------------------------------------------
+def _same_device(what: str, dev: torch.device, *tensors) -> None:
+    if dev.type != "cuda":
+        raise ValueError(f"{what}: tensors on the GPU expected")
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{what}: all tensors must be on {dev}")
+
+
+def _rows(what: str, t: torch.Tensor, n: Optional[int] = None, d: Optional[int] = None) -> int:
+    """Checks a [n, d] tensor of contiguous rows; returns its leading dimension."""
+    if t.dim() != 2 or (n is not None and t.shape[0] != n) or (d is not None and t.shape[1] != d):
+        want = "[rows, columns]" if d is None else f"[{'n' if n is None else n}, {d}]"
+        raise ValueError(f"{what} must be {want}, got {list(t.shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what} must have contiguous rows")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _vector(what: str, t: torch.Tensor, n: int, dtype: torch.dtype) -> None:
+    if t.shape != (n,) or t.dtype != dtype or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of {n} entries")
+
+
+def _on(dev: torch.device, stream, *tensors):
+    """Context and stream handle of a call on ``dev``: the device is made the
+    current one, and tensors the call allocated itself are kept for a stream
+    other than the one they were allocated on."""
+    if stream is not None and isinstance(stream, torch.cuda.Stream):
+        for t in tensors:
+            t.record_stream(stream)
+    return torch.cuda.device(dev), _stream(dev, stream)
+
+
+class I8Weight:
+    """An int8 base weight: W int8 [d_out, d_in] and its channel scales fp32
+    [d_out], on the GPU (tcl_i8_weight)."""
+
+    def __init__(self, W: torch.Tensor, scale: torch.Tensor):
+        if W.dtype != torch.int8:
+            raise TypeError("I8Weight: W must be int8")
+        if W.dim() != 2 or not W.is_contiguous():
+            raise ValueError("I8Weight: W must be [d_out, d_in], contiguous")
+        _vector("I8Weight: scale", scale, W.shape[0], torch.float32)
+        _same_device("I8Weight", W.device, scale)
+        self.W, self.scale = W, scale
+        self.d_out, self.d_in = W.shape
+        self.desc = I8WeightDesc(self.d_in, self.d_out, W.data_ptr(), scale.data_ptr())
+
+
+def i8_quant(x: torch.Tensor, q: Optional[torch.Tensor] = None,
+             scale: Optional[torch.Tensor] = None, stream=None):
+    """tcl_i8_quant: (q int8 [T, d], scale fp32 [T]) of x [T, d], bf16 or fp32."""
+    ldx = _rows("i8_quant: x", x)
+    T, d = x.shape
+    own = []
+    if q is None:
+        q = torch.empty(T, d, dtype=torch.int8, device=x.device)
+        own.append(q)
+    if scale is None:
+        scale = torch.empty(T, dtype=torch.float32, device=x.device)
+        own.append(scale)
+    if q.dtype != torch.int8:
+        raise TypeError("i8_quant: q must be int8")
+    ldq = _rows("i8_quant: q", q, T, d)
+    _vector("i8_quant: scale", scale, T, torch.float32)
+    _same_device("i8_quant", x.device, q, scale)
+    ctx, st = _on(x.device, stream, *own)
+    with ctx:
+        check(lib().tcl_i8_quant(x.data_ptr(), ldx, _dtype_code(x.dtype), T, d, q.data_ptr(), ldq,
+                                 scale.data_ptr(), st))
+    return q, scale
+
+
+def i8_product(w: I8Weight, q: torch.Tensor, scale: torch.Tensor,
+               y: Optional[torch.Tensor] = None, y_dtype: torch.dtype = torch.bfloat16,
+               stream=None) -> torch.Tensor:
+    """tcl_i8_product: y [T, d_out] (written, not added to) of tokens q, scale."""
+    if q.dtype != torch.int8:
+        raise TypeError("i8_product: q must be int8")
+    T = q.shape[0]
+    ldq = _rows("i8_product: q", q, T, w.d_in)
+    _vector("i8_product: scale", scale, T, torch.float32)
+    own = []
+    if y is None:
+        y = torch.empty(T, w.d_out, dtype=y_dtype, device=q.device)
+        own.append(y)
+    ldy = _rows("i8_product: y", y, T, w.d_out)
+    _same_device("i8_product", q.device, scale, y, w.W)
+    ctx, st = _on(q.device, stream, *own)
+    with ctx:
+        check(lib().tcl_i8_product(ctypes.byref(w.desc), q.data_ptr(), ldq, scale.data_ptr(), T,
+                                   y.data_ptr(), ldy, _dtype_code(y.dtype), st))
+    return y
+
+
+class I8Call:
+    """Pre-marshalled arguments of tcl_i8_linear for repeated calls: each call
+    writes the base projection of x into y.  The workspace is the call's own
+    (or ``ws``); calls that may run at the same time need one each."""
+
+    def __init__(self, w: I8Weight, x: torch.Tensor, y: torch.Tensor,
+                 ws: Optional[torch.Tensor] = None):
+        T = x.shape[0]
+        self.ldx = _rows("I8Call: x", x, T, w.d_in)
+        self.ldy = _rows("I8Call: y", y, T, w.d_out)
+        _same_device("I8Call", x.device, y, w.W, ws)
+        self.w, self.x, self.y, self.T = w, x, y, T
+        self.xd, self.yd = _dtype_code(x.dtype), _dtype_code(y.dtype)
+        need = ctypes.c_size_t(0)
+        check(lib().tcl_i8_workspace_bytes(ctypes.byref(w.desc), T, ctypes.byref(need)))
+        if ws is None or ws.numel() * ws.element_size() < need.value:
+            ws = torch.empty(max(need.value, 256), dtype=torch.uint8, device=x.device)
+        self.ws = ws
+
+    def __call__(self, stream=None) -> torch.Tensor:
+        ctx, st = _on(self.x.device, stream, self.ws)
+        with ctx:
+            check(lib().tcl_i8_linear(ctypes.byref(self.w.desc), self.x.data_ptr(), self.ldx,
+                                      self.xd, self.T, self.y.data_ptr(), self.ldy, self.yd,
+                                      self.ws.data_ptr(), self.ws.numel() * self.ws.element_size(),
+                                      st))
+        return self.y
+
+
+def i8_linear(w: I8Weight, x: torch.Tensor, y: Optional[torch.Tensor] = None,
+              y_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+    """tcl_i8_linear: the base projection of x [T, d_in]."""
+    if y is None:
+        y = torch.empty(x.shape[0], w.d_out, dtype=y_dtype, device=x.device)
+        _on(x.device, stream, y)
+    return I8Call(w, x, y)(stream)
+
+
+class KVCache:
+    """One layer's paged key/value cache: K and V bf16 [n_pages, page_size,
+    n_kv_heads, head_dim] views of one stride pattern, the last dimension
+    contiguous (a tensor kept by head inside a page is passed transposed)."""
+
+    def __init__(self, K: torch.Tensor, V: torch.Tensor):
+        if K.dtype != torch.bfloat16 or V.dtype != torch.bfloat16:
+            raise TypeError("KVCache: K and V must be bfloat16")
+        if K.dim() != 4 or K.shape != V.shape:
+            raise ValueError("KVCache: K and V must both be [n_pages, page_size, heads, head_dim]")
+        strides = [K.stride(i) if K.shape[i] > 1 else 0 for i in range(4)]
+        if strides != [V.stride(i) if V.shape[i] > 1 else 0 for i in range(4)]:
+            raise ValueError("KVCache: K and V must have the same strides")
+        if strides[3] != 1 or any(K.shape[i] > 1 and strides[i] == 0 for i in range(3)):
+            raise ValueError("KVCache: contiguous heads that do not overlap expected")
+        _same_device("KVCache", K.device, V)
+        self.K, self.V = K, V
+        self.device = K.device
+        self.n_pages, self.page_size, self.n_kv_heads, self.head_dim = K.shape
+        self.desc = KVDesc(*K.shape, *strides[:3], K.data_ptr(), V.data_ptr())
+
+
+class Rope:
+    """Position rotation: inv_freq fp32 [rot_dim / 2] on the GPU (None: no
+    rotation); pairs (j, j + rot_dim / 2), or (2j, 2j + 1) if interleaved."""
+
+    def __init__(self, inv_freq: Optional[torch.Tensor], interleaved: bool = False):
+        n = 0 if inv_freq is None else inv_freq.numel()
+        if n:
+            _vector("Rope: inv_freq", inv_freq, n, torch.float32)
+        self.inv_freq = inv_freq
+        self.desc = RopeDesc(_ptr(inv_freq) if n else None, 2 * n, int(interleaved))
+
+
+class AppendCall:
+    """Pre-marshalled arguments of tcl_kv_append for repeated calls: k, v [T,
+    heads * head_dim] rows go to ``slot`` (int64 [T]) of the cache, k rotated
+    to ``pos`` (int32 [T]); with q [T, q heads * head_dim] its rotated rows go
+    to q_out (bf16, made here unless given).  Each call returns q_out."""
+
+    def __init__(self, cache: KVCache, k: torch.Tensor, v: torch.Tensor, pos: torch.Tensor,
+                 slot: torch.Tensor, rope: Optional[Rope] = None,
+                 q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None):
+        T, row = k.shape[0], cache.n_kv_heads * cache.head_dim
+        self.ldk = _rows("AppendCall: k", k, T, row)
+        self.ldv = _rows("AppendCall: v", v, T, row)
+        if v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
+            raise TypeError("AppendCall: q, k and v must share a dtype")
+        _vector("AppendCall: pos", pos, T, torch.int32)
+        _vector("AppendCall: slot", slot, T, torch.int64)
+        rope = rope or Rope(None)
+        self.Hq, self.ldq, self.ldqo = 0, 0, 0
+        if q is not None:
+            self.ldq = _rows("AppendCall: q", q, T)
+            if q.shape[1] % cache.head_dim:
+                raise ValueError("AppendCall: q must hold whole heads")
+            self.Hq = q.shape[1] // cache.head_dim
+            if q_out is None:
+                q_out = torch.empty(T, q.shape[1], dtype=torch.bfloat16, device=k.device)
+            if q_out.dtype != torch.bfloat16:
+                raise TypeError("AppendCall: q_out must be bfloat16")
+            self.ldqo = _rows("AppendCall: q_out", q_out, T, q.shape[1])
+        elif q_out is not None:
+            raise ValueError("AppendCall: q_out without q")
+        _same_device("AppendCall", cache.device, k, v, pos, slot, q, q_out, rope.inv_freq)
+        self.cache, self.rope, self.k, self.v, self.q = cache, rope, k, v, q
+        self.pos, self.slot, self.q_out, self.T = pos, slot, q_out, T
+        self.xd = _dtype_code(k.dtype)
+
+    def __call__(self, stream=None) -> Optional[torch.Tensor]:
+        ctx, st = _on(self.cache.device, stream, *([] if self.q_out is None else [self.q_out]))
+        with ctx:
+            check(lib().tcl_kv_append(
+                ctypes.byref(self.cache.desc), ctypes.byref(self.rope.desc), self.k.data_ptr(),
+                self.ldk, self.v.data_ptr(), self.ldv, _ptr(self.q), self.ldq, self.Hq, self.xd,
+                _ptr(self.q_out), self.ldqo, self.T, self.pos.data_ptr(), self.slot.data_ptr(),
+                st))
+        return self.q_out
+
+
+def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, pos: torch.Tensor,
+              slot: torch.Tensor, rope: Optional[Rope] = None, q: Optional[torch.Tensor] = None,
+              q_out: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
+    """tcl_kv_append; returns the rotated queries (None without q)."""
+    return AppendCall(cache, k, v, pos, slot, rope, q, q_out)(stream)

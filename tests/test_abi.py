@@ -367,3 +367,78 @@ def test_host_validation_ignores_the_unused_tail():
         assert O.validate(gt, gp_bad, ad_t, al_t, T, N) == O.EINVAL
         assert tclora.validate_composites(gt, gp_bad, ad_t, al_t, N, n_tokens=T)[0] == \
             tclora.EINVAL
+
+
+def test_i8_host_errors(L):
+    """The int8 calls refuse bad arguments on the host (no GPU)."""
+    P = 0x1000
+    ok = dict(d_in=64, d_out=32, W=P, scale=P)
+
+    def w(**kw):
+        a = {**ok, **kw}
+        return ctypes.byref(tclora.I8WeightDesc(a["d_in"], a["d_out"], a["W"], a["scale"]))
+
+    def quant(x=P, ldx=64, xd=0, T=4, d=64, q=P, ldq=64, s=P):
+        return L.tcl_i8_quant(x, ldx, xd, T, d, q, ldq, s, None)
+
+    def prod(wt=None, q=P, ldq=64, s=P, T=4, y=P, ldy=32, yd=1):
+        return L.tcl_i8_product(wt or w(), q, ldq, s, T, y, ldy, yd, None)
+
+    def lin(wt=None, x=P, ldx=64, xd=0, T=4, y=P, ldy=32, yd=1, ws=0x10000, n=1 << 20):
+        return L.tcl_i8_linear(wt or w(), x, ldx, xd, T, y, ldy, yd, ws, n, None)
+
+    E, A, U = tclora.EINVAL, tclora.EALIGN, tclora.EUNSUPPORTED
+    assert [quant(x=None), quant(q=None), quant(s=None), quant(T=-1), quant(d=8), quant(ldx=56),
+            quant(ldq=48)] == [E] * 7
+    assert [quant(d=40), quant(x=P + 8), quant(q=P + 8), quant(s=P + 2), quant(ldx=68),
+            quant(ldq=72)] == [A] * 6
+    assert quant(xd=2) == U and quant(T=0) == 0
+    for f in (prod, lin):
+        assert [f(y=None), f(T=-1), f(ldy=24), f(w(W=None)), f(w(scale=None)), f(w(d_in=0)),
+                f(w(d_out=-8))] == [E] * 7
+        assert [f(w(d_in=72)), f(w(d_out=36)), f(w(W=P + 4)), f(w(scale=P + 1)), f(y=P + 8),
+                f(ldy=36)] == [A] * 6
+        assert f(yd=2) == U and f(w(d_in=131072)) == U and f(T=0) == 0
+    assert L.tcl_i8_product(None, P, 64, P, 4, P, 32, 1, None) == E
+    assert L.tcl_i8_linear(None, P, 64, 0, 4, P, 32, 1, P, 99, None) == E
+    assert [prod(q=None), prod(s=None), prod(ldq=48)] == [E] * 3
+    assert [prod(q=P + 8), prod(s=P + 2), prod(ldq=72)] == [A] * 3
+    assert [lin(x=None), lin(ldx=56), lin(ws=None)] == [E] * 3 and lin(xd=3) == U
+    assert lin(ws=0x10010) == A and lin(n=64) == tclora.ENOSPC
+    out = ctypes.c_size_t(0)
+    assert L.tcl_i8_workspace_bytes(w(), 4, ctypes.byref(out)) == 0 and out.value == 512
+    assert L.tcl_i8_workspace_bytes(w(), -1, ctypes.byref(out)) == E
+    assert L.tcl_i8_workspace_bytes(None, 4, ctypes.byref(out)) == E
+    assert L.tcl_i8_workspace_bytes(w(), 4, None) == E
+
+
+def test_kv_append_host_errors(L):
+    """tcl_kv_append refuses bad caches, rotations, rows and pointers on the
+    host (no GPU)."""
+    P = 0x1000
+    E, A, U = tclora.EINVAL, tclora.EALIGN, tclora.EUNSUPPORTED
+
+    def call(c=None, r=None, k=P, ldk=128, v=P, ldv=128, q=P, ldq=256, Hq=4, xd=0, qo=2 * P,
+             ldqo=256, T=4, pos=P, slot=P, **kw):
+        cd = dict(n_pages=4, page_size=16, n_kv_heads=2, head_dim=64, stride_page=2048,
+                  stride_slot=64, stride_head=1024, K=P, V=P)
+        rd = dict(inv_freq=P, rot_dim=64, interleaved=0)
+        cd.update({n: x for n, x in kw.items() if n in cd})
+        rd.update({n: x for n, x in kw.items() if n in rd})
+        cp = ctypes.byref(tclora.KVDesc(**cd)) if c is None else None
+        rp = ctypes.byref(tclora.RopeDesc(**rd)) if r is None else None
+        return L.tcl_kv_append(cp, rp, k, ldk, v, ldv, q, ldq, Hq, xd, qo, ldqo, T, pos, slot,
+                               None)
+
+    assert call(T=0) == 0 and call(T=0, rot_dim=0, inv_freq=None) == 0
+    assert [call(c=0), call(r=0), call(T=-1), call(k=None), call(v=None), call(pos=None),
+            call(slot=None), call(K=None), call(V=None), call(n_pages=0), call(n_kv_heads=0),
+            call(stride_head=-8), call(ldk=120), call(ldv=64), call(Hq=0), call(qo=None),
+            call(ldq=192), call(ldqo=192), call(inv_freq=None), call(qo=P, ldqo=264),
+            call(qo=P, xd=1)] == [E] * 21
+    assert [call(k=P + 8), call(v=P + 2), call(q=P + 8), call(qo=P + 8), call(K=P + 8),
+            call(slot=P + 4), call(pos=P + 2), call(ldk=132), call(ldq=260), call(ldqo=260),
+            call(stride_slot=68), call(inv_freq=P + 2)] == [A] * 12
+    assert [call(page_size=24), call(page_size=0), call(page_size=2048), call(head_dim=72),
+            call(head_dim=272), call(rot_dim=24), call(rot_dim=80), call(rot_dim=-16),
+            call(xd=2)] == [U] * 9

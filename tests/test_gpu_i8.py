@@ -1,0 +1,226 @@
+"""tcl_i8_quant, tcl_i8_product and tcl_i8_linear against their definitions in
+64 bits.
+
+The integers of the quantiser and the sums of the product are exact, so the
+quantiser must agree bit for bit, and a product only rounds: the integer sum
+to fp32 and two fp32 multiplications (2^-24 each, relative), and for a bf16
+output one more (2^-8).
+"""
+import numpy as np
+import pytest
+import torch
+
+from tenant_composite_lora_amd import tclora
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def tol(dtype):
+    """Half a step of the output type (finfo.eps / 2, relative) after three
+    half steps of fp32."""
+    t = 3 * torch.finfo(torch.float32).eps / 2
+    return t if dtype == torch.float32 else t + torch.finfo(dtype).eps / 2 * (1 + t)
+
+
+def quant64(x):
+    """The definition: scale rounded to fp32, then the real quotient."""
+    x = x.double().cpu()
+    amax = x.abs().amax(1) if x.shape[1] else x.new_zeros(x.shape[0])
+    s = (amax / 127).float()
+    n = torch.round(x / s.double()[:, None])
+    n = torch.where((s > 0)[:, None], n, 0).clamp(-127, 127)
+    bad = ~torch.isfinite(x).all(1)
+    s[bad] = float("nan")
+    n[bad] = 0
+    return n.to(torch.int8), s
+
+
+def product64(W, ws, q, s):
+    return (q.double().cpu() @ W.double().cpu().T) * s.double().cpu()[:, None] * ws.double().cpu()
+
+
+def close(got, want, dtype):
+    got = got.double().cpu()
+    nan = torch.isnan(want)
+    assert torch.equal(torch.isnan(got), nan)
+    # the smallest normal's rounding is absolute below it
+    tiny = torch.finfo(torch.float32).tiny * torch.finfo(dtype).eps
+    err = ((got - want).abs() - tol(dtype) * want.abs())[~nan]
+    assert err.numel() == 0 or float(err.max()) <= tiny, float(err.max())
+
+
+def weight(seed, d_out, d_in, full=False):
+    g = torch.Generator().manual_seed(seed)
+    W = torch.randint(-128 if full else -127, 128, (d_out, d_in), generator=g, dtype=torch.int32)
+    ws = torch.rand(d_out, generator=g) * 0.01 + 1e-4
+    return W.to(torch.int8).to(DEV), ws.to(DEV)
+
+
+def acts(seed, T, d, dtype):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(T, d, generator=g) * torch.exp2(torch.randint(-3, 4, (T, 1), generator=g))
+            ).to(dtype).to(DEV)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d", [(1, 16), (3, 48), (5, 4096), (2, 16384), (2, 16400), (1, 40000)])
+def test_quant_is_the_definition(T, d, dtype):
+    x = acts(T * 7 + d, T, d, DT[dtype])
+    q, s = tclora.i8_quant(x)
+    n, want = quant64(x)
+    assert torch.equal(s.cpu().view(torch.int32), want.view(torch.int32))
+    assert torch.equal(q.cpu(), n)
+
+
+def test_quant_ties_and_their_neighbours():
+    """A scale of 1 (largest magnitude 127): halves are ties, to even; fp32
+    values one step beside a half go to their own side."""
+    h = np.arange(-126.5, 127, 1.0, dtype=np.float32)
+    up, dn = np.nextafter(h, np.float32(1e9)), np.nextafter(h, np.float32(-1e9))
+    rows = []
+    for v in (h, up, dn):
+        rows.append(np.concatenate([[127.0], v, np.zeros(1)])[:256].astype(np.float32))
+    x = torch.from_numpy(np.stack([np.pad(r, (0, 256 - len(r))) for r in rows])).to(DEV)
+    # other scales whose quotients fall next to ties
+    extra = []
+    for a in (254.0, 1.0, 3.3, 1e-30, 1e30):
+        s = np.float32(a / 127)
+        t = (h.astype(np.float64) * float(s)).astype(np.float32)
+        extra.append(np.pad(np.concatenate([[np.float32(a)], t]), (0, 256 - 1 - len(t))))
+    x = torch.cat([x, torch.from_numpy(np.stack(extra).astype(np.float32)).to(DEV)])
+    q, s = tclora.i8_quant(x)
+    n, want = quant64(x)
+    assert torch.equal(s.cpu(), want)
+    assert torch.equal(q.cpu(), n)
+
+
+def test_quant_special_rows():
+    x = torch.zeros(6, 64)
+    x[1, 5] = float("nan")
+    x[2, 7] = float("inf")
+    x[3, 9] = -float("inf")
+    x[4] = 1e-44          # the scale is zero after rounding, or subnormal
+    x[4, 0] = 1.2e-43
+    x[5] = torch.linspace(-3e38, 3e38, 64)
+    x = x.to(DEV)
+    q, s = tclora.i8_quant(x)
+    assert s[0].item() == 0 and not q[0].any()
+    assert torch.isnan(s[1:4]).all() and not q[1:4].any()
+    n, want = quant64(x)
+    # (the last row's range is beyond fp32: linspace makes infinities of it)
+    assert torch.allclose(s.cpu()[4:], want[4:], rtol=0, atol=0, equal_nan=True)
+    assert torch.equal(q.cpu()[4:], n[4:])
+    W, ws = weight(3, 64, 64)
+    y = tclora.i8_product(tclora.I8Weight(W, ws), q, s, y_dtype=torch.float32)
+    assert not y[0].any() and torch.isnan(y[1:4]).all()
+    close(y[4:], product64(W, ws, n[4:], want[4:]), torch.float32)
+
+
+def test_quant_leaves_columns_behind_d():
+    x = acts(1, 4, 48, torch.bfloat16)
+    buf = torch.full((4, 80), 7, dtype=torch.int8, device=DEV)
+    tclora.i8_quant(x, q=buf[:, :48])
+    assert (buf[:, 48:] == 7).all()
+    assert torch.equal(buf[:, :48].cpu(), quant64(x)[0])
+
+
+SHAPES = [(1, 16, 8), (1, 4096, 1024), (2, 48, 40), (7, 144, 136), (16, 256, 1000),
+          (17, 1040, 264), (32, 4112, 512), (33, 512, 4104), (64, 4096, 4096), (65, 336, 1032),
+          (129, 2064, 72), (177, 1424, 520), (256, 128, 256), (257, 144, 136), (300, 4112, 392),
+          (515, 400, 1032), (1025, 272, 264), (2048, 528, 264), (260, 64, 4104)]
+
+
+@pytest.mark.parametrize("y", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d_in,d_out", SHAPES)
+def test_product(T, d_in, d_out, y):
+    W, ws = weight(T + d_out, d_out, d_in, full=True)
+    g = torch.Generator().manual_seed(T * d_in)
+    q = torch.randint(-128, 128, (T, d_in), generator=g, dtype=torch.int32).to(torch.int8).to(DEV)
+    s = (torch.rand(T, generator=g) + 0.01).to(DEV)
+    got = tclora.i8_product(tclora.I8Weight(W, ws), q, s, y_dtype=DT[y])
+    close(got, product64(W, ws, q, s), DT[y])
+
+
+@pytest.mark.parametrize("T", [3, 70, 300])
+def test_product_strides_and_bounds(T):
+    """Rows wider than the operands: the padding of q is not read into the
+    sums, the padding of y and the rows behind it stay as they were."""
+    d_in, d_out = 208, 136
+    W, ws = weight(9, d_out, d_in)
+    qb = torch.full((T + 2, 256), 99, dtype=torch.int8, device=DEV)
+    q = qb[:T, :d_in]
+    q.copy_(torch.randint(-127, 128, (T, d_in), dtype=torch.int32))
+    s = torch.rand(T, device=DEV) + 0.1
+    yb = torch.full((T + 3, 160), -5.0, device=DEV)
+    tclora.i8_product(tclora.I8Weight(W, ws), q, s, y=yb[:T, :d_out])
+    close(yb[:T, :d_out], product64(W, ws, q, s), torch.float32)
+    assert (yb[T:] == -5).all() and (yb[:, d_out:] == -5).all()
+
+
+@pytest.mark.parametrize("T", [1, 40, 300])
+def test_product_longest_rows_do_not_overflow(T):
+    d_in = 131056
+    W = torch.full((8, d_in), -128, dtype=torch.int8, device=DEV)
+    q = torch.full((T, d_in), -128, dtype=torch.int8, device=DEV)
+    one = torch.ones(8, device=DEV)
+    y = tclora.i8_product(tclora.I8Weight(W, one), q, torch.ones(T, device=DEV),
+                          y_dtype=torch.float32)
+    assert (y == float(d_in) * 16384).all()
+
+
+@pytest.mark.parametrize("x,y", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "bf16"), ("f32", "f32")])
+@pytest.mark.parametrize("T,d_in,d_out", [(1, 4096, 1024), (5, 272, 136), (64, 1024, 4096),
+                                          (300, 1040, 520)])
+def test_linear(T, d_in, d_out, x, y):
+    W, ws = weight(5, d_out, d_in)
+    a = acts(T, T, d_in, DT[x])
+    got = tclora.i8_linear(tclora.I8Weight(W, ws), a, y_dtype=DT[y])
+    n, s = quant64(a)
+    close(got, product64(W, ws, n, s), DT[y])
+
+
+def test_empty_batch_and_empty_weight():
+    W, ws = weight(5, 16, 32)
+    w = tclora.I8Weight(W, ws)
+    assert tclora.i8_linear(w, torch.empty(0, 32, device=DEV)).shape == (0, 16)
+    w0 = tclora.I8Weight(W[:0], ws[:0])
+    assert tclora.i8_linear(w0, acts(1, 3, 32, torch.float32)).shape == (3, 0)
+
+
+@pytest.mark.parametrize("T", [8, 300])
+def test_linear_in_a_graph_and_on_another_stream(T):
+    W, ws = weight(6, 1032, 528)
+    w = tclora.I8Weight(W, ws)
+    x = acts(2, T, 528, torch.bfloat16)
+    y = torch.empty(T, 1032, device=DEV)
+    call = tclora.I8Call(w, x, y)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    call(st)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=st):
+        call()
+    for i in range(4):
+        x.copy_(acts(20 + i, T, 528, torch.bfloat16))
+        y.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        replayed = y.clone()
+        eager = tclora.i8_linear(w, x, y_dtype=torch.float32)
+        assert torch.equal(replayed, eager)
+        n, s = quant64(x)
+        close(replayed, product64(W, ws, n, s), torch.float32)
+
+
+def test_results_repeat_bit_for_bit():
+    W, ws = weight(8, 520, 2064)
+    w = tclora.I8Weight(W, ws)
+    for T in (9, 200, 700):
+        x = acts(T, T, 2064, torch.bfloat16)
+        a = tclora.i8_linear(w, x)
+        # a token's row does not depend on its batch
+        b = tclora.i8_linear(w, x[3:9])
+        assert torch.equal(tclora.i8_linear(w, x), a) and torch.equal(a[3:9], b)
