@@ -697,6 +697,88 @@ int tcl_kv_append(const tcl_kv_cache *c, const tcl_rope *rope, const void *k, in
                   tcl_dtype xd, void *q_out, int64_t ldqo, int32_t n_tokens, const int32_t *pos,
                   const int64_t *slot, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Attention over the paged cache for a batch whose requests share their
+ * group's prefix (ELORA, section V: requests of one adapter hang below the
+ * same prefix blocks; DyMerge-LoRA, section 4.3: a mapping stage once a
+ * batch, then kernels over its tuples).
+ * ------------------------------------------------------------------------ */
+
+/* A batch, every array in DEVICE memory.  Request s owns query tokens
+ * [seq_tok_ptr[s], seq_tok_ptr[s + 1]) (n_seqs + 1 entries from 0, not
+ * decreasing, the last at most n_tokens); group g owns requests
+ * [group_seq_ptr[g], group_seq_ptr[g + 1]) (n_groups + 1 entries from 0 to
+ * n_seqs; a group, e.g. a tenant's adapter and instruction, may be empty).
+ * The keys of a request are its group's prefix, prefix_len[g] slots in pages
+ * prefix_pages[g * ld_prefix ..], then its own, own_len[s] slots in pages
+ * own_pages[s * ld_own ..], each list starting on a page of its own.  A
+ * request's n query tokens are the last n of its keys (they have been
+ * appended): token i of n sees the first prefix_len + own_len - n + i + 1
+ * keys (none if that is not positive).  Page ids behind the lengths are not
+ * read. */
+typedef struct {
+  int32_t n_seqs;
+  int32_t n_groups;
+  int32_t n_tokens;
+  int32_t ld_prefix; /* entries of a row of prefix_pages */
+  int32_t ld_own;    /* entries of a row of own_pages    */
+  const int32_t *seq_tok_ptr;
+  const int32_t *group_seq_ptr;
+  const int32_t *prefix_len;
+  const int32_t *prefix_pages;
+  const int32_t *own_len;
+  const int32_t *own_pages;
+} tcl_attn_batch;
+
+/* Bytes of a batch's plan and of the workspace of tcl_attn_apply, both from
+ * the sizes alone (host only; the batch's array contents are not read). */
+int tcl_attn_plan_bytes(const tcl_attn_batch *b, const tcl_kv_cache *c, int32_t n_q_heads,
+                        size_t *bytes);
+int tcl_attn_workspace_bytes(const tcl_attn_batch *b, const tcl_kv_cache *c, int32_t n_q_heads,
+                             size_t *bytes);
+
+/*
+ * The mapping: checks the batch on the device and cuts it into work items in
+ * `plan` (device, 256-byte aligned, tcl_attn_plan_bytes bytes).  One mapping
+ * serves every layer whose cache has the same pages, heads and head_dim; a
+ * batch of other lengths or tables needs a new one (into the same plan, with
+ * the same sizes, if wanted).  A bad table (pointers that decrease or do not
+ * run as above, a negative length or one beyond its page list, a page id in
+ * use outside the cache) leaves TCL_EINVAL in the plan, and tcl_attn_apply
+ * then changes nothing.  Graph-capturable.
+ * Errors: TCL_EINVAL, TCL_EALIGN, TCL_ENOSPC, TCL_EUNSUPPORTED (head_dim
+ * other than 64, 128 and 256, more than 128 query heads a key head, page
+ * lists of 2^30 keys, n_tokens * n_q_heads of 2^29), TCL_EHIP.
+ */
+int tcl_attn_plan(const tcl_attn_batch *b, const tcl_kv_cache *c, int32_t n_q_heads, void *plan,
+                  size_t plan_bytes, void *stream);
+
+/* Queues a copy of {status code, work items, row tiles, tokens that may share
+ * a prefix} of the plan into the device array dev_status[4]. */
+int tcl_attn_status_async(const void *plan, int32_t *dev_status, void *stream);
+
+/*
+ * o[t][hq] = sum_j softmax_j(scale * q[t][hq] . K[j][hk]) V[j][hk] over the
+ * keys j that token t sees, hk = hq / (n_q_heads / n_kv_heads): q, o device
+ * bf16 [n_tokens][ldq / ldo], n_q_heads heads of head_dim a row; lse (may be
+ * NULL): device fp32 [n_tokens][n_q_heads], the natural logarithm of the sum
+ * of exp(scale * q . k).  A token that sees no key gets o = 0 and lse =
+ * -infinity.  Rows of tokens that no request owns are left as they were.
+ * Keys and values a token does not see do not reach its row, whatever they
+ * hold.  The batch and cache sizes are those of the plan (a plan of others:
+ * nothing is written); q and o may be the same rows.  ws: device workspace of
+ * tcl_attn_workspace_bytes bytes, 256-byte aligned, in use until the call's
+ * work has run; calls that may run at the same time need one each.
+ * Scores, running maxima and sums are fp32; probabilities enter the second
+ * product as bf16 (for tiles of at most 16 rows as two bf16 parts).  Results
+ * are bitwise reproducible for the same batch.
+ * Errors: those of tcl_attn_plan; TCL_EINVAL (NULL, leading dimensions,
+ * scale not finite), TCL_EALIGN, TCL_ENOSPC.
+ */
+int tcl_attn_apply(const tcl_attn_batch *b, const tcl_kv_cache *c, int32_t n_q_heads,
+                   const void *plan, size_t plan_bytes, const void *q, int64_t ldq, void *o,
+                   int64_t ldo, float *lse, float scale, void *ws, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,938 @@
+// Attention of a batch over a paged key/value cache whose requests share
+// their group's prefix (include/tcl.h has the formulas).
+//
+// A query row is one head of one token.  Rows that read the same keys through
+// the same key/value head form a tile: the tokens of one request, or, over a
+// prefix, the tokens of all the short requests of its group, so that the
+// prefix is read once for all of them.  The mapping launch (attn_plan_kernel)
+// cuts the tiles' keys into items of even length; attn_kernel computes an
+// item a workgroup; attn_join_kernel joins the items of rows that have
+// several.
+//
+// attn_kernel computes the transposed products S' = K Q' and O' = V' P' on
+// the matrix cores: a lane then holds scores of one query row only, so that
+// the running maximum and sum are per-lane numbers with one exchange between
+// lane halves (or quarters) a step, and the probabilities leave the first
+// product in the very registers the second wants them in.
+#include <cmath>
+
+#include "kern_common.hpp"
+#include "kv.hpp"
+
+namespace tcl {
+namespace {
+
+constexpr int kRows = 128;      // query rows of a tile of many rows
+constexpr int kFew = 16;        // rows of a tile of few rows (keys split over the waves)
+constexpr int kKeys = 64;       // keys of a step
+constexpr int kMinChunk = 128;  // smallest key range an item is cut to
+constexpr int kTargetWgs = 1024;
+// a request whose rows fill half a tile reads its prefix by itself
+constexpr int kShortRows = 64;
+constexpr int kMagic = 0x41747431;
+
+enum { H_CODE, H_MAGIC, H_SEQS, H_GROUPS, H_TOKENS, H_HEADS, H_KVHEADS, H_DIM, H_PAGES, H_SHIFT,
+       H_LDO, H_LDP, H_ITEMS, H_TILES, H_SHARED, H_WORDS = 64 };
+
+struct Work {
+  int32_t tile;     // for rows and tokens
+  int32_t lo, hi;   // keys [lo, hi) of the requests' concatenated keys
+  int32_t part;     // first partial row, -1: write the output itself
+};
+
+struct Tile {
+  int32_t tok0;     // first token, or first entry of the token list (list 1)
+  int32_t list;
+  int32_t n_tok;    // tokens
+  int32_t seq, group;
+  int32_t prefix;   // keys of the prefix: key j >= prefix is own key j - prefix
+  int32_t lo, hi;   // key range
+  int32_t part0;    // first partial row
+  int32_t n_split;
+  int32_t chunk;    // keys an item
+  int32_t item0;
+};
+
+struct TokRec {
+  int32_t vis;      // keys the token sees, -1: no request owns it
+  int32_t own, own_at;  // tile over its own range, its place among the tile's tokens
+  int32_t pre, pre_at;  // tile over its group's prefix, -1: none
+  int32_t pad[3];
+};
+
+struct PlanArgs {
+  // table
+  const int32_t *seq_tok, *group_seq, *prefix_len, *prefix_pages, *own_len, *own_pages;
+  int32_t S, G, T, ldp, ldo;
+  int32_t Hq, Hkv, D, n_pages, page_shift;
+  int32_t tpt_many, tpt_few;  // whole tokens in a tile
+  int32_t cap_tiles, cap_items, cap_rows, target;
+  // plan
+  int32_t *hdr;
+  TokRec *tok;
+  Tile *tiles;
+  Work *items;
+  int32_t *list;       // [T]
+  int32_t *short_tok;  // [S + 1] tokens of short requests before this one
+  int32_t *short_seq;  // [S + 1] short requests before this one
+  int32_t *utile;      // [G + S] first tile of a unit (groups first)
+};
+
+struct Layout {
+  size_t o_tok, o_tiles, o_items, o_list, o_stok, o_sseq, o_utile, total;
+};
+
+// ---------------------------------------------------------------------------
+// mapping
+// ---------------------------------------------------------------------------
+constexpr int kMapThreads = 1024;
+
+// Exclusive scan over the workgroup; returns the total in every thread.
+__device__ inline int block_scan(int v, int *excl, int *lds) {
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  int inc = v;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int u = __shfl_up(inc, o, 64);
+    if (lane >= o) inc += u;
+  }
+  __syncthreads();
+  if (lane == 63) lds[w] = inc;
+  __syncthreads();
+  int base = 0, tot = 0;
+  for (int i = 0; i < kMapThreads / 64; ++i) {
+    const int x = lds[i];
+    if (i < w) base += x;
+    tot += x;
+  }
+  *excl = base + inc - v;
+  return tot;
+}
+
+__device__ inline int upper(const int32_t *ptr, int n, int x) {
+  // the last i in [0, n) with ptr[i] <= x
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int m = (lo + hi) >> 1;
+    if (ptr[m] <= x)
+      lo = m;
+    else
+      hi = m;
+  }
+  return lo;
+}
+
+struct Unit {
+  int rows, n_tok, tpt;  // rows, tokens, tokens a tile
+  int tok0, list, seq, group, prefix, lo, hi, n_q;
+};
+
+__device__ inline bool is_short(const PlanArgs &a, int q) {
+  return q > 0 && int64_t(q) * (a.Hq / a.Hkv) < kShortRows;
+}
+
+__device__ inline bool shares(const PlanArgs &a, int g) {
+  const int b = a.group_seq[g], e = a.group_seq[g + 1];
+  return a.prefix_len[g] > 0 && a.short_seq[e] - a.short_seq[b] >= 2;
+}
+
+// unit u: group u's prefix for u < G, request u - G's own keys (and its
+// prefix, if it does not share it) above
+__device__ inline Unit unit_of(const PlanArgs &a, int u) {
+  Unit x{};
+  const int gq = a.Hq / a.Hkv;
+  if (u < a.G) {
+    if (!shares(a, u)) return x;
+    const int b = a.group_seq[u], e = a.group_seq[u + 1];
+    x.tok0 = a.short_tok[b];
+    x.n_tok = a.short_tok[e] - x.tok0;
+    x.list = 1;
+    x.group = u;
+    x.prefix = x.hi = a.prefix_len[u];
+  } else {
+    const int s = u - a.G;
+    x.tok0 = a.seq_tok[s];
+    x.n_tok = x.n_q = a.seq_tok[s + 1] - x.tok0;
+    x.seq = s;
+    x.group = upper(a.group_seq, a.G, s);
+    // (empty groups: the one whose range holds s)
+    x.prefix = a.prefix_len[x.group];
+    x.lo = is_short(a, x.n_q) && shares(a, x.group) ? x.prefix : 0;
+    x.hi = x.prefix + a.own_len[s];
+  }
+  x.rows = x.n_tok * gq;
+  x.tpt = x.rows <= kFew ? a.tpt_few : a.tpt_many;
+  return x;
+}
+
+__device__ inline int unit_tiles(const Unit &x) {
+  return x.n_tok == 0 ? 0 : (x.n_tok + x.tpt - 1) / x.tpt;
+}
+
+// last key + 1 of tile i of a unit: the keys its last token sees
+__device__ inline int tile_hi(const Unit &x, int i) {
+  if (x.list) return x.hi;
+  const int last = min(x.n_tok, (i + 1) * x.tpt) - 1;
+  return max(x.lo, min(x.hi, x.hi - x.n_q + last + 1));
+}
+
+__global__ __launch_bounds__(kMapThreads) void attn_plan_kernel(PlanArgs a) {
+  __shared__ int lds[kMapThreads / 64];
+  __shared__ int s_err, s_chunk;
+  __shared__ unsigned long long s_work;
+  const int tid = threadIdx.x, gq = a.Hq / a.Hkv;
+  if (tid == 0) {
+    s_err = 0;
+    s_work = 0;
+    a.hdr[H_MAGIC] = kMagic, a.hdr[H_SEQS] = a.S, a.hdr[H_GROUPS] = a.G, a.hdr[H_TOKENS] = a.T;
+    a.hdr[H_HEADS] = a.Hq, a.hdr[H_KVHEADS] = a.Hkv, a.hdr[H_DIM] = a.D;
+    a.hdr[H_PAGES] = a.n_pages, a.hdr[H_SHIFT] = a.page_shift;
+    a.hdr[H_LDO] = a.ldo, a.hdr[H_LDP] = a.ldp;
+    a.hdr[H_CODE] = TCL_OK, a.hdr[H_ITEMS] = 0, a.hdr[H_TILES] = 0, a.hdr[H_SHARED] = 0;
+  }
+  __syncthreads();
+  // the table
+  bool bad = false;
+  if (tid == 0 && a.S > 0)
+    bad = a.seq_tok[0] != 0 || a.seq_tok[a.S] > a.T || a.group_seq[0] != 0 ||
+          a.group_seq[a.G] != a.S;
+  const int page = 1 << a.page_shift;
+  for (int s = tid; s < a.S; s += kMapThreads) {
+    bad |= a.seq_tok[s + 1] < a.seq_tok[s];
+    bad |= a.own_len[s] < 0 || a.own_len[s] > a.ldo * page;
+  }
+  for (int g = tid; g < a.G; g += kMapThreads) {
+    bad |= a.group_seq[g + 1] < a.group_seq[g];
+    bad |= a.prefix_len[g] < 0 || a.prefix_len[g] > a.ldp * page;
+  }
+  if (bad) s_err = 1;
+  __syncthreads();
+  if (!s_err) {
+    // a row of page ids a wave
+    const int w = tid >> 6, lane = tid & 63;
+    for (int r = w; r < a.S + a.G; r += kMapThreads / 64) {
+      const bool own = r < a.S;
+      const int g = r - a.S;
+      const int n = ((own ? a.own_len[r] : a.prefix_len[g]) + page - 1) >> a.page_shift;
+      const int32_t *p = own ? a.own_pages + int64_t(r) * a.ldo : a.prefix_pages + int64_t(g) * a.ldp;
+      for (int i = lane; i < n; i += 64) bad |= p[i] < 0 || p[i] >= a.n_pages;
+    }
+    if (bad) s_err = 1;
+  }
+  __syncthreads();
+  if (s_err) {
+    if (tid == 0) a.hdr[H_CODE] = TCL_EINVAL;
+    return;
+  }
+  // requests and tokens that may share a prefix, counted in order
+  int tok_base = 0, seq_base = 0;
+  for (int s0 = 0; s0 < a.S; s0 += kMapThreads) {
+    const int s = s0 + tid;
+    const int q = s < a.S ? a.seq_tok[s + 1] - a.seq_tok[s] : 0;
+    const bool sh = is_short(a, q);
+    int et, es;
+    const int nt = block_scan(sh ? q : 0, &et, lds);
+    const int ns = block_scan(sh ? 1 : 0, &es, lds);
+    if (s < a.S) {
+      a.short_tok[s] = tok_base + et;
+      a.short_seq[s] = seq_base + es;
+    }
+    tok_base += nt;
+    seq_base += ns;
+  }
+  if (tid == 0) {
+    a.short_tok[a.S] = tok_base;
+    a.short_seq[a.S] = seq_base;
+  }
+  __syncthreads();
+  // keys over all tiles: the length of an item
+  const int U = a.G + a.S;
+  unsigned long long work = 0;
+  for (int u = tid; u < U; u += kMapThreads) {
+    const Unit x = unit_of(a, u);
+    const int n = unit_tiles(x);
+    for (int i = 0; i < n; ++i) work += unsigned(tile_hi(x, i) - x.lo);
+  }
+  if (work) atomicAdd(&s_work, work);  // (an integer sum: any order)
+  __syncthreads();
+  if (tid == 0) {
+    const unsigned long long c = (s_work + a.target - 1) / a.target;
+    const unsigned long long r = (c + kKeys - 1) / kKeys * kKeys;
+    s_chunk = r < kMinChunk ? kMinChunk : (r > 0x40000000ull ? 0x40000000 : int(r));
+  }
+  __syncthreads();
+  const int chunk = s_chunk;
+  // tiles and items, in unit order
+  int tile_base = 0, item_base = 0, row_base = 0;
+  for (int u0 = 0; u0 < U; u0 += kMapThreads) {
+    const int u = u0 + tid;
+    Unit x{};
+    if (u < U) x = unit_of(a, u);
+    const int n = unit_tiles(x);
+    int ni = 0, nr = 0;
+    for (int i = 0; i < n; ++i) {
+      const int len = tile_hi(x, i) - x.lo, ns = max(1, (len + chunk - 1) / chunk);
+      const int nt = min(x.n_tok, (i + 1) * x.tpt) - i * x.tpt;
+      ni += ns;
+      nr += ns * nt * gq;
+    }
+    int et, ei, er;
+    const int tt = block_scan(n, &et, lds), ti = block_scan(ni, &ei, lds),
+              tr = block_scan(nr, &er, lds);
+    et += tile_base, ei += item_base, er += row_base;
+    if (u < U) a.utile[u] = et;
+    // (the capacities hold every table of these sizes; a tile beyond them
+    // could only come from a table that changed under the launch)
+    for (int i = 0; i < n; ++i) {
+      const int hi = tile_hi(x, i), len = hi - x.lo, ns = max(1, (len + chunk - 1) / chunk);
+      const int nt = min(x.n_tok, (i + 1) * x.tpt) - i * x.tpt;
+      // even lengths, whole steps
+      const int per = max(kKeys, ((len + ns - 1) / ns + kKeys - 1) / kKeys * kKeys);
+      if (et >= a.cap_tiles || ei + ns > a.cap_items || er + ns * nt * gq > a.cap_rows) break;
+      const bool direct = ns == 1 && !x.list && x.lo == 0;
+      a.tiles[et] = Tile{x.tok0 + i * x.tpt, x.list, nt, x.seq, x.group, x.prefix, x.lo, hi,
+                         direct ? -1 : er, ns, per, ei};
+      for (int k = 0; k < ns; ++k) {
+        const int lo = min(hi, x.lo + k * per);
+        a.items[ei + k] = Work{et, lo, min(hi, lo + per), direct ? -1 : er + k * nt * gq};
+      }
+      ++et, ei += ns, er += ns * nt * gq;
+    }
+    tile_base += tt, item_base += ti, row_base += tr;
+  }
+  __syncthreads();
+  // tokens
+  for (int t = tid; t < a.T; t += kMapThreads) {
+    TokRec r{-1, 0, 0, -1, 0, {0, 0, 0}};
+    if (a.S > 0 && t < a.seq_tok[a.S]) {
+      const int s = upper(a.seq_tok, a.S, t);
+      const Unit x = unit_of(a, a.G + s);
+      const int i = t - x.tok0;
+      r.vis = max(0, x.hi - x.n_q + i + 1);
+      r.own = a.utile[a.G + s] + i / x.tpt;
+      r.own_at = i % x.tpt;
+      if (is_short(a, x.n_q) && shares(a, x.group)) {
+        const Unit p = unit_of(a, x.group);
+        const int at = a.short_tok[s] + i;
+        a.list[at] = t;
+        r.pre = a.utile[x.group] + (at - p.tok0) / p.tpt;
+        r.pre_at = (at - p.tok0) % p.tpt;
+      }
+    }
+    a.tok[t] = r;
+  }
+  if (tid == 0) {
+    a.hdr[H_ITEMS] = min(item_base, a.cap_items);
+    a.hdr[H_TILES] = min(tile_base, a.cap_tiles);
+    a.hdr[H_SHARED] = tok_base;
+  }
+}
+
+__global__ void attn_status_kernel(const int32_t *hdr, int32_t *out) {
+  if (threadIdx.x < 4) {
+    const int w[4] = {H_CODE, H_ITEMS, H_TILES, H_SHARED};
+    out[threadIdx.x] = hdr[w[threadIdx.x]];
+  }
+}
+
+// ---------------------------------------------------------------------------
+// attention
+// ---------------------------------------------------------------------------
+struct AttnArgs {
+  KvArgs c;
+  const uint16_t *q;
+  uint16_t *o;
+  float *lse;
+  int64_t ldq, ldo;
+  float scale2;  // scale * log2(e)
+  int32_t S, G, T, ldp, ld_own, Hq;
+  const int32_t *prefix_pages, *own_pages;
+  const int32_t *hdr;
+  const TokRec *tok;
+  const Tile *tiles;
+  const Work *items;
+  const int32_t *list;
+  float *part_o;   // [rows][Hkv][D], not divided by the sum
+  float2 *part_ml; // [rows][Hkv]: running maximum (of base-2 scores), sum
+};
+
+// the plan belongs to these sizes (a plan of other sizes: nothing is done)
+__device__ inline bool plan_fits(const AttnArgs &a) {
+  const int32_t *h = a.hdr;
+  return h[H_MAGIC] == kMagic && h[H_CODE] == TCL_OK && h[H_SEQS] == a.S && h[H_GROUPS] == a.G &&
+         h[H_TOKENS] == a.T && h[H_HEADS] == a.Hq && h[H_KVHEADS] == a.c.H && h[H_DIM] == a.c.D &&
+         h[H_PAGES] == a.c.n_pages && h[H_SHIFT] == a.c.page_shift && h[H_LDO] == a.ld_own &&
+         h[H_LDP] == a.ldp;
+}
+
+typedef __attribute__((__vector_size__(16 * sizeof(float)))) float f32x16_t;
+typedef short s16x4 __attribute__((__vector_size__(4 * sizeof(short))));
+typedef short s16x8 __attribute__((__vector_size__(8 * sizeof(short))));
+
+// LDS holds a step's keys (or values) as rows of D / 8 16-byte chunks; chunk
+// c of row r lies at c ^ swz(r).  A key operand reads one chunk of 16 or 32
+// rows, a transposed value operand four chunks of 4 or 8 rows: both then
+// fall on all banks.
+template <int D>
+__device__ inline int swz(int r) {
+  if constexpr (D == 64)
+    return ((r >> 1) & 1) << 2 | ((r >> 2) & 3);
+  else
+    return (r & 3) << 2 | ((r >> 2) & 3);
+}
+
+// Four keys' values of one dimension: lane l of a group of 16 names four
+// neighbouring elements of key l / 4 and receives element l of keys 0..3.
+__device__ inline s16x4 read_tr(const uint16_t *p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)(p));
+}
+
+__device__ inline uint32_t pack_bf16(float a, float b) {
+  typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+  const bf2 v = {__bf16(a), __bf16(b)};
+  return __builtin_bit_cast(uint32_t, v);
+}
+
+template <int D>
+struct Smem {
+  uint16_t k[2][kKeys * D];
+  uint16_t v[2][kKeys * D];
+};
+
+// Key j of a tile as an offset into the cache.  Page ids are held to the
+// cache's pages, so that a table that changed after its mapping reads other
+// keys, never other memory.
+__device__ inline int64_t key_at(const AttnArgs &a, const Tile &t, int j) {
+  const bool pre = j < t.prefix;
+  const int i = pre ? j : j - t.prefix;
+  const int32_t *row = pre ? a.prefix_pages + int64_t(t.group) * a.ldp
+                           : a.own_pages + int64_t(t.seq) * a.ld_own;
+  const int page = row[i >> a.c.page_shift];
+  const int p = min(max(page, 0), a.c.n_pages - 1);
+  return int64_t(p) * a.c.s_page + int64_t(i & ((1 << a.c.page_shift) - 1)) * a.c.s_slot;
+}
+
+// Writes four neighbouring dimensions of a row: the output itself, or a
+// partial one.
+__device__ inline void put4(uint16_t *o, const float *v, float f) {
+  *reinterpret_cast<nt_u2 *>(o) = nt_u2{pack_bf16(v[0] * f, v[1] * f), pack_bf16(v[2] * f, v[3] * f)};
+}
+
+template <int D>
+__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_kernel(AttnArgs a) {
+  constexpr int CH = D / 8;         // chunks of a row
+  constexpr int RPI = 64 / CH;      // rows a wave loads an instruction
+  constexpr int NI = 16 / RPI;      // instructions for a wave's 16 rows
+  __shared__ __align__(16) Smem<D> sm;
+  if (!plan_fits(a)) return;
+  const int h = blockIdx.x % a.c.H, id = blockIdx.x / a.c.H;
+  if (id >= a.hdr[H_ITEMS]) return;
+  const Work it = a.items[id];
+  const Tile t = a.tiles[it.tile];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  const int gq = a.Hq / a.c.H, rows = t.n_tok * gq;
+  const bool few = rows <= kFew;
+  const int64_t hoff = int64_t(h) * a.c.s_head;
+
+  // staging: wave w moves rows 16 w .. 16 w + 15 of a step
+  const int lr = lane / CH, lc = lane % CH;
+  nt_u4 rk[NI], rv[NI];
+  auto fetch = [&](int j0) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      // behind the range: its last key again (masked below)
+      const int j = min(j0 + 16 * w + i * RPI + lr, it.hi - 1);
+      const int64_t at = key_at(a, t, j) + hoff + 8 * lc;
+      rk[i] = *reinterpret_cast<const nt_u4 *>(a.c.K + at);
+      rv[i] = *reinterpret_cast<const nt_u4 *>(a.c.V + at);
+    }
+  };
+  auto put = [&](int b) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int r = 16 * w + i * RPI + lr, p = r * D + 8 * (lc ^ swz<D>(r));
+      *reinterpret_cast<nt_u4 *>(&sm.k[b][p]) = rk[i];
+      *reinterpret_cast<nt_u4 *>(&sm.v[b][p]) = rv[i];
+    }
+  };
+  auto token = [&](int r) {  // row r of the tile -> token
+    const int i = t.tok0 + r / gq;
+    return t.list ? a.list[i] : i;
+  };
+  const int steps = (it.hi - it.lo + kKeys - 1) / kKeys;
+
+  if (few) {
+    // ---- few rows: every wave holds all of them, over its 16 keys a step
+    const int c = lane & 15, g = lane >> 4;
+    const bool live = c < rows;
+    const int tok = token(live ? c : 0);
+    const int hq = h * gq + (live ? c : 0) % gq;
+    const int vis = live ? a.tok[tok].vis : 0;
+    bf16x8_t qf[D / 32];
+#pragma unroll
+    for (int s = 0; s < D / 32; ++s)
+      qf[s] = *reinterpret_cast<const bf16x8_t *>(a.q + tok * a.ldq + int64_t(hq) * D + 32 * s + 8 * g);
+    f32x4_t o[D / 16];
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) o[i] = f32x4_t{0, 0, 0, 0};
+    float m = -INFINITY, l = 0.f;
+    if (steps > 0) fetch(it.lo);
+    for (int st = 0; st < steps; ++st) {
+      const int j0 = it.lo + st * kKeys, b = st & 1;
+      put(b);
+      if (st + 1 < steps) fetch(j0 + kKeys);
+      __syncthreads();
+      f32x4_t s4 = {0, 0, 0, 0};
+      const int kr = 16 * w + c;
+#pragma unroll
+      for (int s = 0; s < D / 32; ++s) {
+        const bf16x8_t kf =
+            *reinterpret_cast<const bf16x8_t *>(&sm.k[b][kr * D + 8 * ((4 * s + g) ^ swz<D>(kr))]);
+        s4 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[s], s4, 0, 0, 0);
+      }
+      float p[4], mx = -INFINITY;
+      const int left = min(vis, it.hi) - (j0 + 16 * w + 4 * g);  // visible keys of the lane's four
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        p[i] = i < left ? s4[i] * a.scale2 : -INFINITY;
+        mx = fmaxf(mx, p[i]);
+      }
+      mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
+      mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+      const float mn = fmaxf(m, mx), mu = mn == -INFINITY ? 0.f : mn;
+      const float al = __builtin_amdgcn_exp2f(m - mu);
+      m = mn;
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        p[i] = __builtin_amdgcn_exp2f(p[i] - mu);
+        sum += p[i];
+      }
+      l = l * al + sum;
+      // probabilities in two bf16 parts: the matrix cores idle here, and the
+      // rounding of one part would show beside the output's own
+      uint32_t hi2[2], lo2[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        hi2[i] = pack_bf16(p[2 * i], p[2 * i + 1]);
+        lo2[i] = pack_bf16(p[2 * i] - bf16_lo(hi2[i]), p[2 * i + 1] - bf16_hi(hi2[i]));
+      }
+      const s16x4 ph = __builtin_bit_cast(s16x4, nt_u2{hi2[0], hi2[1]});
+      const s16x4 pl = __builtin_bit_cast(s16x4, nt_u2{lo2[0], lo2[1]});
+      const int vr = 16 * w + 4 * g + (c >> 2);
+#pragma unroll
+      for (int d = 0; d < D / 16; ++d) {
+        o[d] *= al;
+        const s16x4 vf = read_tr(&sm.v[b][vr * D + 8 * ((2 * d + ((c & 3) >> 1)) ^ swz<D>(vr)) + 4 * (c & 1)]);
+        o[d] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(vf, ph, o[d], 0, 0, 0);
+        o[d] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(vf, pl, o[d], 0, 0, 0);
+      }
+    }
+    // join the waves: maxima and sums, then outputs, through LDS
+    l += __shfl_xor(l, 16, 64);
+    l += __shfl_xor(l, 32, 64);
+    __syncthreads();
+    float *jo = reinterpret_cast<float *>(&sm);             // [4][16][D]
+    static_assert(sizeof(sm) >= 4 * 16 * D * 4 + 4 * 16 * 8, "LDS of the join");
+    float2 *jm = reinterpret_cast<float2 *>(jo + 4 * 16 * D);  // [4][16]
+    if (g == 0) jm[w * 16 + c] = make_float2(m, l);
+#pragma unroll
+    for (int d = 0; d < D / 16; ++d)
+      *reinterpret_cast<f32x4_t *>(&jo[(w * 16 + c) * D + 16 * d + 4 * g]) = o[d];
+    __syncthreads();
+    for (int x = tid; x < rows * (D / 4); x += 256) {
+      const int r = x / (D / 4), d = x % (D / 4) * 4;
+      float M = -INFINITY, L = 0.f, f[4], v[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) M = fmaxf(M, jm[i * 16 + r].x);
+      const float mu = M == -INFINITY ? 0.f : M;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f[i] = __builtin_amdgcn_exp2f(jm[i * 16 + r].x - mu);
+        L += jm[i * 16 + r].y * f[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const f32x4_t u = *reinterpret_cast<const f32x4_t *>(&jo[(i * 16 + r) * D + d]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += u[e] * f[i];
+      }
+      const int tk = token(r), hh = h * gq + r % gq;
+      if (it.part < 0) {
+        put4(a.o + tk * a.ldo + int64_t(hh) * D + d, v, L > 0.f || L != L ? 1.f / L : 0.f);
+        if (a.lse && d == 0) a.lse[int64_t(tk) * a.Hq + hh] = (M + log2f(L)) * 0.69314718055994531f;
+      } else {
+        const int64_t pr = int64_t(it.part + r) * a.c.H + h;
+        *reinterpret_cast<f32x4_t *>(a.part_o + pr * D + d) = f32x4_t{v[0], v[1], v[2], v[3]};
+        if (d == 0) a.part_ml[pr] = make_float2(M, L);
+      }
+    }
+    return;
+  }
+
+  // ---- many rows: wave w holds rows 32 w .. 32 w + 31 over all keys
+  const int c = lane & 31, g = lane >> 5;
+  const int r = 32 * w + c;
+  const bool live = r < rows, busy = 32 * w < rows;
+  const int tok = token(live ? r : 0);
+  const int hq = h * gq + (live ? r : 0) % gq;
+  const int vis = live ? min(a.tok[tok].vis, it.hi) : it.hi;
+  // the fewest keys a row of the wave sees: no mask below them
+  int clear = vis;
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) clear = min(clear, __shfl_xor(clear, x, 64));
+  clear = __builtin_amdgcn_readfirstlane(clear);
+  bf16x8_t qf[D / 16];
+#pragma unroll
+  for (int s = 0; s < D / 16; ++s)
+    qf[s] = *reinterpret_cast<const bf16x8_t *>(a.q + tok * a.ldq + int64_t(hq) * D + 16 * s + 8 * g);
+  f32x16_t o[D / 32];
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[i][e] = 0.f;
+  float m = -INFINITY, l = 0.f;
+  if (steps > 0) fetch(it.lo);
+  for (int st = 0; st < steps; ++st) {
+    const int j0 = it.lo + st * kKeys, b = st & 1;
+    put(b);
+    if (st + 1 < steps) fetch(j0 + kKeys);
+    __syncthreads();
+    if (!busy) continue;
+    f32x16_t s2[2];
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s2[n][e] = 0.f;
+      const int kr = 32 * n + c;
+#pragma unroll
+      for (int s = 0; s < D / 16; ++s) {
+        const bf16x8_t kf =
+            *reinterpret_cast<const bf16x8_t *>(&sm.k[b][kr * D + 8 * ((2 * s + g) ^ swz<D>(kr))]);
+        s2[n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[s], s2[n], 0, 0, 0);
+      }
+    }
+    float mx = -INFINITY;
+    if (j0 + kKeys <= clear) {
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          s2[n][e] *= a.scale2;
+          mx = fmaxf(mx, s2[n][e]);
+        }
+    } else {
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int j = j0 + 32 * n + 8 * (e / 4) + 4 * g + e % 4;
+          s2[n][e] = j < vis ? s2[n][e] * a.scale2 : -INFINITY;
+          mx = fmaxf(mx, s2[n][e]);
+        }
+    }
+    mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+    const float mn = fmaxf(m, mx), mu = mn == -INFINITY ? 0.f : mn;
+    const float al = __builtin_amdgcn_exp2f(m - mu);
+    m = mn;
+    float sum = 0.f;
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        s2[n][e] = __builtin_amdgcn_exp2f(s2[n][e] - mu);
+        sum += s2[n][e];
+      }
+    l = l * al + sum;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[i][e] *= al;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      // keys 16 s + {4 g + 0..3, 8 + 4 g + 0..3}: the lane's eight, in order
+      uint32_t pw[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        pw[i] = pack_bf16(s2[s / 2][8 * (s & 1) + 2 * i], s2[s / 2][8 * (s & 1) + 2 * i + 1]);
+      const bf16x8_t pf = __builtin_bit_cast(bf16x8_t, nt_u4{pw[0], pw[1], pw[2], pw[3]});
+      const int i16 = lane & 15, sub = (lane >> 4) & 1;
+      const int v0 = 16 * s + 4 * g + (i16 >> 2), v1 = v0 + 8;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const int ch = 4 * i + 2 * sub + ((i16 & 3) >> 1), off = 4 * (i16 & 1);
+        const s16x4 x = read_tr(&sm.v[b][v0 * D + 8 * (ch ^ swz<D>(v0)) + off]);
+        const s16x4 y = read_tr(&sm.v[b][v1 * D + 8 * (ch ^ swz<D>(v1)) + off]);
+        const s16x8 vv = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+        o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, vv), pf, o[i], 0,
+                                                       0, 0);
+      }
+    }
+  }
+  if (!live) return;
+  l += __shfl_xor(l, 32, 64);
+  const float f = it.part >= 0 ? 1.f : (l > 0.f || l != l ? 1.f / l : 0.f);
+  const int64_t pr = int64_t(it.part + r) * a.c.H + h;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int d = 32 * i + 8 * e + 4 * g;
+      const float v[4] = {o[i][4 * e], o[i][4 * e + 1], o[i][4 * e + 2], o[i][4 * e + 3]};
+      if (it.part < 0)
+        put4(a.o + tok * a.ldo + int64_t(hq) * D + d, v, f);
+      else
+        *reinterpret_cast<f32x4_t *>(a.part_o + pr * D + d) = f32x4_t{v[0], v[1], v[2], v[3]};
+    }
+  if (g == 0) {
+    if (it.part >= 0)
+      a.part_ml[pr] = make_float2(m, l);
+    else if (a.lse)
+      a.lse[int64_t(tok) * a.Hq + hq] = (m + log2f(l)) * 0.69314718055994531f;
+  }
+}
+
+// Joins the items of one row a wave: maxima first, then the weighted sums in
+// item order (own items, then the prefix's).
+template <int D>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
+  if (!plan_fits(a)) return;
+  const int lane = threadIdx.x & 63;
+  const int64_t id = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  const int tk = int(id / a.Hq), hh = int(id % a.Hq);
+  if (tk >= a.T) return;
+  const TokRec r = a.tok[tk];
+  if (r.vis < 0) return;
+  const int gq = a.Hq / a.c.H, h = hh / gq;
+  const Tile own = a.tiles[r.own];
+  if (own.part0 < 0 && r.pre < 0) return;  // written already
+  float M = -INFINITY;
+  for (int s = 0; s < 2; ++s) {
+    if (s == 1 && r.pre < 0) break;
+    const Tile t = s ? a.tiles[r.pre] : own;
+    const int row = (s ? r.pre_at : r.own_at) * gq + hh % gq, step = t.n_tok * gq;
+    for (int k = lane; k < t.n_split; k += 64)
+      M = fmaxf(M, a.part_ml[int64_t(t.part0 + row + k * step) * a.c.H + h].x);
+  }
+#pragma unroll
+  for (int x = 32; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor(M, x, 64));
+  const float mu = M == -INFINITY ? 0.f : M;
+  constexpr int E = D / 64;
+  float L = 0.f, v[E] = {};
+  for (int s = 0; s < 2; ++s) {
+    if (s == 1 && r.pre < 0) break;
+    const Tile t = s ? a.tiles[r.pre] : own;
+    const int row = (s ? r.pre_at : r.own_at) * gq + hh % gq, step = t.n_tok * gq;
+    for (int k = 0; k < t.n_split; ++k) {
+      const int64_t pr = int64_t(t.part0 + row + k * step) * a.c.H + h;
+      const float2 ml = a.part_ml[pr];
+      const float f = __builtin_amdgcn_exp2f(ml.x - mu);
+      L += ml.y * f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] += a.part_o[pr * D + lane * E + e] * f;
+    }
+  }
+  const float f = L > 0.f || L != L ? 1.f / L : 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+    a.o[tk * a.ldo + int64_t(hh) * D + lane * E + e] = f32_to_bf16(v[e] * f);
+  if (a.lse && lane == 0) a.lse[int64_t(tk) * a.Hq + hh] = (M + log2f(L)) * 0.69314718055994531f;
+}
+
+// ---------------------------------------------------------------------------
+// checks and launches
+// ---------------------------------------------------------------------------
+bool misaligned(const void *p, uintptr_t m) { return reinterpret_cast<uintptr_t>(p) & (m - 1); }
+
+int check_batch(const tcl_attn_batch *b, const tcl_kv_cache *c, int32_t Hq, KvArgs *kv) {
+  int rc = kv_check(c, kv);
+  if (rc) return rc;
+  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256)
+    return fail(TCL_EUNSUPPORTED, "attn: head_dim %d is not 64, 128 or 256", c->head_dim);
+  if (!b) return fail(TCL_EINVAL, "attn: batch is NULL");
+  if (b->n_seqs < 0 || b->n_groups < 0 || b->n_tokens < 0 || b->ld_own < 0 || b->ld_prefix < 0)
+    return fail(TCL_EINVAL, "attn: negative size");
+  if (Hq < 1 || Hq % c->n_kv_heads)
+    return fail(TCL_EINVAL, "attn: n_q_heads %d is not a multiple of n_kv_heads %d", Hq,
+                c->n_kv_heads);
+  if (Hq / c->n_kv_heads > kRows)
+    return fail(TCL_EUNSUPPORTED, "attn: more than %d query heads a key head", kRows);
+  const int64_t lim = int64_t(1) << 30;
+  if (int64_t(b->ld_own) * c->page_size >= lim || int64_t(b->ld_prefix) * c->page_size >= lim)
+    return fail(TCL_EUNSUPPORTED, "attn: page tables of 2^30 keys or more");
+  if (int64_t(b->n_tokens) * Hq >= lim / 2 || b->n_seqs >= (1 << 24) || b->n_groups >= (1 << 24))
+    return fail(TCL_EUNSUPPORTED, "attn: n_tokens * n_q_heads, n_seqs or n_groups too large");
+  if (b->n_seqs > 0 && (!b->seq_tok_ptr || !b->group_seq_ptr || !b->own_len))
+    return fail(TCL_EINVAL, "attn: batch arrays are NULL");
+  if (b->n_seqs > 0 && b->n_groups < 1) return fail(TCL_EINVAL, "attn: requests without a group");
+  if (b->n_seqs > 0 && (!b->prefix_len || (b->ld_own > 0 && !b->own_pages) ||
+                        (b->ld_prefix > 0 && !b->prefix_pages)))
+    return fail(TCL_EINVAL, "attn: prefix_len or page tables are NULL");
+  const void *p[] = {b->seq_tok_ptr, b->group_seq_ptr, b->prefix_len,
+                     b->prefix_pages, b->own_len, b->own_pages};
+  for (const void *x : p)
+    if (misaligned(x, 4)) return fail(TCL_EALIGN, "attn: batch arrays must be 4-byte aligned");
+  return TCL_OK;
+}
+
+void sizes(const tcl_attn_batch *b, const KvArgs &kv, int32_t Hq, PlanArgs *a, Layout *L) {
+  const int gq = Hq / kv.H;
+  a->S = b->n_seqs, a->G = b->n_groups, a->T = b->n_tokens;
+  a->ldp = b->ld_prefix, a->ldo = b->ld_own;
+  a->Hq = Hq, a->Hkv = kv.H, a->D = kv.D, a->n_pages = kv.n_pages, a->page_shift = kv.page_shift;
+  a->tpt_many = kRows / gq;
+  a->tpt_few = gq <= kFew ? kFew / gq : a->tpt_many;
+  a->target = (kTargetWgs + kv.H - 1) / kv.H;
+  // tiles: whole ones of all tokens twice (own ranges, prefixes) and a
+  // broken one a unit; items: one a tile and the target; partial rows: every
+  // row twice and a whole tile for each item beyond its tile's first
+  a->cap_tiles = 2 * (b->n_tokens / a->tpt_many) + b->n_seqs + b->n_groups;
+  a->cap_items = a->cap_tiles + a->target;
+  a->cap_rows = 2 * b->n_tokens * gq + a->target * kRows;
+  size_t at = H_WORDS * 4;
+  auto take = [&](size_t n) {
+    const size_t o = at;
+    at = (at + n + 255) / 256 * 256;
+    return o;
+  };
+  L->o_tok = take(size_t(a->T) * sizeof(TokRec));
+  L->o_tiles = take(size_t(a->cap_tiles) * sizeof(Tile));
+  L->o_items = take(size_t(a->cap_items) * sizeof(Work));
+  L->o_list = take(size_t(a->T) * 4);
+  L->o_stok = take((size_t(a->S) + 1) * 4);
+  L->o_sseq = take((size_t(a->S) + 1) * 4);
+  L->o_utile = take((size_t(a->S) + a->G) * 4);
+  L->total = at;
+}
+
+size_t ws_rows_bytes(const PlanArgs &a) { return size_t(a.cap_rows) * a.Hkv * a.D * 4; }
+size_t ws_total(const PlanArgs &a) { return ws_rows_bytes(a) + size_t(a.cap_rows) * a.Hkv * 8; }
+
+int check_plan(const void *plan, size_t bytes, size_t need) {
+  if (!plan) return fail(TCL_EINVAL, "attn: plan is NULL");
+  if (misaligned(plan, 256)) return fail(TCL_EALIGN, "attn: plan must be 256-byte aligned");
+  if (bytes < need) return fail(TCL_ENOSPC, "attn: plan holds %zu bytes, needs %zu", bytes, need);
+  return TCL_OK;
+}
+
+template <int D>
+void launch(const AttnArgs &a, int cap_items, hipStream_t s) {
+  hipLaunchKernelGGL(attn_kernel<D>, dim3(unsigned(cap_items) * a.c.H), dim3(256), 0, s, a);
+  const int64_t rows = int64_t(a.T) * a.Hq;
+  hipLaunchKernelGGL(attn_join_kernel<D>, dim3(unsigned((rows + 3) / 4)), dim3(256), 0, s, a);
+}
+
+}  // namespace
+}  // namespace tcl
+
+using namespace tcl;
+
+extern "C" int tcl_attn_plan_bytes(const tcl_attn_batch *b, const tcl_kv_cache *c,
+                                   int32_t n_q_heads, size_t *bytes) {
+  if (!bytes) return fail(TCL_EINVAL, "attn: bytes is NULL");
+  KvArgs kv;
+  int rc = check_batch(b, c, n_q_heads, &kv);
+  if (rc) return rc;
+  PlanArgs a{};
+  Layout L;
+  sizes(b, kv, n_q_heads, &a, &L);
+  *bytes = L.total;
+  return TCL_OK;
+}
+
+extern "C" int tcl_attn_workspace_bytes(const tcl_attn_batch *b, const tcl_kv_cache *c,
+                                        int32_t n_q_heads, size_t *bytes) {
+  if (!bytes) return fail(TCL_EINVAL, "attn: bytes is NULL");
+  KvArgs kv;
+  int rc = check_batch(b, c, n_q_heads, &kv);
+  if (rc) return rc;
+  PlanArgs a{};
+  Layout L;
+  sizes(b, kv, n_q_heads, &a, &L);
+  *bytes = ws_total(a);
+  return TCL_OK;
+}
+
+extern "C" int tcl_attn_plan(const tcl_attn_batch *b, const tcl_kv_cache *c, int32_t n_q_heads,
+                             void *plan, size_t plan_bytes, void *stream) {
+  KvArgs kv;
+  int rc = check_batch(b, c, n_q_heads, &kv);
+  if (rc) return rc;
+  PlanArgs a{};
+  Layout L;
+  sizes(b, kv, n_q_heads, &a, &L);
+  if ((rc = check_plan(plan, plan_bytes, L.total))) return rc;
+  if (b->n_seqs == 0) {
+    // no table is read
+    a.S = a.G = 0;
+  }
+  char *p = static_cast<char *>(plan);
+  a.seq_tok = b->seq_tok_ptr, a.group_seq = b->group_seq_ptr, a.prefix_len = b->prefix_len;
+  a.prefix_pages = b->prefix_pages, a.own_len = b->own_len, a.own_pages = b->own_pages;
+  a.hdr = reinterpret_cast<int32_t *>(p);
+  a.tok = reinterpret_cast<TokRec *>(p + L.o_tok);
+  a.tiles = reinterpret_cast<Tile *>(p + L.o_tiles);
+  a.items = reinterpret_cast<Work *>(p + L.o_items);
+  a.list = reinterpret_cast<int32_t *>(p + L.o_list);
+  a.short_tok = reinterpret_cast<int32_t *>(p + L.o_stok);
+  a.short_seq = reinterpret_cast<int32_t *>(p + L.o_sseq);
+  a.utile = reinterpret_cast<int32_t *>(p + L.o_utile);
+  hipLaunchKernelGGL(attn_plan_kernel, dim3(1), dim3(kMapThreads), 0,
+                     static_cast<hipStream_t>(stream), a);
+  TCL_HIP(hipGetLastError());
+  return TCL_OK;
+}
+
+extern "C" int tcl_attn_status_async(const void *plan, int32_t *dev_status, void *stream) {
+  if (!plan || !dev_status) return fail(TCL_EINVAL, "attn: plan and dev_status are required");
+  if (misaligned(plan, 256) || misaligned(dev_status, 4))
+    return fail(TCL_EALIGN, "attn: plan must be 256-byte, dev_status 4-byte aligned");
+  hipLaunchKernelGGL(attn_status_kernel, dim3(1), dim3(64), 0, static_cast<hipStream_t>(stream),
+                     static_cast<const int32_t *>(plan), dev_status);
+  TCL_HIP(hipGetLastError());
+  return TCL_OK;
+}
+
+extern "C" int tcl_attn_apply(const tcl_attn_batch *b, const tcl_kv_cache *c, int32_t n_q_heads,
+                              const void *plan, size_t plan_bytes, const void *q, int64_t ldq,
+                              void *o, int64_t ldo, float *lse, float scale, void *ws,
+                              size_t ws_bytes, void *stream) {
+  AttnArgs a{};
+  int rc = check_batch(b, c, n_q_heads, &a.c);
+  if (rc) return rc;
+  PlanArgs s{};
+  Layout L;
+  sizes(b, a.c, n_q_heads, &s, &L);
+  if ((rc = check_plan(plan, plan_bytes, L.total))) return rc;
+  const int64_t row = int64_t(n_q_heads) * c->head_dim;
+  if (ldq < row || ldo < row) return fail(TCL_EINVAL, "attn: ldq or ldo below the heads of a row");
+  if (ldq % 8 || ldo % 8) return fail(TCL_EALIGN, "attn: ldq and ldo must be multiples of 8");
+  if (!std::isfinite(scale)) return fail(TCL_EINVAL, "attn: scale is not finite");
+  if (b->n_tokens == 0 || b->n_seqs == 0) return TCL_OK;
+  if (!q || !o || !ws) return fail(TCL_EINVAL, "attn: q, o and ws are required");
+  if (misaligned(q, 16) || misaligned(o, 16) || misaligned(lse, 4) || misaligned(ws, 256))
+    return fail(TCL_EALIGN, "attn: q and o must be 16-byte, lse 4-byte, ws 256-byte aligned");
+  if (ws_bytes < ws_total(s))
+    return fail(TCL_ENOSPC, "attn: workspace holds %zu bytes, needs %zu", ws_bytes, ws_total(s));
+  const char *p = static_cast<const char *>(plan);
+  a.q = static_cast<const uint16_t *>(q), a.o = static_cast<uint16_t *>(o), a.lse = lse;
+  a.ldq = ldq, a.ldo = ldo, a.scale2 = scale * 1.44269504088896341f;
+  a.S = b->n_seqs, a.G = b->n_groups, a.T = b->n_tokens, a.ldp = b->ld_prefix;
+  a.ld_own = b->ld_own, a.Hq = n_q_heads;
+  a.prefix_pages = b->prefix_pages, a.own_pages = b->own_pages;
+  a.hdr = reinterpret_cast<const int32_t *>(p);
+  a.tok = reinterpret_cast<const TokRec *>(p + L.o_tok);
+  a.tiles = reinterpret_cast<const Tile *>(p + L.o_tiles);
+  a.items = reinterpret_cast<const Work *>(p + L.o_items);
+  a.list = reinterpret_cast<const int32_t *>(p + L.o_list);
+  a.part_o = static_cast<float *>(ws);
+  a.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(ws) + ws_rows_bytes(s));
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  switch (c->head_dim) {
+    case 64: launch<64>(a, s.cap_items, st); break;
+    case 128: launch<128>(a, s.cap_items, st); break;
+    default: launch<256>(a, s.cap_items, st); break;
+  }
+  TCL_HIP(hipGetLastError());
+  return TCL_OK;
+}

@@ -37,7 +37,8 @@ EXPORTS = ["tcl_last_error", "tcl_version", "tcl_plan_bytes", "tcl_plan_map", "t
            "tcl_module_pack_bytes", "tcl_module_pack", "tcl_fused_apply_noalloc",
            "tcl_bam_pool_init", "tcl_bam_load",
            "tcl_i8_quant", "tcl_i8_product", "tcl_i8_workspace_bytes", "tcl_i8_linear",
-           "tcl_kv_append"]
+           "tcl_kv_append", "tcl_attn_plan_bytes", "tcl_attn_workspace_bytes", "tcl_attn_plan",
+           "tcl_attn_status_async", "tcl_attn_apply"]
 
 # bytes of the static device workspace of tcl_fused_apply_noalloc
 SCRATCH_BYTES = 32 << 20
@@ -80,6 +81,15 @@ class KVDesc(ctypes.Structure):
 class RopeDesc(ctypes.Structure):
     _fields_ = [("inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int32),
                 ("interleaved", ctypes.c_int32)]
+
+
+class AttnBatch(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int32), ("n_groups", ctypes.c_int32),
+                ("n_tokens", ctypes.c_int32), ("ld_prefix", ctypes.c_int32),
+                ("ld_own", ctypes.c_int32), ("seq_tok_ptr", ctypes.c_void_p),
+                ("group_seq_ptr", ctypes.c_void_p), ("prefix_len", ctypes.c_void_p),
+                ("prefix_pages", ctypes.c_void_p), ("own_len", ctypes.c_void_p),
+                ("own_pages", ctypes.c_void_p)]
 
 
 _lib = None
@@ -151,6 +161,13 @@ def lib(path: Optional[str] = None):
                                 sz, vp]
     L.tcl_kv_append.argtypes = [ctypes.POINTER(KVDesc), ctypes.POINTER(RopeDesc), vp, i64, vp, i64,
                                 vp, i64, i32, i32, vp, i64, i32, vp, vp, vp]
+    bp, cp = ctypes.POINTER(AttnBatch), ctypes.POINTER(KVDesc)
+    L.tcl_attn_plan_bytes.argtypes = [bp, cp, i32, ctypes.POINTER(sz)]
+    L.tcl_attn_workspace_bytes.argtypes = [bp, cp, i32, ctypes.POINTER(sz)]
+    L.tcl_attn_plan.argtypes = [bp, cp, i32, vp, sz, vp]
+    L.tcl_attn_status_async.argtypes = [vp, vp, vp]
+    L.tcl_attn_apply.argtypes = [bp, cp, i32, vp, sz, vp, i64, vp, i64, vp, ctypes.c_float, vp, sz,
+                                 vp]
     L.tcl_lag_select.argtypes = [vp, vp, vp, i32, vp, i32, ctypes.c_double, ctypes.c_double,
                                  i32, i32, vp, vp]
     if path is None:
@@ -951,3 +968,130 @@ def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, pos: torch.Tenso
               q_out: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
     """tcl_kv_append; returns the rotated queries (None without q)."""
     return AppendCall(cache, k, v, pos, slot, rope, q, q_out)(stream)
+
+
+class AttnPlan:
+    """The mapping of an attention batch (tcl_attn_plan): requests in groups
+    that share a prefix.  int32 device tensors: seq_tok_ptr [n_seqs + 1],
+    group_seq_ptr [n_groups + 1], prefix_len [n_groups], prefix_pages
+    [n_groups, m], own_len [n_seqs], own_pages [n_seqs, n].  One plan serves
+    every layer whose cache has the sizes of ``cache``."""
+
+    def __init__(self, cache: KVCache, n_q_heads: int, seq_tok_ptr: torch.Tensor,
+                 group_seq_ptr: torch.Tensor, prefix_len: torch.Tensor,
+                 prefix_pages: torch.Tensor, own_len: torch.Tensor, own_pages: torch.Tensor,
+                 n_tokens: int, stream=None):
+        self.cache, self.n_q_heads, self.n_tokens = cache, int(n_q_heads), int(n_tokens)
+        self.device = cache.device
+        self._set(seq_tok_ptr, group_seq_ptr, prefix_len, prefix_pages, own_len, own_pages)
+        self._sizes = [getattr(self.batch, f) for f, _ in AttnBatch._fields_[:5]]
+        n = ctypes.c_size_t(0)
+        check(lib().tcl_attn_plan_bytes(ctypes.byref(self.batch), ctypes.byref(cache.desc),
+                                        self.n_q_heads, ctypes.byref(n)))
+        self.buf = torch.empty(n.value, dtype=torch.uint8, device=self.device)
+        check(lib().tcl_attn_workspace_bytes(ctypes.byref(self.batch), ctypes.byref(cache.desc),
+                                             self.n_q_heads, ctypes.byref(n)))
+        self.workspace_bytes = n.value
+        self._map(stream)
+
+    def _set(self, *table):
+        seq_tok_ptr, group_seq_ptr, prefix_len, prefix_pages, own_len, own_pages = table
+        S, G = seq_tok_ptr.shape[0] - 1, group_seq_ptr.shape[0] - 1
+        for name, t, n in (("seq_tok_ptr", seq_tok_ptr, S + 1),
+                           ("group_seq_ptr", group_seq_ptr, G + 1),
+                           ("prefix_len", prefix_len, G), ("own_len", own_len, S)):
+            _vector(f"AttnPlan: {name}", t, n, torch.int32)
+        ldp = _rows("AttnPlan: prefix_pages", prefix_pages, G)
+        ldo = _rows("AttnPlan: own_pages", own_pages, S)
+        if prefix_pages.dtype != torch.int32 or own_pages.dtype != torch.int32:
+            raise ValueError("AttnPlan: page tables must be int32")
+        if prefix_pages.shape[1] != ldp or own_pages.shape[1] != ldo:
+            raise ValueError("AttnPlan: page tables must be contiguous")
+        _same_device("AttnPlan", self.device, *table)
+        self.table = table
+        self.batch = AttnBatch(S, G, self.n_tokens, ldp, ldo, *[t.data_ptr() for t in table])
+
+    def _map(self, stream):
+        ctx, st = _on(self.device, stream, self.buf)
+        with ctx:
+            check(lib().tcl_attn_plan(ctypes.byref(self.batch), ctypes.byref(self.cache.desc),
+                                      self.n_q_heads, self.buf.data_ptr(), self.buf.numel(), st))
+
+    def remap(self, seq_tok_ptr, group_seq_ptr, prefix_len, prefix_pages, own_len, own_pages,
+              stream=None) -> None:
+        """Maps a batch of the same sizes into this plan (no allocation; in a
+        graph it follows what the tensors hold at each replay)."""
+        old = self.table, self.batch
+        self._set(seq_tok_ptr, group_seq_ptr, prefix_len, prefix_pages, own_len, own_pages)
+        if [getattr(self.batch, f) for f, _ in AttnBatch._fields_[:5]] != self._sizes:
+            self.table, self.batch = old
+            raise ValueError("AttnPlan.remap: a batch of other sizes needs a plan of its own")
+        self._map(stream)
+
+    def status_async(self, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """Queues a copy of {code, items, tiles, tokens that may share} into a
+        device int32 tensor of 4 entries (tcl_attn_status_async)."""
+        own = out is None
+        if own:
+            out = torch.empty(4, dtype=torch.int32, device=self.device)
+        _vector("AttnPlan: status", out, 4, torch.int32)
+        _same_device("AttnPlan", self.device, out)
+        ctx, st = _on(self.device, stream, *([out] if own else []))
+        with ctx:
+            check(lib().tcl_attn_status_async(self.buf.data_ptr(), out.data_ptr(), st))
+        return out
+
+    def status(self, stream=None) -> int:
+        """The mapping's verdict (TCL_OK or TCL_EINVAL); synchronises."""
+        out = self.status_async(stream=stream)
+        torch.cuda.synchronize(self.device)
+        return int(out[0].item())
+
+
+class AttnCall:
+    """Pre-marshalled arguments of tcl_attn_apply for repeated calls: each
+    call writes o (bf16 [n_tokens, q heads * head_dim], made here unless
+    given) and, if given, lse (fp32 [n_tokens, q heads]).  ``cache`` is the
+    layer's (the plan's by default); the workspace is the call's own, or
+    ``ws``; calls that may run at the same time need one each."""
+
+    def __init__(self, plan: AttnPlan, q: torch.Tensor, o: Optional[torch.Tensor] = None,
+                 lse: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                 cache: Optional[KVCache] = None, ws: Optional[torch.Tensor] = None):
+        cache = cache or plan.cache
+        if any(getattr(cache, f) != getattr(plan.cache, f)
+               for f in ("n_pages", "page_size", "n_kv_heads", "head_dim")):
+            raise ValueError("AttnCall: the cache's sizes are not the plan's")
+        T, row = plan.n_tokens, plan.n_q_heads * cache.head_dim
+        if o is None:
+            o = torch.empty(T, row, dtype=torch.bfloat16, device=q.device)
+        if q.dtype != torch.bfloat16 or o.dtype != torch.bfloat16:
+            raise TypeError("AttnCall: q and o must be bfloat16")
+        self.ldq, self.ldo = _rows("AttnCall: q", q, T, row), _rows("AttnCall: o", o, T, row)
+        if lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, plan.n_q_heads)
+                                or not lse.is_contiguous()):
+            raise ValueError("AttnCall: lse must be float32 [n_tokens, q heads], contiguous")
+        _same_device("AttnCall", plan.device, q, o, lse, cache.K, ws)
+        self.plan, self.cache, self.q, self.o, self.lse = plan, cache, q, o, lse
+        self.scale = cache.head_dim ** -0.5 if scale is None else float(scale)
+        if ws is None or ws.numel() * ws.element_size() < plan.workspace_bytes:
+            ws = torch.empty(max(plan.workspace_bytes, 256), dtype=torch.uint8, device=plan.device)
+        self.ws = ws
+
+    def __call__(self, stream=None) -> torch.Tensor:
+        p = self.plan
+        ctx, st = _on(p.device, stream, self.ws, self.o)
+        with ctx:
+            check(lib().tcl_attn_apply(
+                ctypes.byref(p.batch), ctypes.byref(self.cache.desc), p.n_q_heads,
+                p.buf.data_ptr(), p.buf.numel(), self.q.data_ptr(), self.ldq, self.o.data_ptr(),
+                self.ldo, _ptr(self.lse), self.scale, self.ws.data_ptr(),
+                self.ws.numel() * self.ws.element_size(), st))
+        return self.o
+
+
+def attention(plan: AttnPlan, q: torch.Tensor, o: Optional[torch.Tensor] = None,
+              lse: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+              cache: Optional[KVCache] = None, stream=None) -> torch.Tensor:
+    """tcl_attn_apply: attention of the plan's batch over the cache."""
+    return AttnCall(plan, q, o, lse, scale, cache)(stream)

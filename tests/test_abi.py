@@ -442,3 +442,55 @@ def test_kv_append_host_errors(L):
     assert [call(page_size=24), call(page_size=0), call(page_size=2048), call(head_dim=72),
             call(head_dim=272), call(rot_dim=24), call(rot_dim=80), call(rot_dim=-16),
             call(xd=2)] == [U] * 9
+
+
+def test_attn_host_errors(L):
+    """The attention calls refuse bad sizes and pointers on the host (no GPU)."""
+    P = 0x1000
+    E, A, U = tclora.EINVAL, tclora.EALIGN, tclora.EUNSUPPORTED
+    out = ctypes.c_size_t(0)
+
+    def args(kw):
+        cd = dict(n_pages=4, page_size=16, n_kv_heads=2, head_dim=64, stride_page=2048,
+                  stride_slot=64, stride_head=1024, K=P, V=P)
+        bd = dict(n_seqs=3, n_groups=2, n_tokens=5, ld_prefix=4, ld_own=4, seq_tok_ptr=P,
+                  group_seq_ptr=P, prefix_len=P, prefix_pages=P, own_len=P, own_pages=P)
+        for d in (cd, bd):
+            d.update({n: kw.pop(n) for n in list(kw) if n in d})
+        return ctypes.byref(tclora.AttnBatch(**bd)), ctypes.byref(tclora.KVDesc(**cd))
+
+    def nbytes(f=L.tcl_attn_plan_bytes, Hq=4, res=ctypes.byref(out), **kw):
+        return f(*args(kw), Hq, res)
+
+    assert nbytes() == 0
+    need = out.value
+    assert need % 256 == 0 and nbytes(L.tcl_attn_workspace_bytes) == 0
+    ws = out.value
+    assert ws >= 2 * 5 * 2 * 2 * 64 * 4
+
+    def plan(Hq=4, p=0x10000, n=need, **kw):
+        return L.tcl_attn_plan(*args(kw), Hq, p, n, None)
+
+    def apply(Hq=4, p=0x10000, n=need, q=P, ldq=256, o=P, ldo=256, lse=None, scale=0.1,
+              w=0x20000, wn=ws, **kw):
+        return L.tcl_attn_apply(*args(kw), Hq, p, n, q, ldq, o, ldo, lse, scale, w, wn, None)
+
+    for f in (nbytes, lambda **k: nbytes(L.tcl_attn_workspace_bytes, **k), plan, apply):
+        assert [f(Hq=0), f(Hq=5), f(n_seqs=-1), f(n_tokens=-1), f(ld_own=-1), f(n_groups=0),
+                f(seq_tok_ptr=None), f(group_seq_ptr=None), f(own_len=None), f(own_pages=None),
+                f(prefix_len=None), f(prefix_pages=None), f(K=None)] == [E] * 13
+        assert [f(seq_tok_ptr=P + 2), f(own_pages=P + 1), f(stride_head=4)] == [A] * 3
+        assert [f(head_dim=96), f(page_size=3), f(Hq=2 * 129), f(ld_own=1 << 26),
+                f(n_tokens=1 << 28)] == [U] * 5
+    assert nbytes(res=None) == E and nbytes(L.tcl_attn_workspace_bytes, res=None) == E
+    for f in (plan, apply):
+        assert [f(p=None), f(p=0x10010), f(n=need - 1)] == [E, A, tclora.ENOSPC]
+    assert [apply(q=None), apply(o=None), apply(w=None), apply(ldq=192), apply(ldo=248),
+            apply(scale=float("nan")), apply(scale=float("inf"))] == [E] * 7
+    assert [apply(q=P + 8), apply(o=P + 2), apply(lse=P + 2), apply(w=0x20010), apply(ldq=260),
+            apply(ldo=260)] == [A] * 6
+    assert apply(wn=ws - 1) == tclora.ENOSPC
+    assert apply(n_tokens=0) == 0 and apply(n_seqs=0) == 0
+    assert L.tcl_attn_status_async(None, P, None) == E
+    assert L.tcl_attn_status_async(0x10000, None, None) == E
+    assert L.tcl_attn_status_async(0x10010, P, None) == A
