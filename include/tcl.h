@@ -581,14 +581,28 @@ int tcl_lag_select(const double *arrival, const int32_t *req_ptr, const int32_t 
 
 /* One int8 base weight.  d_in is a multiple of 16 and at most
  * TCL_I8_MAX_D_IN (the integer sums then fit 32 bits for any entries), d_out
- * a multiple of 8.  Rows are contiguous; W is 16-byte, scale 4-byte aligned. */
+ * a multiple of 8.  Rows are contiguous; W is 16-byte, scale 4-byte aligned.
+ * W_p is an optional copy in the order the matrix cores take it
+ * (tcl_i8_pack); where it is given the products read it and W may be NULL. */
 #define TCL_I8_MAX_D_IN 131056
 typedef struct {
   int32_t d_in;
   int32_t d_out;
   const int8_t *W;     /* device [d_out][d_in] */
   const float *scale;  /* device [d_out]       */
+  const void *W_p;     /* device, or NULL      */
 } tcl_i8_weight;
+
+/*
+ * The packed copy: blocks of 16 rows by 64 columns (rows and columns padded
+ * with zeros), the block of rows 16 i .. and columns 64 j .. at 1024 * (i *
+ * ceil(d_in / 64) + j), the 16 columns 16 g .. of its row r at 256 g + 16 r.
+ * tcl_i8_pack writes it on `stream` into W_p (caller-owned device memory of
+ * tcl_i8_pack_bytes bytes, 256-byte aligned) and sets w->W_p.
+ * Errors: TCL_EINVAL, TCL_EALIGN, TCL_ENOSPC, TCL_EUNSUPPORTED, TCL_EHIP.
+ */
+int tcl_i8_pack_bytes(const tcl_i8_weight *w, size_t *bytes);
+int tcl_i8_pack(tcl_i8_weight *w, void *W_p, size_t bytes, void *stream);
 
 /*
  * Activations to 8 bits, a scale for each token:

@@ -4,9 +4,16 @@
 //   i8_skinny  few tokens: the weight streams once from memory straight into
 //              matrix-core operands, the waves of a workgroup split d_in and
 //              add their integer sums in LDS;
-//   i8_tile    many tokens: tiles of both operands go through LDS, double
-//              buffered, and the time is the matrix cores'.
+//   i8_tile    many tokens: tiles of both operands go through LDS, three
+//              stages deep, and the time is the matrix cores'.
 // Integer sums are exact in any order, so neither split changes a result.
+//
+// Both read their operands in blocks of 16 rows by 64 bytes, the 16-byte
+// chunk g of row r at 256 g + 16 r: the order in which the lanes of a wave
+// take them, so that a load instruction reads 1 KiB in a row.  The packed
+// weight (tcl_i8_pack) and the activations tcl_i8_linear rounds itself are
+// stored so.  From rows in memory the same instruction touches 16 lines a row
+// stride apart, and the kernels take about twice as long at few tokens.
 #include <cmath>
 
 #include "kern_common.hpp"
@@ -17,10 +24,30 @@ namespace {
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x16 __attribute__((ext_vector_type(16)));
 
+// An int8 matrix of n rows: in rows (ld bytes apart) or in blocks (kb blocks
+// a row of blocks).
+struct Mat8 {
+  const int8_t *p;
+  int64_t ld;
+  int32_t n, kb, packed;
+};
+
+// Offset of chunk g of row r in the first block, and the step to the next one.
+__device__ inline int64_t mat_at(const Mat8 &m, int r, int g) {
+  if (m.packed) {
+    r = min(r, (m.n - 1) | 15);  // rows are padded to whole blocks
+    return int64_t(r >> 4) * m.kb * 1024 + g * 256 + (r & 15) * 16;
+  }
+  return int64_t(min(r, m.n - 1)) * m.ld + g * 16;
+}
+__device__ inline int mat_step(const Mat8 &m) { return m.packed ? 1024 : 64; }
+
 // ---------------------------------------------------------------------------
 // activations to 8 bits
 // ---------------------------------------------------------------------------
-constexpr int kQThreads = 256;
+// 64 bytes of a block's chunk column are four rows: a workgroup of four rows
+// writes whole sectors.
+constexpr int kQRows = 4;
 // chunks of 16 elements a thread keeps in registers between the two passes;
 // longer rows are read again from L2
 constexpr int kQKeep = 4;
@@ -28,51 +55,45 @@ constexpr int kQKeep = 4;
 struct QuantArgs {
   const void *x;
   int64_t ldx, ldq;
-  int32_t d;
+  int32_t T, d, kb, packed;
   int8_t *q;
   float *scale;
 };
 
-struct Chunk16 {
-  float v[16];
+template <typename T>
+struct Raw16;  // 16 elements as loaded
+
+template <>
+struct Raw16<bf16_t> {
+  nt_u4 u[2];
+  __device__ inline void load(const void *row, int c) {
+    const nt_u4 *p = reinterpret_cast<const nt_u4 *>(row) + 2 * c;
+    u[0] = p[0];
+    u[1] = p[1];
+  }
+  __device__ inline float at(int i) const {
+    const uint32_t w = u[i >> 3][(i >> 1) & 3];
+    return i & 1 ? bf16_hi(w) : bf16_lo(w);
+  }
 };
 
-template <typename T>
-__device__ inline void load16(const void *row, int c, Chunk16 &o);
-
 template <>
-__device__ inline void load16<bf16_t>(const void *row, int c, Chunk16 &o) {
-  const uint4 *p = reinterpret_cast<const uint4 *>(row) + 2 * c;
-  uint4 u[2] = {p[0], p[1]};
+struct Raw16<float> {
+  nt_f4 f[4];
+  __device__ inline void load(const void *row, int c) {
+    const nt_f4 *p = reinterpret_cast<const nt_f4 *>(row) + 4 * c;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint32_t w[4] = {u[h].x, u[h].y, u[h].z, u[h].w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      o.v[8 * h + 2 * i] = bf16_lo(w[i]);
-      o.v[8 * h + 2 * i + 1] = bf16_hi(w[i]);
-    }
+    for (int i = 0; i < 4; ++i) f[i] = p[i];
   }
-}
-
-template <>
-__device__ inline void load16<float>(const void *row, int c, Chunk16 &o) {
-  const float4 *p = reinterpret_cast<const float4 *>(row) + 4 * c;
-#pragma unroll
-  for (int h = 0; h < 4; ++h) {
-    const float4 f = p[h];
-    o.v[4 * h] = f.x;
-    o.v[4 * h + 1] = f.y;
-    o.v[4 * h + 2] = f.z;
-    o.v[4 * h + 3] = f.w;
-  }
-}
+  __device__ inline float at(int i) const { return f[i >> 2][i & 3]; }
+};
 
 // The largest magnitude as raw bits without the sign: their order is the
 // numbers' order, and a NaN (above infinity's bits) wins over everything.
-__device__ inline uint32_t absmax16(const Chunk16 &c, uint32_t m) {
+template <typename R>
+__device__ inline uint32_t absmax16(const R &c, uint32_t m) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(c.v[i]) & 0x7fffffffu);
+  for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(c.at(i)) & 0x7fffffffu);
   return m;
 }
 
@@ -90,74 +111,96 @@ __device__ inline int round_quotient(float v, float s) {
   return int(fminf(fmaxf(n, -127.f), 127.f));
 }
 
-__device__ inline void store_q(int8_t *row, int c, const Chunk16 &x, float s) {
-  const bool zero = !(s > 0.f);  // a row of zeros, or a NaN scale
-  int w[4];
+template <typename R>
+__device__ inline i32x4 quant16(const R &x, float s) {
+  i32x4 w = {0, 0, 0, 0};
+  if (!(s > 0.f)) return w;  // a row of zeros, or a NaN scale
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     uint32_t b = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      b |= uint32_t(uint8_t(zero ? 0 : round_quotient(x.v[4 * i + j], s))) << (8 * j);
+      b |= uint32_t(uint8_t(round_quotient(x.at(4 * i + j), s))) << (8 * j);
     w[i] = int(b);
   }
-  reinterpret_cast<i32x4 *>(row)[c] = i32x4{w[0], w[1], w[2], w[3]};
+  return w;
 }
 
-// One workgroup a token: the row is read once into registers, its largest
-// magnitude reduced, the integers written.
-template <typename T>
-__global__ __launch_bounds__(kQThreads) void i8_quant_kernel(QuantArgs a) {
-  __shared__ uint32_t wmax[kQThreads / 64];
-  const int tid = threadIdx.x;
-  const int64_t t = blockIdx.x;
-  const char *row = static_cast<const char *>(a.x) + t * a.ldx * int64_t(sizeof(T));
-  int8_t *qrow = a.q + t * a.ldq;
-  const int nc = a.d / 16;
-  Chunk16 keep[kQKeep];
+// WPR waves a row, kQRows rows a workgroup: a row is read once into
+// registers, its largest magnitude reduced, the integers written.
+template <typename T, int WPR>
+__global__ __launch_bounds__(64 * WPR * kQRows) void i8_quant_kernel(QuantArgs a) {
+  __shared__ uint32_t wmax[kQRows][WPR];
+  constexpr int TH = 64 * WPR;
+  const int tid = threadIdx.x % TH, r = threadIdx.x / TH;
+  const int t = blockIdx.x * kQRows + r;
+  const bool live = t < a.T;
+  const char *row = static_cast<const char *>(a.x) + int64_t(live ? t : 0) * a.ldx * int64_t(sizeof(T));
+  const int nc = live ? a.d / 16 : 0;
+  Raw16<T> keep[kQKeep];
   uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < kQKeep; ++i) {
-    const int c = tid + i * kQThreads;
-    if (c < nc) {
-      load16<T>(row, c, keep[i]);
-      m = absmax16(keep[i], m);
-    }
-  }
-  for (int c = tid + kQKeep * kQThreads; c < nc; c += kQThreads) {
-    Chunk16 x;
-    load16<T>(row, c, x);
+  for (int i = 0; i < kQKeep; ++i)
+    if (tid + i * TH < nc) keep[i].load(row, tid + i * TH);
+#pragma unroll
+  for (int i = 0; i < kQKeep; ++i)
+    if (tid + i * TH < nc) m = absmax16(keep[i], m);
+  for (int c = tid + kQKeep * TH; c < nc; c += TH) {
+    Raw16<T> x;
+    x.load(row, c);
     m = absmax16(x, m);
   }
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) m = max(m, uint32_t(__shfl_xor(int(m), o, 64)));
-  if ((tid & 63) == 0) wmax[tid >> 6] = m;
-  __syncthreads();
+  if constexpr (WPR > 1) {
+    if ((tid & 63) == 0) wmax[r][tid >> 6] = m;
+    __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kQThreads / 64; ++w) m = max(m, wmax[w]);
+    for (int w = 0; w < WPR; ++w) m = max(m, wmax[r][w]);
+  }
+  if (!live) return;
   const float s = m >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : __uint_as_float(m) / 127.f;
   if (tid == 0) a.scale[t] = s;
+  auto put = [&](int c, i32x4 w) {
+    int8_t *p = a.packed ? a.q + (int64_t(t >> 4) * a.kb + (c >> 2)) * 1024 + (c & 3) * 256 + (t & 15) * 16
+                         : a.q + int64_t(t) * a.ldq + 16 * c;
+    *reinterpret_cast<i32x4 *>(p) = w;
+  };
 #pragma unroll
-  for (int i = 0; i < kQKeep; ++i) {
-    const int c = tid + i * kQThreads;
-    if (c < nc) store_q(qrow, c, keep[i], s);
+  for (int i = 0; i < kQKeep; ++i)
+    if (tid + i * TH < nc) put(tid + i * TH, quant16(keep[i], s));
+  for (int c = tid + kQKeep * TH; c < nc; c += TH) {
+    Raw16<T> x;
+    x.load(row, c);
+    put(c, quant16(x, s));
   }
-  for (int c = tid + kQKeep * kQThreads; c < nc; c += kQThreads) {
-    Chunk16 x;
-    load16<T>(row, c, x);
-    store_q(qrow, c, x, s);
-  }
+  // the last block's chunks behind the row
+  if (a.packed && tid < 4 * a.kb - nc) put(nc + tid, i32x4{0, 0, 0, 0});
+}
+
+// Rows to blocks, zeros behind them; a thread a chunk.
+__global__ __launch_bounds__(256) void i8_pack_kernel(const int8_t *W, int32_t K, int32_t N,
+                                                      int32_t kb, int8_t *out) {
+  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t blk = i >> 6;
+  const int64_t rb = blk / kb;
+  if (rb >= (N + 15) / 16) return;
+  const int r = int(rb) * 16 + int(i & 15), k = int(blk % kb) * 64 + 16 * int((i >> 4) & 3);
+  i32x4 v = {0, 0, 0, 0};
+  if (r < N && k < K) v = *reinterpret_cast<const i32x4 *>(W + int64_t(r) * K + k);
+  reinterpret_cast<i32x4 *>(out)[i] = v;
 }
 
 // ---------------------------------------------------------------------------
 // product
 // ---------------------------------------------------------------------------
 struct ProdArgs {
-  const int8_t *W, *q;
+  Mat8 w, x;
   const float *ws, *xs;
   void *y;
-  int64_t ldq, ldy;
+  int64_t ldy;
   int32_t T, K, N;
+  int32_t t0;      // i8_skinny: first token
   int32_t nt, nc;  // i8_tile: token tiles, channel tiles
 };
 
@@ -179,49 +222,58 @@ __device__ inline void store_y4(const ProdArgs &a, int t, int c, i32x4 s) {
   }
 }
 
-// 16 * MB channels by 16 * NB tokens; wave w of WV takes the 128-byte groups
-// of d_in w, w + WV, ...  v_mfma_i32_16x16x64_i8 with the weight's rows as
-// the first operand: a lane of the result holds four channels of one token.
-// U groups are loaded before their products.
-template <int MB, int NB, int WV, int U, typename TY>
+// 16 * MB channels by 16 * NB tokens; wave w of WV takes the pairs of 64-byte
+// blocks w, w + WV, ... of d_in.  v_mfma_i32_16x16x64_i8 with the weight's
+// rows as the first operand: a lane of the result holds four channels of one
+// token.  The operands of P pairs are in flight or in use at a time.
+template <int MB, int NB, int WV, int P, typename TY>
 __global__ __launch_bounds__(64 * WV) void i8_skinny(ProdArgs a) {
-  __shared__ i32x4 part[WV][MB * NB][64];
+  __shared__ i32x4 part[WV / 2][MB * NB][64];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int c0 = blockIdx.x * 16 * MB, t0 = blockIdx.y * 16 * NB;
-  const int r = lane & 15, kg = 16 * (lane >> 4);
+  const int c0 = blockIdx.x * 16 * MB, t0 = a.t0 + blockIdx.y * 16 * NB;
+  const int r = lane & 15, g = lane >> 4;
   const int8_t *wp[MB], *xp[NB];
 #pragma unroll
-  for (int m = 0; m < MB; ++m)
-    wp[m] = a.W + int64_t(min(c0 + 16 * m + r, a.N - 1)) * a.K;
+  for (int m = 0; m < MB; ++m) wp[m] = a.w.p + mat_at(a.w, c0 + 16 * m + r, g);
 #pragma unroll
-  for (int n = 0; n < NB; ++n)
-    xp[n] = a.q + int64_t(min(t0 + 16 * n + r, a.T - 1)) * a.ldq;
+  for (int n = 0; n < NB; ++n) xp[n] = a.x.p + mat_at(a.x, t0 + 16 * n + r, g);
+  const int sw = mat_step(a.w), sx = mat_step(a.x);
+  const int kb = (a.K + 63) / 64;
   i32x4 acc[MB][NB];
 #pragma unroll
   for (int m = 0; m < MB; ++m)
 #pragma unroll
     for (int n = 0; n < NB; ++n) acc[m][n] = i32x4{0, 0, 0, 0};
-  const int groups = (a.K + 127) / 128;
-  for (int g = w; g < groups; g += WV * U) {
-    i32x4 wf[U][2][MB], xf[U][2][NB];
+  i32x4 wf[P][2][MB], xf[P][2][NB];
+  auto load = [&](int p, int pair) {
+    int b[2];
+    bool in[2];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int h = 0; h < 2; ++h) {
+      // past the row's end: any bytes of the weight times zeros
+      b[h] = 2 * pair + h;
+      in[h] = 64 * b[h] + 16 * g < a.K;
+      if (!in[h]) b[h] = 0;
+    }
+#pragma unroll
+    for (int m = 0; m < MB; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        wf[p][h][m] = *reinterpret_cast<const i32x4 *>(wp[m] + int64_t(b[h]) * sw);
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        // past the row's end: any bytes of the weight's row times zeros
-        const int k = (g + u * WV) * 128 + 64 * h + kg;
-        const bool in = k < a.K;
-        const int kc = in ? k : 0;
-#pragma unroll
-        for (int m = 0; m < MB; ++m) wf[u][h][m] = *reinterpret_cast<const i32x4 *>(wp[m] + kc);
-#pragma unroll
-        for (int n = 0; n < NB; ++n) {
-          xf[u][h][n] = *reinterpret_cast<const i32x4 *>(xp[n] + kc);
-          if (!in) xf[u][h][n] = i32x4{0, 0, 0, 0};
-        }
+        xf[p][h][n] = *reinterpret_cast<const i32x4 *>(xp[n] + int64_t(b[h]) * sx);
+        if (!in[h]) xf[p][h][n] = i32x4{0, 0, 0, 0};
       }
+  };
+  const int pairs = (kb + 1) / 2;
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+  for (int p = 0; p < P; ++p) load(p, w + p * WV);
+  for (int i = w; i < pairs; i += P * WV) {
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -229,115 +281,167 @@ __global__ __launch_bounds__(64 * WV) void i8_skinny(ProdArgs a) {
 #pragma unroll
           for (int n = 0; n < NB; ++n)
             acc[m][n] =
-                __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[u][h][m], xf[u][h][n], acc[m][n], 0, 0, 0);
+                __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[p][h][m], xf[p][h][n], acc[m][n], 0, 0, 0);
+      load(p, i + (P + p) * WV);  // (zeros past the end)
+    }
   }
+  // the waves' sums, halves added to halves
 #pragma unroll
-  for (int m = 0; m < MB; ++m)
+  for (int s = WV / 2; s > 0; s >>= 1) {
+    if (w >= s && w < 2 * s) {
 #pragma unroll
-    for (int n = 0; n < NB; ++n) part[w][m * NB + n][lane] = acc[m][n];
-  __syncthreads();
-  for (int j = threadIdx.x; j < MB * NB * 64; j += 64 * WV) {
-    const int b = j >> 6, l = j & 63;
-    i32x4 s = part[0][b][l];
+      for (int m = 0; m < MB; ++m)
 #pragma unroll
-    for (int v = 1; v < WV; ++v) s += part[v][b][l];
-    const int c = c0 + 16 * (b / NB) + 4 * (l >> 4), t = t0 + 16 * (b % NB) + (l & 15);
-    if (c < a.N && t < a.T) store_y4<TY>(a, t, c, s);
+        for (int n = 0; n < NB; ++n) part[w - s][m * NB + n][lane] = acc[m][n];
+    }
+    __syncthreads();
+    if (w < s) {
+#pragma unroll
+      for (int m = 0; m < MB; ++m)
+#pragma unroll
+        for (int n = 0; n < NB; ++n) acc[m][n] += part[w][m * NB + n][lane];
+    }
+    if (s > 1) __syncthreads();
+  }
+  if (w == 0) {
+#pragma unroll
+    for (int m = 0; m < MB; ++m)
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        const int c = c0 + 16 * m + 4 * g, t = t0 + 16 * n + r;
+        if (c < a.N && t < a.T) store_y4<TY>(a, t, c, acc[m][n]);
+      }
   }
 }
 
-// 128 channels by 128 tokens, 4 waves of 64 x 64, 128 bytes of d_in a step.
-// LDS holds rows of eight 16-byte chunks; chunk c of row r lies at c ^ ((r >>
-// 1) & 7), so that the 32 rows an operand load touches fall on all banks.
-constexpr int kTB = 128;
-
-template <typename TY>
-__global__ __launch_bounds__(256, 2) void i8_tile(ProdArgs a) {
-  __shared__ i32x4 lw[2][kTB * 8], lx[2][kTB * 8];
+// BC channels by BT tokens, WC x WT waves, one 64-byte block of d_in a step.
+// LDS holds three steps in the blocks' own order, which every operand load
+// reads in a row.  At the end of a step its successor lies in LDS whole, so a
+// wave reads its next operands before the barrier and goes on multiplying
+// behind it; the step after that is written from registers, and the loads of
+// the one after go out.  Reads and writes are dealt out among the matrix
+// instructions (sched_group_barrier): issued in one go they held the first
+// one back by some hundred cycles a step.
+template <int BC, int BT, int WC, int WT, typename TY>
+__global__ __launch_bounds__(64 * WC * WT, 2) void i8_tile(ProdArgs a) {
+  constexpr int TH = 64 * WC * WT;
+  constexpr int NW = BC * 4 / TH, NX = BT * 4 / TH;      // chunks a thread moves a step
+  constexpr int FC = BC / WC / 32, FT = BT / WT / 32;    // 32-row operands of a wave
+  __shared__ i32x4 lw[3][BC * 4], lx[3][BT * 4];
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   // workgroups go to the eight XCDs in turn: each gets a run of tiles, token
   // tiles next to each other, so that its L2 holds their weight rows
   const int n = a.nt * a.nc, per = (n + 7) / 8;
   const int id = int(blockIdx.x & 7) * per + int(blockIdx.x >> 3);
   if (int(blockIdx.x >> 3) >= per || id >= n) return;
-  const int c0 = id / a.nt * kTB, t0 = id % a.nt * kTB;
-  const int wc = (w & 1) * 64, wt = (w >> 1) * 64;
+  const int c0 = id / a.nt * BC, t0 = id % a.nt * BT;
 
-  const int8_t *gw[4], *gx[4];
-  int pos[4];
+  const int kb = (a.K + 63) / 64, sw = mat_step(a.w), sx = mat_step(a.x);
+  const int8_t *pw[NW], *px[NX];
+  const int g = (tid >> 4) & 3;  // the thread's chunk of a block's row
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int p = tid + 256 * i, row = p >> 3, c = p & 7;
-    gw[i] = a.W + int64_t(min(c0 + row, a.N - 1)) * a.K;
-    gx[i] = a.q + int64_t(min(t0 + row, a.T - 1)) * a.ldq;
-    pos[i] = row * 8 + (c ^ ((row >> 1) & 7));
-  }
-  const int kc = 16 * (tid & 7);
-  i32x4 rw[4], rx[4];
-  auto load = [&](int k0) {
-    const int k = k0 + kc;
-    const bool in = k < a.K;
-    const int kk = in ? k : 0;
+  for (int i = 0; i < NW; ++i)
+    pw[i] = a.w.p + mat_at(a.w, c0 + ((tid + i * TH) >> 6) * 16 + (tid & 15), g);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      rw[i] = *reinterpret_cast<const i32x4 *>(gw[i] + kk);
-      rx[i] = *reinterpret_cast<const i32x4 *>(gx[i] + kk);
-      if (!in) rx[i] = i32x4{0, 0, 0, 0};
-    }
+  for (int i = 0; i < NX; ++i)
+    px[i] = a.x.p + mat_at(a.x, t0 + ((tid + i * TH) >> 6) * 16 + (tid & 15), g);
+  i32x4 rw[NW], rx[NX];
+  auto load = [&](int st) {
+    const int b = 64 * st + 16 * g < a.K ? st : 0;
+#pragma unroll
+    for (int i = 0; i < NW; ++i)
+      rw[i] = *reinterpret_cast<const i32x4 *>(pw[i] + int64_t(b) * sw);
+#pragma unroll
+    for (int i = 0; i < NX; ++i)
+      rx[i] = *reinterpret_cast<const i32x4 *>(px[i] + int64_t(b) * sx);
   };
-  auto put = [&](int b) {
+  auto put = [&](int b, int st) {
+    const bool in = 64 * st + 16 * g < a.K;  // zeros past the row's end
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      lw[b][pos[i]] = rw[i];
-      lx[b][pos[i]] = rx[i];
-    }
+    for (int i = 0; i < NW; ++i) lw[b][tid + i * TH] = rw[i];
+#pragma unroll
+    for (int i = 0; i < NX; ++i) lx[b][tid + i * TH] = in ? rx[i] : i32x4{0, 0, 0, 0};
   };
-  i32x16 acc[2][2];
+  i32x16 acc[FC][FT];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < FC; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < FT; ++j)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
-
-  load(0);
-  put(0);
-  __syncthreads();
   const int r = lane & 31, h = lane >> 5;
-  int b = 0;
-  for (int k0 = 0; k0 < a.K; k0 += 128, b ^= 1) {
-    const bool more = k0 + 128 < a.K;
-    if (more) load(k0 + 128);
+  // operand rows r, r + 32, ... of the wave, chunk 2 s + h
+  const int aw = (w % WC) * (BC / WC) * 4 + (r >> 4) * 64 + h * 16 + (r & 15);
+  const int ax = (w / WC) * (BT / WT) * 4 + (r >> 4) * 64 + h * 16 + (r & 15);
+  i32x4 fw[2][FC], fx[2][FT];
+  auto read = [&](int b, int s) {
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      i32x4 fw[2], fx[2];
+    for (int i = 0; i < FC; ++i) fw[s][i] = lw[b][aw + i * 128 + s * 32];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int rw_ = wc + 32 * i + r, rx_ = wt + 32 * i + r;
-        fw[i] = lw[b][rw_ * 8 + ((2 * s + h) ^ ((rw_ >> 1) & 7))];
-        fx[i] = lx[b][rx_ * 8 + ((2 * s + h) ^ ((rx_ >> 1) & 7))];
+    for (int i = 0; i < FT; ++i) fx[s][i] = lx[b][ax + i * 128 + s * 32];
+  };
+  auto multiply = [&](int s) {
+#pragma unroll
+    for (int i = 0; i < FC; ++i)
+#pragma unroll
+      for (int j = 0; j < FT; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[s][i], fx[s][j], acc[i][j], 0, 0, 0);
+  };
+  // (LDS only: global loads stay in flight across it)
+  auto barrier = [&] {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+  };
+  constexpr int M = FC * FT, RD = FC + FT, WR = NW + NX, WRI = (WR + M / 2 - 1) / (M / 2);
+  load(0);
+  put(0, 0);
+  load(1);
+  put(1, 1);
+  load(2);
+  barrier();
+  read(0, 0);
+  int b0 = 0, b1 = 1, b2 = 2;
+  for (int st = 0; st < kb; ++st) {
+    read(b0, 1);
+    put(b2, st + 2);
+    load(st + 3);
+    multiply(0);
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);                  // a matrix instruction
+      if (i < RD) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);    // an LDS read
+      if (i >= M / 2) {
+        __builtin_amdgcn_sched_group_barrier(0x200, WRI, 0);            // LDS writes
+        __builtin_amdgcn_sched_group_barrier(0x20, WRI, 0);             // loads
       }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[i], fx[j], acc[i][j], 0, 0, 0);
     }
-    if (more) put(b ^ 1);
-    __syncthreads();
-  }
+    __builtin_amdgcn_sched_barrier(0);
+    read(b1, 0);
+    multiply(1);
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int t = t0 + wt + 32 * j + r;
+    for (int i = 0; i < M; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+      if (i < RD) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    barrier();
+    const int t = b0;
+    b0 = b1, b1 = b2, b2 = t;
+  }
+  const int wc = c0 + (w % WC) * (BC / WC), wt = t0 + (w / WC) * (BT / WT);
+#pragma unroll
+  for (int j = 0; j < FT; ++j) {
+    const int t = wt + 32 * j + r;
     if (t >= a.T) continue;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < FC; ++i)
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int c = c0 + wc + 32 * i + 8 * g + 4 * h;
+      for (int e = 0; e < 4; ++e) {
+        const int c = wc + 32 * i + 8 * e + 4 * h;
         if (c < a.N)
-          store_y4<TY>(a, t, c, i32x4{acc[i][j][4 * g], acc[i][j][4 * g + 1],
-                                      acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]});
+          store_y4<TY>(a, t, c, i32x4{acc[i][j][4 * e], acc[i][j][4 * e + 1],
+                                      acc[i][j][4 * e + 2], acc[i][j][4 * e + 3]});
       }
   }
 }
@@ -356,8 +460,9 @@ int check_weight(const tcl_i8_weight *w) {
   if (w->d_in % 16 || w->d_out % 8)
     return fail(TCL_EALIGN, "i8: d_in %d is not a multiple of 16 or d_out %d not of 8", w->d_in,
                 w->d_out);
-  if (w->d_out > 0 && (!w->W || !w->scale)) return fail(TCL_EINVAL, "i8: weight arrays are NULL");
-  if (misaligned(w->W, 16)) return fail(TCL_EALIGN, "i8: W must be 16-byte aligned");
+  if (w->d_out > 0 && ((!w->W && !w->W_p) || !w->scale)) return fail(TCL_EINVAL, "i8: weight arrays are NULL");
+  if (misaligned(w->W, 16) || misaligned(w->W_p, 256))
+    return fail(TCL_EALIGN, "i8: W must be 16-byte, W_p 256-byte aligned");
   if (misaligned(w->scale, 4)) return fail(TCL_EALIGN, "i8: scale must be 4-byte aligned");
   return TCL_OK;
 }
@@ -384,57 +489,104 @@ int check_y(const tcl_i8_weight *w, int32_t n_tokens, const void *y, int64_t ldy
   return TCL_OK;
 }
 
+int32_t blocks_of(int32_t d) { return (d + 63) / 64; }
+
 int launch_quant(const void *x, int64_t ldx, int xd, int32_t n, int32_t d, int8_t *q, int64_t ldq,
-                 float *scale, hipStream_t s) {
+                 bool packed, float *scale, hipStream_t s) {
   if (n == 0) return TCL_OK;
-  QuantArgs a{x, ldx, ldq, d, q, scale};
-  if (xd == TCL_BF16)
-    hipLaunchKernelGGL(i8_quant_kernel<bf16_t>, dim3(n), dim3(kQThreads), 0, s, a);
-  else
-    hipLaunchKernelGGL(i8_quant_kernel<float>, dim3(n), dim3(kQThreads), 0, s, a);
+  QuantArgs a{x, ldx, ldq, n, d, blocks_of(d), packed, q, scale};
+  const dim3 grid((n + kQRows - 1) / kQRows);
+  // few rows: four waves each, for the length of one row's work
+  const bool wide = n <= 1024;
+#define QUANT(T, W) hipLaunchKernelGGL((i8_quant_kernel<T, W>), grid, dim3(64 * W * kQRows), 0, s, a)
+  if (xd == TCL_BF16) {
+    if (wide) QUANT(bf16_t, 4);
+    else QUANT(bf16_t, 1);
+  } else {
+    if (wide) QUANT(float, 4);
+    else QUANT(float, 1);
+  }
+#undef QUANT
   TCL_HIP(hipGetLastError());
   return TCL_OK;
 }
 
-template <int MB, int NB, int WV, int U, typename TY>
+template <int MB, int NB, int WV, int P, typename TY>
 void go_skinny(const ProdArgs &a, hipStream_t s) {
-  hipLaunchKernelGGL((i8_skinny<MB, NB, WV, U, TY>),
-                     dim3((a.N + 16 * MB - 1) / (16 * MB), (a.T + 16 * NB - 1) / (16 * NB)),
+  hipLaunchKernelGGL((i8_skinny<MB, NB, WV, P, TY>),
+                     dim3((a.N + 16 * MB - 1) / (16 * MB), (a.T - a.t0 + 16 * NB - 1) / (16 * NB)),
                      dim3(64 * WV), 0, s, a);
 }
 
-template <int NB, typename TY>
-void skinny(const ProdArgs &a, hipStream_t s) {
-  const int64_t tb = (a.T + 16 * NB - 1) / (16 * NB);
-  if (tb * (a.N / 64) >= 192)
-    go_skinny<4, NB, 4, 1, TY>(a, s);
-  else if (tb * (a.N / 32) >= 192)
-    go_skinny<2, NB, 8, 1, TY>(a, s);
+template <int BC, int BT, int WC, int WT, typename TY>
+void go_tile(ProdArgs &a, hipStream_t s) {
+  a.nt = (a.T + BT - 1) / BT;
+  a.nc = (a.N + BC - 1) / BC;
+  hipLaunchKernelGGL((i8_tile<BC, BT, WC, WT, TY>), dim3((a.nt * a.nc + 7) / 8 * 8),
+                     dim3(64 * WC * WT), 0, s, a);
+}
+
+// Which kernel: by how many workgroups each would have, for 256 CUs (us on
+// packed operands of uniform random bytes, d_in 4096 unless said).
+//   up to 16 tokens: 16 channels a workgroup, 8 waves over d_in (1 token,
+//     1024 channels: 4.1; 32 channels: 5.5);
+//   up to 32: the same with two token blocks (4096 channels: 7.4; 32: 8.3);
+//   more, as long as 128 x 128 tiles are fewer than 192: 64 channels x 64
+//     tokens from 512 workgroups on (512 tokens x 4096 channels: 22.2, 32
+//     channels 27.8, tiles 28.4); 32 x 64, 4 waves, from 257 on (64 x 14336:
+//     20.3, 32 x 32 23.9; 177 x 4096 of d_in 14336: 34.8, 47.5); else 32 x 32,
+//     8 waves (128 x 4096: 10.6, 32 x 64 12.6);
+//   tiles of 128 x 128 (1024 x 4096: 31.3, 256 x 256 55), of 256 x 128 from
+//     384 of them on (4096 x 4096: 90, 128 x 128 106), of 256 x 256 from
+//     three rounds of them over the CUs on (4224 x 14336: 301, 256 x 128 310).
+template <typename TY>
+void product_skinny(const ProdArgs &a, hipStream_t s) {
+  const int64_t t = a.T - a.t0, tb = (t + 63) / 64;
+  if (t <= 16)
+    go_skinny<1, 1, 8, 2, TY>(a, s);
+  else if (t <= 32)
+    go_skinny<1, 2, 8, 2, TY>(a, s);
+  else if (tb * ((a.N + 63) / 64) >= 512)
+    go_skinny<4, 4, 4, 2, TY>(a, s);
+  else if (tb * ((a.N + 31) / 32) > 256)
+    go_skinny<2, 4, 4, 2, TY>(a, s);
   else
-    go_skinny<1, NB, 16, 1, TY>(a, s);
+    go_skinny<2, 2, 8, 2, TY>(a, s);
 }
 
 template <typename TY>
 void product(ProdArgs &a, hipStream_t s) {
-  if (a.T <= 256) {
-    if (a.T <= 16)
-      skinny<1, TY>(a, s);
-    else if (a.T <= 32)
-      skinny<2, TY>(a, s);
-    else
-      skinny<4, TY>(a, s);
-    return;
+  auto up = [](int64_t n, int64_t d) { return (n + d - 1) / d; };
+  if (a.T <= 32 || up(a.T, 128) * up(a.N, 128) < 192) {
+    product_skinny<TY>(a, s);
+  } else if (up(a.T, 256) * up(a.N, 256) > 768) {
+    go_tile<256, 256, 4, 2, TY>(a, s);
+  } else if (up(a.T, 128) * up(a.N, 256) >= 384) {
+    // two workgroups a CU: where at most a quarter of a last round is left,
+    // and that is few tokens, they go to the other kernel (4224 x 4096: 115
+    // in one launch; 90 + 11)
+    const int64_t nt = up(a.T, 128), nc = up(a.N, 256), left = nt * nc % 512, k = up(left, nc);
+    const bool split = nt * nc > 512 && left > 0 && left <= 128 && k <= 2;
+    const int T = a.T;
+    if (split) a.T = int((nt - k) * 128);
+    go_tile<256, 128, 4, 2, TY>(a, s);
+    if (split) {
+      a.t0 = a.T;
+      a.T = T;
+      product_skinny<TY>(a, s);
+    }
+  } else {
+    go_tile<128, 128, 4, 2, TY>(a, s);
   }
-  a.nt = (a.T + kTB - 1) / kTB;
-  a.nc = (a.N + kTB - 1) / kTB;
-  const int per = (a.nt * a.nc + 7) / 8;
-  hipLaunchKernelGGL(i8_tile<TY>, dim3(8 * per), dim3(256), 0, s, a);
 }
 
-int launch_product(const tcl_i8_weight *w, const int8_t *q, int64_t ldq, const float *scale,
-                   int32_t n, void *y, int64_t ldy, int yd, hipStream_t s) {
-  if (n == 0 || w->d_out == 0) return TCL_OK;
-  ProdArgs a{w->W, q, w->scale, scale, y, ldq, ldy, n, w->d_in, w->d_out, 0, 0};
+int launch_product(const tcl_i8_weight *w, const Mat8 &x, const float *scale, void *y, int64_t ldy,
+                   int yd, hipStream_t s) {
+  if (x.n == 0 || w->d_out == 0) return TCL_OK;
+  const int32_t kb = blocks_of(w->d_in);
+  const Mat8 wm = w->W_p ? Mat8{static_cast<const int8_t *>(w->W_p), 0, w->d_out, kb, 1}
+                         : Mat8{w->W, w->d_in, w->d_out, kb, 0};
+  ProdArgs a{wm, x, w->scale, scale, y, ldy, x.n, w->d_in, w->d_out, 0, 0, 0};
   if (yd == TCL_BF16)
     product<uint16_t>(a, s);
   else
@@ -443,9 +595,9 @@ int launch_product(const tcl_i8_weight *w, const int8_t *q, int64_t ldq, const f
   return TCL_OK;
 }
 
-// workspace of tcl_i8_linear: the integers, then the scales
+// workspace of tcl_i8_linear: the integers in blocks, then the scales
 size_t ws_q_bytes(const tcl_i8_weight *w, int32_t n) {
-  return (size_t(n) * size_t(w->d_in) + 255) / 256 * 256;
+  return (size_t(n) + 15) / 16 * size_t(blocks_of(w->d_in)) * 1024;
 }
 
 size_t ws_bytes_of(const tcl_i8_weight *w, int32_t n) {
@@ -466,7 +618,8 @@ extern "C" int tcl_i8_quant(const void *x, int64_t ldx, tcl_dtype xd, int32_t n_
   if (misaligned(q, 16) || ldq % 16)
     return fail(TCL_EALIGN, "i8: q must be 16-byte aligned, ldq a multiple of 16");
   if (misaligned(scale, 4)) return fail(TCL_EALIGN, "i8: scale must be 4-byte aligned");
-  return launch_quant(x, ldx, xd, n_tokens, d, q, ldq, scale, static_cast<hipStream_t>(stream));
+  return launch_quant(x, ldx, xd, n_tokens, d, q, ldq, false, scale,
+                      static_cast<hipStream_t>(stream));
 }
 
 extern "C" int tcl_i8_product(const tcl_i8_weight *w, const int8_t *q, int64_t ldq,
@@ -480,7 +633,32 @@ extern "C" int tcl_i8_product(const tcl_i8_weight *w, const int8_t *q, int64_t l
   if (misaligned(q, 16) || ldq % 16)
     return fail(TCL_EALIGN, "i8: q must be 16-byte aligned, ldq a multiple of 16");
   if (misaligned(scale, 4)) return fail(TCL_EALIGN, "i8: scale must be 4-byte aligned");
-  return launch_product(w, q, ldq, scale, n_tokens, y, ldy, yd, static_cast<hipStream_t>(stream));
+  return launch_product(w, Mat8{q, ldq, n_tokens, blocks_of(w->d_in), 0}, scale, y, ldy, yd,
+                        static_cast<hipStream_t>(stream));
+}
+
+extern "C" int tcl_i8_pack_bytes(const tcl_i8_weight *w, size_t *bytes) {
+  if (!bytes) return fail(TCL_EINVAL, "i8: bytes is NULL");
+  int rc = check_weight(w);
+  if (rc) return rc;
+  *bytes = (size_t(w->d_out) + 15) / 16 * size_t(blocks_of(w->d_in)) * 1024;
+  return TCL_OK;
+}
+
+extern "C" int tcl_i8_pack(tcl_i8_weight *w, void *W_p, size_t bytes, void *stream) {
+  size_t need = 0;
+  int rc = tcl_i8_pack_bytes(w, &need);
+  if (rc) return rc;
+  if (w->d_out == 0) return TCL_OK;
+  if (!w->W || !W_p) return fail(TCL_EINVAL, "i8: pack needs W and W_p");
+  if (misaligned(W_p, 256)) return fail(TCL_EALIGN, "i8: W_p must be 256-byte aligned");
+  if (bytes < need) return fail(TCL_ENOSPC, "i8: W_p holds %zu bytes, needs %zu", bytes, need);
+  hipLaunchKernelGGL(i8_pack_kernel, dim3(unsigned((need / 16 + 255) / 256)), dim3(256), 0,
+                     static_cast<hipStream_t>(stream), w->W, w->d_in, w->d_out,
+                     blocks_of(w->d_in), static_cast<int8_t *>(W_p));
+  TCL_HIP(hipGetLastError());
+  w->W_p = W_p;
+  return TCL_OK;
 }
 
 extern "C" int tcl_i8_workspace_bytes(const tcl_i8_weight *w, int32_t n_tokens, size_t *bytes) {
@@ -508,6 +686,6 @@ extern "C" int tcl_i8_linear(const tcl_i8_weight *w, const void *x, int64_t ldx,
   int8_t *q = static_cast<int8_t *>(ws);
   float *scale = reinterpret_cast<float *>(q + ws_q_bytes(w, n_tokens));
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if ((rc = launch_quant(x, ldx, xd, n_tokens, w->d_in, q, w->d_in, scale, s))) return rc;
-  return launch_product(w, q, w->d_in, scale, n_tokens, y, ldy, yd, s);
+  if ((rc = launch_quant(x, ldx, xd, n_tokens, w->d_in, q, 0, true, scale, s))) return rc;
+  return launch_product(w, Mat8{q, 0, n_tokens, blocks_of(w->d_in), 1}, scale, y, ldy, yd, s);
 }

@@ -37,6 +37,7 @@ EXPORTS = ["tcl_last_error", "tcl_version", "tcl_plan_bytes", "tcl_plan_map", "t
            "tcl_module_pack_bytes", "tcl_module_pack", "tcl_fused_apply_noalloc",
            "tcl_bam_pool_init", "tcl_bam_load",
            "tcl_i8_quant", "tcl_i8_product", "tcl_i8_workspace_bytes", "tcl_i8_linear",
+           "tcl_i8_pack_bytes", "tcl_i8_pack",
            "tcl_kv_append", "tcl_attn_plan_bytes", "tcl_attn_workspace_bytes", "tcl_attn_plan",
            "tcl_attn_status_async", "tcl_attn_apply"]
 
@@ -68,7 +69,7 @@ class ModuleDesc(ctypes.Structure):
 
 class I8WeightDesc(ctypes.Structure):
     _fields_ = [("d_in", ctypes.c_int32), ("d_out", ctypes.c_int32), ("W", ctypes.c_void_p),
-                ("scale", ctypes.c_void_p)]
+                ("scale", ctypes.c_void_p), ("W_p", ctypes.c_void_p)]
 
 
 class KVDesc(ctypes.Structure):
@@ -157,6 +158,8 @@ def lib(path: Optional[str] = None):
     L.tcl_i8_quant.argtypes = [vp, i64, i32, i32, i32, vp, i64, vp, vp]
     L.tcl_i8_product.argtypes = [ctypes.POINTER(I8WeightDesc), vp, i64, vp, i32, vp, i64, i32, vp]
     L.tcl_i8_workspace_bytes.argtypes = [ctypes.POINTER(I8WeightDesc), i32, ctypes.POINTER(sz)]
+    L.tcl_i8_pack_bytes.argtypes = [ctypes.POINTER(I8WeightDesc), ctypes.POINTER(sz)]
+    L.tcl_i8_pack.argtypes = [ctypes.POINTER(I8WeightDesc), vp, sz, vp]
     L.tcl_i8_linear.argtypes = [ctypes.POINTER(I8WeightDesc), vp, i64, i32, i32, vp, i64, i32, vp,
                                 sz, vp]
     L.tcl_kv_append.argtypes = [ctypes.POINTER(KVDesc), ctypes.POINTER(RopeDesc), vp, i64, vp, i64,
@@ -773,30 +776,59 @@ def _vector(what: str, t: torch.Tensor, n: int, dtype: torch.dtype) -> None:
         raise ValueError(f"{what} must be a contiguous {dtype} tensor of {n} entries")
 
 
+class _Here:
+    """The context of a call whose device is the current one."""
+
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE = _Here()
+
+
 def _on(dev: torch.device, stream, *tensors):
     """Context and stream handle of a call on ``dev``: the device is made the
     current one, and tensors the call allocated itself are kept for a stream
     other than the one they were allocated on."""
-    if stream is not None and isinstance(stream, torch.cuda.Stream):
+    i = dev.index
+    ctx = _HERE if torch.cuda.current_device() == i else torch.cuda.device(i)
+    if stream is None:
+        return ctx, torch._C._cuda_getCurrentRawStream(i)
+    if isinstance(stream, torch.cuda.Stream):
         for t in tensors:
             t.record_stream(stream)
-    return torch.cuda.device(dev), _stream(dev, stream)
+    return ctx, _stream(dev, stream)
 
 
 class I8Weight:
     """An int8 base weight: W int8 [d_out, d_in] and its channel scales fp32
-    [d_out], on the GPU (tcl_i8_weight)."""
+    [d_out], on the GPU (tcl_i8_weight).  The products read a copy in the
+    matrix cores' order (tcl_i8_pack), made here unless ``pack`` is False;
+    with it W itself is not kept."""
 
-    def __init__(self, W: torch.Tensor, scale: torch.Tensor):
+    def __init__(self, W: torch.Tensor, scale: torch.Tensor, pack: bool = True, stream=None):
         if W.dtype != torch.int8:
             raise TypeError("I8Weight: W must be int8")
         if W.dim() != 2 or not W.is_contiguous():
             raise ValueError("I8Weight: W must be [d_out, d_in], contiguous")
         _vector("I8Weight: scale", scale, W.shape[0], torch.float32)
         _same_device("I8Weight", W.device, scale)
-        self.W, self.scale = W, scale
+        self.W, self.scale, self.device = W, scale, W.device
         self.d_out, self.d_in = W.shape
-        self.desc = I8WeightDesc(self.d_in, self.d_out, W.data_ptr(), scale.data_ptr())
+        self.desc = I8WeightDesc(self.d_in, self.d_out, W.data_ptr(), scale.data_ptr(), None)
+        if pack and W.numel():
+            n = ctypes.c_size_t(0)
+            check(lib().tcl_i8_pack_bytes(ctypes.byref(self.desc), ctypes.byref(n)))
+            self.W_p = torch.empty(n.value, dtype=torch.uint8, device=W.device)
+            ctx, st = _on(W.device, stream, self.W_p)
+            if isinstance(stream, torch.cuda.Stream):
+                W.record_stream(stream)
+            with ctx:
+                check(lib().tcl_i8_pack(ctypes.byref(self.desc), self.W_p.data_ptr(), n.value, st))
+            self.W, self.desc.W = None, None
 
 
 def i8_quant(x: torch.Tensor, q: Optional[torch.Tensor] = None,
@@ -837,7 +869,7 @@ def i8_product(w: I8Weight, q: torch.Tensor, scale: torch.Tensor,
         y = torch.empty(T, w.d_out, dtype=y_dtype, device=q.device)
         own.append(y)
     ldy = _rows("i8_product: y", y, T, w.d_out)
-    _same_device("i8_product", q.device, scale, y, w.W)
+    _same_device("i8_product", q.device, scale, y, w.scale)
     ctx, st = _on(q.device, stream, *own)
     with ctx:
         check(lib().tcl_i8_product(ctypes.byref(w.desc), q.data_ptr(), ldq, scale.data_ptr(), T,
@@ -855,22 +887,22 @@ class I8Call:
         T = x.shape[0]
         self.ldx = _rows("I8Call: x", x, T, w.d_in)
         self.ldy = _rows("I8Call: y", y, T, w.d_out)
-        _same_device("I8Call", x.device, y, w.W, ws)
+        _same_device("I8Call", x.device, y, w.scale, ws)
         self.w, self.x, self.y, self.T = w, x, y, T
         self.xd, self.yd = _dtype_code(x.dtype), _dtype_code(y.dtype)
         need = ctypes.c_size_t(0)
         check(lib().tcl_i8_workspace_bytes(ctypes.byref(w.desc), T, ctypes.byref(need)))
         if ws is None or ws.numel() * ws.element_size() < need.value:
             ws = torch.empty(max(need.value, 256), dtype=torch.uint8, device=x.device)
-        self.ws = ws
+        self.ws, self.device = ws, x.device
+        self._fn = lib().tcl_i8_linear
+        self._args = (ctypes.byref(w.desc), x.data_ptr(), self.ldx, self.xd, T, y.data_ptr(),
+                      self.ldy, self.yd, ws.data_ptr(), ws.numel() * ws.element_size())
 
     def __call__(self, stream=None) -> torch.Tensor:
-        ctx, st = _on(self.x.device, stream, self.ws)
+        ctx, st = _on(self.device, stream, self.ws)
         with ctx:
-            check(lib().tcl_i8_linear(ctypes.byref(self.w.desc), self.x.data_ptr(), self.ldx,
-                                      self.xd, self.T, self.y.data_ptr(), self.ldy, self.yd,
-                                      self.ws.data_ptr(), self.ws.numel() * self.ws.element_size(),
-                                      st))
+            check(self._fn(*self._args, st))
         return self.y
 
 
@@ -950,16 +982,16 @@ class AppendCall:
         _same_device("AppendCall", cache.device, k, v, pos, slot, q, q_out, rope.inv_freq)
         self.cache, self.rope, self.k, self.v, self.q = cache, rope, k, v, q
         self.pos, self.slot, self.q_out, self.T = pos, slot, q_out, T
-        self.xd = _dtype_code(k.dtype)
+        self.xd, self.device = _dtype_code(k.dtype), cache.device
+        self._fn = lib().tcl_kv_append
+        self._args = (ctypes.byref(cache.desc), ctypes.byref(rope.desc), k.data_ptr(), self.ldk,
+                      v.data_ptr(), self.ldv, _ptr(q), self.ldq, self.Hq, self.xd, _ptr(q_out),
+                      self.ldqo, T, pos.data_ptr(), slot.data_ptr())
 
     def __call__(self, stream=None) -> Optional[torch.Tensor]:
-        ctx, st = _on(self.cache.device, stream, *([] if self.q_out is None else [self.q_out]))
+        ctx, st = _on(self.device, stream, *([] if self.q_out is None else [self.q_out]))
         with ctx:
-            check(lib().tcl_kv_append(
-                ctypes.byref(self.cache.desc), ctypes.byref(self.rope.desc), self.k.data_ptr(),
-                self.ldk, self.v.data_ptr(), self.ldv, _ptr(self.q), self.ldq, self.Hq, self.xd,
-                _ptr(self.q_out), self.ldqo, self.T, self.pos.data_ptr(), self.slot.data_ptr(),
-                st))
+            check(self._fn(*self._args, st))
         return self.q_out
 
 
@@ -1077,16 +1109,16 @@ class AttnCall:
         if ws is None or ws.numel() * ws.element_size() < plan.workspace_bytes:
             ws = torch.empty(max(plan.workspace_bytes, 256), dtype=torch.uint8, device=plan.device)
         self.ws = ws
+        self._fn = lib().tcl_attn_apply
+        self._args = (ctypes.byref(cache.desc), plan.n_q_heads, plan.buf.data_ptr(),
+                      plan.buf.numel(), q.data_ptr(), self.ldq, o.data_ptr(), self.ldo, _ptr(lse),
+                      self.scale, ws.data_ptr(), ws.numel() * ws.element_size())
 
     def __call__(self, stream=None) -> torch.Tensor:
         p = self.plan
         ctx, st = _on(p.device, stream, self.ws, self.o)
-        with ctx:
-            check(lib().tcl_attn_apply(
-                ctypes.byref(p.batch), ctypes.byref(self.cache.desc), p.n_q_heads,
-                p.buf.data_ptr(), p.buf.numel(), self.q.data_ptr(), self.ldq, self.o.data_ptr(),
-                self.ldo, _ptr(self.lse), self.scale, self.ws.data_ptr(),
-                self.ws.numel() * self.ws.element_size(), st))
+        with ctx:  # (the batch's tables are the plan's last ones)
+            check(self._fn(ctypes.byref(p.batch), *self._args, st))
         return self.o
 
 

@@ -376,7 +376,8 @@ def test_i8_host_errors(L):
 
     def w(**kw):
         a = {**ok, **kw}
-        return ctypes.byref(tclora.I8WeightDesc(a["d_in"], a["d_out"], a["W"], a["scale"]))
+        return ctypes.byref(tclora.I8WeightDesc(a["d_in"], a["d_out"], a["W"], a["scale"],
+                                                a.get("W_p")))
 
     def quant(x=P, ldx=64, xd=0, T=4, d=64, q=P, ldq=64, s=P):
         return L.tcl_i8_quant(x, ldx, xd, T, d, q, ldq, s, None)
@@ -406,7 +407,15 @@ def test_i8_host_errors(L):
     assert [lin(x=None), lin(ldx=56), lin(ws=None)] == [E] * 3 and lin(xd=3) == U
     assert lin(ws=0x10010) == A and lin(n=64) == tclora.ENOSPC
     out = ctypes.c_size_t(0)
-    assert L.tcl_i8_workspace_bytes(w(), 4, ctypes.byref(out)) == 0 and out.value == 512
+    assert L.tcl_i8_workspace_bytes(w(), 4, ctypes.byref(out)) == 0 and out.value == 1024 + 256
+    assert L.tcl_i8_pack_bytes(w(), ctypes.byref(out)) == 0 and out.value == 2048
+    assert L.tcl_i8_pack_bytes(w(d_in=80, d_out=8), ctypes.byref(out)) == 0 and out.value == 2048
+    assert L.tcl_i8_pack_bytes(None, ctypes.byref(out)) == E and L.tcl_i8_pack_bytes(w(), None) == E
+    assert L.tcl_i8_pack(w(), None, 4096, None) == E
+    assert L.tcl_i8_pack(w(W=None, W_p=P), P, 4096, None) == E
+    assert L.tcl_i8_pack(w(), P + 16, 4096, None) == A
+    assert L.tcl_i8_pack(w(), P, 2047, None) == tclora.ENOSPC
+    assert prod(w(W_p=P + 16)) == A and prod(w(W=None, W_p=P), T=0) == 0
     assert L.tcl_i8_workspace_bytes(w(), -1, ctypes.byref(out)) == E
     assert L.tcl_i8_workspace_bytes(None, 4, ctypes.byref(out)) == E
     assert L.tcl_i8_workspace_bytes(w(), 4, None) == E

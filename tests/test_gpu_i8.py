@@ -132,14 +132,15 @@ SHAPES = [(1, 16, 8), (1, 4096, 1024), (2, 48, 40), (7, 144, 136), (16, 256, 100
           (515, 400, 1032), (1025, 272, 264), (2048, 528, 264), (260, 64, 4104)]
 
 
+@pytest.mark.parametrize("pack", [True, False])
 @pytest.mark.parametrize("y", ["bf16", "f32"])
 @pytest.mark.parametrize("T,d_in,d_out", SHAPES)
-def test_product(T, d_in, d_out, y):
+def test_product(T, d_in, d_out, y, pack):
     W, ws = weight(T + d_out, d_out, d_in, full=True)
     g = torch.Generator().manual_seed(T * d_in)
     q = torch.randint(-128, 128, (T, d_in), generator=g, dtype=torch.int32).to(torch.int8).to(DEV)
     s = (torch.rand(T, generator=g) + 0.01).to(DEV)
-    got = tclora.i8_product(tclora.I8Weight(W, ws), q, s, y_dtype=DT[y])
+    got = tclora.i8_product(tclora.I8Weight(W, ws, pack), q, s, y_dtype=DT[y])
     close(got, product64(W, ws, q, s), DT[y])
 
 
@@ -172,13 +173,26 @@ def test_product_longest_rows_do_not_overflow(T):
 
 @pytest.mark.parametrize("x,y", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "bf16"), ("f32", "f32")])
 @pytest.mark.parametrize("T,d_in,d_out", [(1, 4096, 1024), (5, 272, 136), (64, 1024, 4096),
-                                          (300, 1040, 520)])
+                                          (300, 1040, 520), (4097, 400, 4104),
+                                          (2100, 48, 8200)])
 def test_linear(T, d_in, d_out, x, y):
     W, ws = weight(5, d_out, d_in)
     a = acts(T, T, d_in, DT[x])
     got = tclora.i8_linear(tclora.I8Weight(W, ws), a, y_dtype=DT[y])
     n, s = quant64(a)
     close(got, product64(W, ws, n, s), DT[y])
+
+
+@pytest.mark.parametrize("d_out,d_in", [(8, 16), (16, 64), (40, 80), (264, 1040)])
+def test_packed_copy(d_out, d_in):
+    """The documented order, zeros behind rows and columns."""
+    W, ws = weight(1, d_out, d_in, full=True)
+    got = tclora.I8Weight(W, ws).W_p.view(torch.int8).cpu()
+    R, C = -(-d_out // 16), -(-d_in // 64)
+    want = torch.zeros(R * 16, C * 64, dtype=torch.int8)
+    want[:d_out, :d_in] = W.cpu()
+    want = want.view(R, 16, C, 4, 16).permute(0, 2, 3, 1, 4)  # [R, C, chunk, row, 16]
+    assert torch.equal(got, want.reshape(-1))
 
 
 def test_empty_batch_and_empty_weight():
