@@ -45,9 +45,6 @@ __device__ inline int mat_step(const Mat8 &m) { return m.packed ? 1024 : 64; }
 // ---------------------------------------------------------------------------
 // activations to 8 bits
 // ---------------------------------------------------------------------------
-// 64 bytes of a block's chunk column are four rows: a workgroup of four rows
-// writes whole sectors.
-constexpr int kQRows = 4;
 // chunks of 16 elements a thread keeps in registers between the two passes;
 // longer rows are read again from L2
 constexpr int kQKeep = 4;
@@ -100,7 +97,7 @@ __device__ inline uint32_t absmax16(const R &c, uint32_t m) {
 // rint(v / s) of the real quotient.  The fp32 quotient is correctly rounded,
 // so it leaves a tie's wrong side only by landing on the tie itself; there
 // the remainder v - t * s, exact by fma, tells the side.
-__device__ inline int round_quotient(float v, float s) {
+__device__ inline float round_quotient(float v, float s) {
   const float t = v / s;
   float n = rintf(t);
   const float d = t - n;
@@ -108,32 +105,50 @@ __device__ inline int round_quotient(float v, float s) {
     const float rem = fmaf(-t, s, v);
     if (rem != 0.f) n = rem > 0.f ? ceilf(t) : floorf(t);
   }
-  return int(fminf(fmaxf(n, -127.f), 127.f));
+  return fminf(fmaxf(n, -127.f), 127.f);
 }
 
+// 16 quotients to bytes.  v * inv, inv = 1 / s rounded, is off by less than
+// 2^-22 of at most 127.5, so unless it lies within 2^-14 of a tie its nearest
+// integer is the quotient's; four values of a wave rarely do (the full
+// division on all of them costs as much time as the row's memory traffic).
+// Below 2^-100 a scale's reciprocal is not relied on.
 template <typename R>
-__device__ inline i32x4 quant16(const R &x, float s) {
+__device__ inline i32x4 quant16(const R &x, float s, float inv) {
   i32x4 w = {0, 0, 0, 0};
   if (!(s > 0.f)) return w;  // a row of zeros, or a NaN scale
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
+    float n[4], d = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float t = x.at(4 * i + j) * inv;
+      n[j] = rintf(t);
+      d = fmaxf(d, fabsf(t - n[j]));
+    }
+    if (d > 0.5f - 0x1p-14f || s < 0x1p-100f) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) n[j] = round_quotient(x.at(4 * i + j), s);
+    }
+    // (bytes of n + 128, then the sign bit turned)
     uint32_t b = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      b |= uint32_t(uint8_t(round_quotient(x.at(4 * i + j), s))) << (8 * j);
-    w[i] = int(b);
+    for (int j = 0; j < 4; ++j) b = __builtin_amdgcn_cvt_pk_u8_f32(n[j] + 128.f, j, b);
+    w[i] = int(b ^ 0x80808080u);
   }
   return w;
 }
 
-// WPR waves a row, kQRows rows a workgroup: a row is read once into
-// registers, its largest magnitude reduced, the integers written.
-template <typename T, int WPR>
-__global__ __launch_bounds__(64 * WPR * kQRows) void i8_quant_kernel(QuantArgs a) {
-  __shared__ uint32_t wmax[kQRows][WPR];
+// WPR waves a row, ROWS rows a workgroup: a row is read once into registers,
+// its largest magnitude reduced, the integers written.  Many rows: four a
+// workgroup, which writes whole 64-byte sectors of the blocks.  Few: one, so
+// that there are more workgroups.
+template <typename T, int WPR, int ROWS>
+__global__ __launch_bounds__(64 * WPR * ROWS) void i8_quant_kernel(QuantArgs a) {
+  __shared__ uint32_t wmax[ROWS][WPR];
   constexpr int TH = 64 * WPR;
   const int tid = threadIdx.x % TH, r = threadIdx.x / TH;
-  const int t = blockIdx.x * kQRows + r;
+  const int t = blockIdx.x * ROWS + r;
   const bool live = t < a.T;
   const char *row = static_cast<const char *>(a.x) + int64_t(live ? t : 0) * a.ldx * int64_t(sizeof(T));
   const int nc = live ? a.d / 16 : 0;
@@ -160,6 +175,7 @@ __global__ __launch_bounds__(64 * WPR * kQRows) void i8_quant_kernel(QuantArgs a
   }
   if (!live) return;
   const float s = m >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : __uint_as_float(m) / 127.f;
+  const float inv = 1.f / s;
   if (tid == 0) a.scale[t] = s;
   auto put = [&](int c, i32x4 w) {
     int8_t *p = a.packed ? a.q + (int64_t(t >> 4) * a.kb + (c >> 2)) * 1024 + (c & 3) * 256 + (t & 15) * 16
@@ -168,11 +184,11 @@ __global__ __launch_bounds__(64 * WPR * kQRows) void i8_quant_kernel(QuantArgs a
   };
 #pragma unroll
   for (int i = 0; i < kQKeep; ++i)
-    if (tid + i * TH < nc) put(tid + i * TH, quant16(keep[i], s));
+    if (tid + i * TH < nc) put(tid + i * TH, quant16(keep[i], s, inv));
   for (int c = tid + kQKeep * TH; c < nc; c += TH) {
     Raw16<T> x;
     x.load(row, c);
-    put(c, quant16(x, s));
+    put(c, quant16(x, s, inv));
   }
   // the last block's chunks behind the row
   if (a.packed && tid < 4 * a.kb - nc) put(nc + tid, i32x4{0, 0, 0, 0});
@@ -495,16 +511,14 @@ int launch_quant(const void *x, int64_t ldx, int xd, int32_t n, int32_t d, int8_
                  bool packed, float *scale, hipStream_t s) {
   if (n == 0) return TCL_OK;
   QuantArgs a{x, ldx, ldq, n, d, blocks_of(d), packed, q, scale};
-  const dim3 grid((n + kQRows - 1) / kQRows);
-  // few rows: four waves each, for the length of one row's work
-  const bool wide = n <= 1024;
-#define QUANT(T, W) hipLaunchKernelGGL((i8_quant_kernel<T, W>), grid, dim3(64 * W * kQRows), 0, s, a)
+#define QUANT(T, W, R) \
+  hipLaunchKernelGGL((i8_quant_kernel<T, W, R>), dim3((n + R - 1) / R), dim3(64 * W * R), 0, s, a)
   if (xd == TCL_BF16) {
-    if (wide) QUANT(bf16_t, 4);
-    else QUANT(bf16_t, 1);
+    if (n <= 1024) QUANT(bf16_t, 4, 1);
+    else QUANT(bf16_t, 1, 4);
   } else {
-    if (wide) QUANT(float, 4);
-    else QUANT(float, 1);
+    if (n <= 1024) QUANT(float, 4, 1);
+    else QUANT(float, 1, 4);
   }
 #undef QUANT
   TCL_HIP(hipGetLastError());
