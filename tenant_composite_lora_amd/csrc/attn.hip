@@ -15,6 +15,7 @@
 // lane halves (or quarters) a step, and the probabilities leave the first
 // product in the very registers the second wants them in.
 #include <cmath>
+#include <type_traits>
 
 #include "kern_common.hpp"
 #include "kv.hpp"
@@ -26,18 +27,34 @@ constexpr int kRows = 128;      // query rows of a tile of many rows
 constexpr int kFew = 16;        // rows of a tile of few rows (keys split over the waves)
 constexpr int kKeys = 64;       // keys of a step
 constexpr int kMinChunk = 128;  // smallest key range an item is cut to
-constexpr int kTargetWgs = 1024;
+// Workgroups that a batch is cut into where it has fewer tiles.  Few rows:
+// four a CU.  Many: two, as many as run at a time; their partial outputs
+// weigh more (64 requests over a prefix of 8192: 35 + 8 us, with 1024 41 +
+// 10; chunks of 256..512 tokens over 4096: 41 us of joining, with 1024 107).
+constexpr int kTargetFew = 1024, kTargetMany = 512;
 // a request whose rows fill half a tile reads its prefix by itself
 constexpr int kShortRows = 64;
-constexpr int kMagic = 0x41747431;
+constexpr int kMagic = 0x41747432;
+
+// A request's keys are numbered with its own ones starting on a step of their
+// own: key j < prefix is the prefix's, key j >= whole(prefix) is own key j -
+// whole(prefix), and the numbers between name none.  A step then never holds
+// keys of both, and every 16 keys of a step lie in one page of 16 or more.
+__host__ __device__ inline int whole(int prefix) { return (prefix + kKeys - 1) / kKeys * kKeys; }
+// the number behind the first n keys
+__device__ inline int key_end(int prefix, int n) {
+  return n <= prefix ? n : n + whole(prefix) - prefix;
+}
 
 enum { H_CODE, H_MAGIC, H_SEQS, H_GROUPS, H_TOKENS, H_HEADS, H_KVHEADS, H_DIM, H_PAGES, H_SHIFT,
        H_LDO, H_LDP, H_ITEMS, H_TILES, H_SHARED, H_WORDS = 64 };
 
-struct Work {
-  int32_t tile;     // for rows and tokens
-  int32_t lo, hi;   // keys [lo, hi) of the requests' concatenated keys
+struct alignas(16) Work {
+  int32_t tok0, list, n_tok;    // as in Tile
+  int32_t seq, group, prefix;
+  int32_t lo, hi;   // keys [lo, hi), lo a whole step
   int32_t part;     // first partial row, -1: write the output itself
+  int32_t pad[3];
 };
 
 struct Tile {
@@ -45,7 +62,7 @@ struct Tile {
   int32_t list;
   int32_t n_tok;    // tokens
   int32_t seq, group;
-  int32_t prefix;   // keys of the prefix: key j >= prefix is own key j - prefix
+  int32_t prefix;   // keys of the prefix
   int32_t lo, hi;   // key range
   int32_t part0;    // first partial row
   int32_t n_split;
@@ -66,7 +83,7 @@ struct PlanArgs {
   int32_t S, G, T, ldp, ldo;
   int32_t Hq, Hkv, D, n_pages, page_shift;
   int32_t tpt_many, tpt_few;  // whole tokens in a tile
-  int32_t cap_tiles, cap_items, cap_rows, target;
+  int32_t cap_tiles, cap_items, cap_rows, target_few, target_many;
   // plan
   int32_t *hdr;
   TokRec *tok;
@@ -157,8 +174,8 @@ __device__ inline Unit unit_of(const PlanArgs &a, int u) {
     x.group = upper(a.group_seq, a.G, s);
     // (empty groups: the one whose range holds s)
     x.prefix = a.prefix_len[x.group];
-    x.lo = is_short(a, x.n_q) && shares(a, x.group) ? x.prefix : 0;
-    x.hi = x.prefix + a.own_len[s];
+    x.lo = is_short(a, x.n_q) && shares(a, x.group) ? whole(x.prefix) : 0;
+    x.hi = x.prefix + a.own_len[s];  // (a count here)
   }
   x.rows = x.n_tok * gq;
   x.tpt = x.rows <= kFew ? a.tpt_few : a.tpt_many;
@@ -173,12 +190,12 @@ __device__ inline int unit_tiles(const Unit &x) {
 __device__ inline int tile_hi(const Unit &x, int i) {
   if (x.list) return x.hi;
   const int last = min(x.n_tok, (i + 1) * x.tpt) - 1;
-  return max(x.lo, min(x.hi, x.hi - x.n_q + last + 1));
+  return max(x.lo, key_end(x.prefix, max(0, x.hi - x.n_q + last + 1)));
 }
 
 __global__ __launch_bounds__(kMapThreads) void attn_plan_kernel(PlanArgs a) {
   __shared__ int lds[kMapThreads / 64];
-  __shared__ int s_err, s_chunk;
+  __shared__ int s_err, s_chunk[2];
   __shared__ unsigned long long s_work;
   const int tid = threadIdx.x, gq = a.Hq / a.Hkv;
   if (tid == 0) {
@@ -255,20 +272,19 @@ __global__ __launch_bounds__(kMapThreads) void attn_plan_kernel(PlanArgs a) {
   }
   if (work) atomicAdd(&s_work, work);  // (an integer sum: any order)
   __syncthreads();
-  if (tid == 0) {
-    const unsigned long long c = (s_work + a.target - 1) / a.target;
-    const unsigned long long r = (c + kKeys - 1) / kKeys * kKeys;
-    s_chunk = r < kMinChunk ? kMinChunk : (r > 0x40000000ull ? 0x40000000 : int(r));
+  if (tid < 2) {
+    const unsigned t = tid ? a.target_many : a.target_few;
+    const unsigned long long r = ((s_work + t - 1) / t + kKeys - 1) / kKeys * kKeys;
+    s_chunk[tid] = r < kMinChunk ? kMinChunk : (r > 0x40000000ull ? 0x40000000 : int(r));
   }
   __syncthreads();
-  const int chunk = s_chunk;
   // tiles and items, in unit order
   int tile_base = 0, item_base = 0, row_base = 0;
   for (int u0 = 0; u0 < U; u0 += kMapThreads) {
     const int u = u0 + tid;
     Unit x{};
     if (u < U) x = unit_of(a, u);
-    const int n = unit_tiles(x);
+    const int n = unit_tiles(x), chunk = s_chunk[x.rows > kFew];
     int ni = 0, nr = 0;
     for (int i = 0; i < n; ++i) {
       const int len = tile_hi(x, i) - x.lo, ns = max(1, (len + chunk - 1) / chunk);
@@ -294,7 +310,8 @@ __global__ __launch_bounds__(kMapThreads) void attn_plan_kernel(PlanArgs a) {
                          direct ? -1 : er, ns, per, ei};
       for (int k = 0; k < ns; ++k) {
         const int lo = min(hi, x.lo + k * per);
-        a.items[ei + k] = Work{et, lo, min(hi, lo + per), direct ? -1 : er + k * nt * gq};
+        a.items[ei + k] = Work{x.tok0 + i * x.tpt, x.list, nt, x.seq, x.group, x.prefix, lo,
+                               min(hi, lo + per), direct ? -1 : er + k * nt * gq, {}};
       }
       ++et, ei += ns, er += ns * nt * gq;
     }
@@ -308,7 +325,7 @@ __global__ __launch_bounds__(kMapThreads) void attn_plan_kernel(PlanArgs a) {
       const int s = upper(a.seq_tok, a.S, t);
       const Unit x = unit_of(a, a.G + s);
       const int i = t - x.tok0;
-      r.vis = max(0, x.hi - x.n_q + i + 1);
+      r.vis = max(0, x.hi - x.n_q + i + 1);  // (a count)
       r.own = a.utile[a.G + s] + i / x.tpt;
       r.own_at = i % x.tpt;
       if (is_short(a, x.n_q) && shares(a, x.group)) {
@@ -344,7 +361,8 @@ struct AttnArgs {
   uint16_t *o;
   float *lse;
   int64_t ldq, ldo;
-  float scale2;  // scale * log2(e)
+  float scale2;    // |scale| * log2(e)
+  int32_t q_sign;  // the sign bit of a bf16 number where scale is negative
   int32_t S, G, T, ldp, ld_own, Hq;
   const int32_t *prefix_pages, *own_pages;
   const int32_t *hdr;
@@ -399,270 +417,481 @@ struct Smem {
   uint16_t v[2][kKeys * D];
 };
 
-// Key j of a tile as an offset into the cache.  Page ids are held to the
-// cache's pages, so that a table that changed after its mapping reads other
-// keys, never other memory.
-__device__ inline int64_t key_at(const AttnArgs &a, const Tile &t, int j) {
-  const bool pre = j < t.prefix;
-  const int i = pre ? j : j - t.prefix;
-  const int32_t *row = pre ? a.prefix_pages + int64_t(t.group) * a.ldp
-                           : a.own_pages + int64_t(t.seq) * a.ld_own;
-  const int page = row[i >> a.c.page_shift];
-  const int p = min(max(page, 0), a.c.n_pages - 1);
-  return int64_t(p) * a.c.s_page + int64_t(i & ((1 << a.c.page_shift) - 1)) * a.c.s_slot;
-}
-
 // Writes four neighbouring dimensions of a row: the output itself, or a
 // partial one.
 __device__ inline void put4(uint16_t *o, const float *v, float f) {
   *reinterpret_cast<nt_u2 *>(o) = nt_u2{pack_bf16(v[0] * f, v[1] * f), pack_bf16(v[2] * f, v[3] * f)};
 }
 
+// A step's keys: key i0 + r of the part (prefix or own) for row r, the part's
+// last key again behind it (masked where it is used).
+struct Part {
+  const int32_t *table;
+  int i0, last;
+};
+__device__ inline Part part_of(const AttnArgs &a, const Work &t, int j0) {
+  const int w = whole(t.prefix);
+  if (j0 < w) return {a.prefix_pages + int64_t(t.group) * a.ldp, j0, min(t.prefix, t.hi) - 1};
+  return {a.own_pages + int64_t(t.seq) * a.ld_own, j0 - w, t.hi - w - 1};
+}
+
+// Infinities and NaNs among the values of keys that a row does not see must
+// not reach it, and a zero weight does not keep them out (0 * inf is NaN).
+// Where a step hides keys from some row, the values are looked over as they
+// pass through registers; where any is not finite, its products are added one
+// by one to the rows that see it, zero takes its place in LDS, and the matrix
+// product goes on as ever.
+__device__ inline bool bad_bf16(uint32_t w) { return (w & 0x7f80u) == 0x7f80u; }
+
+// Moves an item's keys and values, 64 a step, through registers into LDS:
+// wave w the rows 16 w .. 16 w + 15 of a step.  Where those lie in one page
+// its id is read two steps ahead, and the rows' addresses are a scalar and
+// lane offsets that never change; else (small pages, a part's last step) each
+// lane looks its rows up.  Page ids are held to the cache's pages, so that a
+// table that changed after its mapping reads other keys, never other memory.
 template <int D>
-__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_kernel(AttnArgs a) {
-  constexpr int CH = D / 8;         // chunks of a row
-  constexpr int RPI = 64 / CH;      // rows a wave loads an instruction
-  constexpr int NI = 16 / RPI;      // instructions for a wave's 16 rows
-  __shared__ __align__(16) Smem<D> sm;
-  if (!plan_fits(a)) return;
-  const int h = blockIdx.x % a.c.H, id = blockIdx.x / a.c.H;
-  if (id >= a.hdr[H_ITEMS]) return;
-  const Work it = a.items[id];
-  const Tile t = a.tiles[it.tile];
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-  const int gq = a.Hq / a.c.H, rows = t.n_tok * gq;
-  const bool few = rows <= kFew;
-  const int64_t hoff = int64_t(h) * a.c.s_head;
+struct Stage {
+  static constexpr int CH = D / 8;     // chunks of a row
+  static constexpr int RPI = 64 / CH;  // rows a wave loads an instruction
+  static constexpr int NI = 16 / RPI;  // instructions for a wave's 16 rows
+  nt_u4 k[NI], v[NI];
+  int page;  // of the wave's rows of the next step to be loaded
+  int w, row, col;
+  unsigned lane_off;  // bytes, of the wave's first RPI rows
+  int64_t head;
+  bool paged;
 
-  // staging: wave w moves rows 16 w .. 16 w + 15 of a step
-  const int lr = lane / CH, lc = lane % CH;
-  nt_u4 rk[NI], rv[NI];
-  auto fetch = [&](int j0) {
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      // behind the range: its last key again (masked below)
-      const int j = min(j0 + 16 * w + i * RPI + lr, it.hi - 1);
-      const int64_t at = key_at(a, t, j) + hoff + 8 * lc;
-      rk[i] = *reinterpret_cast<const nt_u4 *>(a.c.K + at);
-      rv[i] = *reinterpret_cast<const nt_u4 *>(a.c.V + at);
-    }
-  };
-  auto put = [&](int b) {
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int r = 16 * w + i * RPI + lr, p = r * D + 8 * (lc ^ swz<D>(r));
-      *reinterpret_cast<nt_u4 *>(&sm.k[b][p]) = rk[i];
-      *reinterpret_cast<nt_u4 *>(&sm.v[b][p]) = rv[i];
-    }
-  };
-  auto token = [&](int r) {  // row r of the tile -> token
-    const int i = t.tok0 + r / gq;
-    return t.list ? a.list[i] : i;
-  };
-  const int steps = (it.hi - it.lo + kKeys - 1) / kKeys;
-
-  if (few) {
-    // ---- few rows: every wave holds all of them, over its 16 keys a step
-    const int c = lane & 15, g = lane >> 4;
-    const bool live = c < rows;
-    const int tok = token(live ? c : 0);
-    const int hq = h * gq + (live ? c : 0) % gq;
-    const int vis = live ? a.tok[tok].vis : 0;
-    bf16x8_t qf[D / 32];
-#pragma unroll
-    for (int s = 0; s < D / 32; ++s)
-      qf[s] = *reinterpret_cast<const bf16x8_t *>(a.q + tok * a.ldq + int64_t(hq) * D + 32 * s + 8 * g);
-    f32x4_t o[D / 16];
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i) o[i] = f32x4_t{0, 0, 0, 0};
-    float m = -INFINITY, l = 0.f;
-    if (steps > 0) fetch(it.lo);
-    for (int st = 0; st < steps; ++st) {
-      const int j0 = it.lo + st * kKeys, b = st & 1;
-      put(b);
-      if (st + 1 < steps) fetch(j0 + kKeys);
-      __syncthreads();
-      f32x4_t s4 = {0, 0, 0, 0};
-      const int kr = 16 * w + c;
-#pragma unroll
-      for (int s = 0; s < D / 32; ++s) {
-        const bf16x8_t kf =
-            *reinterpret_cast<const bf16x8_t *>(&sm.k[b][kr * D + 8 * ((4 * s + g) ^ swz<D>(kr))]);
-        s4 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[s], s4, 0, 0, 0);
-      }
-      float p[4], mx = -INFINITY;
-      const int left = min(vis, it.hi) - (j0 + 16 * w + 4 * g);  // visible keys of the lane's four
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        p[i] = i < left ? s4[i] * a.scale2 : -INFINITY;
-        mx = fmaxf(mx, p[i]);
-      }
-      mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
-      mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
-      const float mn = fmaxf(m, mx), mu = mn == -INFINITY ? 0.f : mn;
-      const float al = __builtin_amdgcn_exp2f(m - mu);
-      m = mn;
-      float sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        p[i] = __builtin_amdgcn_exp2f(p[i] - mu);
-        sum += p[i];
-      }
-      l = l * al + sum;
-      // probabilities in two bf16 parts: the matrix cores idle here, and the
-      // rounding of one part would show beside the output's own
-      uint32_t hi2[2], lo2[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        hi2[i] = pack_bf16(p[2 * i], p[2 * i + 1]);
-        lo2[i] = pack_bf16(p[2 * i] - bf16_lo(hi2[i]), p[2 * i + 1] - bf16_hi(hi2[i]));
-      }
-      const s16x4 ph = __builtin_bit_cast(s16x4, nt_u2{hi2[0], hi2[1]});
-      const s16x4 pl = __builtin_bit_cast(s16x4, nt_u2{lo2[0], lo2[1]});
-      const int vr = 16 * w + 4 * g + (c >> 2);
-#pragma unroll
-      for (int d = 0; d < D / 16; ++d) {
-        o[d] *= al;
-        const s16x4 vf = read_tr(&sm.v[b][vr * D + 8 * ((2 * d + ((c & 3) >> 1)) ^ swz<D>(vr)) + 4 * (c & 1)]);
-        o[d] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(vf, ph, o[d], 0, 0, 0);
-        o[d] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(vf, pl, o[d], 0, 0, 0);
-      }
-    }
-    // join the waves: maxima and sums, then outputs, through LDS
-    l += __shfl_xor(l, 16, 64);
-    l += __shfl_xor(l, 32, 64);
-    __syncthreads();
-    float *jo = reinterpret_cast<float *>(&sm);             // [4][16][D]
-    static_assert(sizeof(sm) >= 4 * 16 * D * 4 + 4 * 16 * 8, "LDS of the join");
-    float2 *jm = reinterpret_cast<float2 *>(jo + 4 * 16 * D);  // [4][16]
-    if (g == 0) jm[w * 16 + c] = make_float2(m, l);
-#pragma unroll
-    for (int d = 0; d < D / 16; ++d)
-      *reinterpret_cast<f32x4_t *>(&jo[(w * 16 + c) * D + 16 * d + 4 * g]) = o[d];
-    __syncthreads();
-    for (int x = tid; x < rows * (D / 4); x += 256) {
-      const int r = x / (D / 4), d = x % (D / 4) * 4;
-      float M = -INFINITY, L = 0.f, f[4], v[4] = {0, 0, 0, 0};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) M = fmaxf(M, jm[i * 16 + r].x);
-      const float mu = M == -INFINITY ? 0.f : M;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        f[i] = __builtin_amdgcn_exp2f(jm[i * 16 + r].x - mu);
-        L += jm[i * 16 + r].y * f[i];
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const f32x4_t u = *reinterpret_cast<const f32x4_t *>(&jo[(i * 16 + r) * D + d]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] += u[e] * f[i];
-      }
-      const int tk = token(r), hh = h * gq + r % gq;
-      if (it.part < 0) {
-        put4(a.o + tk * a.ldo + int64_t(hh) * D + d, v, L > 0.f || L != L ? 1.f / L : 0.f);
-        if (a.lse && d == 0) a.lse[int64_t(tk) * a.Hq + hh] = (M + log2f(L)) * 0.69314718055994531f;
-      } else {
-        const int64_t pr = int64_t(it.part + r) * a.c.H + h;
-        *reinterpret_cast<f32x4_t *>(a.part_o + pr * D + d) = f32x4_t{v[0], v[1], v[2], v[3]};
-        if (d == 0) a.part_ml[pr] = make_float2(M, L);
-      }
-    }
-    return;
+  __device__ inline void init(const AttnArgs &a, int h) {
+    const int lane = threadIdx.x & 63;
+    w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    row = lane / CH;
+    col = lane % CH;
+    head = int64_t(h) * a.c.s_head;
+    paged = a.c.page_shift >= 4 && a.c.s_slot < (int64_t(1) << 26);
+    lane_off = 2 * (unsigned(row) * unsigned(a.c.s_slot) + 8 * col);
   }
+  __device__ inline int clamp(const AttnArgs &a, int p) const {
+    return min(max(p, 0), a.c.n_pages - 1);
+  }
+  __device__ inline void pages(const AttnArgs &a, const Work &t, int j0) {
+    if (!paged || j0 >= t.hi) return;
+    const Part p = part_of(a, t, j0);
+    page = p.table[min(p.i0 + 16 * w, p.last) >> a.c.page_shift];
+  }
+  __device__ inline void load(const AttnArgs &a, const Work &t, int j0) {
+    const Part p = part_of(a, t, j0);
+    const int mask = (1 << a.c.page_shift) - 1;
+    if (paged && p.i0 + kKeys - 1 <= p.last) {
+      const int64_t at = int64_t(clamp(a, __builtin_amdgcn_readfirstlane(page))) * a.c.s_page +
+                         int64_t((p.i0 + 16 * w) & mask) * a.c.s_slot + head;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const char *bk = reinterpret_cast<const char *>(a.c.K + at + i * RPI * a.c.s_slot);
+        const char *bv = reinterpret_cast<const char *>(a.c.V + at + i * RPI * a.c.s_slot);
+        k[i] = *reinterpret_cast<const nt_u4 *>(bk + lane_off);
+        v[i] = *reinterpret_cast<const nt_u4 *>(bv + lane_off);
+      }
+      return;
+    }
+    int64_t at[NI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int j = min(p.i0 + 16 * w + row + i * RPI, p.last);
+      at[i] = int64_t(clamp(a, p.table[j >> a.c.page_shift])) * a.c.s_page +
+              int64_t(j & mask) * a.c.s_slot + head + 8 * col;
+    }
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      k[i] = *reinterpret_cast<const nt_u4 *>(a.c.K + at[i]);
+      v[i] = *reinterpret_cast<const nt_u4 *>(a.c.V + at[i]);
+    }
+  }
+  // a value that is not finite among those in registers
+  __device__ inline bool bad() const {
+    // (magnitudes in order of their bits, two at a time)
+    typedef uint16_t us2 __attribute__((ext_vector_type(2)));
+    us2 x = {0, 0};
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        x = __builtin_elementwise_max(x, __builtin_bit_cast(us2, v[i][e] & 0x7fff7fffu));
+    return x[0] >= 0x7f80 || x[1] >= 0x7f80;
+  }
+  // zero for those among the wave's own rows in LDS
+  __device__ inline void clean(uint16_t *sv) const {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int r = 16 * w + row + i * RPI;
+      nt_u4 *p = reinterpret_cast<nt_u4 *>(sv + r * D + 8 * (col ^ swz<D>(r)));
+      nt_u4 u = *p;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        u[e] = (bad_bf16(u[e]) ? 0 : u[e] & 0xffffu) | (bad_bf16(u[e] >> 16) ? 0 : u[e] & 0xffff0000u);
+      *p = u;
+    }
+  }
+  __device__ inline void put(uint16_t *sk, uint16_t *sv) const {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int r = 16 * w + row + i * RPI, p = r * D + 8 * (col ^ swz<D>(r));
+      *reinterpret_cast<nt_u4 *>(sk + p) = k[i];
+      *reinterpret_cast<nt_u4 *>(sv + p) = v[i];
+    }
+  }
+};
 
-  // ---- many rows: wave w holds rows 32 w .. 32 w + 31 over all keys
+// The number behind the keys that a row with `vis` keys sees of the step at
+// j0.
+__device__ inline int step_end(const Work &t, int vis, int j0) {
+  const int w = whole(t.prefix);
+  return j0 < w ? min(vis, t.prefix) : vis + w - t.prefix;
+}
+
+// value d of row r in LDS
+template <int D>
+__device__ inline uint32_t value_at(const uint16_t *sv, int r, int d) {
+  return sv[r * D + 8 * ((d >> 3) ^ swz<D>(r)) + (d & 7)];
+}
+
+// The step's barrier: LDS only, global loads stay in flight across it.
+__device__ inline void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+__device__ inline int token_of(const AttnArgs &a, const Work &t, int gq, int r) {
+  const int i = t.tok0 + r / gq;
+  return t.list ? a.list[i] : i;
+}
+
+__device__ inline float log_sum(float m, float l) {
+  return (m + __log2f(l)) * 0.69314718055994531f;
+}
+
+// A maximum that only follows the scores when they pass it by kSlack (in
+// powers of two): weights then reach 2^kSlack, which neither fp32 sums nor
+// bf16's relative rounding mind, and the outputs are rescaled a few times an
+// item instead of every step.
+constexpr float kSlack = 8.f;
+
+// The larger of two numbers as a median with infinity: fmaxf first passes each
+// score of a matrix instruction through a multiplication by one.
+__device__ inline float larger(float a, float b) { return __builtin_amdgcn_fmed3f(a, b, INFINITY); }
+
+// the larger of a lane's value and that of the lane 32 away
+__device__ inline float half_max(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+// Few rows: every wave holds all of them, over its own 16 keys of a step; the
+// waves' results are joined through LDS.
+template <int D>
+__device__ inline void attend_few(const AttnArgs &a, const Work &t, int h, int gq, Smem<D> &sm) {
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  const int rows = t.n_tok * gq, steps = (t.hi - t.lo + kKeys - 1) / kKeys;
+  Stage<D> st;
+  st.init(a, h);
+  if (steps > 0) st.pages(a, t, t.lo);
+  const int c = lane & 15, g = lane >> 4;
+  const bool live = c < rows;
+  const int tok = token_of(a, t, gq, live ? c : 0);
+  const int hq = h * gq + (live ? c : 0) % gq;
+  if (steps > 0) {
+    st.load(a, t, t.lo);
+    st.pages(a, t, t.lo + kKeys);
+  }
+  const int vis = live ? a.tok[tok].vis : 0;
+  s16x8 qf[D / 32];
+#pragma unroll
+  for (int s = 0; s < D / 32; ++s)
+    qf[s] = *reinterpret_cast<const s16x8 *>(a.q + tok * a.ldq + int64_t(hq) * D + 32 * s + 8 * g) ^
+            short(a.q_sign);
+  f32x4_t o[D / 16];
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) o[i] = f32x4_t{0, 0, 0, 0};
+  float m = -INFINITY, l = 0.f;
+  for (int n = 0; n < steps; ++n) {
+    const int j0 = t.lo + n * kKeys, b = n & 1;
+    st.put(sm.k[b], sm.v[b]);
+    // (here in every step: a weight's second part may be zero or negative)
+    const bool rare = __any(st.bad());
+    if (n + 1 < steps) {
+      st.load(a, t, j0 + kKeys);
+      st.pages(a, t, j0 + 2 * kKeys);
+    }
+    // (a wave reads only what it wrote)
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+    f32x4_t s4 = {0, 0, 0, 0};
+    const int kr = 16 * w + c;
+#pragma unroll
+    for (int s = 0; s < D / 32; ++s) {
+      const bf16x8_t kf =
+          *reinterpret_cast<const bf16x8_t *>(&sm.k[b][kr * D + 8 * ((4 * s + g) ^ swz<D>(kr))]);
+      s4 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, __builtin_bit_cast(bf16x8_t, qf[s]), s4, 0, 0, 0);
+    }
+    float p[4], mx = -INFINITY;
+    // visible keys of the lane's four
+    const int left = min(step_end(t, vis, j0), t.hi) - (j0 + 16 * w + 4 * g);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      p[i] = i < left ? s4[i] : -INFINITY;
+      mx = fmaxf(mx, p[i]);
+    }
+    mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
+    mx = fmaxf(mx, __shfl_xor(mx, 32, 64)) * a.scale2;
+    if (__any(mx > m + kSlack)) {
+      const float mn = fmaxf(m, mx), al = mn == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - mn);
+      m = mn;
+      l *= al;
+#pragma unroll
+      for (int d = 0; d < D / 16; ++d) o[d] *= al;
+    }
+    const float mu = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      p[i] = __builtin_amdgcn_exp2f(fmaf(p[i], a.scale2, -mu));
+      l += p[i];
+    }
+    // probabilities in two bf16 parts: the matrix cores idle here, and the
+    // rounding of one part would show beside the output's own
+    uint32_t hi2[2], lo2[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      hi2[i] = pack_bf16(p[2 * i], p[2 * i + 1]);
+      lo2[i] = pack_bf16(p[2 * i] - bf16_lo(hi2[i]), p[2 * i + 1] - bf16_hi(hi2[i]));
+    }
+    const s16x4 ph = __builtin_bit_cast(s16x4, nt_u2{hi2[0], hi2[1]});
+    const s16x4 pl = __builtin_bit_cast(s16x4, nt_u2{lo2[0], lo2[1]});
+    if (rare) {
+#pragma unroll 1
+      for (int k = 0; k < 16; ++k) {
+        const float q = k & 2 ? (k & 1 ? p[3] : p[2]) : (k & 1 ? p[1] : p[0]);
+        const float pk = __shfl(q, c + 16 * (k >> 2), 64);
+        if (k >= left + 4 * g) continue;
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t u = value_at<D>(sm.v[b], 16 * w + k, 16 * d + 4 * g + e);
+            if (bad_bf16(u)) o[d][e] += pk * __uint_as_float(u << 16);
+          }
+      }
+      st.clean(sm.v[b]);
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+    }
+    const int vr = 16 * w + 4 * g + (c >> 2);
+#pragma unroll
+    for (int d = 0; d < D / 16; ++d) {
+      const s16x4 vf = read_tr(&sm.v[b][vr * D + 8 * ((2 * d + ((c & 3) >> 1)) ^ swz<D>(vr)) + 4 * (c & 1)]);
+      o[d] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(vf, ph, o[d], 0, 0, 0);
+      o[d] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(vf, pl, o[d], 0, 0, 0);
+    }
+  }
+  // join the waves: maxima and sums, then outputs, through LDS
+  l += __shfl_xor(l, 16, 64);
+  l += __shfl_xor(l, 32, 64);
+  __syncthreads();
+  float *jo = reinterpret_cast<float *>(&sm);  // [4][16][D]
+  static_assert(sizeof(sm) >= 4 * 16 * D * 4 + 4 * 16 * 8, "LDS of the join");
+  float2 *jm = reinterpret_cast<float2 *>(jo + 4 * 16 * D);  // [4][16]
+  if (g == 0) jm[w * 16 + c] = make_float2(m, l);
+#pragma unroll
+  for (int d = 0; d < D / 16; ++d)
+    *reinterpret_cast<f32x4_t *>(&jo[(w * 16 + c) * D + 16 * d + 4 * g]) = o[d];
+  __syncthreads();
+  for (int x = tid; x < rows * (D / 4); x += 256) {
+    const int r = x / (D / 4), d = x % (D / 4) * 4;
+    float M = -INFINITY, L = 0.f, f[4], v[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) M = fmaxf(M, jm[i * 16 + r].x);
+    const float mu = M == -INFINITY ? 0.f : M;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[i] = __builtin_amdgcn_exp2f(jm[i * 16 + r].x - mu);
+      L += jm[i * 16 + r].y * f[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f32x4_t u = *reinterpret_cast<const f32x4_t *>(&jo[(i * 16 + r) * D + d]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] += u[e] * f[i];
+    }
+    const int tk = token_of(a, t, gq, r), hh = h * gq + r % gq;
+    if (t.part < 0) {
+      put4(a.o + tk * a.ldo + int64_t(hh) * D + d, v, L > 0.f || L != L ? 1.f / L : 0.f);
+      if (a.lse && d == 0) a.lse[int64_t(tk) * a.Hq + hh] = log_sum(M, L);
+    } else {
+      const int64_t pr = int64_t(t.part + r) * a.c.H + h;
+      *reinterpret_cast<f32x4_t *>(a.part_o + pr * D + d) = f32x4_t{v[0], v[1], v[2], v[3]};
+      if (d == 0) a.part_ml[pr] = make_float2(M, L);
+    }
+  }
+}
+
+// Many rows: wave w holds rows 32 w .. 32 w + 31 over all keys of a step.
+template <int D>
+__device__ inline void attend_many(const AttnArgs &a, const Work &t, int h, int gq, Smem<D> &sm) {
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int rows = t.n_tok * gq, steps = (t.hi - t.lo + kKeys - 1) / kKeys;
+  Stage<D> st;
+  st.init(a, h);
+  if (steps > 0) st.pages(a, t, t.lo);
   const int c = lane & 31, g = lane >> 5;
   const int r = 32 * w + c;
   const bool live = r < rows, busy = 32 * w < rows;
-  const int tok = token(live ? r : 0);
+  const int tok = token_of(a, t, gq, live ? r : 0);
   const int hq = h * gq + (live ? r : 0) % gq;
-  const int vis = live ? min(a.tok[tok].vis, it.hi) : it.hi;
-  // the fewest keys a row of the wave sees: no mask below them
-  int clear = vis;
+  if (steps > 0) {
+    st.load(a, t, t.lo);
+    st.pages(a, t, t.lo + kKeys);
+  }
+  const int vis = a.tok[tok].vis;
+  // the fewest keys a row of the wave sees: a step beyond them hides some
+  int least = live ? vis : 0x7fffffff;
 #pragma unroll
-  for (int x = 16; x > 0; x >>= 1) clear = min(clear, __shfl_xor(clear, x, 64));
-  clear = __builtin_amdgcn_readfirstlane(clear);
-  bf16x8_t qf[D / 16];
+  for (int x = 16; x > 0; x >>= 1) least = min(least, __shfl_xor(least, x, 64));
+  least = __builtin_amdgcn_readfirstlane(least);
+  s16x8 qf[D / 16];
 #pragma unroll
   for (int s = 0; s < D / 16; ++s)
-    qf[s] = *reinterpret_cast<const bf16x8_t *>(a.q + tok * a.ldq + int64_t(hq) * D + 16 * s + 8 * g);
+    qf[s] = *reinterpret_cast<const s16x8 *>(a.q + tok * a.ldq + int64_t(hq) * D + 16 * s + 8 * g) ^
+            short(a.q_sign);
   f32x16_t o[D / 32];
 #pragma unroll
   for (int i = 0; i < D / 32; ++i)
 #pragma unroll
     for (int e = 0; e < 16; ++e) o[i][e] = 0.f;
   float m = -INFINITY, l = 0.f;
-  if (steps > 0) fetch(it.lo);
-  for (int st = 0; st < steps; ++st) {
-    const int j0 = it.lo + st * kKeys, b = st & 1;
-    put(b);
-    if (st + 1 < steps) fetch(j0 + kKeys);
+  // operand positions in LDS: key row c and value row vr[x] of the first
+  // chunks; chunk 2 s (or block i of 32 dimensions) on, the position's bits
+  // change as by the swizzle, by exclusive or
+  const int i16 = lane & 15, sub = (lane >> 4) & 1;
+  const int kpos = c * D + 8 * (g ^ swz<D>(c));
+  int vpos[2];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int vr = 8 * x + 4 * g + (i16 >> 2);
+    vpos[x] = vr * D + 8 * ((2 * sub + ((i16 & 3) >> 1)) ^ swz<D>(vr)) + 4 * (i16 & 1);
+  }
+  // (of the whole tile: its steps that hide keys look values over together)
+  int tile_least = least;
+  {
+    int *x = reinterpret_cast<int *>(&sm);
+    if (lane == 0) x[w] = least;
     __syncthreads();
+    for (int i = 0; i < 4; ++i) tile_least = min(tile_least, x[i]);
+    __syncthreads();
+    tile_least = __builtin_amdgcn_readfirstlane(tile_least);
+  }
+  for (int n = 0; n < steps; ++n) {
+    const int j0 = t.lo + n * kKeys, b = n & 1;
+    st.put(sm.k[b], sm.v[b]);
+    bool rare = false;
+    if (j0 + kKeys > min(step_end(t, tile_least, j0), t.hi))
+      rare = __syncthreads_or(st.bad());
+    if (n + 1 < steps) {
+      st.load(a, t, j0 + kKeys);
+      st.pages(a, t, j0 + 2 * kKeys);
+    }
+    lds_barrier();
+    const uint16_t *sk = sm.k[0];
+    uint16_t *sv = sm.v[0];
+    const int kp = kpos + b * kKeys * D, vp0 = vpos[0] + b * kKeys * D, vp1 = vpos[1] + b * kKeys * D;
+    uint32_t pw[4][4];
+    int end = 0;
+    if (busy) {
+      f32x16_t s2[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s2[x][e] = 0.f;
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) {
+          const bf16x8_t kf = *reinterpret_cast<const bf16x8_t *>(sk + ((kp ^ (16 * s)) + 32 * x * D));
+          s2[x] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, __builtin_bit_cast(bf16x8_t, qf[s]),
+                                                          s2[x], 0, 0, 0);
+        }
+      }
+      if (j0 + kKeys > min(step_end(t, least, j0), t.hi)) {
+        end = min(step_end(t, vis, j0), t.hi);
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            // (a constant against the lane's limit)
+            if (32 * x + 8 * (e / 4) + e % 4 >= end - j0 - 4 * g) s2[x][e] = -INFINITY;
+          }
+      }
+      float mx = -INFINITY;
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) mx = larger(mx, s2[x][e]);
+      mx = half_max(mx) * a.scale2;
+      if (__any(mx > m + kSlack)) {
+        const float mn = fmaxf(m, mx), al = mn == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - mn);
+        m = mn;
+        l *= al;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[i][e] *= al;
+      }
+      const float mu = m == -INFINITY ? 0.f : m;
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) {
+          const float p = __builtin_amdgcn_exp2f(fmaf(s2[x][e], a.scale2, -mu));
+          const float q = __builtin_amdgcn_exp2f(fmaf(s2[x][e + 1], a.scale2, -mu));
+          l += p;
+          l += q;
+          pw[2 * x + e / 8][e % 8 / 2] = pack_bf16(p, q);
+        }
+    }
+    if (rare) {
+      if (busy) {
+        end = min(step_end(t, vis, j0), t.hi);
+#pragma unroll 1
+        for (int k = 0; k < kKeys; ++k) {
+          // key k's weights: word k / 16, k / 8 % 2, k / 2 % 2 of the lane
+          // half k / 4 % 2
+          uint32_t u = 0;
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              if (s == k >> 4 && x == ((k >> 3 & 1) << 1 | (k >> 1 & 1))) u = pw[s][x];
+          u = __shfl(int(u), c + 32 * (k >> 2 & 1), 64);
+          const float pk = k & 1 ? bf16_hi(u) : bf16_lo(u);
+          if (j0 + k >= end) continue;
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const uint32_t y = value_at<D>(sm.v[b], k, 32 * i + 8 * (e / 4) + 4 * g + e % 4);
+              if (bad_bf16(y)) o[i][e] += pk * __uint_as_float(y << 16);
+            }
+        }
+      }
+      __syncthreads();
+      st.clean(sm.v[b]);
+      __syncthreads();
+    }
     if (!busy) continue;
-    f32x16_t s2[2];
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) s2[n][e] = 0.f;
-      const int kr = 32 * n + c;
-#pragma unroll
-      for (int s = 0; s < D / 16; ++s) {
-        const bf16x8_t kf =
-            *reinterpret_cast<const bf16x8_t *>(&sm.k[b][kr * D + 8 * ((2 * s + g) ^ swz<D>(kr))]);
-        s2[n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[s], s2[n], 0, 0, 0);
-      }
-    }
-    float mx = -INFINITY;
-    if (j0 + kKeys <= clear) {
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          s2[n][e] *= a.scale2;
-          mx = fmaxf(mx, s2[n][e]);
-        }
-    } else {
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int j = j0 + 32 * n + 8 * (e / 4) + 4 * g + e % 4;
-          s2[n][e] = j < vis ? s2[n][e] * a.scale2 : -INFINITY;
-          mx = fmaxf(mx, s2[n][e]);
-        }
-    }
-    mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
-    const float mn = fmaxf(m, mx), mu = mn == -INFINITY ? 0.f : mn;
-    const float al = __builtin_amdgcn_exp2f(m - mu);
-    m = mn;
-    float sum = 0.f;
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        s2[n][e] = __builtin_amdgcn_exp2f(s2[n][e] - mu);
-        sum += s2[n][e];
-      }
-    l = l * al + sum;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) o[i][e] *= al;
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       // keys 16 s + {4 g + 0..3, 8 + 4 g + 0..3}: the lane's eight, in order
-      uint32_t pw[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        pw[i] = pack_bf16(s2[s / 2][8 * (s & 1) + 2 * i], s2[s / 2][8 * (s & 1) + 2 * i + 1]);
-      const bf16x8_t pf = __builtin_bit_cast(bf16x8_t, nt_u4{pw[0], pw[1], pw[2], pw[3]});
-      const int i16 = lane & 15, sub = (lane >> 4) & 1;
-      const int v0 = 16 * s + 4 * g + (i16 >> 2), v1 = v0 + 8;
+      const bf16x8_t pf = __builtin_bit_cast(bf16x8_t, nt_u4{pw[s][0], pw[s][1], pw[s][2], pw[s][3]});
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
-        const int ch = 4 * i + 2 * sub + ((i16 & 3) >> 1), off = 4 * (i16 & 1);
-        const s16x4 x = read_tr(&sm.v[b][v0 * D + 8 * (ch ^ swz<D>(v0)) + off]);
-        const s16x4 y = read_tr(&sm.v[b][v1 * D + 8 * (ch ^ swz<D>(v1)) + off]);
+        const s16x4 x = read_tr(sv + ((vp0 ^ (32 * i)) + 16 * s * D));
+        const s16x4 y = read_tr(sv + ((vp1 ^ (32 * i)) + 16 * s * D));
         const s16x8 vv = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
         o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, vv), pf, o[i], 0,
                                                        0, 0);
@@ -671,25 +900,41 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_kernel(AttnArgs a)
   }
   if (!live) return;
   l += __shfl_xor(l, 32, 64);
-  const float f = it.part >= 0 ? 1.f : (l > 0.f || l != l ? 1.f / l : 0.f);
-  const int64_t pr = int64_t(it.part + r) * a.c.H + h;
+  const float f = t.part >= 0 ? 1.f : (l > 0.f || l != l ? 1.f / l : 0.f);
+  const int64_t pr = int64_t(t.part + r) * a.c.H + h;
 #pragma unroll
   for (int i = 0; i < D / 32; ++i)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int d = 32 * i + 8 * e + 4 * g;
       const float v[4] = {o[i][4 * e], o[i][4 * e + 1], o[i][4 * e + 2], o[i][4 * e + 3]};
-      if (it.part < 0)
+      if (t.part < 0)
         put4(a.o + tok * a.ldo + int64_t(hq) * D + d, v, f);
       else
         *reinterpret_cast<f32x4_t *>(a.part_o + pr * D + d) = f32x4_t{v[0], v[1], v[2], v[3]};
     }
   if (g == 0) {
-    if (it.part >= 0)
+    if (t.part >= 0)
       a.part_ml[pr] = make_float2(m, l);
     else if (a.lse)
-      a.lse[int64_t(tok) * a.Hq + hq] = (m + log2f(l)) * 0.69314718055994531f;
+      a.lse[int64_t(tok) * a.Hq + hq] = log_sum(m, l);
   }
+}
+
+template <int D>
+__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_kernel(AttnArgs a) {
+  __shared__ __align__(16) Smem<D> sm;
+  if (!plan_fits(a)) return;
+  // (workgroups go to the XCDs in turn: with eight key heads each XCD's L2
+  // holds one head)
+  const int h = blockIdx.x % a.c.H, id = blockIdx.x / a.c.H;
+  if (id >= a.hdr[H_ITEMS]) return;
+  const Work t = a.items[id];
+  const int gq = a.Hq / a.c.H;
+  if (t.n_tok * gq <= kFew)
+    attend_few<D>(a, t, h, gq, sm);
+  else
+    attend_many<D>(a, t, h, gq, sm);
 }
 
 // Joins the items of one row a wave: maxima first, then the weighted sums in
@@ -718,25 +963,44 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
   for (int x = 32; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor(M, x, 64));
   const float mu = M == -INFINITY ? 0.f : M;
   constexpr int E = D / 64;
-  float L = 0.f, v[E] = {};
+  typedef float fe __attribute__((ext_vector_type(E)));
+  float L = 0.f;
+  fe v;
+#pragma unroll
+  for (int e = 0; e < E; ++e) v[e] = 0.f;
   for (int s = 0; s < 2; ++s) {
     if (s == 1 && r.pre < 0) break;
     const Tile t = s ? a.tiles[r.pre] : own;
     const int row = (s ? r.pre_at : r.own_at) * gq + hh % gq, step = t.n_tok * gq;
-    for (int k = 0; k < t.n_split; ++k) {
-      const int64_t pr = int64_t(t.part0 + row + k * step) * a.c.H + h;
-      const float2 ml = a.part_ml[pr];
-      const float f = __builtin_amdgcn_exp2f(ml.x - mu);
-      L += ml.y * f;
+    const int64_t pr = int64_t(t.part0 + row) * a.c.H + h;
+    auto add = [&](auto n_, int k0) {
+      constexpr int n = decltype(n_)::value;
+      float2 ml[n];
+      fe u[n];
 #pragma unroll
-      for (int e = 0; e < E; ++e) v[e] += a.part_o[pr * D + lane * E + e] * f;
-    }
+      for (int k = 0; k < n; ++k) {
+        const int64_t p = pr + int64_t(k0 + k) * step * a.c.H;
+        ml[k] = a.part_ml[p];
+        u[k] = *reinterpret_cast<const fe *>(a.part_o + p * D + lane * E);
+      }
+#pragma unroll
+      for (int k = 0; k < n; ++k) {
+        const float f = __builtin_amdgcn_exp2f(ml[k].x - mu);
+        L += ml[k].y * f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] += u[k][e] * f;
+      }
+    };
+    int k = 0;
+    for (; k + 8 <= t.n_split; k += 8) add(std::integral_constant<int, 8>{}, k);
+    for (; k + 2 <= t.n_split; k += 2) add(std::integral_constant<int, 2>{}, k);
+    if (k < t.n_split) add(std::integral_constant<int, 1>{}, k);
   }
   const float f = L > 0.f || L != L ? 1.f / L : 0.f;
 #pragma unroll
   for (int e = 0; e < E; ++e)
     a.o[tk * a.ldo + int64_t(hh) * D + lane * E + e] = f32_to_bf16(v[e] * f);
-  if (a.lse && lane == 0) a.lse[int64_t(tk) * a.Hq + hh] = (M + log2f(L)) * 0.69314718055994531f;
+  if (a.lse && lane == 0) a.lse[int64_t(tk) * a.Hq + hh] = log_sum(M, L);
 }
 
 // ---------------------------------------------------------------------------
@@ -782,13 +1046,14 @@ void sizes(const tcl_attn_batch *b, const KvArgs &kv, int32_t Hq, PlanArgs *a, L
   a->Hq = Hq, a->Hkv = kv.H, a->D = kv.D, a->n_pages = kv.n_pages, a->page_shift = kv.page_shift;
   a->tpt_many = kRows / gq;
   a->tpt_few = gq <= kFew ? kFew / gq : a->tpt_many;
-  a->target = (kTargetWgs + kv.H - 1) / kv.H;
+  a->target_few = (kTargetFew + kv.H - 1) / kv.H;
+  a->target_many = (kTargetMany + kv.H - 1) / kv.H;
   // tiles: whole ones of all tokens twice (own ranges, prefixes) and a
-  // broken one a unit; items: one a tile and the target; partial rows: every
-  // row twice and a whole tile for each item beyond its tile's first
+  // broken one a unit; items: one a tile and the larger target; partial rows:
+  // every row twice and a whole tile for each item beyond its tile's first
   a->cap_tiles = 2 * (b->n_tokens / a->tpt_many) + b->n_seqs + b->n_groups;
-  a->cap_items = a->cap_tiles + a->target;
-  a->cap_rows = 2 * b->n_tokens * gq + a->target * kRows;
+  a->cap_items = a->cap_tiles + a->target_few;
+  a->cap_rows = 2 * b->n_tokens * gq + a->target_many * kRows + a->target_few * kFew;
   size_t at = H_WORDS * 4;
   auto take = [&](size_t n) {
     const size_t o = at;
@@ -916,7 +1181,10 @@ extern "C" int tcl_attn_apply(const tcl_attn_batch *b, const tcl_kv_cache *c, in
     return fail(TCL_ENOSPC, "attn: workspace holds %zu bytes, needs %zu", ws_bytes, ws_total(s));
   const char *p = static_cast<const char *>(plan);
   a.q = static_cast<const uint16_t *>(q), a.o = static_cast<uint16_t *>(o), a.lse = lse;
-  a.ldq = ldq, a.ldo = ldo, a.scale2 = scale * 1.44269504088896341f;
+  a.ldq = ldq, a.ldo = ldo;
+  // (never zero: a hidden key's -infinity times zero would be a NaN)
+  a.scale2 = std::fmax(std::fabs(scale) * 1.44269504088896341f, 1e-37f);
+  a.q_sign = scale < 0 ? 0x8000 : 0;
   a.S = b->n_seqs, a.G = b->n_groups, a.T = b->n_tokens, a.ldp = b->ld_prefix;
   a.ld_own = b->ld_own, a.Hq = n_q_heads;
   a.prefix_pages = b->prefix_pages, a.own_pages = b->own_pages;

@@ -216,6 +216,49 @@ def test_extreme_scores():
     assert float((err > 0.05).double().mean()) < 0.01
 
 
+@pytest.mark.parametrize("Hq,Hkv,D,page,head_major", [
+    (8, 2, 64, 16, True), (4, 1, 128, 32, False), (3, 1, 256, 64, True), (32, 1, 128, 8, True)])
+@pytest.mark.parametrize("where", ["V", "K"])
+def test_infinities_and_nans_of_hidden_keys(where, Hq, Hkv, D, page, head_major):
+    """Keys that only some rows see (the newest ones, the end of a prefix that
+    a request without own keys does not reach) and slots behind every length
+    hold infinities and NaNs: rows that do not see them are as ever, rows that
+    do are what the sum gives in 64 bits."""
+    b = Batch(15, [(70, [(3, 20), (90, 100), (1, 9), (2, 70)]), (130, [(150, 20), (1, 0), (40, 70)])],
+              Hq, Hkv, D, page, head_major)
+    X = b.Vh if where == "V" else b.Kh
+    g = torch.Generator().manual_seed(1)
+    kinds = torch.tensor([float("nan"), float("inf"), -float("inf")])
+    used = torch.zeros(X.shape[:2], dtype=torch.bool)
+
+    def slots(pages, n, at):
+        return int(pages[at // page]), at % page
+
+    for pages, n in [(b.prefix_pages[i], p) for i, (p, _) in enumerate(b.groups)] + [
+            (b.own_pages[i], s[1]) for i, s in enumerate(b.seqs)]:
+        for j in range(n):
+            used[slots(pages, n, j)] = True
+        for back in (1, 2, 5, 17):  # the last keys, a few dimensions each
+            if n > back:
+                pg, of = slots(pages, n, n - back)
+                d = torch.randint(0, D, (3,), generator=g)
+                X[pg, of, int(torch.randint(0, Hkv, (1,), generator=g)), d] = kinds[
+                    torch.randint(0, 3, (3,), generator=g)].to(X.dtype)
+    b.Kh[~used] = float("nan")
+    b.Vh[~used] = float("nan")
+    b.up(b.Kh, b.Vh)
+    o = tclora.attention(b.plan(), b.qd).double().cpu().view(b.T, Hq, D)
+    wo, _, tol = b.want()
+    assert torch.equal(torch.isnan(o), torch.isnan(wo))
+    inf = torch.isinf(wo)
+    assert torch.equal(o[inf], wo[inf]) and bool(inf.any()) == (where == "V")
+    ok = torch.isfinite(wo)
+    assert float(ok.double().mean()) > 0.2
+    # (a row's bound counts every visible |V|: where one is infinite only the
+    # finite dimensions are held to theirs)
+    assert float(((o - wo).abs() - tol)[ok].max()) <= 1e-30
+
+
 def test_bad_tables_change_nothing():
     base = [(100, [(1, 30), (2, 40)]), (50, [(1, 20)])]
     o = torch.full((4, 256), 3.0, dtype=torch.bfloat16, device=DEV)
