@@ -14,6 +14,7 @@
 // the running maximum and sum are per-lane numbers with one exchange between
 // lane halves (or quarters) a step, and the probabilities leave the first
 // product in the very registers the second wants them in.
+#include <algorithm>
 #include <cmath>
 #include <type_traits>
 
@@ -47,34 +48,34 @@ __device__ inline int key_end(int prefix, int n) {
 }
 
 enum { H_CODE, H_MAGIC, H_SEQS, H_GROUPS, H_TOKENS, H_HEADS, H_KVHEADS, H_DIM, H_PAGES, H_SHIFT,
-       H_LDO, H_LDP, H_ITEMS, H_TILES, H_SHARED, H_WORDS = 64 };
+       H_LDO, H_LDP, H_ITEMS, H_TILES, H_SHARED, H_FLAGS = 16, H_WORDS = 64 };
+constexpr int kCheckers = 16;  // workgroups that look page ids over, a flag each
 
 struct alignas(16) Work {
-  int32_t tok0, list, n_tok;    // as in Tile
-  int32_t seq, group, prefix;
-  int32_t lo, hi;   // keys [lo, hi), lo a whole step
-  int32_t part;     // first partial row, -1: write the output itself
-  int32_t pad[3];
-};
-
-struct Tile {
   int32_t tok0;     // first token, or first entry of the token list (list 1)
   int32_t list;
   int32_t n_tok;    // tokens
   int32_t seq, group;
   int32_t prefix;   // keys of the prefix
-  int32_t lo, hi;   // key range
-  int32_t part0;    // first partial row
-  int32_t n_split;
-  int32_t chunk;    // keys an item
-  int32_t item0;
+  int32_t lo, hi;   // keys [lo, hi), lo a whole step
+  int32_t part;     // first partial row, -1: write the output itself
+  int32_t pad[3];
 };
 
-struct TokRec {
-  int32_t vis;      // keys the token sees, -1: no request owns it
-  int32_t own, own_at;  // tile over its own range, its place among the tile's tokens
-  int32_t pre, pre_at;  // tile over its group's prefix, -1: none
-  int32_t pad[3];
+struct alignas(16) Tile {
+  int32_t n_tok;    // tokens
+  int32_t n_split;  // items
+  int32_t part0;    // first partial row, -1: its one item writes the output
+  int32_t pad;
+};
+
+// A token: where the partial rows of its first head lie.  Item i of its own
+// range has row own + i * own_step, i < own_n; of its group's prefix likewise.
+struct alignas(16) TokRec {
+  int32_t vis;  // keys the token sees, -1: no request owns it
+  int32_t own, own_n, own_step;
+  int32_t pre, pre_n, pre_step;
+  int32_t join;  // 0: an item wrote the output
 };
 
 struct PlanArgs {
@@ -93,6 +94,14 @@ struct PlanArgs {
   int32_t *short_tok;  // [S + 1] tokens of short requests before this one
   int32_t *short_seq;  // [S + 1] short requests before this one
   int32_t *utile;      // [G + S] first tile of a unit (groups first)
+};
+
+// The mapping's view of the small arrays: in LDS for up to kMapThreads
+// requests and groups (every phase reads them, and a round trip to memory
+// each made up most of the launch), else in memory.
+struct MapView {
+  const int32_t *seq_tok, *group_seq, *prefix_len, *own_len;
+  int32_t *short_tok, *short_seq, *utile;
 };
 
 struct Layout {
@@ -148,34 +157,34 @@ __device__ inline bool is_short(const PlanArgs &a, int q) {
   return q > 0 && int64_t(q) * (a.Hq / a.Hkv) < kShortRows;
 }
 
-__device__ inline bool shares(const PlanArgs &a, int g) {
-  const int b = a.group_seq[g], e = a.group_seq[g + 1];
-  return a.prefix_len[g] > 0 && a.short_seq[e] - a.short_seq[b] >= 2;
+__device__ inline bool shares(const PlanArgs &a, const MapView &m, int g) {
+  const int b = m.group_seq[g], e = m.group_seq[g + 1];
+  return m.prefix_len[g] > 0 && m.short_seq[e] - m.short_seq[b] >= 2;
 }
 
 // unit u: group u's prefix for u < G, request u - G's own keys (and its
 // prefix, if it does not share it) above
-__device__ inline Unit unit_of(const PlanArgs &a, int u) {
+__device__ inline Unit unit_of(const PlanArgs &a, const MapView &m, int u) {
   Unit x{};
   const int gq = a.Hq / a.Hkv;
   if (u < a.G) {
-    if (!shares(a, u)) return x;
-    const int b = a.group_seq[u], e = a.group_seq[u + 1];
-    x.tok0 = a.short_tok[b];
-    x.n_tok = a.short_tok[e] - x.tok0;
+    if (!shares(a, m, u)) return x;
+    const int b = m.group_seq[u], e = m.group_seq[u + 1];
+    x.tok0 = m.short_tok[b];
+    x.n_tok = m.short_tok[e] - x.tok0;
     x.list = 1;
     x.group = u;
-    x.prefix = x.hi = a.prefix_len[u];
+    x.prefix = x.hi = m.prefix_len[u];
   } else {
     const int s = u - a.G;
-    x.tok0 = a.seq_tok[s];
-    x.n_tok = x.n_q = a.seq_tok[s + 1] - x.tok0;
+    x.tok0 = m.seq_tok[s];
+    x.n_tok = x.n_q = m.seq_tok[s + 1] - x.tok0;
     x.seq = s;
-    x.group = upper(a.group_seq, a.G, s);
+    x.group = upper(m.group_seq, a.G, s);
     // (empty groups: the one whose range holds s)
-    x.prefix = a.prefix_len[x.group];
-    x.lo = is_short(a, x.n_q) && shares(a, x.group) ? whole(x.prefix) : 0;
-    x.hi = x.prefix + a.own_len[s];  // (a count here)
+    x.prefix = m.prefix_len[x.group];
+    x.lo = is_short(a, x.n_q) && shares(a, m, x.group) ? whole(x.prefix) : 0;
+    x.hi = x.prefix + m.own_len[s];  // (a count here)
   }
   x.rows = x.n_tok * gq;
   x.tpt = x.rows <= kFew ? a.tpt_few : a.tpt_many;
@@ -193,14 +202,52 @@ __device__ inline int tile_hi(const Unit &x, int i) {
   return max(x.lo, key_end(x.prefix, max(0, x.hi - x.n_q + last + 1)));
 }
 
+// Workgroups 1 .. kCheckers look page ids over, a row of a page table a wave,
+// and leave a flag each; workgroup 0 does the rest.  One launch: the flags
+// are read with the header.
+template <bool LDS>
 __global__ __launch_bounds__(kMapThreads) void attn_plan_kernel(PlanArgs a) {
   __shared__ int lds[kMapThreads / 64];
   __shared__ int s_err, s_chunk[2];
   __shared__ unsigned long long s_work;
+  constexpr int NS = LDS ? kMapThreads + 1 : 1;
+  __shared__ int32_t l_seq_tok[NS], l_group_seq[NS], l_prefix_len[NS], l_own_len[NS],
+      l_short_tok[NS], l_short_seq[NS], l_utile[2 * NS];
   const int tid = threadIdx.x, gq = a.Hq / a.Hkv;
+  const int page = 1 << a.page_shift;
   if (tid == 0) {
     s_err = 0;
     s_work = 0;
+  }
+  if (blockIdx.x > 0) {
+    __syncthreads();
+    const int w = (int(blockIdx.x) - 1) * (kMapThreads / 64) + (tid >> 6), lane = tid & 63;
+    bool bad = false;
+    for (int r = w; r < a.S + a.G; r += kCheckers * (kMapThreads / 64)) {
+      const bool own = r < a.S;
+      const int g = r - a.S, ld = own ? a.ldo : a.ldp;
+      // (a length that does not fit is workgroup 0's finding)
+      const int len = min(max(own ? a.own_len[r] : a.prefix_len[g], 0), ld * page);
+      const int n = (len + page - 1) >> a.page_shift;
+      const int32_t *p = own ? a.own_pages + int64_t(r) * a.ldo : a.prefix_pages + int64_t(g) * a.ldp;
+      for (int i = lane; i < n; i += 64) bad |= p[i] < 0 || p[i] >= a.n_pages;
+    }
+    if (bad) s_err = 1;
+    __syncthreads();
+    if (tid == 0) a.hdr[H_FLAGS + blockIdx.x - 1] = s_err;
+    return;
+  }
+  MapView m{a.seq_tok, a.group_seq, a.prefix_len, a.own_len, a.short_tok, a.short_seq, a.utile};
+  if constexpr (LDS) {
+    if (a.S > 0) {
+      for (int i = tid; i <= a.S; i += kMapThreads) l_seq_tok[i] = a.seq_tok[i];
+      for (int i = tid; i <= a.G; i += kMapThreads) l_group_seq[i] = a.group_seq[i];
+      if (tid < a.S) l_own_len[tid] = a.own_len[tid];
+      if (tid < a.G) l_prefix_len[tid] = a.prefix_len[tid];
+    }
+    m = MapView{l_seq_tok, l_group_seq, l_prefix_len, l_own_len, l_short_tok, l_short_seq, l_utile};
+  }
+  if (tid == 0) {
     a.hdr[H_MAGIC] = kMagic, a.hdr[H_SEQS] = a.S, a.hdr[H_GROUPS] = a.G, a.hdr[H_TOKENS] = a.T;
     a.hdr[H_HEADS] = a.Hq, a.hdr[H_KVHEADS] = a.Hkv, a.hdr[H_DIM] = a.D;
     a.hdr[H_PAGES] = a.n_pages, a.hdr[H_SHIFT] = a.page_shift;
@@ -211,31 +258,17 @@ __global__ __launch_bounds__(kMapThreads) void attn_plan_kernel(PlanArgs a) {
   // the table
   bool bad = false;
   if (tid == 0 && a.S > 0)
-    bad = a.seq_tok[0] != 0 || a.seq_tok[a.S] > a.T || a.group_seq[0] != 0 ||
-          a.group_seq[a.G] != a.S;
-  const int page = 1 << a.page_shift;
+    bad = m.seq_tok[0] != 0 || m.seq_tok[a.S] > a.T || m.group_seq[0] != 0 ||
+          m.group_seq[a.G] != a.S;
   for (int s = tid; s < a.S; s += kMapThreads) {
-    bad |= a.seq_tok[s + 1] < a.seq_tok[s];
-    bad |= a.own_len[s] < 0 || a.own_len[s] > a.ldo * page;
+    bad |= m.seq_tok[s + 1] < m.seq_tok[s];
+    bad |= m.own_len[s] < 0 || m.own_len[s] > a.ldo * page;
   }
   for (int g = tid; g < a.G; g += kMapThreads) {
-    bad |= a.group_seq[g + 1] < a.group_seq[g];
-    bad |= a.prefix_len[g] < 0 || a.prefix_len[g] > a.ldp * page;
+    bad |= m.group_seq[g + 1] < m.group_seq[g];
+    bad |= m.prefix_len[g] < 0 || m.prefix_len[g] > a.ldp * page;
   }
   if (bad) s_err = 1;
-  __syncthreads();
-  if (!s_err) {
-    // a row of page ids a wave
-    const int w = tid >> 6, lane = tid & 63;
-    for (int r = w; r < a.S + a.G; r += kMapThreads / 64) {
-      const bool own = r < a.S;
-      const int g = r - a.S;
-      const int n = ((own ? a.own_len[r] : a.prefix_len[g]) + page - 1) >> a.page_shift;
-      const int32_t *p = own ? a.own_pages + int64_t(r) * a.ldo : a.prefix_pages + int64_t(g) * a.ldp;
-      for (int i = lane; i < n; i += 64) bad |= p[i] < 0 || p[i] >= a.n_pages;
-    }
-    if (bad) s_err = 1;
-  }
   __syncthreads();
   if (s_err) {
     if (tid == 0) a.hdr[H_CODE] = TCL_EINVAL;
@@ -245,28 +278,28 @@ __global__ __launch_bounds__(kMapThreads) void attn_plan_kernel(PlanArgs a) {
   int tok_base = 0, seq_base = 0;
   for (int s0 = 0; s0 < a.S; s0 += kMapThreads) {
     const int s = s0 + tid;
-    const int q = s < a.S ? a.seq_tok[s + 1] - a.seq_tok[s] : 0;
+    const int q = s < a.S ? m.seq_tok[s + 1] - m.seq_tok[s] : 0;
     const bool sh = is_short(a, q);
     int et, es;
     const int nt = block_scan(sh ? q : 0, &et, lds);
     const int ns = block_scan(sh ? 1 : 0, &es, lds);
     if (s < a.S) {
-      a.short_tok[s] = tok_base + et;
-      a.short_seq[s] = seq_base + es;
+      m.short_tok[s] = tok_base + et;
+      m.short_seq[s] = seq_base + es;
     }
     tok_base += nt;
     seq_base += ns;
   }
   if (tid == 0) {
-    a.short_tok[a.S] = tok_base;
-    a.short_seq[a.S] = seq_base;
+    m.short_tok[a.S] = tok_base;
+    m.short_seq[a.S] = seq_base;
   }
   __syncthreads();
   // keys over all tiles: the length of an item
   const int U = a.G + a.S;
   unsigned long long work = 0;
   for (int u = tid; u < U; u += kMapThreads) {
-    const Unit x = unit_of(a, u);
+    const Unit x = unit_of(a, m, u);
     const int n = unit_tiles(x);
     for (int i = 0; i < n; ++i) work += unsigned(tile_hi(x, i) - x.lo);
   }
@@ -283,7 +316,7 @@ __global__ __launch_bounds__(kMapThreads) void attn_plan_kernel(PlanArgs a) {
   for (int u0 = 0; u0 < U; u0 += kMapThreads) {
     const int u = u0 + tid;
     Unit x{};
-    if (u < U) x = unit_of(a, u);
+    if (u < U) x = unit_of(a, m, u);
     const int n = unit_tiles(x), chunk = s_chunk[x.rows > kFew];
     int ni = 0, nr = 0;
     for (int i = 0; i < n; ++i) {
@@ -296,7 +329,7 @@ __global__ __launch_bounds__(kMapThreads) void attn_plan_kernel(PlanArgs a) {
     const int tt = block_scan(n, &et, lds), ti = block_scan(ni, &ei, lds),
               tr = block_scan(nr, &er, lds);
     et += tile_base, ei += item_base, er += row_base;
-    if (u < U) a.utile[u] = et;
+    if (u < U) m.utile[u] = et;
     // (the capacities hold every table of these sizes; a tile beyond them
     // could only come from a table that changed under the launch)
     for (int i = 0; i < n; ++i) {
@@ -306,8 +339,7 @@ __global__ __launch_bounds__(kMapThreads) void attn_plan_kernel(PlanArgs a) {
       const int per = max(kKeys, ((len + ns - 1) / ns + kKeys - 1) / kKeys * kKeys);
       if (et >= a.cap_tiles || ei + ns > a.cap_items || er + ns * nt * gq > a.cap_rows) break;
       const bool direct = ns == 1 && !x.list && x.lo == 0;
-      a.tiles[et] = Tile{x.tok0 + i * x.tpt, x.list, nt, x.seq, x.group, x.prefix, x.lo, hi,
-                         direct ? -1 : er, ns, per, ei};
+      a.tiles[et] = Tile{nt, ns, direct ? -1 : er, 0};
       for (int k = 0; k < ns; ++k) {
         const int lo = min(hi, x.lo + k * per);
         a.items[ei + k] = Work{x.tok0 + i * x.tpt, x.list, nt, x.seq, x.group, x.prefix, lo,
@@ -320,20 +352,25 @@ __global__ __launch_bounds__(kMapThreads) void attn_plan_kernel(PlanArgs a) {
   __syncthreads();
   // tokens
   for (int t = tid; t < a.T; t += kMapThreads) {
-    TokRec r{-1, 0, 0, -1, 0, {0, 0, 0}};
-    if (a.S > 0 && t < a.seq_tok[a.S]) {
-      const int s = upper(a.seq_tok, a.S, t);
-      const Unit x = unit_of(a, a.G + s);
+    TokRec r{-1, 0, 0, 0, 0, 0, 0, 0};
+    if (a.S > 0 && t < m.seq_tok[a.S]) {
+      const int s = upper(m.seq_tok, a.S, t);
+      const Unit x = unit_of(a, m, a.G + s);
       const int i = t - x.tok0;
       r.vis = max(0, x.hi - x.n_q + i + 1);  // (a count)
-      r.own = a.utile[a.G + s] + i / x.tpt;
-      r.own_at = i % x.tpt;
-      if (is_short(a, x.n_q) && shares(a, x.group)) {
-        const Unit p = unit_of(a, x.group);
-        const int at = a.short_tok[s] + i;
-        a.list[at] = t;
-        r.pre = a.utile[x.group] + (at - p.tok0) / p.tpt;
-        r.pre_at = (at - p.tok0) % p.tpt;
+      const Tile o = a.tiles[min(m.utile[a.G + s] + i / x.tpt, a.cap_tiles - 1)];
+      r.own = o.part0 + i % x.tpt * gq;
+      r.own_n = o.n_split;
+      r.own_step = o.n_tok * gq;
+      r.join = o.part0 >= 0;
+      if (is_short(a, x.n_q) && shares(a, m, x.group)) {
+        const Unit p = unit_of(a, m, x.group);
+        const int at = m.short_tok[s] + i;
+        a.list[min(at, a.T - 1)] = t;
+        const Tile q = a.tiles[min(m.utile[x.group] + (at - p.tok0) / p.tpt, a.cap_tiles - 1)];
+        r.pre = q.part0 + (at - p.tok0) % p.tpt * gq;
+        r.pre_n = q.n_split;
+        r.pre_step = q.n_tok * gq;
       }
     }
     a.tok[t] = r;
@@ -345,11 +382,20 @@ __global__ __launch_bounds__(kMapThreads) void attn_plan_kernel(PlanArgs a) {
   }
 }
 
+__device__ inline bool pages_ok(const int32_t *hdr) {
+  int bad = 0;
+#pragma unroll
+  for (int i = 0; i < kCheckers; ++i) bad |= hdr[H_FLAGS + i];
+  return bad == 0;
+}
+
 __global__ void attn_status_kernel(const int32_t *hdr, int32_t *out) {
-  if (threadIdx.x < 4) {
-    const int w[4] = {H_CODE, H_ITEMS, H_TILES, H_SHARED};
-    out[threadIdx.x] = hdr[w[threadIdx.x]];
-  }
+  if (threadIdx.x > 0) return;
+  const bool ok = hdr[H_CODE] == TCL_OK && pages_ok(hdr);
+  out[0] = ok ? TCL_OK : TCL_EINVAL;
+  out[1] = ok ? hdr[H_ITEMS] : 0;
+  out[2] = ok ? hdr[H_TILES] : 0;
+  out[3] = ok ? hdr[H_SHARED] : 0;
 }
 
 // ---------------------------------------------------------------------------
@@ -367,7 +413,6 @@ struct AttnArgs {
   const int32_t *prefix_pages, *own_pages;
   const int32_t *hdr;
   const TokRec *tok;
-  const Tile *tiles;
   const Work *items;
   const int32_t *list;
   float *part_o;   // [rows][Hkv][D], not divided by the sum
@@ -380,7 +425,7 @@ __device__ inline bool plan_fits(const AttnArgs &a) {
   return h[H_MAGIC] == kMagic && h[H_CODE] == TCL_OK && h[H_SEQS] == a.S && h[H_GROUPS] == a.G &&
          h[H_TOKENS] == a.T && h[H_HEADS] == a.Hq && h[H_KVHEADS] == a.c.H && h[H_DIM] == a.c.D &&
          h[H_PAGES] == a.c.n_pages && h[H_SHIFT] == a.c.page_shift && h[H_LDO] == a.ld_own &&
-         h[H_LDP] == a.ldp;
+         h[H_LDP] == a.ldp && pages_ok(h);
 }
 
 typedef __attribute__((__vector_size__(16 * sizeof(float)))) float f32x16_t;
@@ -937,70 +982,65 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_kernel(AttnArgs a)
     attend_many<D>(a, t, h, gq, sm);
 }
 
-// Joins the items of one row a wave: maxima first, then the weighted sums in
-// item order (own items, then the prefix's).
+// Joins the items of a token's rows, a row a wave at a time: maxima first,
+// then the weighted sums in item order (own items, then the prefix's).
 template <int D>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
-  if (!plan_fits(a)) return;
-  const int lane = threadIdx.x & 63;
-  const int64_t id = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
-  const int tk = int(id / a.Hq), hh = int(id % a.Hq);
-  if (tk >= a.T) return;
+  const int tk = blockIdx.x;
   const TokRec r = a.tok[tk];
-  if (r.vis < 0) return;
-  const int gq = a.Hq / a.c.H, h = hh / gq;
-  const Tile own = a.tiles[r.own];
-  if (own.part0 < 0 && r.pre < 0) return;  // written already
-  float M = -INFINITY;
-  for (int s = 0; s < 2; ++s) {
-    if (s == 1 && r.pre < 0) break;
-    const Tile t = s ? a.tiles[r.pre] : own;
-    const int row = (s ? r.pre_at : r.own_at) * gq + hh % gq, step = t.n_tok * gq;
-    for (int k = lane; k < t.n_split; k += 64)
-      M = fmaxf(M, a.part_ml[int64_t(t.part0 + row + k * step) * a.c.H + h].x);
-  }
-#pragma unroll
-  for (int x = 32; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor(M, x, 64));
-  const float mu = M == -INFINITY ? 0.f : M;
+  if (!plan_fits(a) || r.vis < 0 || !r.join) return;
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int gq = a.Hq / a.c.H;
   constexpr int E = D / 64;
   typedef float fe __attribute__((ext_vector_type(E)));
-  float L = 0.f;
-  fe v;
+  for (int hh = blockIdx.y * 4 + w; hh < a.Hq; hh += gridDim.y * 4) {
+    const int h = hh / gq;
+    // partial row (times heads) of item k: first + k * step
+    const int64_t first[2] = {int64_t(r.own + hh % gq) * a.c.H + h, int64_t(r.pre + hh % gq) * a.c.H + h};
+    const int64_t step[2] = {int64_t(r.own_step) * a.c.H, int64_t(r.pre_step) * a.c.H};
+    const int n[2] = {r.own_n, r.pre_n};
+    float M = -INFINITY;
 #pragma unroll
-  for (int e = 0; e < E; ++e) v[e] = 0.f;
-  for (int s = 0; s < 2; ++s) {
-    if (s == 1 && r.pre < 0) break;
-    const Tile t = s ? a.tiles[r.pre] : own;
-    const int row = (s ? r.pre_at : r.own_at) * gq + hh % gq, step = t.n_tok * gq;
-    const int64_t pr = int64_t(t.part0 + row) * a.c.H + h;
-    auto add = [&](auto n_, int k0) {
-      constexpr int n = decltype(n_)::value;
-      float2 ml[n];
-      fe u[n];
+    for (int s = 0; s < 2; ++s)
+      for (int k = lane; k < n[s]; k += 64) M = fmaxf(M, a.part_ml[first[s] + k * step[s]].x);
 #pragma unroll
-      for (int k = 0; k < n; ++k) {
-        const int64_t p = pr + int64_t(k0 + k) * step * a.c.H;
-        ml[k] = a.part_ml[p];
-        u[k] = *reinterpret_cast<const fe *>(a.part_o + p * D + lane * E);
-      }
+    for (int x = 32; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor(M, x, 64));
+    const float mu = M == -INFINITY ? 0.f : M;
+    float L = 0.f;
+    fe v;
 #pragma unroll
-      for (int k = 0; k < n; ++k) {
-        const float f = __builtin_amdgcn_exp2f(ml[k].x - mu);
-        L += ml[k].y * f;
+    for (int e = 0; e < E; ++e) v[e] = 0.f;
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[e] += u[k][e] * f;
-      }
-    };
-    int k = 0;
-    for (; k + 8 <= t.n_split; k += 8) add(std::integral_constant<int, 8>{}, k);
-    for (; k + 2 <= t.n_split; k += 2) add(std::integral_constant<int, 2>{}, k);
-    if (k < t.n_split) add(std::integral_constant<int, 1>{}, k);
+    for (int s = 0; s < 2; ++s) {
+      auto add = [&](auto n_, int k0) {
+        constexpr int N = decltype(n_)::value;
+        float2 ml[N];
+        fe u[N];
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          const int64_t p = first[s] + (k0 + k) * step[s];
+          ml[k] = a.part_ml[p];
+          u[k] = *reinterpret_cast<const fe *>(a.part_o + p * D + lane * E);
+        }
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          const float f = __builtin_amdgcn_exp2f(ml[k].x - mu);
+          L += ml[k].y * f;
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[e] += u[k][e] * f;
+        }
+      };
+      int k = 0;
+      for (; k + 8 <= n[s]; k += 8) add(std::integral_constant<int, 8>{}, k);
+      for (; k + 2 <= n[s]; k += 2) add(std::integral_constant<int, 2>{}, k);
+      if (k < n[s]) add(std::integral_constant<int, 1>{}, k);
+    }
+    const float f = L > 0.f || L != L ? 1.f / L : 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      a.o[tk * a.ldo + int64_t(hh) * D + lane * E + e] = f32_to_bf16(v[e] * f);
+    if (a.lse && lane == 0) a.lse[int64_t(tk) * a.Hq + hh] = log_sum(M, L);
   }
-  const float f = L > 0.f || L != L ? 1.f / L : 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e)
-    a.o[tk * a.ldo + int64_t(hh) * D + lane * E + e] = f32_to_bf16(v[e] * f);
-  if (a.lse && lane == 0) a.lse[int64_t(tk) * a.Hq + hh] = log_sum(M, L);
 }
 
 // ---------------------------------------------------------------------------
@@ -1083,8 +1123,9 @@ int check_plan(const void *plan, size_t bytes, size_t need) {
 template <int D>
 void launch(const AttnArgs &a, int cap_items, hipStream_t s) {
   hipLaunchKernelGGL(attn_kernel<D>, dim3(unsigned(cap_items) * a.c.H), dim3(256), 0, s, a);
-  const int64_t rows = int64_t(a.T) * a.Hq;
-  hipLaunchKernelGGL(attn_join_kernel<D>, dim3(unsigned((rows + 3) / 4)), dim3(256), 0, s, a);
+  // a row a wave, until that is eight workgroups a CU and more
+  const int by_row = (a.Hq + 3) / 4, parts = a.T >= 2048 ? 1 : std::min(by_row, 4096 / a.T + 1);
+  hipLaunchKernelGGL(attn_join_kernel<D>, dim3(a.T, parts), dim3(256), 0, s, a);
 }
 
 }  // namespace
@@ -1142,8 +1183,12 @@ extern "C" int tcl_attn_plan(const tcl_attn_batch *b, const tcl_kv_cache *c, int
   a.short_tok = reinterpret_cast<int32_t *>(p + L.o_stok);
   a.short_seq = reinterpret_cast<int32_t *>(p + L.o_sseq);
   a.utile = reinterpret_cast<int32_t *>(p + L.o_utile);
-  hipLaunchKernelGGL(attn_plan_kernel, dim3(1), dim3(kMapThreads), 0,
-                     static_cast<hipStream_t>(stream), a);
+  const dim3 grid(1 + kCheckers), block(kMapThreads);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (a.S <= kMapThreads && a.G <= kMapThreads)
+    hipLaunchKernelGGL(attn_plan_kernel<true>, grid, block, 0, s, a);
+  else
+    hipLaunchKernelGGL(attn_plan_kernel<false>, grid, block, 0, s, a);
   TCL_HIP(hipGetLastError());
   return TCL_OK;
 }
@@ -1190,7 +1235,6 @@ extern "C" int tcl_attn_apply(const tcl_attn_batch *b, const tcl_kv_cache *c, in
   a.prefix_pages = b->prefix_pages, a.own_pages = b->own_pages;
   a.hdr = reinterpret_cast<const int32_t *>(p);
   a.tok = reinterpret_cast<const TokRec *>(p + L.o_tok);
-  a.tiles = reinterpret_cast<const Tile *>(p + L.o_tiles);
   a.items = reinterpret_cast<const Work *>(p + L.o_items);
   a.list = reinterpret_cast<const int32_t *>(p + L.o_list);
   a.part_o = static_cast<float *>(ws);
