@@ -487,6 +487,12 @@ __device__ inline Part part_of(const AttnArgs &a, const Work &t, int j0) {
 // by one to the rows that see it, zero takes its place in LDS, and the matrix
 // product goes on as ever.
 __device__ inline bool bad_bf16(uint32_t w) { return (w & 0x7f80u) == 0x7f80u; }
+__device__ inline nt_u4 cleaned(nt_u4 u) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    u[e] = (bad_bf16(u[e]) ? 0 : u[e] & 0xffffu) | (bad_bf16(u[e] >> 16) ? 0 : u[e] & 0xffff0000u);
+  return u;
+}
 
 // Moves an item's keys and values, 64 a step, through registers into LDS:
 // wave w the rows 16 w .. 16 w + 15 of a step.  Where those lie in one page
@@ -569,11 +575,7 @@ struct Stage {
     for (int i = 0; i < NI; ++i) {
       const int r = 16 * w + row + i * RPI;
       nt_u4 *p = reinterpret_cast<nt_u4 *>(sv + r * D + 8 * (col ^ swz<D>(r)));
-      nt_u4 u = *p;
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        u[e] = (bad_bf16(u[e]) ? 0 : u[e] & 0xffffu) | (bad_bf16(u[e] >> 16) ? 0 : u[e] & 0xffff0000u);
-      *p = u;
+      *p = cleaned(*p);
     }
   }
   __device__ inline void put(uint16_t *sk, uint16_t *sv) const {
@@ -778,23 +780,131 @@ __device__ inline void attend_few(const AttnArgs &a, const Work &t, int h, int g
   }
 }
 
+// Moves a step's keys and values straight into LDS, wave w the rows 16 w .. 16
+// w + 15: 64 lanes write 1 KiB in a row, so a lane fetches the chunk that
+// belongs where it writes.  Such loads take no registers and are not counted
+// by the compiler; arrived() waits for all of them.  Their immediate offset
+// moves source and destination alike, so one M0 serves four instructions.
+template <int D>
+struct Direct {
+  static constexpr int CH = D / 8;     // chunks of a row
+  static constexpr int RPI = 64 / CH;  // rows an instruction moves
+  static constexpr int NI = 16 / RPI;  // instructions for a wave's 16 rows
+  static_assert(NI == 2 || NI == 4 || NI == 8, "head dimension");
+  int w, row, page;
+  unsigned off[NI];  // bytes from the wave's first row, less the immediate offset
+  int64_t head;
+  bool paged;
+
+  __device__ inline void init(const AttnArgs &a, int h) {
+    const int lane = threadIdx.x & 63;
+    w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    row = lane / CH;
+    head = int64_t(h) * a.c.s_head;
+    paged = a.c.page_shift >= 4 && a.c.s_slot >= D && a.c.s_slot < (int64_t(1) << 26);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int r = i * RPI + row;
+      off[i] = 2 * (unsigned(r) * unsigned(a.c.s_slot) + 8 * (lane % CH ^ swz<D>(r))) - 1024 * (i & 3);
+    }
+  }
+  __device__ inline int clamp(const AttnArgs &a, int p) const {
+    return min(max(p, 0), a.c.n_pages - 1);
+  }
+  // reads the page of the wave's rows of the next step to be loaded
+  __device__ inline void pages(const AttnArgs &a, const Work &t, int j0) {
+    if (!paged || j0 >= t.hi) return;
+    const Part p = part_of(a, t, j0);
+    page = p.table[min(p.i0 + 16 * w, p.last) >> a.c.page_shift];
+  }
+  __device__ static inline uint32_t lds(const uint16_t *p) {
+    return uint32_t(uintptr_t((__attribute__((address_space(3))) const uint16_t *)(p)));
+  }
+  __device__ inline void load(const AttnArgs &a, const Work &t, int j0, uint16_t *sk,
+                              uint16_t *sv) const {
+    const Part p = part_of(a, t, j0);
+    const int mask = (1 << a.c.page_shift) - 1;
+    const uint32_t to[2] = {lds(sk + 16 * w * D), lds(sv + 16 * w * D)};
+    if (paged && p.i0 + kKeys - 1 <= p.last) {
+      const int64_t at = int64_t(clamp(a, __builtin_amdgcn_readfirstlane(page))) * a.c.s_page +
+                         int64_t((p.i0 + 16 * w) & mask) * a.c.s_slot + head;
+      const uint16_t *from[2] = {a.c.K + at, a.c.V + at};
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if constexpr (NI == 2)
+          asm volatile(
+              "s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %3\n\t"
+              "global_load_lds_dwordx4 %2, %3 offset:1024" ::"s"(to[x]),
+              "v"(off[0]), "v"(off[1]), "s"(from[x])
+              : "memory", "m0");
+        else
+#pragma unroll
+          for (int i = 0; i < NI; i += 4)
+            asm volatile(
+                "s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %5\n\t"
+                "global_load_lds_dwordx4 %2, %5 offset:1024\n\t"
+                "global_load_lds_dwordx4 %3, %5 offset:2048\n\t"
+                "global_load_lds_dwordx4 %4, %5 offset:3072" ::"s"(to[x] + 1024 * i),
+                "v"(off[i]), "v"(off[i + 1]), "v"(off[i + 2]), "v"(off[i + 3]), "s"(from[x])
+                : "memory", "m0");
+      }
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int r = 16 * w + i * RPI + row, j = min(p.i0 + r, p.last);
+      const int64_t at = int64_t(clamp(a, p.table[j >> a.c.page_shift])) * a.c.s_page +
+                         int64_t(j & mask) * a.c.s_slot + head +
+                         8 * ((threadIdx.x & 63) % CH ^ swz<D>(r));
+      const uint16_t *from[2] = {a.c.K + at, a.c.V + at};
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to[x] + 1024 * i),
+                     "v"(from[x])
+                     : "memory", "m0");
+    }
+  }
+  __device__ inline void arrived() const { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+  // values that are not finite among the wave's rows in LDS; zero for them
+  __device__ inline nt_u4 *chunk(uint16_t *sv, int i) const {
+    return reinterpret_cast<nt_u4 *>(sv + 16 * w * D) + 64 * i + (threadIdx.x & 63);
+  }
+  __device__ inline bool bad(uint16_t *sv) const {
+    bool x = false;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const nt_u4 u = *chunk(sv, i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x |= bad_bf16(u[e]) || bad_bf16(u[e] >> 16);
+    }
+    return x;
+  }
+  __device__ inline void clean(uint16_t *sv) const {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) *chunk(sv, i) = cleaned(*chunk(sv, i));
+  }
+};
+
 // Many rows: wave w holds rows 32 w .. 32 w + 31 over all keys of a step.
+// Operands are read from LDS some instructions before the matrix instruction
+// that takes them (sched_group_barrier): left to itself the compiler reads
+// each right before, and the LDS latencies, 48 a step, are twice the matrix
+// cores' time.
 template <int D>
 __device__ inline void attend_many(const AttnArgs &a, const Work &t, int h, int gq, Smem<D> &sm) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int rows = t.n_tok * gq, steps = (t.hi - t.lo + kKeys - 1) / kKeys;
-  Stage<D> st;
+  Direct<D> st;
   st.init(a, h);
-  if (steps > 0) st.pages(a, t, t.lo);
+  st.pages(a, t, t.lo);
   const int c = lane & 31, g = lane >> 5;
   const int r = 32 * w + c;
   const bool live = r < rows, busy = 32 * w < rows;
   const int tok = token_of(a, t, gq, live ? r : 0);
   const int hq = h * gq + (live ? r : 0) % gq;
-  if (steps > 0) {
-    st.load(a, t, t.lo);
-    st.pages(a, t, t.lo + kKeys);
-  }
+  if (steps > 0) st.load(a, t, t.lo, sm.k[0], sm.v[0]);
+  st.pages(a, t, t.lo + kKeys);
   const int vis = a.tok[tok].vis;
   // the fewest keys a row of the wave sees: a step beyond them hides some
   int least = live ? vis : 0x7fffffff;
@@ -823,54 +933,58 @@ __device__ inline void attend_many(const AttnArgs &a, const Work &t, int h, int 
     const int vr = 8 * x + 4 * g + (i16 >> 2);
     vpos[x] = vr * D + 8 * ((2 * sub + ((i16 & 3) >> 1)) ^ swz<D>(vr)) + 4 * (i16 & 1);
   }
-  // (of the whole tile: its steps that hide keys look values over together)
-  int tile_least = least;
-  {
-    int *x = reinterpret_cast<int *>(&sm);
-    if (lane == 0) x[w] = least;
-    __syncthreads();
-    for (int i = 0; i < 4; ++i) tile_least = min(tile_least, x[i]);
-    __syncthreads();
-    tile_least = __builtin_amdgcn_readfirstlane(tile_least);
-  }
+  // the whole tile's fewest keys: steps beyond them look their values over
+  __shared__ int s_least[4];
+  if (lane == 0) s_least[w] = least;
+  __syncthreads();
+  const int tile_least = __builtin_amdgcn_readfirstlane(
+      min(min(s_least[0], s_least[1]), min(s_least[2], s_least[3])));
+  auto hides = [&](int j0, int least_) { return j0 + kKeys > min(step_end(t, least_, j0), t.hi); };
   for (int n = 0; n < steps; ++n) {
     const int j0 = t.lo + n * kKeys, b = n & 1;
-    st.put(sm.k[b], sm.v[b]);
-    bool rare = false;
-    if (j0 + kKeys > min(step_end(t, tile_least, j0), t.hi))
-      rare = __syncthreads_or(st.bad());
+    // this step's keys and values have come; every wave is done with the
+    // buffers that the next loads write
+    st.arrived();
+    lds_barrier();
     if (n + 1 < steps) {
-      st.load(a, t, j0 + kKeys);
+      st.load(a, t, j0 + kKeys, sm.k[b ^ 1], sm.v[b ^ 1]);
       st.pages(a, t, j0 + 2 * kKeys);
     }
-    lds_barrier();
-    const uint16_t *sk = sm.k[0];
-    uint16_t *sv = sm.v[0];
-    const int kp = kpos + b * kKeys * D, vp0 = vpos[0] + b * kKeys * D, vp1 = vpos[1] + b * kKeys * D;
+    bool rare = false;
+    if (hides(j0, tile_least)) rare = __syncthreads_or(st.bad(sm.v[b]));
     uint32_t pw[4][4];
-    int end = 0;
     if (busy) {
+      const uint16_t *sk = sm.k[0];
+      const int kp = kpos + b * kKeys * D;
       f32x16_t s2[2];
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
+      for (int x = 0; x < 2; ++x)
 #pragma unroll
         for (int e = 0; e < 16; ++e) s2[x][e] = 0.f;
+      constexpr int AHEAD = 6;
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int s = 0; s < D / 16; ++s) {
+      for (int s = 0; s < D / 16; ++s)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
           const bf16x8_t kf = *reinterpret_cast<const bf16x8_t *>(sk + ((kp ^ (16 * s)) + 32 * x * D));
           s2[x] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, __builtin_bit_cast(bf16x8_t, qf[s]),
                                                           s2[x], 0, 0, 0);
         }
+      __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+        if (i + AHEAD < D / 8) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
       }
-      if (j0 + kKeys > min(step_end(t, least, j0), t.hi)) {
-        end = min(step_end(t, vis, j0), t.hi);
+      __builtin_amdgcn_sched_barrier(0);
+      if (hides(j0, least)) {
+        const int end = min(step_end(t, vis, j0), t.hi);
 #pragma unroll
         for (int x = 0; x < 2; ++x)
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            // (a constant against the lane's limit)
+          for (int e = 0; e < 16; ++e)  // (a constant against the lane's limit)
             if (32 * x + 8 * (e / 4) + e % 4 >= end - j0 - 4 * g) s2[x][e] = -INFINITY;
-          }
       }
       float mx = -INFINITY;
 #pragma unroll
@@ -901,7 +1015,7 @@ __device__ inline void attend_many(const AttnArgs &a, const Work &t, int h, int 
     }
     if (rare) {
       if (busy) {
-        end = min(step_end(t, vis, j0), t.hi);
+        const int end = min(step_end(t, vis, j0), t.hi);
 #pragma unroll 1
         for (int k = 0; k < kKeys; ++k) {
           // key k's weights: word k / 16, k / 8 % 2, k / 2 % 2 of the lane
@@ -913,22 +1027,25 @@ __device__ inline void attend_many(const AttnArgs &a, const Work &t, int h, int 
             for (int x = 0; x < 4; ++x)
               if (s == k >> 4 && x == ((k >> 3 & 1) << 1 | (k >> 1 & 1))) u = pw[s][x];
           u = __shfl(int(u), c + 32 * (k >> 2 & 1), 64);
-          const float pk = k & 1 ? bf16_hi(u) : bf16_lo(u);
+          const float wk = k & 1 ? bf16_hi(u) : bf16_lo(u);
           if (j0 + k >= end) continue;
 #pragma unroll
           for (int i = 0; i < D / 32; ++i)
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               const uint32_t y = value_at<D>(sm.v[b], k, 32 * i + 8 * (e / 4) + 4 * g + e % 4);
-              if (bad_bf16(y)) o[i][e] += pk * __uint_as_float(y << 16);
+              if (bad_bf16(y)) o[i][e] += wk * __uint_as_float(y << 16);
             }
         }
       }
-      __syncthreads();
+      lds_barrier();
       st.clean(sm.v[b]);
-      __syncthreads();
+      lds_barrier();
     }
     if (!busy) continue;
+    const uint16_t *sv = sm.v[0];
+    const int vp0 = vpos[0] + b * kKeys * D, vp1 = vpos[1] + b * kKeys * D;
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       // keys 16 s + {4 g + 0..3, 8 + 4 g + 0..3}: the lane's eight, in order
@@ -942,6 +1059,14 @@ __device__ inline void attend_many(const AttnArgs &a, const Work &t, int h, int 
                                                        0, 0);
       }
     }
+    constexpr int AHEAD = 6;
+    __builtin_amdgcn_sched_group_barrier(0x100, 2 * AHEAD, 0);
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+      if (i + AHEAD < D / 8) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
   }
   if (!live) return;
   l += __shfl_xor(l, 32, 64);
