@@ -113,26 +113,41 @@ struct Layout {
 // ---------------------------------------------------------------------------
 constexpr int kMapThreads = 1024;
 
-// Exclusive scan over the workgroup; returns the total in every thread.
-__device__ inline int block_scan(int v, int *excl, int *lds) {
+// Exclusive scans of N numbers a thread over the workgroup: v becomes the sum
+// before the thread, total the workgroup's.
+template <int N>
+__device__ inline void block_scan(int (&v)[N], int (&total)[N], int (*lds)[kMapThreads / 64]) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  int inc = v;
+  constexpr int W = kMapThreads / 64;
+  int inc[N];
 #pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int u = __shfl_up(inc, o, 64);
-    if (lane >= o) inc += u;
+  for (int i = 0; i < N; ++i) {
+    inc[i] = v[i];
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int u = __shfl_up(inc[i], o, 64);
+      if (lane >= o) inc[i] += u;
+    }
   }
   __syncthreads();
-  if (lane == 63) lds[w] = inc;
-  __syncthreads();
-  int base = 0, tot = 0;
-  for (int i = 0; i < kMapThreads / 64; ++i) {
-    const int x = lds[i];
-    if (i < w) base += x;
-    tot += x;
+  if (lane == 63) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) lds[i][w] = inc[i];
   }
-  *excl = base + inc - v;
-  return tot;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    // the waves' sums, scanned by every wave
+    const int x = lane < W ? lds[i][lane] : 0;
+    int y = x;
+#pragma unroll
+    for (int o = 1; o < W; o <<= 1) {
+      const int u = __shfl_up(y, o, 64);
+      if (lane >= o) y += u;
+    }
+    total[i] = __shfl(y, W - 1, 64);
+    v[i] = inc[i] - v[i] + __shfl(y - x, w, 64);
+  }
 }
 
 __device__ inline int upper(const int32_t *ptr, int n, int x) {
@@ -207,7 +222,7 @@ __device__ inline int tile_hi(const Unit &x, int i) {
 // are read with the header.
 template <bool LDS>
 __global__ __launch_bounds__(kMapThreads) void attn_plan_kernel(PlanArgs a) {
-  __shared__ int lds[kMapThreads / 64];
+  __shared__ int lds[3][kMapThreads / 64];
   __shared__ int s_err, s_chunk[2];
   __shared__ unsigned long long s_work;
   constexpr int NS = LDS ? kMapThreads + 1 : 1;
@@ -230,7 +245,7 @@ __global__ __launch_bounds__(kMapThreads) void attn_plan_kernel(PlanArgs a) {
       const int len = min(max(own ? a.own_len[r] : a.prefix_len[g], 0), ld * page);
       const int n = (len + page - 1) >> a.page_shift;
       const int32_t *p = own ? a.own_pages + int64_t(r) * a.ldo : a.prefix_pages + int64_t(g) * a.ldp;
-      for (int i = lane; i < n; i += 64) bad |= p[i] < 0 || p[i] >= a.n_pages;
+= p[i] < 0 |= p[i] < 0 || p[i] >= a.n_pages;
     }
     if (bad) s_err = 1;
     __syncthreads();
@@ -280,15 +295,14 @@ __global__ __launch_bounds__(kMapThreads) void attn_plan_kernel(PlanArgs a) {
     const int s = s0 + tid;
     const int q = s < a.S ? m.seq_tok[s + 1] - m.seq_tok[s] : 0;
     const bool sh = is_short(a, q);
-    int et, es;
-    const int nt = block_scan(sh ? q : 0, &et, lds);
-    const int ns = block_scan(sh ? 1 : 0, &es, lds);
+    int v[2] = {sh ? q : 0, sh ? 1 : 0}, total[2];
+    block_scan(v, total, lds);
     if (s < a.S) {
-      m.short_tok[s] = tok_base + et;
-      m.short_seq[s] = seq_base + es;
+      m.short_tok[s] = tok_base + v[0];
+      m.short_seq[s] = seq_base + v[1];
     }
-    tok_base += nt;
-    seq_base += ns;
+    tok_base += total[0];
+    seq_base += total[1];
   }
   if (tid == 0) {
     m.short_tok[a.S] = tok_base;
@@ -325,10 +339,9 @@ __global__ __launch_bounds__(kMapThreads) void attn_plan_kernel(PlanArgs a) {
       ni += ns;
       nr += ns * nt * gq;
     }
-    int et, ei, er;
-    const int tt = block_scan(n, &et, lds), ti = block_scan(ni, &ei, lds),
-              tr = block_scan(nr, &er, lds);
-    et += tile_base, ei += item_base, er += row_base;
+    int v[3] = {n, ni, nr}, total[3];
+    block_scan(v, total, lds);
+    int et = tile_base + v[0], ei = item_base + v[1], er = row_base + v[2];
     if (u < U) m.utile[u] = et;
     // (the capacities hold every table of these sizes; a tile beyond them
     // could only come from a table that changed under the launch)
@@ -347,7 +360,7 @@ __global__ __launch_bounds__(kMapThreads) void attn_plan_kernel(PlanArgs a) {
       }
       ++et, ei += ns, er += ns * nt * gq;
     }
-    tile_base += tt, item_base += ti, row_base += tr;
+    tile_base += total[0], item_base += total[1], row_base += total[2];
   }
   __syncthreads();
   // tokens

@@ -222,8 +222,7 @@ struct ProdArgs {
 
 // four neighbouring channels of one token
 template <typename TY>
-__device__ inline void store_y4(const ProdArgs &a, int t, int c, i32x4 s) {
-  const float xs = a.xs[t];
+__device__ inline void store_y4(const ProdArgs &a, int t, int c, i32x4 s, float xs) {
   const nt_f4 w = *reinterpret_cast<const nt_f4 *>(a.ws + c);
   float v[4];
 #pragma unroll
@@ -236,6 +235,10 @@ __device__ inline void store_y4(const ProdArgs &a, int t, int c, i32x4 s) {
         nt_u2{uint32_t(f32_to_bf16(v[0])) | uint32_t(f32_to_bf16(v[1])) << 16,
               uint32_t(f32_to_bf16(v[2])) | uint32_t(f32_to_bf16(v[3])) << 16};
   }
+}
+template <typename TY>
+__device__ inline void store_y4(const ProdArgs &a, int t, int c, i32x4 s) {
+  store_y4<TY>(a, t, c, s, a.xs[t]);
 }
 
 // 16 * MB channels by 16 * NB tokens; wave w of WV takes the pairs of 64-byte
@@ -328,6 +331,81 @@ __global__ __launch_bounds__(64 * WV) void i8_skinny(ProdArgs a) {
         if (c < a.N && t < a.T) store_y4<TY>(a, t, c, acc[m][n]);
       }
   }
+}
+
+// Up to kFewTok tokens in one launch: each workgroup rounds the tokens itself
+// (16 channels, 8 waves; the weight's first operands are on their way
+// meanwhile).  The integers lie in LDS, chunk c of token t at 16 (kFewTok c +
+// t).  (One token, d_in 4096 to 1024 channels: 4.7 us, in two launches 7.4;
+// two tokens 5.8; with four, the repeated rounding made it 9.3.)
+constexpr int kFewTok = 2;
+constexpr int kFewBytes = 32768;  // LDS for the integers
+
+template <typename TX, typename TY>
+__global__ __launch_bounds__(512) void i8_token(ProdArgs a, const void *x, int64_t ldx) {
+  __shared__ i32x4 lq[kFewBytes / 16];
+  __shared__ i32x4 part[4][64];
+  __shared__ uint32_t wmax[kFewTok][8];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  const int c0 = blockIdx.x * 16, r = lane & 15, g = lane >> 4;
+  const int8_t *wp = a.w.p + mat_at(a.w, c0 + r, g);
+  const int sw = mat_step(a.w), kb = (a.K + 63) / 64, nc = a.K / 16;
+  i32x4 wf[4];
+  auto load = [&](int p, int b) {
+    wf[p] = *reinterpret_cast<const i32x4 *>(wp + int64_t(64 * b + 16 * g < a.K ? b : 0) * sw);
+  };
+#pragma unroll
+  for (int p = 0; p < 4; ++p) load(p, w + 8 * p);
+
+  // (a chunk of 16 elements a thread; the second pass finds rows in L2)
+  for (int t = 0; t < a.T; ++t) {
+    const char *row = static_cast<const char *>(x) + t * ldx * int64_t(sizeof(TX));
+    uint32_t v = 0;
+    for (int c = tid; c < nc; c += 512) {
+      Raw16<TX> e;
+      e.load(row, c);
+      v = absmax16(e, v);
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) v = max(v, uint32_t(__shfl_xor(int(v), o, 64)));
+    if (lane == 0) wmax[t][w] = v;
+  }
+  __syncthreads();
+  float mine = 0.f;  // the scale of token r
+  for (int t = 0; t < a.T; ++t) {
+    uint32_t v = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v = max(v, wmax[t][i]);
+    const float s = v >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : __uint_as_float(v) / 127.f;
+    const float inv = 1.f / s;
+    if (t == r) mine = s;
+    const char *row = static_cast<const char *>(x) + t * ldx * int64_t(sizeof(TX));
+    for (int c = tid; c < nc; c += 512) {
+      Raw16<TX> e;
+      e.load(row, c);
+      lq[kFewTok * c + t] = quant16(e, s, inv);
+    }
+  }
+  __syncthreads();
+  i32x4 acc = {0, 0, 0, 0};
+  for (int b = w; b < kb; b += 32) {
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      const int c = 4 * (b + 8 * p) + g;
+      const i32x4 xf = r < a.T && c < nc ? lq[kFewTok * c + r] : i32x4{0, 0, 0, 0};
+      acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[p], xf, acc, 0, 0, 0);
+      load(p, b + 8 * (p + 4));
+    }
+  }
+#pragma unroll
+  for (int s = 4; s > 0; s >>= 1) {
+    if (w >= s && w < 2 * s) part[w - s][lane] = acc;
+    __syncthreads();
+    if (w < s) acc += part[w][lane];
+    if (s > 1) __syncthreads();
+  }
+  const int c = c0 + 4 * g;
+  if (w == 0 && r < a.T && c < a.N) store_y4<TY>(a, r, c, acc, mine);
 }
 
 // BC channels by BT tokens, WC x WT waves, one 64-byte block of d_in a step.
@@ -594,17 +672,37 @@ void product(ProdArgs &a, hipStream_t s) {
   }
 }
 
+Mat8 weight_of(const tcl_i8_weight *w) {
+  const int32_t kb = blocks_of(w->d_in);
+  return w->W_p ? Mat8{static_cast<const int8_t *>(w->W_p), 0, w->d_out, kb, 1}
+                : Mat8{w->W, w->d_in, w->d_out, kb, 0};
+}
+
 int launch_product(const tcl_i8_weight *w, const Mat8 &x, const float *scale, void *y, int64_t ldy,
                    int yd, hipStream_t s) {
   if (x.n == 0 || w->d_out == 0) return TCL_OK;
-  const int32_t kb = blocks_of(w->d_in);
-  const Mat8 wm = w->W_p ? Mat8{static_cast<const int8_t *>(w->W_p), 0, w->d_out, kb, 1}
-                         : Mat8{w->W, w->d_in, w->d_out, kb, 0};
-  ProdArgs a{wm, x, w->scale, scale, y, ldy, x.n, w->d_in, w->d_out, 0, 0, 0};
+  ProdArgs a{weight_of(w), x, w->scale, scale, y, ldy, x.n, w->d_in, w->d_out, 0, 0, 0};
   if (yd == TCL_BF16)
     product<uint16_t>(a, s);
   else
     product<float>(a, s);
+  TCL_HIP(hipGetLastError());
+  return TCL_OK;
+}
+
+int launch_token(const tcl_i8_weight *w, const void *x, int64_t ldx, int xd, int32_t n, void *y,
+                 int64_t ldy, int yd, hipStream_t s) {
+  ProdArgs a{weight_of(w), {}, w->scale, nullptr, y, ldy, n, w->d_in, w->d_out, 0, 0, 0};
+  const dim3 grid((w->d_out + 15) / 16), block(512);
+#define TOKEN(TX, TY) hipLaunchKernelGGL((i8_token<TX, TY>), grid, block, 0, s, a, x, ldx)
+  if (xd == TCL_BF16) {
+    if (yd == TCL_BF16) TOKEN(bf16_t, uint16_t);
+    else TOKEN(bf16_t, float);
+  } else {
+    if (yd == TCL_BF16) TOKEN(float, uint16_t);
+    else TOKEN(float, float);
+  }
+#undef TOKEN
   TCL_HIP(hipGetLastError());
   return TCL_OK;
 }
@@ -697,6 +795,8 @@ extern "C" int tcl_i8_linear(const tcl_i8_weight *w, const void *x, int64_t ldx,
   const size_t need = ws_bytes_of(w, n_tokens);
   if (ws_bytes < need)
     return fail(TCL_ENOSPC, "i8: workspace holds %zu bytes, needs %zu", ws_bytes, need);
+  if (n_tokens <= kFewTok && w->d_in <= kFewBytes / kFewTok && w->d_out > 0)
+    return launch_token(w, x, ldx, xd, n_tokens, y, ldy, yd, static_cast<hipStream_t>(stream));
   int8_t *q = static_cast<int8_t *>(ws);
   float *scale = reinterpret_cast<float *>(q + ws_q_bytes(w, n_tokens));
   hipStream_t s = static_cast<hipStream_t>(stream);

@@ -776,31 +776,30 @@ def _vector(what: str, t: torch.Tensor, n: int, dtype: torch.dtype) -> None:
         raise ValueError(f"{what} must be a contiguous {dtype} tensor of {n} entries")
 
 
-class _Here:
-    """The context of a call whose device is the current one."""
-
-    def __enter__(self):
-        return None
-
-    def __exit__(self, *exc):
-        return False
-
-
-_HERE = _Here()
-
-
-def _on(dev: torch.device, stream, *tensors):
-    """Context and stream handle of a call on ``dev``: the device is made the
-    current one, and tensors the call allocated itself are kept for a stream
-    other than the one they were allocated on."""
+def _call(dev: torch.device, fn, args, stream, *own) -> None:
+    """fn(*args, stream) with ``dev`` the current device; tensors the call
+    allocated itself are kept for a stream other than the one they were
+    allocated on."""
     i = dev.index
-    ctx = _HERE if torch.cuda.current_device() == i else torch.cuda.device(i)
     if stream is None:
-        return ctx, torch._C._cuda_getCurrentRawStream(i)
-    if isinstance(stream, torch.cuda.Stream):
-        for t in tensors:
-            t.record_stream(stream)
-    return ctx, _stream(dev, stream)
+        st = torch._C._cuda_getCurrentRawStream(i)
+    else:
+        st = _stream(dev, stream)
+        if isinstance(stream, torch.cuda.Stream):
+            for t in own:
+                t.record_stream(stream)
+    if torch._C._cuda_getDevice() == i:
+        rc = fn(*args, st)
+    else:
+        with torch.cuda.device(i):
+            rc = fn(*args, st)
+    if rc:
+        check(rc)
+
+
+def _packed(fn, args):
+    """The arguments of a call that is made often, converted once."""
+    return tuple(t(v) if isinstance(v, (int, float)) else v for v, t in zip(args, fn.argtypes))
 
 
 class I8Weight:
@@ -823,11 +822,8 @@ class I8Weight:
             n = ctypes.c_size_t(0)
             check(lib().tcl_i8_pack_bytes(ctypes.byref(self.desc), ctypes.byref(n)))
             self.W_p = torch.empty(n.value, dtype=torch.uint8, device=W.device)
-            ctx, st = _on(W.device, stream, self.W_p)
-            if isinstance(stream, torch.cuda.Stream):
-                W.record_stream(stream)
-            with ctx:
-                check(lib().tcl_i8_pack(ctypes.byref(self.desc), self.W_p.data_ptr(), n.value, st))
+            _call(W.device, lib().tcl_i8_pack,
+                  (ctypes.byref(self.desc), self.W_p.data_ptr(), n.value), stream, self.W_p, W)
             self.W, self.desc.W = None, None
 
 
@@ -848,10 +844,9 @@ def i8_quant(x: torch.Tensor, q: Optional[torch.Tensor] = None,
     ldq = _rows("i8_quant: q", q, T, d)
     _vector("i8_quant: scale", scale, T, torch.float32)
     _same_device("i8_quant", x.device, q, scale)
-    ctx, st = _on(x.device, stream, *own)
-    with ctx:
-        check(lib().tcl_i8_quant(x.data_ptr(), ldx, _dtype_code(x.dtype), T, d, q.data_ptr(), ldq,
-                                 scale.data_ptr(), st))
+    _call(x.device, lib().tcl_i8_quant,
+          (x.data_ptr(), ldx, _dtype_code(x.dtype), T, d, q.data_ptr(), ldq, scale.data_ptr()),
+          stream, *own)
     return q, scale
 
 
@@ -870,10 +865,9 @@ def i8_product(w: I8Weight, q: torch.Tensor, scale: torch.Tensor,
         own.append(y)
     ldy = _rows("i8_product: y", y, T, w.d_out)
     _same_device("i8_product", q.device, scale, y, w.scale)
-    ctx, st = _on(q.device, stream, *own)
-    with ctx:
-        check(lib().tcl_i8_product(ctypes.byref(w.desc), q.data_ptr(), ldq, scale.data_ptr(), T,
-                                   y.data_ptr(), ldy, _dtype_code(y.dtype), st))
+    _call(q.device, lib().tcl_i8_product,
+          (ctypes.byref(w.desc), q.data_ptr(), ldq, scale.data_ptr(), T, y.data_ptr(), ldy,
+           _dtype_code(y.dtype)), stream, *own)
     return y
 
 
@@ -896,13 +890,12 @@ class I8Call:
             ws = torch.empty(max(need.value, 256), dtype=torch.uint8, device=x.device)
         self.ws, self.device = ws, x.device
         self._fn = lib().tcl_i8_linear
-        self._args = (ctypes.byref(w.desc), x.data_ptr(), self.ldx, self.xd, T, y.data_ptr(),
-                      self.ldy, self.yd, ws.data_ptr(), ws.numel() * ws.element_size())
+        self._args = _packed(self._fn, (
+            ctypes.byref(w.desc), x.data_ptr(), self.ldx, self.xd, T, y.data_ptr(), self.ldy,
+            self.yd, ws.data_ptr(), ws.numel() * ws.element_size()))
 
     def __call__(self, stream=None) -> torch.Tensor:
-        ctx, st = _on(self.device, stream, self.ws)
-        with ctx:
-            check(self._fn(*self._args, st))
+        _call(self.device, self._fn, self._args, stream, self.ws)
         return self.y
 
 
@@ -911,7 +904,8 @@ def i8_linear(w: I8Weight, x: torch.Tensor, y: Optional[torch.Tensor] = None,
     """tcl_i8_linear: the base projection of x [T, d_in]."""
     if y is None:
         y = torch.empty(x.shape[0], w.d_out, dtype=y_dtype, device=x.device)
-        _on(x.device, stream, y)
+        if isinstance(stream, torch.cuda.Stream):
+            y.record_stream(stream)
     return I8Call(w, x, y)(stream)
 
 
@@ -984,14 +978,14 @@ class AppendCall:
         self.pos, self.slot, self.q_out, self.T = pos, slot, q_out, T
         self.xd, self.device = _dtype_code(k.dtype), cache.device
         self._fn = lib().tcl_kv_append
-        self._args = (ctypes.byref(cache.desc), ctypes.byref(rope.desc), k.data_ptr(), self.ldk,
-                      v.data_ptr(), self.ldv, _ptr(q), self.ldq, self.Hq, self.xd, _ptr(q_out),
-                      self.ldqo, T, pos.data_ptr(), slot.data_ptr())
+        self._args = _packed(self._fn, (
+            ctypes.byref(cache.desc), ctypes.byref(rope.desc), k.data_ptr(), self.ldk,
+            v.data_ptr(), self.ldv, _ptr(q), self.ldq, self.Hq, self.xd, _ptr(q_out), self.ldqo, T,
+            pos.data_ptr(), slot.data_ptr()))
 
     def __call__(self, stream=None) -> Optional[torch.Tensor]:
-        ctx, st = _on(self.device, stream, *([] if self.q_out is None else [self.q_out]))
-        with ctx:
-            check(self._fn(*self._args, st))
+        _call(self.device, self._fn, self._args, stream,
+              *(() if self.q_out is None else (self.q_out,)))
         return self.q_out
 
 
@@ -1042,21 +1036,21 @@ class AttnPlan:
         _same_device("AttnPlan", self.device, *table)
         self.table = table
         self.batch = AttnBatch(S, G, self.n_tokens, ldp, ldo, *[t.data_ptr() for t in table])
+        self.batch_ref = ctypes.byref(self.batch)
 
     def _map(self, stream):
-        ctx, st = _on(self.device, stream, self.buf)
-        with ctx:
-            check(lib().tcl_attn_plan(ctypes.byref(self.batch), ctypes.byref(self.cache.desc),
-                                      self.n_q_heads, self.buf.data_ptr(), self.buf.numel(), st))
+        _call(self.device, lib().tcl_attn_plan,
+              (ctypes.byref(self.batch), ctypes.byref(self.cache.desc), self.n_q_heads,
+               self.buf.data_ptr(), self.buf.numel()), stream, self.buf)
 
     def remap(self, seq_tok_ptr, group_seq_ptr, prefix_len, prefix_pages, own_len, own_pages,
               stream=None) -> None:
         """Maps a batch of the same sizes into this plan (no allocation; in a
         graph it follows what the tensors hold at each replay)."""
-        old = self.table, self.batch
+        old = self.table, self.batch, self.batch_ref
         self._set(seq_tok_ptr, group_seq_ptr, prefix_len, prefix_pages, own_len, own_pages)
         if [getattr(self.batch, f) for f, _ in AttnBatch._fields_[:5]] != self._sizes:
-            self.table, self.batch = old
+            self.table, self.batch, self.batch_ref = old
             raise ValueError("AttnPlan.remap: a batch of other sizes needs a plan of its own")
         self._map(stream)
 
@@ -1068,9 +1062,8 @@ class AttnPlan:
             out = torch.empty(4, dtype=torch.int32, device=self.device)
         _vector("AttnPlan: status", out, 4, torch.int32)
         _same_device("AttnPlan", self.device, out)
-        ctx, st = _on(self.device, stream, *([out] if own else []))
-        with ctx:
-            check(lib().tcl_attn_status_async(self.buf.data_ptr(), out.data_ptr(), st))
+        _call(self.device, lib().tcl_attn_status_async, (self.buf.data_ptr(), out.data_ptr()),
+              stream, *([out] if own else []))
         return out
 
     def status(self, stream=None) -> int:
@@ -1110,15 +1103,14 @@ class AttnCall:
             ws = torch.empty(max(plan.workspace_bytes, 256), dtype=torch.uint8, device=plan.device)
         self.ws = ws
         self._fn = lib().tcl_attn_apply
-        self._args = (ctypes.byref(cache.desc), plan.n_q_heads, plan.buf.data_ptr(),
-                      plan.buf.numel(), q.data_ptr(), self.ldq, o.data_ptr(), self.ldo, _ptr(lse),
-                      self.scale, ws.data_ptr(), ws.numel() * ws.element_size())
+        self._args = _packed(self._fn, (
+            None, ctypes.byref(cache.desc), plan.n_q_heads, plan.buf.data_ptr(), plan.buf.numel(),
+            q.data_ptr(), self.ldq, o.data_ptr(), self.ldo, _ptr(lse), self.scale, ws.data_ptr(),
+            ws.numel() * ws.element_size()))[1:]
 
     def __call__(self, stream=None) -> torch.Tensor:
-        p = self.plan
-        ctx, st = _on(p.device, stream, self.ws, self.o)
-        with ctx:  # (the batch's tables are the plan's last ones)
-            check(self._fn(ctypes.byref(p.batch), *self._args, st))
+        p = self.plan  # (the batch's tables are the plan's last ones)
+        _call(p.device, self._fn, (p.batch_ref, *self._args), stream, self.ws, self.o)
         return self.o
 
 

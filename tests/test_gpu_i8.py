@@ -118,6 +118,21 @@ def test_quant_special_rows():
     close(y[4:], product64(W, ws, n[4:], want[4:]), torch.float32)
 
 
+@pytest.mark.parametrize("T", [1, 3, 4, 5])
+def test_linear_special_rows(T):
+    """Zero rows, infinities and NaNs through the one-launch form and the two
+    launches: each row on its own."""
+    x = acts(4, T, 96, torch.float32)
+    x[0] = 0
+    if T > 1:
+        x[1, 3], x[T - 1, 95] = float("nan"), -float("inf")
+    W, ws = weight(4, 40, 96)
+    y = tclora.i8_linear(tclora.I8Weight(W, ws), x, y_dtype=torch.float32)
+    n, s = quant64(x)
+    assert not y[0].any()
+    close(y, product64(W, ws, n, s), torch.float32)
+
+
 def test_quant_leaves_columns_behind_d():
     x = acts(1, 4, 48, torch.bfloat16)
     buf = torch.full((4, 80), 7, dtype=torch.int8, device=DEV)
@@ -172,7 +187,9 @@ def test_product_longest_rows_do_not_overflow(T):
 
 
 @pytest.mark.parametrize("x,y", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "bf16"), ("f32", "f32")])
-@pytest.mark.parametrize("T,d_in,d_out", [(1, 4096, 1024), (5, 272, 136), (64, 1024, 4096),
+@pytest.mark.parametrize("T,d_in,d_out", [(1, 4096, 1024), (1, 16, 8), (2, 80, 24), (3, 14336, 264),
+                                          (2, 16384, 40), (2, 16400, 40), (4, 16384, 40), (4, 8208, 1032),
+                                          (5, 272, 136), (64, 1024, 4096),
                                           (300, 1040, 520), (4097, 400, 4104),
                                           (2100, 48, 8200)])
 def test_linear(T, d_in, d_out, x, y):
@@ -238,3 +255,4 @@ def test_results_repeat_bit_for_bit():
         # a token's row does not depend on its batch
         b = tclora.i8_linear(w, x[3:9])
         assert torch.equal(tclora.i8_linear(w, x), a) and torch.equal(a[3:9], b)
+        assert torch.equal(tclora.i8_linear(w, x[3:6]), a[3:6])
