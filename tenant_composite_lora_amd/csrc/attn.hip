@@ -245,7 +245,8 @@ __global__ __launch_bounds__(kMapThreads) void attn_plan_kernel(PlanArgs a) {
       const int len = min(max(own ? a.own_len[r] : a.prefix_len[g], 0), ld * page);
       const int n = (len + page - 1) >> a.page_shift;
       const int32_t *p = own ? a.own_pages + int64_t(r) * a.ldo : a.prefix_pages + int64_t(g) * a.ldp;
-= p[i] < 0 |= p[i] < 0 || p[i] >= a.n_pages;
+#pragma unroll 4
+      for (int i = lane; i < n; i += 64) bad |= p[i] < 0 || p[i] >= a.n_pages;
     }
     if (bad) s_err = 1;
     __syncthreads();
