@@ -756,13 +756,14 @@ int tcl_attn_workspace_bytes(const tcl_attn_batch *b, const tcl_kv_cache *c, int
  * `plan` (device, 256-byte aligned, tcl_attn_plan_bytes bytes).  One mapping
  * serves every layer whose cache has the same pages, heads and head_dim; a
  * batch of other lengths or tables needs a new one (into the same plan, with
- * the same sizes, if wanted).  A bad table (pointers that decrease or do not
+ * the same sizes, if wanted, once the work that uses it has run).  A bad table (pointers that decrease or do not
  * run as above, a negative length or one beyond its page list, a page id in
  * use outside the cache) leaves TCL_EINVAL in the plan, and tcl_attn_apply
  * then changes nothing.  Graph-capturable.
  * Errors: TCL_EINVAL, TCL_EALIGN, TCL_ENOSPC, TCL_EUNSUPPORTED (head_dim
  * other than 64, 128 and 256, more than 128 query heads a key head, page
- * lists of 2^30 keys, n_tokens * n_q_heads of 2^29), TCL_EHIP.
+ * lists of 2^29 keys, n_tokens * n_q_heads of 2^29, requests and groups times
+ * key heads of 2^30), TCL_EHIP.
  */
 int tcl_attn_plan(const tcl_attn_batch *b, const tcl_kv_cache *c, int32_t n_q_heads, void *plan,
                   size_t plan_bytes, void *stream);

@@ -8,6 +8,9 @@
 // lane.  The angles of a token are computed once a workgroup, in 64 bits
 // (positions reach far beyond what an fp32 product resolves), reduced to one
 // turn there and handed to the fp32 sine and cosine.
+// Bound by memory for many tokens (4224 tokens, 32 + 8 + 8 heads of 128, fp32
+// in: 156 MB in 24.6 us, 6.3 TB/s, part of it from the last-level cache); 64
+// tokens take 3.0 us, a launch and two round trips to memory.
 #include "kern_common.hpp"
 #include "kv.hpp"
 

@@ -490,7 +490,7 @@ def test_attn_host_errors(L):
                 f(prefix_len=None), f(prefix_pages=None), f(K=None)] == [E] * 13
         assert [f(seq_tok_ptr=P + 2), f(own_pages=P + 1), f(stride_head=4)] == [A] * 3
         assert [f(head_dim=96), f(page_size=3), f(Hq=2 * 129), f(ld_own=1 << 26),
-                f(n_tokens=1 << 28)] == [U] * 5
+                f(n_tokens=1 << 28), f(n_kv_heads=128, Hq=128, n_seqs=1 << 23)] == [U] * 6
     assert nbytes(res=None) == E and nbytes(L.tcl_attn_workspace_bytes, res=None) == E
     for f in (plan, apply):
         assert [f(p=None), f(p=0x10010), f(n=need - 1)] == [E, A, tclora.ENOSPC]
