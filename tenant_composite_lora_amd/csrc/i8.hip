@@ -433,7 +433,12 @@ __global__ __launch_bounds__(64 * WC * WT, 2) void i8_tile(ProdArgs a) {
   constexpr int TH = 64 * WC * WT;
   constexpr int NW = BC * 4 / TH, NX = BT * 4 / TH;      // chunks a thread moves a step
   constexpr int FC = BC / WC / 32, FT = BT / WT / 32;    // 32-row operands of a wave
-  __shared__ i32x4 lw[3][BC * 4], lx[3][BT * 4];
+  __shared__ struct {
+    i32x4 w[3][BC * 4], x[3][BT * 4];
+  } l;
+  auto &lw = l.w;
+  auto &lx = l.x;
+  float *lo = reinterpret_cast<float *>(&l);
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   // workgroups go to the eight XCDs in turn: each gets a run of tiles, token
   // tiles next to each other, so that its L2 holds their weight rows
@@ -535,20 +540,55 @@ __global__ __launch_bounds__(64 * WC * WT, 2) void i8_tile(ProdArgs a) {
     const int t = b0;
     b0 = b1, b1 = b2, b2 = t;
   }
-  const int wc = c0 + (w % WC) * (BC / WC), wt = t0 + (w / WC) * (BT / WT);
+  // The results go through LDS, a wave's 32 tokens at a time, so that a store
+  // covers whole lines of y: straight from the registers (16 bytes a token
+  // and lane half) fp32 rows were written to memory twice over, 133 MB for 67.
+  constexpr int CW = BC / WC, LD = CW + 4;  // channels of a wave; row of LDS, floats
+  static_assert(WC * WT * 32 * LD * 4 <= int(sizeof(l)), "LDS of the results");
+  const int wc = c0 + (w % WC) * CW, wt = t0 + (w / WC) * (BT / WT);
+  float *out = lo + w * 32 * LD;
+  nt_f4 ws[FC][4];
+#pragma unroll
+  for (int i = 0; i < FC; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      ws[i][e] = *reinterpret_cast<const nt_f4 *>(a.ws + min(wc + 32 * i + 8 * e + 4 * h, a.N - 4));
 #pragma unroll
   for (int j = 0; j < FT; ++j) {
-    const int t = wt + 32 * j + r;
-    if (t >= a.T) continue;
+    const float xs = a.xs[min(wt + 32 * j + r, a.T - 1)];
 #pragma unroll
     for (int i = 0; i < FC; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int c = wc + 32 * i + 8 * e + 4 * h;
-        if (c < a.N)
-          store_y4<TY>(a, t, c, i32x4{acc[i][j][4 * e], acc[i][j][4 * e + 1],
-                                      acc[i][j][4 * e + 2], acc[i][j][4 * e + 3]});
+        nt_f4 v;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) v[x] = float(acc[i][j][4 * e + x]) * xs * ws[i][e][x];
+        *reinterpret_cast<nt_f4 *>(out + r * LD + 32 * i + 8 * e + 4 * h) = v;
       }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+    constexpr int PER = sizeof(TY) == 4 ? 4 : 8;          // channels a lane stores: 16 bytes
+    constexpr int LPT = CW / PER;                          // lanes a token
+#pragma unroll
+    for (int k = 0; k < LPT / 2; ++k) {
+      const int x = k * (64 / LPT) + lane / LPT, t = wt + 32 * j + x, c = wc + lane % LPT * PER;
+      const float *in = out + x * LD + lane % LPT * PER;
+      if (t >= a.T || c >= a.N) continue;
+      TY *p = static_cast<TY *>(a.y) + int64_t(t) * a.ldy + c;
+      const nt_f4 u = *reinterpret_cast<const nt_f4 *>(in);
+      if constexpr (sizeof(TY) == 4) {
+        *reinterpret_cast<nt_f4 *>(p) = u;
+      } else {
+        const nt_f4 v = *reinterpret_cast<const nt_f4 *>(in + 4);
+        auto two = [](float x0, float x1) {
+          return uint32_t(f32_to_bf16(x0)) | uint32_t(f32_to_bf16(x1)) << 16;
+        };
+        *reinterpret_cast<nt_u4 *>(p) =
+            nt_u4{two(u[0], u[1]), two(u[2], u[3]), two(v[0], v[1]), two(v[2], v[3])};
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
   }
 }
 
