@@ -145,7 +145,8 @@ __device__ inline i32x4 quant16(const R &x, float s, float inv) {
 // workgroup, which writes whole 64-byte sectors of the blocks.  Few: one, so
 // that there are more workgroups.  4224 x 4096 bf16: 17 us (52 MB, 3.1 TB/s);
 // every wave is resident at once, so that all load, round and store in turn
-// and the three do not overlap.  64 x 4096: 4 us, 177 x 14336 fp32: 8 us.
+// (half the waves with two rows each, the second's loads ahead of the first's
+// rounding, took 21).  64 x 4096: 4 us, 177 x 14336 fp32: 8 us.
 template <typename T, int WPR, int ROWS>
 __global__ __launch_bounds__(64 * WPR * ROWS) void i8_quant_kernel(QuantArgs a) {
   __shared__ uint32_t wmax[ROWS][WPR];
@@ -424,7 +425,7 @@ __global__ __launch_bounds__(512) void i8_token(ProdArgs a, const void *x, int64
 // instructions (sched_group_barrier): issued in one go they held the first
 // one back by some hundred cycles a step (256 x 256 tiles of 4096 tokens x
 // 4096 channels, one a CU: 115 us, dealt out 97).
-// 4224 x 14336 of d_in 4096: 277 us, 1.8 P operations a second.  Operand reads
+// 4224 x 14336 of d_in 4096: 264 us, 1.9 P operations a second.  Operand reads
 // and matrix instructions alone take 250 us at that size on random bytes, with
 // 64 workgroups instead of 952 they run at twice that rate: the clock bounds
 // it.

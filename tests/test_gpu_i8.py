@@ -65,7 +65,8 @@ def acts(seed, T, d, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("T,d", [(1, 16), (3, 48), (5, 4096), (2, 16384), (2, 16400), (1, 40000)])
+@pytest.mark.parametrize("T,d", [(1, 16), (3, 48), (5, 4096), (2, 16384), (2, 16400), (1, 40000),
+                                 (1025, 16), (1031, 4112), (2051, 112), (4100, 80)])
 def test_quant_is_the_definition(T, d, dtype):
     x = acts(T * 7 + d, T, d, DT[dtype])
     q, s = tclora.i8_quant(x)
