@@ -113,22 +113,32 @@ struct Layout {
 // ---------------------------------------------------------------------------
 constexpr int kMapThreads = 1024;
 
+// Inclusive scan over a wave by lane moves: 1, 2, 4 and 8 lanes inside each
+// row of 16, then the last lane of rows 0 and 2 into the row behind, then the
+// last lane of row 1 into rows 2 and 3.  ROWS false: inside rows only.
+template <bool ROWS>
+__device__ inline int lane_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+  if constexpr (ROWS) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);
+  }
+  return v;
+}
+
 // Exclusive scans of N numbers a thread over the workgroup: v becomes the sum
 // before the thread, total the workgroup's.
 template <int N>
 __device__ inline void block_scan(int (&v)[N], int (&total)[N], int (*lds)[kMapThreads / 64]) {
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   constexpr int W = kMapThreads / 64;
+  static_assert(W == 16, "the waves' sums fill a row of lanes");
   int inc[N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    inc[i] = v[i];
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int u = __shfl_up(inc[i], o, 64);
-      if (lane >= o) inc[i] += u;
-    }
-  }
+  for (int i = 0; i < N; ++i) inc[i] = lane_scan<true>(v[i]);
   __syncthreads();
   if (lane == 63) {
 #pragma unroll
@@ -138,15 +148,9 @@ __device__ inline void block_scan(int (&v)[N], int (&total)[N], int (*lds)[kMapT
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     // the waves' sums, scanned by every wave
-    const int x = lane < W ? lds[i][lane] : 0;
-    int y = x;
-#pragma unroll
-    for (int o = 1; o < W; o <<= 1) {
-      const int u = __shfl_up(y, o, 64);
-      if (lane >= o) y += u;
-    }
-    total[i] = __shfl(y, W - 1, 64);
-    v[i] = inc[i] - v[i] + __shfl(y - x, w, 64);
+    const int x = lds[i][lane & (W - 1)], y = lane_scan<false>(x);
+    total[i] = __builtin_amdgcn_readlane(y, W - 1);
+    v[i] = inc[i] - v[i] + __builtin_amdgcn_readlane(y - x, w);
   }
 }
 
@@ -217,8 +221,8 @@ __device__ inline int tile_hi(const Unit &x, int i) {
   return max(x.lo, key_end(x.prefix, max(0, x.hi - x.n_q + last + 1)));
 }
 
-// (64 requests: 13 us, of which the longest unit's items, written one after
-// another, are 4; 3 requests: 9.)
+// 64 requests 10.4 us, 8 prompts of 512 tokens 11.2, 3 requests 7.8: a launch
+// and the round trips of some fifteen phases.
 // Workgroups 1 .. kCheckers look page ids over, a row of a page table a wave,
 // and leave a flag each; workgroup 0 does the rest.  One launch: the flags
 // are read with the header.
@@ -230,6 +234,7 @@ __global__ __launch_bounds__(kMapThreads) void attn_plan_kernel(PlanArgs a) {
   constexpr int NS = LDS ? kMapThreads + 1 : 1;
   __shared__ int32_t l_seq_tok[NS], l_group_seq[NS], l_prefix_len[NS], l_own_len[NS],
       l_short_tok[NS], l_short_seq[NS], l_utile[2 * NS];
+  __shared__ int32_t l_unit[kMapThreads], l_place[kMapThreads], l_item[kMapThreads], l_row[kMapThreads];
   const int tid = threadIdx.x, gq = a.Hq / a.Hkv;
   const int page = 1 << a.page_shift;
   if (tid == 0) {
@@ -328,44 +333,66 @@ __global__ __launch_bounds__(kMapThreads) void attn_plan_kernel(PlanArgs a) {
     s_chunk[tid] = r < kMinChunk ? kMinChunk : (r > 0x40000000ull ? 0x40000000 : int(r));
   }
   __syncthreads();
-  // tiles and items, in unit order
-  int tile_base = 0, item_base = 0, row_base = 0;
+  // the units' first tiles
+  int n_tiles = 0;
   for (int u0 = 0; u0 < U; u0 += kMapThreads) {
     const int u = u0 + tid;
-    Unit x{};
-    if (u < U) x = unit_of(a, m, u);
-    const int n = unit_tiles(x), chunk = s_chunk[x.rows > kFew];
-    int ni = 0, nr = 0;
-    for (int i = 0; i < n; ++i) {
-      const int len = tile_hi(x, i) - x.lo, ns = max(1, (len + chunk - 1) / chunk);
-      const int nt = min(x.n_tok, (i + 1) * x.tpt) - i * x.tpt;
-      ni += ns;
-      nr += ns * nt * gq;
-    }
-    int v[3] = {n, ni, nr}, total[3];
+    int v[1] = {u < U ? unit_tiles(unit_of(a, m, u)) : 0}, total[1];
     block_scan(v, total, lds);
-    int et = tile_base + v[0], ei = item_base + v[1], er = row_base + v[2];
-    if (u < U) m.utile[u] = et;
-    // (the capacities hold every table of these sizes; a tile beyond them
-    // could only come from a table that changed under the launch)
-    for (int i = 0; i < n; ++i) {
-      const int hi = tile_hi(x, i), len = hi - x.lo, ns = max(1, (len + chunk - 1) / chunk);
-      const int nt = min(x.n_tok, (i + 1) * x.tpt) - i * x.tpt;
-      // even lengths, whole steps
-      const int per = max(kKeys, ((len + ns - 1) / ns + kKeys - 1) / kKeys * kKeys);
-      if (et >= a.cap_tiles || ei + ns > a.cap_items || er + ns * nt * gq > a.cap_rows) break;
-      const bool direct = ns == 1 && !x.list && x.lo == 0;
-      a.tiles[et] = Tile{nt, ns, direct ? -1 : er, 0};
-      for (int k = 0; k < ns; ++k) {
-        const int lo = min(hi, x.lo + k * per);
-        a.items[ei + k] = Work{x.tok0 + i * x.tpt, x.list, nt, x.seq, x.group, x.prefix, lo,
-                               min(hi, lo + per), direct ? -1 : er + k * nt * gq, {}};
-      }
-      ++et, ei += ns, er += ns * nt * gq;
-    }
-    tile_base += total[0], item_base += total[1], row_base += total[2];
+    if (u < U) m.utile[u] = n_tiles + v[0];
+    n_tiles += total[0];
   }
   __syncthreads();
+  // tiles, a thread each, then their items, a thread each
+  // (the capacities hold every table of these sizes; what lies beyond them
+  // could only come from a table that changed under the launch)
+  n_tiles = min(n_tiles, a.cap_tiles);
+  int item_base = 0, row_base = 0;
+  struct Cut {
+    Unit x;
+    int i, hi, nt, ns, per;
+  };
+  auto cut = [&](int u, int i) {
+    Cut c{unit_of(a, m, u), i, 0, 0, 0, 0};
+    c.hi = tile_hi(c.x, i);
+    const int len = c.hi - c.x.lo, chunk = s_chunk[c.x.rows > kFew];
+    c.nt = min(c.x.n_tok, (i + 1) * c.x.tpt) - i * c.x.tpt;
+    c.ns = max(1, (len + chunk - 1) / chunk);
+    // even lengths, whole steps
+    c.per = max(kKeys, ((len + c.ns - 1) / c.ns + kKeys - 1) / kKeys * kKeys);
+    return c;
+  };
+  auto direct = [](const Cut &c) { return c.ns == 1 && !c.x.list && c.x.lo == 0; };
+  for (int t0 = 0; t0 < n_tiles; t0 += kMapThreads) {
+    const int t = t0 + tid, here = min(kMapThreads, n_tiles - t0);
+    int v[2] = {0, 0}, total[2];
+    Cut c{};
+    if (tid < here) {
+      const int u = upper(m.utile, U, t);
+      c = cut(u, t - m.utile[u]);
+      v[0] = c.ns;
+      v[1] = c.ns * c.nt * gq;
+      l_unit[tid] = u;
+      l_place[tid] = c.i;
+    }
+    block_scan(v, total, lds);
+    if (tid < here) {
+      l_item[tid] = v[0];
+      l_row[tid] = row_base + v[1];
+      a.tiles[t] = Tile{c.nt, c.ns, direct(c) ? -1 : row_base + v[1], 0};
+    }
+    __syncthreads();
+    for (int k = tid; k < total[0]; k += kMapThreads) {
+      const int j = upper(l_item, here, k), n = k - l_item[j];
+      c = cut(l_unit[j], l_place[j]);
+      const int lo = min(c.hi, c.x.lo + n * c.per), row = l_row[j] + n * c.nt * gq;
+      if (item_base + k >= a.cap_items || row + c.nt * gq > a.cap_rows) continue;
+      a.items[item_base + k] = Work{c.x.tok0 + c.i * c.x.tpt, c.x.list, c.nt, c.x.seq, c.x.group,
+                                    c.x.prefix, lo, min(c.hi, lo + c.per), direct(c) ? -1 : row, {}};
+    }
+    item_base += total[0], row_base += total[1];
+    __syncthreads();
+  }
   // tokens
   for (int t = tid; t < a.T; t += kMapThreads) {
     TokRec r{-1, 0, 0, 0, 0, 0, 0, 0};
@@ -393,7 +420,7 @@ __global__ __launch_bounds__(kMapThreads) void attn_plan_kernel(PlanArgs a) {
   }
   if (tid == 0) {
     a.hdr[H_ITEMS] = min(item_base, a.cap_items);
-    a.hdr[H_TILES] = min(tile_base, a.cap_tiles);
+    a.hdr[H_TILES] = n_tiles;
     a.hdr[H_SHARED] = tok_base;
   }
 }

@@ -178,6 +178,38 @@ def test_heads_of_a_key_head(gq):
     run(Batch(gq, [(90, [(1, 30), (1, 40), (4, 50)])], 2 * gq, 2, 64, 16))
 
 
+def test_more_requests_and_groups_than_threads():
+    """Mappings beyond one pass of the workgroup, and beyond its LDS tables."""
+    r = np.random.default_rng(3)
+    seqs = lambda n, q=1: [(q, q + int(x)) for x in r.integers(0, 8, n)]  # noqa: E731
+    run(Batch(31, [(int(p), seqs(30)) for p in r.integers(0, 40, 50)], 4, 2, 64, 16))
+    run(Batch(32, [(int(p), seqs(int(n))) for p, n in zip(r.integers(0, 9, 1100),
+                                                           r.integers(0, 3, 1100))], 2, 1, 64, 8))
+    # two tiles a request: more tiles than threads
+    run(Batch(33, [(20, seqs(560, 3))], 64, 1, 64, 16))
+
+
+def test_offsets_beyond_32_bits():
+    """Pages at the end of a cache of more than 2^31 elements and 2^32 bytes:
+    the same rows as from a cache that holds nothing else."""
+    b = Batch(34, [(300, [(1, 90), (1, 70), (40, 100)])], 4, 2, 64, 32)
+    want = tclora.attention(b.plan(), b.qd)
+    b.check(want)
+    pages, elems = b.cache.n_pages, 32 * 2 * 64
+    big = (1 << 31) // elems + pages + 1
+    K = torch.zeros(big, 2, 32, 64, dtype=torch.bfloat16, device=DEV)
+    V = torch.zeros_like(K)
+    K[big - pages:] = b.cache.K.transpose(1, 2)
+    V[big - pages:] = b.cache.V.transpose(1, 2)
+    cache = tclora.KVCache(K.transpose(1, 2), V.transpose(1, 2))
+    t = b.table()
+    for i in (3, 5):
+        t[i] = torch.where(t[i] >= 0, t[i] + (big - pages), t[i])
+    plan = tclora.AttnPlan(cache, 4, *t, n_tokens=b.T)
+    assert plan.status() == tclora.OK
+    assert torch.equal(tclora.attention(plan, b.qd), want)
+
+
 def test_rows_behind_the_last_request_stay():
     run(Batch(5, [(100, [(1, 4), (1, 9), (70, 80)])], 8, 2, 64, 16, pad_tokens=9))
     run(Batch(5, [(0, [(0, 4)])], 8, 2, 64, 16, pad_tokens=3))
