@@ -617,7 +617,7 @@ int tcl_i8_pack(tcl_i8_weight *w, void *W_p, size_t bytes, void *stream);
  * device [n_tokens].  d is a multiple of 16.  Columns of q at or beyond d are
  * left as they were.  n_tokens == 0 is a no-op.
  * Errors: TCL_EINVAL (NULL, n_tokens < 0, d < 16, ldx or ldq < d), TCL_EALIGN,
- * TCL_EUNSUPPORTED (xd), TCL_EHIP.
+ * TCL_EUNSUPPORTED (xd, 2^24 tokens or more), TCL_EHIP.
  */
 int tcl_i8_quant(const void *x, int64_t ldx, tcl_dtype xd, int32_t n_tokens, int32_t d,
                  int8_t *q, int64_t ldq, float *scale, void *stream);
@@ -633,7 +633,7 @@ int tcl_i8_quant(const void *x, int64_t ldx, tcl_dtype xd, int32_t n_tokens, int
  * Errors: TCL_EINVAL (NULL, sizes, ldq < d_in, ldy < d_out), TCL_EALIGN (q, W
  * or y not 16-byte aligned, scales not 4-byte aligned, d_in or ldq not a
  * multiple of 16, d_out or ldy not a multiple of 8), TCL_EUNSUPPORTED (yd,
- * d_in beyond TCL_I8_MAX_D_IN), TCL_EHIP.
+ * d_in beyond TCL_I8_MAX_D_IN, 2^24 tokens or more), TCL_EHIP.
  */
 int tcl_i8_product(const tcl_i8_weight *w, const int8_t *q, int64_t ldq, const float *scale,
                    int32_t n_tokens, void *y, int64_t ldy, tcl_dtype yd, void *stream);
@@ -703,8 +703,8 @@ typedef struct {
  * Errors: TCL_EINVAL (NULL, sizes, leading dimensions below the rows),
  * TCL_EALIGN (k, v, q, q_out, K or V not 16-byte aligned, slot not 8-byte,
  * pos or inv_freq not 4-byte aligned, leading dimensions or strides not
- * multiples of 8), TCL_EUNSUPPORTED (head_dim, page_size, rot_dim, xd),
- * TCL_EHIP.
+ * multiples of 8), TCL_EUNSUPPORTED (head_dim, page_size, rot_dim, xd,
+ * 2^24 tokens or more), TCL_EHIP.
  */
 int tcl_kv_append(const tcl_kv_cache *c, const tcl_rope *rope, const void *k, int64_t ldk,
                   const void *v, int64_t ldv, const void *q, int64_t ldq, int32_t n_q_heads,
@@ -756,14 +756,14 @@ int tcl_attn_workspace_bytes(const tcl_attn_batch *b, const tcl_kv_cache *c, int
  * `plan` (device, 256-byte aligned, tcl_attn_plan_bytes bytes).  One mapping
  * serves every layer whose cache has the same pages, heads and head_dim; a
  * batch of other lengths or tables needs a new one (into the same plan, with
- * the same sizes, if wanted, once the work that uses it has run).  A bad table (pointers that decrease or do not
- * run as above, a negative length or one beyond its page list, a page id in
- * use outside the cache) leaves TCL_EINVAL in the plan, and tcl_attn_apply
- * then changes nothing.  Graph-capturable.
+ * the same sizes, if wanted, once the work that uses it has run).  A bad table
+ * (pointers that decrease or do not run as above, a negative length or one
+ * beyond its page list, a page id in use outside the cache) leaves TCL_EINVAL
+ * in the plan, and tcl_attn_apply then changes nothing.  Graph-capturable.
  * Errors: TCL_EINVAL, TCL_EALIGN, TCL_ENOSPC, TCL_EUNSUPPORTED (head_dim
  * other than 64, 128 and 256, more than 128 query heads a key head, page
- * lists of 2^29 keys, n_tokens * n_q_heads of 2^29, requests and groups times
- * key heads of 2^30), TCL_EHIP.
+ * lists of 2^29 keys, n_tokens * n_q_heads of 2^29, 2^24 tokens, 2^24 tiles
+ * of 128 query rows, requests and groups times key heads), TCL_EHIP.
  */
 int tcl_attn_plan(const tcl_attn_batch *b, const tcl_kv_cache *c, int32_t n_q_heads, void *plan,
                   size_t plan_bytes, void *stream);
@@ -788,7 +788,7 @@ int tcl_attn_status_async(const void *plan, int32_t *dev_status, void *stream);
  * product as bf16 (for tiles of at most 16 rows as two bf16 parts).  Results
  * are bitwise reproducible for the same batch.
  * Errors: those of tcl_attn_plan; TCL_EINVAL (NULL, leading dimensions,
- * scale not finite), TCL_EALIGN, TCL_ENOSPC.
+ * scale not finite or of 2^127 and more), TCL_EALIGN, TCL_ENOSPC.
  */
 int tcl_attn_apply(const tcl_attn_batch *b, const tcl_kv_cache *c, int32_t n_q_heads,
                    const void *plan, size_t plan_bytes, const void *q, int64_t ldq, void *o,

@@ -36,6 +36,8 @@ constexpr int kTargetFew = 1024, kTargetMany = 512;
 // a request whose rows fill half a tile reads its prefix by itself
 constexpr int kShortRows = 64;
 constexpr int kMagic = 0x41747432;
+// workgroups of a launch (of 256 threads, below 2^32 of them)
+constexpr int kMaxGrid = 1 << 24;
 
 // A request's keys are numbered with its own ones starting on a step of their
 // own: key j < prefix is the prefix's, key j >= whole(prefix) is own key j -
@@ -889,7 +891,7 @@ struct Direct {
                 "s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %5\n\t"
                 "global_load_lds_dwordx4 %2, %5 offset:1024\n\t"
                 "global_load_lds_dwordx4 %3, %5 offset:2048\n\t"
-                "global_load_lds_dwordx4 %4, %5 offset:3072" ::"s"(to[x] + 1024 * i),
+                "global_load_lds_dwordx4 %4, %5 offset:0xc00" ::"s"(to[x] + 1024 * i),
                 "v"(off[i]), "v"(off[i + 1]), "v"(off[i + 2]), "v"(off[i + 3]), "s"(from[x])
                 : "memory", "m0");
       }
@@ -1239,10 +1241,14 @@ int check_batch(const tcl_attn_batch *b, const tcl_kv_cache *c, int32_t Hq, KvAr
   if (int64_t(b->ld_own) * c->page_size >= lim / 2 ||
       int64_t(b->ld_prefix) * c->page_size >= lim / 2)
     return fail(TCL_EUNSUPPORTED, "attn: page tables of 2^29 keys or more");
-  if (int64_t(b->n_tokens) * Hq >= lim / 2 || b->n_seqs >= (1 << 24) || b->n_groups >= (1 << 24))
-    return fail(TCL_EUNSUPPORTED, "attn: n_tokens * n_q_heads, n_seqs or n_groups too large");
-  if ((int64_t(b->n_seqs) + b->n_groups) * c->n_kv_heads >= lim)
-    return fail(TCL_EUNSUPPORTED, "attn: more than 2^30 requests and groups times key heads");
+  if (int64_t(b->n_tokens) * Hq >= lim / 2 || b->n_tokens >= kMaxGrid || b->n_seqs >= kMaxGrid ||
+      b->n_groups >= kMaxGrid)
+    return fail(TCL_EUNSUPPORTED, "attn: n_tokens * n_q_heads, n_tokens, n_seqs or n_groups too large");
+  const int gq = Hq / c->n_kv_heads;
+  const int64_t items = 2 * int64_t(b->n_tokens / (kRows / gq)) + b->n_seqs + b->n_groups +
+                        (kTargetFew + c->n_kv_heads - 1) / c->n_kv_heads;
+  if (items * c->n_kv_heads >= kMaxGrid)
+    return fail(TCL_EUNSUPPORTED, "attn: 2^24 row tiles, requests and groups times key heads");
   if (b->n_seqs > 0 && (!b->seq_tok_ptr || !b->group_seq_ptr || !b->own_len))
     return fail(TCL_EINVAL, "attn: batch arrays are NULL");
   if (b->n_seqs > 0 && b->n_groups < 1) return fail(TCL_EINVAL, "attn: requests without a group");
@@ -1394,7 +1400,8 @@ extern "C" int tcl_attn_apply(const tcl_attn_batch *b, const tcl_kv_cache *c, in
   const int64_t row = int64_t(n_q_heads) * c->head_dim;
   if (ldq < row || ldo < row) return fail(TCL_EINVAL, "attn: ldq or ldo below the heads of a row");
   if (ldq % 8 || ldo % 8) return fail(TCL_EALIGN, "attn: ldq and ldo must be multiples of 8");
-  if (!std::isfinite(scale)) return fail(TCL_EINVAL, "attn: scale is not finite");
+  if (!std::isfinite(scale * 1.44269504088896341f))  // (scores are in powers of two)
+    return fail(TCL_EINVAL, "attn: scale is not finite, or 2^127 and more");
   if (b->n_tokens == 0 || b->n_seqs == 0) return TCL_OK;
   if (!q || !o || !ws) return fail(TCL_EINVAL, "attn: q, o and ws are required");
   if (misaligned(q, 16) || misaligned(o, 16) || misaligned(lse, 4) || misaligned(ws, 256))

@@ -614,10 +614,14 @@ int check_weight(const tcl_i8_weight *w) {
   return TCL_OK;
 }
 
+// (a launch's threads, up to 256 a token, below 2^32)
+constexpr int kMaxTokens = 1 << 24;
+
 int check_quant(const void *x, int64_t ldx, int xd, int32_t n_tokens, int32_t d) {
   if (n_tokens < 0 || d < 16)
     return fail(TCL_EINVAL, "i8: n_tokens %d < 0 or d %d < 16", n_tokens, d);
   if (xd != TCL_BF16 && xd != TCL_F32) return fail(TCL_EUNSUPPORTED, "i8: x dtype %d", xd);
+  if (n_tokens >= kMaxTokens) return fail(TCL_EUNSUPPORTED, "i8: n_tokens %d, 2^24 or more", n_tokens);
   if (ldx < d) return fail(TCL_EINVAL, "i8: ldx < d");
   if (d % 16 || ldx % 8) return fail(TCL_EALIGN, "i8: d must be a multiple of 16, ldx of 8");
   if (n_tokens > 0 && !x) return fail(TCL_EINVAL, "i8: x is NULL");
@@ -628,6 +632,7 @@ int check_quant(const void *x, int64_t ldx, int xd, int32_t n_tokens, int32_t d)
 int check_y(const tcl_i8_weight *w, int32_t n_tokens, const void *y, int64_t ldy, int yd) {
   if (n_tokens < 0) return fail(TCL_EINVAL, "i8: n_tokens %d < 0", n_tokens);
   if (yd != TCL_BF16 && yd != TCL_F32) return fail(TCL_EUNSUPPORTED, "i8: y dtype %d", yd);
+  if (n_tokens >= kMaxTokens) return fail(TCL_EUNSUPPORTED, "i8: n_tokens %d, 2^24 or more", n_tokens);
   if (w->d_out == 0) return TCL_OK;  // nothing is written
   if (ldy < w->d_out) return fail(TCL_EINVAL, "i8: ldy < d_out");
   if (n_tokens > 0 && !y) return fail(TCL_EINVAL, "i8: y is NULL");

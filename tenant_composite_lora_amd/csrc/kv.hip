@@ -195,6 +195,8 @@ extern "C" int tcl_kv_append(const tcl_kv_cache *c, const tcl_rope *rope, const 
   }
   if (int64_t(q ? n_q_heads : 0) + 2 * int64_t(c->n_kv_heads) > (int64_t(1) << 26))
     return fail(TCL_EUNSUPPORTED, "kv: too many heads");
+  if (n_tokens >= 1 << 24)  // (a launch's threads, 256 a token, below 2^32)
+    return fail(TCL_EUNSUPPORTED, "kv: n_tokens %d, 2^24 or more", n_tokens);
   if (n_tokens == 0) return TCL_OK;
   if (!k || !v || !pos || !slot) return fail(TCL_EINVAL, "kv: k, v, pos and slot are required");
   if (misaligned(k, 16) || misaligned(v, 16) || misaligned(slot, 8) || misaligned(pos, 4) ||

@@ -776,6 +776,23 @@ def _vector(what: str, t: torch.Tensor, n: int, dtype: torch.dtype) -> None:
         raise ValueError(f"{what} must be a contiguous {dtype} tensor of {n} entries")
 
 
+def _stream_object(dev: torch.device, stream):
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    raw = _stream(dev, stream)
+    return torch.cuda.ExternalStream(raw, dev) if raw else torch.cuda.default_stream(dev)
+
+
+def _made_for(dev: torch.device, stream) -> None:
+    """Before a call writes tensors that it makes itself: their memory may have
+    been freed with work of the current stream still to run on it, so another
+    stream waits for that work."""
+    if stream is not None:
+        s, current = _stream_object(dev, stream), torch.cuda.current_stream(dev)
+        if s != current:
+            s.wait_stream(current)
+
+
 def _call(dev: torch.device, fn, args, stream, *own) -> None:
     """fn(*args, stream) with ``dev`` the current device; tensors the call
     allocated itself are kept for a stream other than the one they were
@@ -785,9 +802,9 @@ def _call(dev: torch.device, fn, args, stream, *own) -> None:
         st = torch._C._cuda_getCurrentRawStream(i)
     else:
         st = _stream(dev, stream)
-        if isinstance(stream, torch.cuda.Stream):
-            for t in own:
-                t.record_stream(stream)
+        s = _stream_object(dev, stream)
+        for t in own:
+            t.record_stream(s)
     if torch._C._cuda_getDevice() == i:
         rc = fn(*args, st)
     else:
@@ -818,10 +835,12 @@ class I8Weight:
         self.W, self.scale, self.device = W, scale, W.device
         self.d_out, self.d_in = W.shape
         self.desc = I8WeightDesc(self.d_in, self.d_out, W.data_ptr(), scale.data_ptr(), None)
+        self.W_p = None
         if pack and W.numel():
             n = ctypes.c_size_t(0)
             check(lib().tcl_i8_pack_bytes(ctypes.byref(self.desc), ctypes.byref(n)))
             self.W_p = torch.empty(n.value, dtype=torch.uint8, device=W.device)
+            _made_for(W.device, stream)
             _call(W.device, lib().tcl_i8_pack,
                   (ctypes.byref(self.desc), self.W_p.data_ptr(), n.value), stream, self.W_p, W)
             self.W, self.desc.W = None, None
@@ -844,6 +863,8 @@ def i8_quant(x: torch.Tensor, q: Optional[torch.Tensor] = None,
     ldq = _rows("i8_quant: q", q, T, d)
     _vector("i8_quant: scale", scale, T, torch.float32)
     _same_device("i8_quant", x.device, q, scale)
+    if own:
+        _made_for(x.device, stream)
     _call(x.device, lib().tcl_i8_quant,
           (x.data_ptr(), ldx, _dtype_code(x.dtype), T, d, q.data_ptr(), ldq, scale.data_ptr()),
           stream, *own)
@@ -865,6 +886,10 @@ def i8_product(w: I8Weight, q: torch.Tensor, scale: torch.Tensor,
         own.append(y)
     ldy = _rows("i8_product: y", y, T, w.d_out)
     _same_device("i8_product", q.device, scale, y, w.scale)
+    if own:
+        _made_for(q.device, stream)
+    if w.W_p is not None:
+        own.append(w.W_p)
     _call(q.device, lib().tcl_i8_product,
           (ctypes.byref(w.desc), q.data_ptr(), ldq, scale.data_ptr(), T, y.data_ptr(), ldy,
            _dtype_code(y.dtype)), stream, *own)
@@ -889,13 +914,14 @@ class I8Call:
         if ws is None or ws.numel() * ws.element_size() < need.value:
             ws = torch.empty(max(need.value, 256), dtype=torch.uint8, device=x.device)
         self.ws, self.device = ws, x.device
+        self._own = (ws,) if w.W_p is None else (ws, w.W_p)
         self._fn = lib().tcl_i8_linear
         self._args = _packed(self._fn, (
             ctypes.byref(w.desc), x.data_ptr(), self.ldx, self.xd, T, y.data_ptr(), self.ldy,
             self.yd, ws.data_ptr(), ws.numel() * ws.element_size()))
 
     def __call__(self, stream=None) -> torch.Tensor:
-        _call(self.device, self._fn, self._args, stream, self.ws)
+        _call(self.device, self._fn, self._args, stream, *self._own)
         return self.y
 
 
@@ -904,9 +930,11 @@ def i8_linear(w: I8Weight, x: torch.Tensor, y: Optional[torch.Tensor] = None,
     """tcl_i8_linear: the base projection of x [T, d_in]."""
     if y is None:
         y = torch.empty(x.shape[0], w.d_out, dtype=y_dtype, device=x.device)
-        if isinstance(stream, torch.cuda.Stream):
-            y.record_stream(stream)
-    return I8Call(w, x, y)(stream)
+        if stream is not None and x.is_cuda:
+            y.record_stream(_stream_object(x.device, stream))
+    call = I8Call(w, x, y)
+    _made_for(x.device, stream)
+    return call(stream)
 
 
 class KVCache:
@@ -993,7 +1021,10 @@ def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, pos: torch.Tenso
               slot: torch.Tensor, rope: Optional[Rope] = None, q: Optional[torch.Tensor] = None,
               q_out: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
     """tcl_kv_append; returns the rotated queries (None without q)."""
-    return AppendCall(cache, k, v, pos, slot, rope, q, q_out)(stream)
+    call = AppendCall(cache, k, v, pos, slot, rope, q, q_out)
+    if call.q_out is not None and q_out is None:
+        _made_for(call.device, stream)
+    return call(stream)
 
 
 class AttnPlan:
@@ -1018,6 +1049,7 @@ class AttnPlan:
         check(lib().tcl_attn_workspace_bytes(ctypes.byref(self.batch), ctypes.byref(cache.desc),
                                              self.n_q_heads, ctypes.byref(n)))
         self.workspace_bytes = n.value
+        _made_for(self.device, stream)
         self._map(stream)
 
     def _set(self, *table):
@@ -1062,8 +1094,10 @@ class AttnPlan:
             out = torch.empty(4, dtype=torch.int32, device=self.device)
         _vector("AttnPlan: status", out, 4, torch.int32)
         _same_device("AttnPlan", self.device, out)
+        if own:
+            _made_for(self.device, stream)
         _call(self.device, lib().tcl_attn_status_async, (self.buf.data_ptr(), out.data_ptr()),
-              stream, *([out] if own else []))
+              stream, self.buf, *([out] if own else []))
         return out
 
     def status(self, stream=None) -> int:
@@ -1110,7 +1144,7 @@ class AttnCall:
 
     def __call__(self, stream=None) -> torch.Tensor:
         p = self.plan  # (the batch's tables are the plan's last ones)
-        _call(p.device, self._fn, (p.batch_ref, *self._args), stream, self.ws, self.o)
+        _call(p.device, self._fn, (p.batch_ref, *self._args), stream, self.ws, self.o, p.buf)
         return self.o
 
 
@@ -1118,4 +1152,6 @@ def attention(plan: AttnPlan, q: torch.Tensor, o: Optional[torch.Tensor] = None,
               lse: Optional[torch.Tensor] = None, scale: Optional[float] = None,
               cache: Optional[KVCache] = None, stream=None) -> torch.Tensor:
     """tcl_attn_apply: attention of the plan's batch over the cache."""
-    return AttnCall(plan, q, o, lse, scale, cache)(stream)
+    call = AttnCall(plan, q, o, lse, scale, cache)
+    _made_for(plan.device, stream)
+    return call(stream)

@@ -503,3 +503,30 @@ def test_attn_host_errors(L):
     assert L.tcl_attn_status_async(None, P, None) == E
     assert L.tcl_attn_status_async(0x10000, None, None) == E
     assert L.tcl_attn_status_async(0x10010, P, None) == A
+
+
+def test_launch_sizes_are_refused_on_the_host(L):
+    """Batches whose launches would pass the grid's limits are refused before
+    anything is launched (no GPU)."""
+    P, U, N = 0x1000, tclora.EUNSUPPORTED, 1 << 24
+    w = ctypes.byref(tclora.I8WeightDesc(64, 32, P, P, None))
+    assert L.tcl_i8_quant(P, 64, 0, N, 64, P, 64, P, None) == U
+    assert L.tcl_i8_product(w, P, 64, P, N, P, 32, 1, None) == U
+    assert L.tcl_i8_linear(w, P, 64, 0, N, P, 32, 1, P, 1 << 40, None) == U
+    c = tclora.KVDesc(4, 16, 2, 64, 2048, 64, 1024, P, P)
+    r = tclora.RopeDesc(P, 64, 0)
+    assert L.tcl_kv_append(ctypes.byref(c), ctypes.byref(r), P, 128, P, 128, None, 0, 0, 0, None, 0,
+                           N, P, P, None) == U
+    out = ctypes.c_size_t(0)
+
+    def sizes(S, G, T, heads, Hq):
+        c = tclora.KVDesc(4, 16, heads, 64, 2048, 64, 1024, P, P)
+        b = tclora.AttnBatch(S, G, T, 4, 4, P, P, P, P, P, P)
+        return L.tcl_attn_plan_bytes(ctypes.byref(b), ctypes.byref(c), Hq, ctypes.byref(out))
+
+    assert [sizes(3, 2, N, 2, 4), sizes(N, 2, 5, 1, 1), sizes(N // 128, 2, 5, 128, 128),
+            sizes(3, N // 128, 5, 128, 128), sizes(1, 1, N // 8, 8, 8 * 128)] == [U] * 5
+    assert sizes(N // 256, 2, 5, 128, 128) == 0 and sizes(1, 1, N // 64, 8, 32) == 0
+    w, c = ctypes.byref(tclora.AttnBatch(3, 2, 5, 4, 4, P, P, P, P, P, P)), ctypes.byref(c)
+    assert L.tcl_attn_apply(w, c, 4, 0x10000, 1 << 40, P, 256, P, 256, None, 3e38, 0x20000, 1 << 40,
+                            None) == tclora.EINVAL

@@ -410,3 +410,27 @@ def test_empty_batches():
     o = torch.full_like(q, 4.0)
     tclora.attention(plan, q, o=o)
     assert (o == 4).all()
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_plan_and_attention_on_another_stream(raw):
+    """Plan, workspace and rows made on the way belong to the stream of the
+    call, also when everything is dropped right behind it."""
+    b = Batch(35, [(300, [(1, 90), (1, 70), (40, 100)])], 4, 2, 64, 32)
+    want = tclora.attention(b.plan(), b.qd)
+    t = b.table()
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    s = st.cuda_stream if raw else st
+    for _ in range(3):
+        torch.cuda._sleep(2_000_000)
+        junk = [torch.full((n,), 7, dtype=torch.uint8, device=DEV) for n in (1 << 14, 1 << 20, b.qd.numel() * 2)]
+        kept = [j.clone() for j in junk]
+        del junk
+        plan = tclora.AttnPlan(b.cache, 4, *t, n_tokens=b.T, stream=s)
+        got = tclora.attention(plan, b.qd, stream=s)
+        del plan
+        over = [torch.full((n,), 9, dtype=torch.uint8, device=DEV) for n in (1 << 14, 1 << 20)]
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and all(bool((k == 7).all()) for k in kept)
+        del got, over

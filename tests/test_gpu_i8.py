@@ -257,3 +257,36 @@ def test_results_repeat_bit_for_bit():
         b = tclora.i8_linear(w, x[3:9])
         assert torch.equal(tclora.i8_linear(w, x), a) and torch.equal(a[3:9], b)
         assert torch.equal(tclora.i8_linear(w, x[3:6]), a[3:6])
+
+
+@pytest.mark.parametrize("T,d_out", [(1, 72), (2, 72), (40, 72), (2100, 1288)])
+def test_scales_at_any_float(T, d_out):
+    """Channel scales need no more than their own alignment."""
+    W, ws = weight(9, d_out, 96)
+    off = torch.empty(d_out + 1, device=DEV)[1:]
+    off.copy_(ws)
+    assert off.data_ptr() % 16 == 4
+    x = acts(3, T, 96, torch.bfloat16)
+    assert torch.equal(tclora.i8_linear(tclora.I8Weight(W, off), x, y_dtype=torch.float32),
+                       tclora.i8_linear(tclora.I8Weight(W, ws), x, y_dtype=torch.float32))
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_another_stream_leaves_freed_memory_to_its_readers(raw):
+    """Memory that the current stream still reads may be handed to a call on
+    another stream, which must not write it before that."""
+    W, ws = weight(10, 2048, 256)
+    w = tclora.I8Weight(W, ws)
+    x = acts(4, 512, 256, torch.bfloat16)
+    want = tclora.i8_linear(w, x)
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    old = torch.full((512, 2048), 3.0, dtype=torch.bfloat16, device=DEV)
+    at = old.data_ptr()
+    torch.cuda._sleep(20_000_000)
+    copy = old.clone()
+    del old
+    got = tclora.i8_linear(w, x, stream=st.cuda_stream if raw else st)
+    torch.cuda.synchronize()
+    assert got.data_ptr() == at  # (the allocator hands the block out again)
+    assert bool((copy == 3.0).all()) and torch.equal(got, want)
