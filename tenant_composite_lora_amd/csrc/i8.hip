@@ -220,7 +220,7 @@ struct ProdArgs {
   void *y;
   int64_t ldy;
   int32_t T, K, N;
-  int32_t t0;      // i8_skinny: first token
+  int32_t t0;      // first token
   int32_t nt, nc;  // i8_tile: token tiles, channel tiles
 };
 
@@ -446,7 +446,7 @@ __global__ __launch_bounds__(64 * WC * WT, 2) void i8_tile(ProdArgs a) {
   const int n = a.nt * a.nc, per = (n + 7) / 8;
   const int id = int(blockIdx.x & 7) * per + int(blockIdx.x >> 3);
   if (int(blockIdx.x >> 3) >= per || id >= n) return;
-  const int c0 = id / a.nt * BC, t0 = id % a.nt * BT;
+  const int c0 = id / a.nt * BC, t0 = a.t0 + id % a.nt * BT;
 
   const int kb = (a.K + 63) / 64, sw = mat_step(a.w), sx = mat_step(a.x);
   const int8_t *pw[NW], *px[NX];
@@ -669,8 +669,8 @@ void go_skinny(const ProdArgs &a, hipStream_t s) {
 }
 
 template <int BC, int BT, int WC, int WT, typename TY>
-void go_tile(ProdArgs &a, hipStream_t s) {
-  a.nt = (a.T + BT - 1) / BT;
+void go_tile(ProdArgs a, hipStream_t s) {
+  a.nt = (a.T - a.t0 + BT - 1) / BT;
   a.nc = (a.N + BC - 1) / BC;
   hipLaunchKernelGGL((i8_tile<BC, BT, WC, WT, TY>), dim3((a.nt * a.nc + 7) / 8 * 8),
                      dim3(64 * WC * WT), 0, s, a);
@@ -686,9 +686,8 @@ void go_tile(ProdArgs &a, hipStream_t s) {
 //     channels 27.8, tiles 28.4); 32 x 64, 4 waves, from 257 on (64 x 14336:
 //     20.3, 32 x 32 23.9; 177 x 4096 of d_in 14336: 34.8, 47.5); else 32 x 32,
 //     8 waves (128 x 4096: 10.6, 32 x 64 12.6);
-//   tiles of 128 x 128 (1024 x 4096: 31.3, 256 x 256 55), of 256 x 128 from
-//     384 of them on (4096 x 4096: 90, 128 x 128 106), of 256 x 256 from
-//     three rounds of them over the CUs on (4224 x 14336: 301, 256 x 128 310).
+// Tiles: by whole rounds over the CUs, two workgroups of 128 x 128 or 256 x
+// 128 each or one of 256 x 256 (tile_cost).
 template <typename TY>
 void product_skinny(const ProdArgs &a, hipStream_t s) {
   const int64_t t = a.T - a.t0, tb = (t + 63) / 64;
@@ -704,30 +703,64 @@ void product_skinny(const ProdArgs &a, hipStream_t s) {
     go_skinny<2, 2, 8, 2, TY>(a, s);
 }
 
+enum Kernel { kSkinny, kTile11, kTile21, kTile22 };
+
+int64_t tiles(int64_t n, int64_t d) { return (n + d - 1) / d; }
+
+// What a kernel costs, in tenths of 8 us at d_in 4096 (every one's time grows
+// with d_in alike).  Measured with the quantiser, us: 1024 x 4096: tiles of
+// 128 x 128 39, 256 x 128 48, 256 x 256 63; 2048: 61, 59, 68; 2304: 75, 78,
+// 69; 4096: 108, 96, 89; 5120: 132, 128, 140; 6144: 154, 138, 148; 8192: 202,
+// 178, 172; 2048 x 14336: 159, 155, 142; 4224 x 14336: 338, 301, 288.
+int64_t tile_cost(Kernel k, int64_t T, int64_t N) {
+  switch (k) {
+    case kSkinny: return 10 + 22 * T * N / (1 << 20);
+    case kTile11: return 20 + 25 * tiles(tiles(T, 128) * tiles(N, 128), 256);
+    case kTile21: return 50 * tiles(tiles(T, 128) * tiles(N, 256), 256);
+    default: return 90 * tiles(tiles(T, 256) * tiles(N, 256), 256);
+  }
+}
+
+Kernel cheapest(int64_t T, int64_t N, int64_t *cost) {
+  Kernel best = kSkinny;
+  if (T > 32 && tiles(T, 128) * tiles(N, 128) >= 192) {
+    best = kTile11;
+    for (Kernel k : {kTile21, kTile22})
+      if (tile_cost(k, T, N) < tile_cost(best, T, N)) best = k;
+  }
+  *cost = tile_cost(best, T, N);
+  return best;
+}
+
+template <typename TY>
+void go(Kernel k, const ProdArgs &a, hipStream_t s) {
+  switch (k) {
+    case kSkinny: product_skinny<TY>(a, s); break;
+    case kTile11: go_tile<128, 128, 4, 2, TY>(a, s); break;
+    case kTile21: go_tile<256, 128, 4, 2, TY>(a, s); break;
+    default: go_tile<256, 256, 4, 2, TY>(a, s); break;
+  }
+}
+
 template <typename TY>
 void product(ProdArgs &a, hipStream_t s) {
-  auto up = [](int64_t n, int64_t d) { return (n + d - 1) / d; };
-  if (a.T <= 32 || up(a.T, 128) * up(a.N, 128) < 192) {
-    product_skinny<TY>(a, s);
-  } else if (up(a.T, 256) * up(a.N, 256) > 768) {
-    go_tile<256, 256, 4, 2, TY>(a, s);
-  } else if (up(a.T, 128) * up(a.N, 256) >= 384) {
-    // two workgroups a CU: where at most a quarter of a last round is left,
-    // and that is few tokens, they go to the other kernel (4224 x 4096: 115
-    // in one launch; 90 + 11)
-    const int64_t nt = up(a.T, 128), nc = up(a.N, 256), left = nt * nc % 512, k = up(left, nc);
-    const bool split = nt * nc > 512 && left > 0 && left <= 128 && k <= 2;
-    const int T = a.T;
-    if (split) a.T = int((nt - k) * 128);
-    go_tile<256, 128, 4, 2, TY>(a, s);
-    if (split) {
-      a.t0 = a.T;
+  int64_t cost, rest_cost;
+  const Kernel k = cheapest(a.T, a.N, &cost);
+  // or the tokens of whole rounds of the largest tiles, and the rest in a
+  // launch of their own (4224 x 4096: 107 in one launch, 101)
+  const int64_t nc = tiles(a.N, 256), rounds = tiles(a.T, 256) * nc / 256;
+  const int T = a.T, first = int(rounds * 256 / nc * 256);
+  if (first > 0 && first < T) {
+    const Kernel rest = cheapest(T - first, a.N, &rest_cost);
+    if (90 * rounds + rest_cost < cost) {
+      a.T = first;
+      go<TY>(kTile22, a, s);
+      a.t0 = first;
       a.T = T;
-      product_skinny<TY>(a, s);
+      return go<TY>(rest, a, s);
     }
-  } else {
-    go_tile<128, 128, 4, 2, TY>(a, s);
   }
+  go<TY>(k, a, s);
 }
 
 Mat8 weight_of(const tcl_i8_weight *w) {

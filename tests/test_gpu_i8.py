@@ -290,3 +290,15 @@ def test_another_stream_leaves_freed_memory_to_its_readers(raw):
     torch.cuda.synchronize()
     assert got.data_ptr() == at  # (the allocator hands the block out again)
     assert bool((copy == 3.0).all()) and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("T,d_out", [(300, 12000), (1030, 4104), (2300, 4096), (4100, 4096),
+                                     (4400, 4072), (5200, 4096), (600, 32768)])
+def test_tiles_of_every_size_and_split_batches(T, d_out):
+    """Batches whose tokens go to one kernel or, past a whole round of large
+    tiles, to two."""
+    W, ws = weight(11, d_out, 80)
+    x = acts(5, T, 80, torch.bfloat16)
+    y = tclora.i8_linear(tclora.I8Weight(W, ws), x, y_dtype=torch.float32)
+    n, s = quant64(x)
+    close(y, product64(W, ws, n, s), torch.float32)
