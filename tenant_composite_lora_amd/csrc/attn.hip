@@ -51,7 +51,7 @@ __device__ inline int key_end(int prefix, int n) {
 
 enum { H_CODE, H_MAGIC, H_SEQS, H_GROUPS, H_TOKENS, H_HEADS, H_KVHEADS, H_DIM, H_PAGES, H_SHIFT,
        H_LDO, H_LDP, H_ITEMS, H_TILES, H_SHARED, H_FLAGS = 16, H_WORDS = 64 };
-constexpr int kCheckers = 16;  // workgroups that look page ids over, a flag each
+constexpr int kPageGroups = 16;  // workgroups that look page ids over, a flag each
 
 struct alignas(16) Work {
   int32_t tok0;     // first token, or first entry of the token list (list 1)
@@ -225,7 +225,7 @@ __device__ inline int tile_hi(const Unit &x, int i) {
 
 // 64 requests 10.4 us, 8 prompts of 512 tokens 11.2, 3 requests 7.8: a launch
 // and the round trips of some fifteen phases.
-// Workgroups 1 .. kCheckers look page ids over, a row of a page table a wave,
+// Workgroups 1 .. kPageGroups look page ids over, a row of a page table a wave,
 // and leave a flag each; workgroup 0 does the rest.  One launch: the flags
 // are read with the header.
 template <bool LDS>
@@ -247,7 +247,7 @@ __global__ __launch_bounds__(kMapThreads) void attn_plan_kernel(PlanArgs a) {
     __syncthreads();
     const int w = (int(blockIdx.x) - 1) * (kMapThreads / 64) + (tid >> 6), lane = tid & 63;
     bool bad = false;
-    for (int r = w; r < a.S + a.G; r += kCheckers * (kMapThreads / 64)) {
+    for (int r = w; r < a.S + a.G; r += kPageGroups * (kMapThreads / 64)) {
       const bool own = r < a.S;
       const int g = r - a.S, ld = own ? a.ldo : a.ldp;
       // (a length that does not fit is workgroup 0's finding)
@@ -430,7 +430,7 @@ __global__ __launch_bounds__(kMapThreads) void attn_plan_kernel(PlanArgs a) {
 __device__ inline bool pages_ok(const int32_t *hdr) {
   int bad = 0;
 #pragma unroll
-  for (int i = 0; i < kCheckers; ++i) bad |= hdr[H_FLAGS + i];
+  for (int i = 0; i < kPageGroups; ++i) bad |= hdr[H_FLAGS + i];
   return bad == 0;
 }
 
@@ -1366,7 +1366,7 @@ extern "C" int tcl_attn_plan(const tcl_attn_batch *b, const tcl_kv_cache *c, int
   a.short_tok = reinterpret_cast<int32_t *>(p + L.o_stok);
   a.short_seq = reinterpret_cast<int32_t *>(p + L.o_sseq);
   a.utile = reinterpret_cast<int32_t *>(p + L.o_utile);
-  const dim3 grid(1 + kCheckers), block(kMapThreads);
+  const dim3 grid(1 + kPageGroups), block(kMapThreads);
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (a.S <= kMapThreads && a.G <= kMapThreads)
     hipLaunchKernelGGL(attn_plan_kernel<true>, grid, block, 0, s, a);

@@ -777,6 +777,8 @@ def _vector(what: str, t: torch.Tensor, n: int, dtype: torch.dtype) -> None:
 
 
 def _stream_object(dev: torch.device, stream):
+    if stream is None:
+        return torch.cuda.current_stream(dev)
     if isinstance(stream, torch.cuda.Stream):
         return stream
     raw = _stream(dev, stream)
@@ -789,19 +791,23 @@ def _made_for(dev: torch.device, stream) -> None:
     stream waits for that work."""
     if stream is not None:
         s, current = _stream_object(dev, stream), torch.cuda.current_stream(dev)
-        if s != current:
+        if s.cuda_stream != current.cuda_stream:
             s.wait_stream(current)
 
 
-def _call(dev: torch.device, fn, args, stream, *own) -> None:
-    """fn(*args, stream) with ``dev`` the current device; tensors the call
-    allocated itself are kept for a stream other than the one they were
-    allocated on."""
+def _call(dev: torch.device, fn, args, stream, *own, home: Optional[int] = None) -> None:
+    """fn(*args, stream) with ``dev`` the current device.  Tensors that the
+    library's own objects made (``own``) are kept for a stream other than the
+    one they were allocated on: one that is given, or a current one that is
+    not ``home``."""
     i = dev.index
     if stream is None:
         st = torch._C._cuda_getCurrentRawStream(i)
+        keep = home is not None and st != home
     else:
         st = _stream(dev, stream)
+        keep = True
+    if keep:
         s = _stream_object(dev, stream)
         for t in own:
             t.record_stream(s)
@@ -915,13 +921,14 @@ class I8Call:
             ws = torch.empty(max(need.value, 256), dtype=torch.uint8, device=x.device)
         self.ws, self.device = ws, x.device
         self._own = (ws,) if w.W_p is None else (ws, w.W_p)
+        self._home = _stream(x.device)
         self._fn = lib().tcl_i8_linear
         self._args = _packed(self._fn, (
             ctypes.byref(w.desc), x.data_ptr(), self.ldx, self.xd, T, y.data_ptr(), self.ldy,
             self.yd, ws.data_ptr(), ws.numel() * ws.element_size()))
 
     def __call__(self, stream=None) -> torch.Tensor:
-        _call(self.device, self._fn, self._args, stream, *self._own)
+        _call(self.device, self._fn, self._args, stream, *self._own, home=self._home)
         return self.y
 
 
@@ -1040,6 +1047,7 @@ class AttnPlan:
                  n_tokens: int, stream=None):
         self.cache, self.n_q_heads, self.n_tokens = cache, int(n_q_heads), int(n_tokens)
         self.device = cache.device
+        self.home = _stream(self.device)
         self._set(seq_tok_ptr, group_seq_ptr, prefix_len, prefix_pages, own_len, own_pages)
         self._sizes = [getattr(self.batch, f) for f, _ in AttnBatch._fields_[:5]]
         n = ctypes.c_size_t(0)
@@ -1136,6 +1144,7 @@ class AttnCall:
         if ws is None or ws.numel() * ws.element_size() < plan.workspace_bytes:
             ws = torch.empty(max(plan.workspace_bytes, 256), dtype=torch.uint8, device=plan.device)
         self.ws = ws
+        self._home = _stream(plan.device)
         self._fn = lib().tcl_attn_apply
         self._args = _packed(self._fn, (
             None, ctypes.byref(cache.desc), plan.n_q_heads, plan.buf.data_ptr(), plan.buf.numel(),
@@ -1144,7 +1153,8 @@ class AttnCall:
 
     def __call__(self, stream=None) -> torch.Tensor:
         p = self.plan  # (the batch's tables are the plan's last ones)
-        _call(p.device, self._fn, (p.batch_ref, *self._args), stream, self.ws, self.o, p.buf)
+        _call(p.device, self._fn, (p.batch_ref, *self._args), stream, self.ws, self.o, p.buf,
+              home=self._home if self._home == p.home else -1)
         return self.o
 
 

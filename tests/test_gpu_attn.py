@@ -434,3 +434,19 @@ def test_plan_and_attention_on_another_stream(raw):
         torch.cuda.synchronize()
         assert torch.equal(got, want) and all(bool((k == 7).all()) for k in kept)
         del got, over
+
+
+def test_two_calls_at_once():
+    """Two layers' attention on two streams through one plan, a workspace each."""
+    b = Batch(37, [(300, [(1, 90), (1, 70), (40, 100)]), (64, [(1, 30), (1, 200)])], 8, 2, 128, 16)
+    plan = b.plan()
+    other = tclora.KVCache(b.cache.V, b.cache.K)
+    want = [tclora.attention(plan, b.qd), tclora.attention(plan, b.qd, cache=other)]
+    calls = [tclora.AttnCall(plan, b.qd), tclora.AttnCall(plan, b.qd, cache=other)]
+    st = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for s, c in zip(st, calls):
+            c(s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(c.o, o) for c, o in zip(calls, want))
