@@ -681,26 +681,31 @@ void go_tile(ProdArgs a, hipStream_t s) {
 //   up to 16 tokens: 16 channels a workgroup, 8 waves over d_in (1 token,
 //     1024 channels: 4.1; 32 channels: 5.5);
 //   up to 32: the same with two token blocks (4096 channels: 7.4; 32: 8.3);
-//   more, as long as 128 x 128 tiles are fewer than 192: 64 channels x 64
-//     tokens from 512 workgroups on (512 tokens x 4096 channels: 22.2, 32
-//     channels 27.8, tiles 28.4); 32 x 64, 4 waves, from 257 on (64 x 14336:
-//     20.3, 32 x 32 23.9; 177 x 4096 of d_in 14336: 34.8, 47.5); else 32 x 32,
-//     8 waves (128 x 4096: 10.6, 32 x 64 12.6);
+//   more, as long as 128 x 128 tiles are fewer than 192: by what runs in one
+//     round, two workgroups a CU (with the quantiser): 32 channels x 64
+//     tokens, 4 waves, up to 512 of them (256 x 4096: 22.2; 64 x 48 24.2; 64 x
+//     64 27.2), else 64 x 48 (333 x 4096: 24.8, 32 x 64 28.8, 64 x 64 28.5; 72
+//     x 14336: 27.7, 34.8, 31.0), else 64 x 64 (100 x 14336: 31.4, 32 x 64
+//     36.5, 64 x 48 35.6), else 64 x 48 again (560 x 4096: 34.6, 40.7, 38.3);
+//     and 32 x 32 with 8 waves where 32 x 64 are at most 256 (128 x 4096:
+//     17.2, 32 x 64 19.0).
 // Tiles: by whole rounds over the CUs, two workgroups of 128 x 128 or 256 x
 // 128 each or one of 256 x 256 (tile_cost).
 template <typename TY>
 void product_skinny(const ProdArgs &a, hipStream_t s) {
-  const int64_t t = a.T - a.t0, tb = (t + 63) / 64;
+  const int64_t t = a.T - a.t0, tb = (t + 63) / 64, n64 = (a.N + 63) / 64, n32 = (a.N + 31) / 32;
   if (t <= 16)
     go_skinny<1, 1, 8, 2, TY>(a, s);
   else if (t <= 32)
     go_skinny<1, 2, 8, 2, TY>(a, s);
-  else if (tb * ((a.N + 63) / 64) >= 512)
-    go_skinny<4, 4, 4, 2, TY>(a, s);
-  else if (tb * ((a.N + 31) / 32) > 256)
-    go_skinny<2, 4, 4, 2, TY>(a, s);
-  else
+  else if (tb * n32 <= 256)
     go_skinny<2, 2, 8, 2, TY>(a, s);
+  else if (tb * n32 <= 512)
+    go_skinny<2, 4, 4, 2, TY>(a, s);
+  else if ((t + 47) / 48 * n64 > 512 && tb * n64 <= 512)
+    go_skinny<4, 4, 4, 2, TY>(a, s);
+  else
+    go_skinny<4, 3, 4, 2, TY>(a, s);
 }
 
 enum Kernel { kSkinny, kTile11, kTile21, kTile22 };

@@ -291,7 +291,8 @@ def test_another_stream_leaves_freed_memory_to_its_readers(raw):
 
 
 @pytest.mark.parametrize("T,d_out", [(300, 12000), (1030, 4104), (2300, 4096), (4100, 4096),
-                                     (4400, 4072), (5200, 4096), (600, 32768)])
+                                     (4400, 4072), (5200, 4096), (600, 32768),
+                                     (72, 14336), (100, 14328), (333, 4096), (560, 4088)])
 def test_tiles_of_every_size_and_split_batches(T, d_out):
     """Batches whose tokens go to one kernel or, past a whole round of large
     tiles, to two."""
