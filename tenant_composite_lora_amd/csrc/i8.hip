@@ -141,12 +141,14 @@ __device__ inline i32x4 quant16(const R &x, float s, float inv) {
 }
 
 // WPR waves a row, ROWS rows a workgroup: a row is read once into registers,
-// its largest magnitude reduced, the integers written.  Many rows: four a
-// workgroup, which writes whole 64-byte sectors of the blocks.  Few: one, so
-// that there are more workgroups.  4224 x 4096 bf16: 17 us (52 MB, 3.1 TB/s);
-// every wave is resident at once, so that all load, round and store in turn
-// (half the waves with two rows each, the second's loads ahead of the first's
-// rounding, took 21).  64 x 4096: 4 us, 177 x 14336 fp32: 8 us.
+// its largest magnitude reduced, the integers written.  A wave takes 1024
+// elements at a time; with a wave a row, every wave is resident at once and
+// all load, round and store in turn, with too many the short rows' idle ones
+// cost.  bf16, us, 1 x 4, 2 x 4, 4 x 2, 8 x 1 waves and rows: 4224 x 1024: 7,
+// 8, 11, 16; 4224 x 2048: 12, 11, 14, 19; 4224 x 4096: 20, 19, 18, 22 (52 MB);
+// 4224 x 14336: 86, 70, 63, 75; 256 x 4096: 9.8, 6.7, 5.0, 5.3; 256 x 14336:
+// 33, 19, 12, 9; 1024 x 5120: 14.5, 10.9, 10.3, 10.7.  (Two rows a wave, the
+// second's loads ahead of the first's rounding: 21 for 17 at 4224 x 4096.)
 template <typename T, int WPR, int ROWS>
 __global__ __launch_bounds__(64 * WPR * ROWS) void i8_quant_kernel(QuantArgs a) {
   __shared__ uint32_t wmax[ROWS][WPR];
@@ -649,13 +651,17 @@ int launch_quant(const void *x, int64_t ldx, int xd, int32_t n, int32_t d, int8_
   QuantArgs a{x, ldx, ldq, n, d, blocks_of(d), packed, q, scale};
 #define QUANT(T, W, R) \
   hipLaunchKernelGGL((i8_quant_kernel<T, W, R>), dim3((n + R - 1) / R), dim3(64 * W * R), 0, s, a)
+#define QUANT_D(T)                       \
+  if (d <= 1024) QUANT(T, 1, 4);         \
+  else if (d <= 2048) QUANT(T, 2, 4);    \
+  else if (d <= 4096 || n > 512) QUANT(T, 4, 2); \
+  else QUANT(T, 8, 1)
   if (xd == TCL_BF16) {
-    if (n <= 1024) QUANT(bf16_t, 4, 1);
-    else QUANT(bf16_t, 1, 4);
+    QUANT_D(bf16_t);
   } else {
-    if (n <= 1024) QUANT(float, 4, 1);
-    else QUANT(float, 1, 4);
+    QUANT_D(float);
   }
+#undef QUANT_D
 #undef QUANT
   TCL_HIP(hipGetLastError());
   return TCL_OK;

@@ -340,3 +340,11 @@ def test_two_calls_at_once():
             c(s)
     torch.cuda.synchronize()
     assert all(torch.equal(y, o) for y, o in zip(ys, want))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d", [(7, 1024), (7, 1040), (5, 2048), (1027, 2064), (3, 4112), (512, 4112),
+                                 (513, 4112), (2, 33008), (515, 16400)])
+def test_quant_by_rows_of_every_length(T, d, dtype):
+    """Each number of waves a row, rows beyond what they keep, odd row counts."""
+    test_quant_is_the_definition(T, d, dtype)
