@@ -31,9 +31,9 @@ constexpr int kMinChunk = 128;  // smallest key range an item is cut to
 // Workgroups that a batch is cut into where it has fewer tiles.  Few rows:
 // four a CU (with two, four and eight: 64 requests of 8 tenants 174, 160 and
 // 155 us, 16 requests of 4 tenants 30, 29 and 32).  Many: two, as many as run
-// at a time; their partial outputs
-// weigh more (64 requests over a prefix of 8192: 35 + 8 us, with 1024 41 +
-// 10; chunks of 256..512 tokens over 4096: 41 us of joining, with 1024 107).
+// at a time; their partial outputs weigh more (64 requests over a prefix of
+// 8192: 35 + 8 us, with 1024 41 + 10; chunks of 256..512 tokens over 4096: 41
+// us of joining, with 1024 107).
 constexpr int kTargetFew = 1024, kTargetMany = 512;
 // a request whose rows fill half a tile reads its prefix by itself
 constexpr int kShortRows = 64;

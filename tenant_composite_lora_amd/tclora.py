@@ -1067,11 +1067,12 @@ class AttnPlan:
                            ("group_seq_ptr", group_seq_ptr, G + 1),
                            ("prefix_len", prefix_len, G), ("own_len", own_len, S)):
             _vector(f"AttnPlan: {name}", t, n, torch.int32)
-        ldp = _rows("AttnPlan: prefix_pages", prefix_pages, G)
-        ldo = _rows("AttnPlan: own_pages", own_pages, S)
+        ldp = _rows("AttnPlan: prefix_pages", prefix_pages, G) if prefix_pages.numel() else 0
+        ldo = _rows("AttnPlan: own_pages", own_pages, S) if own_pages.numel() else 0
         if prefix_pages.dtype != torch.int32 or own_pages.dtype != torch.int32:
             raise ValueError("AttnPlan: page tables must be int32")
-        if prefix_pages.shape[1] != ldp or own_pages.shape[1] != ldo:
+        if ((prefix_pages.numel() and prefix_pages.shape[1] != ldp)
+                or (own_pages.numel() and own_pages.shape[1] != ldo)):
             raise ValueError("AttnPlan: page tables must be contiguous")
         _same_device("AttnPlan", self.device, *table)
         self.table = table

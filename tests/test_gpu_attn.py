@@ -450,3 +450,22 @@ def test_two_calls_at_once():
             c(s)
     torch.cuda.synchronize()
     assert all(torch.equal(c.o, o) for c, o in zip(calls, want))
+
+
+def test_no_prefix_pages_at_all():
+    """Groups without prefixes may have a page table of no columns, requests
+    without own keys likewise."""
+    b = Batch(38, [(0, [(1, 20), (30, 40)]), (0, [(1, 5)])], 4, 2, 64, 16)
+    want = tclora.attention(b.plan(), b.qd)
+    t = list(b.table())
+    t[3] = torch.empty(2, 0, dtype=torch.int32, device=DEV)
+    plan = tclora.AttnPlan(b.cache, 4, *t, n_tokens=b.T)
+    assert plan.status() == tclora.OK
+    assert torch.equal(tclora.attention(plan, b.qd), want)
+    b = Batch(39, [(50, [(1, 0), (2, 0)]), (7, [(1, 0)])], 4, 2, 64, 16)
+    want = tclora.attention(b.plan(), b.qd)
+    t = list(b.table())
+    t[5] = torch.empty(3, 0, dtype=torch.int32, device=DEV)
+    plan = tclora.AttnPlan(b.cache, 4, *t, n_tokens=b.T)
+    assert plan.status() == tclora.OK
+    assert torch.equal(tclora.attention(plan, b.qd), want)
