@@ -784,9 +784,12 @@ int tcl_attn_status_async(const void *plan, int32_t *dev_status, void *stream);
  * nothing is written); q and o may be the same rows.  ws: device workspace of
  * tcl_attn_workspace_bytes bytes, 256-byte aligned, in use until the call's
  * work has run; calls that may run at the same time need one each.
- * Scores, running maxima and sums are fp32; probabilities enter the second
- * product as bf16 (for tiles of at most 16 rows as two bf16 parts).  Results
- * are bitwise reproducible for the same batch.
+ * Scores, running maxima and sums are fp32.  Probabilities enter the second
+ * product as two bf16 parts (less than 2^-14 of them lost) for a request of
+ * fewer than 64 query rows a key head (query tokens * n_q_heads /
+ * n_kv_heads), as one bf16 number (2^-8 at most) for a longer one: a
+ * request's own length decides, not its batch.  Results are bitwise
+ * reproducible for the same batch.
  * Errors: those of tcl_attn_plan; TCL_EINVAL (NULL, leading dimensions,
  * scale not finite or of 2^127 and more), TCL_EALIGN, TCL_ENOSPC.
  */

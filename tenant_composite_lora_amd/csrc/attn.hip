@@ -63,7 +63,8 @@ struct alignas(16) Work {
   int32_t prefix;   // keys of the prefix
   int32_t lo, hi;   // keys [lo, hi), lo a whole step
   int32_t part;     // first partial row, -1: write the output itself
-  int32_t pad[3];
+  int32_t fine;     // weights in two parts (attend_many)
+  int32_t pad[2];
 };
 
 struct alignas(16) Tile {
@@ -392,7 +393,8 @@ __global__ __launch_bounds__(kMapThreads) void attn_plan_kernel(PlanArgs a) {
       const int lo = min(c.hi, c.x.lo + n * c.per), row = l_row[j] + n * c.nt * gq;
       if (item_base + k >= a.cap_items || row + c.nt * gq > a.cap_rows) continue;
       a.items[item_base + k] = Work{c.x.tok0 + c.i * c.x.tpt, c.x.list, c.nt, c.x.seq, c.x.group,
-                                    c.x.prefix, lo, min(c.hi, lo + c.per), direct(c) ? -1 : row, {}};
+                                    c.x.prefix, lo, min(c.hi, lo + c.per), direct(c) ? -1 : row,
+                                    c.x.list || is_short(a, c.x.n_q), {}};
     }
     item_base += total[0], row_base += total[1];
     __syncthreads();
@@ -943,7 +945,17 @@ struct Direct {
 // operations: 366 us, read ahead 290, 840 T a second).  What is left is the
 // exponentials and maxima between the two products: two waves a SIMD overlap
 // them in part.
-template <int D>
+//
+// FINE: the weights enter the second product as two bf16 parts, less than
+// 2^-14 of them lost, else as one, 2^-8.  Two for every tile of short
+// requests, so that a token's accuracy does not depend on how many others
+// share its prefix and thus its tile (attend_few has two as well): the error
+// of the output is then that of its own rounding, 1.66e-3 in the mean against
+// 2.2e-3 to 2.3e-3 with one part, and the keys' bytes bound such batches
+// anyway (64 requests over a prefix of 8192: 43 us with one part, 46 with two;
+// of 8 tenants 158 and 159).  One for long requests, where the matrix cores
+// bound (chunks of 8 requests over 4096: 296 us, with two 391).
+template <int D, bool FINE>
 __device__ inline void attend_many(const AttnArgs &a, const Work &t, int h, int gq, Smem<D> &sm) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int rows = t.n_tok * gq, steps = (t.hi - t.lo + kKeys - 1) / kKeys;
@@ -1004,7 +1016,7 @@ __device__ inline void attend_many(const AttnArgs &a, const Work &t, int h, int 
     }
     bool rare = false;
     if (hides(j0, tile_least)) rare = __syncthreads_or(st.bad(sm.v[b]));
-    uint32_t pw[4][4];
+    uint32_t pw[4][4], pl[4][4];
     if (busy) {
       const uint16_t *sk = sm.k[0];
       const int kp = kpos + b * kKeys * D;
@@ -1062,7 +1074,17 @@ __device__ inline void attend_many(const AttnArgs &a, const Work &t, int h, int 
           const float q = __builtin_amdgcn_exp2f(fmaf(s2[x][e + 1], a.scale2, -mu));
           l += p;
           l += q;
-          pw[2 * x + e / 8][e % 8 / 2] = pack_bf16(p, q);
+          uint32_t &hi = pw[2 * x + e / 8][e % 8 / 2];
+          if constexpr (FINE) {
+            // (the high part cut off, not rounded, and 2^-20 added, so that the
+            // low part of a weight is never zero or negative: either would
+            // make a NaN of a seen infinity)
+            hi = __builtin_amdgcn_perm(__float_as_uint(q), __float_as_uint(p), 0x07060302);
+            pl[2 * x + e / 8][e % 8 / 2] =
+                pack_bf16(fmaf(p, 1 + 0x1p-20f, -bf16_lo(hi)), fmaf(q, 1 + 0x1p-20f, -bf16_hi(hi)));
+          } else {
+            hi = pack_bf16(p, q);
+          }
         }
     }
     if (rare) {
@@ -1102,20 +1124,22 @@ __device__ inline void attend_many(const AttnArgs &a, const Work &t, int h, int 
     for (int s = 0; s < 4; ++s) {
       // keys 16 s + {4 g + 0..3, 8 + 4 g + 0..3}: the lane's eight, in order
       const bf16x8_t pf = __builtin_bit_cast(bf16x8_t, nt_u4{pw[s][0], pw[s][1], pw[s][2], pw[s][3]});
+      const bf16x8_t pg = __builtin_bit_cast(bf16x8_t, nt_u4{pl[s][0], pl[s][1], pl[s][2], pl[s][3]});
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
         const s16x4 x = read_tr(sv + ((vp0 ^ (32 * i)) + 16 * s * D));
         const s16x4 y = read_tr(sv + ((vp1 ^ (32 * i)) + 16 * s * D));
         const s16x8 vv = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
-        o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, vv), pf, o[i], 0,
-                                                       0, 0);
+        const bf16x8_t vf = __builtin_bit_cast(bf16x8_t, vv);
+        o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf, o[i], 0, 0, 0);
+        if constexpr (FINE) o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pg, o[i], 0, 0, 0);
       }
     }
     constexpr int AHEAD = 6;
     __builtin_amdgcn_sched_group_barrier(0x100, 2 * AHEAD, 0);
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) {
-      __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x8, FINE ? 2 : 1, 0);
       if (i + AHEAD < D / 8) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -1155,8 +1179,10 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_kernel(AttnArgs a)
   const int gq = a.Hq / a.c.H;
   if (t.n_tok * gq <= kFew)
     attend_few<D>(a, t, h, gq, sm);
+  else if (t.fine)
+    attend_many<D, true>(a, t, h, gq, sm);
   else
-    attend_many<D>(a, t, h, gq, sm);
+    attend_many<D, false>(a, t, h, gq, sm);
 }
 
 // Joins the items of a token's rows, a row a wave at a time: maxima first,
