@@ -17,6 +17,7 @@
 // against 5.9 packed; 177 tokens, d_in 14336, 62 against 35.
 #include <cmath>
 
+#include "i8_index.hpp"
 #include "kern_common.hpp"
 
 namespace tcl {
@@ -24,24 +25,6 @@ namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x16 __attribute__((ext_vector_type(16)));
-
-// An int8 matrix of n rows: in rows (ld bytes apart) or in blocks (kb blocks
-// a row of blocks).
-struct Mat8 {
-  const int8_t *p;
-  int64_t ld;
-  int32_t n, kb, packed;
-};
-
-// Offset of chunk g of row r in the first block, and the step to the next one.
-__device__ inline int64_t mat_at(const Mat8 &m, int r, int g) {
-  if (m.packed) {
-    r = min(r, (m.n - 1) | 15);  // rows are padded to whole blocks
-    return int64_t(r >> 4) * m.kb * 1024 + g * 256 + (r & 15) * 16;
-  }
-  return int64_t(min(r, m.n - 1)) * m.ld + g * 16;
-}
-__device__ inline int mat_step(const Mat8 &m) { return m.packed ? 1024 : 64; }
 
 // ---------------------------------------------------------------------------
 // activations to 8 bits
@@ -280,9 +263,8 @@ __global__ __launch_bounds__(64 * WV) void i8_skinny(ProdArgs a) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       // past the row's end: any bytes of the weight times zeros
-      b[h] = 2 * pair + h;
-      in[h] = 64 * b[h] + 16 * g < a.K;
-      if (!in[h]) b[h] = 0;
+      in[h] = chunk_in(a.K, 2 * pair + h, g);
+      b[h] = block_or_first(a.K, 2 * pair + h, g);
     }
 #pragma unroll
     for (int m = 0; m < MB; ++m)
@@ -362,7 +344,7 @@ __global__ __launch_bounds__(512) void i8_token(ProdArgs a, const void *x, int64
   const int sw = mat_step(a.w), kb = (a.K + 63) / 64, nc = a.K / 16;
   i32x4 wf[4];
   auto load = [&](int p, int b) {
-    wf[p] = *reinterpret_cast<const i32x4 *>(wp + int64_t(64 * b + 16 * g < a.K ? b : 0) * sw);
+    wf[p] = *reinterpret_cast<const i32x4 *>(wp + int64_t(block_or_first(a.K, b, g)) * sw);
   };
 #pragma unroll
   for (int p = 0; p < 4; ++p) load(p, w + 8 * p);
@@ -461,7 +443,7 @@ __global__ __launch_bounds__(64 * WC * WT, 2) void i8_tile(ProdArgs a) {
     px[i] = a.x.p + mat_at(a.x, t0 + ((tid + i * TH) >> 6) * 16 + (tid & 15), g);
   i32x4 rw[NW], rx[NX];
   auto load = [&](int st) {
-    const int b = 64 * st + 16 * g < a.K ? st : 0;
+    const int b = block_or_first(a.K, st, g);
 #pragma unroll
     for (int i = 0; i < NW; ++i)
       rw[i] = *reinterpret_cast<const i32x4 *>(pw[i] + int64_t(b) * sw);
@@ -470,7 +452,7 @@ __global__ __launch_bounds__(64 * WC * WT, 2) void i8_tile(ProdArgs a) {
       rx[i] = *reinterpret_cast<const i32x4 *>(px[i] + int64_t(b) * sx);
   };
   auto put = [&](int b, int st) {
-    const bool in = 64 * st + 16 * g < a.K;  // zeros past the row's end
+    const bool in = chunk_in(a.K, st, g);  // zeros past the row's end
 #pragma unroll
     for (int i = 0; i < NW; ++i) lw[b][tid + i * TH] = rw[i];
 #pragma unroll
@@ -776,8 +758,8 @@ void product(ProdArgs &a, hipStream_t s) {
 
 Mat8 weight_of(const tcl_i8_weight *w) {
   const int32_t kb = blocks_of(w->d_in);
-  return w->W_p ? Mat8{static_cast<const int8_t *>(w->W_p), 0, w->d_out, kb, 1}
-                : Mat8{w->W, w->d_in, w->d_out, kb, 0};
+  return w->W_p ? Mat8{static_cast<const int8_t *>(w->W_p), 0, w->d_out, w->d_in / 16, kb, 1}
+                : Mat8{w->W, w->d_in, w->d_out, w->d_in / 16, kb, 0};
 }
 
 int launch_product(const tcl_i8_weight *w, const Mat8 &x, const float *scale, void *y, int64_t ldy,
@@ -848,8 +830,8 @@ extern "C" int tcl_i8_product(const tcl_i8_weight *w, const int8_t *q, int64_t l
   if (misaligned(q, 16) || ldq % 16)
     return fail(TCL_EALIGN, "i8: q must be 16-byte aligned, ldq a multiple of 16");
   if (misaligned(scale, 4)) return fail(TCL_EALIGN, "i8: scale must be 4-byte aligned");
-  return launch_product(w, Mat8{q, ldq, n_tokens, blocks_of(w->d_in), 0}, scale, y, ldy, yd,
-                        static_cast<hipStream_t>(stream));
+  return launch_product(w, Mat8{q, ldq, n_tokens, w->d_in / 16, blocks_of(w->d_in), 0}, scale, y,
+                        ldy, yd, static_cast<hipStream_t>(stream));
 }
 
 extern "C" int tcl_i8_pack_bytes(const tcl_i8_weight *w, size_t *bytes) {
@@ -904,5 +886,6 @@ extern "C" int tcl_i8_linear(const tcl_i8_weight *w, const void *x, int64_t ldx,
   float *scale = reinterpret_cast<float *>(q + ws_q_bytes(w, n_tokens));
   hipStream_t s = static_cast<hipStream_t>(stream);
   if ((rc = launch_quant(x, ldx, xd, n_tokens, w->d_in, q, 0, true, scale, s))) return rc;
-  return launch_product(w, Mat8{q, 0, n_tokens, blocks_of(w->d_in), 1}, scale, y, ldy, yd, s);
+  return launch_product(w, Mat8{q, 0, n_tokens, w->d_in / 16, blocks_of(w->d_in), 1}, scale, y, ldy,
+                        yd, s);
 }

@@ -348,3 +348,18 @@ def test_two_calls_at_once():
 def test_quant_by_rows_of_every_length(T, d, dtype):
     """Each number of waves a row, rows beyond what they keep, odd row counts."""
     test_quant_is_the_definition(T, d, dtype)
+
+
+@pytest.mark.parametrize("T", [1, 2, 20, 40, 300, 2100])
+@pytest.mark.parametrize("d_in", [16, 32, 48])
+def test_rows_shorter_than_a_block(T, d_in):
+    """Operands in plain rows, whose lanes past the row's end find no block of
+    their own, in every kernel."""
+    d_out = 8200 if T == 2100 else 264
+    W, ws = weight(14, d_out, d_in, full=True)
+    x = acts(8, T, d_in, torch.bfloat16)
+    n, s = quant64(x)
+    w = tclora.I8Weight(W, ws, pack=False)
+    want = product64(W, ws, n, s)
+    close(tclora.i8_linear(w, x, y_dtype=torch.float32), want, torch.float32)
+    close(tclora.i8_product(w, n.to(DEV), s.to(DEV), y_dtype=torch.float32), want, torch.float32)
