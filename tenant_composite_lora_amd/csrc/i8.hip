@@ -80,8 +80,11 @@ __device__ inline uint32_t absmax16(const R &c, uint32_t m) {
 
 // rint(v / s) of the real quotient.  The fp32 quotient is correctly rounded,
 // so it leaves a tie's wrong side only by landing on the tie itself; there
-// the remainder v - t * s, exact by fma, tells the side.
+// the remainder v - t * s, exact by fma, tells the side.  For scales below
+// 2^-125 that remainder may be half the smallest number and round to zero, so
+// small v and s are both raised by a power of two first, which is exact.
 __device__ inline float round_quotient(float v, float s) {
+  if (s < 0x1p-100f) v *= 0x1p64f, s *= 0x1p64f;
   const float t = v / s;
   float n = rintf(t);
   const float d = t - n;

@@ -363,3 +363,34 @@ def test_rows_shorter_than_a_block(T, d_in):
     want = product64(W, ws, n, s)
     close(tclora.i8_linear(w, x, y_dtype=torch.float32), want, torch.float32)
     close(tclora.i8_product(w, n.to(DEV), s.to(DEV), y_dtype=torch.float32), want, torch.float32)
+
+
+@pytest.mark.parametrize("d", [128, 4096])
+def test_quant_next_to_ties_at_small_scales(d):
+    """Scales around and below the smallest normal number: the quotients
+    nearest to every tie, on it and a step of fp32 to either side."""
+    r = np.random.default_rng(15)
+    rows = []
+    for lo, hi in ((-149, -140), (-140, -132), (-132, -126), (-126, -125), (-125, -99)):
+        for _ in range(40):
+            top = np.float32(127 * 2.0 ** r.uniform(lo, hi))
+            s = np.float32(np.float64(top) / 127)
+            v = (np.float64(s) * (r.integers(0, 127, d - 1) + 0.5)).astype(np.float32)
+            v = np.where(r.random(d - 1) < 0.5, np.nextafter(v, np.float32(1)), v)
+            v = np.where(r.random(d - 1) < 0.5, np.nextafter(v, np.float32(0)), v)
+            v = np.minimum(v, top) * r.choice([-1, 1], d - 1).astype(np.float32)
+            rows.append(np.concatenate([[top], v]).astype(np.float32))
+    rows.append(np.zeros(d, np.float32))
+    rows[-1][:2] = 2.5094301558894677e-38, 2.1636421034566686e-38
+    x = torch.from_numpy(np.stack(rows)).to(DEV)
+    q, s = tclora.i8_quant(x)
+    # (the real quotient: an fp64 division rounds the neighbours of some ties)
+    want = (x.double().cpu().abs().amax(1) / 127).float()
+    assert torch.equal(s.cpu().view(torch.int32), want.view(torch.int32))
+    xi = (x.cpu().numpy().astype(np.float64) * 2.0 ** 149).astype(np.int64)
+    si = (want.numpy().astype(np.float64) * 2.0 ** 149).astype(np.int64)[:, None]
+    a = np.abs(xi)
+    n, rem = a // np.maximum(si, 1), a % np.maximum(si, 1)
+    n = n + ((2 * rem > si) | ((2 * rem == si) & (n % 2 == 1)))
+    n = np.where(si > 0, np.sign(xi) * np.minimum(n, 127), 0)
+    assert np.array_equal(q.cpu().numpy().astype(np.int64), n)
