@@ -795,22 +795,16 @@ def _made_for(dev: torch.device, stream) -> None:
             s.wait_stream(current)
 
 
-def _call(dev: torch.device, fn, args, stream, *own, home: Optional[int] = None) -> None:
-    """fn(*args, stream) with ``dev`` the current device.  Tensors that the
-    library's own objects made (``own``) are kept for a stream other than the
-    one they were allocated on: one that is given, or a current one that is
-    not ``home``."""
+def _call(dev: torch.device, fn, args, stream, *own) -> None:
+    """fn(*args, stream) with ``dev`` the current device.  ``own``: tensors
+    that the library's own objects made, each with the stream it was allocated
+    on; one that the call uses on another stream, given or current, is kept
+    until the work there has run."""
     i = dev.index
-    if stream is None:
-        st = torch._C._cuda_getCurrentRawStream(i)
-        keep = home is not None and st != home
-    else:
-        st = _stream(dev, stream)
-        keep = True
-    if keep:
-        s = _stream_object(dev, stream)
-        for t in own:
-            t.record_stream(s)
+    st = torch._C._cuda_getCurrentRawStream(i) if stream is None else _stream(dev, stream)
+    for t, home in own:
+        if st != home:
+            t.record_stream(_stream_object(dev, stream))
     if torch._C._cuda_getDevice() == i:
         rc = fn(*args, st)
     else:
@@ -842,14 +836,19 @@ class I8Weight:
         self.d_out, self.d_in = W.shape
         self.desc = I8WeightDesc(self.d_in, self.d_out, W.data_ptr(), scale.data_ptr(), None)
         self.W_p = None
+        self.home = _stream(W.device) if W.is_cuda else 0
         if pack and W.numel():
             n = ctypes.c_size_t(0)
             check(lib().tcl_i8_pack_bytes(ctypes.byref(self.desc), ctypes.byref(n)))
             self.W_p = torch.empty(n.value, dtype=torch.uint8, device=W.device)
             _made_for(W.device, stream)
             _call(W.device, lib().tcl_i8_pack,
-                  (ctypes.byref(self.desc), self.W_p.data_ptr(), n.value), stream, self.W_p, W)
+                  (ctypes.byref(self.desc), self.W_p.data_ptr(), n.value), stream,
+                  *((t, self.home) for t in (self.W_p, W)))
             self.W, self.desc.W = None, None
+
+    def _own(self):
+        return () if self.W_p is None else ((self.W_p, self.home),)
 
 
 def i8_quant(x: torch.Tensor, q: Optional[torch.Tensor] = None,
@@ -873,7 +872,7 @@ def i8_quant(x: torch.Tensor, q: Optional[torch.Tensor] = None,
         _made_for(x.device, stream)
     _call(x.device, lib().tcl_i8_quant,
           (x.data_ptr(), ldx, _dtype_code(x.dtype), T, d, q.data_ptr(), ldq, scale.data_ptr()),
-          stream, *own)
+          stream, *((t, _stream(x.device)) for t in own))
     return q, scale
 
 
@@ -894,11 +893,9 @@ def i8_product(w: I8Weight, q: torch.Tensor, scale: torch.Tensor,
     _same_device("i8_product", q.device, scale, y, w.scale)
     if own:
         _made_for(q.device, stream)
-    if w.W_p is not None:
-        own.append(w.W_p)
     _call(q.device, lib().tcl_i8_product,
           (ctypes.byref(w.desc), q.data_ptr(), ldq, scale.data_ptr(), T, y.data_ptr(), ldy,
-           _dtype_code(y.dtype)), stream, *own)
+           _dtype_code(y.dtype)), stream, *((t, _stream(q.device)) for t in own), *w._own())
     return y
 
 
@@ -920,15 +917,14 @@ class I8Call:
         if ws is None or ws.numel() * ws.element_size() < need.value:
             ws = torch.empty(max(need.value, 256), dtype=torch.uint8, device=x.device)
         self.ws, self.device = ws, x.device
-        self._own = (ws,) if w.W_p is None else (ws, w.W_p)
-        self._home = _stream(x.device)
+        self._own = ((ws, _stream(x.device)), *w._own())
         self._fn = lib().tcl_i8_linear
         self._args = _packed(self._fn, (
             ctypes.byref(w.desc), x.data_ptr(), self.ldx, self.xd, T, y.data_ptr(), self.ldy,
             self.yd, ws.data_ptr(), ws.numel() * ws.element_size()))
 
     def __call__(self, stream=None) -> torch.Tensor:
-        _call(self.device, self._fn, self._args, stream, *self._own, home=self._home)
+        _call(self.device, self._fn, self._args, stream, *self._own)
         return self.y
 
 
@@ -1012,6 +1008,7 @@ class AppendCall:
         self.cache, self.rope, self.k, self.v, self.q = cache, rope, k, v, q
         self.pos, self.slot, self.q_out, self.T = pos, slot, q_out, T
         self.xd, self.device = _dtype_code(k.dtype), cache.device
+        self._own = () if q_out is None else ((q_out, _stream(self.device)),)
         self._fn = lib().tcl_kv_append
         self._args = _packed(self._fn, (
             ctypes.byref(cache.desc), ctypes.byref(rope.desc), k.data_ptr(), self.ldk,
@@ -1019,8 +1016,7 @@ class AppendCall:
             pos.data_ptr(), slot.data_ptr()))
 
     def __call__(self, stream=None) -> Optional[torch.Tensor]:
-        _call(self.device, self._fn, self._args, stream,
-              *(() if self.q_out is None else (self.q_out,)))
+        _call(self.device, self._fn, self._args, stream, *self._own)
         return self.q_out
 
 
@@ -1082,7 +1078,7 @@ class AttnPlan:
     def _map(self, stream):
         _call(self.device, lib().tcl_attn_plan,
               (ctypes.byref(self.batch), ctypes.byref(self.cache.desc), self.n_q_heads,
-               self.buf.data_ptr(), self.buf.numel()), stream, self.buf)
+               self.buf.data_ptr(), self.buf.numel()), stream, (self.buf, self.home))
 
     def remap(self, seq_tok_ptr, group_seq_ptr, prefix_len, prefix_pages, own_len, own_pages,
               stream=None) -> None:
@@ -1106,7 +1102,7 @@ class AttnPlan:
         if own:
             _made_for(self.device, stream)
         _call(self.device, lib().tcl_attn_status_async, (self.buf.data_ptr(), out.data_ptr()),
-              stream, self.buf, *([out] if own else []))
+              stream, (self.buf, self.home), *([(out, _stream(self.device))] if own else []))
         return out
 
     def status(self, stream=None) -> int:
@@ -1145,7 +1141,8 @@ class AttnCall:
         if ws is None or ws.numel() * ws.element_size() < plan.workspace_bytes:
             ws = torch.empty(max(plan.workspace_bytes, 256), dtype=torch.uint8, device=plan.device)
         self.ws = ws
-        self._home = _stream(plan.device)
+        home = _stream(plan.device)
+        self._own = ((ws, home), (o, home), (plan.buf, plan.home))
         self._fn = lib().tcl_attn_apply
         self._args = _packed(self._fn, (
             None, ctypes.byref(cache.desc), plan.n_q_heads, plan.buf.data_ptr(), plan.buf.numel(),
@@ -1154,8 +1151,7 @@ class AttnCall:
 
     def __call__(self, stream=None) -> torch.Tensor:
         p = self.plan  # (the batch's tables are the plan's last ones)
-        _call(p.device, self._fn, (p.batch_ref, *self._args), stream, self.ws, self.o, p.buf,
-              home=self._home if self._home == p.home else -1)
+        _call(p.device, self._fn, (p.batch_ref, *self._args), stream, *self._own)
         return self.o
 
 
