@@ -795,13 +795,48 @@ def _made_for(dev: torch.device, stream) -> None:
             s.wait_stream(current)
 
 
-def _call(dev: torch.device, fn, args, stream, *own) -> None:
+class _Made:
+    """When an object made its tensors: their memory may have been freed with
+    work of the stream of that time still to run on it, so the object's first
+    call on another stream waits for what that stream held then.
+
+    An event from before a capture cannot be waited for in it, nor one from a
+    capture behind it: a captured call waits only where its object was made in
+    the same capture (torch.cuda.graph waits for all earlier work itself).
+    Objects that are called once, on the stream that they are made on, need
+    none (_once)."""
+
+    def __init__(self, dev: torch.device):
+        with torch.cuda.device(dev):
+            self.stream = torch.cuda.current_stream(dev)
+            captured = torch.cuda.is_current_stream_capturing()
+            self.event = None if captured else self.stream.record_event()
+        self.waited = {int(self.stream.cuda_stream)}
+
+    def before(self, s: torch.cuda.Stream) -> None:
+        with torch.cuda.stream(s):
+            captured = torch.cuda.is_current_stream_capturing()
+        if self.event is not None:
+            if not captured:
+                s.wait_event(self.event)
+                self.waited.add(int(s.cuda_stream))
+        elif captured:
+            with torch.cuda.stream(self.stream):
+                captured = torch.cuda.is_current_stream_capturing()
+            if captured:
+                s.wait_stream(self.stream)
+
+
+def _call(dev: torch.device, fn, args, stream, *own, made: Optional[_Made] = None) -> None:
     """fn(*args, stream) with ``dev`` the current device.  ``own``: tensors
     that the library's own objects made, each with the stream it was allocated
     on; one that the call uses on another stream, given or current, is kept
-    until the work there has run."""
+    until the work there has run.  ``made``: when the call's object made its
+    own, which may have been just before."""
     i = dev.index
     st = torch._C._cuda_getCurrentRawStream(i) if stream is None else _stream(dev, stream)
+    if made is not None and st not in made.waited:
+        made.before(_stream_object(dev, stream))
     for t, home in own:
         if st != home:
             t.record_stream(_stream_object(dev, stream))
@@ -905,7 +940,7 @@ class I8Call:
     (or ``ws``); calls that may run at the same time need one each."""
 
     def __init__(self, w: I8Weight, x: torch.Tensor, y: torch.Tensor,
-                 ws: Optional[torch.Tensor] = None):
+                 ws: Optional[torch.Tensor] = None, *, _once: bool = False):
         T = x.shape[0]
         self.ldx = _rows("I8Call: x", x, T, w.d_in)
         self.ldy = _rows("I8Call: y", y, T, w.d_out)
@@ -914,8 +949,10 @@ class I8Call:
         self.xd, self.yd = _dtype_code(x.dtype), _dtype_code(y.dtype)
         need = ctypes.c_size_t(0)
         check(lib().tcl_i8_workspace_bytes(ctypes.byref(w.desc), T, ctypes.byref(need)))
+        self._made = None
         if ws is None or ws.numel() * ws.element_size() < need.value:
             ws = torch.empty(max(need.value, 256), dtype=torch.uint8, device=x.device)
+            self._made = None if _once else _Made(x.device)
         self.ws, self.device = ws, x.device
         self._own = ((ws, _stream(x.device)), *w._own())
         self._fn = lib().tcl_i8_linear
@@ -924,7 +961,7 @@ class I8Call:
             self.yd, ws.data_ptr(), ws.numel() * ws.element_size()))
 
     def __call__(self, stream=None) -> torch.Tensor:
-        _call(self.device, self._fn, self._args, stream, *self._own)
+        _call(self.device, self._fn, self._args, stream, *self._own, made=self._made)
         return self.y
 
 
@@ -935,9 +972,7 @@ def i8_linear(w: I8Weight, x: torch.Tensor, y: Optional[torch.Tensor] = None,
         y = torch.empty(x.shape[0], w.d_out, dtype=y_dtype, device=x.device)
         if stream is not None and x.is_cuda:
             y.record_stream(_stream_object(x.device, stream))
-    call = I8Call(w, x, y)
-    _made_for(x.device, stream)
-    return call(stream)
+    return I8Call(w, x, y, _once=stream is None)(stream)
 
 
 class KVCache:
@@ -982,7 +1017,8 @@ class AppendCall:
 
     def __init__(self, cache: KVCache, k: torch.Tensor, v: torch.Tensor, pos: torch.Tensor,
                  slot: torch.Tensor, rope: Optional[Rope] = None,
-                 q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None):
+                 q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None, *,
+                 _once: bool = False):
         T, row = k.shape[0], cache.n_kv_heads * cache.head_dim
         self.ldk = _rows("AppendCall: k", k, T, row)
         self.ldv = _rows("AppendCall: v", v, T, row)
@@ -992,6 +1028,7 @@ class AppendCall:
         _vector("AppendCall: slot", slot, T, torch.int64)
         rope = rope or Rope(None)
         self.Hq, self.ldq, self.ldqo = 0, 0, 0
+        self._made = None
         if q is not None:
             self.ldq = _rows("AppendCall: q", q, T)
             if q.shape[1] % cache.head_dim:
@@ -999,6 +1036,7 @@ class AppendCall:
             self.Hq = q.shape[1] // cache.head_dim
             if q_out is None:
                 q_out = torch.empty(T, q.shape[1], dtype=torch.bfloat16, device=k.device)
+                self._made = _Made(k.device) if k.is_cuda and not _once else None
             if q_out.dtype != torch.bfloat16:
                 raise TypeError("AppendCall: q_out must be bfloat16")
             self.ldqo = _rows("AppendCall: q_out", q_out, T, q.shape[1])
@@ -1016,7 +1054,7 @@ class AppendCall:
             pos.data_ptr(), slot.data_ptr()))
 
     def __call__(self, stream=None) -> Optional[torch.Tensor]:
-        _call(self.device, self._fn, self._args, stream, *self._own)
+        _call(self.device, self._fn, self._args, stream, *self._own, made=self._made)
         return self.q_out
 
 
@@ -1024,10 +1062,7 @@ def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, pos: torch.Tenso
               slot: torch.Tensor, rope: Optional[Rope] = None, q: Optional[torch.Tensor] = None,
               q_out: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
     """tcl_kv_append; returns the rotated queries (None without q)."""
-    call = AppendCall(cache, k, v, pos, slot, rope, q, q_out)
-    if call.q_out is not None and q_out is None:
-        _made_for(call.device, stream)
-    return call(stream)
+    return AppendCall(cache, k, v, pos, slot, rope, q, q_out, _once=stream is None)(stream)
 
 
 class AttnPlan:
@@ -1121,12 +1156,14 @@ class AttnCall:
 
     def __init__(self, plan: AttnPlan, q: torch.Tensor, o: Optional[torch.Tensor] = None,
                  lse: Optional[torch.Tensor] = None, scale: Optional[float] = None,
-                 cache: Optional[KVCache] = None, ws: Optional[torch.Tensor] = None):
+                 cache: Optional[KVCache] = None, ws: Optional[torch.Tensor] = None, *,
+                 _once: bool = False):
         cache = cache or plan.cache
         if any(getattr(cache, f) != getattr(plan.cache, f)
                for f in ("n_pages", "page_size", "n_kv_heads", "head_dim")):
             raise ValueError("AttnCall: the cache's sizes are not the plan's")
         T, row = plan.n_tokens, plan.n_q_heads * cache.head_dim
+        made = o is None
         if o is None:
             o = torch.empty(T, row, dtype=torch.bfloat16, device=q.device)
         if q.dtype != torch.bfloat16 or o.dtype != torch.bfloat16:
@@ -1140,7 +1177,9 @@ class AttnCall:
         self.scale = cache.head_dim ** -0.5 if scale is None else float(scale)
         if ws is None or ws.numel() * ws.element_size() < plan.workspace_bytes:
             ws = torch.empty(max(plan.workspace_bytes, 256), dtype=torch.uint8, device=plan.device)
+            made = True
         self.ws = ws
+        self._made = _Made(plan.device) if made and not _once else None
         home = _stream(plan.device)
         self._own = ((ws, home), (o, home), (plan.buf, plan.home))
         self._fn = lib().tcl_attn_apply
@@ -1151,7 +1190,7 @@ class AttnCall:
 
     def __call__(self, stream=None) -> torch.Tensor:
         p = self.plan  # (the batch's tables are the plan's last ones)
-        _call(p.device, self._fn, (p.batch_ref, *self._args), stream, *self._own)
+        _call(p.device, self._fn, (p.batch_ref, *self._args), stream, *self._own, made=self._made)
         return self.o
 
 
@@ -1159,6 +1198,4 @@ def attention(plan: AttnPlan, q: torch.Tensor, o: Optional[torch.Tensor] = None,
               lse: Optional[torch.Tensor] = None, scale: Optional[float] = None,
               cache: Optional[KVCache] = None, stream=None) -> torch.Tensor:
     """tcl_attn_apply: attention of the plan's batch over the cache."""
-    call = AttnCall(plan, q, o, lse, scale, cache)
-    _made_for(plan.device, stream)
-    return call(stream)
+    return AttnCall(plan, q, o, lse, scale, cache, _once=stream is None)(stream)

@@ -120,3 +120,130 @@ def test_attention_made_on_one_stream_over_a_plan_of_another(side):
     assert not handed_out(side, n, at)
     torch.cuda.synchronize()
     assert torch.equal(o, want)
+
+
+class Freed:
+    """Memory of n bytes, freed on the current stream with a copy of it still
+    to be made there; whatever owns it next has to leave it until then."""
+
+    def __init__(self, n):
+        old = torch.full((n,), 3, dtype=torch.uint8, device=DEV)
+        self.at = old.data_ptr()
+        torch.cuda._sleep(SLEEP)
+        self.copy = old.clone()
+
+    def left_alone(self):
+        torch.cuda.synchronize()
+        return bool((self.copy == 3).all())
+
+
+@pytest.mark.parametrize("how", ["given", "raw", "current"])
+def test_calls_made_over_memory_that_is_still_read(how, side):
+    """Calls whose own tensors lie in such memory, their first run on another
+    stream that nothing else orders behind it."""
+    def go(call):
+        if how == "current":
+            with torch.cuda.stream(side):
+                call()
+        else:
+            call(side.cuda_stream if how == "raw" else side)
+
+    W, ws = weight(60, 256, 4096)
+    w = tclora.I8Weight(W, ws)
+    x = acts(60, 512, 4096, torch.bfloat16)
+    want = tclora.i8_linear(w, x)
+    y = torch.zeros_like(want)
+    n = tclora.I8Call(w, x, y).ws.numel()
+    torch.cuda.synchronize()
+    f = Freed(n)
+    call = tclora.I8Call(w, x, y)
+    assert call.ws.data_ptr() == f.at
+    go(call)
+    assert f.left_alone() and torch.equal(y, want)
+
+    cache = tclora.KVCache(*(torch.zeros(40, 16, 2, 64, dtype=torch.bfloat16, device=DEV) for _ in range(2)))
+    q, k = (torch.randn(512, h * 64, device=DEV).to(torch.bfloat16) for h in (64, 2))
+    pos = torch.arange(512, dtype=torch.int32, device=DEV)
+    rope = tclora.Rope(torch.ones(32, device=DEV))
+    want = tclora.kv_append(cache, k, k, pos, pos.long(), rope, q=q)
+    slot = pos.long()
+    torch.cuda.synchronize()
+    f = Freed(q.numel() * 2)
+    call = tclora.AppendCall(cache, k, k, pos, slot, rope, q=q)
+    assert call.q_out.data_ptr() == f.at
+    go(call)
+    assert f.left_alone() and torch.equal(call.q_out, want)
+
+    b = Batch(61, [(300, [(1, 90), (1, 70), (40, 100)])], 64, 8, 64, 32)
+    plan = b.plan()
+    want = tclora.attention(plan, b.qd)
+    o = torch.zeros_like(want)
+    torch.cuda.synchronize()
+    f = Freed(plan.workspace_bytes)
+    call = tclora.AttnCall(plan, b.qd, o=o)
+    assert call.ws.data_ptr() == f.at
+    go(call)
+    assert f.left_alone() and torch.equal(o, want)
+    f = Freed(want.numel() * 2)
+    call = tclora.AttnCall(plan, b.qd, ws=call.ws)
+    assert call.o.data_ptr() == f.at
+    go(call)
+    assert f.left_alone() and torch.equal(call.o, want)
+
+
+def test_a_call_made_and_forked_inside_a_capture(side):
+    """Made in the capture, run on a stream forked from it before: the replay
+    runs it behind what the capture had put into the same memory."""
+    W, ws = weight(62, 256, 4096)
+    w = tclora.I8Weight(W, ws)
+    x = acts(62, 512, 4096, torch.bfloat16)
+    want = tclora.i8_linear(w, x)
+    y = torch.zeros_like(want)
+    n = tclora.I8Call(w, x, y).ws.numel()
+    src = torch.full((n,), 3, dtype=torch.uint8, device=DEV)
+    kept = torch.zeros_like(src)
+    fork = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        fork.wait_stream(side)
+        old = src.clone()
+        kept.copy_(old)
+        at = old.data_ptr()
+        del old
+        call = tclora.I8Call(w, x, y)
+        same = call.ws.data_ptr() == at
+        call(fork)
+        side.wait_stream(fork)
+    assert same
+    for _ in range(4):
+        y.zero_(), kept.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want) and bool((kept == 3).all())
+
+
+def test_calls_made_before_a_capture(side):
+    """Captured on streams other than their own, forked ones among them."""
+    W, ws = weight(63, 264, 1040)
+    w = tclora.I8Weight(W, ws)
+    x = acts(63, 40, 1040, torch.bfloat16)
+    want = tclora.i8_linear(w, x)
+    ys = [torch.zeros_like(want) for _ in range(2)]
+    calls = [tclora.I8Call(w, x, y) for y in ys]
+    fork = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        fork.wait_stream(side)
+        calls[0]()
+        calls[1](fork)
+        side.wait_stream(fork)
+    for _ in range(3):
+        for y in ys:
+            y.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(y, want) for y in ys)
+    calls[1](fork)  # eager, on the stream of the capture
+    torch.cuda.synchronize()
+    assert torch.equal(ys[1], want)
