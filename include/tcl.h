@@ -778,7 +778,8 @@ int tcl_attn_status_async(const void *plan, int32_t *dev_status, void *stream);
  * bf16 [n_tokens][ldq / ldo], n_q_heads heads of head_dim a row; lse (may be
  * NULL): device fp32 [n_tokens][n_q_heads], the natural logarithm of the sum
  * of exp(scale * q . k).  A token that sees no key gets o = 0 and lse =
- * -infinity.  Rows of tokens that no request owns are left as they were.
+ * -infinity; one whose scores are all -infinity gets NaN and the same lse.
+ * Rows of tokens that no request owns are left as they were.
  * Keys and values a token does not see do not reach its row, whatever they
  * hold.  The batch and cache sizes are those of the plan (a plan of others:
  * nothing is written); q and o may be the same rows.  ws: device workspace of

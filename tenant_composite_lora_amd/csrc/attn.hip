@@ -662,6 +662,13 @@ __device__ inline int token_of(const AttnArgs &a, const Work &t, int gq, int r) 
   return t.list ? a.list[i] : i;
 }
 
+// What a row's sums are multiplied by at the end.  Without any weight a row
+// that sees no key is zero; one that sees keys, all with a score of -infinity,
+// has no softmax and is NaN.
+__device__ inline float over_sum(float l, int vis) {
+  return l > 0.f || l != l ? 1.f / l : (vis > 0 ? NAN : 0.f);
+}
+
 __device__ inline float log_sum(float m, float l) {
   return (m + __log2f(l)) * 0.69314718055994531f;
 }
@@ -821,7 +828,7 @@ __device__ inline void attend_few(const AttnArgs &a, const Work &t, int h, int g
     }
     const int tk = token_of(a, t, gq, r), hh = h * gq + r % gq;
     if (t.part < 0) {
-      put4(a.o + tk * a.ldo + int64_t(hh) * D + d, v, L > 0.f || L != L ? 1.f / L : 0.f);
+      put4(a.o + tk * a.ldo + int64_t(hh) * D + d, v, over_sum(L, L == 0.f ? a.tok[tk].vis : 0));
       if (a.lse && d == 0) a.lse[int64_t(tk) * a.Hq + hh] = log_sum(M, L);
     } else {
       const int64_t pr = int64_t(t.part + r) * a.c.H + h;
@@ -1146,7 +1153,7 @@ __device__ inline void attend_many(const AttnArgs &a, const Work &t, int h, int 
   }
   if (!live) return;
   l += __shfl_xor(l, 32, 64);
-  const float f = t.part >= 0 ? 1.f : (l > 0.f || l != l ? 1.f / l : 0.f);
+  const float f = t.part >= 0 ? 1.f : over_sum(l, vis);
   const int64_t pr = int64_t(t.part + r) * a.c.H + h;
 #pragma unroll
   for (int i = 0; i < D / 32; ++i)
@@ -1239,7 +1246,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
       for (; k + 2 <= n[s]; k += 2) add(std::integral_constant<int, 2>{}, k);
       if (k < n[s]) add(std::integral_constant<int, 1>{}, k);
     }
-    const float f = L > 0.f || L != L ? 1.f / L : 0.f;
+    const float f = over_sum(L, r.vis);
 #pragma unroll
     for (int e = 0; e < E; ++e)
       a.o[tk * a.ldo + int64_t(hh) * D + lane * E + e] = f32_to_bf16(v[e] * f);

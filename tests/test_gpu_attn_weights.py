@@ -37,3 +37,46 @@ def test_a_short_requests_accuracy_does_not_depend_on_its_batch(name, groups, Hq
     wo, tol = tight(b)
     got = tclora.attention(b.plan(), b.qd).double().cpu().view(wo.shape)
     assert float(((got - wo).abs() - tol).max()) <= 1e-30
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,page", [(8, 2, 64, 16), (4, 1, 128, 32), (3, 1, 256, 8)])
+def test_rows_whose_scores_are_all_minus_infinity(Hq, Hkv, D, page):
+    """Their softmax is NaN (as of any row of -infinity); rows beside them
+    that see another key, or none, are as ever.  Rows of one item, of few and
+    of many rows, and rows joined from several."""
+    groups = [
+        (0, [(1, 9), (1, 40), (70, 70), (70, 60), (3, 0)]),   # no prefix: written at once
+        (130, [(1, 20), (1, 30), (5, 40), (90, 100)]),        # joined with the prefix's
+        (900, [(1, 5), (2, 30), (1, 0)]),
+    ]
+    b = Batch(70 + D, groups, Hq, Hkv, D, page)
+    b.q.view(b.T, Hq, D)[..., 0] = 1.0
+    low = -float("inf")
+    hide = {0: (0, 9), 2: (0, 70), 3: (0, 30), 5: (0, 20), 7: (0, 38), 9: (0, 5)}
+    for pages, n in [(b.prefix_pages[1], 130), (b.prefix_pages[2], 900)] + [
+            (b.own_pages[s], hi) for s, (_, hi) in hide.items()]:
+        for j in range(n):
+            b.Kh[int(pages[j // page]), j % page, :, 0] = low
+    b.up(b.Kh, b.Vh)
+    lse = torch.zeros(b.T, Hq, device=DEV)
+    o = tclora.attention(b.plan(), b.qd, lse=lse).double().cpu().view(b.T, Hq, D)
+    wo, wl, _ = b.want()
+    assert torch.equal(torch.isnan(o), torch.isnan(wo))
+    nan = torch.isnan(wo).all(-1)
+    assert 0.2 < float(nan.double().mean()) < 0.8
+    assert torch.equal(torch.isinf(lse.cpu()), torch.isinf(wl)) and bool((lse.cpu()[nan] == low).all())
+    none = torch.zeros(b.T, dtype=torch.bool)
+    for s, (q, n) in enumerate(b.seqs):
+        p = groups[0 if s < 5 else 1 if s < 9 else 2][0]
+        none[int(b.seq_tok[s]):int(b.seq_tok[s]) + max(0, q - p - n)] = True
+    assert int(none.sum()) == 13 and not o[none].any() and bool((lse.cpu()[none] == low).all())
+    # finite rows: as ever, with sum |q k| * scale of the finite scores at most
+    # D * D^-0.5 * max |q| * max |K|
+    ok = ~nan & ~none[:, None]
+    V, b.Vh = b.Vh, b.Vh.abs()
+    A, _, _ = b.want()
+    b.Vh = V
+    K0 = torch.where(torch.isinf(b.Kh.float()), 0.0, b.Kh.float().abs()).amax()
+    E = (D + 2) * 2.0 ** -24 * D ** 0.5 * float(K0) * float(b.q.float().abs().max())
+    tol = (2 * E + 2.0 ** -19 + HALF) * A + HALF * wo.abs()
+    assert float(((o - wo).abs() - tol)[ok].max()) <= 1e-30
