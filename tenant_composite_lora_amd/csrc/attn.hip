@@ -16,6 +16,7 @@
 // product in the very registers the second wants them in.
 #include <algorithm>
 #include <cmath>
+#include <limits>
 #include <type_traits>
 
 #include "kern_common.hpp"
@@ -1446,8 +1447,10 @@ extern "C" int tcl_attn_apply(const tcl_attn_batch *b, const tcl_kv_cache *c, in
   const char *p = static_cast<const char *>(plan);
   a.q = static_cast<const uint16_t *>(q), a.o = static_cast<uint16_t *>(o), a.lse = lse;
   a.ldq = ldq, a.ldo = ldo;
-  // (never zero: a hidden key's -infinity times zero would be a NaN)
-  a.scale2 = std::fmax(std::fabs(scale) * 1.44269504088896341f, 1e-37f);
+  // (never zero: a hidden key's -infinity times zero would be a NaN; the
+  // smallest number there is, so that no finite score shows it)
+  a.scale2 = std::fmax(std::fabs(scale) * 1.44269504088896341f,
+                       std::numeric_limits<float>::denorm_min());
   a.q_sign = scale < 0 ? 0x8000 : 0;
   a.S = b->n_seqs, a.G = b->n_groups, a.T = b->n_tokens, a.ldp = b->ld_prefix;
   a.ld_own = b->ld_own, a.Hq = n_q_heads;

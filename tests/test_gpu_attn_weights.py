@@ -80,3 +80,26 @@ def test_rows_whose_scores_are_all_minus_infinity(Hq, Hkv, D, page):
     E = (D + 2) * 2.0 ** -24 * D ** 0.5 * float(K0) * float(b.q.float().abs().max())
     tol = (2 * E + 2.0 ** -19 + HALF) * A + HALF * wo.abs()
     assert float(((o - wo).abs() - tol)[ok].max()) <= 1e-30
+
+
+@pytest.mark.parametrize("scale", [0.0, 1e-45, -1e-40, 1e-38])
+def test_scales_near_zero_and_large_scores(scale):
+    """A scale of zero weighs every key alike, however large its score: the
+    smallest one in use must not make a difference of it.  (Scores up to
+    1e38 here.)"""
+    b = Batch(80, [(150, [(1, 40), (1, 70), (20, 30), (90, 100)])], 4, 2, 64, 16)
+    b.q.mul_(2.0 ** 60)
+    b.Kh.mul_(2.0 ** 60)
+    b.up(b.Kh, b.Vh)
+    o = tclora.attention(b.plan(), b.qd, scale=scale).double().cpu().view(b.T, 4, 64)
+    wo, _, _ = b.want(scale)
+    V, b.Vh = b.Vh, b.Vh.abs()
+    A, _, _ = b.want(scale)
+    b.Vh = V
+    # a score times the scale is off by what the scale loses in fp32, in the
+    # call and times log2(e) (half of the smallest number each; all of it for
+    # zero), and by 66 roundings of the sum, 64 * 2^120 * 32 at most in magnitude
+    top = 2.0 ** 131
+    E = top * (2.0 ** -149 + 66 * 2.0 ** -24 * abs(scale)) + 2.0 ** -20
+    tol = (2 * E + 2.0 ** -19 + HALF) * A + HALF * wo.abs()
+    assert float(((o - wo).abs() - tol).max()) <= 1e-30
