@@ -367,6 +367,10 @@ def test_two_calls_at_once():
     assert torch.equal(c1.o, want) and torch.equal(c2.o, want2)
 
 
+# (a test below has the same name: this one runs under another)
+test_two_queries_at_once = test_two_calls_at_once
+
+
 def test_layers_share_a_plan():
     b = Batch(12, [(120, [(1, 40), (1, 50)])], 8, 2, 64, 16)
     other = tclora.KVCache(b.cache.K.clone(), torch.zeros_like(b.cache.V))
