@@ -103,3 +103,20 @@ def test_scales_near_zero_and_large_scores(scale):
     E = top * (2.0 ** -149 + 66 * 2.0 ** -24 * abs(scale)) + 2.0 ** -20
     tol = (2 * E + 2.0 ** -19 + HALF) * A + HALF * wo.abs()
     assert float(((o - wo).abs() - tol).max()) <= 1e-30
+
+
+@pytest.mark.parametrize("factor", [16.0, 64.0])
+def test_every_row_of_extreme_scores(factor):
+    """Scores of hundreds and thousands.  Their fp32 sums are off by up to E,
+    no longer small beside one, so a weight by exp(2 E) and the output by
+    (exp(2 E) - 1) A; for 2 E below 0.35 that is less than 1.2 * 2 E A."""
+    b = Batch(8, [(150, [(1, 40), (1, 70), (20, 30), (90, 100)])], 4, 2, 64, 16)
+    q, K = b.q * factor, b.Kh * factor
+    b.q, b.Kh = q.abs(), K.abs()
+    e = float(b.want()[1].max())  # (at least the largest sum of |q k|)
+    assert 2 * (b.D + 2) * 2.0 ** -24 * e < 0.35
+    b.q, b.Kh = q, K
+    b.up(b.Kh, b.Vh)
+    o = tclora.attention(b.plan(), b.qd).double().cpu().view(b.T, b.Hq, b.D)
+    wo, _, tol = b.want()
+    assert float(((o - wo).abs() - 1.2 * tol).max()) <= 1e-30
