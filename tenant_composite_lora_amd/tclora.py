@@ -776,6 +776,17 @@ def _vector(what: str, t: torch.Tensor, n: int, dtype: torch.dtype) -> None:
         raise ValueError(f"{what} must be a contiguous {dtype} tensor of {n} entries")
 
 
+def _fits(what: str, ws: Optional[torch.Tensor], need: int) -> bool:
+    """Whether a workspace was given and holds ``need`` bytes.  The calls write
+    it from its first byte on, so its elements have to lie one behind another
+    (an expanded tensor has more of them than memory)."""
+    if ws is None:
+        return False
+    if not ws.is_contiguous():
+        raise ValueError(f"{what}: ws must be contiguous")
+    return ws.numel() * ws.element_size() >= need
+
+
 def _stream_object(dev: torch.device, stream):
     if stream is None:
         return torch.cuda.current_stream(dev)
@@ -950,7 +961,7 @@ class I8Call:
         need = ctypes.c_size_t(0)
         check(lib().tcl_i8_workspace_bytes(ctypes.byref(w.desc), T, ctypes.byref(need)))
         self._made = None
-        if ws is None or ws.numel() * ws.element_size() < need.value:
+        if not _fits("I8Call", ws, need.value):
             ws = torch.empty(max(need.value, 256), dtype=torch.uint8, device=x.device)
             self._made = None if _once else _Made(x.device)
         self.ws, self.device = ws, x.device
@@ -1175,7 +1186,7 @@ class AttnCall:
         _same_device("AttnCall", plan.device, q, o, lse, cache.K, ws)
         self.plan, self.cache, self.q, self.o, self.lse = plan, cache, q, o, lse
         self.scale = cache.head_dim ** -0.5 if scale is None else float(scale)
-        if ws is None or ws.numel() * ws.element_size() < plan.workspace_bytes:
+        if not _fits("AttnCall", ws, plan.workspace_bytes):
             ws = torch.empty(max(plan.workspace_bytes, 256), dtype=torch.uint8, device=plan.device)
             made = True
         self.ws = ws

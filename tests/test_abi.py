@@ -530,3 +530,15 @@ def test_launch_sizes_are_refused_on_the_host(L):
     w, c = ctypes.byref(tclora.AttnBatch(3, 2, 5, 4, 4, P, P, P, P, P, P)), ctypes.byref(c)
     assert L.tcl_attn_apply(w, c, 4, 0x10000, 1 << 40, P, 256, P, 256, None, 3e38, 0x20000, 1 << 40,
                             None) == tclora.EINVAL
+
+
+def test_workspaces_of_the_base_operators_are_whole():
+    """A given workspace counts by its bytes and has to be contiguous: what is
+    expanded or strided does not hold what it counts (no GPU)."""
+    import torch
+    ws = torch.empty(1024, dtype=torch.uint8)
+    assert tclora._fits("x", ws, 1024) and not tclora._fits("x", ws, 1025)
+    assert tclora._fits("x", ws.view(torch.float32), 1024) and not tclora._fits("x", None, 0)
+    for bad in (torch.empty(1, dtype=torch.uint8).expand(1 << 20), ws[::2], ws.view(32, 32).t()):
+        with pytest.raises(ValueError):
+            tclora._fits("x", bad, 16)

@@ -247,3 +247,21 @@ def test_calls_made_before_a_capture(side):
     calls[1](fork)  # eager, on the stream of the capture
     torch.cuda.synchronize()
     assert torch.equal(ys[1], want)
+
+
+def test_given_workspaces():
+    """A workspace that is given and large enough is the one that is used; one
+    whose elements do not lie one behind another is refused."""
+    W, ws = weight(64, 264, 1040)
+    w = tclora.I8Weight(W, ws)
+    x = acts(64, 40, 1040, torch.bfloat16)
+    y = torch.zeros(40, 264, device=DEV)
+    b = Batch(65, [(300, [(1, 90), (40, 100)])], 4, 2, 64, 32)
+    plan = b.plan()
+    for make, n in ((lambda ws: tclora.I8Call(w, x, y, ws=ws), 1 << 17),
+                    (lambda ws: tclora.AttnCall(plan, b.qd, ws=ws), plan.workspace_bytes)):
+        own = torch.empty(n, dtype=torch.uint8, device=DEV)
+        assert make(own).ws is own and make(own[:256]).ws is not own
+        for bad in (own[:1].expand(n), torch.empty(2 * n, dtype=torch.uint8, device=DEV)[::2]):
+            with pytest.raises(ValueError):
+                make(bad)
