@@ -581,7 +581,7 @@ int tcl_lag_select(const double *arrival, const int32_t *req_ptr, const int32_t 
 
 /* One int8 base weight.  d_in is a multiple of 16 and at most
  * TCL_I8_MAX_D_IN (the integer sums then fit 32 bits for any entries), d_out
- * a multiple of 8.  Rows are contiguous; W is 16-byte, scale 4-byte aligned.
+ * a multiple of 8 below 2^27.  Rows are contiguous; W is 16-byte, scale 4-byte aligned.
  * W_p is an optional copy in the order the matrix cores take it
  * (tcl_i8_pack); where it is given the products read it and W may be NULL. */
 #define TCL_I8_MAX_D_IN 131056
@@ -599,7 +599,8 @@ typedef struct {
  * ceil(d_in / 64) + j), the 16 columns 16 g .. of its row r at 256 g + 16 r.
  * tcl_i8_pack writes it on `stream` into W_p (caller-owned device memory of
  * tcl_i8_pack_bytes bytes, 256-byte aligned) and sets w->W_p.
- * Errors: TCL_EINVAL, TCL_EALIGN, TCL_ENOSPC, TCL_EUNSUPPORTED, TCL_EHIP.
+ * Errors: TCL_EINVAL, TCL_EALIGN, TCL_ENOSPC, TCL_EUNSUPPORTED (2^36 bytes or
+ * more among them), TCL_EHIP.
  */
 int tcl_i8_pack_bytes(const tcl_i8_weight *w, size_t *bytes);
 int tcl_i8_pack(tcl_i8_weight *w, void *W_p, size_t bytes, void *stream);
@@ -633,7 +634,8 @@ int tcl_i8_quant(const void *x, int64_t ldx, tcl_dtype xd, int32_t n_tokens, int
  * Errors: TCL_EINVAL (NULL, sizes, ldq < d_in, ldy < d_out), TCL_EALIGN (q, W
  * or y not 16-byte aligned, scales not 4-byte aligned, d_in or ldq not a
  * multiple of 16, d_out or ldy not a multiple of 8), TCL_EUNSUPPORTED (yd,
- * d_in beyond TCL_I8_MAX_D_IN, 2^24 tokens or more), TCL_EHIP.
+ * d_in beyond TCL_I8_MAX_D_IN, d_out of 2^27 or more, 2^24 tokens or more,
+ * n_tokens * d_out of 2^36 or more), TCL_EHIP.
  */
 int tcl_i8_product(const tcl_i8_weight *w, const int8_t *q, int64_t ldq, const float *scale,
                    int32_t n_tokens, void *y, int64_t ldy, tcl_dtype yd, void *stream);

@@ -585,12 +585,21 @@ __global__ __launch_bounds__(64 * WC * WT, 2) void i8_tile(ProdArgs a) {
 // ---------------------------------------------------------------------------
 bool misaligned(const void *p, uintptr_t m) { return reinterpret_cast<uintptr_t>(p) & (m - 1); }
 
+// A launch's threads stay below 2^32: 512 for 16 channels (few tokens), up to
+// 256 a token (quantiser), 512 for 128 x 128 results (tiles), one for 16 bytes
+// of a packed copy.
+constexpr int kMaxChannels = 1 << 27, kMaxTokens = 1 << 24;
+constexpr int64_t kMaxResults = int64_t(1) << 36;
+constexpr size_t kMaxPacked = size_t(1) << 36;
+
 int check_weight(const tcl_i8_weight *w) {
   if (!w) return fail(TCL_EINVAL, "i8: weight is NULL");
   if (w->d_in < 16 || w->d_out < 0)
     return fail(TCL_EINVAL, "i8: d_in %d < 16 or d_out %d < 0", w->d_in, w->d_out);
   if (w->d_in > TCL_I8_MAX_D_IN)
     return fail(TCL_EUNSUPPORTED, "i8: d_in %d beyond %d", w->d_in, TCL_I8_MAX_D_IN);
+  if (w->d_out >= kMaxChannels)
+    return fail(TCL_EUNSUPPORTED, "i8: d_out %d, 2^27 or more", w->d_out);
   if (w->d_in % 16 || w->d_out % 8)
     return fail(TCL_EALIGN, "i8: d_in %d is not a multiple of 16 or d_out %d not of 8", w->d_in,
                 w->d_out);
@@ -600,9 +609,6 @@ int check_weight(const tcl_i8_weight *w) {
   if (misaligned(w->scale, 4)) return fail(TCL_EALIGN, "i8: scale must be 4-byte aligned");
   return TCL_OK;
 }
-
-// (a launch's threads, up to 256 a token, below 2^32)
-constexpr int kMaxTokens = 1 << 24;
 
 int check_quant(const void *x, int64_t ldx, int xd, int32_t n_tokens, int32_t d) {
   if (n_tokens < 0 || d < 16)
@@ -620,6 +626,8 @@ int check_y(const tcl_i8_weight *w, int32_t n_tokens, const void *y, int64_t ldy
   if (n_tokens < 0) return fail(TCL_EINVAL, "i8: n_tokens %d < 0", n_tokens);
   if (yd != TCL_BF16 && yd != TCL_F32) return fail(TCL_EUNSUPPORTED, "i8: y dtype %d", yd);
   if (n_tokens >= kMaxTokens) return fail(TCL_EUNSUPPORTED, "i8: n_tokens %d, 2^24 or more", n_tokens);
+  if (int64_t(n_tokens) * w->d_out >= kMaxResults)
+    return fail(TCL_EUNSUPPORTED, "i8: n_tokens * d_out of 2^36 or more");
   if (w->d_out == 0) return TCL_OK;  // nothing is written
   if (ldy < w->d_out) return fail(TCL_EINVAL, "i8: ldy < d_out");
   if (n_tokens > 0 && !y) return fail(TCL_EINVAL, "i8: y is NULL");
@@ -638,7 +646,7 @@ int launch_quant(const void *x, int64_t ldx, int xd, int32_t n, int32_t d, int8_
   hipLaunchKernelGGL((i8_quant_kernel<T, W, R>), dim3((n + R - 1) / R), dim3(64 * W * R), 0, s, a)
 #define QUANT_D(T)                       \
   if (d <= 1024) QUANT(T, 1, 4);         \
-  else if (d <= 2048) QUANT(T, 2, 4);    \
+  else if (d <= 2048 || n > 1 << 23) QUANT(T, 2, 4); /* (128 threads a token) */ \
   else if (d <= 4096 || n > 512) QUANT(T, 4, 2); \
   else QUANT(T, 8, 1)
   if (xd == TCL_BF16) {
@@ -850,6 +858,7 @@ extern "C" int tcl_i8_pack(tcl_i8_weight *w, void *W_p, size_t bytes, void *stre
   int rc = tcl_i8_pack_bytes(w, &need);
   if (rc) return rc;
   if (w->d_out == 0) return TCL_OK;
+  if (need >= kMaxPacked) return fail(TCL_EUNSUPPORTED, "i8: a packed copy of 2^36 bytes or more");
   if (!w->W || !W_p) return fail(TCL_EINVAL, "i8: pack needs W and W_p");
   if (misaligned(W_p, 256)) return fail(TCL_EALIGN, "i8: W_p must be 256-byte aligned");
   if (bytes < need) return fail(TCL_ENOSPC, "i8: W_p holds %zu bytes, needs %zu", bytes, need);

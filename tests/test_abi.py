@@ -542,3 +542,25 @@ def test_workspaces_of_the_base_operators_are_whole():
     for bad in (torch.empty(1, dtype=torch.uint8).expand(1 << 20), ws[::2], ws.view(32, 32).t()):
         with pytest.raises(ValueError):
             tclora._fits("x", bad, 16)
+
+
+def test_i8_sizes_beyond_the_grid_are_refused(L):
+    """Weights and results whose launches would pass the grid's limits (no
+    GPU): the calls say so before anything is launched."""
+    P, U = 0x1000, tclora.EUNSUPPORTED
+    out = ctypes.c_size_t(0)
+
+    def w(d_in, d_out):
+        return ctypes.byref(tclora.I8WeightDesc(d_in, d_out, P, P, None))
+
+    for n in (1 << 27, (1 << 31) - 8):
+        assert L.tcl_i8_pack_bytes(w(16, n), ctypes.byref(out)) == U
+        assert L.tcl_i8_workspace_bytes(w(16, n), 1, ctypes.byref(out)) == U
+        assert L.tcl_i8_product(w(16, n), P, 16, P, 1, P, n, 1, None) == U
+        assert L.tcl_i8_linear(w(16, n), P, 16, 0, 1, P, n, 1, 0x10000, 1 << 20, None) == U
+    assert L.tcl_i8_pack_bytes(w(16, (1 << 27) - 8), ctypes.byref(out)) == 0
+    big = 1 << 20
+    assert L.tcl_i8_product(w(16, big), P, 16, P, 1 << 16, P, big, 1, None) == U
+    assert L.tcl_i8_linear(w(16, big), P, 16, 0, 1 << 16, P, big, 1, 0x10000, 1 << 40, None) == U
+    assert L.tcl_i8_pack_bytes(w(65536, big), ctypes.byref(out)) == 0 and out.value == 1 << 36
+    assert L.tcl_i8_pack(w(65536, big), P, out.value, None) == U

@@ -394,3 +394,21 @@ def test_quant_next_to_ties_at_small_scales(d):
     n = n + ((2 * rem > si) | ((2 * rem == si) & (n % 2 == 1)))
     n = np.where(si > 0, np.sign(xi) * np.minimum(n, 127), 0)
     assert np.array_equal(q.cpu().numpy().astype(np.int64), n)
+
+
+def test_quant_of_as_many_tokens_as_are_allowed():
+    """2^24 - 1 tokens of rows longer than a pair of waves takes at a time."""
+    T, d = (1 << 24) - 1, 2064
+    if torch.cuda.mem_get_info()[0] < 150 << 30:
+        pytest.skip("needs 104 GB of memory")
+    x = torch.zeros(T, d, dtype=torch.bfloat16, device=DEV)
+    at = torch.tensor([0, 1, 4095, 1 << 23, (1 << 23) + 1, T - 2, T - 1], device=DEV)
+    x[at] = acts(16, len(at), d, torch.bfloat16)
+    q, s = tclora.i8_quant(x)
+    n, want = quant64(x[at])
+    assert torch.equal(q[at].cpu(), n) and torch.equal(s[at].cpu(), want)
+    rows = torch.ones(T, dtype=torch.bool, device=DEV)
+    rows[at] = False
+    assert not s[rows].any()
+    del x, q
+    torch.cuda.empty_cache()
