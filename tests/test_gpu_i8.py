@@ -412,3 +412,16 @@ def test_quant_of_as_many_tokens_as_are_allowed():
     assert not s[rows].any()
     del x, q
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("T,d_in,d_out", [(33, 4096, 24576), (64, 4112, 32768), (49, 4096, 32776),
+                                          (64, 4080, 24584)])
+def test_few_tokens_of_wide_weights(T, d_in, d_out):
+    """Both sides of the sizes where blocks and tiles change places."""
+    W, ws = weight(17, d_out, d_in)
+    x = acts(9, T, d_in, torch.bfloat16)
+    n, s = quant64(x)
+    # (sums of products of 8-bit numbers: exact in 64 bits on the GPU as well)
+    sums = (n.to(DEV).double() @ W.double().t()).cpu()
+    want = sums * s.double()[:, None] * ws.double().cpu()
+    close(tclora.i8_linear(tclora.I8Weight(W, ws), x, y_dtype=torch.float32), want, torch.float32)
