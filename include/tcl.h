@@ -610,9 +610,9 @@ int tcl_i8_pack(tcl_i8_weight *w, void *W_p, size_t bytes, void *stream);
  *   scale[t] = max_d |x[t][d]| / 127, rounded to fp32;
  *   q[t][d]  = x[t][d] / scale[t] rounded to the nearest integer, ties to
  *              even, of the real quotient (no rounding before that one).
- * A row of zeros gets scale 0 and q 0.  A row that holds an infinity or a NaN
- * gets scale NaN and q 0, so that its products are NaN.  Where the scale is a
- * subnormal number q is held to +-127.
+ * A row of zeros, or one whose scale rounds to 0, gets scale 0 and q 0.  A row
+ * that holds an infinity or a NaN gets scale NaN and q 0, so that its products
+ * are NaN.  Where the scale is a subnormal number q is held to +-127.
  * x: device [n_tokens][ldx] of dtype xd, 16-byte aligned, ldx a multiple of
  * 8; q: device [n_tokens][ldq], 16-byte aligned, ldq a multiple of 16; scale:
  * device [n_tokens].  d is a multiple of 16.  Columns of q at or beyond d are

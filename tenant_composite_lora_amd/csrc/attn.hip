@@ -693,7 +693,7 @@ __device__ inline float half_max(float v) {
 // Few rows: every wave holds all of them, over its own 16 keys of a step, and
 // needs no barrier; the waves' results are joined through LDS.  Bound by the
 // keys' and values' bytes: 64 requests of 8 tenants, 760 MB with the prefixes,
-// 145 us, 5.2 TB/s.
+// 150 us, 5.1 TB/s.
 template <int D>
 __device__ inline void attend_few(const AttnArgs &a, const Work &t, int h, int gq, Smem<D> &sm) {
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;

@@ -331,7 +331,7 @@ __global__ __launch_bounds__(64 * WV) void i8_skinny(ProdArgs a) {
 // Up to kFewTok tokens in one launch: each workgroup rounds the tokens itself
 // (16 channels, 8 waves; the weight's first operands are on their way
 // meanwhile).  The integers lie in LDS, chunk c of token t at 16 (kFewTok c +
-// t).  (One token, d_in 4096 to 1024 channels: 4.7 us, in two launches 7.4;
+// t).  (One token, d_in 4096 to 1024 channels: 4.8 us, in two launches 7.4;
 // two tokens 5.8; with four, the repeated rounding made it 9.3.)
 constexpr int kFewTok = 2;
 constexpr int kFewBytes = 32768;  // LDS for the integers

@@ -9,8 +9,9 @@
 // (positions reach far beyond what an fp32 product resolves), reduced to one
 // turn there and handed to the fp32 sine and cosine.
 // Bound by memory for many tokens (4224 tokens, 32 + 8 + 8 heads of 128, fp32
-// in: 156 MB in 24.6 us, 6.3 TB/s, part of it from the last-level cache); 64
-// tokens take 3.0 us, a launch and two round trips to memory.
+// in: 156 MB in 24.2 us, 6.4 TB/s, part of it from the last-level cache); 64
+// tokens take 3.6 us (3.3 in a captured graph), a launch and two round trips
+// to memory.
 #include "kern_common.hpp"
 #include "kv.hpp"
 
