@@ -581,8 +581,8 @@ int tcl_lag_select(const double *arrival, const int32_t *req_ptr, const int32_t 
 
 /* One int8 base weight.  d_in is a multiple of 16 and at most
  * TCL_I8_MAX_D_IN (the integer sums then fit 32 bits for any entries), d_out
- * a multiple of 8 below 2^27.  Rows are contiguous; W is 16-byte, scale 4-byte aligned.
- * W_p is an optional copy in the order the matrix cores take it
+ * a multiple of 8 below 2^27.  Rows are contiguous; W is 16-byte, scale 4-byte
+ * aligned.  W_p is an optional copy in the order the matrix cores take it
  * (tcl_i8_pack); where it is given the products read it and W may be NULL. */
 #define TCL_I8_MAX_D_IN 131056
 typedef struct {

@@ -680,9 +680,8 @@ void go_tile(ProdArgs a, hipStream_t s) {
 //   up to 16 tokens: 16 channels a workgroup, 8 waves over d_in (1 token,
 //     1024 channels: 4.1; 32 channels: 5.5);
 //   up to 32: the same with two token blocks (4096 channels: 7.4; 32: 8.3);
-//   more, as long as 128 x 128 tiles are fewer than 192, and up to 64 tokens
-//     of long rows as long as 64-channel blocks run in one round (few_wide):
-//     by what runs in one
+//   more, as long as 128 x 128 tiles are fewer than 192 (and further for up
+//     to 64 tokens, few_wide): by what runs in one
 //     round, two workgroups a CU (with the quantiser): 32 channels x 64
 //     tokens, 4 waves, up to 512 of them (256 x 4096: 22.2; 64 x 48 24.2; 64 x
 //     64 27.2), else 64 x 48 (333 x 4096: 24.8, 32 x 64 28.8, 64 x 64 28.5; 72
@@ -738,13 +737,13 @@ Kernel cheapest(int64_t T, int64_t N, int64_t *cost) {
   return best;
 }
 
-// Up to 64 tokens fill half a row of 128 x 128 tiles; one round of 64-channel
-// blocks reads the weight as often and takes shorter rows' worth of matrix
-// instructions.  Blocks and tiles, us, 48 and 64 tokens: d_in 14336, 24576
-// channels 87, 98 and 142, 143; 32768 98, 107 and 148, 149; 8192 x 32768 54,
-// 57 and 77, 77; 4096 x 24576 29, 31 and 32, 33; 4096 x 32768 33, 36 and 34,
-// 34.  Past one round: 14336 x 33024 132, 203 and 161, 162.  Shorter rows:
-// 2560 x 28672 25, 28 and 25, 26; 1536 21, 23 and 19, 19.
+// Up to 64 tokens leave half of every 128 x 128 tile to padding, while one
+// round of 64-channel blocks reads the weight once as well.  Blocks and tiles,
+// us, 48 and 64 tokens: d_in 14336, 24576 channels 87, 98 and 142, 143; 32768
+// 98, 107 and 148, 149; 8192 x 32768 54, 57 and 77, 77; 4096 x 24576 29, 31
+// and 32, 33; 4096 x 32768 33, 36 and 34, 34.  Past one round: 14336 x 33024
+// 132, 203 and 161, 162.  Shorter rows: 2560 x 28672 25, 28 and 25, 26; 1536
+// 21, 23 and 19, 19.
 bool few_wide(int64_t T, int64_t K, int64_t N) { return T <= 64 && K >= 4096 && tiles(N, 64) <= 512; }
 
 template <typename TY>

@@ -14,7 +14,7 @@ from test_gpu_i8 import acts, quant64, weight
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
-SLEEP = 20_000_000
+SLEEP = 100_000_000
 
 
 def handed_out(side, n, at, count=6):
@@ -31,6 +31,7 @@ def handed_out(side, n, at, count=6):
 def side():
     st = torch.cuda.Stream()
     torch.cuda.synchronize()
+    torch.cuda.empty_cache()  # (blocks of other tests are not handed out instead)
     yield st
     torch.cuda.synchronize()
 
