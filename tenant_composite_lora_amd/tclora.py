@@ -869,7 +869,8 @@ class I8Weight:
     """An int8 base weight: W int8 [d_out, d_in] and its channel scales fp32
     [d_out], on the GPU (tcl_i8_weight).  The products read a copy in the
     matrix cores' order (tcl_i8_pack), made here unless ``pack`` is False;
-    with it W itself is not kept."""
+    with it W itself is not kept.  The copy is made on ``stream`` or the
+    current one: calls on others have to be ordered behind it."""
 
     def __init__(self, W: torch.Tensor, scale: torch.Tensor, pack: bool = True, stream=None):
         if W.dtype != torch.int8:
@@ -1081,7 +1082,9 @@ class AttnPlan:
     that share a prefix.  int32 device tensors: seq_tok_ptr [n_seqs + 1],
     group_seq_ptr [n_groups + 1], prefix_len [n_groups], prefix_pages
     [n_groups, m], own_len [n_seqs], own_pages [n_seqs, n].  One plan serves
-    every layer whose cache has the sizes of ``cache``."""
+    every layer whose cache has the sizes of ``cache``.  The mapping runs on
+    ``stream`` or the current one: calls on others have to be ordered behind
+    it, and the tables are read by them too."""
 
     def __init__(self, cache: KVCache, n_q_heads: int, seq_tok_ptr: torch.Tensor,
                  group_seq_ptr: torch.Tensor, prefix_len: torch.Tensor,
