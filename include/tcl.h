@@ -713,6 +713,88 @@ int tcl_kv_append(const tcl_kv_cache *c, const tcl_rope *rope, const void *k, in
                   tcl_dtype xd, void *q_out, int64_t ldqo, int32_t n_tokens, const int32_t *pos,
                   const int64_t *slot, void *stream);
 
+/* Norms of queries and keys: each head x of head_dim elements becomes
+ *   x * (mean(x^2) + eps)^(-1/2) * w
+ * before it is rotated; w_q (w_k) NULL leaves the heads of q (k) as they are.
+ * The weights of head h are the head_dim numbers at h * stride of w_q (w_k):
+ * stride 0, one row for every head.  The squares are summed in fp32, in 64 bits
+ * where fp32's range is left.  With eps 0 a head of zeros is NaN; a head that
+ * holds an infinity or a NaN is what the formula gives (a finite element of a
+ * head with an infinity is 0, the infinity itself NaN), others are not touched
+ * by it. */
+typedef struct {
+  const float *w_q;           /* device, 16-byte aligned */
+  const float *w_k;
+  int64_t stride_q, stride_k; /* elements, multiples of 4 */
+  float eps;
+} tcl_head_norm;
+
+/* tcl_kv_append with the norms in the same pass, all of it in fp32 and rounded
+ * to bf16 once.  Errors: those of tcl_kv_append; TCL_EINVAL (norm NULL, eps
+ * negative or not finite, a negative stride), TCL_EALIGN (weights, strides). */
+int tcl_kv_append_norm(const tcl_kv_cache *c, const tcl_rope *rope, const tcl_head_norm *norm,
+                       const void *k, int64_t ldk, const void *v, int64_t ldv, const void *q,
+                       int64_t ldq, int32_t n_q_heads, tcl_dtype xd, void *q_out, int64_t ldqo,
+                       int32_t n_tokens, const int32_t *pos, const int64_t *slot, void *stream);
+
+/*
+ * A step's bookkeeping on the GPU: where the new tokens of a batch go, from
+ * the requests' lengths alone.  Every array is DEVICE memory.  Request s
+ * brings n_new[s] tokens behind the own_len[s] keys it has (its group's prefix
+ * comes before those, prefix_len and group_seq_ptr as in tcl_attn_batch).
+ * With P = page_size, request s needs ceil((own_len[s] + n_new[s]) / P) pages;
+ * those it lacks come from free_pages, a list of page ids of which the first
+ * *used are taken, in order of requests:
+ *   seq_tok_ptr[s + 1] = seq_tok_ptr[s] + n_new[s], seq_tok_ptr[0] = 0;
+ *   own_pages[s * ld_own + p], the ids of its new pages (other entries are
+ *     left as they were);
+ *   pos[t] = prefix + key, slot[t] = page(key / P) * P + key % P with key =
+ *     own_len[s] + t - seq_tok_ptr[s], for its tokens t;
+ *   own_len_out[s] = own_len[s] + n_new[s]; *used_out = *used + pages taken.
+ * Rows of pos and slot behind the last request's tokens (n_tokens may be
+ * more) are padding: position 0, slot -1.  seq_tok_ptr, own_len_out and
+ * own_pages are then what tcl_attn_plan takes, pos and slot what
+ * tcl_kv_append takes.  own_len_out may be own_len and used_out may be used (a
+ * captured step then goes on by itself); no other arrays may overlap.  The ids
+ * in free_pages behind *used must differ from each other and from pages that
+ * are in use.
+ * status[4] = {code, tokens, pages taken, pages left}.  A bad batch (TCL_EINVAL: a
+ * negative length, more than n_tokens tokens, keys beyond a table's row or
+ * positions beyond 2^31 - 1, group_seq_ptr, *used outside 0..n_free, a page id
+ * outside the cache where one is used) or one for which too few pages are left
+ * (TCL_ENOSPC) takes nothing: every row is padding, seq_tok_ptr is all zeros,
+ * own_len_out = own_len, *used_out = *used, own_pages is left as it was; what
+ * follows in the stream then appends nothing and attends to nothing.
+ * Of c, page_size and n_pages count.  One launch, two for more than 8192 rows.
+ * Graph-capturable.
+ * Errors on the host: those of the cache; TCL_EINVAL (NULL, negative sizes,
+ * requests without a group), TCL_EALIGN (slot 8-byte, the others 4-byte
+ * aligned), TCL_EUNSUPPORTED (n_seqs, n_groups or n_tokens of 2^24 or more,
+ * rows of own_pages of 2^29 keys or more), TCL_EHIP.
+ */
+typedef struct {
+  int32_t n_seqs;
+  int32_t n_groups;
+  int32_t n_tokens; /* rows of pos and slot       */
+  int32_t n_free;   /* entries of free_pages      */
+  int32_t ld_own;   /* entries of a row of own_pages */
+  const int32_t *n_new;
+  const int32_t *group_seq_ptr;
+  const int32_t *prefix_len;
+  const int32_t *own_len;
+  const int32_t *free_pages;
+  const int32_t *used;
+  int32_t *own_pages;
+  int32_t *seq_tok_ptr;
+  int32_t *pos;
+  int64_t *slot;
+  int32_t *own_len_out;
+  int32_t *used_out;
+  int32_t *status;
+} tcl_kv_batch;
+
+int tcl_kv_map(const tcl_kv_cache *c, const tcl_kv_batch *b, void *stream);
+
 /* ------------------------------------------------------------------------
  * Attention over the paged cache for a batch whose requests share their
  * group's prefix (ELORA, section V: requests of one adapter hang below the

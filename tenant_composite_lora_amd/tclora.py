@@ -39,7 +39,7 @@ EXPORTS = ["tcl_last_error", "tcl_version", "tcl_plan_bytes", "tcl_plan_map", "t
            "tcl_i8_quant", "tcl_i8_product", "tcl_i8_workspace_bytes", "tcl_i8_linear",
            "tcl_i8_pack_bytes", "tcl_i8_pack",
            "tcl_kv_append", "tcl_attn_plan_bytes", "tcl_attn_workspace_bytes", "tcl_attn_plan",
-           "tcl_attn_status_async", "tcl_attn_apply"]
+           "tcl_attn_status_async", "tcl_attn_apply", "tcl_kv_append_norm", "tcl_kv_map"]
 
 # bytes of the static device workspace of tcl_fused_apply_noalloc
 SCRATCH_BYTES = 32 << 20
@@ -82,6 +82,19 @@ class KVDesc(ctypes.Structure):
 class RopeDesc(ctypes.Structure):
     _fields_ = [("inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int32),
                 ("interleaved", ctypes.c_int32)]
+
+
+class HeadNormDesc(ctypes.Structure):
+    _fields_ = [("w_q", ctypes.c_void_p), ("w_k", ctypes.c_void_p),
+                ("stride_q", ctypes.c_int64), ("stride_k", ctypes.c_int64),
+                ("eps", ctypes.c_float)]
+
+
+class MapBatch(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_seqs", "n_groups", "n_tokens", "n_free", "ld_own")] + [
+        (n, ctypes.c_void_p) for n in ("n_new", "group_seq_ptr", "prefix_len", "own_len", "free_pages",
+                                       "used", "own_pages", "seq_tok_ptr", "pos", "slot",
+                                       "own_len_out", "used_out", "status")]
 
 
 class AttnBatch(ctypes.Structure):
@@ -164,6 +177,9 @@ def lib(path: Optional[str] = None):
                                 sz, vp]
     L.tcl_kv_append.argtypes = [ctypes.POINTER(KVDesc), ctypes.POINTER(RopeDesc), vp, i64, vp, i64,
                                 vp, i64, i32, i32, vp, i64, i32, vp, vp, vp]
+    L.tcl_kv_append_norm.argtypes = [*L.tcl_kv_append.argtypes[:2], ctypes.POINTER(HeadNormDesc),
+                                     *L.tcl_kv_append.argtypes[2:]]
+    L.tcl_kv_map.argtypes = [ctypes.POINTER(KVDesc), ctypes.POINTER(MapBatch), vp]
     bp, cp = ctypes.POINTER(AttnBatch), ctypes.POINTER(KVDesc)
     L.tcl_attn_plan_bytes.argtypes = [bp, cp, i32, ctypes.POINTER(sz)]
     L.tcl_attn_workspace_bytes.argtypes = [bp, cp, i32, ctypes.POINTER(sz)]
@@ -1021,16 +1037,42 @@ class Rope:
         self.desc = RopeDesc(_ptr(inv_freq) if n else None, 2 * n, int(interleaved))
 
 
+class HeadNorm:
+    """Norms of queries and keys by head (tcl_head_norm): weights fp32
+    [head_dim] for every head or [heads, head_dim], on the GPU; None leaves q
+    (or k) as it is."""
+
+    def __init__(self, w_q: Optional[torch.Tensor], w_k: Optional[torch.Tensor], eps: float = 1e-6):
+        stride = []
+        for name, w in (("w_q", w_q), ("w_k", w_k)):
+            if w is not None and w.dtype != torch.float32:
+                raise TypeError(f"HeadNorm: {name} must be float32")
+            if w is not None and (w.dim() not in (1, 2) or not w.is_contiguous()):
+                raise ValueError(f"HeadNorm: {name} must be [head_dim] or [heads, head_dim], contiguous")
+            stride.append(0 if w is None or w.dim() == 1 else w.shape[1])
+        self.w_q, self.w_k, self.eps = w_q, w_k, float(eps)
+        self.desc = HeadNormDesc(_ptr(w_q), _ptr(w_k), *stride, self.eps)
+
+    def fit(self, n_q_heads: int, n_kv_heads: int, head_dim: int) -> None:
+        """Checks the weights against a call's heads."""
+        for name, w, n in (("w_q", self.w_q, n_q_heads), ("w_k", self.w_k, n_kv_heads)):
+            if w is not None and tuple(w.shape) not in ((head_dim,), (n, head_dim)):
+                raise ValueError(f"HeadNorm: {name} must be [{head_dim}] or [{n}, {head_dim}], got "
+                                 f"{list(w.shape)}")
+
+
 class AppendCall:
     """Pre-marshalled arguments of tcl_kv_append for repeated calls: k, v [T,
     heads * head_dim] rows go to ``slot`` (int64 [T]) of the cache, k rotated
     to ``pos`` (int32 [T]); with q [T, q heads * head_dim] its rotated rows go
-    to q_out (bf16, made here unless given).  Each call returns q_out."""
+    to q_out (bf16, made here unless given).  With ``norm`` the heads of q and
+    k are normed before they are rotated (tcl_kv_append_norm).  Each call
+    returns q_out."""
 
     def __init__(self, cache: KVCache, k: torch.Tensor, v: torch.Tensor, pos: torch.Tensor,
                  slot: torch.Tensor, rope: Optional[Rope] = None,
                  q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None, *,
-                 _once: bool = False):
+                 norm: Optional[HeadNorm] = None, _once: bool = False):
         T, row = k.shape[0], cache.n_kv_heads * cache.head_dim
         self.ldk = _rows("AppendCall: k", k, T, row)
         self.ldv = _rows("AppendCall: v", v, T, row)
@@ -1059,9 +1101,14 @@ class AppendCall:
         self.pos, self.slot, self.q_out, self.T = pos, slot, q_out, T
         self.xd, self.device = _dtype_code(k.dtype), cache.device
         self._own = () if q_out is None else ((q_out, _stream(self.device)),)
-        self._fn = lib().tcl_kv_append
+        self.norm, by = norm, ()
+        if norm is not None:
+            norm.fit(self.Hq, cache.n_kv_heads, cache.head_dim)
+            _same_device("AppendCall", cache.device, norm.w_q, norm.w_k)
+            by = (ctypes.byref(norm.desc),)
+        self._fn = lib().tcl_kv_append if norm is None else lib().tcl_kv_append_norm
         self._args = _packed(self._fn, (
-            ctypes.byref(cache.desc), ctypes.byref(rope.desc), k.data_ptr(), self.ldk,
+            ctypes.byref(cache.desc), ctypes.byref(rope.desc), *by, k.data_ptr(), self.ldk,
             v.data_ptr(), self.ldv, _ptr(q), self.ldq, self.Hq, self.xd, _ptr(q_out), self.ldqo, T,
             pos.data_ptr(), slot.data_ptr()))
 
@@ -1072,9 +1119,86 @@ class AppendCall:
 
 def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, pos: torch.Tensor,
               slot: torch.Tensor, rope: Optional[Rope] = None, q: Optional[torch.Tensor] = None,
-              q_out: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
-    """tcl_kv_append; returns the rotated queries (None without q)."""
-    return AppendCall(cache, k, v, pos, slot, rope, q, q_out, _once=stream is None)(stream)
+              q_out: Optional[torch.Tensor] = None, stream=None,
+              norm: Optional[HeadNorm] = None) -> Optional[torch.Tensor]:
+    """tcl_kv_append, or tcl_kv_append_norm with ``norm``; returns the rotated
+    queries (None without q)."""
+    return AppendCall(cache, k, v, pos, slot, rope, q, q_out, norm=norm, _once=stream is None)(stream)
+
+
+class MapCall:
+    """Pre-marshalled arguments of tcl_kv_map for repeated calls: pages,
+    positions and slots of a batch's new tokens.  int32 device tensors: n_new
+    [n_seqs], group_seq_ptr [n_groups + 1], prefix_len [n_groups], own_len
+    [n_seqs] (keys before the call), own_pages [n_seqs, m] (new pages are
+    written into it), free_pages [n] and used [1], how many of them are taken.
+    Each call returns this object, whose seq_tok_ptr [n_seqs + 1], pos int32
+    and slot int64 [n_tokens] are what AppendCall and AttnPlan take, with
+    own_len and used after the call.  ``own_len_out`` and ``used_out`` are made
+    here unless given; given own_len and used themselves a captured call goes
+    on by itself at each replay."""
+
+    def __init__(self, cache: KVCache, n_new: torch.Tensor, group_seq_ptr: torch.Tensor,
+                 prefix_len: torch.Tensor, own_len: torch.Tensor, own_pages: torch.Tensor,
+                 free_pages: torch.Tensor, used: torch.Tensor, n_tokens: int,
+                 own_len_out: Optional[torch.Tensor] = None,
+                 used_out: Optional[torch.Tensor] = None, *, _once: bool = False):
+        S, G, T = n_new.shape[0], group_seq_ptr.shape[0] - 1, int(n_tokens)
+        for name, t, n in (("n_new", n_new, S), ("group_seq_ptr", group_seq_ptr, G + 1),
+                           ("prefix_len", prefix_len, G), ("own_len", own_len, S), ("used", used, 1),
+                           ("free_pages", free_pages, free_pages.numel()),
+                           ("own_len_out", own_len_out, S), ("used_out", used_out, 1)):
+            if t is not None:
+                _vector(f"MapCall: {name}", t, n, torch.int32)
+        if T < 0:
+            raise ValueError("MapCall: n_tokens must not be negative")
+        if own_pages.dtype != torch.int32:
+            raise ValueError("MapCall: own_pages must be int32")
+        ld = _rows("MapCall: own_pages", own_pages, S) if own_pages.numel() else 0
+        self.device = cache.device
+        _same_device("MapCall", self.device, n_new, group_seq_ptr, prefix_len, own_len, own_pages,
+                     free_pages, used, own_len_out, used_out)
+        made = []
+
+        def make(n, dtype=torch.int32):
+            made.append(torch.empty(n, dtype=dtype, device=self.device))
+            return made[-1]
+
+        self.seq_tok_ptr, self.pos, self.slot = make(S + 1), make(T), make(T, torch.int64)
+        self.own_len = make(S) if own_len_out is None else own_len_out
+        self.used = make(1) if used_out is None else used_out
+        self._status = make(4)
+        self._made = None if _once else _Made(self.device)
+        home = _stream(self.device)
+        self._own = tuple((t, home) for t in made)
+        self._in = (n_new, group_seq_ptr, prefix_len, own_len, own_pages, free_pages, used)
+        self.cache, self.own_pages, self.n_tokens = cache, own_pages, T
+        self.batch = MapBatch(S, G, T, free_pages.numel(), ld, *[_ptr(t) for t in (
+            n_new, group_seq_ptr, prefix_len, own_len, free_pages, used, own_pages, self.seq_tok_ptr,
+            self.pos, self.slot, self.own_len, self.used, self._status)])
+        if own_pages.numel() and own_pages.shape[1] != ld:
+            raise ValueError("MapCall: own_pages must be contiguous")
+        self._fn = lib().tcl_kv_map
+        self._args = (ctypes.byref(cache.desc), ctypes.byref(self.batch))
+
+    def __call__(self, stream=None) -> "MapCall":
+        _call(self.device, self._fn, self._args, stream, *self._own, made=self._made)
+        return self
+
+    def status(self):
+        """(code, tokens, pages taken, pages left) of the last call;
+        synchronises."""
+        torch.cuda.synchronize(self.device)
+        return tuple(self._status.tolist())
+
+
+def kv_map(cache: KVCache, n_new: torch.Tensor, group_seq_ptr: torch.Tensor, prefix_len: torch.Tensor,
+           own_len: torch.Tensor, own_pages: torch.Tensor, free_pages: torch.Tensor,
+           used: torch.Tensor, n_tokens: int, own_len_out: Optional[torch.Tensor] = None,
+           used_out: Optional[torch.Tensor] = None, stream=None) -> MapCall:
+    """tcl_kv_map: the call, run, with its outputs."""
+    return MapCall(cache, n_new, group_seq_ptr, prefix_len, own_len, own_pages, free_pages, used,
+                   n_tokens, own_len_out, used_out, _once=stream is None)(stream)
 
 
 class AttnPlan:

@@ -564,3 +564,48 @@ def test_i8_sizes_beyond_the_grid_are_refused(L):
     assert L.tcl_i8_linear(w(16, big), P, 16, 0, 1 << 16, P, big, 1, 0x10000, 1 << 40, None) == U
     assert L.tcl_i8_pack_bytes(w(65536, big), ctypes.byref(out)) == 0 and out.value == 1 << 36
     assert L.tcl_i8_pack(w(65536, big), P, out.value, None) == U
+
+
+def test_kv_append_norm_host_errors(L):
+    """The append with norms refuses what the plain one refuses, and bad norms
+    (no GPU)."""
+    P = 0x1000
+    E, A, U = tclora.EINVAL, tclora.EALIGN, tclora.EUNSUPPORTED
+
+    def call(n=None, T=4, k=P, ldk=128, rot=64, head_dim=64, xd=0, **kw):
+        nd = dict(w_q=P, w_k=P, stride_q=0, stride_k=64, eps=1e-6)
+        nd.update(kw)
+        c = tclora.KVDesc(4, 16, 2, head_dim, 2048, 64, 1024, P, P)
+        r = tclora.RopeDesc(P, rot, 0)
+        norm = ctypes.byref(tclora.HeadNormDesc(**nd)) if n is None else None
+        return L.tcl_kv_append_norm(ctypes.byref(c), ctypes.byref(r), norm, k, ldk, P, 128, P, 256, 4, xd,
+                                    2 * P, 256, T, P, P, None)
+
+    assert call(T=0) == 0 and call(T=0, w_q=None, w_k=None, eps=0.0) == 0
+    assert [call(n=0), call(eps=-1e-9), call(eps=float("nan")), call(eps=float("inf")),
+            call(stride_q=-64), call(stride_k=-4), call(T=-1), call(k=None), call(ldk=120)] == [E] * 9
+    assert [call(w_q=P + 8), call(w_k=P + 4), call(stride_q=2), call(stride_k=65), call(k=P + 8)] == [A] * 5
+    assert [call(rot=24), call(head_dim=72), call(xd=2), call(T=1 << 24)] == [U] * 4
+
+
+def test_kv_map_host_errors(L):
+    """tcl_kv_map refuses bad sizes and pointers on the host (no GPU)."""
+    P = 0x1000
+    E, A, U = tclora.EINVAL, tclora.EALIGN, tclora.EUNSUPPORTED
+    ints = ("n_new", "group_seq_ptr", "prefix_len", "own_len", "free_pages", "used", "own_pages",
+            "seq_tok_ptr", "pos", "own_len_out", "used_out", "status")
+
+    def call(c=None, b=None, n_pages=4, page_size=16, **kw):
+        bd = dict(n_seqs=3, n_groups=2, n_tokens=5, n_free=4, ld_own=4, slot=P, **{n: P for n in ints})
+        bd.update(kw)
+        cp = ctypes.byref(tclora.KVDesc(n_pages, page_size, 1, 16, 256, 16, 16, P, P)) if c is None else None
+        bp = ctypes.byref(tclora.MapBatch(**bd)) if b is None else None
+        return L.tcl_kv_map(cp, bp, None)
+
+    assert [call(c=0), call(b=0), call(n_pages=0)] == [E] * 3 and call(page_size=24) == U
+    assert [call(**{n: -1}) for n in ("n_seqs", "n_groups", "n_tokens", "n_free", "ld_own")] == [E] * 5
+    assert [call(**{n: None}) for n in (*ints, "slot")] == [E] * 13
+    assert call(n_groups=0) == E
+    assert [call(**{n: P + 2}) for n in ints] == [A] * 12 and call(slot=P + 4) == A
+    N = 1 << 24
+    assert [call(n_seqs=N), call(n_groups=N), call(n_tokens=N), call(ld_own=1 << 25)] == [U] * 4

@@ -1,0 +1,251 @@
+"""tcl_kv_map against a walk over requests and keys on the host: integers, to
+be equal."""
+import numpy as np
+import pytest
+import torch
+
+from tenant_composite_lora_amd import tclora
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+def up(a, dtype=np.int32):
+    return torch.from_numpy(np.ascontiguousarray(a, dtype=dtype)).to(DEV)
+
+
+def cache_of(n_pages, page):
+    K, V = (torch.zeros(n_pages, page, 1, 16, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    return tclora.KVCache(K, V)
+
+
+class Step:
+    def __init__(self, seed, S, G, page, new, own, pad=0, spare=5, cols=1, taken=None):
+        r = np.random.default_rng(seed)
+        self.page = page
+        self.n_new = r.integers(0, new + 1, S) if np.isscalar(new) else np.asarray(new)
+        self.own_len = r.integers(0, own + 1, S)
+        self.prefix = r.integers(0, 5000, G)
+        self.group_seq = np.concatenate([[0], np.sort(r.integers(0, S + 1, G - 1)), [S]]) if G else np.zeros(1)
+        have = -(-self.own_len // page)
+        want = -(-(self.own_len + self.n_new) // page)
+        self.want = want
+        n_pages = int(want.sum()) + spare
+        ids = r.permutation(n_pages)
+        self.ld = (int(want.max()) if S else 0) + cols
+        self.pages = np.full((S, self.ld), -7)
+        at = 0
+        for s in range(S):
+            self.pages[s, :have[s]] = ids[at:at + have[s]]
+            at += have[s]
+        self.free, self.used = ids, at
+        self.T = int(self.n_new.sum()) + pad
+        self.cache = cache_of(n_pages, page)
+
+    def tensors(self):
+        return [up(x) for x in (self.n_new, self.group_seq, self.prefix, self.own_len, self.pages,
+                                self.free, [self.used])]
+
+    def want_all(self):
+        P, S = self.page, len(self.n_new)
+        pages, used = self.pages.copy(), self.used
+        ptr, pos, slot = [0], [], []
+        grp = np.searchsorted(self.group_seq, np.arange(S), side="right") - 1
+        for s in range(S):
+            for key in range(self.own_len[s], self.own_len[s] + self.n_new[s]):
+                if key % P == 0:
+                    pages[s, key // P] = self.free[used]
+                    used += 1
+                pos.append(self.prefix[grp[s]] + key)
+                slot.append(int(pages[s, key // P]) * P + key % P)
+            ptr.append(len(pos))
+        n = self.T - len(pos)
+        return dict(seq_tok_ptr=ptr, pos=pos + [0] * n, slot=slot + [-1] * n,
+                    own_len=self.own_len + self.n_new, used=[used], own_pages=pages)
+
+
+def check(call, want, code=tclora.OK):
+    st = call.status()
+    assert st[0] == code, st
+    for k, w in want.items():
+        got = getattr(call, k).cpu().numpy()
+        assert np.array_equal(got, np.asarray(w).reshape(got.shape)), k
+    return st
+
+
+@pytest.mark.parametrize("S,G,page,new,own,pad", [
+    (1, 1, 16, 1, 40, 0), (64, 8, 16, 1, 2048, 0), (3, 1, 1, 5, 9, 2), (64, 5, 64, 3, 300, 64),
+    (1, 1, 1024, 5000, 0, 0), (7, 9, 128, 700, 1000, 1), (1023, 30, 16, 2, 60, 0),
+    (1024, 1, 16, 4, 60, 3), (1025, 200, 32, 4, 60, 3), (3000, 2000, 16, 2, 40, 9),
+    (33, 2, 16, 900, 100, 5), (2500, 17, 16, 20, 100, 100)])
+def test_map(S, G, page, new, own, pad):
+    for seed in range(2):
+        s = Step(S + seed, S, G, page, new, own, pad)
+        if s.n_new.sum() == 0:
+            s = Step(S + seed, S, G, page, [new] * S, own, pad)
+        t = s.tensors()
+        call = tclora.kv_map(s.cache, *t, s.T)
+        want = s.want_all()
+        st = check(call, want)
+        taken = want["used"][0] - s.used
+        assert st[1:] == (s.n_new.sum(), taken, len(s.free) - s.used - taken)
+        # the inputs as they were
+        for x, w in zip(t, (s.n_new, s.group_seq, s.prefix, s.own_len, None, s.free, [s.used])):
+            assert w is None or np.array_equal(x.cpu().numpy(), np.asarray(w))
+        # again: the same
+        check(call(), want)
+
+
+@pytest.mark.parametrize("T", [8191, 8192, 8193, 9216, 9217, 70000])
+def test_around_the_second_launch(T):
+    s = Step(T, 40, 3, 16, 200, 500, 0)
+    s.n_new[7] += T - 3 - s.n_new.sum()
+    s = Step(T, 40, 3, 16, s.n_new, 500, pad=3)
+    assert s.T == T
+    check(tclora.kv_map(s.cache, *s.tensors(), s.T), s.want_all())
+
+
+def test_nothing_new_and_no_requests():
+    s = Step(1, 12, 3, 16, [0] * 12, 100, pad=4)
+    check(tclora.kv_map(s.cache, *s.tensors(), s.T), s.want_all())
+    s = Step(2, 0, 0, 16, [], 0, pad=3, spare=4)
+    t = [up(x) for x in ([], [0], [], [])] + [up(np.zeros((0, 1)))] + [up(s.free), up([0])]
+    check(tclora.kv_map(s.cache, *t, 3), dict(seq_tok_ptr=[0], pos=[0] * 3, slot=[-1] * 3, used=[0]))
+    # every page taken to the last one
+    s = Step(3, 9, 2, 16, 40, 30, spare=0)
+    st = check(tclora.kv_map(s.cache, *s.tensors(), s.T), s.want_all())
+    assert st[3] == 0
+
+
+BAD = {
+    "negative new": lambda s: s.n_new.__setitem__(3, -1),
+    "negative length": lambda s: s.own_len.__setitem__(3, -1),
+    "too many tokens": lambda s: setattr(s, "T", s.T - 3),
+    "a row of tokens and more": lambda s: s.n_new.__setitem__(3, 0x7fffffff),
+    "beyond the table": lambda s: s.own_len.__setitem__(2, s.ld * s.page),
+    "far beyond the table": lambda s: s.own_len.__setitem__(2, 0x7fffffff),
+    "position": lambda s: s.prefix.__setitem__(slice(None), 0x7fffffff),
+    "negative prefix": lambda s: s.prefix.__setitem__(0, -1),
+    "groups short": lambda s: s.group_seq.__setitem__(-1, len(s.n_new) - 1),
+    "groups late": lambda s: s.group_seq.__setitem__(0, 1),
+    "groups decrease": lambda s: s.group_seq.__setitem__(1, len(s.n_new) + 5),
+    "used negative": lambda s: setattr(s, "used", -1),
+    "used beyond": lambda s: setattr(s, "used", len(s.free) + 1),
+    "free page": lambda s: s.free.__setitem__(s.used, len(s.free)),
+    "free page negative": lambda s: s.free.__setitem__(s.used + 1, -1),
+    "page in use": lambda s: s.pages.__setitem__((slice(None), slice(None)), len(s.free)),
+}
+
+
+@pytest.mark.parametrize("large", [False, True])
+@pytest.mark.parametrize("name", list(BAD))
+def test_a_bad_batch_takes_nothing(name, large):
+    S = 10
+    s = Step(5, S, 3, 16, [1000 if large else 20] * S, 77, pad=2)
+    s.own_len[:] = 77 - np.arange(S) % 3
+    s = fresh(s)
+    BAD[name](s)
+    t = s.tensors()
+    call = tclora.kv_map(s.cache, *t, s.T)
+    st = check(call, dict(seq_tok_ptr=[0] * (S + 1), pos=[0] * s.T, slot=[-1] * s.T,
+                          own_len=s.own_len, used=[s.used], own_pages=s.pages), tclora.EINVAL)
+    assert st[1:3] == (0, 0)
+
+
+def fresh(s):
+    """the step with tables that fit its lengths"""
+    r = np.random.default_rng(9)
+    have, want = -(-s.own_len // s.page), -(-(s.own_len + s.n_new) // s.page)
+    n = int(want.sum()) + 3
+    ids, at = r.permutation(n), 0
+    s.ld = int(want.max())
+    s.pages = np.full((len(s.n_new), s.ld), -7)
+    for i, h in enumerate(have):
+        s.pages[i, :h] = ids[at:at + h]
+        at += h
+    s.free, s.used, s.cache = ids, at, cache_of(n, s.page)
+    return s
+
+
+@pytest.mark.parametrize("new", [20, 1000])
+def test_too_few_pages_take_nothing(new):
+    s = Step(6, 10, 2, 16, [new] * 10, 70, pad=1)
+    need = s.want_all()["used"][0]
+    t = s.tensors()
+    t[5] = t[5][:need - 1].contiguous()
+    call = tclora.kv_map(s.cache, *t, s.T)
+    st = check(call, dict(seq_tok_ptr=[0] * 11, pos=[0] * s.T, slot=[-1] * s.T, own_len=s.own_len,
+                          used=[s.used], own_pages=s.pages), tclora.ENOSPC)
+    assert st == (tclora.ENOSPC, 0, 0, need - 1 - s.used)
+
+
+@pytest.mark.parametrize("new", [1, 1200])
+def test_in_place_replays_go_on(new):
+    """own_len and used updated in place: each replay is the next step, until
+    the pages run out."""
+    S, page, steps = 9, 16, 6
+    r = np.random.default_rng(3)
+    own, grp = r.integers(0, 40, S), np.array([0, 4, S])
+    n_pages = int((-(-(own + steps * new) // page)).sum())
+    ids, at = r.permutation(n_pages), 0
+    pages = np.zeros((S, -(-(40 + (steps + 1) * new) // page)), np.int64)
+    for i, h in enumerate(-(-own // page)):
+        pages[i, :h] = ids[at:at + h]
+        at += h
+    cache = cache_of(n_pages, page)
+    t = [up(x) for x in ([new] * S, grp, [100, 7], own, pages, ids, [at])]
+    call = tclora.MapCall(cache, *t, S * new, own_len_out=t[3], used_out=t[6])
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=st):
+        call()
+    seen = set()
+    for i in range(steps):
+        g.replay()
+        assert call.status()[0] == tclora.OK
+        lens = own + (i + 1) * new
+        assert np.array_equal(t[3].cpu().numpy(), lens)
+        pos, slot = call.pos.cpu().numpy(), call.slot.cpu().numpy()
+        base = np.repeat(np.where(np.arange(S) < 4, 100, 7) + lens - new, new)
+        assert np.array_equal(pos, base + np.tile(np.arange(new), S))
+        assert len(seen & set(slot.tolist())) == 0 and len(set(slot.tolist())) == S * new
+        seen |= set(slot.tolist())
+        key, row = pos - np.repeat(np.where(np.arange(S) < 4, 100, 7), new), np.repeat(np.arange(S), new)
+        tab = t[4].cpu().numpy()
+        assert np.array_equal(slot, tab[row, key // page].astype(np.int64) * page + key % page)
+    while True:  # (some steps more, where the last pages have room)
+        before = t[3].cpu().numpy()
+        g.replay()
+        if call.status()[0] != tclora.OK:
+            break
+    assert call.status()[0] in (tclora.ENOSPC, tclora.EINVAL)
+    assert np.array_equal(t[3].cpu().numpy(), before) and (call.slot == -1).all()
+
+
+def test_slots_beyond_32_bits():
+    n_pages, page = (1 << 22) + 2, 1024
+    K = torch.zeros(1, page, 1, 16, dtype=torch.bfloat16, device=DEV)
+    cache = tclora.KVCache(K, K.clone())
+    cache.desc.n_pages = n_pages  # (only its size is looked at)
+    t = [up(x) for x in ([2, 1], [0, 2], [5], [1023, 0], [[n_pages - 1, -1], [-1, -1]],
+                         [3, n_pages - 2, 0], [1])]
+    call = tclora.kv_map(cache, *t, 3)
+    assert call.status()[0] == tclora.OK
+    assert call.slot.tolist() == [n_pages * 1024 - 1, (n_pages - 2) * 1024, 0]
+
+
+def test_binding_refusals():
+    s = Step(8, 6, 2, 16, 5, 20)
+    t = s.tensors()
+    for i, bad in ((0, t[0].long()), (1, t[1][::2]), (2, t[2][:1]), (3, t[3][:5]), (4, t[4][:, ::2]),
+                   (4, t[4][:5]), (4, t[4].long()), (6, t[0]), (5, t[5].cpu()), (3, t[3].cpu())):
+        a = list(t)
+        a[i] = bad
+        with pytest.raises(ValueError):
+            tclora.kv_map(s.cache, *a, s.T)
+    with pytest.raises(ValueError):
+        tclora.kv_map(s.cache, *t, -1)
+    with pytest.raises(ValueError):
+        tclora.kv_map(s.cache, *t, s.T, own_len_out=t[3][:2])
