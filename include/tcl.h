@@ -882,6 +882,28 @@ int tcl_attn_apply(const tcl_attn_batch *b, const tcl_kv_cache *c, int32_t n_q_h
                    const void *plan, size_t plan_bytes, const void *q, int64_t ldq, void *o,
                    int64_t ldo, float *lse, float scale, void *ws, size_t ws_bytes, void *stream);
 
+/*
+ * Attention with a sliding window and sinks: a token that would see the first
+ * `vis` keys (prefix first) sees key j < vis only if j >= vis - window or j <
+ * sinks: its last `window` keys, itself among them, and the first `sinks` of
+ * the request.  window >= 1, sinks >= 0 (more than the keys there are: all of
+ * them).  Hidden keys are not read but for those in the same step of 64 keys
+ * as visible ones, and reach no row, whatever they hold; pages that lie wholly
+ * before a window are read no more, yet their ids have to be ids of the cache.
+ * The mapping and the call have those of tcl_attn_plan and tcl_attn_apply with
+ * the same sizes, buffers, checks and errors (TCL_EINVAL: window < 1, sinks <
+ * 0 as well); a plan serves the window and sinks that it was made for (a plan
+ * of others, or of none: nothing is written).  Layers with and without windows
+ * need a plan each.
+ */
+int tcl_attn_window_plan(const tcl_attn_batch *b, const tcl_kv_cache *c, int32_t n_q_heads,
+                         int32_t window, int32_t sinks, void *plan, size_t plan_bytes,
+                         void *stream);
+int tcl_attn_window_apply(const tcl_attn_batch *b, const tcl_kv_cache *c, int32_t n_q_heads,
+                          int32_t window, int32_t sinks, const void *plan, size_t plan_bytes,
+                          const void *q, int64_t ldq, void *o, int64_t ldo, float *lse,
+                          float scale, void *ws, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

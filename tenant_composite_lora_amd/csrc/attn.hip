@@ -14,6 +14,13 @@
 // the running maximum and sum are per-lane numbers with one exchange between
 // lane halves (or quarters) a step, and the probabilities leave the first
 // product in the very registers the second wants them in.
+//
+// With a sliding window and sinks (WIN) a row sees its last keys and the first
+// few.  A tile then reads two ranges of keys: the steps that hold sinks and
+// those from its first row's window on.  An item's keys are numbered as if the
+// first range lay right before the second (Work::at, gap), so that items are
+// cut and walked as ever; the keys that a step hides from a row are found from
+// three limits a row instead of one.
 #include <algorithm>
 #include <cmath>
 #include <limits>
@@ -54,7 +61,10 @@ __device__ inline int key_end(int prefix, int n) {
 }
 
 enum { H_CODE, H_MAGIC, H_SEQS, H_GROUPS, H_TOKENS, H_HEADS, H_KVHEADS, H_DIM, H_PAGES, H_SHIFT,
-       H_LDO, H_LDP, H_ITEMS, H_TILES, H_SHARED, H_FLAGS = 16, H_WORDS = 64 };
+       H_LDO, H_LDP, H_ITEMS, H_TILES, H_SHARED, H_WINDOW, H_FLAGS = 16, H_SINKS = 32, H_WORDS = 64 };
+// the largest window and count of sinks that are told apart (more keys than a
+// request can have)
+constexpr int kMaxWindow = 1 << 30;
 constexpr int kPageGroups = 16;  // workgroups that look page ids over, a flag each
 
 struct alignas(16) Work {
@@ -66,7 +76,7 @@ struct alignas(16) Work {
   int32_t lo, hi;   // keys [lo, hi), lo a whole step
   int32_t part;     // first partial row, -1: write the output itself
   int32_t fine;     // weights in two parts (attend_many)
-  int32_t pad[2];
+  int32_t at, gap;  // key number j < at stands for key j - gap (windows; else 0)
 };
 
 struct alignas(16) Tile {
@@ -92,6 +102,7 @@ struct PlanArgs {
   int32_t Hq, Hkv, D, n_pages, page_shift;
   int32_t tpt_many, tpt_few;  // whole tokens in a tile
   int32_t cap_tiles, cap_items, cap_rows, target_few, target_many;
+  int32_t window, sinks;      // window 0: none
   // plan
   int32_t *hdr;
   TokRec *tok;
@@ -101,6 +112,7 @@ struct PlanArgs {
   int32_t *short_tok;  // [S + 1] tokens of short requests before this one
   int32_t *short_seq;  // [S + 1] short requests before this one
   int32_t *utile;      // [G + S] first tile of a unit (groups first)
+  int32_t *glow;       // [G] first key that a group's short requests see by their windows
 };
 
 // The mapping's view of the small arrays: in LDS for up to kMapThreads
@@ -108,11 +120,11 @@ struct PlanArgs {
 // each made up most of the launch), else in memory.
 struct MapView {
   const int32_t *seq_tok, *group_seq, *prefix_len, *own_len;
-  int32_t *short_tok, *short_seq, *utile;
+  int32_t *short_tok, *short_seq, *utile, *glow;
 };
 
 struct Layout {
-  size_t o_tok, o_tiles, o_items, o_list, o_stok, o_sseq, o_utile, total;
+  size_t o_tok, o_tiles, o_items, o_list, o_stok, o_sseq, o_utile, o_glow, total;
 };
 
 // ---------------------------------------------------------------------------
@@ -172,19 +184,52 @@ __device__ inline int tile_hi(const Unit &x, int i) {
   return max(x.lo, key_end(x.prefix, max(0, x.hi - x.n_q + last + 1)));
 }
 
+// The keys of tile i of a unit: numbers [lo, hi), those below `at` standing for
+// the keys `gap` before them.  `at`, `gap` and lo are whole steps.
+struct Span {
+  int lo, hi, at, gap;
+};
+template <bool WIN>
+__device__ inline Span span_of(const PlanArgs &a, const MapView &m, const Unit &x, int i) {
+  Span r{x.lo, tile_hi(x, i), 0, 0};
+  if constexpr (WIN) {
+    constexpr int step = ~(kKeys - 1);
+    const int last = min(x.n_tok, (i + 1) * x.tpt) - 1;
+    // the first key of the first row's window, the keys of the last row
+    int ws, vis;
+    if (x.list) {
+      ws = min(m.glow[x.group], x.prefix);
+      vis = x.prefix;
+    } else {
+      ws = max(0, x.hi - x.n_q + i * x.tpt + 1 - a.window);
+      vis = max(0, x.hi - x.n_q + last + 1);
+    }
+    int start = (ws < x.prefix ? ws : ws + whole(x.prefix) - x.prefix) & step;
+    if (x.list && ws >= x.prefix) r.hi = start = whole(x.prefix);
+    start = max(start, x.lo);
+    const int sink = max(x.lo, (key_end(x.prefix, min(a.sinks, vis)) + kKeys - 1) & step);
+    if (sink < start) {
+      r.at = start;
+      r.gap = start - sink;
+      r.lo = x.lo + r.gap;
+    }
+  }
+  return r;
+}
+
 // 64 requests 10.4 us, 8 prompts of 512 tokens 11.2, 3 requests 7.8: a launch
 // and the round trips of some fifteen phases.
 // Workgroups 1 .. kPageGroups look page ids over, a row of a page table a wave,
 // and leave a flag each; workgroup 0 does the rest.  One launch: the flags
 // are read with the header.
-template <bool LDS>
+template <bool LDS, bool WIN>
 __global__ __launch_bounds__(kMapThreads) void attn_plan_kernel(PlanArgs a) {
   __shared__ int lds[3][kMapThreads / 64];
   __shared__ int s_err, s_chunk[2];
   __shared__ unsigned long long s_work;
   constexpr int NS = LDS ? kMapThreads + 1 : 1;
   __shared__ int32_t l_seq_tok[NS], l_group_seq[NS], l_prefix_len[NS], l_own_len[NS],
-      l_short_tok[NS], l_short_seq[NS], l_utile[2 * NS];
+      l_short_tok[NS], l_short_seq[NS], l_utile[2 * NS], l_glow[WIN ? NS : 1];
   __shared__ int32_t l_unit[kMapThreads], l_place[kMapThreads], l_item[kMapThreads], l_row[kMapThreads];
   const int tid = threadIdx.x, gq = a.Hq / a.Hkv;
   const int page = 1 << a.page_shift;
@@ -211,7 +256,7 @@ __global__ __launch_bounds__(kMapThreads) void attn_plan_kernel(PlanArgs a) {
     if (tid == 0) a.hdr[H_FLAGS + blockIdx.x - 1] = s_err;
     return;
   }
-  MapView m{a.seq_tok, a.group_seq, a.prefix_len, a.own_len, a.short_tok, a.short_seq, a.utile};
+  MapView m{a.seq_tok, a.group_seq, a.prefix_len, a.own_len, a.short_tok, a.short_seq, a.utile, a.glow};
   if constexpr (LDS) {
     if (a.S > 0) {
       for (int i = tid; i <= a.S; i += kMapThreads) l_seq_tok[i] = a.seq_tok[i];
@@ -219,7 +264,7 @@ __global__ __launch_bounds__(kMapThreads) void attn_plan_kernel(PlanArgs a) {
       if (tid < a.S) l_own_len[tid] = a.own_len[tid];
       if (tid < a.G) l_prefix_len[tid] = a.prefix_len[tid];
     }
-    m = MapView{l_seq_tok, l_group_seq, l_prefix_len, l_own_len, l_short_tok, l_short_seq, l_utile};
+    m = MapView{l_seq_tok, l_group_seq, l_prefix_len, l_own_len, l_short_tok, l_short_seq, l_utile, l_glow};
   }
   if (tid == 0) {
     a.hdr[H_MAGIC] = kMagic, a.hdr[H_SEQS] = a.S, a.hdr[H_GROUPS] = a.G, a.hdr[H_TOKENS] = a.T;
@@ -227,6 +272,7 @@ __global__ __launch_bounds__(kMapThreads) void attn_plan_kernel(PlanArgs a) {
     a.hdr[H_PAGES] = a.n_pages, a.hdr[H_SHIFT] = a.page_shift;
     a.hdr[H_LDO] = a.ldo, a.hdr[H_LDP] = a.ldp;
     a.hdr[H_CODE] = TCL_OK, a.hdr[H_ITEMS] = 0, a.hdr[H_TILES] = 0, a.hdr[H_SHARED] = 0;
+    a.hdr[H_WINDOW] = WIN ? a.window : 0, a.hdr[H_SINKS] = WIN ? a.sinks : 0;
   }
   __syncthreads();
   // the table
@@ -267,14 +313,27 @@ __global__ __launch_bounds__(kMapThreads) void attn_plan_kernel(PlanArgs a) {
     m.short_tok[a.S] = tok_base;
     m.short_seq[a.S] = seq_base;
   }
+  if constexpr (WIN)
+    for (int g = tid; g < a.G; g += kMapThreads) m.glow[g] = 0x7fffffff;
   __syncthreads();
+  if constexpr (WIN) {
+    for (int s = tid; s < a.S; s += kMapThreads) {
+      const int q = m.seq_tok[s + 1] - m.seq_tok[s], g = upper(m.group_seq, a.G, s);
+      if (is_short(a, q))  // (a minimum: any order)
+        atomicMin(&m.glow[g], max(0, m.prefix_len[g] + m.own_len[s] - q + 1 - a.window));
+    }
+    __syncthreads();
+  }
   // keys over all tiles: the length of an item
   const int U = a.G + a.S;
   unsigned long long work = 0;
   for (int u = tid; u < U; u += kMapThreads) {
     const Unit x = unit_of(a, m, u);
     const int n = unit_tiles(x);
-    for (int i = 0; i < n; ++i) work += unsigned(tile_hi(x, i) - x.lo);
+    for (int i = 0; i < n; ++i) {
+      const Span k = span_of<WIN>(a, m, x, i);
+      work += unsigned(k.hi - k.lo);
+    }
   }
   if (work) atomicAdd(&s_work, work);  // (an integer sum: any order)
   __syncthreads();
@@ -301,12 +360,13 @@ __global__ __launch_bounds__(kMapThreads) void attn_plan_kernel(PlanArgs a) {
   int item_base = 0, row_base = 0;
   struct Cut {
     Unit x;
-    int i, hi, nt, ns, per;
+    Span k;
+    int i, nt, ns, per;
   };
   auto cut = [&](int u, int i) {
-    Cut c{unit_of(a, m, u), i, 0, 0, 0, 0};
-    c.hi = tile_hi(c.x, i);
-    const int len = c.hi - c.x.lo, chunk = s_chunk[c.x.rows > kFew];
+    Cut c{unit_of(a, m, u), {}, i, 0, 0, 0};
+    c.k = span_of<WIN>(a, m, c.x, i);
+    const int len = c.k.hi - c.k.lo, chunk = s_chunk[c.x.rows > kFew];
     c.nt = min(c.x.n_tok, (i + 1) * c.x.tpt) - i * c.x.tpt;
     c.ns = max(1, (len + chunk - 1) / chunk);
     // even lengths, whole steps
@@ -336,11 +396,11 @@ __global__ __launch_bounds__(kMapThreads) void attn_plan_kernel(PlanArgs a) {
     for (int k = tid; k < total[0]; k += kMapThreads) {
       const int j = upper(l_item, here, k), n = k - l_item[j];
       c = cut(l_unit[j], l_place[j]);
-      const int lo = min(c.hi, c.x.lo + n * c.per), row = l_row[j] + n * c.nt * gq;
+      const int lo = min(c.k.hi, c.k.lo + n * c.per), row = l_row[j] + n * c.nt * gq;
       if (item_base + k >= a.cap_items || row + c.nt * gq > a.cap_rows) continue;
       a.items[item_base + k] = Work{c.x.tok0 + c.i * c.x.tpt, c.x.list, c.nt, c.x.seq, c.x.group,
-                                    c.x.prefix, lo, min(c.hi, lo + c.per), direct(c) ? -1 : row,
-                                    c.x.list || is_short(a, c.x.n_q), {}};
+                                    c.x.prefix, lo, min(c.k.hi, lo + c.per), direct(c) ? -1 : row,
+                                    c.x.list || is_short(a, c.x.n_q), c.k.at, c.k.gap};
     }
     item_base += total[0], row_base += total[1];
     __syncthreads();
@@ -405,6 +465,7 @@ struct AttnArgs {
   float scale2;    // |scale| * log2(e)
   int32_t q_sign;  // the sign bit of a bf16 number where scale is negative
   int32_t S, G, T, ldp, ld_own, Hq;
+  int32_t window, sinks;  // window 0: none
   const int32_t *prefix_pages, *own_pages;
   const int32_t *hdr;
   const TokRec *tok;
@@ -420,7 +481,8 @@ __device__ inline bool plan_fits(const AttnArgs &a) {
   return h[H_MAGIC] == kMagic && h[H_CODE] == TCL_OK && h[H_SEQS] == a.S && h[H_GROUPS] == a.G &&
          h[H_TOKENS] == a.T && h[H_HEADS] == a.Hq && h[H_KVHEADS] == a.c.H && h[H_DIM] == a.c.D &&
          h[H_PAGES] == a.c.n_pages && h[H_SHIFT] == a.c.page_shift && h[H_LDO] == a.ld_own &&
-         h[H_LDP] == a.ldp && pages_ok(h);
+         h[H_LDP] == a.ldp && h[H_WINDOW] == a.window && (!a.window || h[H_SINKS] == a.sinks) &&
+         pages_ok(h);
 }
 
 typedef __attribute__((__vector_size__(16 * sizeof(float)))) float f32x16_t;
@@ -590,6 +652,26 @@ __device__ inline int step_end(const Work &t, int vis, int j0) {
   return j0 < w ? min(vis, t.prefix) : vis + w - t.prefix;
 }
 
+// The first key of step n of an item.
+template <bool WIN>
+__device__ inline int step_at(const Work &t, int n) {
+  const int j = t.lo + n * kKeys;
+  return WIN && j < t.at ? j - t.gap : j;
+}
+
+// Keys of the step at j0 below low(vis) are hidden from a row with `vis` keys
+// by its window, but for those below sink_end().
+__device__ inline int own_shift(const Work &t, int j0) {
+  const int w = whole(t.prefix);
+  return j0 < w ? 0 : w - t.prefix;
+}
+__device__ inline int low(const AttnArgs &a, const Work &t, int vis, int j0) {
+  return vis - a.window + own_shift(t, j0);
+}
+__device__ inline int sink_end(const AttnArgs &a, const Work &t, int j0) {
+  return a.sinks + own_shift(t, j0);
+}
+
 // value d of row r in LDS
 template <int D>
 __device__ inline uint32_t value_at(const uint16_t *sv, int r, int d) {
@@ -639,20 +721,20 @@ __device__ inline float half_max(float v) {
 // needs no barrier; the waves' results are joined through LDS.  Bound by the
 // keys' and values' bytes: 64 requests of 8 tenants, 760 MB with the prefixes,
 // 150 us, 5.1 TB/s.
-template <int D>
+template <int D, bool WIN>
 __device__ inline void attend_few(const AttnArgs &a, const Work &t, int h, int gq, Smem<D> &sm) {
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   const int rows = t.n_tok * gq, steps = (t.hi - t.lo + kKeys - 1) / kKeys;
   Stage<D> st;
   st.init(a, h);
-  if (steps > 0) st.pages(a, t, t.lo);
+  if (steps > 0) st.pages(a, t, step_at<WIN>(t, 0));
   const int c = lane & 15, g = lane >> 4;
   const bool live = c < rows;
   const int tok = token_of(a, t, gq, live ? c : 0);
   const int hq = h * gq + (live ? c : 0) % gq;
   if (steps > 0) {
-    st.load(a, t, t.lo);
-    st.pages(a, t, t.lo + kKeys);
+    st.load(a, t, step_at<WIN>(t, 0));
+    st.pages(a, t, step_at<WIN>(t, 1));
   }
   const int vis = live ? a.tok[tok].vis : 0;
   s16x8 qf[D / 32];
@@ -665,13 +747,13 @@ __device__ inline void attend_few(const AttnArgs &a, const Work &t, int h, int g
   for (int i = 0; i < D / 16; ++i) o[i] = f32x4_t{0, 0, 0, 0};
   float m = -INFINITY, l = 0.f;
   for (int n = 0; n < steps; ++n) {
-    const int j0 = t.lo + n * kKeys, b = n & 1;
+    const int j0 = step_at<WIN>(t, n), b = n & 1;
     st.put(sm.k[b], sm.v[b]);
     // (here in every step: a weight's second part may be zero or negative)
     const bool rare = __any(st.bad());
     if (n + 1 < steps) {
-      st.load(a, t, j0 + kKeys);
-      st.pages(a, t, j0 + 2 * kKeys);
+      st.load(a, t, step_at<WIN>(t, n + 1));
+      st.pages(a, t, step_at<WIN>(t, n + 2));
     }
     // (a wave reads only what it wrote)
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
@@ -687,9 +769,12 @@ __device__ inline void attend_few(const AttnArgs &a, const Work &t, int h, int g
     float p[4], mx = -INFINITY;
     // visible keys of the lane's four
     const int left = min(step_end(t, vis, j0), t.hi) - (j0 + 16 * w + 4 * g);
+    // (of a window: hidden from `past` up to `from`)
+    const int past = WIN ? sink_end(a, t, j0) - (j0 + 16 * w + 4 * g) : 0;
+    const int from = WIN ? low(a, t, vis, j0) - (j0 + 16 * w + 4 * g) : 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      p[i] = i < left ? s4[i] : -INFINITY;
+      p[i] = i < left && (!WIN || i < past || i >= from) ? s4[i] : -INFINITY;
       mx = fmaxf(mx, p[i]);
     }
     mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
@@ -722,7 +807,7 @@ __device__ inline void attend_few(const AttnArgs &a, const Work &t, int h, int g
       for (int k = 0; k < 16; ++k) {
         const float q = k & 2 ? (k & 1 ? p[3] : p[2]) : (k & 1 ? p[1] : p[0]);
         const float pk = __shfl(q, c + 16 * (k >> 2), 64);
-        if (k >= left + 4 * g) continue;
+        if (k >= left + 4 * g || (WIN && k >= past + 4 * g && k < from + 4 * g)) continue;
 #pragma unroll
         for (int d = 0; d < D / 16; ++d)
 #pragma unroll
@@ -908,26 +993,34 @@ struct Direct {
 // anyway (64 requests over a prefix of 8192: 43 us with one part, 46 with two;
 // of 8 tenants 158 and 159).  One for long requests, where the matrix cores
 // bound (chunks of 8 requests over 4096: 296 us, with two 391).
-template <int D, bool FINE>
+template <int D, bool FINE, bool WIN>
 __device__ inline void attend_many(const AttnArgs &a, const Work &t, int h, int gq, Smem<D> &sm) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int rows = t.n_tok * gq, steps = (t.hi - t.lo + kKeys - 1) / kKeys;
   Direct<D> st;
   st.init(a, h);
-  st.pages(a, t, t.lo);
+  st.pages(a, t, step_at<WIN>(t, 0));
   const int c = lane & 31, g = lane >> 5;
   const int r = 32 * w + c;
   const bool live = r < rows, busy = 32 * w < rows;
   const int tok = token_of(a, t, gq, live ? r : 0);
   const int hq = h * gq + (live ? r : 0) % gq;
-  if (steps > 0) st.load(a, t, t.lo, sm.k[0], sm.v[0]);
-  st.pages(a, t, t.lo + kKeys);
+  if (steps > 0) st.load(a, t, step_at<WIN>(t, 0), sm.k[0], sm.v[0]);
+  st.pages(a, t, step_at<WIN>(t, 1));
   const int vis = a.tok[tok].vis;
   // the fewest keys a row of the wave sees: a step beyond them hides some
   int least = live ? vis : 0x7fffffff;
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) least = min(least, __shfl_xor(least, x, 64));
   least = __builtin_amdgcn_readfirstlane(least);
+  // and the most: a step before the window of its row hides some
+  int most = 0;
+  if constexpr (WIN) {
+    most = live ? vis : 0;
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) most = max(most, __shfl_xor(most, x, 64));
+    most = __builtin_amdgcn_readfirstlane(most);
+  }
   s16x8 qf[D / 16];
 #pragma unroll
   for (int s = 0; s < D / 16; ++s)
@@ -951,24 +1044,32 @@ __device__ inline void attend_many(const AttnArgs &a, const Work &t, int h, int 
     vpos[x] = vr * D + 8 * ((2 * sub + ((i16 & 3) >> 1)) ^ swz<D>(vr)) + 4 * (i16 & 1);
   }
   // the whole tile's fewest keys: steps beyond them look their values over
-  __shared__ int s_least[4];
+  __shared__ int s_least[4], s_most[WIN ? 4 : 1];
   if (lane == 0) s_least[w] = least;
+  if (WIN && lane == 0) s_most[w] = most;
   __syncthreads();
   const int tile_least = __builtin_amdgcn_readfirstlane(
       min(min(s_least[0], s_least[1]), min(s_least[2], s_least[3])));
-  auto hides = [&](int j0, int least_) { return j0 + kKeys > min(step_end(t, least_, j0), t.hi); };
+  int tile_most = 0;
+  if constexpr (WIN)
+    tile_most = __builtin_amdgcn_readfirstlane(max(max(s_most[0], s_most[1]), max(s_most[2], s_most[3])));
+  auto hides = [&](int j0, int least_, int most_) {
+    bool h = j0 + kKeys > min(step_end(t, least_, j0), t.hi);
+    if constexpr (WIN) h |= j0 < low(a, t, most_, j0) && j0 + kKeys > sink_end(a, t, j0);
+    return h;
+  };
   for (int n = 0; n < steps; ++n) {
-    const int j0 = t.lo + n * kKeys, b = n & 1;
+    const int j0 = step_at<WIN>(t, n), b = n & 1;
     // this step's keys and values have come; every wave is done with the
     // buffers that the next loads write
     st.arrived();
     lds_barrier();
     if (n + 1 < steps) {
-      st.load(a, t, j0 + kKeys, sm.k[b ^ 1], sm.v[b ^ 1]);
-      st.pages(a, t, j0 + 2 * kKeys);
+      st.load(a, t, step_at<WIN>(t, n + 1), sm.k[b ^ 1], sm.v[b ^ 1]);
+      st.pages(a, t, step_at<WIN>(t, n + 2));
     }
     bool rare = false;
-    if (hides(j0, tile_least)) rare = __syncthreads_or(st.bad(sm.v[b]));
+    if (hides(j0, tile_least, tile_most)) rare = __syncthreads_or(st.bad(sm.v[b]));
     uint32_t pw[4][4], pl[4][4];
     if (busy) {
       const uint16_t *sk = sm.k[0];
@@ -995,13 +1096,17 @@ __device__ inline void attend_many(const AttnArgs &a, const Work &t, int h, int 
         if (i + AHEAD < D / 8) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
       }
       __builtin_amdgcn_sched_barrier(0);
-      if (hides(j0, least)) {
+      if (hides(j0, least, most)) {
         const int end = min(step_end(t, vis, j0), t.hi);
+        const int past = WIN ? sink_end(a, t, j0) - j0 - 4 * g : 0;
+        const int from = WIN ? low(a, t, vis, j0) - j0 - 4 * g : 0;
 #pragma unroll
         for (int x = 0; x < 2; ++x)
 #pragma unroll
-          for (int e = 0; e < 16; ++e)  // (a constant against the lane's limit)
-            if (32 * x + 8 * (e / 4) + e % 4 >= end - j0 - 4 * g) s2[x][e] = -INFINITY;
+          for (int e = 0; e < 16; ++e) {  // (a constant against the lane's limits)
+            const int k = 32 * x + 8 * (e / 4) + e % 4;
+            if (k >= end - j0 - 4 * g || (WIN && k >= past && k < from)) s2[x][e] = -INFINITY;
+          }
       }
       float mx = -INFINITY;
 #pragma unroll
@@ -1056,6 +1161,7 @@ __device__ inline void attend_many(const AttnArgs &a, const Work &t, int h, int 
           u = __shfl(int(u), c + 32 * (k >> 2 & 1), 64);
           const float wk = k & 1 ? bf16_hi(u) : bf16_lo(u);
           if (j0 + k >= end) continue;
+          if (WIN && j0 + k >= sink_end(a, t, j0) && j0 + k < low(a, t, vis, j0)) continue;
 #pragma unroll
           for (int i = 0; i < D / 32; ++i)
 #pragma unroll
@@ -1120,7 +1226,7 @@ __device__ inline void attend_many(const AttnArgs &a, const Work &t, int h, int 
   }
 }
 
-template <int D>
+template <int D, bool WIN>
 __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_kernel(AttnArgs a) {
   __shared__ __align__(16) Smem<D> sm;
   if (!plan_fits(a)) return;
@@ -1131,11 +1237,11 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_kernel(AttnArgs a)
   const Work t = a.items[id];
   const int gq = a.Hq / a.c.H;
   if (t.n_tok * gq <= kFew)
-    attend_few<D>(a, t, h, gq, sm);
+    attend_few<D, WIN>(a, t, h, gq, sm);
   else if (t.fine)
-    attend_many<D, true>(a, t, h, gq, sm);
+    attend_many<D, true, WIN>(a, t, h, gq, sm);
   else
-    attend_many<D, false>(a, t, h, gq, sm);
+    attend_many<D, false, WIN>(a, t, h, gq, sm);
 }
 
 // Joins the items of a token's rows, a row a wave at a time: maxima first,
@@ -1271,6 +1377,7 @@ void sizes(const tcl_attn_batch *b, const KvArgs &kv, int32_t Hq, PlanArgs *a, L
   L->o_stok = take((size_t(a->S) + 1) * 4);
   L->o_sseq = take((size_t(a->S) + 1) * 4);
   L->o_utile = take((size_t(a->S) + a->G) * 4);
+  L->o_glow = take(size_t(a->G) * 4);
   L->total = at;
 }
 
@@ -1284,9 +1391,19 @@ int check_plan(const void *plan, size_t bytes, size_t need) {
   return TCL_OK;
 }
 
+int check_window(int32_t window, int32_t sinks) {
+  if (window < 1) return fail(TCL_EINVAL, "attn: window %d < 1", window);
+  if (sinks < 0) return fail(TCL_EINVAL, "attn: sinks %d < 0", sinks);
+  return TCL_OK;
+}
+
 template <int D>
 void launch(const AttnArgs &a, int cap_items, hipStream_t s) {
-  hipLaunchKernelGGL(attn_kernel<D>, dim3(unsigned(cap_items) * a.c.H), dim3(256), 0, s, a);
+  const dim3 grid(unsigned(cap_items) * a.c.H);
+  if (a.window)
+    hipLaunchKernelGGL((attn_kernel<D, true>), grid, dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((attn_kernel<D, false>), grid, dim3(256), 0, s, a);
   // a row a wave, until that is eight workgroups a CU and more
   const int by_row = (a.Hq + 3) / 4, parts = a.T >= 2048 ? 1 : std::min(by_row, 4096 / a.T + 1);
   hipLaunchKernelGGL(attn_join_kernel<D>, dim3(a.T, parts), dim3(256), 0, s, a);
@@ -1323,8 +1440,12 @@ extern "C" int tcl_attn_workspace_bytes(const tcl_attn_batch *b, const tcl_kv_ca
   return TCL_OK;
 }
 
-extern "C" int tcl_attn_plan(const tcl_attn_batch *b, const tcl_kv_cache *c, int32_t n_q_heads,
-                             void *plan, size_t plan_bytes, void *stream) {
+namespace tcl {
+namespace {
+
+// window 0: every earlier key is visible
+int map_batch(const tcl_attn_batch *b, const tcl_kv_cache *c, int32_t n_q_heads, int32_t window,
+              int32_t sinks, void *plan, size_t plan_bytes, void *stream) {
   KvArgs kv;
   int rc = check_batch(b, c, n_q_heads, &kv);
   if (rc) return rc;
@@ -1347,31 +1468,28 @@ extern "C" int tcl_attn_plan(const tcl_attn_batch *b, const tcl_kv_cache *c, int
   a.short_tok = reinterpret_cast<int32_t *>(p + L.o_stok);
   a.short_seq = reinterpret_cast<int32_t *>(p + L.o_sseq);
   a.utile = reinterpret_cast<int32_t *>(p + L.o_utile);
+  a.glow = reinterpret_cast<int32_t *>(p + L.o_glow);
+  a.window = std::min(window, kMaxWindow), a.sinks = std::min(sinks, kMaxWindow);
   const dim3 grid(1 + kPageGroups), block(kMapThreads);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (a.S <= kMapThreads && a.G <= kMapThreads)
-    hipLaunchKernelGGL(attn_plan_kernel<true>, grid, block, 0, s, a);
+  const bool small = a.S <= kMapThreads && a.G <= kMapThreads;
+  if (small && window)
+    hipLaunchKernelGGL((attn_plan_kernel<true, true>), grid, block, 0, s, a);
+  else if (small)
+    hipLaunchKernelGGL((attn_plan_kernel<true, false>), grid, block, 0, s, a);
+  else if (window)
+    hipLaunchKernelGGL((attn_plan_kernel<false, true>), grid, block, 0, s, a);
   else
-    hipLaunchKernelGGL(attn_plan_kernel<false>, grid, block, 0, s, a);
+    hipLaunchKernelGGL((attn_plan_kernel<false, false>), grid, block, 0, s, a);
   TCL_HIP(hipGetLastError());
   return TCL_OK;
 }
 
-extern "C" int tcl_attn_status_async(const void *plan, int32_t *dev_status, void *stream) {
-  if (!plan || !dev_status) return fail(TCL_EINVAL, "attn: plan and dev_status are required");
-  if (misaligned(plan, 256) || misaligned(dev_status, 4))
-    return fail(TCL_EALIGN, "attn: plan must be 256-byte, dev_status 4-byte aligned");
-  hipLaunchKernelGGL(attn_status_kernel, dim3(1), dim3(64), 0, static_cast<hipStream_t>(stream),
-                     static_cast<const int32_t *>(plan), dev_status);
-  TCL_HIP(hipGetLastError());
-  return TCL_OK;
-}
-
-extern "C" int tcl_attn_apply(const tcl_attn_batch *b, const tcl_kv_cache *c, int32_t n_q_heads,
-                              const void *plan, size_t plan_bytes, const void *q, int64_t ldq,
-                              void *o, int64_t ldo, float *lse, float scale, void *ws,
-                              size_t ws_bytes, void *stream) {
+int attend(const tcl_attn_batch *b, const tcl_kv_cache *c, int32_t n_q_heads, int32_t window,
+           int32_t sinks, const void *plan, size_t plan_bytes, const void *q, int64_t ldq, void *o,
+           int64_t ldo, float *lse, float scale, void *ws, size_t ws_bytes, void *stream) {
   AttnArgs a{};
+  a.window = std::min(window, kMaxWindow), a.sinks = std::min(sinks, kMaxWindow);
   int rc = check_batch(b, c, n_q_heads, &a.c);
   if (rc) return rc;
   PlanArgs s{};
@@ -1416,4 +1534,48 @@ extern "C" int tcl_attn_apply(const tcl_attn_batch *b, const tcl_kv_cache *c, in
   }
   TCL_HIP(hipGetLastError());
   return TCL_OK;
+}
+
+}  // namespace
+}  // namespace tcl
+
+extern "C" int tcl_attn_plan(const tcl_attn_batch *b, const tcl_kv_cache *c, int32_t n_q_heads,
+                             void *plan, size_t plan_bytes, void *stream) {
+  return map_batch(b, c, n_q_heads, 0, 0, plan, plan_bytes, stream);
+}
+
+extern "C" int tcl_attn_window_plan(const tcl_attn_batch *b, const tcl_kv_cache *c,
+                                    int32_t n_q_heads, int32_t window, int32_t sinks, void *plan,
+                                    size_t plan_bytes, void *stream) {
+  const int rc = check_window(window, sinks);
+  return rc ? rc : map_batch(b, c, n_q_heads, window, sinks, plan, plan_bytes, stream);
+}
+
+extern "C" int tcl_attn_status_async(const void *plan, int32_t *dev_status, void *stream) {
+  if (!plan || !dev_status) return fail(TCL_EINVAL, "attn: plan and dev_status are required");
+  if (misaligned(plan, 256) || misaligned(dev_status, 4))
+    return fail(TCL_EALIGN, "attn: plan must be 256-byte, dev_status 4-byte aligned");
+  hipLaunchKernelGGL(attn_status_kernel, dim3(1), dim3(64), 0, static_cast<hipStream_t>(stream),
+                     static_cast<const int32_t *>(plan), dev_status);
+  TCL_HIP(hipGetLastError());
+  return TCL_OK;
+}
+
+extern "C" int tcl_attn_apply(const tcl_attn_batch *b, const tcl_kv_cache *c, int32_t n_q_heads,
+                              const void *plan, size_t plan_bytes, const void *q, int64_t ldq,
+                              void *o, int64_t ldo, float *lse, float scale, void *ws,
+                              size_t ws_bytes, void *stream) {
+  return attend(b, c, n_q_heads, 0, 0, plan, plan_bytes, q, ldq, o, ldo, lse, scale, ws, ws_bytes,
+                stream);
+}
+
+extern "C" int tcl_attn_window_apply(const tcl_attn_batch *b, const tcl_kv_cache *c,
+                                     int32_t n_q_heads, int32_t window, int32_t sinks,
+                                     const void *plan, size_t plan_bytes, const void *q,
+                                     int64_t ldq, void *o, int64_t ldo, float *lse, float scale,
+                                     void *ws, size_t ws_bytes, void *stream) {
+  const int rc = check_window(window, sinks);
+  return rc ? rc
+            : attend(b, c, n_q_heads, window, sinks, plan, plan_bytes, q, ldq, o, ldo, lse, scale,
+                     ws, ws_bytes, stream);
 }

@@ -39,7 +39,8 @@ EXPORTS = ["tcl_last_error", "tcl_version", "tcl_plan_bytes", "tcl_plan_map", "t
            "tcl_i8_quant", "tcl_i8_product", "tcl_i8_workspace_bytes", "tcl_i8_linear",
            "tcl_i8_pack_bytes", "tcl_i8_pack",
            "tcl_kv_append", "tcl_attn_plan_bytes", "tcl_attn_workspace_bytes", "tcl_attn_plan",
-           "tcl_attn_status_async", "tcl_attn_apply", "tcl_kv_append_norm", "tcl_kv_map"]
+           "tcl_attn_status_async", "tcl_attn_apply", "tcl_kv_append_norm", "tcl_kv_map",
+           "tcl_attn_window_plan", "tcl_attn_window_apply"]
 
 # bytes of the static device workspace of tcl_fused_apply_noalloc
 SCRATCH_BYTES = 32 << 20
@@ -187,6 +188,8 @@ def lib(path: Optional[str] = None):
     L.tcl_attn_status_async.argtypes = [vp, vp, vp]
     L.tcl_attn_apply.argtypes = [bp, cp, i32, vp, sz, vp, i64, vp, i64, vp, ctypes.c_float, vp, sz,
                                  vp]
+    L.tcl_attn_window_plan.argtypes = [bp, cp, i32, i32, i32, vp, sz, vp]
+    L.tcl_attn_window_apply.argtypes = [bp, cp, i32, i32, *L.tcl_attn_apply.argtypes[2:]]
     L.tcl_lag_select.argtypes = [vp, vp, vp, i32, vp, i32, ctypes.c_double, ctypes.c_double,
                                  i32, i32, vp, vp]
     if path is None:
@@ -1206,15 +1209,22 @@ class AttnPlan:
     that share a prefix.  int32 device tensors: seq_tok_ptr [n_seqs + 1],
     group_seq_ptr [n_groups + 1], prefix_len [n_groups], prefix_pages
     [n_groups, m], own_len [n_seqs], own_pages [n_seqs, n].  One plan serves
-    every layer whose cache has the sizes of ``cache``.  The mapping runs on
-    ``stream`` or the current one: calls on others have to be ordered behind
-    it, and the tables are read by them too."""
+    every layer whose cache has the sizes of ``cache``.  With ``window`` a
+    token sees its last ``window`` keys and the request's first ``sinks``
+    (tcl_attn_window_plan).  The mapping runs on ``stream`` or the current one:
+    calls on others have to be ordered behind it, and the tables are read by
+    them too."""
 
     def __init__(self, cache: KVCache, n_q_heads: int, seq_tok_ptr: torch.Tensor,
                  group_seq_ptr: torch.Tensor, prefix_len: torch.Tensor,
                  prefix_pages: torch.Tensor, own_len: torch.Tensor, own_pages: torch.Tensor,
-                 n_tokens: int, stream=None):
+                 n_tokens: int, stream=None, window: Optional[int] = None, sinks: int = 0):
+        if window is None and sinks:
+            raise ValueError("AttnPlan: sinks without a window")
         self.cache, self.n_q_heads, self.n_tokens = cache, int(n_q_heads), int(n_tokens)
+        self.window, self.sinks = window, sinks
+        most = (1 << 31) - 1  # (more than the keys there can be)
+        self.limits = () if window is None else (min(int(window), most), min(int(sinks), most))
         self.device = cache.device
         self.home = _stream(self.device)
         self._set(seq_tok_ptr, group_seq_ptr, prefix_len, prefix_pages, own_len, own_pages)
@@ -1249,8 +1259,8 @@ class AttnPlan:
         self.batch_ref = ctypes.byref(self.batch)
 
     def _map(self, stream):
-        _call(self.device, lib().tcl_attn_plan,
-              (ctypes.byref(self.batch), ctypes.byref(self.cache.desc), self.n_q_heads,
+        _call(self.device, lib().tcl_attn_window_plan if self.limits else lib().tcl_attn_plan,
+              (ctypes.byref(self.batch), ctypes.byref(self.cache.desc), self.n_q_heads, *self.limits,
                self.buf.data_ptr(), self.buf.numel()), stream, (self.buf, self.home))
 
     def remap(self, seq_tok_ptr, group_seq_ptr, prefix_len, prefix_pages, own_len, own_pages,
@@ -1286,8 +1296,8 @@ class AttnPlan:
 
 
 class AttnCall:
-    """Pre-marshalled arguments of tcl_attn_apply for repeated calls: each
-    call writes o (bf16 [n_tokens, q heads * head_dim], made here unless
+    """Pre-marshalled arguments of tcl_attn_apply (tcl_attn_window_apply for
+    a plan with a window) for repeated calls: each call writes o (bf16 [n_tokens, q heads * head_dim], made here unless
     given) and, if given, lse (fp32 [n_tokens, q heads]).  ``cache`` is the
     layer's (the plan's by default); the workspace is the call's own, or
     ``ws``; calls that may run at the same time need one each."""
@@ -1320,9 +1330,9 @@ class AttnCall:
         self._made = _Made(plan.device) if made and not _once else None
         home = _stream(plan.device)
         self._own = ((ws, home), (o, home), (plan.buf, plan.home))
-        self._fn = lib().tcl_attn_apply
+        self._fn = lib().tcl_attn_window_apply if plan.limits else lib().tcl_attn_apply
         self._args = _packed(self._fn, (
-            None, ctypes.byref(cache.desc), plan.n_q_heads, plan.buf.data_ptr(), plan.buf.numel(),
+            None, ctypes.byref(cache.desc), plan.n_q_heads, *plan.limits, plan.buf.data_ptr(), plan.buf.numel(),
             q.data_ptr(), self.ldq, o.data_ptr(), self.ldo, _ptr(lse), self.scale, ws.data_ptr(),
             ws.numel() * ws.element_size()))[1:]
 

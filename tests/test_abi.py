@@ -609,3 +609,37 @@ def test_kv_map_host_errors(L):
     assert [call(**{n: P + 2}) for n in ints] == [A] * 12 and call(slot=P + 4) == A
     N = 1 << 24
     assert [call(n_seqs=N), call(n_groups=N), call(n_tokens=N), call(ld_own=1 << 25)] == [U] * 4
+
+
+def test_attn_window_host_errors(L):
+    """The windowed attention refuses bad windows, and what the one without
+    refuses (no GPU)."""
+    P = 0x1000
+    E, A, U = tclora.EINVAL, tclora.EALIGN, tclora.EUNSUPPORTED
+    c = ctypes.byref(tclora.KVDesc(4, 16, 2, 64, 2048, 64, 1024, P, P))
+    out = ctypes.c_size_t(0)
+
+    def batch(**kw):
+        bd = dict(n_seqs=3, n_groups=2, n_tokens=5, ld_prefix=4, ld_own=4, seq_tok_ptr=P,
+                  group_seq_ptr=P, prefix_len=P, prefix_pages=P, own_len=P, own_pages=P)
+        bd.update(kw)
+        return ctypes.byref(tclora.AttnBatch(**bd))
+
+    assert L.tcl_attn_plan_bytes(batch(), c, 4, ctypes.byref(out)) == 0
+    need = out.value
+    assert L.tcl_attn_workspace_bytes(batch(), c, 4, ctypes.byref(out)) == 0
+    ws = out.value
+
+    def plan(Hq=4, W=8, N=2, p=0x10000, n=need, **kw):
+        return L.tcl_attn_window_plan(batch(**kw), c, Hq, W, N, p, n, None)
+
+    def apply(Hq=4, W=8, N=2, p=0x10000, n=need, q=P, o=P, w=0x20000, wn=ws, ldq=256, **kw):
+        return L.tcl_attn_window_apply(batch(**kw), c, Hq, W, N, p, n, q, ldq, o, 256, None, 0.1, w, wn, None)
+
+    for f in (plan, apply):
+        assert [f(W=0), f(W=-5), f(N=-1), f(Hq=5), f(n_seqs=-1), f(own_len=None), f(p=None)] == [E] * 7
+        assert [f(p=0x10010), f(n=need - 1), f(own_pages=P + 1), f(n_tokens=1 << 28)] == [
+            A, tclora.ENOSPC, A, U]
+    assert [apply(q=None), apply(o=None), apply(w=None), apply(ldq=192)] == [E] * 4
+    assert apply(wn=ws - 1) == tclora.ENOSPC and apply(q=P + 8) == A
+    assert apply(n_tokens=0) == 0 and apply(n_seqs=0, W=(1 << 31) - 1, N=(1 << 31) - 1) == 0
