@@ -655,6 +655,58 @@ int tcl_i8_linear(const tcl_i8_weight *w, const void *x, int64_t ldx, tcl_dtype 
                   size_t ws_bytes, void *stream);
 
 /* ------------------------------------------------------------------------
+ * 4-bit base projections: weights of 4 bits with a scale, and if wanted a zero
+ * point, for each group of a channel's columns; activations stay bf16.
+ * ------------------------------------------------------------------------ */
+
+/* One 4-bit base weight: weight (c, k) is scale[c][k / group] * (n - z), n the
+ * integer 0..15 of column k, z zero[c][k / group] (any of 0..255), or 8 for
+ * every group where zeros is 0.  W holds two columns a byte, the even one in the
+ * low half.  group is 32, 64 or a multiple of 128, d_in whole groups, at most
+ * TCL_I4_MAX_D_IN; d_out a multiple of 8 below 2^26.  Rows are contiguous; W is
+ * 16-byte, scale 4-byte aligned.  The products read the packed copy W_p
+ * (tcl_i4_pack) alone; W, scale and zero may be NULL once it is made. */
+#define TCL_I4_MAX_D_IN (1 << 20)
+typedef struct {
+  int32_t d_in;
+  int32_t d_out;
+  int32_t group;
+  int32_t zeros;        /* 1: zero points, 0: 8     */
+  const uint8_t *W;     /* device [d_out][d_in / 2]     */
+  const float *scale;   /* device [d_out][d_in / group] */
+  const uint8_t *zero;  /* device [d_out][d_in / group] */
+  const void *W_p;
+} tcl_i4_weight;
+
+/*
+ * The packed copy, in the order the matrix cores take it (weights, scales and
+ * zero points).  tcl_i4_pack writes it on `stream` into W_p (caller-owned
+ * device memory of tcl_i4_pack_bytes bytes, 256-byte aligned) and sets w->W_p.
+ * Errors: TCL_EINVAL, TCL_EALIGN, TCL_ENOSPC, TCL_EUNSUPPORTED (group, sizes,
+ * 2^36 bytes or more), TCL_EHIP.
+ */
+int tcl_i4_pack_bytes(const tcl_i4_weight *w, size_t *bytes);
+int tcl_i4_pack(tcl_i4_weight *w, void *W_p, size_t bytes, void *stream);
+
+/*
+ * y[t][c] = sum_k x[t][k] * scale[c][k / group] * (n[c][k] - z[c][k / group]):
+ * the base projection of n_tokens tokens, written, not added to, so that
+ * tcl_fused_apply on the same rows completes it.  x: device bf16
+ * [n_tokens][ldx], 16-byte aligned; y: device [n_tokens][ldy] of dtype yd,
+ * 16-byte aligned, ldx and ldy multiples of 8; y must not overlap x.  Weights
+ * are not rounded; sums are fp32, a group's first, and y is rounded once.  A
+ * row of x with an infinity or a NaN, or whose sum of |x| over a group times
+ * 272 leaves fp32's range, may be NaN in every channel; no other row's result
+ * is touched.  Results are bitwise reproducible.  n_tokens == 0 or d_out == 0
+ * is a no-op.
+ * Errors: TCL_EINVAL (NULL, sizes, ldx < d_in, ldy < d_out, a weight that is
+ * not packed), TCL_EALIGN, TCL_EUNSUPPORTED (yd, group, d_in or d_out beyond
+ * the limits, 2^24 tokens or more, n_tokens * d_out of 2^36 or more), TCL_EHIP.
+ */
+int tcl_i4_linear(const tcl_i4_weight *w, const void *x, int64_t ldx, int32_t n_tokens, void *y,
+                  int64_t ldy, tcl_dtype yd, void *stream);
+
+/* ------------------------------------------------------------------------
  * Paged key/value cache (ELORA, section V: keys and values hang off the
  * adapter they were computed with, in blocks of one pool; section III-A, Eq.
  * 2: the adapters update W_K and W_V).

@@ -1,0 +1,352 @@
+// Base projections by 4-bit weights with group scales (include/tcl.h has the
+// formulas): bf16 activations, integers 0..15 with a scale and a zero point
+// for each group of a channel's weights.
+//
+// An integer n becomes the bf16 number 16 + n by two operations on a pair of
+// them (a shift, and its four bits under the exponent of 16), exactly.  The
+// matrix cores sum x (16 + n) over a group, and the sums of x over the group
+// come from one more operand, of ones; then
+//   s sum x (n - z) = s (sum x (16 + n) - (16 + z) sum x)
+// is two fused operations an output and group, in fp32.  No weight is rounded.
+//
+// The packed weight holds blocks of 16 channels by 128 columns in the order in
+// which the lanes of a wave take them (1 KiB a load): dword i of lane l has
+// channel l % 16, columns 32 i + 8 (l / 16) + 0..7, column 2 j at bit 4 j and
+// column 2 j + 1 at bit 16 + 4 j.  Behind the blocks come the scales, 16
+// channels of a group side by side, and the zero points likewise.
+#include "kern_common.hpp"
+
+namespace tcl {
+namespace {
+
+struct I4Args {
+  const uint8_t *w;       // packed blocks
+  const float *scale;     // [channel tile][group][16]
+  const uint8_t *zero;    // the same, or NULL: 8
+  const uint16_t *x;
+  void *y;
+  int64_t ldx, ldy;
+  int32_t T, K, N, kb, groups;
+  int32_t blocks;         // blocks of 128 columns of a group (1 where it is shorter)
+};
+
+// ---------------------------------------------------------------------------
+// packing
+// ---------------------------------------------------------------------------
+struct PackArgs {
+  const uint8_t *W, *zero;
+  const float *scale;
+  uint8_t *w, *pz;
+  float *ps;
+  int32_t K, N, kb, groups;
+  int64_t n_w, n_s;  // 16-byte pieces of the blocks; scales
+};
+
+__global__ __launch_bounds__(256) void i4_pack_kernel(PackArgs a) {
+  const int64_t step = int64_t(gridDim.x) * 256, at = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  for (int64_t p = at; p < a.n_w; p += step) {
+    const int lane = int(p & 63);
+    const int64_t blk = p >> 6;
+    const int c = int(blk / a.kb) * 16 + (lane & 15), k0 = int(blk % a.kb) * 128 + 8 * (lane >> 4);
+    nt_u4 out;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t u = 0;
+      if (c < a.N && k0 + 32 * i < a.K) {  // (d_in is a multiple of 32)
+        const uint32_t b = *reinterpret_cast<const uint32_t *>(a.W + (int64_t(c) * a.K + k0 + 32 * i) / 2);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          u |= (b >> 8 * j & 15) << 4 * j | (b >> (8 * j + 4) & 15) << (16 + 4 * j);
+      }
+      out[i] = u;
+    }
+    reinterpret_cast<nt_u4 *>(a.w)[p] = out;
+  }
+  for (int64_t p = at; p < a.n_s; p += step) {
+    const int64_t tg = p >> 4;
+    const int c = int(tg / a.groups) * 16 + int(p & 15), g = int(tg % a.groups);
+    a.ps[p] = c < a.N ? a.scale[int64_t(c) * a.groups + g] : 0.f;
+    if (a.zero) a.pz[p] = c < a.N ? a.zero[int64_t(c) * a.groups + g] : 8;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// products
+// ---------------------------------------------------------------------------
+// eight columns as bf16 numbers 16 + n
+__device__ inline bf16x8_t widen(uint32_t w) {
+  constexpr uint32_t mask = 0x00780078u, base = 0x41804180u;
+  return __builtin_bit_cast(bf16x8_t, nt_u4{(w << 3 & mask) | base, (w >> 1 & mask) | base,
+                                            (w >> 5 & mask) | base, (w >> 9 & mask) | base});
+}
+
+__device__ inline bf16x8_t ones() {
+  return __builtin_bit_cast(bf16x8_t, nt_u4{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u});
+}
+
+__device__ inline f32x4_t mfma(bf16x8_t a, bf16x8_t b, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// 16 NB channels by 16 MT tokens; wave w of WV takes the blocks w, w + WV, ...
+// of 128 columns.  Tokens are the rows of a result, so that a lane holds one
+// channel, its scale and zero point.  GS: groups of a block (4, 2, 1; 1 also
+// for groups of several blocks).
+template <int MT, int NB, int WV, int GS, bool ZP, typename TY>
+__global__ __launch_bounds__(64 * WV) void i4_skinny(I4Args a) {
+  constexpr int LD = 20;  // floats of a token's 16 channels in LDS
+  __shared__ float part[WV][NB][16 * LD];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  const int c = lane & 15, g = lane >> 4;
+  const int c0 = blockIdx.x * 16 * NB, t0 = blockIdx.y * 16 * MT;
+  const int tiles = (a.N + 15) / 16;
+  const uint16_t *xp[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) xp[m] = a.x + int64_t(min(t0 + 16 * m + c, a.T - 1)) * a.ldx + 8 * g;
+  const uint8_t *wp[NB];
+  const float *sp[NB];
+  const uint8_t *zp[NB];
+#pragma unroll
+  for (int n = 0; n < NB; ++n) {
+    // (channel tiles past the last: the last one again, not stored)
+    const int64_t ct = min(blockIdx.x * NB + n, unsigned(tiles - 1));
+    wp[n] = a.w + ct * a.kb * 1024 + 16 * lane;
+    sp[n] = a.scale + ct * a.groups * 16 + c;
+    zp[n] = ZP ? a.zero + ct * a.groups * 16 + c : nullptr;
+  }
+  f32x4_t acc[MT][NB];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int n = 0; n < NB; ++n) acc[m][n] = f32x4_t{0, 0, 0, 0};
+  nt_u4 wq[NB], xr[MT][4];
+  float s[NB][GS], z[NB][GS];
+  auto load_w = [&](int b) {
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      wq[n] = *reinterpret_cast<const nt_u4 *>(wp[n] + int64_t(b) * 1024);
+#pragma unroll
+      for (int e = 0; e < GS; ++e) {
+        // (the last block may hold fewer groups than others)
+        const int gr = GS == 1 ? b / a.blocks : min(b * GS + e, a.groups - 1);
+        s[n][e] = sp[n][gr * 16];
+        z[n][e] = ZP ? 16.f + float(zp[n][gr * 16]) : 24.f;
+      }
+    }
+  };
+  auto load_x = [&](int m, int b) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      // columns past the row's end: zeros
+      const bool in = b * 128 + 32 * i < a.K;
+      const nt_u4 u = *reinterpret_cast<const nt_u4 *>(xp[m] + (in ? b * 128 + 32 * i : 0));
+      xr[m][i] = in ? u : nt_u4{0, 0, 0, 0};
+    }
+  };
+  if (w < a.kb) {
+    load_w(w);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) load_x(m, w);
+  }
+  for (int b = w; b < a.kb; b += WV) {
+    const int next = min(b + WV, a.kb - 1);
+    bf16x8_t wf[NB][4];
+    float sc[NB][GS], zc[NB][GS];
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) wf[n][i] = widen(wq[n][i]);
+#pragma unroll
+      for (int e = 0; e < GS; ++e) sc[n][e] = s[n][e], zc[n][e] = z[n][e];
+    }
+    load_w(next);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      nt_u4 xc[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) xc[i] = xr[m][i];
+      load_x(m, next);
+#pragma unroll
+      for (int e = 0; e < GS; ++e) {
+        f32x4_t sum = {0, 0, 0, 0}, p[NB];
+#pragma unroll
+        for (int n = 0; n < NB; ++n) p[n] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+        for (int i = 4 / GS * e; i < 4 / GS * (e + 1); ++i) {
+          const bf16x8_t xf = __builtin_bit_cast(bf16x8_t, xc[i]);
+          sum = mfma(xf, ones(), sum);
+#pragma unroll
+          for (int n = 0; n < NB; ++n) p[n] = mfma(xf, wf[n][i], p[n]);
+        }
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            acc[m][n][r] = fmaf(sc[n][e], fmaf(-zc[n][e], sum[r], p[n][r]), acc[m][n][r]);
+      }
+    }
+  }
+  // the waves' sums, in order, 16 tokens at a time
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    if (m) __syncthreads();
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) part[w][n][(4 * g + r) * LD + c] = acc[m][n][r];
+    __syncthreads();
+    for (int o = tid; o < NB * 64; o += 64 * WV) {
+      const int n = o >> 6, t = t0 + 16 * m + (o >> 2 & 15), ch = c0 + 16 * n + 4 * (o & 3);
+      if (t >= a.T || ch >= a.N) continue;
+      const float *in = &part[0][n][(o >> 2 & 15) * LD + 4 * (o & 3)];
+      nt_f4 v = *reinterpret_cast<const nt_f4 *>(in);
+#pragma unroll
+      for (int i = 1; i < WV; ++i) v += *reinterpret_cast<const nt_f4 *>(in + i * NB * 16 * LD);
+      TY *p = static_cast<TY *>(a.y) + int64_t(t) * a.ldy + ch;
+      if constexpr (sizeof(TY) == 4) {
+        *reinterpret_cast<nt_f4 *>(p) = v;
+      } else {
+        *reinterpret_cast<nt_u2 *>(p) = nt_u2{uint32_t(f32_to_bf16(v[0])) | uint32_t(f32_to_bf16(v[1])) << 16,
+                                              uint32_t(f32_to_bf16(v[2])) | uint32_t(f32_to_bf16(v[3])) << 16};
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// checks and launches
+// ---------------------------------------------------------------------------
+bool misaligned(const void *p, uintptr_t m) { return reinterpret_cast<uintptr_t>(p) & (m - 1); }
+
+constexpr int kMaxChannels = 1 << 26, kMaxTokens = 1 << 24;
+
+struct Layout {
+  int64_t tiles;
+  int32_t kb, groups;
+  size_t w, scale, total;  // bytes of the blocks; where the zero points are; all
+};
+
+int check_weight(const tcl_i4_weight *w, Layout *l) {
+  if (!w) return fail(TCL_EINVAL, "i4: weight is NULL");
+  if (w->d_in < 32 || w->d_out < 0)
+    return fail(TCL_EINVAL, "i4: d_in %d < 32 or d_out %d < 0", w->d_in, w->d_out);
+  if (w->group != 32 && w->group != 64 && (w->group < 128 || w->group % 128))
+    return fail(TCL_EUNSUPPORTED, "i4: group %d is not 32, 64 or a multiple of 128", w->group);
+  if (w->d_in % w->group) return fail(TCL_EINVAL, "i4: d_in %d is not whole groups of %d", w->d_in, w->group);
+  if (w->d_in > TCL_I4_MAX_D_IN)
+    return fail(TCL_EUNSUPPORTED, "i4: d_in %d beyond %d", w->d_in, TCL_I4_MAX_D_IN);
+  if (w->d_out >= kMaxChannels) return fail(TCL_EUNSUPPORTED, "i4: d_out %d, 2^26 or more", w->d_out);
+  if (w->d_out % 8) return fail(TCL_EALIGN, "i4: d_out %d is not a multiple of 8", w->d_out);
+  if (w->zeros != 0 && w->zeros != 1) return fail(TCL_EINVAL, "i4: zeros %d is not 0 or 1", w->zeros);
+  if (misaligned(w->W, 16) || misaligned(w->scale, 4) || misaligned(w->W_p, 256))
+    return fail(TCL_EALIGN, "i4: W must be 16-byte, scale 4-byte, W_p 256-byte aligned");
+  l->tiles = (int64_t(w->d_out) + 15) / 16;
+  l->kb = (w->d_in + 127) / 128;
+  l->groups = w->d_in / w->group;
+  l->w = size_t(l->tiles) * l->kb * 1024;
+  l->scale = l->w + size_t(l->tiles) * l->groups * 64;
+  l->total = (l->scale + (w->zeros ? size_t(l->tiles) * l->groups * 16 : 0) + 255) / 256 * 256;
+  if (l->total >= size_t(1) << 36) return fail(TCL_EUNSUPPORTED, "i4: a packed copy of 2^36 bytes or more");
+  return TCL_OK;
+}
+
+template <int MT, int NB, int WV, int GS, bool ZP, typename TY>
+void go_skinny(const I4Args &a, hipStream_t s) {
+  hipLaunchKernelGGL((i4_skinny<MT, NB, WV, GS, ZP, TY>),
+                     dim3((a.N + 16 * NB - 1) / (16 * NB), (a.T + 16 * MT - 1) / (16 * MT)), dim3(64 * WV), 0,
+                     s, a);
+}
+
+template <int GS, bool ZP, typename TY>
+void product(const I4Args &a, hipStream_t s) {
+  if (a.T <= 16)
+    go_skinny<1, 1, 8, GS, ZP, TY>(a, s);
+  else if (a.T <= 32)
+    go_skinny<2, 2, 8, GS, ZP, TY>(a, s);
+  else
+    go_skinny<4, 4, 8, GS, ZP, TY>(a, s);
+}
+
+template <int GS, bool ZP>
+void product(const I4Args &a, int yd, hipStream_t s) {
+  if (yd == TCL_BF16)
+    product<GS, ZP, bf16_t>(a, s);
+  else
+    product<GS, ZP, float>(a, s);
+}
+
+template <int GS>
+void product(const I4Args &a, int yd, hipStream_t s) {
+  if (a.zero)
+    product<GS, true>(a, yd, s);
+  else
+    product<GS, false>(a, yd, s);
+}
+
+}  // namespace
+}  // namespace tcl
+
+using namespace tcl;
+
+extern "C" int tcl_i4_pack_bytes(const tcl_i4_weight *w, size_t *bytes) {
+  Layout l;
+  if (!bytes) return fail(TCL_EINVAL, "i4: bytes is NULL");
+  const int rc = check_weight(w, &l);
+  if (rc) return rc;
+  *bytes = l.total;
+  return TCL_OK;
+}
+
+extern "C" int tcl_i4_pack(tcl_i4_weight *w, void *W_p, size_t bytes, void *stream) {
+  Layout l;
+  int rc = check_weight(w, &l);
+  if (rc) return rc;
+  if (!W_p) return fail(TCL_EINVAL, "i4: W_p is NULL");
+  if (misaligned(W_p, 256)) return fail(TCL_EALIGN, "i4: W_p must be 256-byte aligned");
+  if (bytes < l.total) return fail(TCL_ENOSPC, "i4: W_p holds %zu bytes, needs %zu", bytes, l.total);
+  if (w->d_out > 0) {
+    if (!w->W || !w->scale || (w->zeros && !w->zero)) return fail(TCL_EINVAL, "i4: weight arrays are NULL");
+    uint8_t *p = static_cast<uint8_t *>(W_p);
+    PackArgs a{w->W, w->zeros ? w->zero : nullptr, w->scale, p, p + l.scale,
+               reinterpret_cast<float *>(p + l.w), w->d_in, w->d_out, l.kb, l.groups,
+               int64_t(l.w / 16), int64_t(l.scale - l.w) / 4};
+    const int64_t blocks = (a.n_w + 255) / 256;
+    hipLaunchKernelGGL(i4_pack_kernel, dim3(unsigned(blocks < 1 << 16 ? blocks : 1 << 16)), dim3(256), 0,
+                       static_cast<hipStream_t>(stream), a);
+    TCL_HIP(hipGetLastError());
+  }
+  w->W_p = W_p;
+  return TCL_OK;
+}
+
+extern "C" int tcl_i4_linear(const tcl_i4_weight *w, const void *x, int64_t ldx, int32_t n_tokens, void *y,
+                             int64_t ldy, tcl_dtype yd, void *stream) {
+  Layout l;
+  const int rc = check_weight(w, &l);
+  if (rc) return rc;
+  if (n_tokens < 0) return fail(TCL_EINVAL, "i4: n_tokens %d < 0", n_tokens);
+  if (yd != TCL_BF16 && yd != TCL_F32) return fail(TCL_EUNSUPPORTED, "i4: y dtype %d", int(yd));
+  if (n_tokens >= kMaxTokens) return fail(TCL_EUNSUPPORTED, "i4: n_tokens %d, 2^24 or more", n_tokens);
+  if (int64_t(n_tokens) * w->d_out >= int64_t(1) << 36)
+    return fail(TCL_EUNSUPPORTED, "i4: n_tokens * d_out of 2^36 or more");
+  if (w->d_out == 0) return TCL_OK;  // nothing is written
+  if (ldx < w->d_in || ldy < w->d_out) return fail(TCL_EINVAL, "i4: ldx < d_in or ldy < d_out");
+  if (misaligned(x, 16) || misaligned(y, 16) || ldx % 8 || ldy % 8)
+    return fail(TCL_EALIGN, "i4: x and y must be 16-byte aligned, ldx and ldy multiples of 8");
+  if (n_tokens == 0) return TCL_OK;
+  if (!x || !y || !w->W_p) return fail(TCL_EINVAL, "i4: x, y and the packed weight are required");
+  const uint8_t *p = static_cast<const uint8_t *>(w->W_p);
+  I4Args a{p, reinterpret_cast<const float *>(p + l.w), w->zeros ? p + l.scale : nullptr,
+           static_cast<const uint16_t *>(x), y, ldx, ldy, n_tokens, w->d_in, w->d_out, l.kb, l.groups,
+           w->group < 128 ? 1 : w->group / 128};
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  logf("i4: tokens=%d d_in=%d d_out=%d group=%d zeros=%d", a.T, a.K, a.N, w->group, w->zeros);
+  if (w->group == 32)
+    product<4>(a, yd, s);
+  else if (w->group == 64)
+    product<2>(a, yd, s);
+  else
+    product<1>(a, yd, s);
+  TCL_HIP(hipGetLastError());
+  return TCL_OK;
+}

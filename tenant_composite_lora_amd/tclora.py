@@ -40,7 +40,8 @@ EXPORTS = ["tcl_last_error", "tcl_version", "tcl_plan_bytes", "tcl_plan_map", "t
            "tcl_i8_pack_bytes", "tcl_i8_pack",
            "tcl_kv_append", "tcl_attn_plan_bytes", "tcl_attn_workspace_bytes", "tcl_attn_plan",
            "tcl_attn_status_async", "tcl_attn_apply", "tcl_kv_append_norm", "tcl_kv_map",
-           "tcl_attn_window_plan", "tcl_attn_window_apply"]
+           "tcl_attn_window_plan", "tcl_attn_window_apply",
+           "tcl_i4_pack_bytes", "tcl_i4_pack", "tcl_i4_linear"]
 
 # bytes of the static device workspace of tcl_fused_apply_noalloc
 SCRATCH_BYTES = 32 << 20
@@ -71,6 +72,12 @@ class ModuleDesc(ctypes.Structure):
 class I8WeightDesc(ctypes.Structure):
     _fields_ = [("d_in", ctypes.c_int32), ("d_out", ctypes.c_int32), ("W", ctypes.c_void_p),
                 ("scale", ctypes.c_void_p), ("W_p", ctypes.c_void_p)]
+
+
+class I4WeightDesc(ctypes.Structure):
+    _fields_ = [("d_in", ctypes.c_int32), ("d_out", ctypes.c_int32), ("group", ctypes.c_int32),
+                ("zeros", ctypes.c_int32), ("W", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("zero", ctypes.c_void_p), ("W_p", ctypes.c_void_p)]
 
 
 class KVDesc(ctypes.Structure):
@@ -176,6 +183,9 @@ def lib(path: Optional[str] = None):
     L.tcl_i8_pack.argtypes = [ctypes.POINTER(I8WeightDesc), vp, sz, vp]
     L.tcl_i8_linear.argtypes = [ctypes.POINTER(I8WeightDesc), vp, i64, i32, i32, vp, i64, i32, vp,
                                 sz, vp]
+    L.tcl_i4_pack_bytes.argtypes = [ctypes.POINTER(I4WeightDesc), ctypes.POINTER(sz)]
+    L.tcl_i4_pack.argtypes = [ctypes.POINTER(I4WeightDesc), vp, sz, vp]
+    L.tcl_i4_linear.argtypes = [ctypes.POINTER(I4WeightDesc), vp, i64, i32, vp, i64, i32, vp]
     L.tcl_kv_append.argtypes = [ctypes.POINTER(KVDesc), ctypes.POINTER(RopeDesc), vp, i64, vp, i64,
                                 vp, i64, i32, i32, vp, i64, i32, vp, vp, vp]
     L.tcl_kv_append_norm.argtypes = [*L.tcl_kv_append.argtypes[:2], ctypes.POINTER(HeadNormDesc),
@@ -1004,6 +1014,78 @@ def i8_linear(w: I8Weight, x: torch.Tensor, y: Optional[torch.Tensor] = None,
         if stream is not None and x.is_cuda:
             y.record_stream(_stream_object(x.device, stream))
     return I8Call(w, x, y, _once=stream is None)(stream)
+
+
+class I4Weight:
+    """A 4-bit base weight with group scales (tcl_i4_weight): W uint8 [d_out,
+    d_in / 2], the even column of a pair in the low half of its byte, scale
+    fp32 [d_out, groups] and zero uint8 [d_out, groups] (None: 8), on the GPU.
+    The products read a copy in the matrix cores' order (tcl_i4_pack), made
+    here; W, scale and zero themselves are not kept.  The copy is made on
+    ``stream`` or the current one: calls on others have to be ordered behind
+    it."""
+
+    def __init__(self, W: torch.Tensor, scale: torch.Tensor, zero: Optional[torch.Tensor] = None,
+                 stream=None):
+        if W.dtype != torch.uint8 or (zero is not None and zero.dtype != torch.uint8):
+            raise TypeError("I4Weight: W and zero must be uint8")
+        if scale.dtype != torch.float32:
+            raise TypeError("I4Weight: scale must be float32")
+        if W.dim() != 2 or not W.is_contiguous():
+            raise ValueError("I4Weight: W must be [d_out, d_in / 2], contiguous")
+        for name, t in (("scale", scale), ("zero", zero)):
+            if t is not None and (t.dim() != 2 or t.shape != scale.shape or t.shape[0] != W.shape[0]
+                                  or not t.is_contiguous()):
+                raise ValueError(f"I4Weight: {name} must be [d_out, groups], contiguous")
+        self.d_out, self.d_in, self.device = W.shape[0], 2 * W.shape[1], W.device
+        if not scale.shape[1] or self.d_in % scale.shape[1]:
+            raise ValueError("I4Weight: d_in must be whole groups")
+        _same_device("I4Weight", W.device, scale, zero)
+        self.group = self.d_in // scale.shape[1]
+        self.desc = I4WeightDesc(self.d_in, self.d_out, self.group, int(zero is not None),
+                                 W.data_ptr(), scale.data_ptr(), _ptr(zero), None)
+        self.home = _stream(W.device)
+        n = ctypes.c_size_t(0)
+        check(lib().tcl_i4_pack_bytes(ctypes.byref(self.desc), ctypes.byref(n)))
+        self.W_p = torch.empty(max(n.value, 256), dtype=torch.uint8, device=W.device)
+        _made_for(W.device, stream)
+        _call(W.device, lib().tcl_i4_pack, (ctypes.byref(self.desc), self.W_p.data_ptr(), n.value), stream,
+              *((t, self.home) for t in (self.W_p, W, scale, zero) if t is not None))
+        self.desc.W = self.desc.scale = self.desc.zero = None
+
+
+class I4Call:
+    """Pre-marshalled arguments of tcl_i4_linear for repeated calls: each call
+    writes the base projection of x (bf16 [T, d_in]) into y (bf16 or fp32 [T,
+    d_out])."""
+
+    def __init__(self, w: I4Weight, x: torch.Tensor, y: torch.Tensor):
+        if x.dtype != torch.bfloat16:
+            raise TypeError("I4Call: x must be bfloat16")
+        T = x.shape[0]
+        self.ldx, self.ldy = _rows("I4Call: x", x, T, w.d_in), _rows("I4Call: y", y, T, w.d_out)
+        _same_device("I4Call", x.device, y, w.W_p)
+        self.w, self.x, self.y, self.T, self.device = w, x, y, T, x.device
+        self._own = ((w.W_p, w.home),)
+        self._fn = lib().tcl_i4_linear
+        self._args = _packed(self._fn, (ctypes.byref(w.desc), x.data_ptr(), self.ldx, T, y.data_ptr(),
+                                        self.ldy, _dtype_code(y.dtype)))
+
+    def __call__(self, stream=None) -> torch.Tensor:
+        _call(self.device, self._fn, self._args, stream, *self._own)
+        return self.y
+
+
+def i4_linear(w: I4Weight, x: torch.Tensor, y: Optional[torch.Tensor] = None,
+              y_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+    """tcl_i4_linear: the base projection of x [T, d_in] by a 4-bit weight."""
+    if y is None:
+        y = torch.empty(x.shape[0], w.d_out, dtype=y_dtype, device=x.device)
+        if x.is_cuda:
+            _made_for(x.device, stream)
+            if stream is not None:
+                y.record_stream(_stream_object(x.device, stream))
+    return I4Call(w, x, y)(stream)
 
 
 class KVCache:

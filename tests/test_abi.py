@@ -643,3 +643,44 @@ def test_attn_window_host_errors(L):
     assert [apply(q=None), apply(o=None), apply(w=None), apply(ldq=192)] == [E] * 4
     assert apply(wn=ws - 1) == tclora.ENOSPC and apply(q=P + 8) == A
     assert apply(n_tokens=0) == 0 and apply(n_seqs=0, W=(1 << 31) - 1, N=(1 << 31) - 1) == 0
+
+
+def test_i4_host_errors(L):
+    """The 4-bit calls refuse bad weights, sizes and pointers on the host (no
+    GPU)."""
+    P = 0x1000
+    E, A, U = tclora.EINVAL, tclora.EALIGN, tclora.EUNSUPPORTED
+    out = ctypes.c_size_t(0)
+
+    def w(**kw):
+        d = dict(d_in=128, d_out=32, group=32, zeros=1, W=P, scale=P, zero=P, W_p=P)
+        d.update(kw)
+        return ctypes.byref(tclora.I4WeightDesc(**d))
+
+    def nbytes(**kw):
+        return L.tcl_i4_pack_bytes(w(**kw), ctypes.byref(out))
+
+    def pack(p=P, n=1 << 40, **kw):
+        return L.tcl_i4_pack(w(**kw), p, n, None)
+
+    def lin(x=P, ldx=128, T=4, y=P, ldy=32, yd=1, **kw):
+        return L.tcl_i4_linear(w(**kw), x, ldx, T, y, ldy, yd, None)
+
+    assert nbytes() == 0 and out.value == 2 * 1024 + 2 * 4 * 64 + 256
+    assert nbytes(zeros=0, d_in=256, group=256) == 0 and out.value == 2 * 2 * 1024 + 256
+    assert L.tcl_i4_pack_bytes(w(), None) == E
+    for f in (nbytes, pack, lin):
+        assert [f(d_in=0), f(d_out=-8), f(d_in=96, group=64), f(zeros=2), f(zeros=-1)] == [E] * 5
+        assert [f(group=0), f(group=16), f(group=48), f(group=96), f(group=192), f(group=-32),
+                f(d_in=(1 << 20) + 32), f(d_out=1 << 26)] == [U] * 8
+        assert [f(d_out=36), f(W=P + 8), f(scale=P + 2), f(W_p=P + 16)] == [A] * 4
+    assert L.tcl_i4_pack_bytes(None, ctypes.byref(out)) == E
+    assert L.tcl_i4_pack(None, P, 9, None) == E and L.tcl_i4_linear(None, P, 128, 4, P, 32, 1, None) == E
+    assert nbytes(d_in=1 << 20, d_out=1 << 18) == U
+    assert [pack(p=None), pack(W=None), pack(scale=None), pack(zero=None)] == [E] * 4
+    assert pack(p=P + 16) == A and pack(n=2047) == tclora.ENOSPC
+    assert [lin(x=None), lin(y=None), lin(W_p=None), lin(T=-1), lin(ldx=120), lin(ldy=24)] == [E] * 6
+    assert [lin(x=P + 8), lin(y=P + 4), lin(ldx=132), lin(ldy=36)] == [A] * 4
+    assert [lin(yd=2), lin(T=1 << 24), lin(d_out=1 << 20, ldy=1 << 20, T=1 << 16)] == [U] * 3
+    assert lin(T=0) == 0 and lin(d_out=0, x=None) == 0
+    assert lin(T=0, W=None, scale=None, zero=None) == 0
