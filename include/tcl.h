@@ -688,6 +688,9 @@ typedef struct {
 int tcl_i4_pack_bytes(const tcl_i4_weight *w, size_t *bytes);
 int tcl_i4_pack(tcl_i4_weight *w, void *W_p, size_t bytes, void *stream);
 
+/* Device workspace of tcl_i4_linear (host only); none for up to 16 tokens. */
+int tcl_i4_workspace_bytes(const tcl_i4_weight *w, int32_t n_tokens, size_t *bytes);
+
 /*
  * y[t][c] = sum_k x[t][k] * scale[c][k / group] * (n[c][k] - z[c][k / group]):
  * the base projection of n_tokens tokens, written, not added to, so that
@@ -698,13 +701,16 @@ int tcl_i4_pack(tcl_i4_weight *w, void *W_p, size_t bytes, void *stream);
  * row of x with an infinity or a NaN, or whose sum of |x| over a group times
  * 272 leaves fp32's range, may be NaN in every channel; no other row's result
  * is touched.  Results are bitwise reproducible.  n_tokens == 0 or d_out == 0
- * is a no-op.
+ * is a no-op.  ws: device workspace of at least tcl_i4_workspace_bytes bytes,
+ * 256-byte aligned, in use until the call's work has run; calls that may run
+ * at the same time need one each.
  * Errors: TCL_EINVAL (NULL, sizes, ldx < d_in, ldy < d_out, a weight that is
- * not packed), TCL_EALIGN, TCL_EUNSUPPORTED (yd, group, d_in or d_out beyond
- * the limits, 2^24 tokens or more, n_tokens * d_out of 2^36 or more), TCL_EHIP.
+ * not packed), TCL_EALIGN, TCL_ENOSPC, TCL_EUNSUPPORTED (yd, group, d_in or
+ * d_out beyond the limits, 2^24 tokens or more, n_tokens * d_out of 2^36 or
+ * more, n_tokens * d_in of 2^40 or more), TCL_EHIP.
  */
 int tcl_i4_linear(const tcl_i4_weight *w, const void *x, int64_t ldx, int32_t n_tokens, void *y,
-                  int64_t ldy, tcl_dtype yd, void *stream);
+                  int64_t ldy, tcl_dtype yd, void *ws, size_t ws_bytes, void *stream);
 
 /* ------------------------------------------------------------------------
  * Paged key/value cache (ELORA, section V: keys and values hang off the

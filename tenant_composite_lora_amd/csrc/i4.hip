@@ -28,6 +28,9 @@ struct I4Args {
   int64_t ldx, ldy;
   int32_t T, K, N, kb, groups;
   int32_t blocks;         // blocks of 128 columns of a group (1 where it is shorter)
+  const nt_u4 *xb, *xe;   // staged activations and their groups' sums
+  int32_t steps;          // corrections of four groups
+  int32_t nt, nc;         // tiles of tokens, of channels
 };
 
 // ---------------------------------------------------------------------------
@@ -71,6 +74,79 @@ __global__ __launch_bounds__(256) void i4_pack_kernel(PackArgs a) {
 }
 
 // ---------------------------------------------------------------------------
+// activations
+// ---------------------------------------------------------------------------
+// For more than a few tokens the activations are laid out once, in the order
+// in which the products take them, with zeros behind the last token and
+// column: block (token tile, 128 columns) of 4 KiB, piece i of lane l the 16
+// bytes of token l % 16, columns 32 i + 8 (l / 16).  Behind them come the sums
+// of x over the groups (correct): for a token tile and four groups 1 KiB, lane
+// l token l % 16 of group l / 16.
+struct StageArgs {
+  const uint16_t *x;
+  nt_u4 *xb, *xe;
+  int64_t ldx;
+  int32_t T, K, kb, steps;  // steps: groups / 4, rounded up
+};
+
+// v = p[0] + p[1] + p[2] in bf16 numbers, the rest below 2^-24 of v
+__device__ inline void split3(float v, uint32_t *p) {
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    p[i] = f32_to_bf16(v);
+    v -= __uint_as_float(p[i] << 16);
+  }
+}
+
+// The correction of a group, -(s (16 + z)) sum x, as products of bf16 parts on
+// the matrix cores: columns 8 g + 0 .. 5 of one more step of 32 columns hold
+// parts 0 0 1 0 2 1 of group g's sum against parts 0 1 0 2 0 1 of its factor,
+// which leaves out less than 2^-23 of the product.
+__device__ inline nt_u4 parts_x(float v) {
+  uint32_t p[3];
+  split3(v, p);
+  return nt_u4{p[0] | p[0] << 16, p[1] | p[0] << 16, p[2] | p[1] << 16, 0};
+}
+__device__ inline bf16x8_t parts_w(float v) {
+  uint32_t p[3];
+  split3(v, p);
+  return __builtin_bit_cast(bf16x8_t, nt_u4{p[0] | p[1] << 16, p[0] | p[2] << 16, p[0] | p[1] << 16, 0});
+}
+
+// A wave a block.
+template <int GS>
+__global__ __launch_bounds__(256) void i4_stage_kernel(StageArgs a) {
+  constexpr int PER = 4 / GS;  // blocks of a correction step
+  const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+  const int b = blockIdx.y * 4 + (threadIdx.x >> 6);
+  const int t = blockIdx.x * 16 + c;
+  if (b >= a.steps * PER) return;
+  float sum[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int k = 128 * b + 32 * i + 8 * g;
+    nt_u4 u = {0, 0, 0, 0};
+    if (t < a.T && k < a.K) u = *reinterpret_cast<const nt_u4 *>(a.x + t * a.ldx + k);
+    if (b < a.kb) a.xb[(int64_t(blockIdx.x) * a.kb + b) * 256 + 64 * i + lane] = u;
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s += bf16_lo(u[e]) + bf16_hi(u[e]);
+    s += __shfl_xor(s, 16, 64);
+    s += __shfl_xor(s, 32, 64);
+    sum[i] = s;
+  }
+  nt_u4 *xe = a.xe + (int64_t(blockIdx.x) * a.steps + b / PER) * 64 + c;
+  if constexpr (GS == 4) {
+    const float s = g < 2 ? (g ? sum[1] : sum[0]) : (g == 2 ? sum[2] : sum[3]);
+    xe[16 * g] = parts_x(s);
+  } else if constexpr (GS == 2) {
+    if (g < 2) xe[16 * (2 * (b & 1) + g)] = parts_x(g ? sum[2] + sum[3] : sum[0] + sum[1]);
+  } else {
+    if (g == 0) xe[16 * (b & 3)] = parts_x((sum[0] + sum[1]) + (sum[2] + sum[3]));
+  }
+}
+
+// ---------------------------------------------------------------------------
 // products
 // ---------------------------------------------------------------------------
 // eight columns as bf16 numbers 16 + n
@@ -87,15 +163,55 @@ __device__ inline bf16x8_t ones() {
 __device__ inline f32x4_t mfma(bf16x8_t a, bf16x8_t b, f32x4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
+__device__ inline bf16x8_t as_bf16(nt_u4 u) { return __builtin_bit_cast(bf16x8_t, u); }
 
-// 16 NB channels by 16 MT tokens; wave w of WV takes the blocks w, w + WV, ...
-// of 128 columns.  Tokens are the rows of a result, so that a lane holds one
-// channel, its scale and zero point.  GS: groups of a block (4, 2, 1; 1 also
+// Four channels of a token to y.
+template <typename TY>
+__device__ inline void store4(const I4Args &a, int t, int ch, nt_f4 v) {
+  TY *p = static_cast<TY *>(a.y) + int64_t(t) * a.ldy + ch;
+  if constexpr (sizeof(TY) == 4) {
+    *reinterpret_cast<nt_f4 *>(p) = v;
+  } else {
+    *reinterpret_cast<nt_u2 *>(p) = nt_u2{uint32_t(f32_to_bf16(v[0])) | uint32_t(f32_to_bf16(v[1])) << 16,
+                                          uint32_t(f32_to_bf16(v[2])) | uint32_t(f32_to_bf16(v[3])) << 16};
+  }
+}
+
+// The waves' sums of 16 MT tokens by 16 NB channels, added in order, 16 tokens
+// at a time, and stored.
+constexpr int kPartLd = 20;  // floats of a token's 16 channels in LDS
+template <int MT, int NB, int WV, typename TY>
+__device__ inline void join(const I4Args &a, const f32x4_t (&acc)[MT][NB],
+                            float (&part)[WV][NB][16 * kPartLd], int t0, int c0) {
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, c = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    if (m) __syncthreads();
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) part[w][n][(4 * g + r) * kPartLd + c] = acc[m][n][r];
+    __syncthreads();
+    for (int o = tid; o < NB * 64; o += 64 * WV) {
+      const int n = o >> 6, t = t0 + 16 * m + (o >> 2 & 15), ch = c0 + 16 * n + 4 * (o & 3);
+      if (t >= a.T || ch >= a.N) continue;
+      const float *in = &part[0][n][(o >> 2 & 15) * kPartLd + 4 * (o & 3)];
+      nt_f4 v = *reinterpret_cast<const nt_f4 *>(in);
+#pragma unroll
+      for (int i = 1; i < WV; ++i) v += *reinterpret_cast<const nt_f4 *>(in + i * NB * 16 * kPartLd);
+      store4<TY>(a, t, ch, v);
+    }
+  }
+}
+
+// Few tokens, straight from x.  16 NB channels by 16 MT tokens; wave w of WV
+// takes the blocks w, w + WV, ... of 128 columns.  Tokens are the rows of a
+// result, so that a lane holds one channel, its scale and zero point; the sums
+// of x come from an operand of ones.  GS: groups of a block (4, 2, 1; 1 also
 // for groups of several blocks).
 template <int MT, int NB, int WV, int GS, bool ZP, typename TY>
-__global__ __launch_bounds__(64 * WV) void i4_skinny(I4Args a) {
-  constexpr int LD = 20;  // floats of a token's 16 channels in LDS
-  __shared__ float part[WV][NB][16 * LD];
+__global__ __launch_bounds__(64 * WV) void i4_rows(I4Args a) {
+  __shared__ float part[WV][NB][16 * kPartLd];
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   const int c = lane & 15, g = lane >> 4;
   const int c0 = blockIdx.x * 16 * NB, t0 = blockIdx.y * 16 * MT;
@@ -173,10 +289,9 @@ __global__ __launch_bounds__(64 * WV) void i4_skinny(I4Args a) {
         for (int n = 0; n < NB; ++n) p[n] = f32x4_t{0, 0, 0, 0};
 #pragma unroll
         for (int i = 4 / GS * e; i < 4 / GS * (e + 1); ++i) {
-          const bf16x8_t xf = __builtin_bit_cast(bf16x8_t, xc[i]);
-          sum = mfma(xf, ones(), sum);
+          sum = mfma(as_bf16(xc[i]), ones(), sum);
 #pragma unroll
-          for (int n = 0; n < NB; ++n) p[n] = mfma(xf, wf[n][i], p[n]);
+          for (int n = 0; n < NB; ++n) p[n] = mfma(as_bf16(xc[i]), wf[n][i], p[n]);
         }
 #pragma unroll
         for (int n = 0; n < NB; ++n)
@@ -186,30 +301,247 @@ __global__ __launch_bounds__(64 * WV) void i4_skinny(I4Args a) {
       }
     }
   }
-  // the waves' sums, in order, 16 tokens at a time
+  join<MT, NB, WV, TY>(a, acc, part, t0, c0);
+}
+
+// Where a channel tile's factors of a correction step are: lane l has group l /
+// 16 of the step's four, channel l % 16.
+template <int GS, bool ZP>
+struct Correct {
+  const float *sp;
+  const uint8_t *zp;
+  __device__ inline void init(const I4Args &a, int64_t ct, int c) {
+    sp = a.scale + ct * a.groups * 16 + c;
+    zp = ZP ? a.zero + ct * a.groups * 16 + c : nullptr;
+  }
+  // (groups behind the last meet sums of zero)
+  __device__ inline bf16x8_t operand(const I4Args &a, int step, int g) const {
+    const int gr = min(GS == 1 ? (4 * step + g) / a.blocks : 4 * step + g, a.groups - 1);
+    return parts_w(-sp[gr * 16] * (ZP ? 16.f + float(zp[gr * 16]) : 24.f));
+  }
+};
+
+// More tokens, from staged activations: as i4_rows, but the corrections are
+// steps of their own, dealt out to the waves behind the blocks.
+template <int MT, int NB, int WV, int GS, bool ZP, typename TY>
+__global__ __launch_bounds__(64 * WV) void i4_blocks(I4Args a) {
+  __shared__ float part[WV][NB][16 * kPartLd];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  const int c = lane & 15, g = lane >> 4;
+  const int c0 = blockIdx.x * 16 * NB, t0 = blockIdx.y * 16 * MT;
+  const int tiles = (a.N + 15) / 16, tt = (a.T + 15) / 16;
+  const nt_u4 *xp[MT], *ep[MT];
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
-    if (m) __syncthreads();
+    const int64_t tile = min(t0 / 16 + m, tt - 1);
+    xp[m] = a.xb + tile * a.kb * 256 + lane;
+    ep[m] = a.xe + tile * a.steps * 64 + lane;
+  }
+  const uint8_t *wp[NB];
+  Correct<GS, ZP> co[NB];
+#pragma unroll
+  for (int n = 0; n < NB; ++n) {
+    const int64_t ct = min(blockIdx.x * NB + n, unsigned(tiles - 1));
+    wp[n] = a.w + ct * a.kb * 1024 + 16 * lane;
+    co[n].init(a, ct, c);
+  }
+  f32x4_t acc[MT][NB];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int n = 0; n < NB; ++n) acc[m][n] = f32x4_t{0, 0, 0, 0};
+  nt_u4 wq[NB], xr[2][4];
+  float s[NB][GS];
+  auto load_w = [&](int b) {
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      wq[n] = *reinterpret_cast<const nt_u4 *>(wp[n] + int64_t(b) * 1024);
+#pragma unroll
+      for (int e = 0; e < GS; ++e)
+        s[n][e] = co[n].sp[(GS == 1 ? b / a.blocks : min(b * GS + e, a.groups - 1)) * 16];
+    }
+  };
+  auto load_x = [&](int m, int b, nt_u4 (&x)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = xp[m][int64_t(b) * 256 + 64 * i];
+  };
+  if (w < a.kb) {
+    load_w(w);
+    load_x(0, w, xr[0]);
+    if constexpr (MT > 1) load_x(1, w, xr[1]);
+  }
+  for (int b = w; b < a.kb; b += WV) {
+    const int next = min(b + WV, a.kb - 1);
+    bf16x8_t wf[NB][4];
+    float sc[NB][GS];
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) wf[n][i] = widen(wq[n][i]);
+#pragma unroll
+      for (int e = 0; e < GS; ++e) sc[n][e] = s[n][e];
+    }
+    load_w(next);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      constexpr int AHEAD = MT > 1 ? 2 : 1;
+      nt_u4 xc[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) xc[i] = xr[m % AHEAD][i];
+      load_x((m + AHEAD) % MT, m + AHEAD < MT ? b : next, xr[m % AHEAD]);
+#pragma unroll
+      for (int e = 0; e < GS; ++e) {
+        f32x4_t p[NB];
+#pragma unroll
+        for (int n = 0; n < NB; ++n) p[n] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+        for (int i = 4 / GS * e; i < 4 / GS * (e + 1); ++i)
+#pragma unroll
+          for (int n = 0; n < NB; ++n) p[n] = mfma(as_bf16(xc[i]), wf[n][i], p[n]);
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[m][n][r] = fmaf(sc[n][e], p[n][r], acc[m][n][r]);
+      }
+    }
+  }
+  for (int st = w; st < a.steps; st += WV) {
+    bf16x8_t f[NB];
+#pragma unroll
+    for (int n = 0; n < NB; ++n) f[n] = co[n].operand(a, st, g);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const bf16x8_t x = as_bf16(ep[m][int64_t(st) * 64]);
+#pragma unroll
+      for (int n = 0; n < NB; ++n) acc[m][n] = mfma(x, f[n], acc[m][n]);
+    }
+  }
+  join<MT, NB, WV, TY>(a, acc, part, t0, c0);
+}
+
+// Many tokens: tiles of BC channels by BT tokens, WC by WT waves.  A step's
+// activations (128 columns) go through LDS, two stages; a wave's weights come
+// straight from memory, a step ahead.
+template <int BC, int BT, int WC, int WT, int GS, bool ZP, typename TY>
+__global__ __launch_bounds__(64 * WC * WT) void i4_tile(I4Args a) {
+  constexpr int TH = 64 * WC * WT, NB = BC / WC / 16, MT = BT / WT / 16, PER = 4 / GS;
+  constexpr int PIECES = BT / 16 * 256, NP = PIECES / TH;
+  __shared__ nt_u4 lx[2][PIECES];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, c = lane & 15, g = lane >> 4;
+  // workgroups go to the eight XCDs in turn: each gets a run of tiles, token
+  // tiles next to each other, so that its L2 holds their weights
+  const int n_all = a.nt * a.nc, per = (n_all + 7) / 8;
+  const int id = int(blockIdx.x & 7) * per + int(blockIdx.x >> 3);
+  if (int(blockIdx.x >> 3) >= per || id >= n_all) return;
+  const int c0 = id / a.nt * BC + (w % WC) * (BC / WC), t0 = id % a.nt * BT;
+  const int wt = (w / WC) * MT;  // the wave's first token tile
+  const int tiles = (a.N + 15) / 16, tt = (a.T + 15) / 16;
+  const uint8_t *wp[NB];
+  Correct<GS, ZP> co[NB];
+#pragma unroll
+  for (int n = 0; n < NB; ++n) {
+    const int64_t ct = min(c0 / 16 + n, tiles - 1);
+    wp[n] = a.w + ct * a.kb * 1024 + 16 * lane;
+    co[n].init(a, ct, c);
+  }
+  auto stage = [&](int b, int buf) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int p = (w * NP + i) * 64;  // the wave's 64 pieces
+      const nt_u4 *from = a.xb + (int64_t(min(t0 / 16 + p / 256, tt - 1)) * a.kb + b) * 256 + p % 256 + lane;
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint32_t *)(from),
+                                       (__attribute__((address_space(3))) uint32_t *)(&lx[buf][p]), 16, 0, 0);
+    }
+  };
+  f32x4_t acc[MT][NB];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int n = 0; n < NB; ++n) acc[m][n] = f32x4_t{0, 0, 0, 0};
+  nt_u4 wq[NB];
+  float s[NB][GS];
+  auto load_w = [&](int b) {
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      wq[n] = *reinterpret_cast<const nt_u4 *>(wp[n] + int64_t(b) * 1024);
+#pragma unroll
+      for (int e = 0; e < GS; ++e)
+        s[n][e] = co[n].sp[(GS == 1 ? b / a.blocks : min(b * GS + e, a.groups - 1)) * 16];
+    }
+  };
+  stage(0, 0);
+  load_w(0);
+  for (int b = 0; b < a.kb; ++b) {
+    const int buf = b & 1;
+    __syncthreads();
+    const int next = min(b + 1, a.kb - 1);
+    stage(next, buf ^ 1);
+    bf16x8_t wf[NB][4];
+    float sc[NB][GS];
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) wf[n][i] = widen(wq[n][i]);
+#pragma unroll
+      for (int e = 0; e < GS; ++e) sc[n][e] = s[n][e];
+    }
+    load_w(next);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      nt_u4 xc[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) xc[i] = lx[buf][(wt + m) * 256 + 64 * i + lane];
+#pragma unroll
+      for (int e = 0; e < GS; ++e) {
+        f32x4_t p[NB];
+#pragma unroll
+        for (int n = 0; n < NB; ++n) p[n] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+        for (int i = 4 / GS * e; i < 4 / GS * (e + 1); ++i)
+#pragma unroll
+          for (int n = 0; n < NB; ++n) p[n] = mfma(as_bf16(xc[i]), wf[n][i], p[n]);
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[m][n][r] = fmaf(sc[n][e], p[n][r], acc[m][n][r]);
+      }
+    }
+    // corrections every four groups, so that sums stay small
+    if (b % PER == PER - 1 || b == a.kb - 1) {
+      const int st = b / PER;
+      bf16x8_t f[NB];
+#pragma unroll
+      for (int n = 0; n < NB; ++n) f[n] = co[n].operand(a, st, g);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const bf16x8_t x = as_bf16(a.xe[(int64_t(min(t0 / 16 + wt + m, tt - 1)) * a.steps + st) * 64 + lane]);
+#pragma unroll
+        for (int n = 0; n < NB; ++n) acc[m][n] = mfma(x, f[n], acc[m][n]);
+      }
+    }
+  }
+  // Results through LDS, a wave's 16 tokens at a time, so that a store covers
+  // whole lines of y.
+  __syncthreads();
+  constexpr int LD = 16 * NB + 4;
+  static_assert(WC * WT * 16 * LD * 4 <= int(sizeof(lx)), "LDS of the results");
+  float *out = reinterpret_cast<float *>(&lx) + w * 16 * LD;
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
 #pragma unroll
     for (int n = 0; n < NB; ++n)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) part[w][n][(4 * g + r) * LD + c] = acc[m][n][r];
-    __syncthreads();
-    for (int o = tid; o < NB * 64; o += 64 * WV) {
-      const int n = o >> 6, t = t0 + 16 * m + (o >> 2 & 15), ch = c0 + 16 * n + 4 * (o & 3);
-      if (t >= a.T || ch >= a.N) continue;
-      const float *in = &part[0][n][(o >> 2 & 15) * LD + 4 * (o & 3)];
-      nt_f4 v = *reinterpret_cast<const nt_f4 *>(in);
+      for (int r = 0; r < 4; ++r) out[(4 * g + r) * LD + 16 * n + c] = acc[m][n][r];
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
 #pragma unroll
-      for (int i = 1; i < WV; ++i) v += *reinterpret_cast<const nt_f4 *>(in + i * NB * 16 * LD);
-      TY *p = static_cast<TY *>(a.y) + int64_t(t) * a.ldy + ch;
-      if constexpr (sizeof(TY) == 4) {
-        *reinterpret_cast<nt_f4 *>(p) = v;
-      } else {
-        *reinterpret_cast<nt_u2 *>(p) = nt_u2{uint32_t(f32_to_bf16(v[0])) | uint32_t(f32_to_bf16(v[1])) << 16,
-                                              uint32_t(f32_to_bf16(v[2])) | uint32_t(f32_to_bf16(v[3])) << 16};
-      }
+    for (int k = 0; k < NB; ++k) {
+      const int o = k * 64 + lane, x = o / (4 * NB), t = t0 + 16 * (wt + m) + x, ch = o % (4 * NB) * 4;
+      if (t < a.T && c0 + ch < a.N)
+        store4<TY>(a, t, c0 + ch, *reinterpret_cast<const nt_f4 *>(out + x * LD + ch));
     }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
   }
 }
 
@@ -219,6 +551,9 @@ __global__ __launch_bounds__(64 * WV) void i4_skinny(I4Args a) {
 bool misaligned(const void *p, uintptr_t m) { return reinterpret_cast<uintptr_t>(p) & (m - 1); }
 
 constexpr int kMaxChannels = 1 << 26, kMaxTokens = 1 << 24;
+
+// up to as many tokens are taken from x as it is, in one launch
+constexpr int kRows = 16;
 
 struct Layout {
   int64_t tiles;
@@ -251,20 +586,43 @@ int check_weight(const tcl_i4_weight *w, Layout *l) {
 }
 
 template <int MT, int NB, int WV, int GS, bool ZP, typename TY>
-void go_skinny(const I4Args &a, hipStream_t s) {
-  hipLaunchKernelGGL((i4_skinny<MT, NB, WV, GS, ZP, TY>),
+void go_rows(const I4Args &a, hipStream_t s) {
+  hipLaunchKernelGGL((i4_rows<MT, NB, WV, GS, ZP, TY>),
                      dim3((a.N + 16 * NB - 1) / (16 * NB), (a.T + 16 * MT - 1) / (16 * MT)), dim3(64 * WV), 0,
                      s, a);
 }
 
+template <int MT, int NB, int WV, int GS, bool ZP, typename TY>
+void go_blocks(const I4Args &a, hipStream_t s) {
+  hipLaunchKernelGGL((i4_blocks<MT, NB, WV, GS, ZP, TY>),
+                     dim3((a.N + 16 * NB - 1) / (16 * NB), (a.T + 16 * MT - 1) / (16 * MT)), dim3(64 * WV), 0,
+                     s, a);
+}
+
+template <int BC, int BT, int WC, int WT, int GS, bool ZP, typename TY>
+void go_tile(I4Args a, hipStream_t s) {
+  a.nt = (a.T + BT - 1) / BT;
+  a.nc = (a.N + BC - 1) / BC;
+  hipLaunchKernelGGL((i4_tile<BC, BT, WC, WT, GS, ZP, TY>), dim3((a.nt * a.nc + 7) / 8 * 8),
+                     dim3(64 * WC * WT), 0, s, a);
+}
+
 template <int GS, bool ZP, typename TY>
 void product(const I4Args &a, hipStream_t s) {
-  if (a.T <= 16)
-    go_skinny<1, 1, 8, GS, ZP, TY>(a, s);
-  else if (a.T <= 32)
-    go_skinny<2, 2, 8, GS, ZP, TY>(a, s);
-  else
-    go_skinny<4, 4, 8, GS, ZP, TY>(a, s);
+  if (a.T <= kRows)
+    go_rows<1, 1, 8, GS, ZP, TY>(a, s);
+  else {
+    const StageArgs g{a.x, const_cast<nt_u4 *>(a.xb), const_cast<nt_u4 *>(a.xe), a.ldx, a.T, a.K, a.kb,
+                      a.steps};
+    hipLaunchKernelGGL(i4_stage_kernel<GS>, dim3((a.T + 15) / 16, (a.steps * (4 / GS) + 3) / 4), dim3(256), 0,
+                       s, g);
+    if (a.T <= 32)
+      go_blocks<2, 1, 8, GS, ZP, TY>(a, s);
+    else if (a.T <= 64)
+      go_blocks<4, 4, 8, GS, ZP, TY>(a, s);
+    else
+      go_tile<256, 128, 4, 1, GS, ZP, TY>(a, s);
+  }
 }
 
 template <int GS, bool ZP>
@@ -319,26 +677,70 @@ extern "C" int tcl_i4_pack(tcl_i4_weight *w, void *W_p, size_t bytes, void *stre
   return TCL_OK;
 }
 
-extern "C" int tcl_i4_linear(const tcl_i4_weight *w, const void *x, int64_t ldx, int32_t n_tokens, void *y,
-                             int64_t ldy, tcl_dtype yd, void *stream) {
-  Layout l;
-  const int rc = check_weight(w, &l);
-  if (rc) return rc;
+namespace tcl {
+namespace {
+
+// Bytes of the staged activations, and with their sums.
+struct Space {
+  size_t x, total;
+  int32_t steps;
+};
+Space space(const tcl_i4_weight *w, const Layout &l, int32_t n_tokens) {
+  if (n_tokens <= kRows || w->d_out == 0) return {0, 0, 0};
+  const size_t tiles = (size_t(n_tokens) + 15) / 16;
+  const int32_t groups = w->group < 128 ? l.groups : l.kb;  // longer ones count by their blocks
+  const int32_t steps = (groups + 3) / 4;
+  const size_t x = tiles * l.kb * 4096;
+  return {x, x + tiles * steps * 1024, steps};
+}
+
+int check_tokens(const tcl_i4_weight *w, int32_t n_tokens) {
   if (n_tokens < 0) return fail(TCL_EINVAL, "i4: n_tokens %d < 0", n_tokens);
-  if (yd != TCL_BF16 && yd != TCL_F32) return fail(TCL_EUNSUPPORTED, "i4: y dtype %d", int(yd));
   if (n_tokens >= kMaxTokens) return fail(TCL_EUNSUPPORTED, "i4: n_tokens %d, 2^24 or more", n_tokens);
   if (int64_t(n_tokens) * w->d_out >= int64_t(1) << 36)
     return fail(TCL_EUNSUPPORTED, "i4: n_tokens * d_out of 2^36 or more");
+  if (int64_t(n_tokens) * w->d_in >= int64_t(1) << 40)
+    return fail(TCL_EUNSUPPORTED, "i4: n_tokens * d_in of 2^40 or more");
+  return TCL_OK;
+}
+
+}  // namespace
+}  // namespace tcl
+
+extern "C" int tcl_i4_workspace_bytes(const tcl_i4_weight *w, int32_t n_tokens, size_t *bytes) {
+  Layout l;
+  if (!bytes) return fail(TCL_EINVAL, "i4: bytes is NULL");
+  int rc = check_weight(w, &l);
+  if (rc || (rc = check_tokens(w, n_tokens))) return rc;
+  *bytes = space(w, l, n_tokens).total;
+  return TCL_OK;
+}
+
+extern "C" int tcl_i4_linear(const tcl_i4_weight *w, const void *x, int64_t ldx, int32_t n_tokens, void *y,
+                             int64_t ldy, tcl_dtype yd, void *ws, size_t ws_bytes, void *stream) {
+  Layout l;
+  int rc = check_weight(w, &l);
+  if (rc || (rc = check_tokens(w, n_tokens))) return rc;
+  if (yd != TCL_BF16 && yd != TCL_F32) return fail(TCL_EUNSUPPORTED, "i4: y dtype %d", int(yd));
   if (w->d_out == 0) return TCL_OK;  // nothing is written
   if (ldx < w->d_in || ldy < w->d_out) return fail(TCL_EINVAL, "i4: ldx < d_in or ldy < d_out");
   if (misaligned(x, 16) || misaligned(y, 16) || ldx % 8 || ldy % 8)
     return fail(TCL_EALIGN, "i4: x and y must be 16-byte aligned, ldx and ldy multiples of 8");
   if (n_tokens == 0) return TCL_OK;
   if (!x || !y || !w->W_p) return fail(TCL_EINVAL, "i4: x, y and the packed weight are required");
+  const Space sp = space(w, l, n_tokens);
+  if (sp.total) {
+    if (!ws) return fail(TCL_EINVAL, "i4: ws is NULL");
+    if (misaligned(ws, 256)) return fail(TCL_EALIGN, "i4: ws must be 256-byte aligned");
+    if (ws_bytes < sp.total)
+      return fail(TCL_ENOSPC, "i4: workspace holds %zu bytes, needs %zu", ws_bytes, sp.total);
+  }
   const uint8_t *p = static_cast<const uint8_t *>(w->W_p);
+  char *q = static_cast<char *>(ws);
   I4Args a{p, reinterpret_cast<const float *>(p + l.w), w->zeros ? p + l.scale : nullptr,
            static_cast<const uint16_t *>(x), y, ldx, ldy, n_tokens, w->d_in, w->d_out, l.kb, l.groups,
-           w->group < 128 ? 1 : w->group / 128};
+           w->group < 128 ? 1 : w->group / 128, reinterpret_cast<nt_u4 *>(q),
+           reinterpret_cast<nt_u4 *>(q + sp.x), sp.steps, 0, 0};
   hipStream_t s = static_cast<hipStream_t>(stream);
   logf("i4: tokens=%d d_in=%d d_out=%d group=%d zeros=%d", a.T, a.K, a.N, w->group, w->zeros);
   if (w->group == 32)

@@ -41,7 +41,7 @@ EXPORTS = ["tcl_last_error", "tcl_version", "tcl_plan_bytes", "tcl_plan_map", "t
            "tcl_kv_append", "tcl_attn_plan_bytes", "tcl_attn_workspace_bytes", "tcl_attn_plan",
            "tcl_attn_status_async", "tcl_attn_apply", "tcl_kv_append_norm", "tcl_kv_map",
            "tcl_attn_window_plan", "tcl_attn_window_apply",
-           "tcl_i4_pack_bytes", "tcl_i4_pack", "tcl_i4_linear"]
+           "tcl_i4_pack_bytes", "tcl_i4_pack", "tcl_i4_workspace_bytes", "tcl_i4_linear"]
 
 # bytes of the static device workspace of tcl_fused_apply_noalloc
 SCRATCH_BYTES = 32 << 20
@@ -185,7 +185,8 @@ def lib(path: Optional[str] = None):
                                 sz, vp]
     L.tcl_i4_pack_bytes.argtypes = [ctypes.POINTER(I4WeightDesc), ctypes.POINTER(sz)]
     L.tcl_i4_pack.argtypes = [ctypes.POINTER(I4WeightDesc), vp, sz, vp]
-    L.tcl_i4_linear.argtypes = [ctypes.POINTER(I4WeightDesc), vp, i64, i32, vp, i64, i32, vp]
+    L.tcl_i4_workspace_bytes.argtypes = [ctypes.POINTER(I4WeightDesc), i32, ctypes.POINTER(sz)]
+    L.tcl_i4_linear.argtypes = [ctypes.POINTER(I4WeightDesc), vp, i64, i32, vp, i64, i32, vp, sz, vp]
     L.tcl_kv_append.argtypes = [ctypes.POINTER(KVDesc), ctypes.POINTER(RopeDesc), vp, i64, vp, i64,
                                 vp, i64, i32, i32, vp, i64, i32, vp, vp, vp]
     L.tcl_kv_append_norm.argtypes = [*L.tcl_kv_append.argtypes[:2], ctypes.POINTER(HeadNormDesc),
@@ -1057,22 +1058,34 @@ class I4Weight:
 class I4Call:
     """Pre-marshalled arguments of tcl_i4_linear for repeated calls: each call
     writes the base projection of x (bf16 [T, d_in]) into y (bf16 or fp32 [T,
-    d_out])."""
+    d_out]).  The workspace is the call's own (or ``ws``); calls that may run
+    at the same time need one each."""
 
-    def __init__(self, w: I4Weight, x: torch.Tensor, y: torch.Tensor):
+    def __init__(self, w: I4Weight, x: torch.Tensor, y: torch.Tensor,
+                 ws: Optional[torch.Tensor] = None, *, _once: bool = False):
         if x.dtype != torch.bfloat16:
             raise TypeError("I4Call: x must be bfloat16")
         T = x.shape[0]
         self.ldx, self.ldy = _rows("I4Call: x", x, T, w.d_in), _rows("I4Call: y", y, T, w.d_out)
-        _same_device("I4Call", x.device, y, w.W_p)
+        _same_device("I4Call", x.device, y, w.W_p, ws)
         self.w, self.x, self.y, self.T, self.device = w, x, y, T, x.device
-        self._own = ((w.W_p, w.home),)
+        need = ctypes.c_size_t(0)
+        check(lib().tcl_i4_workspace_bytes(ctypes.byref(w.desc), T, ctypes.byref(need)))
+        self._made = None
+        if not need.value:
+            ws = None
+        elif not _fits("I4Call", ws, need.value):
+            ws = torch.empty(need.value, dtype=torch.uint8, device=x.device)
+            self._made = None if _once else _Made(x.device)
+        self.ws = ws
+        self._own = ((w.W_p, w.home),) + (() if ws is None else ((ws, _stream(x.device)),))
         self._fn = lib().tcl_i4_linear
-        self._args = _packed(self._fn, (ctypes.byref(w.desc), x.data_ptr(), self.ldx, T, y.data_ptr(),
-                                        self.ldy, _dtype_code(y.dtype)))
+        self._args = _packed(self._fn, (
+            ctypes.byref(w.desc), x.data_ptr(), self.ldx, T, y.data_ptr(), self.ldy,
+            _dtype_code(y.dtype), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size()))
 
     def __call__(self, stream=None) -> torch.Tensor:
-        _call(self.device, self._fn, self._args, stream, *self._own)
+        _call(self.device, self._fn, self._args, stream, *self._own, made=self._made)
         return self.y
 
 
@@ -1085,7 +1098,7 @@ def i4_linear(w: I4Weight, x: torch.Tensor, y: Optional[torch.Tensor] = None,
             _made_for(x.device, stream)
             if stream is not None:
                 y.record_stream(_stream_object(x.device, stream))
-    return I4Call(w, x, y)(stream)
+    return I4Call(w, x, y, _once=stream is None)(stream)
 
 
 class KVCache:

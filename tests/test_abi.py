@@ -663,8 +663,8 @@ def test_i4_host_errors(L):
     def pack(p=P, n=1 << 40, **kw):
         return L.tcl_i4_pack(w(**kw), p, n, None)
 
-    def lin(x=P, ldx=128, T=4, y=P, ldy=32, yd=1, **kw):
-        return L.tcl_i4_linear(w(**kw), x, ldx, T, y, ldy, yd, None)
+    def lin(x=P, ldx=128, T=4, y=P, ldy=32, yd=1, ws=P, n=1 << 40, **kw):
+        return L.tcl_i4_linear(w(**kw), x, ldx, T, y, ldy, yd, ws, n, None)
 
     assert nbytes() == 0 and out.value == 2 * 1024 + 2 * 4 * 64 + 256
     assert nbytes(zeros=0, d_in=256, group=256) == 0 and out.value == 2 * 2 * 1024 + 256
@@ -675,7 +675,7 @@ def test_i4_host_errors(L):
                 f(d_in=(1 << 20) + 32), f(d_out=1 << 26)] == [U] * 8
         assert [f(d_out=36), f(W=P + 8), f(scale=P + 2), f(W_p=P + 16)] == [A] * 4
     assert L.tcl_i4_pack_bytes(None, ctypes.byref(out)) == E
-    assert L.tcl_i4_pack(None, P, 9, None) == E and L.tcl_i4_linear(None, P, 128, 4, P, 32, 1, None) == E
+    assert L.tcl_i4_pack(None, P, 9, None) == E and L.tcl_i4_linear(None, P, 128, 4, P, 32, 1, P, 9, None) == E
     assert nbytes(d_in=1 << 20, d_out=1 << 18) == U
     assert [pack(p=None), pack(W=None), pack(scale=None), pack(zero=None)] == [E] * 4
     assert pack(p=P + 16) == A and pack(n=2047) == tclora.ENOSPC
@@ -684,3 +684,10 @@ def test_i4_host_errors(L):
     assert [lin(yd=2), lin(T=1 << 24), lin(d_out=1 << 20, ldy=1 << 20, T=1 << 16)] == [U] * 3
     assert lin(T=0) == 0 and lin(d_out=0, x=None) == 0
     assert lin(T=0, W=None, scale=None, zero=None) == 0
+    assert [L.tcl_i4_workspace_bytes(w(), T, ctypes.byref(out)) for T in (16, 17)] == [0, 0]
+    assert out.value == 2 * 4096 + 2 * 1024  # (one block and one step of four groups, two tiles)
+    assert [lin(T=17, ws=None), lin(T=17, ws=P + 16), lin(T=17, n=out.value - 1)] == [E, A, tclora.ENOSPC]
+    assert L.tcl_i4_workspace_bytes(w(), 4, ctypes.byref(out)) == 0 and out.value == 0
+    assert L.tcl_i4_workspace_bytes(w(), -1, ctypes.byref(out)) == E
+    assert L.tcl_i4_workspace_bytes(None, 4, ctypes.byref(out)) == E
+    assert L.tcl_i4_workspace_bytes(w(), 4, None) == E
