@@ -27,8 +27,9 @@ struct I4Args {
   void *y;
   int64_t ldx, ldy;
   int32_t T, K, N, kb, groups;
-  int32_t blocks;         // blocks of 128 columns of a group (1 where it is shorter)
-  const nt_u4 *xb, *xe;   // staged activations and their groups' sums
+  uint64_t per_block;     // 2^32 / blocks of 128 columns of a group, rounded up (group_of)
+  const nt_u4 *xb;        // staged activations
+  const float *xe;        // and their groups' sums
   int32_t steps;          // corrections of four groups
   int32_t nt, nc;         // tiles of tokens, of channels
 };
@@ -80,11 +81,12 @@ __global__ __launch_bounds__(256) void i4_pack_kernel(PackArgs a) {
 // in which the products take them, with zeros behind the last token and
 // column: block (token tile, 128 columns) of 4 KiB, piece i of lane l the 16
 // bytes of token l % 16, columns 32 i + 8 (l / 16).  Behind them come the sums
-// of x over the groups (correct): for a token tile and four groups 1 KiB, lane
+// of x over the groups, fp32: for a token tile and four groups 64 of them, lane
 // l token l % 16 of group l / 16.
 struct StageArgs {
   const uint16_t *x;
-  nt_u4 *xb, *xe;
+  nt_u4 *xb;
+  float *xe;
   int64_t ldx;
   int32_t T, K, kb, steps;  // steps: groups / 4, rounded up
 };
@@ -93,7 +95,7 @@ struct StageArgs {
 __device__ inline void split3(float v, uint32_t *p) {
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
-    p[i] = f32_to_bf16(v);
+    p[i] = __builtin_bit_cast(uint16_t, __bf16(v));
     v -= __uint_as_float(p[i] << 16);
   }
 }
@@ -102,10 +104,10 @@ __device__ inline void split3(float v, uint32_t *p) {
 // the matrix cores: columns 8 g + 0 .. 5 of one more step of 32 columns hold
 // parts 0 0 1 0 2 1 of group g's sum against parts 0 1 0 2 0 1 of its factor,
 // which leaves out less than 2^-23 of the product.
-__device__ inline nt_u4 parts_x(float v) {
+__device__ inline bf16x8_t parts_x(float v) {
   uint32_t p[3];
   split3(v, p);
-  return nt_u4{p[0] | p[0] << 16, p[1] | p[0] << 16, p[2] | p[1] << 16, 0};
+  return __builtin_bit_cast(bf16x8_t, nt_u4{p[0] | p[0] << 16, p[1] | p[0] << 16, p[2] | p[1] << 16, 0});
 }
 __device__ inline bf16x8_t parts_w(float v) {
   uint32_t p[3];
@@ -135,26 +137,34 @@ __global__ __launch_bounds__(256) void i4_stage_kernel(StageArgs a) {
     s += __shfl_xor(s, 32, 64);
     sum[i] = s;
   }
-  nt_u4 *xe = a.xe + (int64_t(blockIdx.x) * a.steps + b / PER) * 64 + c;
+  float *xe = a.xe + (int64_t(blockIdx.x) * a.steps + b / PER) * 64 + c;
   if constexpr (GS == 4) {
     const float s = g < 2 ? (g ? sum[1] : sum[0]) : (g == 2 ? sum[2] : sum[3]);
-    xe[16 * g] = parts_x(s);
+    xe[16 * g] = s;
   } else if constexpr (GS == 2) {
-    if (g < 2) xe[16 * (2 * (b & 1) + g)] = parts_x(g ? sum[2] + sum[3] : sum[0] + sum[1]);
+    if (g < 2) xe[16 * (2 * (b & 1) + g)] = g ? sum[2] + sum[3] : sum[0] + sum[1];
   } else {
-    if (g == 0) xe[16 * (b & 3)] = parts_x((sum[0] + sum[1]) + (sum[2] + sum[3]));
+    if (g == 0) xe[16 * (b & 3)] = (sum[0] + sum[1]) + (sum[2] + sum[3]);
   }
 }
 
 // ---------------------------------------------------------------------------
 // products
 // ---------------------------------------------------------------------------
-// eight columns as bf16 numbers 16 + n
-__device__ inline bf16x8_t widen(uint32_t w) {
-  constexpr uint32_t mask = 0x00780078u, base = 0x41804180u;
-  return __builtin_bit_cast(bf16x8_t, nt_u4{(w << 3 & mask) | base, (w >> 1 & mask) | base,
-                                            (w >> 5 & mask) | base, (w >> 9 & mask) | base});
-}
+// Eight columns as bf16 numbers 16 + n.  (The mask in a scalar and the exponent
+// in a vector register, which the compiler has to be told: it then needs one
+// operation for both, with literals two.)
+struct Widen {
+  uint32_t mask, base;
+  __device__ inline Widen() {
+    asm("s_mov_b32 %0, 0x780078" : "=s"(mask));
+    asm("v_mov_b32 %0, 0x41804180" : "=v"(base));
+  }
+  __device__ inline bf16x8_t operator()(uint32_t w) const {
+    return __builtin_bit_cast(bf16x8_t, nt_u4{(w << 3 & mask) | base, (w >> 1 & mask) | base,
+                                              (w >> 5 & mask) | base, (w >> 9 & mask) | base});
+  }
+};
 
 __device__ inline bf16x8_t ones() {
   return __builtin_bit_cast(bf16x8_t, nt_u4{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u});
@@ -164,6 +174,15 @@ __device__ inline f32x4_t mfma(bf16x8_t a, bf16x8_t b, f32x4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 __device__ inline bf16x8_t as_bf16(nt_u4 u) { return __builtin_bit_cast(bf16x8_t, u); }
+
+// The group of block b where groups have blocks of 128 columns, n of them: b /
+// n, exact for b and n up to 2^13.
+__device__ inline int group_of(const I4Args &a, int b) { return int(uint64_t(unsigned(b)) * a.per_block >> 32); }
+// the group of the block's part e (the last block may hold fewer than others)
+template <int GS>
+__device__ inline int group_at(const I4Args &a, int b, int e) {
+  return GS == 1 ? group_of(a, b) : min(b * GS + e, a.groups - 1);
+}
 
 // Four channels of a token to y.
 template <typename TY>
@@ -211,6 +230,7 @@ __device__ inline void join(const I4Args &a, const f32x4_t (&acc)[MT][NB],
 // for groups of several blocks).
 template <int MT, int NB, int WV, int GS, bool ZP, typename TY>
 __global__ __launch_bounds__(64 * WV) void i4_rows(I4Args a) {
+  const Widen widen;
   __shared__ float part[WV][NB][16 * kPartLd];
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   const int c = lane & 15, g = lane >> 4;
@@ -244,7 +264,7 @@ __global__ __launch_bounds__(64 * WV) void i4_rows(I4Args a) {
 #pragma unroll
       for (int e = 0; e < GS; ++e) {
         // (the last block may hold fewer groups than others)
-        const int gr = GS == 1 ? b / a.blocks : min(b * GS + e, a.groups - 1);
+        const int gr = group_at<GS>(a, b, e);
         s[n][e] = sp[n][gr * 16];
         z[n][e] = ZP ? 16.f + float(zp[n][gr * 16]) : 24.f;
       }
@@ -314,23 +334,30 @@ struct Correct {
     sp = a.scale + ct * a.groups * 16 + c;
     zp = ZP ? a.zero + ct * a.groups * 16 + c : nullptr;
   }
+  struct Raw {
+    float s;
+    uint8_t z;
+  };
   // (groups behind the last meet sums of zero)
-  __device__ inline bf16x8_t operand(const I4Args &a, int step, int g) const {
-    const int gr = min(GS == 1 ? (4 * step + g) / a.blocks : 4 * step + g, a.groups - 1);
-    return parts_w(-sp[gr * 16] * (ZP ? 16.f + float(zp[gr * 16]) : 24.f));
+  __device__ inline Raw load(const I4Args &a, int step, int g) const {
+    const int gr = min(GS == 1 ? group_of(a, 4 * step + g) : 4 * step + g, a.groups - 1);
+    return {sp[gr * 16], ZP ? zp[gr * 16] : uint8_t(8)};
   }
+  __device__ inline bf16x8_t operand(Raw r) const { return parts_w(-r.s * (16.f + float(r.z))); }
 };
 
 // More tokens, from staged activations: as i4_rows, but the corrections are
 // steps of their own, dealt out to the waves behind the blocks.
 template <int MT, int NB, int WV, int GS, bool ZP, typename TY>
 __global__ __launch_bounds__(64 * WV) void i4_blocks(I4Args a) {
+  const Widen widen;
   __shared__ float part[WV][NB][16 * kPartLd];
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   const int c = lane & 15, g = lane >> 4;
   const int c0 = blockIdx.x * 16 * NB, t0 = blockIdx.y * 16 * MT;
   const int tiles = (a.N + 15) / 16, tt = (a.T + 15) / 16;
-  const nt_u4 *xp[MT], *ep[MT];
+  const nt_u4 *xp[MT];
+  const float *ep[MT];
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     const int64_t tile = min(t0 / 16 + m, tt - 1);
@@ -358,7 +385,7 @@ __global__ __launch_bounds__(64 * WV) void i4_blocks(I4Args a) {
       wq[n] = *reinterpret_cast<const nt_u4 *>(wp[n] + int64_t(b) * 1024);
 #pragma unroll
       for (int e = 0; e < GS; ++e)
-        s[n][e] = co[n].sp[(GS == 1 ? b / a.blocks : min(b * GS + e, a.groups - 1)) * 16];
+        s[n][e] = co[n].sp[(group_at<GS>(a, b, e)) * 16];
     }
   };
   auto load_x = [&](int m, int b, nt_u4 (&x)[4]) {
@@ -408,10 +435,10 @@ __global__ __launch_bounds__(64 * WV) void i4_blocks(I4Args a) {
   for (int st = w; st < a.steps; st += WV) {
     bf16x8_t f[NB];
 #pragma unroll
-    for (int n = 0; n < NB; ++n) f[n] = co[n].operand(a, st, g);
+    for (int n = 0; n < NB; ++n) f[n] = co[n].operand(co[n].load(a, st, g));
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      const bf16x8_t x = as_bf16(ep[m][int64_t(st) * 64]);
+      const bf16x8_t x = parts_x(ep[m][int64_t(st) * 64]);
 #pragma unroll
       for (int n = 0; n < NB; ++n) acc[m][n] = mfma(x, f[n], acc[m][n]);
     }
@@ -419,38 +446,92 @@ __global__ __launch_bounds__(64 * WV) void i4_blocks(I4Args a) {
   join<MT, NB, WV, TY>(a, acc, part, t0, c0);
 }
 
-// Many tokens: tiles of BC channels by BT tokens, WC by WT waves.  A step's
-// activations (128 columns) go through LDS, two stages; a wave's weights come
-// straight from memory, a step ahead.
-template <int BC, int BT, int WC, int WT, int GS, bool ZP, typename TY>
-__global__ __launch_bounds__(64 * WC * WT) void i4_tile(I4Args a) {
-  constexpr int TH = 64 * WC * WT, NB = BC / WC / 16, MT = BT / WT / 16, PER = 4 / GS;
-  constexpr int PIECES = BT / 16 * 256, NP = PIECES / TH;
-  __shared__ nt_u4 lx[2][PIECES];
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, c = lane & 15, g = lane >> 4;
+// Loads straight into LDS: 64 lanes write 16 (or 4) bytes each, in a row from
+// `to`; the compiler does not count them (arrived).  An immediate offset moves
+// source and destination alike.
+__device__ inline uint32_t lds_at(const void *p) {
+  return uint32_t(uintptr_t((__attribute__((address_space(3))) const char *)(p)));
+}
+template <int N>
+__device__ inline void move16(uint32_t to, const void *from, uint32_t off) {
+  static_assert(N == 1 || N == 2 || N == 4, "pieces of 1 KiB");
+  if constexpr (N == 4)
+    asm volatile(
+        "s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2\n\t"
+        "global_load_lds_dwordx4 %1, %2 offset:1024\n\tglobal_load_lds_dwordx4 %1, %2 offset:2048\n\t"
+        "global_load_lds_dwordx4 %1, %2 offset:3072" ::"s"(to), "v"(off), "s"(from) : "memory", "m0");
+  else if constexpr (N == 2)
+    asm volatile(
+        "s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2\n\t"
+        "global_load_lds_dwordx4 %1, %2 offset:1024" ::"s"(to), "v"(off), "s"(from) : "memory", "m0");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(off),
+                 "s"(from)
+                 : "memory", "m0");
+}
+__device__ inline void move4(uint32_t to, const void *from, uint32_t off) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(to), "v"(off), "s"(from)
+               : "memory", "m0");
+}
+
+// Many tokens: tiles of 256 channels by BT tokens, WC by 8 / WC waves.  Blocks
+// of 128 columns go through LDS in three stages, activations and weights alike,
+// each filled while the block two before it is multiplied (a wave's own
+// registers hold no load: one block's time does not cover a trip to memory);
+// scales, zero points and sums of x come with every four groups.
+template <int BT, int WC, int GS, bool ZP, typename TY>
+__global__ __launch_bounds__(512, 2) void i4_tile(I4Args a) {
+  const Widen widen;
+  constexpr int BC = 256, WV = 8, WT = WV / WC, NB = BC / WC / 16, MT = BT / WT / 16, PER = 4 / GS;
+  constexpr int NX = BT / 16 * 4 / WV;  // KiB of activations a wave moves a block
+  constexpr int NS = BT / 16 > WV ? BT / 16 / WV : 1;
+  __shared__ struct {
+    nt_u4 x[3][BT / 16 * 256];
+    nt_u4 w[3][BC / 16 * 64];
+    float sum[2][BT / 16 * 64];   // of four groups
+    float s[2][BC / 16 * 64];
+    uint8_t z[2][BC / 16 * 64];
+  } l;
+  const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, g = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   // workgroups go to the eight XCDs in turn: each gets a run of tiles, token
   // tiles next to each other, so that its L2 holds their weights
   const int n_all = a.nt * a.nc, per = (n_all + 7) / 8;
   const int id = int(blockIdx.x & 7) * per + int(blockIdx.x >> 3);
   if (int(blockIdx.x >> 3) >= per || id >= n_all) return;
-  const int c0 = id / a.nt * BC + (w % WC) * (BC / WC), t0 = id % a.nt * BT;
-  const int wt = (w / WC) * MT;  // the wave's first token tile
+  const int c0 = id / a.nt * BC, t0 = id % a.nt * BT;
+  const int wc = (w % WC) * NB, wt = (w / WC) * MT;  // the wave's first tiles
   const int tiles = (a.N + 15) / 16, tt = (a.T + 15) / 16;
-  const uint8_t *wp[NB];
-  Correct<GS, ZP> co[NB];
+  // (tiles past the last: the last again, not stored)
+  auto c_tile = [&](int i) { return int64_t(min(c0 / 16 + i, tiles - 1)); };
+  auto t_tile = [&](int i) { return int64_t(min(t0 / 16 + i, tt - 1)); };
+  auto stage = [&](int b, int slot) {
+    move16<NX>(lds_at(&l.x[slot][w * NX * 64]),
+               a.xb + (t_tile(w * NX / 4) * a.kb + b) * 256 + w * NX % 4 * 64, 16 * lane);
 #pragma unroll
-  for (int n = 0; n < NB; ++n) {
-    const int64_t ct = min(c0 / 16 + n, tiles - 1);
-    wp[n] = a.w + ct * a.kb * 1024 + 16 * lane;
-    co[n].init(a, ct, c);
-  }
-  auto stage = [&](int b, int buf) {
+    for (int i = 0; i < 2; ++i)
+      move16<1>(lds_at(&l.w[slot][(2 * w + i) * 64]), a.w + (c_tile(2 * w + i) * a.kb + b) * 1024, 16 * lane);
+  };
+  // A step's groups; lanes of groups behind the last take the last one's
+  // factors, their sums are zero.
+  auto stage_step = [&](int st) {
+    const int sl = st & 1;
 #pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      const int p = (w * NP + i) * 64;  // the wave's 64 pieces
-      const nt_u4 *from = a.xb + (int64_t(min(t0 / 16 + p / 256, tt - 1)) * a.kb + b) * 256 + p % 256 + lane;
-      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint32_t *)(from),
-                                       (__attribute__((address_space(3))) uint32_t *)(&lx[buf][p]), 16, 0, 0);
+    for (int i = 0; i < NS; ++i) {
+      const int t = (w * NS + i) % (BT / 16);
+      move4(lds_at(&l.sum[sl][t * 64]), a.xe + (t_tile(t) * a.steps + st) * 64, 4 * lane);
+    }
+    const int gr = min(GS == 1 ? group_of(a, 4 * st + g) : 4 * st + g, a.groups - 1);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      move4(lds_at(&l.s[sl][(2 * w + i) * 64]), a.scale + c_tile(2 * w + i) * a.groups * 16,
+            4 * (gr * 16 + c));
+    if constexpr (ZP) {
+      // four channel tiles an instruction, four channels a lane
+      const int i = w % 4, gz = min(GS == 1 ? group_of(a, 4 * st + (lane >> 2 & 3)) : 4 * st + (lane >> 2 & 3),
+                                    a.groups - 1);
+      move4(lds_at(&l.z[sl][4 * i * 64]), a.zero + c_tile(4 * i) * a.groups * 16,
+            uint32_t((c_tile(4 * i + g) - c_tile(4 * i)) * a.groups * 16 + gz * 16 + 4 * (lane & 3)));
     }
   };
   f32x4_t acc[MT][NB];
@@ -458,39 +539,35 @@ __global__ __launch_bounds__(64 * WC * WT) void i4_tile(I4Args a) {
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int n = 0; n < NB; ++n) acc[m][n] = f32x4_t{0, 0, 0, 0};
-  nt_u4 wq[NB];
-  float s[NB][GS];
-  auto load_w = [&](int b) {
-#pragma unroll
-    for (int n = 0; n < NB; ++n) {
-      wq[n] = *reinterpret_cast<const nt_u4 *>(wp[n] + int64_t(b) * 1024);
-#pragma unroll
-      for (int e = 0; e < GS; ++e)
-        s[n][e] = co[n].sp[(GS == 1 ? b / a.blocks : min(b * GS + e, a.groups - 1)) * 16];
-    }
-  };
+  stage_step(0);
   stage(0, 0);
-  load_w(0);
+  stage(min(1, a.kb - 1), 1);
+  int slot = 0;
   for (int b = 0; b < a.kb; ++b) {
-    const int buf = b & 1;
-    __syncthreads();
-    const int next = min(b + 1, a.kb - 1);
-    stage(next, buf ^ 1);
+    // all but the newest block's loads have come; every wave is done with
+    // what the next loads write
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(NX + 2) : "memory");
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+    if ((b + 1) % PER == 0) stage_step(min((b + 1) / PER, a.steps - 1));
+    stage(min(b + 2, a.kb - 1), slot == 0 ? 2 : slot - 1);
+    const int sl = b / PER & 1;
     bf16x8_t wf[NB][4];
     float sc[NB][GS];
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
+      const nt_u4 q = l.w[slot][(wc + n) * 64 + lane];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) wf[n][i] = widen(wq[n][i]);
+      for (int i = 0; i < 4; ++i) wf[n][i] = widen(q[i]);
 #pragma unroll
-      for (int e = 0; e < GS; ++e) sc[n][e] = s[n][e];
+      for (int e = 0; e < GS; ++e) sc[n][e] = l.s[sl][(wc + n) * 64 + (b % PER * GS + e) * 16 + c];
     }
-    load_w(next);
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       nt_u4 xc[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) xc[i] = lx[buf][(wt + m) * 256 + 64 * i + lane];
+      for (int i = 0; i < 4; ++i) xc[i] = l.x[slot][(wt + m) * 256 + 64 * i + lane];
 #pragma unroll
       for (int e = 0; e < GS; ++e) {
         f32x4_t p[NB];
@@ -508,24 +585,28 @@ __global__ __launch_bounds__(64 * WC * WT) void i4_tile(I4Args a) {
     }
     // corrections every four groups, so that sums stay small
     if (b % PER == PER - 1 || b == a.kb - 1) {
-      const int st = b / PER;
       bf16x8_t f[NB];
 #pragma unroll
-      for (int n = 0; n < NB; ++n) f[n] = co[n].operand(a, st, g);
+      for (int n = 0; n < NB; ++n) {
+        const int at = (wc + n) * 64 + lane;
+        f[n] = parts_w(-l.s[sl][at] * (ZP ? 16.f + float(l.z[sl][at]) : 24.f));
+      }
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        const bf16x8_t x = as_bf16(a.xe[(int64_t(min(t0 / 16 + wt + m, tt - 1)) * a.steps + st) * 64 + lane]);
+        const bf16x8_t x = parts_x(l.sum[sl][(wt + m) * 64 + lane]);
 #pragma unroll
         for (int n = 0; n < NB; ++n) acc[m][n] = mfma(x, f[n], acc[m][n]);
       }
     }
+    slot = slot == 2 ? 0 : slot + 1;
   }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
   // Results through LDS, a wave's 16 tokens at a time, so that a store covers
   // whole lines of y.
-  __syncthreads();
   constexpr int LD = 16 * NB + 4;
-  static_assert(WC * WT * 16 * LD * 4 <= int(sizeof(lx)), "LDS of the results");
-  float *out = reinterpret_cast<float *>(&lx) + w * 16 * LD;
+  static_assert(WV * 16 * LD * 4 <= int(sizeof(l)), "LDS of the results");
+  float *out = reinterpret_cast<float *>(&l) + w * 16 * LD;
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
 #pragma unroll
@@ -537,8 +618,8 @@ __global__ __launch_bounds__(64 * WC * WT) void i4_tile(I4Args a) {
 #pragma unroll
     for (int k = 0; k < NB; ++k) {
       const int o = k * 64 + lane, x = o / (4 * NB), t = t0 + 16 * (wt + m) + x, ch = o % (4 * NB) * 4;
-      if (t < a.T && c0 + ch < a.N)
-        store4<TY>(a, t, c0 + ch, *reinterpret_cast<const nt_f4 *>(out + x * LD + ch));
+      if (t < a.T && c0 + 16 * wc + ch < a.N)
+        store4<TY>(a, t, c0 + 16 * wc + ch, *reinterpret_cast<const nt_f4 *>(out + x * LD + ch));
     }
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
@@ -599,12 +680,11 @@ void go_blocks(const I4Args &a, hipStream_t s) {
                      s, a);
 }
 
-template <int BC, int BT, int WC, int WT, int GS, bool ZP, typename TY>
+template <int BT, int WC, int GS, bool ZP, typename TY>
 void go_tile(I4Args a, hipStream_t s) {
   a.nt = (a.T + BT - 1) / BT;
-  a.nc = (a.N + BC - 1) / BC;
-  hipLaunchKernelGGL((i4_tile<BC, BT, WC, WT, GS, ZP, TY>), dim3((a.nt * a.nc + 7) / 8 * 8),
-                     dim3(64 * WC * WT), 0, s, a);
+  a.nc = (a.N + 255) / 256;
+  hipLaunchKernelGGL((i4_tile<BT, WC, GS, ZP, TY>), dim3((a.nt * a.nc + 7) / 8 * 8), dim3(512), 0, s, a);
 }
 
 template <int GS, bool ZP, typename TY>
@@ -612,7 +692,7 @@ void product(const I4Args &a, hipStream_t s) {
   if (a.T <= kRows)
     go_rows<1, 1, 8, GS, ZP, TY>(a, s);
   else {
-    const StageArgs g{a.x, const_cast<nt_u4 *>(a.xb), const_cast<nt_u4 *>(a.xe), a.ldx, a.T, a.K, a.kb,
+    const StageArgs g{a.x, const_cast<nt_u4 *>(a.xb), const_cast<float *>(a.xe), a.ldx, a.T, a.K, a.kb,
                       a.steps};
     hipLaunchKernelGGL(i4_stage_kernel<GS>, dim3((a.T + 15) / 16, (a.steps * (4 / GS) + 3) / 4), dim3(256), 0,
                        s, g);
@@ -621,7 +701,7 @@ void product(const I4Args &a, hipStream_t s) {
     else if (a.T <= 64)
       go_blocks<4, 4, 8, GS, ZP, TY>(a, s);
     else
-      go_tile<256, 128, 4, 1, GS, ZP, TY>(a, s);
+      go_tile<128, 4, GS, ZP, TY>(a, s);
   }
 }
 
@@ -691,7 +771,7 @@ Space space(const tcl_i4_weight *w, const Layout &l, int32_t n_tokens) {
   const int32_t groups = w->group < 128 ? l.groups : l.kb;  // longer ones count by their blocks
   const int32_t steps = (groups + 3) / 4;
   const size_t x = tiles * l.kb * 4096;
-  return {x, x + tiles * steps * 1024, steps};
+  return {x, x + tiles * steps * 256, steps};
 }
 
 int check_tokens(const tcl_i4_weight *w, int32_t n_tokens) {
@@ -739,8 +819,8 @@ extern "C" int tcl_i4_linear(const tcl_i4_weight *w, const void *x, int64_t ldx,
   char *q = static_cast<char *>(ws);
   I4Args a{p, reinterpret_cast<const float *>(p + l.w), w->zeros ? p + l.scale : nullptr,
            static_cast<const uint16_t *>(x), y, ldx, ldy, n_tokens, w->d_in, w->d_out, l.kb, l.groups,
-           w->group < 128 ? 1 : w->group / 128, reinterpret_cast<nt_u4 *>(q),
-           reinterpret_cast<nt_u4 *>(q + sp.x), sp.steps, 0, 0};
+           w->group < 128 ? 0 : ((uint64_t(1) << 32) + w->group / 128 - 1) / (w->group / 128), reinterpret_cast<nt_u4 *>(q),
+           reinterpret_cast<float *>(q + sp.x), sp.steps, 0, 0};
   hipStream_t s = static_cast<hipStream_t>(stream);
   logf("i4: tokens=%d d_in=%d d_out=%d group=%d zeros=%d", a.T, a.K, a.N, w->group, w->zeros);
   if (w->group == 32)

@@ -685,7 +685,7 @@ def test_i4_host_errors(L):
     assert lin(T=0) == 0 and lin(d_out=0, x=None) == 0
     assert lin(T=0, W=None, scale=None, zero=None) == 0
     assert [L.tcl_i4_workspace_bytes(w(), T, ctypes.byref(out)) for T in (16, 17)] == [0, 0]
-    assert out.value == 2 * 4096 + 2 * 1024  # (one block and one step of four groups, two tiles)
+    assert out.value == 2 * 4096 + 2 * 256  # (one block and one step of four groups, two tiles)
     assert [lin(T=17, ws=None), lin(T=17, ws=P + 16), lin(T=17, n=out.value - 1)] == [E, A, tclora.ENOSPC]
     assert L.tcl_i4_workspace_bytes(w(), 4, ctypes.byref(out)) == 0 and out.value == 0
     assert L.tcl_i4_workspace_bytes(w(), -1, ctypes.byref(out)) == E
