@@ -2,18 +2,28 @@
 // formulas): bf16 activations, integers 0..15 with a scale and a zero point
 // for each group of a channel's weights.
 //
-// An integer n becomes the bf16 number 16 + n by two operations on a pair of
-// them (a shift, and its four bits under the exponent of 16), exactly.  The
-// matrix cores sum x (16 + n) over a group, and the sums of x over the group
-// come from one more operand, of ones; then
-//   s sum x (n - z) = s (sum x (16 + n) - (16 + z) sum x)
-// is two fused operations an output and group, in fp32.  No weight is rounded.
+// An integer n becomes the bf16 number 16 + n by at most two operations on a
+// pair of them (a shift, and its four bits under the exponent of 16), exactly.
+// The matrix cores sum x (16 + n) over a group, and with the sums of x over the
+// groups
+//   y = sum_g s_g sum_g x (n - z) = sum_g s_g sum_g x (16 + n) - sum_g s_g (16 + z_g) sum_g x
+// takes one fused operation an output and group, in fp32, and a short product
+// of fp32 numbers in bf16 parts.  No weight is rounded.
 //
-// The packed weight holds blocks of 16 channels by 128 columns in the order in
-// which the lanes of a wave take them (1 KiB a load): dword i of lane l has
-// channel l % 16, columns 32 i + 8 (l / 16) + 0..7, column 2 j at bit 4 j and
-// column 2 j + 1 at bit 16 + 4 j.  Behind the blocks come the scales, 16
-// channels of a group side by side, and the zero points likewise.
+// Three kernels:
+//   i4_rows    up to 16 tokens, straight from their rows, one launch;
+//   i4_blocks  more: the activations are laid out first (i4_stage_kernel); the
+//              weight streams from memory into matrix-core operands, the waves
+//              of a workgroup split d_in and add their sums in LDS;
+//   i4_tile    many: tiles of both operands go through LDS.
+//
+// The packed weight holds blocks of 32 channels by 64 columns, 1 KiB, 16 bytes a
+// lane: lane l has channel l % 32 and, in its dwords 0..3, the eights of columns
+// o, 4 + o, 2 + o and 6 + o of the block, o = l / 32.  A lane of a 32 x 32 x 16
+// product takes all four, one of a 16 x 16 x 32 product one half.  Columns 2 j
+// and 2 j + 1 of an eight lie at bits 3 + 4 j and 19 + 4 j, those beyond bit 31
+// at its start.  Behind the blocks come the scales, 32 channels of a group side
+// by side, and the zero points likewise.
 #include "kern_common.hpp"
 
 namespace tcl {
@@ -21,12 +31,12 @@ namespace {
 
 struct I4Args {
   const uint8_t *w;       // packed blocks
-  const float *scale;     // [channel tile][group][16]
+  const float *scale;     // [32 channels][group][32]
   const uint8_t *zero;    // the same, or NULL: 8
   const uint16_t *x;
   void *y;
   int64_t ldx, ldy;
-  int32_t T, K, N, kb, groups;
+  int32_t T, K, N, kb, groups;  // kb: 128 columns
   uint64_t per_block;     // 2^32 / blocks of 128 columns of a group, rounded up (group_of)
   const nt_u4 *xb;        // staged activations
   const float *xe;        // and their groups' sums
@@ -51,24 +61,26 @@ __global__ __launch_bounds__(256) void i4_pack_kernel(PackArgs a) {
   for (int64_t p = at; p < a.n_w; p += step) {
     const int lane = int(p & 63);
     const int64_t blk = p >> 6;
-    const int c = int(blk / a.kb) * 16 + (lane & 15), k0 = int(blk % a.kb) * 128 + 8 * (lane >> 4);
+    const int c = int(blk / (2 * a.kb)) * 32 + (lane & 31);
+    const int k0 = int(blk % (2 * a.kb)) * 64 + 8 * (lane >> 5);
     nt_u4 out;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+      const int k = k0 + 16 * ((i & 1) << 1 | i >> 1);
       uint32_t u = 0;
-      if (c < a.N && k0 + 32 * i < a.K) {  // (d_in is a multiple of 32)
-        const uint32_t b = *reinterpret_cast<const uint32_t *>(a.W + (int64_t(c) * a.K + k0 + 32 * i) / 2);
+      if (c < a.N && k < a.K) {  // (d_in is a multiple of 32)
+        const uint32_t b = *reinterpret_cast<const uint32_t *>(a.W + (int64_t(c) * a.K + k) / 2);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           u |= (b >> 8 * j & 15) << 4 * j | (b >> (8 * j + 4) & 15) << (16 + 4 * j);
       }
-      out[i] = u;
+      out[i] = u << 3 | u >> 29;
     }
     reinterpret_cast<nt_u4 *>(a.w)[p] = out;
   }
   for (int64_t p = at; p < a.n_s; p += step) {
-    const int64_t tg = p >> 4;
-    const int c = int(tg / a.groups) * 16 + int(p & 15), g = int(tg % a.groups);
+    const int64_t tg = p >> 5;
+    const int c = int(tg / a.groups) * 32 + int(p & 31), g = int(tg % a.groups);
     a.ps[p] = c < a.N ? a.scale[int64_t(c) * a.groups + g] : 0.f;
     if (a.zero) a.pz[p] = c < a.N ? a.zero[int64_t(c) * a.groups + g] : 8;
   }
@@ -79,10 +91,9 @@ __global__ __launch_bounds__(256) void i4_pack_kernel(PackArgs a) {
 // ---------------------------------------------------------------------------
 // For more than a few tokens the activations are laid out once, in the order
 // in which the products take them, with zeros behind the last token and
-// column: block (token tile, 128 columns) of 4 KiB, piece i of lane l the 16
-// bytes of token l % 16, columns 32 i + 8 (l / 16).  Behind them come the sums
-// of x over the groups, fp32: for a token tile and four groups 64 of them, lane
-// l token l % 16 of group l / 16.
+// column: 4 KiB of 32 tokens by 64 columns, piece i of lane l the 16 bytes of
+// token l % 32, columns 16 i + 8 (l / 32).  Behind them come the sums of x over
+// the groups, fp32: [32 tokens][four groups][4][32].
 struct StageArgs {
   const uint16_t *x;
   nt_u4 *xb;
@@ -91,60 +102,34 @@ struct StageArgs {
   int32_t T, K, kb, steps;  // steps: groups / 4, rounded up
 };
 
-// v = p[0] + p[1] + p[2] in bf16 numbers, the rest below 2^-24 of v
-__device__ inline void split3(float v, uint32_t *p) {
-#pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    p[i] = __builtin_bit_cast(uint16_t, __bf16(v));
-    v -= __uint_as_float(p[i] << 16);
-  }
-}
-
-// The correction of a group, -(s (16 + z)) sum x, as products of bf16 parts on
-// the matrix cores: columns 8 g + 0 .. 5 of one more step of 32 columns hold
-// parts 0 0 1 0 2 1 of group g's sum against parts 0 1 0 2 0 1 of its factor,
-// which leaves out less than 2^-23 of the product.
-__device__ inline bf16x8_t parts_x(float v) {
-  uint32_t p[3];
-  split3(v, p);
-  return __builtin_bit_cast(bf16x8_t, nt_u4{p[0] | p[0] << 16, p[1] | p[0] << 16, p[2] | p[1] << 16, 0});
-}
-__device__ inline bf16x8_t parts_w(float v) {
-  uint32_t p[3];
-  split3(v, p);
-  return __builtin_bit_cast(bf16x8_t, nt_u4{p[0] | p[1] << 16, p[0] | p[2] << 16, p[0] | p[1] << 16, 0});
-}
-
-// A wave a block.
+// 32 tokens by 128 columns a wave.
 template <int GS>
 __global__ __launch_bounds__(256) void i4_stage_kernel(StageArgs a) {
   constexpr int PER = 4 / GS;  // blocks of a correction step
-  const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+  const int lane = threadIdx.x & 63, c = lane & 31, h = lane >> 5;
   const int b = blockIdx.y * 4 + (threadIdx.x >> 6);
-  const int t = blockIdx.x * 16 + c;
+  const int t = blockIdx.x * 32 + c;
   if (b >= a.steps * PER) return;
-  float sum[4];
+  float sum[4] = {0, 0, 0, 0};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int k = 128 * b + 32 * i + 8 * g;
+  for (int i = 0; i < 8; ++i) {
+    const int k = 128 * b + 16 * i + 8 * h;
     nt_u4 u = {0, 0, 0, 0};
     if (t < a.T && k < a.K) u = *reinterpret_cast<const nt_u4 *>(a.x + t * a.ldx + k);
-    if (b < a.kb) a.xb[(int64_t(blockIdx.x) * a.kb + b) * 256 + 64 * i + lane] = u;
-    float s = 0.f;
+    if (b < a.kb) a.xb[(int64_t(blockIdx.x) * a.kb + b) * 512 + 64 * i + lane] = u;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) s += bf16_lo(u[e]) + bf16_hi(u[e]);
-    s += __shfl_xor(s, 16, 64);
-    s += __shfl_xor(s, 32, 64);
-    sum[i] = s;
+    for (int e = 0; e < 4; ++e) sum[i / 2] += bf16_lo(u[e]) + bf16_hi(u[e]);
   }
-  float *xe = a.xe + (int64_t(blockIdx.x) * a.steps + b / PER) * 64 + c;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) sum[i] += __shfl_xor(sum[i], 32, 64);
+  float *xe = a.xe + (int64_t(blockIdx.x) * a.steps + b / PER) * 128 + c;
   if constexpr (GS == 4) {
-    const float s = g < 2 ? (g ? sum[1] : sum[0]) : (g == 2 ? sum[2] : sum[3]);
-    xe[16 * g] = s;
+    xe[32 * h] = h ? sum[1] : sum[0];
+    xe[64 + 32 * h] = h ? sum[3] : sum[2];
   } else if constexpr (GS == 2) {
-    if (g < 2) xe[16 * (2 * (b & 1) + g)] = g ? sum[2] + sum[3] : sum[0] + sum[1];
+    xe[64 * (b & 1) + 32 * h] = h ? sum[2] + sum[3] : sum[0] + sum[1];
   } else {
-    if (g == 0) xe[16 * (b & 3)] = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    if (h == 0) xe[32 * (b & 3)] = (sum[0] + sum[1]) + (sum[2] + sum[3]);
   }
 }
 
@@ -161,8 +146,9 @@ struct Widen {
     asm("v_mov_b32 %0, 0x41804180" : "=v"(base));
   }
   __device__ inline bf16x8_t operator()(uint32_t w) const {
-    return __builtin_bit_cast(bf16x8_t, nt_u4{(w << 3 & mask) | base, (w >> 1 & mask) | base,
-                                              (w >> 5 & mask) | base, (w >> 9 & mask) | base});
+    const uint32_t top = __builtin_amdgcn_alignbit(w, w, 12);
+    return __builtin_bit_cast(bf16x8_t, nt_u4{(w & mask) | base, (w >> 4 & mask) | base,
+                                              (w >> 8 & mask) | base, (top & mask) | base});
   }
 };
 
@@ -170,8 +156,15 @@ __device__ inline bf16x8_t ones() {
   return __builtin_bit_cast(bf16x8_t, nt_u4{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u});
 }
 
+typedef __attribute__((__vector_size__(16 * sizeof(float)))) float f32x16_t;
 __device__ inline f32x4_t mfma(bf16x8_t a, bf16x8_t b, f32x4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ inline f32x16_t mfma(bf16x8_t a, bf16x8_t b, f32x16_t c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ inline f32x16_t nothing() {
+  return f32x16_t{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
 }
 __device__ inline bf16x8_t as_bf16(nt_u4 u) { return __builtin_bit_cast(bf16x8_t, u); }
 
@@ -182,6 +175,30 @@ __device__ inline int group_of(const I4Args &a, int b) { return int(uint64_t(uns
 template <int GS>
 __device__ inline int group_at(const I4Args &a, int b, int e) {
   return GS == 1 ? group_of(a, b) : min(b * GS + e, a.groups - 1);
+}
+
+// v = p[0] + p[1] + p[2] in bf16 numbers, the rest below 2^-24 of v
+__device__ inline void split3(float v, uint32_t *p) {
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    p[i] = __builtin_bit_cast(uint16_t, __bf16(v));
+    v -= __uint_as_float(p[i] << 16);
+  }
+}
+
+// The correction of a group, -(s (16 + z)) sum x, as products of bf16 parts on
+// the matrix cores: columns 0 .. 5 of a lane's eight hold parts 0 0 1 0 2 1 of
+// its group's sum against parts 0 1 0 2 0 1 of its factor, which leaves out less
+// than 2^-23 of the product.
+__device__ inline bf16x8_t parts_x(float v) {
+  uint32_t p[3];
+  split3(v, p);
+  return as_bf16(nt_u4{p[0] | p[0] << 16, p[1] | p[0] << 16, p[2] | p[1] << 16, 0});
+}
+__device__ inline bf16x8_t parts_w(float v) {
+  uint32_t p[3];
+  split3(v, p);
+  return as_bf16(nt_u4{p[0] | p[1] << 16, p[0] | p[2] << 16, p[0] | p[1] << 16, 0});
 }
 
 // Four channels of a token to y.
@@ -196,30 +213,18 @@ __device__ inline void store4(const I4Args &a, int t, int ch, nt_f4 v) {
   }
 }
 
-// The waves' sums of 16 MT tokens by 16 NB channels, added in order, 16 tokens
-// at a time, and stored.
-constexpr int kPartLd = 20;  // floats of a token's 16 channels in LDS
-template <int MT, int NB, int WV, typename TY>
-__device__ inline void join(const I4Args &a, const f32x4_t (&acc)[MT][NB],
-                            float (&part)[WV][NB][16 * kPartLd], int t0, int c0) {
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, c = lane & 15, g = lane >> 4;
+// The waves' sums of a tile of R tokens by 16 CH channels, added in order, and
+// stored: part[wave][token][LD].
+template <int R, int CH, int LD, int WV, typename TY>
+__device__ inline void add_up(const I4Args &a, const float *part, int t0, int c0) {
+  for (int o = threadIdx.x; o < R * CH * 4; o += 64 * WV) {
+    const int r = o / (4 * CH), t = t0 + r, ch = c0 + o % (4 * CH) * 4;
+    if (t >= a.T || ch >= a.N) continue;
+    const float *in = part + r * LD + o % (4 * CH) * 4;
+    nt_f4 v = *reinterpret_cast<const nt_f4 *>(in);
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    if (m) __syncthreads();
-#pragma unroll
-    for (int n = 0; n < NB; ++n)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) part[w][n][(4 * g + r) * kPartLd + c] = acc[m][n][r];
-    __syncthreads();
-    for (int o = tid; o < NB * 64; o += 64 * WV) {
-      const int n = o >> 6, t = t0 + 16 * m + (o >> 2 & 15), ch = c0 + 16 * n + 4 * (o & 3);
-      if (t >= a.T || ch >= a.N) continue;
-      const float *in = &part[0][n][(o >> 2 & 15) * kPartLd + 4 * (o & 3)];
-      nt_f4 v = *reinterpret_cast<const nt_f4 *>(in);
-#pragma unroll
-      for (int i = 1; i < WV; ++i) v += *reinterpret_cast<const nt_f4 *>(in + i * NB * 16 * kPartLd);
-      store4<TY>(a, t, ch, v);
-    }
+    for (int i = 1; i < WV; ++i) v += *reinterpret_cast<const nt_f4 *>(in + i * R * LD);
+    store4<TY>(a, t, ch, v);
   }
 }
 
@@ -231,8 +236,9 @@ __device__ inline void join(const I4Args &a, const f32x4_t (&acc)[MT][NB],
 template <int MT, int NB, int WV, int GS, bool ZP, typename TY>
 __global__ __launch_bounds__(64 * WV) void i4_rows(I4Args a) {
   const Widen widen;
-  __shared__ float part[WV][NB][16 * kPartLd];
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  constexpr int LD = 16 * NB + 4;
+  __shared__ __align__(16) float part[WV * 16 * LD];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int c = lane & 15, g = lane >> 4;
   const int c0 = blockIdx.x * 16 * NB, t0 = blockIdx.y * 16 * MT;
   const int tiles = (a.N + 15) / 16;
@@ -245,28 +251,31 @@ __global__ __launch_bounds__(64 * WV) void i4_rows(I4Args a) {
 #pragma unroll
   for (int n = 0; n < NB; ++n) {
     // (channel tiles past the last: the last one again, not stored)
-    const int64_t ct = min(blockIdx.x * NB + n, unsigned(tiles - 1));
-    wp[n] = a.w + ct * a.kb * 1024 + 16 * lane;
-    sp[n] = a.scale + ct * a.groups * 16 + c;
-    zp[n] = ZP ? a.zero + ct * a.groups * 16 + c : nullptr;
+    const int ct = int(min(blockIdx.x * NB + n, unsigned(tiles - 1)));
+    const int64_t t32 = ct >> 1;
+    wp[n] = a.w + t32 * a.kb * 2048 + (g & 1) * 512 + (ct & 1) * 256 + c * 16 + (g >> 1) * 8;
+    sp[n] = a.scale + t32 * a.groups * 32 + (ct & 1) * 16 + c;
+    zp[n] = ZP ? a.zero + t32 * a.groups * 32 + (ct & 1) * 16 + c : nullptr;
   }
   f32x4_t acc[MT][NB];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int n = 0; n < NB; ++n) acc[m][n] = f32x4_t{0, 0, 0, 0};
-  nt_u4 wq[NB], xr[MT][4];
+  nt_u2 wq[NB][2];
+  nt_u4 xr[MT][4];
   float s[NB][GS], z[NB][GS];
   auto load_w = [&](int b) {
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
-      wq[n] = *reinterpret_cast<const nt_u4 *>(wp[n] + int64_t(b) * 1024);
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        wq[n][k] = *reinterpret_cast<const nt_u2 *>(wp[n] + int64_t(b) * 2048 + 1024 * k);
 #pragma unroll
       for (int e = 0; e < GS; ++e) {
-        // (the last block may hold fewer groups than others)
         const int gr = group_at<GS>(a, b, e);
-        s[n][e] = sp[n][gr * 16];
-        z[n][e] = ZP ? 16.f + float(zp[n][gr * 16]) : 24.f;
+        s[n][e] = sp[n][gr * 32];
+        z[n][e] = ZP ? 16.f + float(zp[n][gr * 32]) : 24.f;
       }
     }
   };
@@ -291,7 +300,7 @@ __global__ __launch_bounds__(64 * WV) void i4_rows(I4Args a) {
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) wf[n][i] = widen(wq[n][i]);
+      for (int i = 0; i < 4; ++i) wf[n][i] = widen(wq[n][i >> 1][i & 1]);
 #pragma unroll
       for (int e = 0; e < GS; ++e) sc[n][e] = s[n][e], zc[n][e] = z[n][e];
     }
@@ -321,121 +330,118 @@ __global__ __launch_bounds__(64 * WV) void i4_rows(I4Args a) {
       }
     }
   }
-  join<MT, NB, WV, TY>(a, acc, part, t0, c0);
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    if (m) __syncthreads();
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) part[(w * 16 + 4 * g + r) * LD + 16 * n + c] = acc[m][n][r];
+    __syncthreads();
+    add_up<16, NB, LD, WV, TY>(a, part, t0 + 16 * m, c0);
+  }
 }
 
-// Where a channel tile's factors of a correction step are: lane l has group l /
-// 16 of the step's four, channel l % 16.
-template <int GS, bool ZP>
-struct Correct {
-  const float *sp;
-  const uint8_t *zp;
-  __device__ inline void init(const I4Args &a, int64_t ct, int c) {
-    sp = a.scale + ct * a.groups * 16 + c;
-    zp = ZP ? a.zero + ct * a.groups * 16 + c : nullptr;
-  }
-  struct Raw {
-    float s;
-    uint8_t z;
-  };
-  // (groups behind the last meet sums of zero)
-  __device__ inline Raw load(const I4Args &a, int step, int g) const {
-    const int gr = min(GS == 1 ? group_of(a, 4 * step + g) : 4 * step + g, a.groups - 1);
-    return {sp[gr * 16], ZP ? zp[gr * 16] : uint8_t(8)};
-  }
-  __device__ inline bf16x8_t operand(Raw r) const { return parts_w(-r.s * (16.f + float(r.z))); }
-};
+// The row of a 32 x 32 result that element e of a lane of half h holds.
+__device__ inline int row_of(int e, int h) { return 8 * (e / 4) + 4 * h + e % 4; }
 
-// More tokens, from staged activations: as i4_rows, but the corrections are
-// steps of their own, dealt out to the waves behind the blocks.
+// The position in a packed lane of columns 16 i ..
+__device__ inline constexpr int place(int i) { return (i & 1) << 1 | i >> 1; }
+
+// More tokens, from staged activations: 32 NB channels by 32 MT tokens, the
+// blocks dealt out to the waves as in i4_rows, then the corrections.
 template <int MT, int NB, int WV, int GS, bool ZP, typename TY>
 __global__ __launch_bounds__(64 * WV) void i4_blocks(I4Args a) {
   const Widen widen;
-  __shared__ float part[WV][NB][16 * kPartLd];
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-  const int c = lane & 15, g = lane >> 4;
-  const int c0 = blockIdx.x * 16 * NB, t0 = blockIdx.y * 16 * MT;
-  const int tiles = (a.N + 15) / 16, tt = (a.T + 15) / 16;
+  constexpr int LD = 32 * NB + 8;
+  __shared__ __align__(16) float part[WV * 32 * LD];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int c = lane & 31, h = lane >> 5;
+  const int c0 = blockIdx.x * 32 * NB, t0 = blockIdx.y * 32 * MT;
+  const int tiles = (a.N + 31) / 32, tt = (a.T + 31) / 32;
   const nt_u4 *xp[MT];
   const float *ep[MT];
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
-    const int64_t tile = min(t0 / 16 + m, tt - 1);
-    xp[m] = a.xb + tile * a.kb * 256 + lane;
-    ep[m] = a.xe + tile * a.steps * 64 + lane;
+    const int64_t tile = min(t0 / 32 + m, tt - 1);
+    xp[m] = a.xb + tile * a.kb * 512 + lane;
+    ep[m] = a.xe + tile * a.steps * 128 + lane;
   }
-  const uint8_t *wp[NB];
-  Correct<GS, ZP> co[NB];
+  const nt_u4 *wp[NB];
+  const float *sp[NB];
+  const uint8_t *zp[NB];
 #pragma unroll
   for (int n = 0; n < NB; ++n) {
+    // (channel tiles past the last: the last one again, not stored)
     const int64_t ct = min(blockIdx.x * NB + n, unsigned(tiles - 1));
-    wp[n] = a.w + ct * a.kb * 1024 + 16 * lane;
-    co[n].init(a, ct, c);
+    wp[n] = reinterpret_cast<const nt_u4 *>(a.w) + ct * a.kb * 128 + lane;
+    sp[n] = a.scale + ct * a.groups * 32 + c;
+    zp[n] = ZP ? a.zero + ct * a.groups * 32 + c : nullptr;
   }
-  f32x4_t acc[MT][NB];
+  f32x16_t acc[MT][NB];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int n = 0; n < NB; ++n) acc[m][n] = f32x4_t{0, 0, 0, 0};
-  nt_u4 wq[NB], xr[2][4];
+    for (int n = 0; n < NB; ++n) acc[m][n] = nothing();
+  nt_u4 wq[NB][2], xr[8];
   float s[NB][GS];
   auto load_w = [&](int b) {
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
-      wq[n] = *reinterpret_cast<const nt_u4 *>(wp[n] + int64_t(b) * 1024);
 #pragma unroll
-      for (int e = 0; e < GS; ++e)
-        s[n][e] = co[n].sp[(group_at<GS>(a, b, e)) * 16];
+      for (int k = 0; k < 2; ++k) wq[n][k] = wp[n][int64_t(b) * 128 + 64 * k];
+#pragma unroll
+      for (int e = 0; e < GS; ++e) s[n][e] = sp[n][group_at<GS>(a, b, e) * 32];
     }
   };
-  auto load_x = [&](int m, int b, nt_u4 (&x)[4]) {
+  auto load_x = [&](int m, int b) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = xp[m][int64_t(b) * 256 + 64 * i];
+    for (int i = 0; i < 8; ++i) xr[i] = xp[m][int64_t(b) * 512 + 64 * i];
   };
   if (w < a.kb) {
     load_w(w);
-    load_x(0, w, xr[0]);
-    if constexpr (MT > 1) load_x(1, w, xr[1]);
+    load_x(0, w);
   }
   for (int b = w; b < a.kb; b += WV) {
     const int next = min(b + WV, a.kb - 1);
-    bf16x8_t wf[NB][4];
+    bf16x8_t wf[NB][8];
     float sc[NB][GS];
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) wf[n][i] = widen(wq[n][i]);
+      for (int i = 0; i < 8; ++i) wf[n][i] = widen(wq[n][i / 4][place(i % 4)]);
 #pragma unroll
       for (int e = 0; e < GS; ++e) sc[n][e] = s[n][e];
     }
     load_w(next);
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      constexpr int AHEAD = MT > 1 ? 2 : 1;
-      nt_u4 xc[4];
+      nt_u4 xc[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) xc[i] = xr[m % AHEAD][i];
-      load_x((m + AHEAD) % MT, m + AHEAD < MT ? b : next, xr[m % AHEAD]);
+      for (int i = 0; i < 8; ++i) xc[i] = xr[i];
+      load_x(m + 1 < MT ? m + 1 : 0, m + 1 < MT ? b : next);
 #pragma unroll
       for (int e = 0; e < GS; ++e) {
-        f32x4_t p[NB];
+        f32x16_t p[NB];
 #pragma unroll
-        for (int n = 0; n < NB; ++n) p[n] = f32x4_t{0, 0, 0, 0};
+        for (int n = 0; n < NB; ++n) p[n] = nothing();
 #pragma unroll
-        for (int i = 4 / GS * e; i < 4 / GS * (e + 1); ++i)
+        for (int i = 8 / GS * e; i < 8 / GS * (e + 1); ++i)
 #pragma unroll
           for (int n = 0; n < NB; ++n) p[n] = mfma(as_bf16(xc[i]), wf[n][i], p[n]);
 #pragma unroll
         for (int n = 0; n < NB; ++n)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) acc[m][n][r] = fmaf(sc[n][e], p[n][r], acc[m][n][r]);
+          for (int r = 0; r < 16; ++r) acc[m][n][r] = fmaf(sc[n][e], p[n][r], acc[m][n][r]);
       }
     }
   }
-  for (int st = w; st < a.steps; st += WV) {
+  // (two groups a step: a half each; groups behind the last meet sums of zero)
+  for (int st = w; st < 2 * a.steps; st += WV) {
+    const int gr = min(GS == 1 ? group_of(a, 2 * st + h) : 2 * st + h, a.groups - 1);
     bf16x8_t f[NB];
 #pragma unroll
-    for (int n = 0; n < NB; ++n) f[n] = co[n].operand(co[n].load(a, st, g));
+    for (int n = 0; n < NB; ++n) f[n] = parts_w(-sp[n][gr * 32] * (ZP ? 16.f + float(zp[n][gr * 32]) : 24.f));
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       const bf16x8_t x = parts_x(ep[m][int64_t(st) * 64]);
@@ -443,7 +449,16 @@ __global__ __launch_bounds__(64 * WV) void i4_blocks(I4Args a) {
       for (int n = 0; n < NB; ++n) acc[m][n] = mfma(x, f[n], acc[m][n]);
     }
   }
-  join<MT, NB, WV, TY>(a, acc, part, t0, c0);
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    if (m) __syncthreads();
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) part[(w * 32 + row_of(r, h)) * LD + 32 * n + c] = acc[m][n][r];
+    __syncthreads();
+    add_up<32, 2 * NB, LD, WV, TY>(a, part, t0 + 32 * m, c0);
+  }
 }
 
 // Loads straight into LDS: 64 lanes write 16 (or 4) bytes each, in a row from
@@ -482,17 +497,16 @@ __device__ inline void move4(uint32_t to, const void *from, uint32_t off) {
 template <int BT, int WC, int GS, bool ZP, typename TY>
 __global__ __launch_bounds__(512, 2) void i4_tile(I4Args a) {
   const Widen widen;
-  constexpr int BC = 256, WV = 8, WT = WV / WC, NB = BC / WC / 16, MT = BT / WT / 16, PER = 4 / GS;
-  constexpr int NX = BT / 16 * 4 / WV;  // KiB of activations a wave moves a block
-  constexpr int NS = BT / 16 > WV ? BT / 16 / WV : 1;
+  constexpr int BC = 256, WV = 8, WT = WV / WC, NB = BC / WC / 32, MT = BT / WT / 32, PER = 4 / GS;
+  constexpr int NX = BT / 32;  // KiB of activations a wave moves a block
   __shared__ struct {
-    nt_u4 x[3][BT / 16 * 256];
-    nt_u4 w[3][BC / 16 * 64];
-    float sum[2][BT / 16 * 64];   // of four groups
-    float s[2][BC / 16 * 64];
-    uint8_t z[2][BC / 16 * 64];
+    nt_u4 x[3][BT / 32 * 512];
+    nt_u4 w[3][BC / 32 * 128];
+    float sum[2][BT / 32 * 128];  // of four groups
+    float s[2][BC / 32 * 128];
+    uint8_t z[2][BC / 32 * 128];
   } l;
-  const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, g = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, c = lane & 31, h = lane >> 5;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   // workgroups go to the eight XCDs in turn: each gets a run of tiles, token
   // tiles next to each other, so that its L2 holds their weights
@@ -501,44 +515,38 @@ __global__ __launch_bounds__(512, 2) void i4_tile(I4Args a) {
   if (int(blockIdx.x >> 3) >= per || id >= n_all) return;
   const int c0 = id / a.nt * BC, t0 = id % a.nt * BT;
   const int wc = (w % WC) * NB, wt = (w / WC) * MT;  // the wave's first tiles
-  const int tiles = (a.N + 15) / 16, tt = (a.T + 15) / 16;
+  const int tiles = (a.N + 31) / 32, tt = (a.T + 31) / 32;
   // (tiles past the last: the last again, not stored)
-  auto c_tile = [&](int i) { return int64_t(min(c0 / 16 + i, tiles - 1)); };
-  auto t_tile = [&](int i) { return int64_t(min(t0 / 16 + i, tt - 1)); };
+  auto c_tile = [&](int i) { return int64_t(min(c0 / 32 + i, tiles - 1)); };
+  auto t_tile = [&](int i) { return int64_t(min(t0 / 32 + i, tt - 1)); };
   auto stage = [&](int b, int slot) {
     move16<NX>(lds_at(&l.x[slot][w * NX * 64]),
-               a.xb + (t_tile(w * NX / 4) * a.kb + b) * 256 + w * NX % 4 * 64, 16 * lane);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      move16<1>(lds_at(&l.w[slot][(2 * w + i) * 64]), a.w + (c_tile(2 * w + i) * a.kb + b) * 1024, 16 * lane);
+               a.xb + (t_tile(w * NX / 8) * a.kb + b) * 512 + w * NX % 8 * 64, 16 * lane);
+    move16<2>(lds_at(&l.w[slot][w * 128]), a.w + (c_tile(w) * a.kb + b) * 2048, 16 * lane);
   };
   // A step's groups; lanes of groups behind the last take the last one's
   // factors, their sums are zero.
+  auto group = [&](int st, int i) { return min(GS == 1 ? group_of(a, 4 * st + i) : 4 * st + i, a.groups - 1); };
   auto stage_step = [&](int st) {
-    const int sl = st & 1;
-#pragma unroll
-    for (int i = 0; i < NS; ++i) {
-      const int t = (w * NS + i) % (BT / 16);
-      move4(lds_at(&l.sum[sl][t * 64]), a.xe + (t_tile(t) * a.steps + st) * 64, 4 * lane);
-    }
-    const int gr = min(GS == 1 ? group_of(a, 4 * st + g) : 4 * st + g, a.groups - 1);
+    const int sl = st & 1, p = w % (BT / 16);  // 64 sums a wave
+    move4(lds_at(&l.sum[sl][p * 64]), a.xe + (t_tile(p / 2) * a.steps + st) * 128 + p % 2 * 64, 4 * lane);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      move4(lds_at(&l.s[sl][(2 * w + i) * 64]), a.scale + c_tile(2 * w + i) * a.groups * 16,
-            4 * (gr * 16 + c));
+      move4(lds_at(&l.s[sl][w * 128 + 64 * i]), a.scale + c_tile(w) * a.groups * 32,
+            4 * (group(st, 2 * i + h) * 32 + c));
     if constexpr (ZP) {
-      // four channel tiles an instruction, four channels a lane
-      const int i = w % 4, gz = min(GS == 1 ? group_of(a, 4 * st + (lane >> 2 & 3)) : 4 * st + (lane >> 2 & 3),
-                                    a.groups - 1);
-      move4(lds_at(&l.z[sl][4 * i * 64]), a.zero + c_tile(4 * i) * a.groups * 16,
-            uint32_t((c_tile(4 * i + g) - c_tile(4 * i)) * a.groups * 16 + gz * 16 + 4 * (lane & 3)));
+      // two channel tiles an instruction, four channels a lane
+      const int i = w % 4 * 2;
+      move4(lds_at(&l.z[sl][i * 128]), a.zero + c_tile(i) * a.groups * 32,
+            uint32_t((c_tile(i + h) - c_tile(i)) * a.groups * 32 + group(st, lane >> 3 & 3) * 32 +
+                     4 * (lane & 7)));
     }
   };
-  f32x4_t acc[MT][NB];
+  f32x16_t acc[MT][NB];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int n = 0; n < NB; ++n) acc[m][n] = f32x4_t{0, 0, 0, 0};
+    for (int n = 0; n < NB; ++n) acc[m][n] = nothing();
   stage_step(0);
   stage(0, 0);
   stage(min(1, a.kb - 1), 1);
@@ -553,73 +561,79 @@ __global__ __launch_bounds__(512, 2) void i4_tile(I4Args a) {
     if ((b + 1) % PER == 0) stage_step(min((b + 1) / PER, a.steps - 1));
     stage(min(b + 2, a.kb - 1), slot == 0 ? 2 : slot - 1);
     const int sl = b / PER & 1;
-    bf16x8_t wf[NB][4];
+    bf16x8_t wf[NB][8];
     float sc[NB][GS];
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
-      const nt_u4 q = l.w[slot][(wc + n) * 64 + lane];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) wf[n][i] = widen(q[i]);
+      for (int k = 0; k < 2; ++k) {
+        const nt_u4 q = l.w[slot][(wc + n) * 128 + 64 * k + lane];
 #pragma unroll
-      for (int e = 0; e < GS; ++e) sc[n][e] = l.s[sl][(wc + n) * 64 + (b % PER * GS + e) * 16 + c];
+        for (int i = 0; i < 4; ++i) wf[n][4 * k + i] = widen(q[place(i)]);
+      }
+#pragma unroll
+      for (int e = 0; e < GS; ++e) sc[n][e] = l.s[sl][(wc + n) * 128 + (b % PER * GS + e) * 32 + c];
     }
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      nt_u4 xc[4];
+      nt_u4 xc[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) xc[i] = l.x[slot][(wt + m) * 256 + 64 * i + lane];
+      for (int i = 0; i < 8; ++i) xc[i] = l.x[slot][(wt + m) * 512 + 64 * i + lane];
 #pragma unroll
       for (int e = 0; e < GS; ++e) {
-        f32x4_t p[NB];
+        f32x16_t p[NB];
 #pragma unroll
-        for (int n = 0; n < NB; ++n) p[n] = f32x4_t{0, 0, 0, 0};
+        for (int n = 0; n < NB; ++n) p[n] = nothing();
 #pragma unroll
-        for (int i = 4 / GS * e; i < 4 / GS * (e + 1); ++i)
+        for (int i = 8 / GS * e; i < 8 / GS * (e + 1); ++i)
 #pragma unroll
           for (int n = 0; n < NB; ++n) p[n] = mfma(as_bf16(xc[i]), wf[n][i], p[n]);
 #pragma unroll
         for (int n = 0; n < NB; ++n)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) acc[m][n][r] = fmaf(sc[n][e], p[n][r], acc[m][n][r]);
+          for (int r = 0; r < 16; ++r) acc[m][n][r] = fmaf(sc[n][e], p[n][r], acc[m][n][r]);
       }
     }
     // corrections every four groups, so that sums stay small
     if (b % PER == PER - 1 || b == a.kb - 1) {
-      bf16x8_t f[NB];
 #pragma unroll
-      for (int n = 0; n < NB; ++n) {
-        const int at = (wc + n) * 64 + lane;
-        f[n] = parts_w(-l.s[sl][at] * (ZP ? 16.f + float(l.z[sl][at]) : 24.f));
-      }
+      for (int k = 0; k < 2; ++k) {
+        bf16x8_t f[NB];
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const bf16x8_t x = parts_x(l.sum[sl][(wt + m) * 64 + lane]);
+        for (int n = 0; n < NB; ++n) {
+          const int at = (wc + n) * 128 + 64 * k + lane;
+          f[n] = parts_w(-l.s[sl][at] * (ZP ? 16.f + float(l.z[sl][at]) : 24.f));
+        }
 #pragma unroll
-        for (int n = 0; n < NB; ++n) acc[m][n] = mfma(x, f[n], acc[m][n]);
+        for (int m = 0; m < MT; ++m) {
+          const bf16x8_t x = parts_x(l.sum[sl][(wt + m) * 128 + 64 * k + lane]);
+#pragma unroll
+          for (int n = 0; n < NB; ++n) acc[m][n] = mfma(x, f[n], acc[m][n]);
+        }
       }
     }
     slot = slot == 2 ? 0 : slot + 1;
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
-  // Results through LDS, a wave's 16 tokens at a time, so that a store covers
+  // Results through LDS, a wave's 32 tokens at a time, so that a store covers
   // whole lines of y.
-  constexpr int LD = 16 * NB + 4;
-  static_assert(WV * 16 * LD * 4 <= int(sizeof(l)), "LDS of the results");
-  float *out = reinterpret_cast<float *>(&l) + w * 16 * LD;
+  constexpr int LD = 32 * NB + 8;
+  static_assert(WV * 32 * LD * 4 <= int(sizeof(l)), "LDS of the results");
+  float *out = reinterpret_cast<float *>(&l) + w * 32 * LD;
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
 #pragma unroll
     for (int n = 0; n < NB; ++n)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) out[(4 * g + r) * LD + 16 * n + c] = acc[m][n][r];
+      for (int r = 0; r < 16; ++r) out[row_of(r, h) * LD + 32 * n + c] = acc[m][n][r];
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
 #pragma unroll
-    for (int k = 0; k < NB; ++k) {
-      const int o = k * 64 + lane, x = o / (4 * NB), t = t0 + 16 * (wt + m) + x, ch = o % (4 * NB) * 4;
-      if (t < a.T && c0 + 16 * wc + ch < a.N)
-        store4<TY>(a, t, c0 + 16 * wc + ch, *reinterpret_cast<const nt_f4 *>(out + x * LD + ch));
+    for (int k = 0; k < 4 * NB; ++k) {
+      const int o = k * 64 + lane, x = o / (8 * NB), t = t0 + 32 * (wt + m) + x;
+      const int ch = o % (8 * NB) * 4, at = c0 + 32 * wc + ch;
+      if (t < a.T && at < a.N) store4<TY>(a, t, at, *reinterpret_cast<const nt_f4 *>(out + x * LD + ch));
     }
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
@@ -656,12 +670,12 @@ int check_weight(const tcl_i4_weight *w, Layout *l) {
   if (w->zeros != 0 && w->zeros != 1) return fail(TCL_EINVAL, "i4: zeros %d is not 0 or 1", w->zeros);
   if (misaligned(w->W, 16) || misaligned(w->scale, 4) || misaligned(w->W_p, 256))
     return fail(TCL_EALIGN, "i4: W must be 16-byte, scale 4-byte, W_p 256-byte aligned");
-  l->tiles = (int64_t(w->d_out) + 15) / 16;
+  l->tiles = (int64_t(w->d_out) + 31) / 32;
   l->kb = (w->d_in + 127) / 128;
   l->groups = w->d_in / w->group;
-  l->w = size_t(l->tiles) * l->kb * 1024;
-  l->scale = l->w + size_t(l->tiles) * l->groups * 64;
-  l->total = (l->scale + (w->zeros ? size_t(l->tiles) * l->groups * 16 : 0) + 255) / 256 * 256;
+  l->w = size_t(l->tiles) * l->kb * 2048;
+  l->scale = l->w + size_t(l->tiles) * l->groups * 128;
+  l->total = (l->scale + (w->zeros ? size_t(l->tiles) * l->groups * 32 : 0) + 255) / 256 * 256;
   if (l->total >= size_t(1) << 36) return fail(TCL_EUNSUPPORTED, "i4: a packed copy of 2^36 bytes or more");
   return TCL_OK;
 }
@@ -676,7 +690,7 @@ void go_rows(const I4Args &a, hipStream_t s) {
 template <int MT, int NB, int WV, int GS, bool ZP, typename TY>
 void go_blocks(const I4Args &a, hipStream_t s) {
   hipLaunchKernelGGL((i4_blocks<MT, NB, WV, GS, ZP, TY>),
-                     dim3((a.N + 16 * NB - 1) / (16 * NB), (a.T + 16 * MT - 1) / (16 * MT)), dim3(64 * WV), 0,
+                     dim3((a.N + 32 * NB - 1) / (32 * NB), (a.T + 32 * MT - 1) / (32 * MT)), dim3(64 * WV), 0,
                      s, a);
 }
 
@@ -687,19 +701,23 @@ void go_tile(I4Args a, hipStream_t s) {
   hipLaunchKernelGGL((i4_tile<BT, WC, GS, ZP, TY>), dim3((a.nt * a.nc + 7) / 8 * 8), dim3(512), 0, s, a);
 }
 
+template <int GS>
+void go_stage(const I4Args &a, hipStream_t s) {
+  const StageArgs g{a.x, const_cast<nt_u4 *>(a.xb), const_cast<float *>(a.xe), a.ldx, a.T, a.K, a.kb, a.steps};
+  hipLaunchKernelGGL(i4_stage_kernel<GS>, dim3((a.T + 31) / 32, (a.steps * (4 / GS) + 3) / 4), dim3(256), 0, s,
+                     g);
+}
+
 template <int GS, bool ZP, typename TY>
 void product(const I4Args &a, hipStream_t s) {
   if (a.T <= kRows)
     go_rows<1, 1, 8, GS, ZP, TY>(a, s);
   else {
-    const StageArgs g{a.x, const_cast<nt_u4 *>(a.xb), const_cast<float *>(a.xe), a.ldx, a.T, a.K, a.kb,
-                      a.steps};
-    hipLaunchKernelGGL(i4_stage_kernel<GS>, dim3((a.T + 15) / 16, (a.steps * (4 / GS) + 3) / 4), dim3(256), 0,
-                       s, g);
+    go_stage<GS>(a, s);
     if (a.T <= 32)
-      go_blocks<2, 1, 8, GS, ZP, TY>(a, s);
+      go_blocks<1, 1, 8, GS, ZP, TY>(a, s);
     else if (a.T <= 64)
-      go_blocks<4, 4, 8, GS, ZP, TY>(a, s);
+      go_blocks<2, 2, 8, GS, ZP, TY>(a, s);
     else
       go_tile<128, 4, GS, ZP, TY>(a, s);
   }
@@ -767,11 +785,11 @@ struct Space {
 };
 Space space(const tcl_i4_weight *w, const Layout &l, int32_t n_tokens) {
   if (n_tokens <= kRows || w->d_out == 0) return {0, 0, 0};
-  const size_t tiles = (size_t(n_tokens) + 15) / 16;
+  const size_t tiles = (size_t(n_tokens) + 31) / 32;
   const int32_t groups = w->group < 128 ? l.groups : l.kb;  // longer ones count by their blocks
   const int32_t steps = (groups + 3) / 4;
-  const size_t x = tiles * l.kb * 4096;
-  return {x, x + tiles * steps * 256, steps};
+  const size_t x = tiles * l.kb * 8192;
+  return {x, x + tiles * steps * 512, steps};
 }
 
 int check_tokens(const tcl_i4_weight *w, int32_t n_tokens) {

@@ -666,8 +666,8 @@ def test_i4_host_errors(L):
     def lin(x=P, ldx=128, T=4, y=P, ldy=32, yd=1, ws=P, n=1 << 40, **kw):
         return L.tcl_i4_linear(w(**kw), x, ldx, T, y, ldy, yd, ws, n, None)
 
-    assert nbytes() == 0 and out.value == 2 * 1024 + 2 * 4 * 64 + 256
-    assert nbytes(zeros=0, d_in=256, group=256) == 0 and out.value == 2 * 2 * 1024 + 256
+    assert nbytes() == 0 and out.value == 2048 + 4 * 128 + 256  # (zero points: 128)
+    assert nbytes(zeros=0, d_in=256, group=256) == 0 and out.value == 2 * 2048 + 256  # (scales: 128)
     assert L.tcl_i4_pack_bytes(w(), None) == E
     for f in (nbytes, pack, lin):
         assert [f(d_in=0), f(d_out=-8), f(d_in=96, group=64), f(zeros=2), f(zeros=-1)] == [E] * 5
@@ -685,7 +685,7 @@ def test_i4_host_errors(L):
     assert lin(T=0) == 0 and lin(d_out=0, x=None) == 0
     assert lin(T=0, W=None, scale=None, zero=None) == 0
     assert [L.tcl_i4_workspace_bytes(w(), T, ctypes.byref(out)) for T in (16, 17)] == [0, 0]
-    assert out.value == 2 * 4096 + 2 * 256  # (one block and one step of four groups, two tiles)
+    assert out.value == 8192 + 512  # (32 tokens: one block and one step of four groups)
     assert [lin(T=17, ws=None), lin(T=17, ws=P + 16), lin(T=17, n=out.value - 1)] == [E, A, tclora.ENOSPC]
     assert L.tcl_i4_workspace_bytes(w(), 4, ctypes.byref(out)) == 0 and out.value == 0
     assert L.tcl_i4_workspace_bytes(w(), -1, ctypes.byref(out)) == E

@@ -145,27 +145,29 @@ def test_packed_copy_holds_the_weight():
     for d_out, d_in, group, zeros in ((40, 352, 32, True), (16, 128, 128, False), (8, 64, 64, True)):
         w, n = weight(6, d_out, d_in, group, zeros)
         p = tclora.I4Weight(*w).W_p.cpu().numpy()
-        ct, kb, G = -(-d_out // 16), -(-d_in // 128), d_in // group
+        ct, kb, G = -(-d_out // 32), 2 * -(-d_in // 128), d_in // group
         want = np.zeros((ct, kb, 64, 4), np.uint32)
-        full = np.zeros((ct * 16, kb * 128), np.uint32)
+        full = np.zeros((ct * 32, kb * 64), np.uint32)
         full[:d_out, :d_in] = n.numpy()
         for lane in range(64):
-            for i in range(4):
-                k = 32 * i + 8 * (lane // 16) + np.arange(kb) * 128
-                rows = full[np.arange(ct) * 16 + lane % 16]
+            for i, eight in enumerate((0, 4, 2, 6)):
+                k = 8 * (eight + lane // 32) + np.arange(kb) * 64
+                rows = full[np.arange(ct) * 32 + lane % 32]
+                u = np.zeros((ct, kb), np.uint64)
                 for j in range(8):
-                    want[:, :, lane, i] |= rows[:, k + j] << (4 * (j // 2) + 16 * (j % 2))
+                    u |= rows[:, k + j].astype(np.uint64) << np.uint64(3 + 4 * (j // 2) + 16 * (j % 2))
+                want[:, :, lane, i] = (u | u >> np.uint64(32)).astype(np.uint32)
         nw = ct * kb * 1024
         assert np.array_equal(p[:nw].view(np.uint32).reshape(want.shape), want)
-        s = np.zeros((ct * 16, G), np.float32)
+        s = np.zeros((ct * 32, G), np.float32)
         s[:d_out] = w[1].cpu().numpy()
-        got = p[nw:nw + ct * G * 64].view(np.float32).reshape(ct, G, 16)
-        assert np.array_equal(got, s.reshape(ct, 16, G).transpose(0, 2, 1))
+        got = p[nw:nw + ct * G * 128].view(np.float32).reshape(ct, G, 32)
+        assert np.array_equal(got, s.reshape(ct, 32, G).transpose(0, 2, 1))
         if zeros:
-            z = np.full((ct * 16, G), 8, np.uint8)
+            z = np.full((ct * 32, G), 8, np.uint8)
             z[:d_out] = w[2].cpu().numpy()
-            got = p[nw + ct * G * 64:nw + ct * G * 80].reshape(ct, G, 16)
-            assert np.array_equal(got, z.reshape(ct, 16, G).transpose(0, 2, 1))
+            got = p[nw + ct * G * 128:nw + ct * G * 160].reshape(ct, G, 32)
+            assert np.array_equal(got, z.reshape(ct, 32, G).transpose(0, 2, 1))
 
 
 def test_empty_batch_and_empty_weight():
