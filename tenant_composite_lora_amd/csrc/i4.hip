@@ -42,6 +42,8 @@ struct I4Args {
   const float *xe;        // and their groups' sums
   int32_t steps;          // corrections of four groups
   int32_t nt, nc;         // tiles of tokens, of channels
+  int32_t ks;             // workgroups that share a tile's columns (i4_blocks)
+  float *part;            // [ks][T][N], where ks > 1
 };
 
 // ---------------------------------------------------------------------------
@@ -213,10 +215,10 @@ __device__ inline void store4(const I4Args &a, int t, int ch, nt_f4 v) {
   }
 }
 
-// The waves' sums of a tile of R tokens by 16 CH channels, added in order, and
-// stored: part[wave][token][LD].
-template <int R, int CH, int LD, int WV, typename TY>
-__device__ inline void add_up(const I4Args &a, const float *part, int t0, int c0) {
+// The waves' sums of a tile of R tokens by 16 CH channels, added in order:
+// put(token, channel, four channels) of each; part[wave][token][LD].
+template <int R, int CH, int LD, int WV, typename F>
+__device__ inline void add_up(const I4Args &a, const float *part, int t0, int c0, F put) {
   for (int o = threadIdx.x; o < R * CH * 4; o += 64 * WV) {
     const int r = o / (4 * CH), t = t0 + r, ch = c0 + o % (4 * CH) * 4;
     if (t >= a.T || ch >= a.N) continue;
@@ -224,7 +226,7 @@ __device__ inline void add_up(const I4Args &a, const float *part, int t0, int c0
     nt_f4 v = *reinterpret_cast<const nt_f4 *>(in);
 #pragma unroll
     for (int i = 1; i < WV; ++i) v += *reinterpret_cast<const nt_f4 *>(in + i * R * LD);
-    store4<TY>(a, t, ch, v);
+    put(t, ch, v);
   }
 }
 
@@ -262,55 +264,39 @@ __global__ __launch_bounds__(64 * WV) void i4_rows(I4Args a) {
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int n = 0; n < NB; ++n) acc[m][n] = f32x4_t{0, 0, 0, 0};
+  // (operands are replaced by the wave's next block's, as in i4_blocks)
   nt_u2 wq[NB][2];
   nt_u4 xr[MT][4];
   float s[NB][GS], z[NB][GS];
-  auto load_w = [&](int b) {
+  auto load_w = [&](int n, int k, int b) {
+    wq[n][k] = *reinterpret_cast<const nt_u2 *>(wp[n] + int64_t(b) * 2048 + 1024 * k);
+  };
+  auto load_s = [&](int n, int b) {
 #pragma unroll
-    for (int n = 0; n < NB; ++n) {
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-        wq[n][k] = *reinterpret_cast<const nt_u2 *>(wp[n] + int64_t(b) * 2048 + 1024 * k);
-#pragma unroll
-      for (int e = 0; e < GS; ++e) {
-        const int gr = group_at<GS>(a, b, e);
-        s[n][e] = sp[n][gr * 32];
-        z[n][e] = ZP ? 16.f + float(zp[n][gr * 32]) : 24.f;
-      }
+    for (int e = 0; e < GS; ++e) {
+      const int gr = group_at<GS>(a, b, e);
+      s[n][e] = sp[n][gr * 32];
+      z[n][e] = ZP ? 16.f + float(zp[n][gr * 32]) : 24.f;
     }
   };
-  auto load_x = [&](int m, int b) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      // columns past the row's end: zeros
-      const bool in = b * 128 + 32 * i < a.K;
-      const nt_u4 u = *reinterpret_cast<const nt_u4 *>(xp[m] + (in ? b * 128 + 32 * i : 0));
-      xr[m][i] = in ? u : nt_u4{0, 0, 0, 0};
-    }
+  auto load_x = [&](int m, int i, int b) {
+    // columns past the row's end: zeros
+    const bool in = b * 128 + 32 * i < a.K;
+    const nt_u4 u = *reinterpret_cast<const nt_u4 *>(xp[m] + (in ? b * 128 + 32 * i : 0));
+    xr[m][i] = in ? u : nt_u4{0, 0, 0, 0};
   };
   if (w < a.kb) {
-    load_w(w);
 #pragma unroll
-    for (int m = 0; m < MT; ++m) load_x(m, w);
+    for (int n = 0; n < NB; ++n) load_w(n, 0, w), load_w(n, 1, w), load_s(n, w);
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) load_x(m, i, w);
   }
   for (int b = w; b < a.kb; b += WV) {
     const int next = min(b + WV, a.kb - 1);
-    bf16x8_t wf[NB][4];
-    float sc[NB][GS], zc[NB][GS];
 #pragma unroll
-    for (int n = 0; n < NB; ++n) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) wf[n][i] = widen(wq[n][i >> 1][i & 1]);
-#pragma unroll
-      for (int e = 0; e < GS; ++e) sc[n][e] = s[n][e], zc[n][e] = z[n][e];
-    }
-    load_w(next);
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      nt_u4 xc[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) xc[i] = xr[m][i];
-      load_x(m, next);
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int e = 0; e < GS; ++e) {
         f32x4_t sum = {0, 0, 0, 0}, p[NB];
@@ -318,17 +304,23 @@ __global__ __launch_bounds__(64 * WV) void i4_rows(I4Args a) {
         for (int n = 0; n < NB; ++n) p[n] = f32x4_t{0, 0, 0, 0};
 #pragma unroll
         for (int i = 4 / GS * e; i < 4 / GS * (e + 1); ++i) {
-          sum = mfma(as_bf16(xc[i]), ones(), sum);
+          sum = mfma(as_bf16(xr[m][i]), ones(), sum);
 #pragma unroll
-          for (int n = 0; n < NB; ++n) p[n] = mfma(as_bf16(xc[i]), wf[n][i], p[n]);
+          for (int n = 0; n < NB; ++n) p[n] = mfma(as_bf16(xr[m][i]), widen(wq[n][i >> 1][i & 1]), p[n]);
+          load_x(m, i, next);
+          if (m == MT - 1 && i % 2 == 1)
+#pragma unroll
+            for (int n = 0; n < NB; ++n) load_w(n, i / 2, next);
+          __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
         for (int n = 0; n < NB; ++n)
 #pragma unroll
           for (int r = 0; r < 4; ++r)
-            acc[m][n][r] = fmaf(sc[n][e], fmaf(-zc[n][e], sum[r], p[n][r]), acc[m][n][r]);
+            acc[m][n][r] = fmaf(s[n][e], fmaf(-z[n][e], sum[r], p[n][r]), acc[m][n][r]);
       }
-    }
+#pragma unroll
+    for (int n = 0; n < NB; ++n) load_s(n, next);
   }
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
@@ -338,7 +330,7 @@ __global__ __launch_bounds__(64 * WV) void i4_rows(I4Args a) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) part[(w * 16 + 4 * g + r) * LD + 16 * n + c] = acc[m][n][r];
     __syncthreads();
-    add_up<16, NB, LD, WV, TY>(a, part, t0 + 16 * m, c0);
+    add_up<16, NB, LD, WV>(a, part, t0 + 16 * m, c0, [&](int t, int ch, nt_f4 v) { store4<TY>(a, t, ch, v); });
   }
 }
 
@@ -358,6 +350,7 @@ __global__ __launch_bounds__(64 * WV) void i4_blocks(I4Args a) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int c = lane & 31, h = lane >> 5;
   const int c0 = blockIdx.x * 32 * NB, t0 = blockIdx.y * 32 * MT;
+  const int first = blockIdx.z * WV + w, stride = a.ks * WV;
   const int tiles = (a.N + 31) / 32, tt = (a.T + 31) / 32;
   const nt_u4 *xp[MT];
   const float *ep[MT];
@@ -383,61 +376,56 @@ __global__ __launch_bounds__(64 * WV) void i4_blocks(I4Args a) {
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int n = 0; n < NB; ++n) acc[m][n] = nothing();
-  nt_u4 wq[NB][2], xr[8];
+  // A block's operands, each replaced by the wave's next block's as soon as its
+  // products have been issued: a block is always on its way, and no register
+  // waits for it twice.  (The scheduling barriers hold the loads there; left to
+  // itself the compiler puts them right before their use.)
+  nt_u4 wq[NB][2], xr[MT][8];
   float s[NB][GS];
-  auto load_w = [&](int b) {
+  auto load_w = [&](int n, int k, int b) { wq[n][k] = wp[n][int64_t(b) * 128 + 64 * k]; };
+  auto load_s = [&](int n, int b) {
 #pragma unroll
-    for (int n = 0; n < NB; ++n) {
-#pragma unroll
-      for (int k = 0; k < 2; ++k) wq[n][k] = wp[n][int64_t(b) * 128 + 64 * k];
-#pragma unroll
-      for (int e = 0; e < GS; ++e) s[n][e] = sp[n][group_at<GS>(a, b, e) * 32];
-    }
+    for (int e = 0; e < GS; ++e) s[n][e] = sp[n][group_at<GS>(a, b, e) * 32];
   };
-  auto load_x = [&](int m, int b) {
+  auto load_x = [&](int m, int i, int b) { xr[m][i] = xp[m][int64_t(b) * 512 + 64 * i]; };
+  if (first < a.kb) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) xr[i] = xp[m][int64_t(b) * 512 + 64 * i];
-  };
-  if (w < a.kb) {
-    load_w(w);
-    load_x(0, w);
+    for (int n = 0; n < NB; ++n) load_w(n, 0, first), load_w(n, 1, first), load_s(n, first);
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) load_x(m, i, first);
   }
-  for (int b = w; b < a.kb; b += WV) {
-    const int next = min(b + WV, a.kb - 1);
-    bf16x8_t wf[NB][8];
-    float sc[NB][GS];
+  for (int b = first; b < a.kb; b += stride) {
+    const int next = min(b + stride, a.kb - 1);
 #pragma unroll
-    for (int n = 0; n < NB; ++n) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) wf[n][i] = widen(wq[n][i / 4][place(i % 4)]);
-#pragma unroll
-      for (int e = 0; e < GS; ++e) sc[n][e] = s[n][e];
-    }
-    load_w(next);
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      nt_u4 xc[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) xc[i] = xr[i];
-      load_x(m + 1 < MT ? m + 1 : 0, m + 1 < MT ? b : next);
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int e = 0; e < GS; ++e) {
         f32x16_t p[NB];
 #pragma unroll
         for (int n = 0; n < NB; ++n) p[n] = nothing();
 #pragma unroll
-        for (int i = 8 / GS * e; i < 8 / GS * (e + 1); ++i)
+        for (int i = 8 / GS * e; i < 8 / GS * (e + 1); ++i) {
 #pragma unroll
-          for (int n = 0; n < NB; ++n) p[n] = mfma(as_bf16(xc[i]), wf[n][i], p[n]);
+          for (int n = 0; n < NB; ++n)
+            p[n] = mfma(as_bf16(xr[m][i]), widen(wq[n][i / 4][place(i % 4)]), p[n]);
+          load_x(m, i, next);
+          if (m == MT - 1 && i % 4 == 3)
+#pragma unroll
+            for (int n = 0; n < NB; ++n) load_w(n, i / 4, next);
+          __builtin_amdgcn_sched_barrier(0);
+        }
 #pragma unroll
         for (int n = 0; n < NB; ++n)
 #pragma unroll
-          for (int r = 0; r < 16; ++r) acc[m][n][r] = fmaf(sc[n][e], p[n][r], acc[m][n][r]);
+          for (int r = 0; r < 16; ++r) acc[m][n][r] = fmaf(s[n][e], p[n][r], acc[m][n][r]);
       }
-    }
+#pragma unroll
+    for (int n = 0; n < NB; ++n) load_s(n, next);
   }
   // (two groups a step: a half each; groups behind the last meet sums of zero)
-  for (int st = w; st < 2 * a.steps; st += WV) {
+  for (int st = first; st < 2 * a.steps; st += stride) {
     const int gr = min(GS == 1 ? group_of(a, 2 * st + h) : 2 * st + h, a.groups - 1);
     bf16x8_t f[NB];
 #pragma unroll
@@ -457,7 +445,25 @@ __global__ __launch_bounds__(64 * WV) void i4_blocks(I4Args a) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) part[(w * 32 + row_of(r, h)) * LD + 32 * n + c] = acc[m][n][r];
     __syncthreads();
-    add_up<32, 2 * NB, LD, WV, TY>(a, part, t0 + 32 * m, c0);
+    add_up<32, 2 * NB, LD, WV>(a, part, t0 + 32 * m, c0, [&](int t, int ch, nt_f4 v) {
+      if (a.ks == 1)
+        store4<TY>(a, t, ch, v);
+      else
+        *reinterpret_cast<nt_f4 *>(a.part + ((int64_t(blockIdx.z) * a.T + t) * a.N + ch)) = v;
+    });
+  }
+}
+
+// Adds the parts of the workgroups that shared columns, in order.
+template <typename TY>
+__global__ __launch_bounds__(256) void i4_join_kernel(I4Args a) {
+  const int64_t n4 = a.N / 4, all = a.T * n4;
+  for (int64_t o = int64_t(blockIdx.x) * 256 + threadIdx.x; o < all; o += int64_t(gridDim.x) * 256) {
+    const nt_f4 *in = reinterpret_cast<const nt_f4 *>(a.part) + o;
+    nt_f4 v = in[0];
+#pragma unroll 4
+    for (int z = 1; z < a.ks; ++z) v += in[z * all];
+    store4<TY>(a, int(o / n4), int(o % n4) * 4, v);
   }
 }
 
@@ -561,39 +567,62 @@ __global__ __launch_bounds__(512, 2) void i4_tile(I4Args a) {
     if ((b + 1) % PER == 0) stage_step(min((b + 1) / PER, a.steps - 1));
     stage(min(b + 2, a.kb - 1), slot == 0 ? 2 : slot - 1);
     const int sl = b / PER & 1;
-    bf16x8_t wf[NB][8];
+    // Sixteen columns at a time; the next ones are read and widened between
+    // the matrix instructions of these.
+    nt_u4 q[NB][2], xf[2][MT];
+    bf16x8_t wf[2][NB];
     float sc[NB][GS];
+    f32x16_t p[MT][NB];
+    auto read = [&](int i) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m) xf[i & 1][m] = l.x[slot][(wt + m) * 512 + 64 * i + lane];
+    };
+    auto widen_all = [&](int i) {
+#pragma unroll
+      for (int n = 0; n < NB; ++n) wf[i & 1][n] = widen(q[n][i / 4][place(i % 4)]);
+    };
+    auto multiply = [&](int i) {
+      constexpr int LEN = 8 / GS;  // steps of sixteen of a group
+      if (i % LEN == 0)
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int n = 0; n < NB; ++n) p[m][n] = nothing();
+      if (i < 7) {
+        read(i + 1);
+        widen_all(i + 1);
+      }
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) p[m][n] = mfma(as_bf16(xf[i & 1][m]), wf[i & 1][n], p[m][n]);
+      __builtin_amdgcn_sched_group_barrier(0x100, MT, 0);  // LDS reads
+#pragma unroll
+      for (int k = 0; k < MT * NB; ++k) {
+        __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);       // a matrix instruction
+        __builtin_amdgcn_sched_group_barrier(0x2, 8 / MT, 0);  // widening
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      if (i % LEN == LEN - 1)
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[m][n][r] = fmaf(sc[n][i / LEN], p[m][n][r], acc[m][n][r]);
+    };
+    read(0);
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const nt_u4 q = l.w[slot][(wc + n) * 128 + 64 * k + lane];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) wf[n][4 * k + i] = widen(q[place(i)]);
-      }
+      for (int k = 0; k < 2; ++k) q[n][k] = l.w[slot][(wc + n) * 128 + 64 * k + lane];
 #pragma unroll
       for (int e = 0; e < GS; ++e) sc[n][e] = l.s[sl][(wc + n) * 128 + (b % PER * GS + e) * 32 + c];
     }
+    widen_all(0);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      nt_u4 xc[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) xc[i] = l.x[slot][(wt + m) * 512 + 64 * i + lane];
-#pragma unroll
-      for (int e = 0; e < GS; ++e) {
-        f32x16_t p[NB];
-#pragma unroll
-        for (int n = 0; n < NB; ++n) p[n] = nothing();
-#pragma unroll
-        for (int i = 8 / GS * e; i < 8 / GS * (e + 1); ++i)
-#pragma unroll
-          for (int n = 0; n < NB; ++n) p[n] = mfma(as_bf16(xc[i]), wf[n][i], p[n]);
-#pragma unroll
-        for (int n = 0; n < NB; ++n)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) acc[m][n][r] = fmaf(sc[n][e], p[n][r], acc[m][n][r]);
-      }
-    }
+    for (int i = 0; i < 8; ++i) multiply(i);
     // corrections every four groups, so that sums stay small
     if (b % PER == PER - 1 || b == a.kb - 1) {
 #pragma unroll
@@ -690,8 +719,12 @@ void go_rows(const I4Args &a, hipStream_t s) {
 template <int MT, int NB, int WV, int GS, bool ZP, typename TY>
 void go_blocks(const I4Args &a, hipStream_t s) {
   hipLaunchKernelGGL((i4_blocks<MT, NB, WV, GS, ZP, TY>),
-                     dim3((a.N + 32 * NB - 1) / (32 * NB), (a.T + 32 * MT - 1) / (32 * MT)), dim3(64 * WV), 0,
-                     s, a);
+                     dim3((a.N + 32 * NB - 1) / (32 * NB), (a.T + 32 * MT - 1) / (32 * MT), a.ks), dim3(64 * WV),
+                     0, s, a);
+  if (a.ks > 1) {
+    const int64_t n = (int64_t(a.T) * a.N / 4 + 255) / 256;
+    hipLaunchKernelGGL(i4_join_kernel<TY>, dim3(unsigned(n < 2048 ? n : 2048)), dim3(256), 0, s, a);
+  }
 }
 
 template <int BT, int WC, int GS, bool ZP, typename TY>
@@ -838,7 +871,7 @@ extern "C" int tcl_i4_linear(const tcl_i4_weight *w, const void *x, int64_t ldx,
   I4Args a{p, reinterpret_cast<const float *>(p + l.w), w->zeros ? p + l.scale : nullptr,
            static_cast<const uint16_t *>(x), y, ldx, ldy, n_tokens, w->d_in, w->d_out, l.kb, l.groups,
            w->group < 128 ? 0 : ((uint64_t(1) << 32) + w->group / 128 - 1) / (w->group / 128), reinterpret_cast<nt_u4 *>(q),
-           reinterpret_cast<float *>(q + sp.x), sp.steps, 0, 0};
+           reinterpret_cast<float *>(q + sp.x), sp.steps, 0, 0, 1, nullptr};
   hipStream_t s = static_cast<hipStream_t>(stream);
   logf("i4: tokens=%d d_in=%d d_out=%d group=%d zeros=%d", a.T, a.K, a.N, w->group, w->zeros);
   if (w->group == 32)
