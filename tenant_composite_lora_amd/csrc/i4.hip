@@ -24,6 +24,8 @@
 // and 2 j + 1 of an eight lie at bits 3 + 4 j and 19 + 4 j, those beyond bit 31
 // at its start.  Behind the blocks come the scales, 32 channels of a group side
 // by side, and the zero points likewise.
+#include <type_traits>
+
 #include "kern_common.hpp"
 
 namespace tcl {
@@ -44,6 +46,7 @@ struct I4Args {
   int32_t nt, nc;         // tiles of tokens, of channels
   int32_t ks;             // workgroups that share a tile's columns (i4_blocks)
   float *part;            // [ks][T][N], where ks > 1
+  bool y_f32;
 };
 
 // ---------------------------------------------------------------------------
@@ -204,13 +207,12 @@ __device__ inline bf16x8_t parts_w(float v) {
 }
 
 // Four channels of a token to y.
-template <typename TY>
 __device__ inline void store4(const I4Args &a, int t, int ch, nt_f4 v) {
-  TY *p = static_cast<TY *>(a.y) + int64_t(t) * a.ldy + ch;
-  if constexpr (sizeof(TY) == 4) {
-    *reinterpret_cast<nt_f4 *>(p) = v;
+  const int64_t at = int64_t(t) * a.ldy + ch;
+  if (a.y_f32) {
+    *reinterpret_cast<nt_f4 *>(static_cast<float *>(a.y) + at) = v;
   } else {
-    *reinterpret_cast<nt_u2 *>(p) = nt_u2{uint32_t(f32_to_bf16(v[0])) | uint32_t(f32_to_bf16(v[1])) << 16,
+    *reinterpret_cast<nt_u2 *>(static_cast<uint16_t *>(a.y) + at) = nt_u2{uint32_t(f32_to_bf16(v[0])) | uint32_t(f32_to_bf16(v[1])) << 16,
                                           uint32_t(f32_to_bf16(v[2])) | uint32_t(f32_to_bf16(v[3])) << 16};
   }
 }
@@ -230,14 +232,31 @@ __device__ inline void add_up(const I4Args &a, const float *part, int t0, int c0
   }
 }
 
+// A wave's blocks first, first + step, ... below n, from slots 0 .. AHEAD - 1 in
+// turn: block(slot, number, whether the slot is to be filled again).  No branch
+// lies around a load: where two paths meet, the compiler waits for the longer
+// one.  (Slots that nothing uses again are filled with the last block, fewer
+// than AHEAD of them.)
+template <int AHEAD, typename F>
+__device__ inline void stream(int first, int step, int n, F block) {
+  int b = first;
+  for (; b + AHEAD * step < n; b += AHEAD * step)
+#pragma unroll
+    for (int d = 0; d < AHEAD; ++d) block(d, b + d * step, std::true_type{});
+#pragma unroll
+  for (int d = 0; d < AHEAD; ++d)
+    if (b + d * step < n) block(d, b + d * step, std::false_type{});
+}
+
 // Few tokens, straight from x.  16 NB channels by 16 MT tokens; wave w of WV
 // takes the blocks w, w + WV, ... of 128 columns.  Tokens are the rows of a
 // result, so that a lane holds one channel, its scale and zero point; the sums
 // of x come from an operand of ones.  GS: groups of a block (4, 2, 1; 1 also
 // for groups of several blocks).
-template <int MT, int NB, int WV, int GS, bool ZP, typename TY>
+template <int MT, int NB, int WV, int GS, bool ZP>
 __global__ __launch_bounds__(64 * WV) void i4_rows(I4Args a) {
   const Widen widen;
+  constexpr int AHEAD = NB > 2 ? 2 : 4;  // blocks on their way
   constexpr int LD = 16 * NB + 4;
   __shared__ __align__(16) float part[WV * 16 * LD];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
@@ -264,37 +283,39 @@ __global__ __launch_bounds__(64 * WV) void i4_rows(I4Args a) {
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int n = 0; n < NB; ++n) acc[m][n] = f32x4_t{0, 0, 0, 0};
-  // (operands are replaced by the wave's next block's, as in i4_blocks)
-  nt_u2 wq[NB][2];
-  nt_u4 xr[MT][4];
-  float s[NB][GS], z[NB][GS];
-  auto load_w = [&](int n, int k, int b) {
-    wq[n][k] = *reinterpret_cast<const nt_u2 *>(wp[n] + int64_t(b) * 2048 + 1024 * k);
+  // (operands are replaced as in i4_blocks)
+  nt_u2 wq[AHEAD][NB][2];
+  nt_u4 xr[AHEAD][MT][4];
+  float s[AHEAD][NB][GS], z[AHEAD][NB][GS];
+  auto load_w = [&](int d, int n, int k, int b) {
+    wq[d][n][k] = *reinterpret_cast<const nt_u2 *>(wp[n] + int64_t(min(b, a.kb - 1)) * 2048 + 1024 * k);
   };
-  auto load_s = [&](int n, int b) {
+  auto load_s = [&](int d, int n, int b) {
 #pragma unroll
     for (int e = 0; e < GS; ++e) {
-      const int gr = group_at<GS>(a, b, e);
-      s[n][e] = sp[n][gr * 32];
-      z[n][e] = ZP ? 16.f + float(zp[n][gr * 32]) : 24.f;
+      const int gr = group_at<GS>(a, min(b, a.kb - 1), e);
+      s[d][n][e] = sp[n][gr * 32];
+      z[d][n][e] = ZP ? 16.f + float(zp[n][gr * 32]) : 24.f;
     }
   };
-  auto load_x = [&](int m, int i, int b) {
-    // columns past the row's end: zeros
-    const bool in = b * 128 + 32 * i < a.K;
-    const nt_u4 u = *reinterpret_cast<const nt_u4 *>(xp[m] + (in ? b * 128 + 32 * i : 0));
-    xr[m][i] = in ? u : nt_u4{0, 0, 0, 0};
+  auto load_x = [&](int d, int m, int i, int b) {
+    // (columns past the row's end: any of it)
+    const int k = b * 128 + 32 * i;
+    xr[d][m][i] = *reinterpret_cast<const nt_u4 *>(xp[m] + (k < a.K ? k : 0));
   };
-  if (w < a.kb) {
 #pragma unroll
-    for (int n = 0; n < NB; ++n) load_w(n, 0, w), load_w(n, 1, w), load_s(n, w);
+  for (int d = 0; d < AHEAD; ++d) {
+    const int b = w + d * WV;
+#pragma unroll
+    for (int n = 0; n < NB; ++n) load_w(d, n, 0, b), load_w(d, n, 1, b), load_s(d, n, b);
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) load_x(m, i, w);
+      for (int i = 0; i < 4; ++i) load_x(d, m, i, b);
+    __builtin_amdgcn_sched_barrier(0);
   }
-  for (int b = w; b < a.kb; b += WV) {
-    const int next = min(b + WV, a.kb - 1);
+  // block b from slot d, which block b + AHEAD * WV then takes
+  auto block = [&](int d, int b, auto more) {
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -304,24 +325,32 @@ __global__ __launch_bounds__(64 * WV) void i4_rows(I4Args a) {
         for (int n = 0; n < NB; ++n) p[n] = f32x4_t{0, 0, 0, 0};
 #pragma unroll
         for (int i = 4 / GS * e; i < 4 / GS * (e + 1); ++i) {
-          sum = mfma(as_bf16(xr[m][i]), ones(), sum);
+          // columns past the row's end: zeros (here, not where they are read,
+          // which would wait for them)
+          const bf16x8_t x = as_bf16(b * 128 + 32 * i < a.K ? xr[d][m][i] : nt_u4{0, 0, 0, 0});
+          sum = mfma(x, ones(), sum);
 #pragma unroll
-          for (int n = 0; n < NB; ++n) p[n] = mfma(as_bf16(xr[m][i]), widen(wq[n][i >> 1][i & 1]), p[n]);
-          load_x(m, i, next);
-          if (m == MT - 1 && i % 2 == 1)
+          for (int n = 0; n < NB; ++n)
+            p[n] = mfma(x, widen(wq[d][n][i >> 1][i & 1]), p[n]);
+          if constexpr (more) {
+            load_x(d, m, i, b + AHEAD * WV);
+            if (m == MT - 1 && i % 2 == 1)
 #pragma unroll
-            for (int n = 0; n < NB; ++n) load_w(n, i / 2, next);
+              for (int n = 0; n < NB; ++n) load_w(d, n, i / 2, b + AHEAD * WV);
+          }
           __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
         for (int n = 0; n < NB; ++n)
 #pragma unroll
           for (int r = 0; r < 4; ++r)
-            acc[m][n][r] = fmaf(s[n][e], fmaf(-z[n][e], sum[r], p[n][r]), acc[m][n][r]);
+            acc[m][n][r] = fmaf(s[d][n][e], fmaf(-z[d][n][e], sum[r], p[n][r]), acc[m][n][r]);
       }
+    if constexpr (more)
 #pragma unroll
-    for (int n = 0; n < NB; ++n) load_s(n, next);
-  }
+      for (int n = 0; n < NB; ++n) load_s(d, n, b + AHEAD * WV);
+  };
+  stream<AHEAD>(w, WV, a.kb, block);
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     if (m) __syncthreads();
@@ -330,7 +359,7 @@ __global__ __launch_bounds__(64 * WV) void i4_rows(I4Args a) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) part[(w * 16 + 4 * g + r) * LD + 16 * n + c] = acc[m][n][r];
     __syncthreads();
-    add_up<16, NB, LD, WV>(a, part, t0 + 16 * m, c0, [&](int t, int ch, nt_f4 v) { store4<TY>(a, t, ch, v); });
+    add_up<16, NB, LD, WV>(a, part, t0 + 16 * m, c0, [&](int t, int ch, nt_f4 v) { store4(a, t, ch, v); });
   }
 }
 
@@ -342,15 +371,17 @@ __device__ inline constexpr int place(int i) { return (i & 1) << 1 | i >> 1; }
 
 // More tokens, from staged activations: 32 NB channels by 32 MT tokens, the
 // blocks dealt out to the waves as in i4_rows, then the corrections.
-template <int MT, int NB, int WV, int GS, bool ZP, typename TY>
+template <int MT, int NB, int WV, int GS, bool ZP>
 __global__ __launch_bounds__(64 * WV) void i4_blocks(I4Args a) {
   const Widen widen;
+  constexpr int AHEAD = 1;  // blocks on their way
   constexpr int LD = 32 * NB + 8;
   __shared__ __align__(16) float part[WV * 32 * LD];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int c = lane & 31, h = lane >> 5;
-  const int c0 = blockIdx.x * 32 * NB, t0 = blockIdx.y * 32 * MT;
-  const int first = blockIdx.z * WV + w, stride = a.ks * WV;
+  const int nx = (a.N + 32 * NB - 1) / (32 * NB);
+  const int c0 = blockIdx.x % nx * 32 * NB, t0 = blockIdx.x / nx * 32 * MT;
+  const int first = blockIdx.y * WV + w, stride = a.ks * WV;
   const int tiles = (a.N + 31) / 32, tt = (a.T + 31) / 32;
   const nt_u4 *xp[MT];
   const float *ep[MT];
@@ -366,7 +397,7 @@ __global__ __launch_bounds__(64 * WV) void i4_blocks(I4Args a) {
 #pragma unroll
   for (int n = 0; n < NB; ++n) {
     // (channel tiles past the last: the last one again, not stored)
-    const int64_t ct = min(blockIdx.x * NB + n, unsigned(tiles - 1));
+    const int64_t ct = min(c0 / 32 + n, tiles - 1);
     wp[n] = reinterpret_cast<const nt_u4 *>(a.w) + ct * a.kb * 128 + lane;
     sp[n] = a.scale + ct * a.groups * 32 + c;
     zp[n] = ZP ? a.zero + ct * a.groups * 32 + c : nullptr;
@@ -376,28 +407,36 @@ __global__ __launch_bounds__(64 * WV) void i4_blocks(I4Args a) {
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int n = 0; n < NB; ++n) acc[m][n] = nothing();
-  // A block's operands, each replaced by the wave's next block's as soon as its
-  // products have been issued: a block is always on its way, and no register
-  // waits for it twice.  (The scheduling barriers hold the loads there; left to
-  // itself the compiler puts them right before their use.)
-  nt_u4 wq[NB][2], xr[MT][8];
-  float s[NB][GS];
-  auto load_w = [&](int n, int k, int b) { wq[n][k] = wp[n][int64_t(b) * 128 + 64 * k]; };
-  auto load_s = [&](int n, int b) {
-#pragma unroll
-    for (int e = 0; e < GS; ++e) s[n][e] = sp[n][group_at<GS>(a, b, e) * 32];
+  // A block's operands, each replaced by that of AHEAD blocks on as soon as its
+  // products have been issued: loads are always on their way, and no register
+  // waits for them twice.  Activations as far ahead as weights, although they
+  // come from L2: loads are waited for in the order of their issue.  (The
+  // scheduling barriers hold the loads there; left to itself the compiler puts
+  // them right before their use.)
+  nt_u4 wq[AHEAD][NB][2], xr[AHEAD][MT][8];
+  float s[AHEAD][NB][GS];
+  auto load_w = [&](int d, int n, int k, int b) {
+    wq[d][n][k] = wp[n][int64_t(min(b, a.kb - 1)) * 128 + 64 * k];
   };
-  auto load_x = [&](int m, int i, int b) { xr[m][i] = xp[m][int64_t(b) * 512 + 64 * i]; };
-  if (first < a.kb) {
+  auto load_s = [&](int d, int n, int b) {
 #pragma unroll
-    for (int n = 0; n < NB; ++n) load_w(n, 0, first), load_w(n, 1, first), load_s(n, first);
+    for (int e = 0; e < GS; ++e) s[d][n][e] = sp[n][group_at<GS>(a, min(b, a.kb - 1), e) * 32];
+  };
+  auto load_x = [&](int d, int m, int i, int b) {
+    xr[d][m][i] = xp[m][int64_t(min(b, a.kb - 1)) * 512 + 64 * i];
+  };
+#pragma unroll
+  for (int d = 0; d < AHEAD; ++d) {
+    const int b = first + d * stride;
+#pragma unroll
+    for (int n = 0; n < NB; ++n) load_w(d, n, 0, b), load_w(d, n, 1, b), load_s(d, n, b);
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) load_x(m, i, first);
+      for (int i = 0; i < 8; ++i) load_x(d, m, i, b);
+    __builtin_amdgcn_sched_barrier(0);
   }
-  for (int b = first; b < a.kb; b += stride) {
-    const int next = min(b + stride, a.kb - 1);
+  auto block = [&](int d, int b, auto more) {
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -409,21 +448,25 @@ __global__ __launch_bounds__(64 * WV) void i4_blocks(I4Args a) {
         for (int i = 8 / GS * e; i < 8 / GS * (e + 1); ++i) {
 #pragma unroll
           for (int n = 0; n < NB; ++n)
-            p[n] = mfma(as_bf16(xr[m][i]), widen(wq[n][i / 4][place(i % 4)]), p[n]);
-          load_x(m, i, next);
-          if (m == MT - 1 && i % 4 == 3)
+            p[n] = mfma(as_bf16(xr[d][m][i]), widen(wq[d][n][i / 4][place(i % 4)]), p[n]);
+          if constexpr (more) {
+            load_x(d, m, i, b + AHEAD * stride);
+            if (m == MT - 1 && i % 4 == 3)
 #pragma unroll
-            for (int n = 0; n < NB; ++n) load_w(n, i / 4, next);
+              for (int n = 0; n < NB; ++n) load_w(d, n, i / 4, b + AHEAD * stride);
+          }
           __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
         for (int n = 0; n < NB; ++n)
 #pragma unroll
-          for (int r = 0; r < 16; ++r) acc[m][n][r] = fmaf(s[n][e], p[n][r], acc[m][n][r]);
+          for (int r = 0; r < 16; ++r) acc[m][n][r] = fmaf(s[d][n][e], p[n][r], acc[m][n][r]);
       }
+    if constexpr (more)
 #pragma unroll
-    for (int n = 0; n < NB; ++n) load_s(n, next);
-  }
+      for (int n = 0; n < NB; ++n) load_s(d, n, b + AHEAD * stride);
+  };
+  stream<AHEAD>(first, stride, a.kb, block);
   // (two groups a step: a half each; groups behind the last meet sums of zero)
   for (int st = first; st < 2 * a.steps; st += stride) {
     const int gr = min(GS == 1 ? group_of(a, 2 * st + h) : 2 * st + h, a.groups - 1);
@@ -447,15 +490,14 @@ __global__ __launch_bounds__(64 * WV) void i4_blocks(I4Args a) {
     __syncthreads();
     add_up<32, 2 * NB, LD, WV>(a, part, t0 + 32 * m, c0, [&](int t, int ch, nt_f4 v) {
       if (a.ks == 1)
-        store4<TY>(a, t, ch, v);
+        store4(a, t, ch, v);
       else
-        *reinterpret_cast<nt_f4 *>(a.part + ((int64_t(blockIdx.z) * a.T + t) * a.N + ch)) = v;
+        *reinterpret_cast<nt_f4 *>(a.part + ((int64_t(blockIdx.y) * a.T + t) * a.N + ch)) = v;
     });
   }
 }
 
 // Adds the parts of the workgroups that shared columns, in order.
-template <typename TY>
 __global__ __launch_bounds__(256) void i4_join_kernel(I4Args a) {
   const int64_t n4 = a.N / 4, all = a.T * n4;
   for (int64_t o = int64_t(blockIdx.x) * 256 + threadIdx.x; o < all; o += int64_t(gridDim.x) * 256) {
@@ -463,7 +505,7 @@ __global__ __launch_bounds__(256) void i4_join_kernel(I4Args a) {
     nt_f4 v = in[0];
 #pragma unroll 4
     for (int z = 1; z < a.ks; ++z) v += in[z * all];
-    store4<TY>(a, int(o / n4), int(o % n4) * 4, v);
+    store4(a, int(o / n4), int(o % n4) * 4, v);
   }
 }
 
@@ -500,7 +542,7 @@ __device__ inline void move4(uint32_t to, const void *from, uint32_t off) {
 // each filled while the block two before it is multiplied (a wave's own
 // registers hold no load: one block's time does not cover a trip to memory);
 // scales, zero points and sums of x come with every four groups.
-template <int BT, int WC, int GS, bool ZP, typename TY>
+template <int BT, int WC, int GS, bool ZP>
 __global__ __launch_bounds__(512, 2) void i4_tile(I4Args a) {
   const Widen widen;
   constexpr int BC = 256, WV = 8, WT = WV / WC, NB = BC / WC / 32, MT = BT / WT / 32, PER = 4 / GS;
@@ -662,7 +704,7 @@ __global__ __launch_bounds__(512, 2) void i4_tile(I4Args a) {
     for (int k = 0; k < 4 * NB; ++k) {
       const int o = k * 64 + lane, x = o / (8 * NB), t = t0 + 32 * (wt + m) + x;
       const int ch = o % (8 * NB) * 4, at = c0 + 32 * wc + ch;
-      if (t < a.T && at < a.N) store4<TY>(a, t, at, *reinterpret_cast<const nt_f4 *>(out + x * LD + ch));
+      if (t < a.T && at < a.N) store4(a, t, at, *reinterpret_cast<const nt_f4 *>(out + x * LD + ch));
     }
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
@@ -678,6 +720,45 @@ constexpr int kMaxChannels = 1 << 26, kMaxTokens = 1 << 24;
 
 // up to as many tokens are taken from x as it is, in one launch
 constexpr int kRows = 16;
+
+// Which kernel.  Measured on captured calls with weights from memory, groups of
+// 128, us, staging included; d_in 4096 unless said.
+//   i4_rows, as many channels a workgroup as leave 192 of them: 1 token, 1024
+//     channels: 16 channels 4.5, 32 5.7; 4096 channels 4.9, 6.1; 14336: 16
+//     channels 10.6, 64 8.7 (16 tokens: 19.1, 9.9).
+//   i4_blocks likewise: 64 tokens, 4096 channels: 32 channels a workgroup 10.9,
+//     64 11.8, 128 15.2; 14336: 22.9, 23.0, 17.6; 23 tokens, 14336: 15.0, 13.1,
+//     16.4.  What bounds it is what a CU takes in, some 60 GB/s each, so that
+//     few workgroups with long rows are split over d_in and joined by a launch
+//     more: 23 tokens, 4096 channels, d_in 14336: whole 23.3, in four 17.8; d_in
+//     4096 10.3 and 11.6.
+//   Tiles by whole rounds over the CUs (half_us): 512 tokens, 4096 channels:
+//     blocks 29.8, tiles of 64 tokens 43.2, of 128 60.1; 1024: 53.5, 50.2, 62.2;
+//     2048: 103, 98, 83; 512 x 14336: 91.7, 84.9, 68.8.
+struct Choice {
+  enum { kFew, kBlocks, kTile64, kTile128 } kernel;
+  int nb;  // 16 (few) or 32 (blocks) channels a workgroup times this
+  int ks;
+};
+
+int64_t rounds(int64_t workgroups) { return (workgroups + 255) / 256; }
+
+Choice choose(int32_t n_tokens, int32_t d_out, int32_t kb) {
+  const int64_t T = n_tokens, N = d_out;
+  auto over = [](int64_t n, int64_t d) { return (n + d - 1) / d; };
+  if (T <= kRows) return {Choice::kFew, over(N, 64) >= 192 ? 4 : over(N, 32) >= 192 ? 2 : 1, 1};
+  const int64_t tb = over(T, 32), w2 = tb * over(N, 64), w4 = tb * over(N, 128);
+  if (w4 >= 192) {
+    const int64_t half_us[3] = {10 + 24 * rounds(w4), 16 + 80 * rounds(over(T, 64) * over(N, 256)),
+                                10 + 132 * rounds(over(T, 128) * over(N, 256))};
+    if (half_us[0] <= half_us[1] && half_us[0] <= half_us[2]) return {Choice::kBlocks, 4, 1};
+    return {half_us[1] < half_us[2] ? Choice::kTile64 : Choice::kTile128, 0, 1};
+  }
+  if (w2 >= 192) return {Choice::kBlocks, 2, 1};
+  // (a wave keeps two blocks at least)
+  const int64_t ks = kb < 64 ? 1 : 256 / w2 < kb / 16 ? 256 / w2 : kb / 16;
+  return {Choice::kBlocks, ks > 1 ? 2 : 1, int(ks < 1 ? 1 : ks)};
+}
 
 struct Layout {
   int64_t tiles;
@@ -709,29 +790,29 @@ int check_weight(const tcl_i4_weight *w, Layout *l) {
   return TCL_OK;
 }
 
-template <int MT, int NB, int WV, int GS, bool ZP, typename TY>
+template <int MT, int NB, int WV, int GS, bool ZP>
 void go_rows(const I4Args &a, hipStream_t s) {
-  hipLaunchKernelGGL((i4_rows<MT, NB, WV, GS, ZP, TY>),
+  hipLaunchKernelGGL((i4_rows<MT, NB, WV, GS, ZP>),
                      dim3((a.N + 16 * NB - 1) / (16 * NB), (a.T + 16 * MT - 1) / (16 * MT)), dim3(64 * WV), 0,
                      s, a);
 }
 
-template <int MT, int NB, int WV, int GS, bool ZP, typename TY>
+template <int MT, int NB, int WV, int GS, bool ZP>
 void go_blocks(const I4Args &a, hipStream_t s) {
-  hipLaunchKernelGGL((i4_blocks<MT, NB, WV, GS, ZP, TY>),
-                     dim3((a.N + 32 * NB - 1) / (32 * NB), (a.T + 32 * MT - 1) / (32 * MT), a.ks), dim3(64 * WV),
-                     0, s, a);
+  hipLaunchKernelGGL((i4_blocks<MT, NB, WV, GS, ZP>),
+                     dim3(unsigned((a.N + 32 * NB - 1) / (32 * NB)) * ((a.T + 32 * MT - 1) / (32 * MT)), a.ks),
+                     dim3(64 * WV), 0, s, a);
   if (a.ks > 1) {
     const int64_t n = (int64_t(a.T) * a.N / 4 + 255) / 256;
-    hipLaunchKernelGGL(i4_join_kernel<TY>, dim3(unsigned(n < 2048 ? n : 2048)), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(i4_join_kernel, dim3(unsigned(n < 2048 ? n : 2048)), dim3(256), 0, s, a);
   }
 }
 
-template <int BT, int WC, int GS, bool ZP, typename TY>
+template <int BT, int WC, int GS, bool ZP>
 void go_tile(I4Args a, hipStream_t s) {
   a.nt = (a.T + BT - 1) / BT;
   a.nc = (a.N + 255) / 256;
-  hipLaunchKernelGGL((i4_tile<BT, WC, GS, ZP, TY>), dim3((a.nt * a.nc + 7) / 8 * 8), dim3(512), 0, s, a);
+  hipLaunchKernelGGL((i4_tile<BT, WC, GS, ZP>), dim3((a.nt * a.nc + 7) / 8 * 8), dim3(512), 0, s, a);
 }
 
 template <int GS>
@@ -741,35 +822,37 @@ void go_stage(const I4Args &a, hipStream_t s) {
                      g);
 }
 
-template <int GS, bool ZP, typename TY>
-void product(const I4Args &a, hipStream_t s) {
-  if (a.T <= kRows)
-    go_rows<1, 1, 8, GS, ZP, TY>(a, s);
-  else {
-    go_stage<GS>(a, s);
-    if (a.T <= 32)
-      go_blocks<1, 1, 8, GS, ZP, TY>(a, s);
-    else if (a.T <= 64)
-      go_blocks<2, 2, 8, GS, ZP, TY>(a, s);
-    else
-      go_tile<128, 4, GS, ZP, TY>(a, s);
-  }
-}
-
 template <int GS, bool ZP>
-void product(const I4Args &a, int yd, hipStream_t s) {
-  if (yd == TCL_BF16)
-    product<GS, ZP, bf16_t>(a, s);
+void product(const I4Args &a, hipStream_t s) {
+  const Choice c = choose(a.T, a.N, a.kb);
+  if (c.kernel == Choice::kFew) {
+    if (c.nb == 4)
+      go_rows<1, 4, 8, GS, ZP>(a, s);
+    else if (c.nb == 2)
+      go_rows<1, 2, 8, GS, ZP>(a, s);
+    else
+      go_rows<1, 1, 8, GS, ZP>(a, s);
+    return;
+  }
+  go_stage<GS>(a, s);
+  if (c.kernel == Choice::kTile64)
+    go_tile<64, 4, GS, ZP>(a, s);
+  else if (c.kernel == Choice::kTile128)
+    go_tile<128, 4, GS, ZP>(a, s);
+  else if (c.nb == 4)
+    go_blocks<1, 4, 8, GS, ZP>(a, s);
+  else if (c.nb == 2)
+    go_blocks<1, 2, 8, GS, ZP>(a, s);
   else
-    product<GS, ZP, float>(a, s);
+    go_blocks<1, 1, 8, GS, ZP>(a, s);
 }
 
 template <int GS>
-void product(const I4Args &a, int yd, hipStream_t s) {
+void product(const I4Args &a, hipStream_t s) {
   if (a.zero)
-    product<GS, true>(a, yd, s);
+    product<GS, true>(a, s);
   else
-    product<GS, false>(a, yd, s);
+    product<GS, false>(a, s);
 }
 
 }  // namespace
@@ -811,18 +894,21 @@ extern "C" int tcl_i4_pack(tcl_i4_weight *w, void *W_p, size_t bytes, void *stre
 namespace tcl {
 namespace {
 
-// Bytes of the staged activations, and with their sums.
+// Bytes of the staged activations, with their sums, with the parts of
+// workgroups that share columns.
 struct Space {
-  size_t x, total;
-  int32_t steps;
+  size_t x, sums, total;
+  int32_t steps, ks;
 };
 Space space(const tcl_i4_weight *w, const Layout &l, int32_t n_tokens) {
-  if (n_tokens <= kRows || w->d_out == 0) return {0, 0, 0};
+  if (n_tokens <= kRows || w->d_out == 0) return {0, 0, 0, 0, 1};
   const size_t tiles = (size_t(n_tokens) + 31) / 32;
   const int32_t groups = w->group < 128 ? l.groups : l.kb;  // longer ones count by their blocks
   const int32_t steps = (groups + 3) / 4;
   const size_t x = tiles * l.kb * 8192;
-  return {x, x + tiles * steps * 512, steps};
+  const size_t sums = x + tiles * steps * 512;
+  const int32_t ks = choose(n_tokens, w->d_out, l.kb).ks;
+  return {x, sums, sums + (ks > 1 ? size_t(ks) * n_tokens * w->d_out * 4 : 0), steps, ks};
 }
 
 int check_tokens(const tcl_i4_weight *w, int32_t n_tokens) {
@@ -871,15 +957,16 @@ extern "C" int tcl_i4_linear(const tcl_i4_weight *w, const void *x, int64_t ldx,
   I4Args a{p, reinterpret_cast<const float *>(p + l.w), w->zeros ? p + l.scale : nullptr,
            static_cast<const uint16_t *>(x), y, ldx, ldy, n_tokens, w->d_in, w->d_out, l.kb, l.groups,
            w->group < 128 ? 0 : ((uint64_t(1) << 32) + w->group / 128 - 1) / (w->group / 128), reinterpret_cast<nt_u4 *>(q),
-           reinterpret_cast<float *>(q + sp.x), sp.steps, 0, 0, 1, nullptr};
+           reinterpret_cast<float *>(q + sp.x), sp.steps, 0, 0, sp.ks,
+           reinterpret_cast<float *>(q + sp.sums), yd == TCL_F32};
   hipStream_t s = static_cast<hipStream_t>(stream);
   logf("i4: tokens=%d d_in=%d d_out=%d group=%d zeros=%d", a.T, a.K, a.N, w->group, w->zeros);
   if (w->group == 32)
-    product<4>(a, yd, s);
+    product<4>(a, s);
   else if (w->group == 64)
-    product<2>(a, yd, s);
+    product<2>(a, s);
   else
-    product<1>(a, yd, s);
+    product<1>(a, s);
   TCL_HIP(hipGetLastError());
   return TCL_OK;
 }

@@ -82,6 +82,29 @@ def test_tokens_and_channels_around_the_tiles(T, d_out):
     close(tclora.i4_linear(tclora.I4Weight(*w), x, y_dtype=torch.float32), *product64(w, n, x))
 
 
+# (calls that take tiles of 64 and of 128 tokens, whole and ragged, blocks of
+# three widths, and columns split over workgroups)
+@pytest.mark.parametrize("T,d_out", [(1024, 4096), (1000, 4000), (2048, 4096), (2030, 4104), (500, 14336),
+                                     (700, 7000), (33, 6200), (64, 14336), (300, 2600)])
+@pytest.mark.parametrize("d_in,group", [(96, 32), (192, 64), (640, 128), (768, 384), (64, 64), (32, 32)])
+def test_many_tokens(T, d_out, d_in, group):
+    w, n = weight(T + d_in, d_out, d_in, group, d_in % 3 == 0, full=True)
+    x = acts(T, T, d_in)
+    y = torch.full((T + 1, d_out), 7.0, device=DEV)
+    tclora.i4_linear(tclora.I4Weight(*w), x, y=y[:T])
+    close(y[:T], *product64(w, n, x))
+    assert (y[T] == 7).all()
+
+
+@pytest.mark.parametrize("T", [17, 40, 64])
+@pytest.mark.parametrize("d_in,d_out,group", [(8192, 1024, 128), (14336, 72, 32), (9216, 2048, 64),
+                                              (16128, 4096, 384), (8224, 520, 32)])
+def test_long_rows(T, d_in, d_out, group):
+    w, n = weight(T, d_out, d_in, group, T == 40)
+    x = acts(T, T, d_in)
+    close(tclora.i4_linear(tclora.I4Weight(*w), x, y_dtype=torch.float32), *product64(w, n, x))
+
+
 @pytest.mark.parametrize("T", [1, 20, 64, 200])
 @pytest.mark.parametrize("d_in", [32, 64, 96, 160, 224, 416, 1120])
 def test_rows_that_end_inside_a_block(T, d_in):
