@@ -3,12 +3,12 @@
 //
 // Whether a batch is good is known only once all of it has been looked over
 // (lengths, page ids, pages left), and nothing of a bad one may be written, so
-// one workgroup checks and then writes what belongs to requests.  What belongs
-// to tokens (positions, slots, the page ids of new pages) it writes as well in
-// small batches, where a launch more is what would cost; in larger ones a
-// second launch does, whose workgroups take kMapThreads tokens each and repeat
-// the scan over the requests, which is cheaper than a round trip of its
-// results through memory.
+// one workgroup checks and then writes what belongs to requests: pointers,
+// lengths, page tables.  What belongs to tokens (positions and slots) it writes
+// as well in small batches, where a launch more is what would cost; in larger
+// ones a second launch does, from what the first has left.
+// A launch and some ten round trips and barriers each: 64 requests of one token
+// MAP_DECODE us, 1152 requests with 43 000 tokens MAP_MIXED.
 #include "kern_common.hpp"
 #include "kv.hpp"
 #include "scan.hpp"
@@ -18,6 +18,8 @@ namespace {
 
 // Tokens that the first launch writes itself.
 constexpr int kMapOne = 8192;
+// Requests whose pointers the second launch searches in LDS.
+constexpr int kMapPtr = 8191;
 
 struct MapArgs {
   int32_t S, G, T, n_free, ld;
@@ -27,21 +29,49 @@ struct MapArgs {
   int64_t *slot;
 };
 
-__device__ inline int64_t block_sum(int64_t v, int64_t *lds) {
+// The workgroup's sums of u and v, and whether any thread has found it bad.
+__device__ inline void block_sums(int64_t &u, int64_t &v, bool &bad, int64_t (*lds)[kMapThreads / 64], int *flag) {
 #pragma unroll
-  for (int x = 32; x > 0; x >>= 1) v += __shfl_xor(v, x, 64);
+  for (int x = 32; x > 0; x >>= 1) {
+    u += __shfl_xor(u, x, 64);
+    v += __shfl_xor(v, x, 64);
+  }
+  if ((threadIdx.x & 63) == 0) {
+    lds[0][threadIdx.x >> 6] = u;
+    lds[1][threadIdx.x >> 6] = v;
+  }
+  if (bad) *flag = 1;
   __syncthreads();
-  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
-  __syncthreads();
-  int64_t s = 0;
+  u = v = 0;
 #pragma unroll
-  for (int i = 0; i < kMapThreads / 64; ++i) s += lds[i];
-  return s;
+  for (int i = 0; i < kMapThreads / 64; ++i) {
+    u += lds[0][i];
+    v += lds[1][i];
+  }
+  bad = *flag;
 }
 
 __device__ inline int pages_of(const MapArgs &a, int n) {
   return (n >> a.shift) + ((n & ((1 << a.shift) - 1)) != 0);
 }
+
+// The groups' tables, in LDS where they fit (a search in memory is a round trip
+// a step).
+struct Groups {
+  int32_t seq[kMapThreads + 1], prefix[kMapThreads];
+  __device__ inline void load(const MapArgs &a) {
+    if (a.G > kMapThreads) return;
+    for (int g = threadIdx.x; g < a.G; g += blockDim.x) {
+      seq[g] = a.group_seq[g];
+      prefix[g] = a.prefix_len[g];
+    }
+    if (threadIdx.x == 0 && a.G > 0) seq[a.G] = a.group_seq[a.G];
+  }
+  // prefix of the group of request s
+  __device__ inline int prefix_of(const MapArgs &a, int s) const {
+    return a.G > kMapThreads ? a.prefix_len[upper(a.group_seq, a.G, s)] : prefix[upper(seq, a.G, s)];
+  }
+};
 
 // A chunk of kMapThreads requests in LDS: tokens and pages before each, its
 // keys before, its prefix.
@@ -49,18 +79,23 @@ struct Chunk {
   int32_t tok[kMapThreads], page[kMapThreads], have[kMapThreads], prefix[kMapThreads];
 };
 
-// Tokens [t0, t1) of the chunk's requests s0 .. s0 + n - 1.
-__device__ inline void fill(const MapArgs &a, const Chunk &c, int s0, int n, int t0, int t1, int used) {
+// The tokens [t0, t1) of the chunk's requests s0 .. s0 + n - 1.
+__device__ inline void put_tokens(const MapArgs &a, const Chunk &c, int s0, int n, int t0, int t1, int used) {
   const int mask = (1 << a.shift) - 1;
   for (int t = t0 + threadIdx.x; t < t1; t += kMapThreads) {
     const int i = upper(c.tok, n, t), have = c.have[i];
     const int key = have + (t - c.tok[i]), p = key >> a.shift, hp = pages_of(a, have);
-    int32_t *row = a.own_pages + int64_t(s0 + i) * a.ld;
-    const int id = p < hp ? row[p] : a.free_pages[used + c.page[i] + p - hp];
-    // (a page's first key brings it into the table)
-    if ((key & mask) == 0) row[p] = id;
+    const int id = p < hp ? a.own_pages[int64_t(s0 + i) * a.ld + p] : a.free_pages[used + c.page[i] + p - hp];
     a.pos[t] = c.prefix[i] + key;
     a.slot[t] = (int64_t(id) << a.shift) + (key & mask);
+  }
+}
+
+// The pages [g0, g1) that the chunk's requests take (counted over all requests).
+__device__ inline void put_pages(const MapArgs &a, const Chunk &c, int s0, int n, int g0, int g1, int used) {
+  for (int g = g0 + threadIdx.x; g < g1; g += kMapThreads) {
+    const int i = upper(c.page, n, g), p = pages_of(a, c.have[i]) + g - c.page[i];
+    a.own_pages[int64_t(s0 + i) * a.ld + p] = a.free_pages[used + g];
   }
 }
 
@@ -71,65 +106,33 @@ __device__ inline void pad(const MapArgs &a, int t0, int t1) {
   }
 }
 
-// The scan over the requests; the chunk's tokens are written where `tokens`.
-// OLD: own_len as before the call (else as after it).  WRITE: pointers,
-// lengths and the count of pages in use.
-template <bool OLD, bool WRITE>
-__device__ inline void walk(const MapArgs &a, Chunk &c, int (*lds)[kMapThreads / 64], int used, int t0,
-                            int t1) {
-  const int tid = threadIdx.x;
-  int tok = 0, page = 0;
-  for (int s0 = 0; s0 < a.S; s0 += kMapThreads) {
-    const int s = s0 + tid, n = min(kMapThreads, a.S - s0);
-    int q = 0, have = 0, v[2] = {0, 0}, total[2], prefix = 0;
-    if (s < a.S) {
-      q = a.n_new[s];
-      have = OLD ? a.own_len[s] : a.own_out[s] - q;
-      prefix = a.prefix_len[upper(a.group_seq, a.G, s)];
-      v[0] = q;
-      v[1] = pages_of(a, have + q) - pages_of(a, have);
-    }
-    block_scan(v, total, lds);  // (its barriers also end the chunk before)
-    c.tok[tid] = tok + v[0];
-    c.page[tid] = page + v[1];
-    c.have[tid] = have;
-    c.prefix[tid] = prefix;
-    if (WRITE && s < a.S) {
-      a.seq_tok[s] = tok + v[0];
-      a.own_out[s] = have + q;
-    }
-    __syncthreads();
-    const int end = tok + total[0];
-    fill(a, c, s0, n, max(t0, tok), min(t1, end), used);
-    tok = end;
-    page += total[1];
-    if (!WRITE && tok >= t1) break;
-  }
-  if (WRITE && tid == 0) {
-    a.seq_tok[a.S] = tok;
-    a.used_out[0] = used + page;
-  }
-}
-
 __global__ __launch_bounds__(kMapThreads) void kv_map_kernel(MapArgs a) {
   __shared__ int lds[2][kMapThreads / 64];
-  __shared__ int64_t sums[kMapThreads / 64];
+  __shared__ int64_t sums[2][kMapThreads / 64];
   __shared__ int s_bad;
+  __shared__ Groups groups;
   __shared__ Chunk chunk;
   const int tid = threadIdx.x;
   const int used = a.used[0];
+  // (the first chunk's requests stay in registers)
+  const int q0 = tid < a.S ? a.n_new[tid] : 0, n0 = tid < a.S ? a.own_len[tid] : 0;
+  groups.load(a);
   if (tid == 0) s_bad = 0;
   __syncthreads();
   // the batch
   bool bad = used < 0 || used > a.n_free;
   if (a.S > 0 && tid == 0) bad |= a.group_seq[0] != 0 || a.group_seq[a.G] != a.S;
-  for (int g = tid; g < a.G; g += kMapThreads)
-    bad |= a.group_seq[g + 1] < a.group_seq[g] || a.prefix_len[g] < 0;
+  if (a.G <= kMapThreads) {
+    if (tid < a.G) bad |= groups.seq[tid + 1] < groups.seq[tid] || groups.prefix[tid] < 0;
+  } else {
+    for (int g = tid; g < a.G; g += kMapThreads)
+      bad |= a.group_seq[g + 1] < a.group_seq[g] || a.prefix_len[g] < 0;
+  }
   int64_t tokens = 0, pages = 0;
   for (int s = tid; s < a.S; s += kMapThreads) {
-    const int64_t q = a.n_new[s], n = a.own_len[s];
+    const int64_t q = s == tid ? q0 : a.n_new[s], n = s == tid ? n0 : a.own_len[s];
     const int64_t cap = int64_t(a.ld) << a.shift;
-    const int32_t prefix = a.prefix_len[upper(a.group_seq, a.G, s)];
+    const int32_t prefix = groups.prefix_of(a, s);
     if (q < 0 || n < 0 || n + q > cap || prefix + n + q > int64_t(0x7fffffff)) {
       bad = true;
       continue;
@@ -142,16 +145,17 @@ __global__ __launch_bounds__(kMapThreads) void kv_map_kernel(MapArgs a) {
     tokens += q;
     pages += pages_of(a, int(n + q)) - pages_of(a, int(n));
   }
-  tokens = block_sum(tokens, sums);
-  pages = block_sum(pages, sums);
+  block_sums(tokens, pages, bad, sums, &s_bad);
   bad |= tokens > a.T;
   const bool enough = pages <= int64_t(a.n_free) - used;
   // the page ids that are taken
-  if (!bad && enough)
+  if (!bad && enough) {
+#pragma unroll 4
     for (int i = tid; i < int(pages); i += kMapThreads) {
       const int id = a.free_pages[used + i];
       bad |= id < 0 || id >= a.n_pages;
     }
+  }
   if (bad) s_bad = 1;
   __syncthreads();
   const int code = s_bad ? TCL_EINVAL : (enough ? TCL_OK : TCL_ENOSPC);
@@ -160,6 +164,7 @@ __global__ __launch_bounds__(kMapThreads) void kv_map_kernel(MapArgs a) {
     a.status[1] = code == TCL_OK ? int(tokens) : 0;
     a.status[2] = code == TCL_OK ? int(pages) : 0;
     a.status[3] = a.n_free - used - (code == TCL_OK ? int(pages) : 0);
+    a.used_out[0] = used + (code == TCL_OK ? int(pages) : 0);
   }
   const bool all = a.T <= kMapOne;
   if (code != TCL_OK) {
@@ -167,22 +172,63 @@ __global__ __launch_bounds__(kMapThreads) void kv_map_kernel(MapArgs a) {
       a.seq_tok[s] = 0;
       if (s < a.S) a.own_out[s] = a.own_len[s];
     }
-    if (tid == 0) a.used_out[0] = used;
     if (all) pad(a, 0, a.T);
     return;
   }
-  walk<true, true>(a, chunk, lds, used, 0, all ? a.T : 0);
-  if (all) pad(a, int(tokens), a.T);
+  int tok = 0, page = 0;
+  for (int s0 = 0; s0 < a.S; s0 += kMapThreads) {
+    const int s = s0 + tid, n = min(kMapThreads, a.S - s0);
+    int q = 0, have = 0, v[2] = {0, 0}, total[2], prefix = 0;
+    if (s < a.S) {
+      q = s0 ? a.n_new[s] : q0;
+      have = s0 ? a.own_len[s] : n0;
+      prefix = groups.prefix_of(a, s);
+      v[0] = q;
+      v[1] = pages_of(a, have + q) - pages_of(a, have);
+    }
+    block_scan(v, total, lds);  // (its barriers also end the chunk before)
+    chunk.tok[tid] = tok + v[0];
+    chunk.page[tid] = page + v[1];
+    chunk.have[tid] = have;
+    chunk.prefix[tid] = prefix;
+    if (s < a.S) {
+      a.seq_tok[s] = tok + v[0];
+      a.own_out[s] = have + q;
+    }
+    __syncthreads();
+    put_pages(a, chunk, s0, n, page, page + total[1], used);
+    if (all) put_tokens(a, chunk, s0, n, tok, tok + total[0], used);
+    tok += total[0];
+    page += total[1];
+  }
+  if (tid == 0) a.seq_tok[a.S] = tok;
+  if (all) pad(a, tok, a.T);
 }
 
-// the tokens of a batch that kv_map_kernel has looked over
+// The tokens of a batch that kv_map_kernel has looked over, kMapThreads a
+// workgroup: token t of request s is key own_out[s] - (seq_tok[s + 1] - t).
+template <bool LDS>
 __global__ __launch_bounds__(kMapThreads) void kv_map_fill_kernel(MapArgs a) {
-  __shared__ int lds[2][kMapThreads / 64];
-  __shared__ Chunk chunk;
-  const int t0 = blockIdx.x * kMapThreads, t1 = min(a.T, t0 + kMapThreads);
-  const int tokens = a.status[1];
-  if (t0 < tokens) walk<false, false>(a, chunk, lds, a.used_out[0] - a.status[2], t0, min(t1, tokens));
-  pad(a, max(t0, tokens), t1);
+  __shared__ Groups groups;
+  __shared__ int32_t l_ptr[LDS ? kMapPtr + 1 : 1];
+  const int t = blockIdx.x * kMapThreads + threadIdx.x, tokens = a.status[1];
+  if (int(blockIdx.x) * kMapThreads < tokens) {
+    groups.load(a);
+    if (LDS)
+      for (int s = threadIdx.x; s <= a.S; s += kMapThreads) l_ptr[s] = a.seq_tok[s];
+    __syncthreads();
+  }
+  if (t >= a.T) return;
+  if (t >= tokens) {
+    a.pos[t] = 0;
+    a.slot[t] = -1;
+    return;
+  }
+  const int32_t *ptr = LDS ? l_ptr : a.seq_tok;
+  const int s = upper(ptr, a.S, t), key = a.own_out[s] - (ptr[s + 1] - t);
+  const int id = a.own_pages[int64_t(s) * a.ld + (key >> a.shift)];
+  a.pos[t] = groups.prefix_of(a, s) + key;
+  a.slot[t] = (int64_t(id) << a.shift) + (key & ((1 << a.shift) - 1));
 }
 
 bool misaligned(const void *p, uintptr_t m) { return reinterpret_cast<uintptr_t>(p) & (m - 1); }
@@ -223,8 +269,11 @@ extern "C" int tcl_kv_map(const tcl_kv_cache *c, const tcl_kv_batch *b, void *st
   hipLaunchKernelGGL(kv_map_kernel, dim3(1), dim3(kMapThreads), 0, s, a);
   TCL_HIP(hipGetLastError());
   if (a.T > kMapOne) {
-    hipLaunchKernelGGL(kv_map_fill_kernel, dim3((a.T + kMapThreads - 1) / kMapThreads), dim3(kMapThreads),
-                       0, s, a);
+    const dim3 grid((a.T + kMapThreads - 1) / kMapThreads);
+    if (a.S <= kMapPtr)
+      hipLaunchKernelGGL(kv_map_fill_kernel<true>, grid, dim3(kMapThreads), 0, s, a);
+    else
+      hipLaunchKernelGGL(kv_map_fill_kernel<false>, grid, dim3(kMapThreads), 0, s, a);
     TCL_HIP(hipGetLastError());
   }
   return TCL_OK;

@@ -77,7 +77,8 @@ def check(call, want, code=tclora.OK):
     (1, 1, 16, 1, 40, 0), (64, 8, 16, 1, 2048, 0), (3, 1, 1, 5, 9, 2), (64, 5, 64, 3, 300, 64),
     (1, 1, 1024, 5000, 0, 0), (7, 9, 128, 700, 1000, 1), (1023, 30, 16, 2, 60, 0),
     (1024, 1, 16, 4, 60, 3), (1025, 200, 32, 4, 60, 3), (3000, 2000, 16, 2, 40, 9),
-    (33, 2, 16, 900, 100, 5), (2500, 17, 16, 20, 100, 100)])
+    (33, 2, 16, 900, 100, 5), (2500, 17, 16, 20, 100, 100),
+    (9000, 1100, 16, 3, 30, 7), (8191, 3, 32, 2, 9, 0), (8192, 1025, 8, 3, 9, 700)])
 def test_map(S, G, page, new, own, pad):
     for seed in range(2):
         s = Step(S + seed, S, G, page, new, own, pad)
