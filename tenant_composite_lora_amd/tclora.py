@@ -1152,9 +1152,10 @@ class HeadNorm:
         self.desc = HeadNormDesc(_ptr(w_q), _ptr(w_k), *stride, self.eps)
 
     def fit(self, n_q_heads: int, n_kv_heads: int, head_dim: int) -> None:
-        """Checks the weights against a call's heads."""
+        """Checks the weights against a call's heads (n_q_heads 0: it has no
+        queries)."""
         for name, w, n in (("w_q", self.w_q, n_q_heads), ("w_k", self.w_k, n_kv_heads)):
-            if w is not None and tuple(w.shape) not in ((head_dim,), (n, head_dim)):
+            if w is not None and n and tuple(w.shape) not in ((head_dim,), (n, head_dim)):
                 raise ValueError(f"HeadNorm: {name} must be [{head_dim}] or [{n}, {head_dim}], got "
                                  f"{list(w.shape)}")
 
@@ -1248,8 +1249,8 @@ class MapCall:
                            ("own_len_out", own_len_out, S), ("used_out", used_out, 1)):
             if t is not None:
                 _vector(f"MapCall: {name}", t, n, torch.int32)
-        if T < 0:
-            raise ValueError("MapCall: n_tokens must not be negative")
+        if not 0 <= T < 1 << 31 or free_pages.numel() >= 1 << 31:
+            raise ValueError("MapCall: n_tokens and the list of free pages must be counts below 2^31")
         if own_pages.dtype != torch.int32:
             raise ValueError("MapCall: own_pages must be int32")
         ld = _rows("MapCall: own_pages", own_pages, S) if own_pages.numel() else 0

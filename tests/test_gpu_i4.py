@@ -164,6 +164,22 @@ def test_activations_with_an_offset(T):
     close(tclora.i4_linear(tclora.I4Weight(*w), x, y_dtype=torch.float32), *product64(w, n, x))
 
 
+@pytest.mark.parametrize("T", [3, 64, 200, 2048])
+@pytest.mark.parametrize("size", [1e-36, 1e-38, 3e-39, 1e30])
+def test_activations_at_the_ends_of_their_range(T, size):
+    """Next to and below the smallest normal number, with scales that bring the
+    results back; and large ones."""
+    w, n = weight(14, 4096 if T == 2048 else 264, 256, 64, True, full=True)
+    w[1].mul_(1e30 if size < 1 else 1e-25)
+    x = (acts(14, T, 256).double() * size).to(torch.bfloat16)
+    y, tol = product64(w, n, x)
+    # (what falls below 2^-149 in a sum is lost there: up to 2 L times, on both
+    # sides of the correction)
+    s = w[1].double().abs().sum(1)
+    close(tclora.i4_linear(tclora.I4Weight(*w), x, y_dtype=torch.float32), y,
+          tol + 2.0 ** -149 * 2 * 64 * (1 + 16 + 255) * s)
+
+
 def test_packed_copy_holds_the_weight():
     for d_out, d_in, group, zeros in ((40, 352, 32, True), (16, 128, 128, False), (8, 64, 64, True)):
         w, n = weight(6, d_out, d_in, group, zeros)

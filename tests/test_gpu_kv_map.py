@@ -246,7 +246,11 @@ def test_binding_refusals():
         a[i] = bad
         with pytest.raises(ValueError):
             tclora.kv_map(s.cache, *a, s.T)
-    with pytest.raises(ValueError):
-        tclora.kv_map(s.cache, *t, -1)
+    for n in (-1, 1 << 31, (1 << 32) + 5):
+        with pytest.raises(ValueError):
+            tclora.kv_map(s.cache, *t, n)
+    with pytest.raises(tclora.TclError) as e:
+        tclora.kv_map(s.cache, *t, 1 << 24)
+    assert e.value.code == tclora.EUNSUPPORTED
     with pytest.raises(ValueError):
         tclora.kv_map(s.cache, *t, s.T, own_len_out=t[3][:2])

@@ -125,6 +125,18 @@ def test_padding_strides_in_place():
     assert torch.equal(q, want)
 
 
+def test_weights_by_head_without_queries():
+    cache, (q, k, v), slot = make(12, 9, 6, 2, 64, 16, torch.bfloat16)
+    pos, rope = torch.arange(9, dtype=torch.int32, device=DEV), tclora.Rope(inv_freq(64))
+    norm = tclora.HeadNorm(*weights(12, 6, 2, 64, True))
+    tclora.kv_append(cache, k, v, pos, slot, rope, q=q, norm=norm)
+    K = cache.K.clone()
+    cache.K.zero_()
+    assert tclora.kv_append(cache, k, v, pos, slot, rope, norm=norm) is None
+    page, off = slot // 16, slot % 16
+    assert torch.equal(cache.K[page, off], K[page, off])
+
+
 def test_empty_batch():
     cache, (q, k, v), slot = make(9, 0, 4, 2, 64, 16, torch.bfloat16)
     out = tclora.kv_append(cache, k, v, slot.to(torch.int32), slot, q=q,
