@@ -339,17 +339,14 @@ __global__ __launch_bounds__(kMapThreads) void attn_plan_kernel(PlanArgs a) {
   if (work) atomicAdd(&s_work, work);  // (an integer sum: any order)
   if (WIN && many) atomicAdd(&s_many, many);
   __syncthreads();
-  if (tid < 3) {
-    auto length = [](unsigned long long keys, unsigned t) {
-      const unsigned long long r = ((keys + t - 1) / t + kKeys - 1) / kKeys * kKeys;
-      return r < kMinChunk ? kMinChunk : (r > 0x40000000ull ? 0x40000000 : int(r));
-    };
-    // Shared windows are cut as finely as few rows are, as long as that leaves
-    // no more items of many rows than their target, which the partial rows'
-    // capacity counts (64 requests of 8 tenants, windows of 4096: 106 us, 96).
-    s_chunk[tid] = tid == 0   ? length(s_work, a.target_few)
-                   : tid == 1 ? length(s_work, a.target_many)
-                              : max(length(s_work, a.target_few), length(s_many, a.target_many));
+  // Shared windows are cut as finely as few rows are, as long as that leaves no
+  // more items of many rows than their target, which the partial rows' capacity
+  // counts (64 requests of 8 tenants, windows of 4096: 106 us, 96).
+  if (tid < (WIN ? 3 : 2)) {
+    const unsigned t = tid ? a.target_many : a.target_few;
+    const unsigned long long k = tid < 2 ? s_work : s_many;
+    const unsigned long long r = ((k + t - 1) / t + kKeys - 1) / kKeys * kKeys;
+    s_chunk[tid] = r < kMinChunk ? kMinChunk : (r > 0x40000000ull ? 0x40000000 : int(r));
   }
   __syncthreads();
   // the units' first tiles
@@ -376,7 +373,8 @@ __global__ __launch_bounds__(kMapThreads) void attn_plan_kernel(PlanArgs a) {
     Cut c{unit_of(a, m, u), {}, i, 0, 0, 0};
     c.k = span_of<WIN>(a, m, c.x, i);
     const int len = c.k.hi - c.k.lo;
-    const int chunk = s_chunk[c.x.rows <= kFew ? 0 : WIN && c.x.list ? 2 : 1];
+    int chunk = s_chunk[c.x.rows > kFew];
+    if (WIN && c.x.rows > kFew && c.x.list) chunk = max(s_chunk[0], s_chunk[2]);
     c.nt = min(c.x.n_tok, (i + 1) * c.x.tpt) - i * c.x.tpt;
     c.ns = max(1, (len + chunk - 1) / chunk);
     // even lengths, whole steps
@@ -486,12 +484,13 @@ struct AttnArgs {
 };
 
 // the plan belongs to these sizes (a plan of other sizes: nothing is done)
+template <bool WIN>
 __device__ inline bool plan_fits(const AttnArgs &a) {
   const int32_t *h = a.hdr;
   return h[H_MAGIC] == kMagic && h[H_CODE] == TCL_OK && h[H_SEQS] == a.S && h[H_GROUPS] == a.G &&
          h[H_TOKENS] == a.T && h[H_HEADS] == a.Hq && h[H_KVHEADS] == a.c.H && h[H_DIM] == a.c.D &&
          h[H_PAGES] == a.c.n_pages && h[H_SHIFT] == a.c.page_shift && h[H_LDO] == a.ld_own &&
-         h[H_LDP] == a.ldp && h[H_WINDOW] == a.window && (!a.window || h[H_SINKS] == a.sinks) &&
+         h[H_LDP] == a.ldp && h[H_WINDOW] == (WIN ? a.window : 0) && (!WIN || h[H_SINKS] == a.sinks) &&
          pages_ok(h);
 }
 
@@ -1239,7 +1238,7 @@ __device__ inline void attend_many(const AttnArgs &a, const Work &t, int h, int 
 template <int D, bool WIN>
 __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_kernel(AttnArgs a) {
   __shared__ __align__(16) Smem<D> sm;
-  if (!plan_fits(a)) return;
+  if (!plan_fits<WIN>(a)) return;
   // (workgroups go to the XCDs in turn: with eight key heads each XCD's L2
   // holds one head)
   const int h = blockIdx.x % a.c.H, id = blockIdx.x / a.c.H;
@@ -1257,11 +1256,11 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_kernel(AttnArgs a)
 // Joins the items of a token's rows, a row a wave at a time: maxima first,
 // then the weighted sums in item order (own items, then the prefix's).  64
 // tokens of 32 heads, 16 items a row: 7 us for 17 MB, load latencies.
-template <int D>
+template <int D, bool WIN>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
   const int tk = blockIdx.x;
   const TokRec r = a.tok[tk];
-  if (!plan_fits(a) || r.vis < 0 || !r.join) return;
+  if (!plan_fits<WIN>(a) || r.vis < 0 || !r.join) return;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int gq = a.Hq / a.c.H;
   constexpr int E = D / 64;
@@ -1410,13 +1409,16 @@ int check_window(int32_t window, int32_t sinks) {
 template <int D>
 void launch(const AttnArgs &a, int cap_items, hipStream_t s) {
   const dim3 grid(unsigned(cap_items) * a.c.H);
-  if (a.window)
-    hipLaunchKernelGGL((attn_kernel<D, true>), grid, dim3(256), 0, s, a);
-  else
-    hipLaunchKernelGGL((attn_kernel<D, false>), grid, dim3(256), 0, s, a);
   // a row a wave, until that is eight workgroups a CU and more
   const int by_row = (a.Hq + 3) / 4, parts = a.T >= 2048 ? 1 : std::min(by_row, 4096 / a.T + 1);
-  hipLaunchKernelGGL(attn_join_kernel<D>, dim3(a.T, parts), dim3(256), 0, s, a);
+  const dim3 join(a.T, parts);
+  if (a.window) {
+    hipLaunchKernelGGL((attn_kernel<D, true>), grid, dim3(256), 0, s, a);
+    hipLaunchKernelGGL((attn_join_kernel<D, true>), join, dim3(256), 0, s, a);
+  } else {
+    hipLaunchKernelGGL((attn_kernel<D, false>), grid, dim3(256), 0, s, a);
+    hipLaunchKernelGGL((attn_join_kernel<D, false>), join, dim3(256), 0, s, a);
+  }
 }
 
 }  // namespace
