@@ -688,7 +688,8 @@ typedef struct {
 int tcl_i4_pack_bytes(const tcl_i4_weight *w, size_t *bytes);
 int tcl_i4_pack(tcl_i4_weight *w, void *W_p, size_t bytes, void *stream);
 
-/* Device workspace of tcl_i4_linear (host only); none for up to 16 tokens. */
+/* Device workspace of tcl_i4_linear (host only); 0 bytes where it needs none,
+ * as for up to 16 tokens.  Fewer tokens may need more than more do. */
 int tcl_i4_workspace_bytes(const tcl_i4_weight *w, int32_t n_tokens, size_t *bytes);
 
 /*

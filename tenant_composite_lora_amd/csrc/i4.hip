@@ -10,12 +10,15 @@
 // takes one fused operation an output and group, in fp32, and a short product
 // of fp32 numbers in bf16 parts.  No weight is rounded.
 //
-// Three kernels:
-//   i4_rows    up to 16 tokens, straight from their rows, one launch;
-//   i4_blocks  more: the activations are laid out first (i4_stage_kernel); the
-//              weight streams from memory into matrix-core operands, the waves
-//              of a workgroup split d_in and add their sums in LDS;
-//   i4_tile    many: tiles of both operands go through LDS.
+// Four kernels (choose):
+//   i4_rows    up to 16 tokens: the weight streams from memory into matrix-core
+//              operands, the waves of a workgroup split d_in and add their sums
+//              in LDS;
+//   i4_direct  more, in tiles of 32: likewise, x turned in LDS;
+//   i4_blocks  wide outputs: likewise, after a launch that lays x out in operands
+//              and sums it over the groups (i4_stage_kernel);
+//   i4_tile    many tokens, from laid-out activations: tiles of both operands go
+//              through LDS.
 //
 // The packed weight holds blocks of 32 channels by 64 columns, 1 KiB, 16 bytes a
 // lane: lane l has channel l % 32 and, in its dwords 0..3, the eights of columns
@@ -24,12 +27,15 @@
 // and 2 j + 1 of an eight lie at bits 3 + 4 j and 19 + 4 j, those beyond bit 31
 // at its start.  Behind the blocks come the scales, 32 channels of a group side
 // by side, and the zero points likewise.
+#include <algorithm>
 #include <type_traits>
 
 #include "kern_common.hpp"
 
 namespace tcl {
 namespace {
+
+constexpr int kWaves = 8;  // a workgroup's, but in i4_tile
 
 struct I4Args {
   const uint8_t *w;       // packed blocks
@@ -44,7 +50,7 @@ struct I4Args {
   const float *xe;        // and their groups' sums
   int32_t steps;          // corrections of four groups
   int32_t nt, nc;         // tiles of tokens, of channels
-  int32_t ks;             // workgroups that share a tile's columns (i4_blocks)
+  int32_t ks;             // workgroups that share a tile's columns (i4_direct)
   float *part;            // [ks][T][N], where ks > 1
   bool y_f32;
 };
@@ -248,24 +254,22 @@ __device__ inline void stream(int first, int step, int n, F block) {
     if (b + d * step < n) block(d, b + d * step, std::false_type{});
 }
 
-// Few tokens, straight from x.  16 NB channels by 16 MT tokens; wave w of WV
-// takes the blocks w, w + WV, ... of 128 columns.  Tokens are the rows of a
+// Few tokens, straight from x.  16 NB channels a workgroup; wave w of WV takes
+// the blocks w, w + WV, ... of 128 columns.  Tokens are the rows of a
 // result, so that a lane holds one channel, its scale and zero point; the sums
 // of x come from an operand of ones.  GS: groups of a block (4, 2, 1; 1 also
 // for groups of several blocks).
-template <int MT, int NB, int WV, int GS, bool ZP>
-__global__ __launch_bounds__(64 * WV) void i4_rows(I4Args a) {
+template <int NB, int GS, bool ZP>
+__global__ __launch_bounds__(64 * kWaves) void i4_rows(I4Args a) {
   const Widen widen;
   constexpr int AHEAD = NB > 2 ? 2 : 4;  // blocks on their way
-  constexpr int LD = 16 * NB + 4;
+  constexpr int WV = kWaves, LD = 16 * NB + 4;
   __shared__ __align__(16) float part[WV * 16 * LD];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
-  const int c0 = blockIdx.x * 16 * NB, t0 = blockIdx.y * 16 * MT;
+  const int c0 = blockIdx.x * 16 * NB;
   const int tiles = (a.N + 15) / 16;
-  const uint16_t *xp[MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) xp[m] = a.x + int64_t(min(t0 + 16 * m + c, a.T - 1)) * a.ldx + 8 * g;
+  const uint16_t *xp = a.x + int64_t(min(c, a.T - 1)) * a.ldx + 8 * g;
   const uint8_t *wp[NB];
   const float *sp[NB];
   const uint8_t *zp[NB];
@@ -278,14 +282,12 @@ __global__ __launch_bounds__(64 * WV) void i4_rows(I4Args a) {
     sp[n] = a.scale + t32 * a.groups * 32 + (ct & 1) * 16 + c;
     zp[n] = ZP ? a.zero + t32 * a.groups * 32 + (ct & 1) * 16 + c : nullptr;
   }
-  f32x4_t acc[MT][NB];
+  f32x4_t acc[NB];
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int n = 0; n < NB; ++n) acc[m][n] = f32x4_t{0, 0, 0, 0};
+  for (int n = 0; n < NB; ++n) acc[n] = f32x4_t{0, 0, 0, 0};
   // (operands are replaced as in i4_blocks)
   nt_u2 wq[AHEAD][NB][2];
-  nt_u4 xr[AHEAD][MT][4];
+  nt_u4 xr[AHEAD][4];
   float s[AHEAD][NB][GS], z[AHEAD][NB][GS];
   auto load_w = [&](int d, int n, int k, int b) {
     wq[d][n][k] = *reinterpret_cast<const nt_u2 *>(wp[n] + int64_t(min(b, a.kb - 1)) * 2048 + 1024 * k);
@@ -298,10 +300,10 @@ __global__ __launch_bounds__(64 * WV) void i4_rows(I4Args a) {
       z[d][n][e] = ZP ? 16.f + float(zp[n][gr * 32]) : 24.f;
     }
   };
-  auto load_x = [&](int d, int m, int i, int b) {
+  auto load_x = [&](int d, int i, int b) {
     // (columns past the row's end: any of it)
     const int k = b * 128 + 32 * i;
-    xr[d][m][i] = *reinterpret_cast<const nt_u4 *>(xp[m] + (k < a.K ? k : 0));
+    xr[d][i] = *reinterpret_cast<const nt_u4 *>(xp + (k < a.K ? k : 0));
   };
 #pragma unroll
   for (int d = 0; d < AHEAD; ++d) {
@@ -309,58 +311,49 @@ __global__ __launch_bounds__(64 * WV) void i4_rows(I4Args a) {
 #pragma unroll
     for (int n = 0; n < NB; ++n) load_w(d, n, 0, b), load_w(d, n, 1, b), load_s(d, n, b);
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) load_x(d, m, i, b);
+    for (int i = 0; i < 4; ++i) load_x(d, i, b);
     __builtin_amdgcn_sched_barrier(0);
   }
   // block b from slot d, which block b + AHEAD * WV then takes
   auto block = [&](int d, int b, auto more) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int e = 0; e < GS; ++e) {
+      f32x4_t sum = {0, 0, 0, 0}, p[NB];
 #pragma unroll
-      for (int e = 0; e < GS; ++e) {
-        f32x4_t sum = {0, 0, 0, 0}, p[NB];
+      for (int n = 0; n < NB; ++n) p[n] = f32x4_t{0, 0, 0, 0};
 #pragma unroll
-        for (int n = 0; n < NB; ++n) p[n] = f32x4_t{0, 0, 0, 0};
+      for (int i = 4 / GS * e; i < 4 / GS * (e + 1); ++i) {
+        // columns past the row's end: zeros (here, not where they are read,
+        // which would wait for them)
+        const bf16x8_t x = as_bf16(b * 128 + 32 * i < a.K ? xr[d][i] : nt_u4{0, 0, 0, 0});
+        sum = mfma(x, ones(), sum);
 #pragma unroll
-        for (int i = 4 / GS * e; i < 4 / GS * (e + 1); ++i) {
-          // columns past the row's end: zeros (here, not where they are read,
-          // which would wait for them)
-          const bf16x8_t x = as_bf16(b * 128 + 32 * i < a.K ? xr[d][m][i] : nt_u4{0, 0, 0, 0});
-          sum = mfma(x, ones(), sum);
+        for (int n = 0; n < NB; ++n) p[n] = mfma(x, widen(wq[d][n][i >> 1][i & 1]), p[n]);
+        if constexpr (more) {
+          load_x(d, i, b + AHEAD * WV);
+          if (i % 2 == 1)
 #pragma unroll
-          for (int n = 0; n < NB; ++n)
-            p[n] = mfma(x, widen(wq[d][n][i >> 1][i & 1]), p[n]);
-          if constexpr (more) {
-            load_x(d, m, i, b + AHEAD * WV);
-            if (m == MT - 1 && i % 2 == 1)
-#pragma unroll
-              for (int n = 0; n < NB; ++n) load_w(d, n, i / 2, b + AHEAD * WV);
-          }
-          __builtin_amdgcn_sched_barrier(0);
+            for (int n = 0; n < NB; ++n) load_w(d, n, i / 2, b + AHEAD * WV);
         }
-#pragma unroll
-        for (int n = 0; n < NB; ++n)
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            acc[m][n][r] = fmaf(s[d][n][e], fmaf(-z[d][n][e], sum[r], p[n][r]), acc[m][n][r]);
+        __builtin_amdgcn_sched_barrier(0);
       }
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          acc[n][r] = fmaf(s[d][n][e], fmaf(-z[d][n][e], sum[r], p[n][r]), acc[n][r]);
+    }
     if constexpr (more)
 #pragma unroll
       for (int n = 0; n < NB; ++n) load_s(d, n, b + AHEAD * WV);
   };
   stream<AHEAD>(w, WV, a.kb, block);
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    if (m) __syncthreads();
+  for (int n = 0; n < NB; ++n)
 #pragma unroll
-    for (int n = 0; n < NB; ++n)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) part[(w * 16 + 4 * g + r) * LD + 16 * n + c] = acc[m][n][r];
-    __syncthreads();
-    add_up<16, NB, LD, WV>(a, part, t0 + 16 * m, c0, [&](int t, int ch, nt_f4 v) { store4(a, t, ch, v); });
-  }
+    for (int r = 0; r < 4; ++r) part[(w * 16 + 4 * g + r) * LD + 16 * n + c] = acc[n][r];
+  __syncthreads();
+  add_up<16, NB, LD, WV>(a, part, 0, c0, [&](int t, int ch, nt_f4 v) { store4(a, t, ch, v); });
 }
 
 // The row of a 32 x 32 result that element e of a lane of half h holds.
@@ -369,28 +362,21 @@ __device__ inline int row_of(int e, int h) { return 8 * (e / 4) + 4 * h + e % 4;
 // The position in a packed lane of columns 16 i ..
 __device__ inline constexpr int place(int i) { return (i & 1) << 1 | i >> 1; }
 
-// More tokens, from staged activations: 32 NB channels by 32 MT tokens, the
-// blocks dealt out to the waves as in i4_rows, then the corrections.
-template <int MT, int NB, int WV, int GS, bool ZP>
-__global__ __launch_bounds__(64 * WV) void i4_blocks(I4Args a) {
+// More tokens, from staged activations: 32 NB channels by 32 tokens, the blocks
+// dealt out to the waves as in i4_rows, then the corrections.
+template <int NB, int GS, bool ZP>
+__global__ __launch_bounds__(64 * kWaves) void i4_blocks(I4Args a) {
   const Widen widen;
-  constexpr int AHEAD = 1;  // blocks on their way
-  constexpr int LD = 32 * NB + 8;
+  constexpr int WV = kWaves, LD = 32 * NB + 8;
   __shared__ __align__(16) float part[WV * 32 * LD];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 31, h = lane >> 5;
   const int nx = (a.N + 32 * NB - 1) / (32 * NB);
-  const int c0 = blockIdx.x % nx * 32 * NB, t0 = blockIdx.x / nx * 32 * MT;
-  const int first = blockIdx.y * WV + w, stride = a.ks * WV;
-  const int tiles = (a.N + 31) / 32, tt = (a.T + 31) / 32;
-  const nt_u4 *xp[MT];
-  const float *ep[MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int64_t tile = min(t0 / 32 + m, tt - 1);
-    xp[m] = a.xb + tile * a.kb * 512 + lane;
-    ep[m] = a.xe + tile * a.steps * 128 + lane;
-  }
+  const int c0 = blockIdx.x % nx * 32 * NB, t0 = blockIdx.x / nx * 32;
+  const int tiles = (a.N + 31) / 32;
+  const int64_t tile = t0 / 32;
+  const nt_u4 *xp = a.xb + tile * a.kb * 512;
+  const float *ep = a.xe + tile * a.steps * 128 + lane;
   const nt_u4 *wp[NB];
   const float *sp[NB];
   const uint8_t *zp[NB];
@@ -398,103 +384,187 @@ __global__ __launch_bounds__(64 * WV) void i4_blocks(I4Args a) {
   for (int n = 0; n < NB; ++n) {
     // (channel tiles past the last: the last one again, not stored)
     const int64_t ct = min(c0 / 32 + n, tiles - 1);
-    wp[n] = reinterpret_cast<const nt_u4 *>(a.w) + ct * a.kb * 128 + lane;
-    sp[n] = a.scale + ct * a.groups * 32 + c;
-    zp[n] = ZP ? a.zero + ct * a.groups * 32 + c : nullptr;
+    wp[n] = reinterpret_cast<const nt_u4 *>(a.w) + ct * a.kb * 128;
+    sp[n] = a.scale + ct * a.groups * 32;
+    zp[n] = ZP ? a.zero + ct * a.groups * 32 : nullptr;
   }
-  f32x16_t acc[MT][NB];
+  f32x16_t acc[NB];
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int n = 0; n < NB; ++n) acc[m][n] = nothing();
-  // A block's operands, each replaced by that of AHEAD blocks on as soon as its
+  for (int n = 0; n < NB; ++n) acc[n] = nothing();
+  // A block's operands, each replaced by that of the next as soon as its
   // products have been issued: loads are always on their way, and no register
   // waits for them twice.  Activations as far ahead as weights, although they
   // come from L2: loads are waited for in the order of their issue.  (The
   // scheduling barriers hold the loads there; left to itself the compiler puts
   // them right before their use.)
-  nt_u4 wq[AHEAD][NB][2], xr[AHEAD][MT][8];
-  float s[AHEAD][NB][GS];
-  auto load_w = [&](int d, int n, int k, int b) {
-    wq[d][n][k] = wp[n][int64_t(min(b, a.kb - 1)) * 128 + 64 * k];
+  nt_u4 wq[NB][2], xr[8];
+  float s[NB][GS];
+  auto load_w = [&](int n, int k, int b) { wq[n][k] = (wp[n] + int64_t(min(b, a.kb - 1)) * 128 + 64 * k)[lane]; };
+  auto load_s = [&](int n, int b) {
+#pragma unroll
+    for (int e = 0; e < GS; ++e) s[n][e] = (sp[n] + group_at<GS>(a, min(b, a.kb - 1), e) * 32)[c];
   };
-  auto load_s = [&](int d, int n, int b) {
+  auto load_x = [&](int i, int b) { xr[i] = (xp + int64_t(min(b, a.kb - 1)) * 512 + 64 * i)[lane]; };
 #pragma unroll
-    for (int e = 0; e < GS; ++e) s[d][n][e] = sp[n][group_at<GS>(a, min(b, a.kb - 1), e) * 32];
-  };
-  auto load_x = [&](int d, int m, int i, int b) {
-    xr[d][m][i] = xp[m][int64_t(min(b, a.kb - 1)) * 512 + 64 * i];
-  };
+  for (int n = 0; n < NB; ++n) load_w(n, 0, w), load_w(n, 1, w), load_s(n, w);
 #pragma unroll
-  for (int d = 0; d < AHEAD; ++d) {
-    const int b = first + d * stride;
+  for (int i = 0; i < 8; ++i) load_x(i, w);
+  __builtin_amdgcn_sched_barrier(0);
+  auto block = [&](int, int b, auto more) {
 #pragma unroll
-    for (int n = 0; n < NB; ++n) load_w(d, n, 0, b), load_w(d, n, 1, b), load_s(d, n, b);
+    for (int e = 0; e < GS; ++e) {
+      f32x16_t p[NB];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+      for (int n = 0; n < NB; ++n) p[n] = nothing();
 #pragma unroll
-      for (int i = 0; i < 8; ++i) load_x(d, m, i, b);
-    __builtin_amdgcn_sched_barrier(0);
-  }
-  auto block = [&](int d, int b, auto more) {
+      for (int i = 8 / GS * e; i < 8 / GS * (e + 1); ++i) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+        for (int n = 0; n < NB; ++n) p[n] = mfma(as_bf16(xr[i]), widen(wq[n][i / 4][place(i % 4)]), p[n]);
+        if constexpr (more) {
+          load_x(i, b + WV);
+          if (i % 4 == 3)
 #pragma unroll
-      for (int e = 0; e < GS; ++e) {
-        f32x16_t p[NB];
-#pragma unroll
-        for (int n = 0; n < NB; ++n) p[n] = nothing();
-#pragma unroll
-        for (int i = 8 / GS * e; i < 8 / GS * (e + 1); ++i) {
-#pragma unroll
-          for (int n = 0; n < NB; ++n)
-            p[n] = mfma(as_bf16(xr[d][m][i]), widen(wq[d][n][i / 4][place(i % 4)]), p[n]);
-          if constexpr (more) {
-            load_x(d, m, i, b + AHEAD * stride);
-            if (m == MT - 1 && i % 4 == 3)
-#pragma unroll
-              for (int n = 0; n < NB; ++n) load_w(d, n, i / 4, b + AHEAD * stride);
-          }
-          __builtin_amdgcn_sched_barrier(0);
+            for (int n = 0; n < NB; ++n) load_w(n, i / 4, b + WV);
         }
-#pragma unroll
-        for (int n = 0; n < NB; ++n)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) acc[m][n][r] = fmaf(s[d][n][e], p[n][r], acc[m][n][r]);
+        __builtin_amdgcn_sched_barrier(0);
       }
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[n][r] = fmaf(s[n][e], p[n][r], acc[n][r]);
+    }
     if constexpr (more)
 #pragma unroll
-      for (int n = 0; n < NB; ++n) load_s(d, n, b + AHEAD * stride);
+      for (int n = 0; n < NB; ++n) load_s(n, b + WV);
   };
-  stream<AHEAD>(first, stride, a.kb, block);
+  stream<1>(w, WV, a.kb, block);
   // (two groups a step: a half each; groups behind the last meet sums of zero)
-  for (int st = first; st < 2 * a.steps; st += stride) {
+  for (int st = w; st < 2 * a.steps; st += WV) {
     const int gr = min(GS == 1 ? group_of(a, 2 * st + h) : 2 * st + h, a.groups - 1);
-    bf16x8_t f[NB];
-#pragma unroll
-    for (int n = 0; n < NB; ++n) f[n] = parts_w(-sp[n][gr * 32] * (ZP ? 16.f + float(zp[n][gr * 32]) : 24.f));
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const bf16x8_t x = parts_x(ep[m][int64_t(st) * 64]);
-#pragma unroll
-      for (int n = 0; n < NB; ++n) acc[m][n] = mfma(x, f[n], acc[m][n]);
-    }
-  }
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    if (m) __syncthreads();
+    const bf16x8_t x = parts_x(ep[int64_t(st) * 64]);
 #pragma unroll
     for (int n = 0; n < NB; ++n)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) part[(w * 32 + row_of(r, h)) * LD + 32 * n + c] = acc[m][n][r];
-    __syncthreads();
-    add_up<32, 2 * NB, LD, WV>(a, part, t0 + 32 * m, c0, [&](int t, int ch, nt_f4 v) {
-      if (a.ks == 1)
-        store4(a, t, ch, v);
-      else
-        *reinterpret_cast<nt_f4 *>(a.part + ((int64_t(blockIdx.y) * a.T + t) * a.N + ch)) = v;
-    });
+      acc[n] = mfma(x, parts_w(-sp[n][gr * 32 + c] * (ZP ? 16.f + float(zp[n][gr * 32 + c]) : 24.f)), acc[n]);
   }
+#pragma unroll
+  for (int n = 0; n < NB; ++n)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) part[(w * 32 + row_of(r, h)) * LD + 32 * n + c] = acc[n][r];
+  __syncthreads();
+  add_up<32, 2 * NB, LD, WV>(a, part, t0, c0, [&](int t, int ch, nt_f4 v) { store4(a, t, ch, v); });
+}
+
+// The same without a launch that lays out the activations: a wave reads its
+// block of them in rows of 256 bytes, a block ahead, and turns it in LDS; the
+// sums of x come from an operand of ones.  32 NB channels by 32 tokens; with
+// ks > 1 as many workgroups, blockIdx.y, share their columns.
+template <int NB, int GS, bool ZP>
+__global__ __launch_bounds__(64 * kWaves) void i4_direct(I4Args a) {
+  const Widen widen;
+  constexpr int WV = kWaves, LD = 32 * NB + 8;
+  __shared__ __align__(16) union {
+    float part[WV * 32 * LD];
+    nt_u4 x[WV][32 * 16];  // chunk c of row r at 16 r + (c ^ r % 16)
+  } l;
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane & 31, h = lane >> 5;
+  const int nx = (a.N + 32 * NB - 1) / (32 * NB);
+  const int c0 = blockIdx.x % nx * 32 * NB, t0 = blockIdx.x / nx * 32;
+  const int first = blockIdx.y * WV + w, stride = a.ks * WV;
+  const int tiles = (a.N + 31) / 32;
+  const nt_u4 *wp[NB];
+  const float *sp[NB];
+  const uint8_t *zp[NB];
+#pragma unroll
+  for (int n = 0; n < NB; ++n) {
+    // (channel tiles past the last: the last one again, not stored)
+    const int64_t ct = min(c0 / 32 + n, tiles - 1);
+    wp[n] = reinterpret_cast<const nt_u4 *>(a.w) + ct * a.kb * 128;
+    sp[n] = a.scale + ct * a.groups * 32;
+    zp[n] = ZP ? a.zero + ct * a.groups * 32 : nullptr;
+  }
+  f32x16_t acc[NB];
+#pragma unroll
+  for (int n = 0; n < NB; ++n) acc[n] = nothing();
+  nt_u4 wq[NB][2], xr[8];
+  float s[NB][GS], z[NB][GS];
+  const int row = lane >> 4, chunk = lane & 15;
+  auto load_w = [&](int n, int k, int b) { wq[n][k] = (wp[n] + int64_t(min(b, a.kb - 1)) * 128 + 64 * k)[lane]; };
+  auto load_s = [&](int n, int b) {
+#pragma unroll
+    for (int e = 0; e < GS; ++e) {
+      const int gr = group_at<GS>(a, min(b, a.kb - 1), e);
+      s[n][e] = (sp[n] + gr * 32)[c];
+      z[n][e] = ZP ? 16.f + float((zp[n] + gr * 32)[c]) : 24.f;
+    }
+  };
+  auto load_x = [&](int j, int b) {
+    // (columns past the row's end: any of it; rows past the last: the last)
+    const int k = b * 128 + 8 * chunk;
+    xr[j] = *reinterpret_cast<const nt_u4 *>(a.x + int64_t(min(t0 + 4 * j + row, a.T - 1)) * a.ldx +
+                                             (k < a.K ? k : 0));
+  };
+#pragma unroll
+  for (int j = 0; j < 8; ++j) load_x(j, first);
+#pragma unroll
+  for (int n = 0; n < NB; ++n) load_w(n, 0, first), load_w(n, 1, first), load_s(n, first);
+  auto block = [&](int, int b, auto more) {
+    const bool in = b * 128 + 8 * chunk < a.K;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int r = 4 * j + row;
+      l.x[w][16 * r + (chunk ^ (r & 15))] = in ? xr[j] : nt_u4{0, 0, 0, 0};
+      if constexpr (more) load_x(j, b + stride);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int e = 0; e < GS; ++e) {
+      f32x16_t sum = nothing();
+      f32x16_t p[NB];
+#pragma unroll
+      for (int n = 0; n < NB; ++n) p[n] = nothing();
+      nt_u4 xo[2];
+      auto read = [&](int i) { xo[i & 1] = l.x[w][16 * c + ((2 * i + h) ^ (c & 15))]; };
+      read(8 / GS * e);
+#pragma unroll
+      for (int i = 8 / GS * e; i < 8 / GS * (e + 1); ++i) {
+        if (i + 1 < 8 / GS * (e + 1)) read(i + 1);
+        const bf16x8_t x = as_bf16(xo[i & 1]);
+        sum = mfma(x, ones(), sum);
+#pragma unroll
+        for (int n = 0; n < NB; ++n) p[n] = mfma(x, widen(wq[n][i / 4][place(i % 4)]), p[n]);
+        if constexpr (more)
+          if (i % 4 == 3)
+#pragma unroll
+            for (int n = 0; n < NB; ++n) load_w(n, i / 4, b + stride);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          acc[n][r] = fmaf(s[n][e], fmaf(-z[n][e], sum[r], p[n][r]), acc[n][r]);
+    }
+    if constexpr (more)
+#pragma unroll
+      for (int n = 0; n < NB; ++n) load_s(n, b + stride);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  stream<1>(first, stride, a.kb, block);
+  __syncthreads();  // (the waves' activations lie where their sums go)
+#pragma unroll
+  for (int n = 0; n < NB; ++n)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) l.part[(w * 32 + row_of(r, h)) * LD + 32 * n + c] = acc[n][r];
+  __syncthreads();
+  add_up<32, 2 * NB, LD, WV>(a, l.part, t0, c0, [&](int t, int ch, nt_f4 v) {
+    if (a.ks == 1)
+      store4(a, t, ch, v);
+    else
+      *reinterpret_cast<nt_f4 *>(a.part + ((int64_t(blockIdx.y) * a.T + t) * a.N + ch)) = v;
+  });
 }
 
 // Adds the parts of the workgroups that shared columns, in order.
@@ -722,22 +792,26 @@ constexpr int kMaxChannels = 1 << 26, kMaxTokens = 1 << 24;
 constexpr int kRows = 16;
 
 // Which kernel.  Measured on captured calls with weights from memory, groups of
-// 128, us, staging included; d_in 4096 unless said.
+// 128, us, staging and joins included; d_in 4096 unless said.
 //   i4_rows, as many channels a workgroup as leave 192 of them: 1 token, 1024
 //     channels: 16 channels 4.5, 32 5.7; 4096 channels 4.9, 6.1; 14336: 16
 //     channels 10.6, 64 8.7 (16 tokens: 19.1, 9.9).
-//   i4_blocks likewise: 64 tokens, 4096 channels: 32 channels a workgroup 10.9,
-//     64 11.8, 128 15.2; 14336: 22.9, 23.0, 17.6; 23 tokens, 14336: 15.0, 13.1,
-//     16.4.  What bounds it is what a CU takes in, some 60 GB/s each, so that
-//     few workgroups with long rows are split over d_in and joined by a launch
-//     more: 23 tokens, 4096 channels, d_in 14336: whole 23.3, in four 17.8; d_in
-//     4096 10.3 and 11.6.
-//   Tiles by whole rounds over the CUs (half_us): 512 tokens, 4096 channels:
-//     blocks 29.8, tiles of 64 tokens 43.2, of 128 60.1; 1024: 53.5, 50.2, 62.2;
-//     2048: 103, 98, 83; 512 x 14336: 91.7, 84.9, 68.8.
+//   The others by whole rounds over the CUs (half_us: one workgroup a CU).
+//     i4_direct, 32 channels a workgroup, 64, i4_blocks with 128: 64 tokens,
+//     4096 channels 8.7, 9.8, 15.1; 32 x 14336 15.1, 11.3, 16.8; 64 x 14336
+//     31.2, 21.1, 19.0 (i4_blocks with 32 or 64, that is the launch that lays
+//     out the activations: 11.2 and 12.1, 16.1 and 13.9, 24.0 and 21.6).
+//     i4_blocks, i4_tile of 64 tokens, of 128: 512 tokens, 4096 channels 29.8,
+//     43.2, 60.1; 1024: 53.5, 50.2, 62.2; 2048: 103, 98, 83; 512 x 14336: 91.7,
+//     84.9, 68.8.
+//   What bounds all of these is what a CU takes in, some 60 GB/s each, so that
+//     few workgroups with long rows are split over d_in (ks) and joined by a
+//     launch more.  d_in 14336: 23 tokens, 4096 channels 19.7, in two 15.6; 32,
+//     2048 channels 18.8, in four 11.8; 64, 4096 channels 23.7, in two of 64
+//     channels 20.8.  d_in 4096: 17 tokens, 1024 channels 7.3, in eight 7.4.
 struct Choice {
-  enum { kFew, kBlocks, kTile64, kTile128 } kernel;
-  int nb;  // 16 (few) or 32 (blocks) channels a workgroup times this
+  enum { kFew, kDirect, kBlocks, kTile64, kTile128 } kernel;
+  int nb;  // 16 (few) or 32 (direct) channels a workgroup times this
   int ks;
 };
 
@@ -747,17 +821,20 @@ Choice choose(int32_t n_tokens, int32_t d_out, int32_t kb) {
   const int64_t T = n_tokens, N = d_out;
   auto over = [](int64_t n, int64_t d) { return (n + d - 1) / d; };
   if (T <= kRows) return {Choice::kFew, over(N, 64) >= 192 ? 4 : over(N, 32) >= 192 ? 2 : 1, 1};
-  const int64_t tb = over(T, 32), w2 = tb * over(N, 64), w4 = tb * over(N, 128);
-  if (w4 >= 192) {
-    const int64_t half_us[3] = {10 + 24 * rounds(w4), 16 + 80 * rounds(over(T, 64) * over(N, 256)),
-                                10 + 132 * rounds(over(T, 128) * over(N, 256))};
-    if (half_us[0] <= half_us[1] && half_us[0] <= half_us[2]) return {Choice::kBlocks, 4, 1};
-    return {half_us[1] < half_us[2] ? Choice::kTile64 : Choice::kTile128, 0, 1};
+  const int64_t tb = over(T, 32), w1 = tb * over(N, 32), w2 = tb * over(N, 64);
+  if (kb >= 64 && w2 <= 128)
+    return w1 <= 128 ? Choice{Choice::kDirect, 1, int(std::min<int64_t>(256 / w1, kb / 8))}
+                     : Choice{Choice::kDirect, 2, 2};
+  const int64_t half_us[5] = {3 + 14 * rounds(w1), 3 + 19 * rounds(w2), 10 + 24 * rounds(tb * over(N, 128)),
+                              16 + 80 * rounds(over(T, 64) * over(N, 256)),
+                              10 + 132 * rounds(over(T, 128) * over(N, 256))};
+  switch (std::min_element(half_us, half_us + 5) - half_us) {
+    case 0: return {Choice::kDirect, 1, 1};
+    case 1: return {Choice::kDirect, 2, 1};
+    case 2: return {Choice::kBlocks, 4, 1};
+    case 3: return {Choice::kTile64, 0, 1};
+    default: return {Choice::kTile128, 0, 1};
   }
-  if (w2 >= 192) return {Choice::kBlocks, 2, 1};
-  // (a wave keeps two blocks at least)
-  const int64_t ks = kb < 64 ? 1 : 256 / w2 < kb / 16 ? 256 / w2 : kb / 16;
-  return {Choice::kBlocks, ks > 1 ? 2 : 1, int(ks < 1 ? 1 : ks)};
 }
 
 struct Layout {
@@ -790,29 +867,20 @@ int check_weight(const tcl_i4_weight *w, Layout *l) {
   return TCL_OK;
 }
 
-template <int MT, int NB, int WV, int GS, bool ZP>
+template <int NB, int GS, bool ZP>
 void go_rows(const I4Args &a, hipStream_t s) {
-  hipLaunchKernelGGL((i4_rows<MT, NB, WV, GS, ZP>),
-                     dim3((a.N + 16 * NB - 1) / (16 * NB), (a.T + 16 * MT - 1) / (16 * MT)), dim3(64 * WV), 0,
-                     s, a);
+  hipLaunchKernelGGL((i4_rows<NB, GS, ZP>), dim3((a.N + 16 * NB - 1) / (16 * NB)), dim3(64 * kWaves), 0, s, a);
 }
 
-template <int MT, int NB, int WV, int GS, bool ZP>
-void go_blocks(const I4Args &a, hipStream_t s) {
-  hipLaunchKernelGGL((i4_blocks<MT, NB, WV, GS, ZP>),
-                     dim3(unsigned((a.N + 32 * NB - 1) / (32 * NB)) * ((a.T + 32 * MT - 1) / (32 * MT)), a.ks),
-                     dim3(64 * WV), 0, s, a);
+template <int NB, int GS, bool ZP>
+void go_direct(const I4Args &a, hipStream_t s) {
+  hipLaunchKernelGGL((i4_direct<NB, GS, ZP>),
+                     dim3(unsigned((a.N + 32 * NB - 1) / (32 * NB)) * ((a.T + 31) / 32), a.ks), dim3(64 * kWaves),
+                     0, s, a);
   if (a.ks > 1) {
     const int64_t n = (int64_t(a.T) * a.N / 4 + 255) / 256;
     hipLaunchKernelGGL(i4_join_kernel, dim3(unsigned(n < 2048 ? n : 2048)), dim3(256), 0, s, a);
   }
-}
-
-template <int BT, int WC, int GS, bool ZP>
-void go_tile(I4Args a, hipStream_t s) {
-  a.nt = (a.T + BT - 1) / BT;
-  a.nc = (a.N + 255) / 256;
-  hipLaunchKernelGGL((i4_tile<BT, WC, GS, ZP>), dim3((a.nt * a.nc + 7) / 8 * 8), dim3(512), 0, s, a);
 }
 
 template <int GS>
@@ -823,28 +891,35 @@ void go_stage(const I4Args &a, hipStream_t s) {
 }
 
 template <int GS, bool ZP>
+void go_blocks(const I4Args &a, hipStream_t s) {
+  go_stage<GS>(a, s);
+  hipLaunchKernelGGL((i4_blocks<4, GS, ZP>), dim3(unsigned((a.N + 127) / 128) * ((a.T + 31) / 32)),
+                     dim3(64 * kWaves), 0, s, a);
+}
+
+template <int BT, int GS, bool ZP>
+void go_tile(I4Args a, hipStream_t s) {
+  go_stage<GS>(a, s);
+  a.nt = (a.T + BT - 1) / BT;
+  a.nc = (a.N + 255) / 256;
+  hipLaunchKernelGGL((i4_tile<BT, 4, GS, ZP>), dim3((a.nt * a.nc + 7) / 8 * 8), dim3(512), 0, s, a);
+}
+
+template <int GS, bool ZP>
 void product(const I4Args &a, hipStream_t s) {
   const Choice c = choose(a.T, a.N, a.kb);
-  if (c.kernel == Choice::kFew) {
-    if (c.nb == 4)
-      go_rows<1, 4, 8, GS, ZP>(a, s);
-    else if (c.nb == 2)
-      go_rows<1, 2, 8, GS, ZP>(a, s);
-    else
-      go_rows<1, 1, 8, GS, ZP>(a, s);
-    return;
+  switch (c.kernel) {
+    case Choice::kFew:
+      return c.nb == 4 ? go_rows<4, GS, ZP>(a, s) : c.nb == 2 ? go_rows<2, GS, ZP>(a, s) : go_rows<1, GS, ZP>(a, s);
+    case Choice::kDirect:
+      return c.nb == 2 ? go_direct<2, GS, ZP>(a, s) : go_direct<1, GS, ZP>(a, s);
+    case Choice::kBlocks:
+      return go_blocks<GS, ZP>(a, s);
+    case Choice::kTile64:
+      return go_tile<64, GS, ZP>(a, s);
+    case Choice::kTile128:
+      return go_tile<128, GS, ZP>(a, s);
   }
-  go_stage<GS>(a, s);
-  if (c.kernel == Choice::kTile64)
-    go_tile<64, 4, GS, ZP>(a, s);
-  else if (c.kernel == Choice::kTile128)
-    go_tile<128, 4, GS, ZP>(a, s);
-  else if (c.nb == 4)
-    go_blocks<1, 4, 8, GS, ZP>(a, s);
-  else if (c.nb == 2)
-    go_blocks<1, 2, 8, GS, ZP>(a, s);
-  else
-    go_blocks<1, 1, 8, GS, ZP>(a, s);
 }
 
 template <int GS>
@@ -894,21 +969,21 @@ extern "C" int tcl_i4_pack(tcl_i4_weight *w, void *W_p, size_t bytes, void *stre
 namespace tcl {
 namespace {
 
-// Bytes of the staged activations, with their sums, with the parts of
+// Bytes of the staged activations, with their sums, and of the parts of
 // workgroups that share columns.
 struct Space {
-  size_t x, sums, total;
+  size_t x, total;
   int32_t steps, ks;
 };
 Space space(const tcl_i4_weight *w, const Layout &l, int32_t n_tokens) {
-  if (n_tokens <= kRows || w->d_out == 0) return {0, 0, 0, 0, 1};
-  const size_t tiles = (size_t(n_tokens) + 31) / 32;
   const int32_t groups = w->group < 128 ? l.groups : l.kb;  // longer ones count by their blocks
   const int32_t steps = (groups + 3) / 4;
-  const size_t x = tiles * l.kb * 8192;
-  const size_t sums = x + tiles * steps * 512;
-  const int32_t ks = choose(n_tokens, w->d_out, l.kb).ks;
-  return {x, sums, sums + (ks > 1 ? size_t(ks) * n_tokens * w->d_out * 4 : 0), steps, ks};
+  if (n_tokens == 0 || w->d_out == 0) return {0, 0, steps, 1};
+  const Choice c = choose(n_tokens, w->d_out, l.kb);
+  if (c.kernel == Choice::kFew || c.kernel == Choice::kDirect)
+    return {0, c.ks > 1 ? size_t(c.ks) * n_tokens * w->d_out * 4 : 0, steps, c.ks};
+  const size_t tiles = (size_t(n_tokens) + 31) / 32, x = tiles * l.kb * 8192;
+  return {x, x + tiles * steps * 512, steps, 1};
 }
 
 int check_tokens(const tcl_i4_weight *w, int32_t n_tokens) {
@@ -958,7 +1033,7 @@ extern "C" int tcl_i4_linear(const tcl_i4_weight *w, const void *x, int64_t ldx,
            static_cast<const uint16_t *>(x), y, ldx, ldy, n_tokens, w->d_in, w->d_out, l.kb, l.groups,
            w->group < 128 ? 0 : ((uint64_t(1) << 32) + w->group / 128 - 1) / (w->group / 128), reinterpret_cast<nt_u4 *>(q),
            reinterpret_cast<float *>(q + sp.x), sp.steps, 0, 0, sp.ks,
-           reinterpret_cast<float *>(q + sp.sums), yd == TCL_F32};
+           reinterpret_cast<float *>(q), yd == TCL_F32};
   hipStream_t s = static_cast<hipStream_t>(stream);
   logf("i4: tokens=%d d_in=%d d_out=%d group=%d zeros=%d", a.T, a.K, a.N, w->group, w->zeros);
   if (w->group == 32)

@@ -685,8 +685,11 @@ def test_i4_host_errors(L):
     assert lin(T=0) == 0 and lin(d_out=0, x=None) == 0
     assert lin(T=0, W=None, scale=None, zero=None) == 0
     assert [L.tcl_i4_workspace_bytes(w(), T, ctypes.byref(out)) for T in (16, 17)] == [0, 0]
-    assert out.value == 8192 + 512  # (32 tokens: one block and one step of four groups)
-    assert [lin(T=17, ws=None), lin(T=17, ws=P + 16), lin(T=17, n=out.value - 1)] == [E, A, tclora.ENOSPC]
+    for kw, n in ((dict(d_out=25600), 8192 + 512),  # 32 tokens: one block and one step of four groups
+                  (dict(d_in=8192), 8 * 17 * 32 * 4)):  # parts of eight workgroups
+        assert L.tcl_i4_workspace_bytes(w(**kw), 17, ctypes.byref(out)) == 0 and out.value == n
+        kw = dict(T=17, ldx=8192, ldy=25600, **kw)
+        assert [lin(ws=None, **kw), lin(ws=P + 16, **kw), lin(n=n - 1, **kw)] == [E, A, tclora.ENOSPC]
     assert L.tcl_i4_workspace_bytes(w(), 4, ctypes.byref(out)) == 0 and out.value == 0
     assert L.tcl_i4_workspace_bytes(w(), -1, ctypes.byref(out)) == E
     assert L.tcl_i4_workspace_bytes(None, 4, ctypes.byref(out)) == E

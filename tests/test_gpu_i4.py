@@ -116,6 +116,23 @@ def test_rows_that_end_inside_a_block(T, d_in):
     close(tclora.i4_linear(tclora.I4Weight(*w), x, y_dtype=torch.float32), *product64(w, n, x))
 
 
+@pytest.mark.parametrize("T,d_out", [(17, 25592), (64, 25592), (1000, 4088), (2040, 4088)])
+@pytest.mark.parametrize("d_in,group", [(96, 32), (416, 32), (448, 64), (1152, 384)])
+def test_laid_out_activations(T, d_out, d_in, group):
+    """Wide outputs and many tokens: NaNs behind the rows, zero points up to
+    255, scales of any size, rows that are not finite."""
+    w, n = weight(T, d_out, d_in, group, True, full=True)
+    W, s, z = w
+    z.copy_(torch.randint(0, 256, z.shape, dtype=torch.uint8))
+    s[0], s[1], s[2], s[3] = 0, -s[1], s[2] * 1e20, s[3] * 1e-30
+    wide = torch.full((T, d_in + 8), float("nan"), dtype=torch.bfloat16, device=DEV)
+    x = wide[:, :d_in].copy_(acts(T, T, d_in))
+    x[T // 2, 5], x[1, d_in - 1] = float("inf"), float("nan")
+    rest = [t for t in range(T) if t not in (1, T // 2)]
+    y = tclora.i4_linear(tclora.I4Weight(*w), x, y_dtype=torch.float32)
+    close(y[rest], *product64(w, n, x[rest]))
+
+
 @pytest.mark.parametrize("T", [3, 40, 70, 300])
 @pytest.mark.parametrize("y", ["bf16", "f32"])
 def test_strides_and_bounds(T, y):
