@@ -824,7 +824,7 @@ int tcl_kv_append_norm(const tcl_kv_cache *c, const tcl_rope *rope, const tcl_he
  * (TCL_ENOSPC) takes nothing: every row is padding, seq_tok_ptr is all zeros,
  * own_len_out = own_len, *used_out = *used, own_pages is left as it was; what
  * follows in the stream then appends nothing and attends to nothing.
- * Of c, page_size and n_pages count.  One launch, two for more than 8192 rows.
+ * Of c, page_size and n_pages count.  One launch, two for more than 4096 rows.
  * Graph-capturable.
  * Errors on the host: those of the cache; TCL_EINVAL (NULL, negative sizes,
  * requests without a group), TCL_EALIGN (slot 8-byte, the others 4-byte

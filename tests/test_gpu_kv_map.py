@@ -97,9 +97,9 @@ def test_map(S, G, page, new, own, pad):
         check(call(), want)
 
 
-@pytest.mark.parametrize("T", [8191, 8192, 8193, 9216, 9217, 70000])
+@pytest.mark.parametrize("T", [4095, 4096, 4097, 8191, 8192, 8193, 9216, 9217, 70000])
 def test_around_the_second_launch(T):
-    s = Step(T, 40, 3, 16, 200, 500, 0)
+    s = Step(T, 40, 3, 16, 200 if T > 8000 else 90, 500, 0)
     s.n_new[7] += T - 3 - s.n_new.sum()
     s = Step(T, 40, 3, 16, s.n_new, 500, pad=3)
     assert s.T == T
@@ -223,6 +223,31 @@ def test_in_place_replays_go_on(new):
             break
     assert call.status()[0] in (tclora.ENOSPC, tclora.EINVAL)
     assert np.array_equal(t[3].cpu().numpy(), before) and (call.slot == -1).all()
+
+
+@pytest.mark.parametrize("new", [3, 900])
+@pytest.mark.parametrize("raw", [False, True])
+def test_on_another_stream(raw, new):
+    """Outputs belong to the stream of the call, two calls at once to their
+    own, also when a call is dropped right behind it."""
+    a, b = Step(41, 40, 3, 16, new, 100, pad=4), Step(42, 30, 4, 32, new, 50)
+    ta, tb = a.tensors(), b.tensors()
+    st = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    s = [x.cuda_stream if raw else x for x in st]
+    for _ in range(3):
+        torch.cuda._sleep(2_000_000)
+        junk = [torch.full((n,), 7, dtype=torch.uint8, device=DEV) for n in (1 << 9, 1 << 12, 1 << 17, 1 << 18)]
+        kept = [j.clone() for j in junk]
+        del junk
+        tclora.kv_map(a.cache, *ta, a.T, stream=s[0])
+        calls = [tclora.kv_map(x.cache, *t, x.T, stream=i) for x, t, i in zip((a, b), (ta, tb), s)]
+        over = [torch.full((n,), 9, dtype=torch.uint8, device=DEV) for n in (1 << 9, 1 << 12, 1 << 17, 1 << 18)]
+        torch.cuda.synchronize()
+        for x, call in zip((a, b), calls):
+            check(call, x.want_all())
+        assert all(bool((k == 7).all()) for k in kept)
+        del over
 
 
 def test_slots_beyond_32_bits():
