@@ -20,7 +20,11 @@
 // those from its first row's window on.  An item's keys are numbered as if the
 // first range lay right before the second (Work::at, gap), so that items are
 // cut and walked as ever; the keys that a step hides from a row are found from
-// three limits a row instead of one.
+// three limits a row instead of one.  The bounds are those without a window: 64
+// requests of 8 tenants, windows of 4096, 430 MB, 88.8 + 6.8 us joining, 4.8
+// TB/s; chunks of 8 requests, windows of 1024, 60 G operations, 118 us captured:
+// the exponentials, and 768 workgroups on 512 places, the last half round of
+// them alone.
 #include <algorithm>
 #include <cmath>
 #include <limits>

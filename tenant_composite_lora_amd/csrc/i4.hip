@@ -257,7 +257,10 @@ __device__ inline void stream(int first, int step, int n, F block) {
 // Few tokens, straight from x.  16 NB channels a workgroup; wave w of WV takes
 // the blocks w, w + WV, ... of 128 columns.  Tokens are the rows of a
 // result, so that a lane holds one channel, its scale and zero point; the sums
-// of x come from an operand of ones.  GS: groups of a block (4, 2, 1; 1 also
+// of x come from an operand of ones.  Operands are on their way up to four
+// blocks ahead, since a wave has few: at 1 token, 4096 -> 1024, 64 workgroups of
+// 8 waves have 4 blocks each, 4.9 us, a launch and two trips to memory; 4096 ->
+// 14336, 31 MB, 8.7 us, 3.6 TB/s.  GS: groups of a block (4, 2, 1; 1 also
 // for groups of several blocks).
 template <int NB, int GS, bool ZP>
 __global__ __launch_bounds__(64 * kWaves) void i4_rows(I4Args a) {
@@ -363,7 +366,11 @@ __device__ inline int row_of(int e, int h) { return 8 * (e / 4) + 4 * h + e % 4;
 __device__ inline constexpr int place(int i) { return (i & 1) << 1 | i >> 1; }
 
 // More tokens, from staged activations: 32 NB channels by 32 tokens, the blocks
-// dealt out to the waves as in i4_rows, then the corrections.
+// dealt out to the waves as in i4_rows, then the corrections.  128 channels a
+// workgroup, so that activations are read from L2 by few of them: 64 tokens,
+// 4096 -> 14336, 14.5 us behind 4.3 of laying them out, 32 MB from memory and 88
+// more from L2.  Widening, scaling and the trips to L2 share the time; the matrix
+// cores are busy for a third of it.
 template <int NB, int GS, bool ZP>
 __global__ __launch_bounds__(64 * kWaves) void i4_blocks(I4Args a) {
   const Widen widen;
@@ -457,7 +464,11 @@ __global__ __launch_bounds__(64 * kWaves) void i4_blocks(I4Args a) {
 // The same without a launch that lays out the activations: a wave reads its
 // block of them in rows of 256 bytes, a block ahead, and turns it in LDS; the
 // sums of x come from an operand of ones.  32 NB channels by 32 tokens; with
-// ks > 1 as many workgroups, blockIdx.y, share their columns.
+// ks > 1 as many workgroups, blockIdx.y, share their columns.  32 x 4096 -> 4096
+// 8.3 us, 64 8.7; 23 tokens, 14336 -> 4096 in two, groups of 32, 15.3 us of 37 MB
+// and 3.8 joining.  A CU takes in some 60 GB/s, rows and weights together; 128
+// channels a workgroup do not fit the registers (30 of them spilled, 13.9 us
+// where 64 take 9.6).
 template <int NB, int GS, bool ZP>
 __global__ __launch_bounds__(64 * kWaves) void i4_direct(I4Args a) {
   const Widen widen;
@@ -611,7 +622,11 @@ __device__ inline void move4(uint32_t to, const void *from, uint32_t off) {
 // of 128 columns go through LDS in three stages, activations and weights alike,
 // each filled while the block two before it is multiplied (a wave's own
 // registers hold no load: one block's time does not cover a trip to memory);
-// scales, zero points and sums of x come with every four groups.
+// scales, zero points and sums of x come with every four groups.  2048 tokens,
+// 4096 -> 14336: 265 us with the 10 of laying x out, 0.91 P operations a second;
+// the same matrix instructions alone take 176 (the clock under full load), what
+// comes on top is LDS filled (31), sums scaled (31), corrections (16), operands
+// read (16); widening, dealt out among the products, 3.
 template <int BT, int WC, int GS, bool ZP>
 __global__ __launch_bounds__(512, 2) void i4_tile(I4Args a) {
   const Widen widen;

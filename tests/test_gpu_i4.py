@@ -234,12 +234,13 @@ def test_empty_batch_and_empty_weight():
     assert tclora.i4_linear(w0, acts(7, 3, 64)).shape == (3, 0)
 
 
-@pytest.mark.parametrize("T", [1, 64, 300])
-def test_in_a_graph_and_bit_for_bit(T):
-    w, n = weight(8, 1032, 1024, 128, True)
+@pytest.mark.parametrize("T,d_in,d_out", [(1, 1024, 1032), (64, 1024, 1032), (300, 1024, 1032),
+                                          (40, 8192, 1032), (600, 1024, 4096), (1024, 1024, 4096)])
+def test_in_a_graph_and_bit_for_bit(T, d_in, d_out):
+    w, n = weight(8, d_out, d_in, 128, True)
     p = tclora.I4Weight(*w)
-    x = acts(8, T, 1024)
-    y = torch.empty(T, 1032, device=DEV)
+    x = acts(8, T, d_in)
+    y = torch.empty(T, d_out, device=DEV)
     call = tclora.I4Call(p, x, y)
     st = torch.cuda.Stream()
     st.wait_stream(torch.cuda.current_stream())
@@ -249,7 +250,7 @@ def test_in_a_graph_and_bit_for_bit(T):
     with torch.cuda.graph(g, stream=st):
         call()
     for i in range(4):
-        x.copy_(acts(20 + i, T, 1024))
+        x.copy_(acts(20 + i, T, d_in))
         y.fill_(float("nan"))
         g.replay()
         torch.cuda.synchronize()
@@ -258,10 +259,11 @@ def test_in_a_graph_and_bit_for_bit(T):
         close(got, *product64(w, n, x))
 
 
-def test_two_calls_at_once():
-    w, _ = weight(10, 2048, 2048, 128)
+@pytest.mark.parametrize("d_in", [2048, 8192])
+def test_two_calls_at_once(d_in):
+    w, _ = weight(10, 2048, d_in, 128)
     p = tclora.I4Weight(*w)
-    xs = [acts(30 + i, t, 2048) for i, t in enumerate((64, 300))]
+    xs = [acts(30 + i, t, d_in) for i, t in enumerate((64, 300))]
     want = [tclora.i4_linear(p, x) for x in xs]
     calls = [tclora.I4Call(p, x, torch.empty_like(y)) for x, y in zip(xs, want)]
     st = [torch.cuda.Stream(), torch.cuda.Stream()]
@@ -284,12 +286,13 @@ def test_a_token_does_not_depend_on_its_batch():
         assert torch.equal(tclora.i4_linear(p, x[perm], y_dtype=torch.float32), y[perm])
 
 
+@pytest.mark.parametrize("d_in", [1024, 8192])
 @pytest.mark.parametrize("raw", [False, True])
-def test_on_another_stream(raw):
+def test_on_another_stream(raw, d_in):
     """Weight, packed copy and result made on the way belong to the stream of
     the call, also when everything is dropped right behind it."""
-    w, _ = weight(12, 512, 1024, 128, True)
-    x = acts(12, 32, 1024)
+    w, _ = weight(12, 512, d_in, 128, True)
+    x = acts(12, 32, d_in)
     want = tclora.i4_linear(tclora.I4Weight(*w), x)
     st = torch.cuda.Stream()
     torch.cuda.synchronize()
