@@ -15,8 +15,8 @@
 //              operands, the waves of a workgroup split d_in and add their sums
 //              in LDS;
 //   i4_direct  more, in tiles of 32: likewise, x turned in LDS;
-//   i4_blocks  wide outputs: likewise, after a launch that lays x out in operands
-//              and sums it over the groups (i4_stage_kernel);
+//   i4_blocks  wide outputs in short groups: likewise, after a launch that lays x
+//              out in operands and sums it over the groups (i4_stage_kernel);
 //   i4_tile    many tokens, from laid-out activations: tiles of both operands go
 //              through LDS.
 //
@@ -366,11 +366,11 @@ __device__ inline int row_of(int e, int h) { return 8 * (e / 4) + 4 * h + e % 4;
 __device__ inline constexpr int place(int i) { return (i & 1) << 1 | i >> 1; }
 
 // More tokens, from staged activations: 32 NB channels by 32 tokens, the blocks
-// dealt out to the waves as in i4_rows, then the corrections.  128 channels a
-// workgroup, so that activations are read from L2 by few of them: 64 tokens,
-// 4096 -> 14336, 14.5 us behind 4.3 of laying them out, 32 MB from memory and 88
-// more from L2.  Widening, scaling and the trips to L2 share the time; the matrix
-// cores are busy for a third of it.
+// dealt out to the waves as in i4_rows, then the corrections.  For
+// groups of 32 and 64: 64 tokens, 4096 -> 14336, groups of 32, 25.2 us with the 4.2
+// of laying the activations out.  What scales the sums, two operations an
+// element and group in i4_direct, one here, shares the issue slots with widening
+// and the matrix instructions.
 template <int NB, int GS, bool ZP>
 __global__ __launch_bounds__(64 * kWaves) void i4_blocks(I4Args a) {
   const Widen widen;
@@ -461,135 +461,6 @@ __global__ __launch_bounds__(64 * kWaves) void i4_blocks(I4Args a) {
   add_up<32, 2 * NB, LD, WV>(a, part, t0, c0, [&](int t, int ch, nt_f4 v) { store4(a, t, ch, v); });
 }
 
-// The same without a launch that lays out the activations: a wave reads its
-// block of them in rows of 256 bytes, a block ahead, and turns it in LDS; the
-// sums of x come from an operand of ones.  32 NB channels by 32 tokens; with
-// ks > 1 as many workgroups, blockIdx.y, share their columns.  32 x 4096 -> 4096
-// 8.3 us, 64 8.7; 23 tokens, 14336 -> 4096 in two, groups of 32, 15.3 us of 37 MB
-// and 3.8 joining.  A CU takes in some 60 GB/s, rows and weights together; 128
-// channels a workgroup do not fit the registers (30 of them spilled, 13.9 us
-// where 64 take 9.6).
-template <int NB, int GS, bool ZP>
-__global__ __launch_bounds__(64 * kWaves) void i4_direct(I4Args a) {
-  const Widen widen;
-  constexpr int WV = kWaves, LD = 32 * NB + 8;
-  __shared__ __align__(16) union {
-    float part[WV * 32 * LD];
-    nt_u4 x[WV][32 * 16];  // chunk c of row r at 16 r + (c ^ r % 16)
-  } l;
-  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int c = lane & 31, h = lane >> 5;
-  const int nx = (a.N + 32 * NB - 1) / (32 * NB);
-  const int c0 = blockIdx.x % nx * 32 * NB, t0 = blockIdx.x / nx * 32;
-  const int first = blockIdx.y * WV + w, stride = a.ks * WV;
-  const int tiles = (a.N + 31) / 32;
-  const nt_u4 *wp[NB];
-  const float *sp[NB];
-  const uint8_t *zp[NB];
-#pragma unroll
-  for (int n = 0; n < NB; ++n) {
-    // (channel tiles past the last: the last one again, not stored)
-    const int64_t ct = min(c0 / 32 + n, tiles - 1);
-    wp[n] = reinterpret_cast<const nt_u4 *>(a.w) + ct * a.kb * 128;
-    sp[n] = a.scale + ct * a.groups * 32;
-    zp[n] = ZP ? a.zero + ct * a.groups * 32 : nullptr;
-  }
-  f32x16_t acc[NB];
-#pragma unroll
-  for (int n = 0; n < NB; ++n) acc[n] = nothing();
-  nt_u4 wq[NB][2], xr[8];
-  float s[NB][GS], z[NB][GS];
-  const int row = lane >> 4, chunk = lane & 15;
-  auto load_w = [&](int n, int k, int b) { wq[n][k] = (wp[n] + int64_t(min(b, a.kb - 1)) * 128 + 64 * k)[lane]; };
-  auto load_s = [&](int n, int b) {
-#pragma unroll
-    for (int e = 0; e < GS; ++e) {
-      const int gr = group_at<GS>(a, min(b, a.kb - 1), e);
-      s[n][e] = (sp[n] + gr * 32)[c];
-      z[n][e] = ZP ? 16.f + float((zp[n] + gr * 32)[c]) : 24.f;
-    }
-  };
-  auto load_x = [&](int j, int b) {
-    // (columns past the row's end: any of it; rows past the last: the last)
-    const int k = b * 128 + 8 * chunk;
-    xr[j] = *reinterpret_cast<const nt_u4 *>(a.x + int64_t(min(t0 + 4 * j + row, a.T - 1)) * a.ldx +
-                                             (k < a.K ? k : 0));
-  };
-#pragma unroll
-  for (int j = 0; j < 8; ++j) load_x(j, first);
-#pragma unroll
-  for (int n = 0; n < NB; ++n) load_w(n, 0, first), load_w(n, 1, first), load_s(n, first);
-  auto block = [&](int, int b, auto more) {
-    const bool in = b * 128 + 8 * chunk < a.K;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int r = 4 * j + row;
-      l.x[w][16 * r + (chunk ^ (r & 15))] = in ? xr[j] : nt_u4{0, 0, 0, 0};
-      if constexpr (more) load_x(j, b + stride);
-    }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int e = 0; e < GS; ++e) {
-      f32x16_t sum = nothing();
-      f32x16_t p[NB];
-#pragma unroll
-      for (int n = 0; n < NB; ++n) p[n] = nothing();
-      nt_u4 xo[2];
-      auto read = [&](int i) { xo[i & 1] = l.x[w][16 * c + ((2 * i + h) ^ (c & 15))]; };
-      read(8 / GS * e);
-#pragma unroll
-      for (int i = 8 / GS * e; i < 8 / GS * (e + 1); ++i) {
-        if (i + 1 < 8 / GS * (e + 1)) read(i + 1);
-        const bf16x8_t x = as_bf16(xo[i & 1]);
-        sum = mfma(x, ones(), sum);
-#pragma unroll
-        for (int n = 0; n < NB; ++n) p[n] = mfma(x, widen(wq[n][i / 4][place(i % 4)]), p[n]);
-        if constexpr (more)
-          if (i % 4 == 3)
-#pragma unroll
-            for (int n = 0; n < NB; ++n) load_w(n, i / 4, b + stride);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-#pragma unroll
-      for (int n = 0; n < NB; ++n)
-#pragma unroll
-        for (int r = 0; r < 16; ++r)
-          acc[n][r] = fmaf(s[n][e], fmaf(-z[n][e], sum[r], p[n][r]), acc[n][r]);
-    }
-    if constexpr (more)
-#pragma unroll
-      for (int n = 0; n < NB; ++n) load_s(n, b + stride);
-    __builtin_amdgcn_sched_barrier(0);
-  };
-  stream<1>(first, stride, a.kb, block);
-  __syncthreads();  // (the waves' activations lie where their sums go)
-#pragma unroll
-  for (int n = 0; n < NB; ++n)
-#pragma unroll
-    for (int r = 0; r < 16; ++r) l.part[(w * 32 + row_of(r, h)) * LD + 32 * n + c] = acc[n][r];
-  __syncthreads();
-  add_up<32, 2 * NB, LD, WV>(a, l.part, t0, c0, [&](int t, int ch, nt_f4 v) {
-    if (a.ks == 1)
-      store4(a, t, ch, v);
-    else
-      *reinterpret_cast<nt_f4 *>(a.part + ((int64_t(blockIdx.y) * a.T + t) * a.N + ch)) = v;
-  });
-}
-
-// Adds the parts of the workgroups that shared columns, in order.
-__global__ __launch_bounds__(256) void i4_join_kernel(I4Args a) {
-  const int64_t n4 = a.N / 4, all = a.T * n4;
-  for (int64_t o = int64_t(blockIdx.x) * 256 + threadIdx.x; o < all; o += int64_t(gridDim.x) * 256) {
-    const nt_f4 *in = reinterpret_cast<const nt_f4 *>(a.part) + o;
-    nt_f4 v = in[0];
-#pragma unroll 4
-    for (int z = 1; z < a.ks; ++z) v += in[z * all];
-    store4(a, int(o / n4), int(o % n4) * 4, v);
-  }
-}
-
 // Loads straight into LDS: 64 lanes write 16 (or 4) bytes each, in a row from
 // `to`; the compiler does not count them (arrived).  An immediate offset moves
 // source and destination alike.
@@ -617,13 +488,151 @@ __device__ inline void move4(uint32_t to, const void *from, uint32_t off) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(to), "v"(off), "s"(from)
                : "memory", "m0");
 }
+__device__ inline void move16(uint32_t to, const void *from) {  // an address a lane
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from) : "memory", "m0");
+}
+
+// The same without a launch that lays out the activations: a wave moves its
+// block of them, rows of 256 bytes, into LDS, a block ahead, and turns it in
+// reading; the sums of x come from an operand of ones.  32 NB channels by 32
+// tokens; with ks > 1 as many workgroups, blockIdx.y, share their columns.  32 x
+// 4096 -> 4096 8.1 us, 64 8.7; 64 x 4096 -> 14336 15.6; 23 tokens, 14336 -> 4096 in
+// two, groups of 32, 15.1 us of 37 MB and 4 joining.  A CU takes in some 60
+// GB/s, rows and weights together.  (Rows through registers take 32 more of them:
+// 64 x 4096 -> 14336, 30 spilled, 20.7.  Weights two blocks ahead: 32 x 4096 ->
+// 14336 12.6 where one takes 11.4.)
+template <int NB, int GS, bool ZP>
+__global__ __launch_bounds__(64 * kWaves) void i4_direct(I4Args a) {
+  const Widen widen;
+  constexpr int WV = kWaves, LD = 32 * NB + 8;
+  __shared__ __align__(16) union {
+    float part[WV * 32 * LD];
+    nt_u4 x[WV][2][32 * 16];  // chunk c of row r at 16 r + (c ^ r % 16)
+  } l;
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane & 31, h = lane >> 5;
+  const int nx = (a.N + 32 * NB - 1) / (32 * NB);
+  const int c0 = blockIdx.x % nx * 32 * NB, t0 = blockIdx.x / nx * 32;
+  const int first = blockIdx.y * WV + w, stride = a.ks * WV;
+  const int tiles = (a.N + 31) / 32;
+  const nt_u4 *wp[NB];
+  const float *sp[NB];
+  const uint8_t *zp[NB];
+#pragma unroll
+  for (int n = 0; n < NB; ++n) {
+    // (channel tiles past the last: the last one again, not stored)
+    const int64_t ct = min(c0 / 32 + n, tiles - 1);
+    wp[n] = reinterpret_cast<const nt_u4 *>(a.w) + ct * a.kb * 128;
+    sp[n] = a.scale + ct * a.groups * 32;
+    zp[n] = ZP ? a.zero + ct * a.groups * 32 : nullptr;
+  }
+  f32x16_t acc[NB];
+#pragma unroll
+  for (int n = 0; n < NB; ++n) acc[n] = nothing();
+  nt_u4 wq[NB][2];
+  float s[NB][GS], z[NB][GS];
+  auto load_w = [&](int n, int k, int b) { wq[n][k] = (wp[n] + int64_t(min(b, a.kb - 1)) * 128 + 64 * k)[lane]; };
+  auto load_s = [&](int n, int b) {
+#pragma unroll
+    for (int e = 0; e < GS; ++e) {
+      const int gr = group_at<GS>(a, min(b, a.kb - 1), e);
+      s[n][e] = (sp[n] + gr * 32)[c];
+      z[n][e] = ZP ? 16.f + float((zp[n] + gr * 32)[c]) : 24.f;
+    }
+  };
+  // rows of a block into LDS, four an instruction (columns past the row's end:
+  // any of it; rows past the last: the last)
+  auto load_x = [&](int b, int slot) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int row = 4 * j + (lane >> 4), k = b * 128 + 8 * ((lane ^ row) & 15);
+      move16(lds_at(&l.x[w][slot][64 * j]), a.x + int64_t(min(t0 + row, a.T - 1)) * a.ldx + (k < a.K ? k : 0));
+    }
+  };
+  load_x(first, 0);
+#pragma unroll
+  for (int n = 0; n < NB; ++n) load_w(n, 0, first), load_w(n, 1, first), load_s(n, first);
+  int slot = 0;
+  auto block = [&](int, int b, auto more) {
+    // The block's rows have come: at least the 2 NB loads of its weights were
+    // issued behind them.  What the next rows replace has been read.
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(2 * NB) : "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (more) load_x(b + stride, slot ^ 1);
+    __builtin_amdgcn_sched_barrier(0);
+    const nt_u4 *xl = &l.x[w][slot][16 * c];
+    slot ^= 1;
+#pragma unroll
+    for (int e = 0; e < GS; ++e) {
+      f32x16_t sum = nothing();
+      f32x16_t p[NB];
+#pragma unroll
+      for (int n = 0; n < NB; ++n) p[n] = nothing();
+      nt_u4 xo[2];
+      auto read = [&](int i) { xo[i & 1] = xl[(2 * i + h) ^ (c & 15)]; };
+      read(8 / GS * e);
+#pragma unroll
+      for (int i = 8 / GS * e; i < 8 / GS * (e + 1); ++i) {
+        if (i + 1 < 8 / GS * (e + 1)) read(i + 1);
+        // (a row's last block may end before 128 columns)
+        const bf16x8_t x = as_bf16(more || b * 128 + 8 * (2 * i + h) < a.K ? xo[i & 1] : nt_u4{0, 0, 0, 0});
+        sum = mfma(x, ones(), sum);
+#pragma unroll
+        for (int n = 0; n < NB; ++n) p[n] = mfma(x, widen(wq[n][i / 4][place(i % 4)]), p[n]);
+        if constexpr (more)
+          if (i % 4 == 3)
+#pragma unroll
+            for (int n = 0; n < NB; ++n) load_w(n, i / 4, b + stride);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          acc[n][r] = fmaf(s[n][e], fmaf(-z[n][e], sum[r], p[n][r]), acc[n][r]);
+    }
+    if constexpr (more)
+#pragma unroll
+      for (int n = 0; n < NB; ++n) load_s(n, b + stride);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  stream<1>(first, stride, a.kb, block);
+  // the waves' activations lie where their sums go; rows of a wave without a
+  // block may still be on their way
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+#pragma unroll
+  for (int n = 0; n < NB; ++n)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) l.part[(w * 32 + row_of(r, h)) * LD + 32 * n + c] = acc[n][r];
+  __syncthreads();
+  add_up<32, 2 * NB, LD, WV>(a, l.part, t0, c0, [&](int t, int ch, nt_f4 v) {
+    if (a.ks == 1)
+      store4(a, t, ch, v);
+    else
+      *reinterpret_cast<nt_f4 *>(a.part + ((int64_t(blockIdx.y) * a.T + t) * a.N + ch)) = v;
+  });
+}
+
+// Adds the parts of the workgroups that shared columns, in order.
+__global__ __launch_bounds__(256) void i4_join_kernel(I4Args a) {
+  const int64_t n4 = a.N / 4, all = a.T * n4;
+  for (int64_t o = int64_t(blockIdx.x) * 256 + threadIdx.x; o < all; o += int64_t(gridDim.x) * 256) {
+    const nt_f4 *in = reinterpret_cast<const nt_f4 *>(a.part) + o;
+    nt_f4 v = in[0];
+#pragma unroll 4
+    for (int z = 1; z < a.ks; ++z) v += in[z * all];
+    store4(a, int(o / n4), int(o % n4) * 4, v);
+  }
+}
 
 // Many tokens: tiles of 256 channels by BT tokens, WC by 8 / WC waves.  Blocks
 // of 128 columns go through LDS in three stages, activations and weights alike,
 // each filled while the block two before it is multiplied (a wave's own
 // registers hold no load: one block's time does not cover a trip to memory);
 // scales, zero points and sums of x come with every four groups.  2048 tokens,
-// 4096 -> 14336: 265 us with the 10 of laying x out, 0.91 P operations a second;
+// 4096 -> 14336: 258 to 265 us with the 10 of laying x out, 0.92 P operations a second;
 // the same matrix instructions alone take 176 (the clock under full load), what
 // comes on top is LDS filled (31), sums scaled (31), corrections (16), operands
 // read (16); widening, dealt out among the products, 3.
@@ -812,27 +821,29 @@ constexpr int kRows = 16;
 //     channels: 16 channels 4.5, 32 5.7; 4096 channels 4.9, 6.1; 14336: 16
 //     channels 10.6, 64 8.7 (16 tokens: 19.1, 9.9).
 //   The others by whole rounds over the CUs (half_us: one workgroup a CU).
-//     i4_direct, 32 channels a workgroup, 64, i4_blocks with 128: 64 tokens,
-//     4096 channels 8.7, 9.8, 15.1; 32 x 14336 15.1, 11.3, 16.8; 64 x 14336
-//     31.2, 21.1, 19.0 (i4_blocks with 32 or 64, that is the launch that lays
-//     out the activations: 11.2 and 12.1, 16.1 and 13.9, 24.0 and 21.6).
-//     i4_blocks, i4_tile of 64 tokens, of 128: 512 tokens, 4096 channels 29.8,
-//     43.2, 60.1; 1024: 53.5, 50.2, 62.2; 2048: 103, 98, 83; 512 x 14336: 91.7,
-//     84.9, 68.8.
+//     i4_direct with 32 channels a workgroup, 64, 128: 64 tokens, 4096 channels
+//     8.7, 9.7, 13.2; 32 x 14336 16.1, 11.4, 14.4; 64 x 14336 29.7, 20.1, 15.6
+//     (i4_blocks, that is the launch that lays out the activations, 18.2); 192 x
+//     4096 21.4, 18.1, 14.2 (16.8).  In groups of 32 128 channels with their
+//     factors do not fit the registers: 64 x 14336 35.8, 25.6, 30.6 (25.2), 128 x
+//     14336 57.1, 46.4, 54.8 (41.1); there i4_blocks takes them.
+//     128 channels, i4_tile of 64 tokens, of 128: 512 tokens, 4096 channels 28.7,
+//     44.3, 60.4; 1024: 55.3, 49.3, 62.5; 2048: 111, 101, 78; 256 x 14336: 56.3,
+//     49.8, 62.7; 512 x 14336: 101, 87, 68.
 //   What bounds all of these is what a CU takes in, some 60 GB/s each, so that
 //     few workgroups with long rows are split over d_in (ks) and joined by a
-//     launch more.  d_in 14336: 23 tokens, 4096 channels 19.7, in two 15.6; 32,
-//     2048 channels 18.8, in four 11.8; 64, 4096 channels 23.7, in two of 64
-//     channels 20.8.  d_in 4096: 17 tokens, 1024 channels 7.3, in eight 7.4.
+//     launch more.  d_in 14336: 23 tokens, 4096 channels 19.0, in two 15.1; 32,
+//     2048 channels 18.8, in four 11.8; 64, 4096 channels 22.2, in two of 64
+//     channels 18.4.  d_in 4096: 17 tokens, 1024 channels 7.2, in two 7.4.
 struct Choice {
   enum { kFew, kDirect, kBlocks, kTile64, kTile128 } kernel;
-  int nb;  // 16 (few) or 32 (direct) channels a workgroup times this
+  int nb;  // 16 (few) or 32 (direct, blocks) channels a workgroup times this
   int ks;
 };
 
 int64_t rounds(int64_t workgroups) { return (workgroups + 255) / 256; }
 
-Choice choose(int32_t n_tokens, int32_t d_out, int32_t kb) {
+Choice choose(int32_t n_tokens, int32_t d_out, int32_t kb, bool shorter) {  // groups of less than 128
   const int64_t T = n_tokens, N = d_out;
   auto over = [](int64_t n, int64_t d) { return (n + d - 1) / d; };
   if (T <= kRows) return {Choice::kFew, over(N, 64) >= 192 ? 4 : over(N, 32) >= 192 ? 2 : 1, 1};
@@ -840,13 +851,14 @@ Choice choose(int32_t n_tokens, int32_t d_out, int32_t kb) {
   if (kb >= 64 && w2 <= 128)
     return w1 <= 128 ? Choice{Choice::kDirect, 1, int(std::min<int64_t>(256 / w1, kb / 8))}
                      : Choice{Choice::kDirect, 2, 2};
-  const int64_t half_us[5] = {3 + 14 * rounds(w1), 3 + 19 * rounds(w2), 10 + 24 * rounds(tb * over(N, 128)),
+  const int64_t half_us[5] = {3 + 14 * rounds(w1), 3 + 19 * rounds(w2),
+                              (shorter ? 10 : 5) + (shorter ? 24 : 26) * rounds(tb * over(N, 128)),
                               16 + 80 * rounds(over(T, 64) * over(N, 256)),
                               10 + 132 * rounds(over(T, 128) * over(N, 256))};
   switch (std::min_element(half_us, half_us + 5) - half_us) {
     case 0: return {Choice::kDirect, 1, 1};
     case 1: return {Choice::kDirect, 2, 1};
-    case 2: return {Choice::kBlocks, 4, 1};
+    case 2: return {shorter ? Choice::kBlocks : Choice::kDirect, 4, 1};
     case 3: return {Choice::kTile64, 0, 1};
     default: return {Choice::kTile128, 0, 1};
   }
@@ -922,14 +934,17 @@ void go_tile(I4Args a, hipStream_t s) {
 
 template <int GS, bool ZP>
 void product(const I4Args &a, hipStream_t s) {
-  const Choice c = choose(a.T, a.N, a.kb);
+  const Choice c = choose(a.T, a.N, a.kb, GS > 1);
   switch (c.kernel) {
     case Choice::kFew:
       return c.nb == 4 ? go_rows<4, GS, ZP>(a, s) : c.nb == 2 ? go_rows<2, GS, ZP>(a, s) : go_rows<1, GS, ZP>(a, s);
     case Choice::kDirect:
+      if constexpr (GS == 1)
+        if (c.nb == 4) return go_direct<4, GS, ZP>(a, s);
       return c.nb == 2 ? go_direct<2, GS, ZP>(a, s) : go_direct<1, GS, ZP>(a, s);
     case Choice::kBlocks:
-      return go_blocks<GS, ZP>(a, s);
+      if constexpr (GS > 1) go_blocks<GS, ZP>(a, s);
+      return;
     case Choice::kTile64:
       return go_tile<64, GS, ZP>(a, s);
     case Choice::kTile128:
@@ -994,7 +1009,7 @@ Space space(const tcl_i4_weight *w, const Layout &l, int32_t n_tokens) {
   const int32_t groups = w->group < 128 ? l.groups : l.kb;  // longer ones count by their blocks
   const int32_t steps = (groups + 3) / 4;
   if (n_tokens == 0 || w->d_out == 0) return {0, 0, steps, 1};
-  const Choice c = choose(n_tokens, w->d_out, l.kb);
+  const Choice c = choose(n_tokens, w->d_out, l.kb, w->group < 128);
   if (c.kernel == Choice::kFew || c.kernel == Choice::kDirect)
     return {0, c.ks > 1 ? size_t(c.ks) * n_tokens * w->d_out * 4 : 0, steps, c.ks};
   const size_t tiles = (size_t(n_tokens) + 31) / 32, x = tiles * l.kb * 8192;
