@@ -146,6 +146,20 @@ def test_strides_and_bounds(T, y):
     assert (yb[T:] == 5).all() and (yb[:, d_out:] == 5).all()
 
 
+@pytest.mark.parametrize("T,d_in,d_out,group", [(3, 256, 72, 64), (20, 256, 72, 128), (20, 8192, 72, 128),
+                                                (20, 256, 25600, 32), (20, 256, 25600, 128), (24, 256, 65536, 128)])
+def test_offsets_beyond_32_bits(T, d_in, d_out, group):
+    w, n = weight(19, d_out, d_in, group, True)
+    far = (1 << 31) // 2 + 64 if T < 4 else 1 << 27
+    x = torch.empty((T - 1) * far + d_in, dtype=torch.bfloat16, device=DEV).as_strided((T, d_in), (far, 1))
+    y = torch.empty((T - 1) * far + d_out, dtype=torch.float32, device=DEV).as_strided((T, d_out), (far, 1))
+    x.copy_(acts(19, T, d_in))
+    tclora.I4Call(tclora.I4Weight(*w), x, y)()
+    close(y.clone(), *product64(w, n, x.contiguous()))
+    del x, y
+    torch.cuda.empty_cache()
+
+
 @pytest.mark.parametrize("T", [5, 50, 200])
 def test_rows_that_are_not_finite_stay_alone(T):
     w, n = weight(3, 264, 512, 128)
