@@ -497,7 +497,7 @@ __device__ inline void move16(uint32_t to, const void *from) {  // an address a 
 // reading; the sums of x come from an operand of ones.  32 NB channels by 32
 // tokens; with ks > 1 as many workgroups, blockIdx.y, share their columns.  32 x
 // 4096 -> 4096 8.1 us, 64 8.7; 64 x 4096 -> 14336 15.6; 23 tokens, 14336 -> 4096 in
-// two, groups of 32, 15.1 us of 37 MB and 4 joining.  A CU takes in some 60
+// four, groups of 32, 14.0 us of 37 MB and 3.8 joining.  A CU takes in some 60
 // GB/s, rows and weights together.  (Rows through registers take 32 more of them:
 // 64 x 4096 -> 14336, 30 spilled, 20.7.  Weights two blocks ahead: 32 x 4096 ->
 // 14336 12.6 where one takes 11.4.)
@@ -832,9 +832,12 @@ constexpr int kRows = 16;
 //     49.8, 62.7; 512 x 14336: 101, 87, 68.
 //   What bounds all of these is what a CU takes in, some 60 GB/s each, so that
 //     few workgroups with long rows are split over d_in (ks) and joined by a
-//     launch more.  d_in 14336: 23 tokens, 4096 channels 19.0, in two 15.1; 32,
-//     2048 channels 18.8, in four 11.8; 64, 4096 channels 22.2, in two of 64
-//     channels 18.4.  d_in 4096: 17 tokens, 1024 channels 7.2, in two 7.4.
+//     launch more, of 64 channels where that leaves them 256 parts, since rows
+//     are most of what they take in.  d_in 14336: 23 tokens, 4096 channels 19.3, 32
+//     channels in two 15.4, 64 in four 14.2; 32, 2048 channels 18.4, 32 in four
+//     11.6, 64 in eight 11.4; 64, 4096 channels 22.3, 64 in two 19.1; d_in 8192, 17
+//     tokens, 1024 channels 11.6, 32 in eight 7.7, 64 in eight 8.5.  d_in 4096: 17
+//     tokens, 1024 channels 7.2, in two 7.4.
 struct Choice {
   enum { kFew, kDirect, kBlocks, kTile64, kTile128 } kernel;
   int nb;  // 16 (few) or 32 (direct, blocks) channels a workgroup times this
@@ -849,8 +852,8 @@ Choice choose(int32_t n_tokens, int32_t d_out, int32_t kb, bool shorter) {  // g
   if (T <= kRows) return {Choice::kFew, over(N, 64) >= 192 ? 4 : over(N, 32) >= 192 ? 2 : 1, 1};
   const int64_t tb = over(T, 32), w1 = tb * over(N, 32), w2 = tb * over(N, 64);
   if (kb >= 64 && w2 <= 128)
-    return w1 <= 128 ? Choice{Choice::kDirect, 1, int(std::min<int64_t>(256 / w1, kb / 8))}
-                     : Choice{Choice::kDirect, 2, 2};
+    return w1 < 64 ? Choice{Choice::kDirect, 1, int(std::min<int64_t>(256 / w1, kb / 8))}
+                   : Choice{Choice::kDirect, 2, int(256 / w2)};
   const int64_t half_us[5] = {3 + 14 * rounds(w1), 3 + 19 * rounds(w2),
                               (shorter ? 10 : 5) + (shorter ? 24 : 26) * rounds(tb * over(N, 128)),
                               16 + 80 * rounds(over(T, 64) * over(N, 256)),
