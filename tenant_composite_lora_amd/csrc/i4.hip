@@ -198,7 +198,7 @@ __device__ inline void split3(float v, uint32_t *p) {
 }
 
 // The correction of a group, -(s (16 + z)) sum x, as products of bf16 parts on
-// the matrix cores: columns 0 .. 5 of a lane's eight hold parts 0 0 1 0 2 1 of
+// the matrix cores (i4_tile): columns 0 .. 5 of a lane's eight hold parts 0 0 1 0 2 1 of
 // its group's sum against parts 0 1 0 2 0 1 of its factor, which leaves out less
 // than 2^-23 of the product.
 __device__ inline bf16x8_t parts_x(float v) {
@@ -365,14 +365,34 @@ __device__ inline int row_of(int e, int h) { return 8 * (e / 4) + 4 * h + e % 4;
 // The position in a packed lane of columns 16 i ..
 __device__ inline constexpr int place(int i) { return (i & 1) << 1 | i >> 1; }
 
+// A group's correction, -(16 + z) sum x, as a product of bf16 parts: columns 0 ..
+// 5 of a lane's eight hold parts 0 0 1 1 2 2 of the sum against the even part of
+// 16 + z (at most 270, so exactly a bf16 number) and the odd one (0 or 1) in turn.
+__device__ inline nt_u4 parts_sum(float v) {
+  uint32_t p[3];
+  split3(v, p);
+  return nt_u4{p[0] | p[0] << 16, p[1] | p[1] << 16, p[2] | p[2] << 16, 0};
+}
+__device__ inline bf16x8_t parts_zero(uint32_t z) {  // z: zero point
+  const uint32_t n = 16 + z, even = __float_as_uint(-float(n & ~1u)), odd = __float_as_uint(-float(n & 1));
+  const uint32_t w = __builtin_amdgcn_perm(odd, even, 0x07060302);
+  return as_bf16(nt_u4{w, w, w, 0});
+}
+
 // More tokens, from staged activations: 32 NB channels by 32 tokens, the blocks
-// dealt out to the waves as in i4_rows, then the corrections.  For
-// groups of 32 and 64: 64 tokens, 4096 -> 14336, groups of 32, 25.2 us with the 4.2
-// of laying the activations out.  What scales the sums, two operations an
-// element and group in i4_direct, one here, shares the issue slots with widening
-// and the matrix instructions.
+// dealt out to the waves as in i4_rows.  For groups of 32 and 64: 64 tokens, 4096 ->
+// 14336, groups of 32, 24.0 us with the 4.2 of laying the activations out (zero
+// points 24.8), 128 tokens 39.2.  A group's products start from its correction, a
+// matrix product in which one half of the lanes (the group's, two groups in turn)
+// holds the sum of x: what is scaled and added up is then no larger than the
+// result's own terms.  (Corrections taken off at the end, all groups' together:
+// 65536 columns of activations of one sign, 16 times the error that a group's own
+// roundings allow.)  What scales the sums, two operations an element and group in
+// i4_direct, one here, shares the issue slots with widening and the matrix
+// instructions.
 template <int NB, int GS, bool ZP>
 __global__ __launch_bounds__(64 * kWaves) void i4_blocks(I4Args a) {
+  static_assert(GS > 1, "two groups share a correction's operands");
   const Widen widen;
   constexpr int WV = kWaves, LD = 32 * NB + 8;
   __shared__ __align__(16) float part[WV * 32 * LD];
@@ -383,7 +403,7 @@ __global__ __launch_bounds__(64 * kWaves) void i4_blocks(I4Args a) {
   const int tiles = (a.N + 31) / 32;
   const int64_t tile = t0 / 32;
   const nt_u4 *xp = a.xb + tile * a.kb * 512;
-  const float *ep = a.xe + tile * a.steps * 128 + lane;
+  const float *ep = a.xe + tile * a.steps * 128;
   const nt_u4 *wp[NB];
   const float *sp[NB];
   const uint8_t *zp[NB];
@@ -405,13 +425,27 @@ __global__ __launch_bounds__(64 * kWaves) void i4_blocks(I4Args a) {
   // scheduling barriers hold the loads there; left to itself the compiler puts
   // them right before their use.)
   nt_u4 wq[NB][2], xr[8];
-  float s[NB][GS];
-  auto load_w = [&](int n, int k, int b) { wq[n][k] = (wp[n] + int64_t(min(b, a.kb - 1)) * 128 + 64 * k)[lane]; };
+  float s[NB][GS], v;
+  uint32_t z[NB];
+  auto load_w = [&](int n, int k, int b) {
+    const nt_u4 *at = wp[n] + int64_t(min(b, a.kb - 1)) * 128 + 64 * k;
+    asm("" : "+s"(at));  // (a scalar: else the lane's addresses take eight registers all along)
+    wq[n][k] = at[lane];
+  };
   auto load_s = [&](int n, int b) {
 #pragma unroll
     for (int e = 0; e < GS; ++e) s[n][e] = (sp[n] + group_at<GS>(a, min(b, a.kb - 1), e) * 32)[c];
   };
   auto load_x = [&](int i, int b) { xr[i] = (xp + int64_t(min(b, a.kb - 1)) * 512 + 64 * i)[lane]; };
+  // the sum of x of group 2 k + h of the block and its zero points (behind the last
+  // group sums of zero), half a block ahead: a whole one takes registers that spill
+  auto load_c = [&](int k, int b) {
+    const int pair = min(b, a.kb - 1) * (GS / 2) + k;
+    v = (ep + int64_t(pair) * 64)[lane];
+#pragma unroll
+    for (int n = 0; n < NB; ++n) z[n] = ZP ? zp[n][unsigned(min(2 * pair + h, a.groups - 1) * 32 + c)] : 8;
+  };
+  load_c(0, w);
 #pragma unroll
   for (int n = 0; n < NB; ++n) load_w(n, 0, w), load_w(n, 1, w), load_s(n, w);
 #pragma unroll
@@ -421,8 +455,15 @@ __global__ __launch_bounds__(64 * kWaves) void i4_blocks(I4Args a) {
 #pragma unroll
     for (int e = 0; e < GS; ++e) {
       f32x16_t p[NB];
+      const nt_u4 sum = parts_sum(h == (e & 1) ? v : 0.f);
 #pragma unroll
-      for (int n = 0; n < NB; ++n) p[n] = nothing();
+      for (int n = 0; n < NB; ++n) {
+        p[n] = mfma(as_bf16(sum), parts_zero(z[n]), nothing());
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (e == 1 && GS == 4) load_c(1, b);
+      if constexpr (more)
+        if (e == GS - 1) load_c(0, b + WV);
 #pragma unroll
       for (int i = 8 / GS * e; i < 8 / GS * (e + 1); ++i) {
 #pragma unroll
@@ -445,14 +486,6 @@ __global__ __launch_bounds__(64 * kWaves) void i4_blocks(I4Args a) {
       for (int n = 0; n < NB; ++n) load_s(n, b + WV);
   };
   stream<1>(w, WV, a.kb, block);
-  // (two groups a step: a half each; groups behind the last meet sums of zero)
-  for (int st = w; st < 2 * a.steps; st += WV) {
-    const int gr = min(GS == 1 ? group_of(a, 2 * st + h) : 2 * st + h, a.groups - 1);
-    const bf16x8_t x = parts_x(ep[int64_t(st) * 64]);
-#pragma unroll
-    for (int n = 0; n < NB; ++n)
-      acc[n] = mfma(x, parts_w(-sp[n][gr * 32 + c] * (ZP ? 16.f + float(zp[n][gr * 32 + c]) : 24.f)), acc[n]);
-  }
 #pragma unroll
   for (int n = 0; n < NB; ++n)
 #pragma unroll
@@ -825,8 +858,8 @@ constexpr int kRows = 16;
 //     8.7, 9.7, 13.2; 32 x 14336 16.1, 11.4, 14.4; 64 x 14336 29.7, 20.1, 15.6
 //     (i4_blocks, that is the launch that lays out the activations, 18.2); 192 x
 //     4096 21.4, 18.1, 14.2 (16.8).  In groups of 32 128 channels with their
-//     factors do not fit the registers: 64 x 14336 35.8, 25.6, 30.6 (25.2), 128 x
-//     14336 57.1, 46.4, 54.8 (41.1); there i4_blocks takes them.
+//     factors do not fit the registers: 64 x 14336 35.8, 25.6, 30.6 (24.0), 128 x
+//     14336 57.1, 46.4, 54.8 (39.2); there i4_blocks takes them.
 //     128 channels, i4_tile of 64 tokens, of 128: 512 tokens, 4096 channels 28.7,
 //     44.3, 60.4; 1024: 55.3, 49.3, 62.5; 2048: 111, 101, 78; 256 x 14336: 56.3,
 //     49.8, 62.7; 512 x 14336: 101, 87, 68.
