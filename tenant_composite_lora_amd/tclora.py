@@ -1300,6 +1300,14 @@ def kv_map(cache: KVCache, n_new: torch.Tensor, group_seq_ptr: torch.Tensor, pre
                    n_tokens, own_len_out, used_out, _once=stream is None)(stream)
 
 
+def window_limits(window: int, sinks: int):
+    """A window and its sinks as the library takes them, in 32 bits: what is
+    above them is more than the keys there can be, what is below 0 stays so
+    (and is refused)."""
+    most = (1 << 31) - 1
+    return max(-1, min(int(window), most)), max(-1, min(int(sinks), most))
+
+
 class AttnPlan:
     """The mapping of an attention batch (tcl_attn_plan): requests in groups
     that share a prefix.  int32 device tensors: seq_tok_ptr [n_seqs + 1],
@@ -1319,8 +1327,7 @@ class AttnPlan:
             raise ValueError("AttnPlan: sinks without a window")
         self.cache, self.n_q_heads, self.n_tokens = cache, int(n_q_heads), int(n_tokens)
         self.window, self.sinks = window, sinks
-        most = (1 << 31) - 1  # (more than the keys there can be)
-        self.limits = () if window is None else (min(int(window), most), min(int(sinks), most))
+        self.limits = () if window is None else window_limits(window, sinks)
         self.device = cache.device
         self.home = _stream(self.device)
         self._set(seq_tok_ptr, group_seq_ptr, prefix_len, prefix_pages, own_len, own_pages)

@@ -645,6 +645,25 @@ def test_attn_window_host_errors(L):
     assert apply(n_tokens=0) == 0 and apply(n_seqs=0, W=(1 << 31) - 1, N=(1 << 31) - 1) == 0
 
 
+def test_windows_beyond_32_bits(L):
+    """Windows and sinks that 32 bits do not hold: more than all keys where they
+    are positive, refused as any other where they are negative (no GPU)."""
+    P = 0x10000
+    c = ctypes.byref(tclora.KVDesc(4, 16, 2, 64, 2048, 64, 1024, P, P))
+    b = ctypes.byref(tclora.AttnBatch(0, 0, 0, 4, 4))
+
+    def rc(window, sinks=0):
+        return L.tcl_attn_window_apply(b, c, 4, *tclora.window_limits(window, sinks), P, 1 << 30, P, 256, P,
+                                       256, None, 0.1, P, 1 << 40, None)
+
+    for big in (5, (1 << 31) - 1, 1 << 31, (1 << 32) + 5, 1 << 40):
+        assert rc(big) == 0 and rc(1, big) == 0
+        assert tclora.window_limits(big, 0) == (min(big, (1 << 31) - 1), 0)
+    for bad in (0, -1, -(1 << 31), 5 - (1 << 32), -(1 << 40)):
+        assert rc(bad) == tclora.EINVAL
+        assert bad == 0 or rc(1, bad) == tclora.EINVAL
+
+
 def test_i4_host_errors(L):
     """The 4-bit calls refuse bad weights, sizes and pointers on the host (no
     GPU)."""
