@@ -135,7 +135,8 @@ __global__ __launch_bounds__(kMapThreads) void kv_map_kernel(MapArgs a) {
     const int64_t q = s == tid ? q0 : a.n_new[s], n = s == tid ? n0 : a.own_len[s];
     const int64_t cap = int64_t(a.ld) << a.shift;
     const int32_t prefix = groups.prefix_of(a, s);
-    if (q < 0 || n < 0 || n + q > cap || prefix + n + q > int64_t(0x7fffffff)) {
+    // (the last new key's position; without one nothing has a position)
+    if (q < 0 || n < 0 || n + q > cap || (q > 0 && prefix + n + q - 1 > int64_t(0x7fffffff))) {
       bad = true;
       continue;
     }
