@@ -379,7 +379,9 @@ __device__ inline bf16x8_t parts_zero(uint32_t z) {  // z: zero point
   return as_bf16(nt_u4{w, w, w, 0});
 }
 
-// More tokens, from staged activations: 32 NB channels by 32 tokens, the blocks
+constexpr int kBlockTiles = 4;  // tiles of 32 channels of a workgroup of i4_blocks
+
+// More tokens, from staged activations: 128 channels by 32 tokens, the blocks
 // dealt out to the waves as in i4_rows.  For groups of 32 and 64: 64 tokens, 4096 ->
 // 14336, groups of 32, 24.0 us with the 4.2 of laying the activations out (zero
 // points 24.8), 128 tokens 39.2.  A group's products start from its correction, a
@@ -390,11 +392,11 @@ __device__ inline bf16x8_t parts_zero(uint32_t z) {  // z: zero point
 // roundings allow.)  What scales the sums, two operations an element and group in
 // i4_direct, one here, shares the issue slots with widening and the matrix
 // instructions.
-template <int NB, int GS, bool ZP>
+template <int GS, bool ZP>
 __global__ __launch_bounds__(64 * kWaves) void i4_blocks(I4Args a) {
   static_assert(GS > 1, "two groups share a correction's operands");
   const Widen widen;
-  constexpr int WV = kWaves, LD = 32 * NB + 8;
+  constexpr int NB = kBlockTiles, WV = kWaves, LD = 32 * NB + 8;
   __shared__ __align__(16) float part[WV * 32 * LD];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 31, h = lane >> 5;
@@ -660,7 +662,7 @@ __global__ __launch_bounds__(256) void i4_join_kernel(I4Args a) {
   }
 }
 
-// Many tokens: tiles of 256 channels by BT tokens, WC by 8 / WC waves.  Blocks
+// Many tokens: tiles of 256 channels by BT tokens, four by two waves.  Blocks
 // of 128 columns go through LDS in three stages, activations and weights alike,
 // each filled while the block two before it is multiplied (a wave's own
 // registers hold no load: one block's time does not cover a trip to memory);
@@ -669,10 +671,10 @@ __global__ __launch_bounds__(256) void i4_join_kernel(I4Args a) {
 // the same matrix instructions alone take 176 (the clock under full load), what
 // comes on top is LDS filled (31), sums scaled (31), corrections (16), operands
 // read (16); widening, dealt out among the products, 3.
-template <int BT, int WC, int GS, bool ZP>
+template <int BT, int GS, bool ZP>
 __global__ __launch_bounds__(512, 2) void i4_tile(I4Args a) {
   const Widen widen;
-  constexpr int BC = 256, WV = 8, WT = WV / WC, NB = BC / WC / 32, MT = BT / WT / 32, PER = 4 / GS;
+  constexpr int BC = 256, WV = 8, WC = 4, WT = WV / WC, NB = BC / WC / 32, MT = BT / WT / 32, PER = 4 / GS;
   constexpr int NX = BT / 32;  // KiB of activations a wave moves a block
   __shared__ struct {
     nt_u4 x[3][BT / 32 * 512];
@@ -956,7 +958,8 @@ void go_stage(const I4Args &a, hipStream_t s) {
 template <int GS, bool ZP>
 void go_blocks(const I4Args &a, hipStream_t s) {
   go_stage<GS>(a, s);
-  hipLaunchKernelGGL((i4_blocks<4, GS, ZP>), dim3(unsigned((a.N + 127) / 128) * ((a.T + 31) / 32)),
+  constexpr int channels = 32 * kBlockTiles;
+  hipLaunchKernelGGL((i4_blocks<GS, ZP>), dim3(unsigned((a.N + channels - 1) / channels) * ((a.T + 31) / 32)),
                      dim3(64 * kWaves), 0, s, a);
 }
 
@@ -965,7 +968,7 @@ void go_tile(I4Args a, hipStream_t s) {
   go_stage<GS>(a, s);
   a.nt = (a.T + BT - 1) / BT;
   a.nc = (a.N + 255) / 256;
-  hipLaunchKernelGGL((i4_tile<BT, 4, GS, ZP>), dim3((a.nt * a.nc + 7) / 8 * 8), dim3(512), 0, s, a);
+  hipLaunchKernelGGL((i4_tile<BT, GS, ZP>), dim3((a.nt * a.nc + 7) / 8 * 8), dim3(512), 0, s, a);
 }
 
 template <int GS, bool ZP>
