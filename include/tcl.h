@@ -698,10 +698,16 @@ int tcl_i4_workspace_bytes(const tcl_i4_weight *w, int32_t n_tokens, size_t *byt
  * tcl_fused_apply on the same rows completes it.  x: device bf16
  * [n_tokens][ldx], 16-byte aligned; y: device [n_tokens][ldy] of dtype yd,
  * 16-byte aligned, ldx and ldy multiples of 8; y must not overlap x.  Weights
- * are not rounded; sums are fp32, a group's first, and y is rounded once.  A
- * row of x with an infinity or a NaN, or whose sum of |x| over a group times
- * 272 leaves fp32's range, may be NaN in every channel; no other row's result
- * is touched.  Results are bitwise reproducible.  n_tokens == 0 or d_out == 0
+ * are not rounded; sums are fp32, joined a group at a time, or up to four for
+ * many tokens, and y is rounded once.  A group is summed as x (16 + n) less 16
+ * + z times the sum of x: what fp32 loses is relative to those, 2^-24 of |x| (16
+ * + n) and |x| (16 + z) a rounding, not to |x| |n - z|, which shows where one
+ * activation is hundreds of times the others and its weights lie at their zero
+ * points (3000 among numbers around 1: some 3e-5 of the result).  A row of x
+ * with an infinity or a NaN, or whose sum of |x| over a group times 272, or
+ * times 272 and a scale, leaves fp32's range, may be NaN in every channel; no
+ * other row's result is touched.  More is lost where a group's sum of x, or a
+ * scale times 16 + z, is below 2^-100.  Results are bitwise reproducible.  n_tokens == 0 or d_out == 0
  * is a no-op.  ws: device workspace of at least tcl_i4_workspace_bytes bytes,
  * 256-byte aligned, in use until the call's work has run; calls that may run
  * at the same time need one each.

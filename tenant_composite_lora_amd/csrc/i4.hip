@@ -6,9 +6,12 @@
 // pair of them (a shift, and its four bits under the exponent of 16), exactly.
 // The matrix cores sum x (16 + n) over a group, and with the sums of x over the
 // groups
-//   y = sum_g s_g sum_g x (n - z) = sum_g s_g sum_g x (16 + n) - sum_g s_g (16 + z_g) sum_g x
-// takes one fused operation an output and group, in fp32, and a short product
-// of fp32 numbers in bf16 parts.  No weight is rounded.
+//   y = sum_g s_g sum_g x (n - z) = sum_g s_g (sum_g x (16 + n) - (16 + z_g) sum_g x)
+// takes one or two fused operations an output and group, in fp32.  The correction
+// is the second of them (i4_rows, i4_direct), what a group's products start from,
+// a short product of fp32 numbers in bf16 parts (i4_blocks), or such a product
+// every four groups (i4_tile): running sums never hold more than four groups'
+// uncorrected.  No weight is rounded.
 //
 // Four kernels (choose):
 //   i4_rows    up to 16 tokens: the weight streams from memory into matrix-core
@@ -259,7 +262,7 @@ __device__ inline void stream(int first, int step, int n, F block) {
 // result, so that a lane holds one channel, its scale and zero point; the sums
 // of x come from an operand of ones.  Operands are on their way up to four
 // blocks ahead, since a wave has few: at 1 token, 4096 -> 1024, 64 workgroups of
-// 8 waves have 4 blocks each, 4.9 us, a launch and two trips to memory; 4096 ->
+// 8 waves have 4 blocks each, 4.5 us, a launch and two trips to memory; 4096 ->
 // 14336, 31 MB, 8.7 us, 3.6 TB/s.  GS: groups of a block (4, 2, 1; 1 also
 // for groups of several blocks).
 template <int NB, int GS, bool ZP>
@@ -532,8 +535,11 @@ __device__ inline void move16(uint32_t to, const void *from) {  // an address a 
 // reading; the sums of x come from an operand of ones.  32 NB channels by 32
 // tokens; with ks > 1 as many workgroups, blockIdx.y, share their columns.  32 x
 // 4096 -> 4096 8.1 us, 64 8.7; 64 x 4096 -> 14336 15.6; 23 tokens, 14336 -> 4096 in
-// four, groups of 32, 14.0 us of 37 MB and 3.8 joining.  A CU takes in some 60
-// GB/s, rows and weights together.  (Rows through registers take 32 more of them:
+// four, groups of 32, 13.5 us of 37 MB and 4.0 joining.  With a block of rows and
+// one of weights on their way a wave, a CU takes in 26 to 41 GB/s, rows and weights
+// together (23 tokens, 14336 -> 4096: 364 KB a workgroup; 64, 4096 -> 14336: 528; 32,
+// 4096 -> 4096: 324): no rate of its own, rather too little on its way.  A last tile of fewer than 32 tokens
+// takes in its last row again for those that it lacks.  (Rows through registers take 32 more of them:
 // 64 x 4096 -> 14336, 30 spilled, 20.7.  Weights two blocks ahead: 32 x 4096 ->
 // 14336 12.6 where one takes 11.4.)
 template <int NB, int GS, bool ZP>
@@ -667,8 +673,9 @@ __global__ __launch_bounds__(256) void i4_join_kernel(I4Args a) {
 // each filled while the block two before it is multiplied (a wave's own
 // registers hold no load: one block's time does not cover a trip to memory);
 // scales, zero points and sums of x come with every four groups.  2048 tokens,
-// 4096 -> 14336: 258 to 265 us with the 10 of laying x out, 0.92 P operations a second;
-// the same matrix instructions alone take 176 (the clock under full load), what
+// 4096 -> 14336: 258 to 272 us with the 10 of laying x out, 0.9 P operations a second
+// (launch by launch: 267 in the median and at first, 310 to 330 from the fourth or
+// seventh launch behind a pause on for a while); the same matrix instructions alone take 176 (the clock under full load), what
 // comes on top is LDS filled (31), sums scaled (31), corrections (16), operands
 // read (16); widening, dealt out among the products, 3.
 template <int BT, int GS, bool ZP>
@@ -865,10 +872,11 @@ constexpr int kRows = 16;
 //     128 channels, i4_tile of 64 tokens, of 128: 512 tokens, 4096 channels 28.7,
 //     44.3, 60.4; 1024: 55.3, 49.3, 62.5; 2048: 111, 101, 78; 256 x 14336: 56.3,
 //     49.8, 62.7; 512 x 14336: 101, 87, 68.
-//   What bounds all of these is what a CU takes in, some 60 GB/s each, so that
+//   What bounds all of these is how long a CU takes to take its operands in, so that
 //     few workgroups with long rows are split over d_in (ks) and joined by a
 //     launch more, of 64 channels where that leaves them 256 parts, since rows
-//     are most of what they take in.  d_in 14336: 23 tokens, 4096 channels 19.3, 32
+//     are most of what they take in.  From 8192 columns on; between 4096 and
+//     that neither side has been measured.  d_in 14336: 23 tokens, 4096 channels 19.3, 32
 //     channels in two 15.4, 64 in four 14.2; 32, 2048 channels 18.4, 32 in four
 //     11.6, 64 in eight 11.4; 64, 4096 channels 22.3, 64 in two 19.1; d_in 8192, 17
 //     tokens, 1024 channels 11.6, 32 in eight 7.7, 64 in eight 8.5.  d_in 4096: 17

@@ -170,7 +170,7 @@ __device__ inline float head_sum(float v, int n) {
 // (zeros, numbers whose squares leave fp32's range, infinities) is summed again
 // in 64 bits, so that no finite head overflows or vanishes.  Bound by the rows'
 // bytes as the plain append is: 4224 tokens of 32 + 8 + 8 heads of 128 in fp32,
-// 156 MB, 28.0 us, 5.6 TB/s (without the norms 24.2); 64 tokens 4.1 us, a launch.
+// 156 MB, 28.4 us, 5.5 TB/s (without the norms 24.2); 64 tokens 4.0 us, a launch.
 template <typename T>
 __global__ __launch_bounds__(kAppThreads) void kv_append_norm_kernel(NormArgs n) {
   __shared__ float2 cs[128];

@@ -8,8 +8,8 @@
 // as well in small batches, where a launch more is what would cost; in larger
 // ones a second launch does, from what the first has left.
 // Bound by the launch and some ten round trips to memory and barriers, one
-// behind the other: 64 requests of one token 5.7 us, 1152 requests with 43 000
-// tokens 10.5 and, by the second launch, 4.0.
+// behind the other: 64 requests of one token 5.8 us, 1152 requests with 43 000
+// tokens 10.4 and, by the second launch, 3.9.
 #include "kern_common.hpp"
 #include "kv.hpp"
 #include "scan.hpp"

@@ -1400,8 +1400,9 @@ class AttnPlan:
 
 class AttnCall:
     """Pre-marshalled arguments of tcl_attn_apply (tcl_attn_window_apply for
-    a plan with a window) for repeated calls: each call writes o (bf16 [n_tokens, q heads * head_dim], made here unless
-    given) and, if given, lse (fp32 [n_tokens, q heads]).  ``cache`` is the
+    a plan with a window) for repeated calls: each call writes o (bf16
+    [n_tokens, q heads * head_dim], made here unless given) and, if given, lse
+    (fp32 [n_tokens, q heads]).  ``cache`` is the
     layer's (the plan's by default); the workspace is the call's own, or
     ``ws``; calls that may run at the same time need one each."""
 

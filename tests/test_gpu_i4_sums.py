@@ -84,3 +84,20 @@ def test_one_signed_activations_of_long_rows(T, group):
     """Sums that were joined only at the end would be off by many times the bound,
     and more the longer the row (1024 tokens: laid-out rows in blocks)."""
     run(T, 65536, 520, group, True, 0)
+
+
+@pytest.mark.parametrize("T,d_in,d_out,group", [
+    (3, 4096, 264, 32), (64, 4096, 264, 128), (64, 4096, 14336, 128), (64, 4096, 14336, 32), (40, 8192, 2056, 32),
+    (1024, 1024, 4096, 64), (2048, 1024, 4096, 128)])
+def test_one_strong_activation_at_its_zero_points(T, d_in, d_out, group):
+    """It adds nothing to the result, yet sums are as exact as |x| (16 + n) lets
+    them be, not as |x| |n - z|: the bound is that of all products."""
+    (W, s, _), n = weight(T, d_out, d_in, group, full=True)
+    n[:, 7] = 8
+    W[:, 3] = (W[:, 3] & 15) | 8 << 4
+    torch.manual_seed(T)
+    x = torch.randn(T, d_in, device=DEV)
+    x[:, 7] = 3000
+    x = x.to(torch.bfloat16)
+    got = tclora.i4_linear(tclora.I4Weight(W, s), x, y_dtype=torch.float32)
+    close(got, *product64((W, s, None), n, x))
