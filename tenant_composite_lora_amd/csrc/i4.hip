@@ -386,7 +386,7 @@ constexpr int kBlockTiles = 4;  // tiles of 32 channels of a workgroup of i4_blo
 
 // More tokens, from staged activations: 128 channels by 32 tokens, the blocks
 // dealt out to the waves as in i4_rows.  For groups of 32 and 64: 64 tokens, 4096 ->
-// 14336, groups of 32, 24.0 us with the 4.2 of laying the activations out (zero
+// 14336, groups of 32, 24.0 us with the 4.8 of laying the activations out (zero
 // points 24.8), 128 tokens 39.2.  A group's products start from its correction, a
 // matrix product in which one half of the lanes (the group's, two groups in turn)
 // holds the sum of x: what is scaled and added up is then no larger than the
